@@ -76,7 +76,7 @@ extern "C" {
 #define K3HUF_E_BADLEN  -4   /* a code length above 12 */
 #define K3HUF_E_FORMAT  -5   /* container malformed: magic, version, sizes, offsets */
 #define K3HUF_E_CUDA    -6   /* a CUDA runtime call failed; see k3huf_last_cuda_error */
-#define K3HUF_E_NOMEM   -7   /* host allocation failed (encoder / ring only) */
+#define K3HUF_E_NOMEM   -7   /* host allocation failed (encoder, ring, embedding lookup) */
 #define K3HUF_E_IO      -8   /* file open or read failed (storage feed only) */
 
 /* bits OR-ed into *d_status by the decode kernels */
@@ -85,6 +85,7 @@ extern "C" {
 #define K3HUF_ST_INDEX    4u  /* a chunk did not end at the next chunk's recorded offset */
 #define K3HUF_ST_HEADER   8u  /* a device-side stripe header disagrees with the layer header */
 #define K3HUF_ST_TIMEOUT 16u  /* a bounded wait for an asynchronous copy gave up (work skipped) */
+#define K3HUF_ST_TOKEN   32u  /* a token id or adapter index past its range (taken as "none") */
 
 typedef struct {
     uint32_t chunk_syms, n_tables, n_tensors, n_stripes;
@@ -446,6 +447,121 @@ typedef struct {
 int k3huf_ring_run_file(k3huf_ring *ring, k3huf_feed *feed, int n_layers, const uint64_t *file_offsets,
                         const size_t *layer_bytes, void *const *d_outs, const size_t *out_bytes, uint32_t *d_status,
                         k3huf_feed_stats_t *stats);
+
+/* ---------------------------------------------------------------------------
+ * Operators next to the coded weights: embedding rows, low-rank adapters and
+ * token log probabilities, each with its gradient.  They follow the
+ * conventions above, with these of their own:
+ *  - an element type is K3HUF_BF16 or K3HUF_F32; pointers are aligned to
+ *    their elements (scratch to 256 bytes), and a matrix's stride is the
+ *    number of elements from one row to the next, at least its columns (any
+ *    alignment works; rows of 16-byte aligned addresses are the fast ones);
+ *  - ids are int32 or int64 (id_bytes 4 or 8).  A negative id means "none"
+ *    (padding, an unscored token, a request without an adapter); one past
+ *    the range is taken as none too and sets K3HUF_ST_TOKEN in *d_status;
+ *  - sums, softmax statistics and rank-wide intermediates are fp32; bf16
+ *    results are rounded once, to nearest.  Results do not depend on timing:
+ *    the same call on the same inputs gives the same bits;
+ *  - scratch is the caller's, need not be initialised, and must not be given
+ *    to two calls that may run at the same time;
+ *  - a call over zero tokens launches nothing that reads or writes them. */
+#define K3HUF_BF16 0u
+#define K3HUF_F32  1u
+
+/* Flag of the gradient calls: add to the parameter gradients instead of
+ * overwriting them. */
+#define K3HUF_ACCUMULATE 4u
+
+/* out[t] = scale * W[ids[t]] for tensor `tensor` of the layer as a row-major
+ * table of `cols` columns: only the sub-streams that the rows meet are
+ * decoded.  Any container (chunk and sub-stream sizes, rows that start
+ * anywhere in a chunk); tables of up to 256 stripes.
+ *  h_layer_hdr .. layer_bytes: as for k3huf_decode_layer;
+ *  d_ids: n_tokens ids; a row of zeros is written for "none";
+ *  d_out: n_tokens rows of `cols` elements of out_type, out_stride apart.
+ * Stream faults set bits in *d_status as a decode does. */
+int k3huf_embed_layer(const void *h_layer_hdr, size_t hdr_bytes, const void *d_layer, size_t layer_bytes,
+                      uint32_t tensor, uint64_t cols, const void *d_ids, uint32_t id_bytes, uint64_t n_tokens,
+                      float scale, void *d_out, uint32_t out_type, uint64_t out_stride, uint32_t *d_status,
+                      void *stream);
+
+/* The gradient of such a lookup: grad[v] = scale * (sum of dY[t] over the
+ * tokens t with ids[t] = v, in the order of the tokens), for a table of
+ * `rows` rows; rows without a token are zero.  With K3HUF_ACCUMULATE the sums
+ * are added to grad and the other rows are left alone.
+ *  d_dy: n_tokens rows of `cols` elements of dy_type, dy_stride apart;
+ *  d_grad: rows x cols floats, contiguous;
+ *  d_scratch: k3huf_embed_grad_scratch_bytes(...) bytes. */
+int k3huf_embed_grad_scratch_bytes(uint64_t n_tokens, uint64_t rows, uint64_t cols, size_t *scratch_bytes);
+int k3huf_embed_grad(const void *d_ids, uint32_t id_bytes, uint64_t n_tokens, const void *d_dy, uint32_t dy_type,
+                     uint64_t dy_stride, uint64_t rows, uint64_t cols, float scale, float *d_grad, void *d_scratch,
+                     size_t scratch_bytes, uint32_t *d_status, uint32_t flags, void *stream);
+
+/* Adapters of one projection (cols inputs, rows outputs), resident on the
+ * device: a is n_adapters x rank x cols and b is n_adapters x rank x rows,
+ * bf16, contiguous (both rank-major: b holds the transpose of the output
+ * factor); scales holds n_adapters floats.  Adapters of a smaller rank are
+ * padded with zero rows. */
+#define K3HUF_MAX_RANK 128u
+typedef struct {
+    const void *a, *b;
+    const float *scales;
+    uint32_t n_adapters, rank;
+    uint64_t cols, rows;
+} k3huf_adapters_t;
+
+/* Scratch of k3huf_adapter_apply (grad 0) and k3huf_adapter_grad (grad 1). */
+int k3huf_adapter_scratch_bytes(uint64_t n_tokens, uint32_t n_adapters, uint32_t rank, uint64_t cols, uint64_t rows,
+                                int grad, size_t *scratch_bytes);
+
+/* y[t] = base[t] + scales[i] (x[t] a_i^T) b_i with i = ids[t]; y[t] = base[t]
+ * without an adapter.  base is the shared projection's output for these
+ * tokens (of y's type; may be y itself), or NULL for zero: written first, y
+ * then takes k3huf_gemv_layer_batch's additions.
+ *  d_x: n_tokens rows of cols bf16; d_ids: int32; d_y: rows of y_type. */
+int k3huf_adapter_apply(const k3huf_adapters_t *adapters, const void *d_x, uint64_t x_stride, const int32_t *d_ids,
+                        uint64_t n_tokens, const void *d_base, uint64_t base_stride, void *d_y, uint64_t y_stride,
+                        uint32_t y_type, void *d_scratch, size_t scratch_bytes, uint32_t *d_status, void *stream);
+
+/* Gradients of k3huf_adapter_apply for the upstream gradient dy (bf16): with
+ * dh[t] = scales[i] dy[t] b_i^T and h[t] = scales[i] x[t] a_i^T,
+ *  dx[t] = dx_base[t] + dh[t] a_i (d_dx NULL: not wanted; dx_base: the shared
+ *    projection's part, of dx's type, may be dx itself, NULL for zero);
+ *  da[i] = sum over its tokens of dh[t]^T x[t], db[i] = sum of h[t]^T dy[t]:
+ *    floats laid out as a and b; adapters without a token get zeros (with
+ *    K3HUF_ACCUMULATE: are left alone). */
+int k3huf_adapter_grad(const k3huf_adapters_t *adapters, const void *d_x, uint64_t x_stride, const int32_t *d_ids,
+                       uint64_t n_tokens, const void *d_dy, uint64_t dy_stride, const void *d_dx_base,
+                       uint64_t dx_base_stride, void *d_dx, uint64_t dx_stride, uint32_t dx_type, float *d_da,
+                       float *d_db, void *d_scratch, size_t scratch_bytes, uint32_t *d_status, uint32_t flags,
+                       void *stream);
+
+/* Log probabilities of one given token per row of logits (type, stride) under
+ * softmax(scale * logits), scale > 0 (an inverse temperature):
+ *  d_logprob: n floats, 0 for "none"; d_entropy, d_lse (log of the sum of
+ *    exponentials of the scaled logits): n floats, or NULL;
+ *  top (0 .. K3HUF_MAX_TOP, at most vocab): the `top` largest logits of every
+ *    row, largest first, ties to the lower index: d_top_ids and
+ *    d_top_logprobs, n x top.
+ * Logits of -infinity have probability 0 and take no part in the entropy; a
+ * row with no other logits has lse -infinity and entropy 0.  A NaN, or
+ * +infinity, makes the row's statistics NaN. */
+#define K3HUF_MAX_TOP 64u
+int k3huf_token_logprobs(const void *d_logits, uint32_t type, uint64_t stride, uint64_t n, uint32_t vocab, float scale,
+                         const void *d_tokens, uint32_t id_bytes, float *d_logprob, float *d_entropy, float *d_lse,
+                         uint32_t top, int32_t *d_top_ids, float *d_top_logprobs, uint32_t *d_status, void *stream);
+
+/* Its gradient with respect to the logits: with p = exp(scale x - lse), g the
+ * gradient of the log probability (not read for "none") and h that of the
+ * entropy (d_g_entropy NULL: zero, and d_entropy is not read),
+ *   dlogits[j] = scale (g (1[j = token] - p_j) - h p_j (log p_j + entropy)).
+ *  d_lse, d_entropy: as k3huf_token_logprobs gave them;
+ *  d_dlogits: of the logits' type, out_stride apart; may be d_logits itself
+ *    (then out_stride = stride). */
+int k3huf_token_logprobs_grad(const void *d_logits, uint32_t type, uint64_t stride, uint64_t n, uint32_t vocab,
+                              float scale, const void *d_tokens, uint32_t id_bytes, const float *d_lse,
+                              const float *d_entropy, const float *d_g_logprob, const float *d_g_entropy,
+                              void *d_dlogits, uint64_t out_stride, uint32_t *d_status, void *stream);
 
 /* Last CUDA error code seen by this library on the calling thread. */
 int k3huf_last_cuda_error(void);

@@ -20,7 +20,7 @@ import numpy as np
 from . import _build
 
 OK, E_ARG, E_EMPTY, E_OVERSUB, E_BADLEN, E_FORMAT, E_CUDA, E_NOMEM, E_IO = 0, -1, -2, -3, -4, -5, -6, -7, -8
-ST_BADCODE, ST_OVERRUN, ST_INDEX, ST_HEADER, ST_TIMEOUT = 1, 2, 4, 8, 16
+ST_BADCODE, ST_OVERRUN, ST_INDEX, ST_HEADER, ST_TIMEOUT, ST_TOKEN = 1, 2, 4, 8, 16, 32
 MAXLEN = 12
 STRIPE_VALUES = 1 << 25
 
@@ -32,7 +32,9 @@ EXPORTS = [
     "k3huf_ring_destroy", "k3huf_last_cuda_error", "k3huf_strerror", "k3huf_feed_open", "k3huf_feed_direct",
     "k3huf_feed_read", "k3huf_feed_close", "k3huf_ring_create_staged", "k3huf_ring_run_file",
     "k3huf_encode_scratch_bytes", "k3huf_encode_bound", "k3huf_encode_layer_gpu", "k3huf_gemv_layer",
-    "k3huf_gemv_layer_ex", "k3huf_gemv_layer_batch",
+    "k3huf_gemv_layer_ex", "k3huf_gemv_layer_batch", "k3huf_embed_layer", "k3huf_embed_grad_scratch_bytes",
+    "k3huf_embed_grad", "k3huf_adapter_scratch_bytes", "k3huf_adapter_apply", "k3huf_adapter_grad",
+    "k3huf_token_logprobs", "k3huf_token_logprobs_grad",
 ]
 FILE_ALIGN = 4096
 
@@ -66,6 +68,12 @@ class RingStats(ctypes.Structure):
 class FeedStats(ctypes.Structure):
     _fields_ = [("total_ms", ctypes.c_float), ("read_ms", ctypes.c_float), ("copy_ms", ctypes.c_float),
                 ("decode_ms", ctypes.c_float), ("read_bytes", ctypes.c_uint64), ("out_bytes", ctypes.c_uint64)]
+
+
+class Adapters(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("n_adapters", ctypes.c_uint32), ("rank", ctypes.c_uint32), ("cols", ctypes.c_uint64),
+                ("rows", ctypes.c_uint64)]
 
 
 _lib_handle = None
@@ -125,6 +133,18 @@ def _lib():
             L.k3huf_ring_run_file.argtypes = [_vp, _vp, ctypes.c_int, ctypes.POINTER(ctypes.c_uint64),
                                               ctypes.POINTER(_sz), ctypes.POINTER(_vp), ctypes.POINTER(_sz), _vp,
                                               ctypes.POINTER(FeedStats)]
+            u32, u64, f32 = ctypes.c_uint32, ctypes.c_uint64, ctypes.c_float
+            L.k3huf_embed_layer.argtypes = [_vp, _sz, _vp, _sz, u32, u64, _vp, u32, u64, f32, _vp, u32, u64, _vp, _vp]
+            L.k3huf_embed_grad_scratch_bytes.argtypes = [u64, u64, u64, ctypes.POINTER(_sz)]
+            L.k3huf_embed_grad.argtypes = [_vp, u32, u64, _vp, u32, u64, u64, u64, f32, _vp, _vp, _sz, _vp, u32, _vp]
+            L.k3huf_adapter_scratch_bytes.argtypes = [u64, u32, u32, u64, u64, ctypes.c_int, ctypes.POINTER(_sz)]
+            L.k3huf_adapter_apply.argtypes = [_vp, _vp, u64, _vp, u64, _vp, u64, _vp, u64, u32, _vp, _sz, _vp, _vp]
+            L.k3huf_adapter_grad.argtypes = [_vp, _vp, u64, _vp, u64, _vp, u64, _vp, u64, _vp, u64, u32, _vp, _vp, _vp,
+                                             _sz, _vp, u32, _vp]
+            L.k3huf_token_logprobs.argtypes = [_vp, u32, u64, u64, u32, f32, _vp, u32, _vp, _vp, _vp, u32, _vp, _vp,
+                                               _vp, _vp]
+            L.k3huf_token_logprobs_grad.argtypes = [_vp, u32, u64, u64, u32, f32, _vp, u32, _vp, _vp, _vp, _vp, _vp,
+                                                    u64, _vp, _vp]
             L.k3huf_strerror.restype = ctypes.c_char_p
             L.k3huf_strerror.argtypes = [ctypes.c_int]
             _lib_handle = L
@@ -372,6 +392,191 @@ def decode_stripe(codelen, chunk_syms: int, sub_syms: int, d_stripe, stripe_byte
 def set_decoder_variant(variant: int) -> None:
     """Codes per lockstep table lookup: 0 = default (2), 1 or 2."""
     _check(_lib().k3huf_set_decoder_variant(variant), "k3huf_set_decoder_variant")
+
+
+# --- operators next to the coded weights ---------------------------------------
+# Tensors are CUDA tensors; a matrix's rows may be any stride apart, its columns
+# are adjacent.  The calls are asynchronous on ``stream`` (the current one) and
+# OR faults into ``d_status`` (an int32 CUDA tensor) as the decode calls do.
+
+MAX_RANK, MAX_TOP = 128, 64
+ACCUMULATE = 4
+_BF16, _F32 = 0, 1
+
+
+def _elem(t) -> int:
+    """Element type of a bf16 or fp32 tensor."""
+    name = str(t.dtype)
+    if name == "torch.bfloat16":
+        return _BF16
+    if name == "torch.float32":
+        return _F32
+    raise TypeError(f"expected a bf16 or fp32 tensor, got {name}")
+
+
+def _matrix(t, shape, what: str, elem: int | None = None):
+    """(address, element type, row stride) of a CUDA matrix of this shape."""
+    if not t.is_cuda:
+        raise TypeError(f"{what}: expected a CUDA tensor")
+    e = _elem(t)
+    if elem is not None and e != elem:
+        raise TypeError(f"{what}: wrong element type {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+    rows, cols = t.stride()
+    if cols != 1 and shape[1] > 1:
+        raise ValueError(f"{what}: columns must be adjacent")
+    return t.data_ptr(), e, rows if shape[0] > 1 else max(rows, shape[1])
+
+
+def _dense(t, shape, what: str, dtype: str, optional: bool = False):
+    """Address of a contiguous CUDA tensor of this shape and dtype (None if optional and None)."""
+    if t is None and optional:
+        return None
+    if not t.is_cuda:
+        raise TypeError(f"{what}: expected a CUDA tensor")
+    if str(t.dtype) != dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor of shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _ids(t, what: str = "ids"):
+    """(address, bytes per id, count) of a contiguous int32 or int64 CUDA vector."""
+    if not t.is_cuda:
+        raise TypeError(f"{what}: expected a CUDA tensor")
+    size = {"torch.int32": 4, "torch.int64": 8}.get(str(t.dtype))
+    if size is None:
+        raise TypeError(f"{what}: expected int32 or int64, got {t.dtype}")
+    if t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous vector")
+    return t.data_ptr(), size, t.numel()
+
+
+def embed_layer(hdr, d_layer, tensor: int, cols: int, ids, out, d_status, scale: float = 1.0, stream=None,
+                layer_bytes: int | None = None) -> None:
+    """out[t] = scale * W[ids[t]] for tensor ``tensor`` of the layer as a table of
+    ``cols`` columns (k3huf_embed_layer): only what the rows meet is decoded.
+    ``ids``: int32 or int64, negative for a row of zeros; ``out``: bf16 or fp32,
+    len(ids) x cols."""
+    h = _host(hdr)
+    lb = _nbytes(d_layer) if layer_bytes is None else layer_bytes
+    ip, ib, n = _ids(ids)
+    op, oe, os_ = _matrix(out, (n, cols), "out")
+    _check(_lib().k3huf_embed_layer(h.ctypes.data, h.size, _dptr(d_layer), lb, int(tensor), cols, ip, ib, n, scale,
+                                    op, oe, os_, _dptr(d_status), _stream(stream)), "k3huf_embed_layer")
+
+
+def embed_grad_scratch_bytes(n_tokens: int, rows: int, cols: int) -> int:
+    """Device scratch bytes of embed_grad."""
+    out = _sz(0)
+    _check(_lib().k3huf_embed_grad_scratch_bytes(n_tokens, rows, cols, ctypes.byref(out)),
+           "k3huf_embed_grad_scratch_bytes")
+    return int(out.value)
+
+
+def embed_grad(ids, dy, grad, scratch, d_status, scale: float = 1.0, accumulate: bool = False, stream=None) -> None:
+    """grad[v] = scale * (sum of dy[t] over the tokens with ids[t] = v), rows
+    without a token zero (k3huf_embed_grad); ``accumulate``: added to grad.
+    ``dy``: bf16 or fp32, len(ids) x cols; ``grad``: fp32, rows x cols."""
+    ip, ib, n = _ids(ids)
+    rows, cols = grad.shape
+    gp = _dense(grad, (rows, cols), "grad", "torch.float32")
+    dp, de, ds = _matrix(dy, (n, cols), "dy")
+    _check(_lib().k3huf_embed_grad(ip, ib, n, dp, de, ds, rows, cols, scale, gp, _dptr(scratch), _nbytes(scratch),
+                                   _dptr(d_status), ACCUMULATE if accumulate else 0, _stream(stream)),
+           "k3huf_embed_grad")
+
+
+def adapter_scratch_bytes(n_tokens: int, n_adapters: int, rank: int, cols: int, rows: int, grad: bool = False) -> int:
+    """Device scratch bytes of adapter_apply, or of adapter_grad."""
+    out = _sz(0)
+    _check(_lib().k3huf_adapter_scratch_bytes(n_tokens, n_adapters, rank, cols, rows, int(grad), ctypes.byref(out)),
+           "k3huf_adapter_scratch_bytes")
+    return int(out.value)
+
+
+def _adapters(a, b, scales) -> Adapters:
+    n, rank, cols = a.shape
+    rows = b.shape[2]
+    return Adapters(_dense(a, (n, rank, cols), "a", "torch.bfloat16"), _dense(b, (n, rank, rows), "b", "torch.bfloat16"),
+                    _dense(scales, (n,), "scales", "torch.float32"), n, rank, cols, rows)
+
+
+def adapter_apply(x, a, b, ids, scales, y, scratch, d_status, base=None, stream=None) -> None:
+    """y[t] = base[t] + scales[i] (x[t] a[i]^T) b[i] with i = ids[t], base alone
+    where ids[t] < 0 (k3huf_adapter_apply).  ``a``: bf16, adapters x rank x cols;
+    ``b``: bf16, adapters x rank x rows; ``ids``: int32; ``y``: fp32 or bf16;
+    ``base``: of y's type, may be y, None for zero."""
+    ad = _adapters(a, b, scales)
+    n = ids.numel()
+    ip = _dense(ids, (n,), "ids", "torch.int32")
+    xp, _, xs = _matrix(x, (n, ad.cols), "x", _BF16)
+    yp, ye, ys = _matrix(y, (n, ad.rows), "y")
+    bp, _, bs = (None, ye, 0) if base is None else _matrix(base, (n, ad.rows), "base", ye)
+    _check(_lib().k3huf_adapter_apply(ctypes.addressof(ad), xp, xs, ip, n, bp, bs, yp, ys, ye, _dptr(scratch),
+                                      _nbytes(scratch), _dptr(d_status), _stream(stream)), "k3huf_adapter_apply")
+
+
+def adapter_grad(x, a, b, ids, scales, dy, da, db, scratch, d_status, dx=None, dx_base=None, accumulate: bool = False,
+                 stream=None) -> None:
+    """Gradients of adapter_apply for the bf16 gradient ``dy`` (k3huf_adapter_grad):
+    ``da``, ``db`` fp32, shaped as a and b (``accumulate``: added to); ``dx`` (fp32
+    or bf16, None if not wanted) = dx_base + the adapters' part."""
+    ad = _adapters(a, b, scales)
+    n = ids.numel()
+    ip = _dense(ids, (n,), "ids", "torch.int32")
+    xp, _, xs = _matrix(x, (n, ad.cols), "x", _BF16)
+    yp, _, ys = _matrix(dy, (n, ad.rows), "dy", _BF16)
+    if dx is None and dx_base is not None:
+        raise ValueError("dx_base without dx")
+    dp, de, ds = (None, _BF16, 0) if dx is None else _matrix(dx, (n, ad.cols), "dx")
+    bp, _, bs = (None, de, 0) if dx_base is None else _matrix(dx_base, (n, ad.cols), "dx_base", de)
+    _check(_lib().k3huf_adapter_grad(ctypes.addressof(ad), xp, xs, ip, n, yp, ys, bp, bs, dp, ds, de,
+                                     _dense(da, tuple(a.shape), "da", "torch.float32"),
+                                     _dense(db, tuple(b.shape), "db", "torch.float32"), _dptr(scratch),
+                                     _nbytes(scratch), _dptr(d_status), ACCUMULATE if accumulate else 0,
+                                     _stream(stream)), "k3huf_adapter_grad")
+
+
+def token_logprobs(logits, tokens, logprob, d_status, entropy=None, lse=None, top_ids=None, top_logprobs=None,
+                   scale: float = 1.0, stream=None) -> None:
+    """Log probabilities of one token per row under softmax(scale * logits), with
+    entropy, log-sum-exp and the largest logits (k3huf_token_logprobs).
+    ``logits``: bf16 or fp32, n x vocab; ``tokens``: int32 or int64, negative for
+    an unscored row; outputs fp32 of n, ``top_ids`` int32 and ``top_logprobs`` fp32
+    of n x top (both or neither)."""
+    tp, tb, n = _ids(tokens, "tokens")
+    vocab = logits.shape[1]
+    xp, xe, xs = _matrix(logits, (n, vocab), "logits")
+    f32 = "torch.float32"
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs go together")
+    top = 0 if top_ids is None else top_ids.shape[1]
+    _check(_lib().k3huf_token_logprobs(xp, xe, xs, n, vocab, scale, tp, tb, _dense(logprob, (n,), "logprob", f32),
+                                       _dense(entropy, (n,), "entropy", f32, True), _dense(lse, (n,), "lse", f32, True),
+                                       top, _dense(top_ids, (n, top), "top_ids", "torch.int32", True),
+                                       _dense(top_logprobs, (n, top), "top_logprobs", f32, True), _dptr(d_status),
+                                       _stream(stream)), "k3huf_token_logprobs")
+
+
+def token_logprobs_grad(logits, tokens, lse, g_logprob, dlogits, d_status, entropy=None, g_entropy=None,
+                        scale: float = 1.0, stream=None) -> None:
+    """Gradient of token_logprobs with respect to the logits
+    (k3huf_token_logprobs_grad), for the gradients of the log probabilities and
+    (with ``entropy`` as the forward gave it) of the entropies.  ``dlogits``: as
+    logits, may be logits itself."""
+    tp, tb, n = _ids(tokens, "tokens")
+    vocab = logits.shape[1]
+    xp, xe, xs = _matrix(logits, (n, vocab), "logits")
+    dp, _, ds = _matrix(dlogits, (n, vocab), "dlogits", xe)
+    f32 = "torch.float32"
+    _check(_lib().k3huf_token_logprobs_grad(xp, xe, xs, n, vocab, scale, tp, tb, _dense(lse, (n,), "lse", f32),
+                                            _dense(entropy, (n,), "entropy", f32, True),
+                                            _dense(g_logprob, (n,), "g_logprob", f32),
+                                            _dense(g_entropy, (n,), "g_entropy", f32, True), dp, ds,
+                                            _dptr(d_status), _stream(stream)), "k3huf_token_logprobs_grad")
 
 
 class Feed:

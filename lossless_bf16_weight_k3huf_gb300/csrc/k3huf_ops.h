@@ -1,0 +1,45 @@
+// Shared by the translation units of the operators that stand next to the
+// coded weights (embedding rows, adapters, token log probabilities): element
+// loads and stores, warp sums, launches and argument checks.  Included from
+// .cu files only.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "k3huf_internal.h"
+
+namespace k3huf {
+
+// --- device -----------------------------------------------------------------
+__device__ __forceinline__ float ld_f32(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float ld_f32(const float *p) { return *p; }
+// (one rounding, to nearest, at the end of an fp32 computation)
+__device__ __forceinline__ void st_f32(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void st_f32(float *p, float v) { *p = v; }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+
+// A token id or adapter index of 4 or 8 bytes; negative ones mean "none".
+__device__ __forceinline__ int64_t ld_id(const void *ids, uint32_t id_bytes, uint64_t i) {
+    return id_bytes == 8 ? static_cast<const int64_t *>(ids)[i] : int64_t(static_cast<const int32_t *>(ids)[i]);
+}
+
+// --- host -------------------------------------------------------------------
+inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline bool elem_ok(uint32_t type) { return type == K3HUF_BF16 || type == K3HUF_F32; }
+inline size_t elem_bytes(uint32_t type) { return type == K3HUF_F32 ? 4 : 2; }
+
+inline int cuda_rc(cudaError_t e) {
+    if (e == cudaSuccess) return K3HUF_OK;
+    set_cuda_error(int(e));
+    return K3HUF_E_CUDA;
+}
+
+}  // namespace k3huf
