@@ -8,25 +8,135 @@
 //   top: the largest logits, ties to the lower index
 // and, for upstream gradients g of logprob and h of entropy, p_j = exp(z_j - lse):
 //   dx_j = s (g (1[j = token] - p_j) - h p_j (log p_j + entropy))
-// Logits of -infinity take no part (p_j = 0).  One CTA takes a row.
+// Logits of -infinity take no part (p_j = 0).
+//
+// Forward, one read of the logits: a CTA of 256 threads streams a row (or, when
+// there are fewer rows than the GPU holds CTAs, the CTAs of a cluster take a
+// slice each and their results meet in the first one's shared memory).  Every
+// thread keeps a running maximum with sum and dot rescaled to it (in base 2);
+// 4 x 16 bytes per thread and step, the next step's loads issued before this
+// one's arithmetic.  What bounds it: the read of the logits from HBM; per
+// value one exponential and about six more instructions, half of them paired.
+//
+// Top alternatives in the same pass: an element can only be among the `top`
+// largest if it is not below the top-th largest of any set of elements.  Each
+// step counts the threads whose largest value reaches the threshold so far;
+// when they are more than a few, the threshold is raised to the top-th largest
+// of the threads' own largest values (bit by bit, one barrier count each).
+// Then few threads' values reach it and go to a list in shared memory, which
+// is cut to its `top` largest before it could overflow and ranked at the end.  Values as whole numbers with the index below
+// them make one order, so ties need no more.
+//
+// Backward: elementwise, 16 bytes per thread and load, one read and one write.
+#include <cooperative_groups.h>
+
 #include <cmath>
 
 #include "k3huf_ops.h"
+
+namespace cg = cooperative_groups;
 
 namespace k3huf {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kVecs = 4;                      // 16-byte vectors per thread and step
+constexpr int kMaxCluster = 16;
+constexpr uint32_t kList = 4096;              // candidates held in shared memory
+constexpr uint32_t kMostPerStep = (K3HUF_MAX_TOP + 8) * kVecs * 8;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // (value, index) order of the top alternatives: larger values first, ties to
-// the lower index.  A value's order as a whole number; +0 and -0 are equal
-// and a NaN sorts by its bits.
-__device__ __forceinline__ int32_t order_of(float x) {
-    const int32_t b = __float_as_int(x + 0.f);
-    return b < 0 ? b ^ 0x7FFFFFFF : b;
+// the lower index.  +0 and -0 are equal and a NaN ranks as -infinity; never 0.
+__device__ __forceinline__ uint32_t order_of(float x) {
+    const uint32_t b = __float_as_uint(x == x ? x + 0.f : -INFINITY);
+    return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
-__device__ __forceinline__ uint64_t key_of(float x, uint32_t j) {
-    return (uint64_t(uint32_t(order_of(x)) ^ 0x80000000u) << 32) | (0xFFFFFFFFu - j);
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t j) { return (uint64_t(order_of(x)) << 32) | (0xFFFFFFFFu - j); }
+
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The cluster's barrier in its two halves; the stores before the one are seen after the other.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// A running softmax state: e_j = 2^((x_j - m) c), sum of e_j, sum of e_j (x_j - m) c.
+struct State {
+    float m, sum, dot;
+};
+// An exponent below which 2^x is 0 in fp32, and which times 0 is 0 (minus infinity is not).
+constexpr float kFloor = -2000.f;
+__device__ __forceinline__ void rescale(State &s, float m, float c) {
+    const float d = max_nan((s.m - m) * c, kFloor), f = exp2_fast(d);
+    s.dot = f * fmaf(d, s.sum, s.dot);
+    s.sum *= f;
+    s.m = m;
+}
+__device__ __forceinline__ State join(State a, State b, float c) {
+    const float m = fmaxf(a.m, b.m);
+    rescale(a, m, c);
+    rescale(b, m, c);
+    return {m, a.sum + b.sum, a.dot + b.dot};
+}
+
+template <typename T> constexpr int kPer = 16 / int(sizeof(T));       // values per vector
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4 v, float (&f)[kPer<T>]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            f[i] = __uint_as_float(w[i]);
+        } else {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+// Vector v of a row whose first value sits `shift` values into its 16-byte
+// block: values [v E - shift, v E - shift + E) of the row; those outside the
+// row read as -infinity.
+template <typename T>
+__device__ __forceinline__ uint4 load_vec(const T *row, uint32_t shift, uint32_t n, uint32_t v) {
+    constexpr int E = kPer<T>;
+    const int64_t j = int64_t(v) * E - shift;
+    if (j >= 0 && j + E <= int64_t(n)) return __ldcs(reinterpret_cast<const uint4 *>(row + j));
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            w[i] = j + i >= 0 && j + i < int64_t(n) ? __float_as_uint(row[j + i]) : 0xFF800000u;
+        } else {
+            const uint16_t *p = reinterpret_cast<const uint16_t *>(row);
+            const int64_t a = j + 2 * i, b = a + 1;
+            w[i] = (a >= 0 && a < int64_t(n) ? p[a] : 0xFF80u) | (b >= 0 && b < int64_t(n) ? uint32_t(p[b]) << 16 : 0xFF800000u);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The `k`-th largest key of the CTA's threads (mine: each thread's own), down
+// to bit `to`, given that its bits above `from` are those of `t`: the largest
+// t' with k or more keys at or above it (0 if there are fewer than k keys).
+__device__ uint64_t kth_largest(uint64_t mine, uint32_t k, uint64_t t, int from, int to) {
+    for (int b = from; b >= to; --b) {
+        const uint64_t tryit = t | (1ull << b);
+        if (uint32_t(__syncthreads_count(mine >= tryit)) >= k) t = tryit;
+    }
+    return t;
 }
 
 struct LogprobParams {
@@ -36,67 +146,233 @@ struct LogprobParams {
     int32_t *top_ids;
     uint32_t *status;
     uint64_t stride;
-    uint32_t n, vocab, id_bytes, top;
+    uint32_t vocab, id_bytes, top;
     float scale;
 };
 
-template <typename T, typename F>
-__device__ T block_reduce(T v, F f, T *buf) {
+// Cuts the list to its `top` largest keys.
+__device__ void cut_list(uint64_t *list, uint32_t *count, uint32_t top) {
+    constexpr int kMine = kList / kThreads;
+    __shared__ uint32_t s_above[2];
     __syncthreads();
-    buf[threadIdx.x] = v;
-    __syncthreads();
-    for (int d = kThreads / 2; d; d >>= 1) {
-        if (threadIdx.x < d) buf[threadIdx.x] = f(buf[threadIdx.x], buf[threadIdx.x + d]);
+    const uint32_t n = *count;
+    if (n <= top) return;
+    if (n <= 2 * kThreads) {
+        // few: every key's rank is its place
+        const uint64_t a = threadIdx.x < n ? list[threadIdx.x] : 0, b = threadIdx.x + kThreads < n ? list[threadIdx.x + kThreads] : 0;
+        uint32_t above_a = 0, above_b = 0;
+        for (uint32_t i = 0; i < n; ++i) {
+            const uint64_t k = list[i];
+            above_a += k > a;
+            above_b += k > b;
+        }
         __syncthreads();
+        if (a && above_a < top) list[above_a] = a;
+        if (b && above_b < top) list[above_b] = b;
+        if (threadIdx.x == 0) *count = top;
+        __syncthreads();
+        return;
     }
-    return buf[0];
+    uint64_t mine[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) mine[i] = threadIdx.x + i * kThreads < n ? list[threadIdx.x + i * kThreads] : 0;
+    if (threadIdx.x < 2) s_above[threadIdx.x] = 0;
+    uint64_t t = 0;
+    for (int b = 63; b >= 0; --b) {
+        const uint64_t tryit = t | (1ull << b);
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) c += mine[i] >= tryit;
+        c = __reduce_add_sync(0xffffffffu, c);
+        __syncthreads();
+        if (threadIdx.x % 32 == 0 && c) atomicAdd(&s_above[b & 1], c);
+        if (threadIdx.x == 0) s_above[(b + 1) & 1] = 0;
+        __syncthreads();
+        if (s_above[b & 1] >= top) t = tryit;
+    }
+    if (threadIdx.x == 0) *count = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+        if (mine[i] >= t) list[atomicAdd(count, 1u)] = mine[i];       // (keys differ: exactly `top` of them)
+    __syncthreads();
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) logprob_kernel(const LogprobParams P) {
-    __shared__ float s_f[kThreads];
-    __shared__ uint64_t s_k[kThreads];
-    const uint32_t row = blockIdx.x;
+template <typename T, bool kTop>
+__global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) logprob_kernel(const LogprobParams P) {
+    constexpr int E = kPer<T>;
+    __shared__ State s_part[kWarps], s_all[kMaxCluster];
+    __shared__ uint32_t s_count, s_counts[kMaxCluster];
+    __shared__ uint64_t s_list[kTop ? kList : 1], s_sent[kTop ? (kMaxCluster - 1) * K3HUF_MAX_TOP : 1];
+    const cg::cluster_group cluster = cg::this_cluster();
+    const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank(), row = blockIdx.x / C;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const T *x = static_cast<const T *>(P.x) + uint64_t(row) * P.stride;
-    float m = -INFINITY;
-    for (uint32_t j = threadIdx.x; j < P.vocab; j += kThreads) m = fmaxf(m, ld_f32(x + j) * P.scale);
-    m = block_reduce(m, [](float a, float b) { return fmaxf(a, b); }, s_f);
-    float sum = 0.f, dot = 0.f;
-    const float shift = m == -INFINITY ? 0.f : m;          // (a row with no finite logit: every e is 0)
-    for (uint32_t j = threadIdx.x; j < P.vocab; j += kThreads) {
-        const float z = ld_f32(x + j) * P.scale, e = expf(z - shift);
-        sum += e;
-        dot += e == 0.f ? 0.f : e * (z - shift);           // (0 times infinity)
+    const float c = P.scale * kLog2e;
+    const uint32_t shift = uint32_t(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
+    const uint32_t vecs = (P.vocab + shift + E - 1) / E;
+    // this CTA's vectors: whole steps, as even as they come
+    const uint32_t steps = (vecs + kThreads * kVecs - 1) / (kThreads * kVecs);
+    const uint32_t step0 = uint32_t(uint64_t(steps) * rank / C), step1 = uint32_t(uint64_t(steps) * (rank + 1) / C);
+    if (C > 1) cluster_arrive();                           // (waited for before the first remote store)
+    if (kTop && tid == 0) s_count = 0;
+    if (kTop) __syncthreads();
+
+    uint4 v[kVecs], next[kVecs];
+    auto load = [&](uint4 (&to)[kVecs], uint32_t step) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const uint32_t at = (step * kVecs + i) * kThreads + tid;
+            to[i] = step < step1 && at < vecs ? load_vec(x, shift, P.vocab, at)
+                                              : (sizeof(T) == 4 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
+                                                                : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u));
+        }
+    };
+    // (-FLT_MAX, not -infinity: then -infinity minus it is -infinity)
+    State s{-3.402823466e38f, 0.f, 0.f};
+    uint64_t threshold = 0;
+    load(next, step0);
+    for (uint32_t step = step0; step < step1; ++step) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) v[i] = next[i];
+        load(next, step + 1);
+        float big = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                float f[E];
+                unpack<T>(v[i], f);
+                big = fmaxf(big, fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])));
+            } else {
+                const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v[i]);
+                const __nv_bfloat162 a = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+                big = fmaxf(big, fmaxf(__low2float(a), __high2float(a)));
+            }
+        }
+        rescale(s, fmaxf(s.m, big), c);
+        const float2 minus_m = make_float2(-s.m, -s.m), cc = make_float2(c, c);
+        float2 sum = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            float f[E];
+            unpack<T>(v[i], f);
+#pragma unroll
+            for (int k = 0; k < E; k += 2) {
+                float2 t = __fmul2_rn(__fadd2_rn(make_float2(f[k], f[k + 1]), minus_m), cc);
+                t.x = max_nan(t.x, kFloor);
+                t.y = max_nan(t.y, kFloor);
+                const float2 e = make_float2(exp2_fast(t.x), exp2_fast(t.y));
+                sum = __fadd2_rn(sum, e);
+                dot = __ffma2_rn(e, t, dot);
+            }
+        }
+        s.sum += sum.x + sum.y;
+        s.dot += dot.x + dot.y;
+        if constexpr (kTop) {
+            const uint32_t mine = step * (kVecs * kThreads) + tid < vecs ? order_of(big) : 0u;
+            const uint32_t reach = uint32_t(__syncthreads_count(mine >= uint32_t(threshold >> 32)));
+            if (reach == 0) continue;
+            const uint32_t few = P.top + 8;
+            if (reach > few) {
+                // (the 16 high bits are a bf16 value; for fp32 a little lower a threshold)
+                uint64_t t = kth_largest(uint64_t(mine) << 32, P.top, 0, 63, 48);
+                // (0: fewer than `top` threads have values at all)
+                if (t && uint32_t(__syncthreads_count((uint64_t(mine) << 32) >= t)) > few) {
+                    // many equal ones: the whole key of each thread's first largest value decides
+                    uint64_t key = 0;
+#pragma unroll
+                    for (int i = 0; i < kVecs; ++i) {
+                        float f[E];
+                        unpack<T>(v[i], f);
+#pragma unroll
+                        for (int k = 0; k < E; ++k) {
+                            const int64_t j = int64_t((step * kVecs + i) * kThreads + tid) * E + k - shift;
+                            if (j >= 0 && j < int64_t(P.vocab)) key = max(key, key_of(f[k], uint32_t(j)));
+                        }
+                    }
+                    t = kth_largest(key, P.top, t, 47, 0);
+                }
+                threshold = max(threshold, t);
+            }
+            if (mine >= uint32_t(threshold >> 32)) {
+#pragma unroll
+                for (int i = 0; i < kVecs; ++i) {
+                    float f[E];
+                    unpack<T>(v[i], f);
+#pragma unroll
+                    for (int k = 0; k < E; ++k) {
+                        const int64_t j = int64_t((step * kVecs + i) * kThreads + tid) * E + k - shift;
+                        if (j < 0 || j >= int64_t(P.vocab)) continue;
+                        const uint64_t key = key_of(f[k], uint32_t(j));
+                        if (key < threshold) continue;
+                        s_list[atomicAdd(&s_count, 1u)] = key;
+
+                    }
+                }
+            }
+            // at most top + 8 <= 72 threads, of 32 values or fewer each, add to the list in a step
+            __syncthreads();
+            if (s_count > kList - kMostPerStep) cut_list(s_list, &s_count, P.top);
+        }
     }
-    auto add = [](float a, float b) { return a + b; };
-    sum = block_reduce(sum, add, s_f);
-    dot = block_reduce(dot, add, s_f);
-    const float logsum = logf(sum), lse = shift + logsum;  // (-infinity for such a row)
-    if (threadIdx.x == 0) {
+    // the CTA's state, and its candidates
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s = join(s, State{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d), __shfl_xor_sync(0xffffffffu, s.dot, d)}, c);
+    if (lane == 0) s_part[warp] = s;
+    if (kTop && C > 1) cut_list(s_list, &s_count, P.top);
+    __syncthreads();
+    s = s_part[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) s = join(s, s_part[w], c);
+    uint32_t count = kTop ? s_count : 0;
+    if (C > 1) {
+        // to the first CTA of the cluster: the state, and at most `top` candidates
+        cluster_wait();
+        if (tid == 0) {
+            cluster.map_shared_rank(s_all, 0)[rank] = s;
+            if (kTop) cluster.map_shared_rank(s_counts, 0)[rank] = count;
+        }
+        if (kTop && rank > 0)
+            for (uint32_t i = tid; i < count; i += kThreads) cluster.map_shared_rank(s_sent, 0)[(rank - 1) * K3HUF_MAX_TOP + i] = s_list[i];
+        cluster_arrive();
+        cluster_wait();
+        if (rank > 0) return;
+        for (uint32_t r = 1; r < C; ++r) s = join(s, s_all[r], c);
+        if (kTop) {
+            for (uint32_t r = 1; r < C; ++r) {
+                for (uint32_t i = tid; i < s_counts[r]; i += kThreads) s_list[count + i] = s_sent[(r - 1) * K3HUF_MAX_TOP + i];
+                count += s_counts[r];
+            }
+            if (tid == 0) s_count = count;
+            __syncthreads();
+        }
+    }
+    // a row with no finite logit: sum is 0, lse -infinity
+    const bool none = s.sum == 0.f;
+    const float log2sum = log2f(s.sum), logsum = log2sum * kLn2;
+    auto log_prob = [&](float z) { return z == -INFINITY ? z : fmaf(z - s.m, P.scale, -logsum); };
+    if (tid == 0) {
         const int64_t t = ld_id(P.tokens, P.id_bytes, row);
         float lp = 0.f;
         if (t >= int64_t(P.vocab)) atomicOr(P.status, K3HUF_ST_TOKEN);
-        else if (t >= 0) {
-            const float z = ld_f32(x + t) * P.scale;
-            lp = z == -INFINITY ? z : (z - shift) - logsum;
-        }
+        else if (t >= 0) lp = log_prob(ld_f32(x + t));
         P.logprob[row] = lp;
-        if (P.entropy) P.entropy[row] = sum > 0.f ? logsum - dot / sum : sum;
-        if (P.lse) P.lse[row] = lse;
+        if (P.entropy) P.entropy[row] = none ? 0.f : logsum - s.dot / s.sum * kLn2;
+        if (P.lse) P.lse[row] = none ? -INFINITY : fmaf(s.m, P.scale, logsum);
     }
-    uint64_t below = ~0ull;
-    for (uint32_t k = 0; k < P.top; ++k) {
-        uint64_t best = 0;
-        for (uint32_t j = threadIdx.x; j < P.vocab; j += kThreads) {
-            const uint64_t key = key_of(ld_f32(x + j), j);
-            if (key < below && key > best) best = key;
+    if constexpr (kTop) {
+        if (count > 2 * kThreads) {
+            cut_list(s_list, &s_count, P.top);
+            count = s_count;
         }
-        below = block_reduce(best, [](uint64_t a, uint64_t b) { return a > b ? a : b; }, s_k);
-        if (threadIdx.x == 0) {
-            const uint32_t j = 0xFFFFFFFFu - uint32_t(below);
-            const float z = ld_f32(x + j) * P.scale;
-            P.top_ids[uint64_t(row) * P.top + k] = int32_t(j);
-            P.top_logprobs[uint64_t(row) * P.top + k] = z == -INFINITY ? z : (z - shift) - logsum;
+        for (uint32_t i = tid; i < count; i += kThreads) {
+            const uint64_t key = s_list[i];
+            uint32_t above = 0;
+            for (uint32_t k = 0; k < count; ++k) above += s_list[k] > key;
+            if (above >= P.top) continue;
+            const uint32_t j = 0xFFFFFFFFu - uint32_t(key);
+            P.top_ids[uint64_t(row) * P.top + above] = int32_t(j);
+            P.top_logprobs[uint64_t(row) * P.top + above] = log_prob(ld_f32(x + j));
         }
     }
 }
@@ -108,24 +384,116 @@ struct GradParams {
     const float *lse, *entropy, *g_logprob, *g_entropy;
     uint32_t *status;
     uint64_t stride, dx_stride;
-    uint32_t n, vocab, id_bytes;
+    uint32_t vocab, id_bytes;
     float scale;
 };
 
-template <typename T>
+constexpr int kGradVecs = 4;
+
+// kVec: logits and gradients sit alike in their 16-byte blocks
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads) logprob_grad_kernel(const GradParams P) {
-    const uint32_t row = blockIdx.x;
+    constexpr int E = kVec ? kPer<T> : 1;
+    const uint32_t row = blockIdx.y;
     const T *x = static_cast<const T *>(P.x) + uint64_t(row) * P.stride;
     T *dx = static_cast<T *>(P.dx) + uint64_t(row) * P.dx_stride;
+    const uint32_t shift = kVec ? uint32_t(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T)) : 0u;
     const int64_t t = ld_id(P.tokens, P.id_bytes, row);
-    if (t >= int64_t(P.vocab) && threadIdx.x == 0) atomicOr(P.status, K3HUF_ST_TOKEN);
-    const float g = t >= 0 && t < int64_t(P.vocab) ? P.g_logprob[row] : 0.f;
+    const bool scored = t >= 0 && t < int64_t(P.vocab);
+    if (!scored && t >= 0 && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(P.status, K3HUF_ST_TOKEN);
+    const float g = scored ? P.g_logprob[row] : 0.f;
     const float h = P.g_entropy ? P.g_entropy[row] : 0.f, ent = P.g_entropy ? P.entropy[row] : 0.f, lse = P.lse[row];
-    for (uint32_t j = threadIdx.x; j < P.vocab; j += kThreads) {
-        const float z = ld_f32(x + j) * P.scale, lp = z == -INFINITY ? z : z - lse, p = expf(lp);
-        const float d = p == 0.f ? 0.f : -p * (g + h * (lp + ent));   // (0 times infinity)
-        st_f32(dx + j, P.scale * (d + (int64_t(j) == t ? g : 0.f)));
+    auto grad = [&](float v, int64_t j) {
+        const float z = v * P.scale, lp = z == -INFINITY ? z : z - lse, p = exp2_fast(lp * kLog2e);
+        const float d = p == 0.f ? 0.f : -p * fmaf(h, lp + ent, g);       // (0 times infinity)
+        return P.scale * (j == t ? d + g : d);
+    };
+    const uint32_t vecs = (P.vocab + shift + E - 1) / E;
+    const uint32_t v0 = blockIdx.x * (kThreads * kGradVecs) + threadIdx.x;
+    if constexpr (kVec) {
+        uint4 v[kGradVecs];
+#pragma unroll
+        for (int i = 0; i < kGradVecs; ++i)
+            if (v0 + i * kThreads < vecs) v[i] = load_vec(x, shift, P.vocab, v0 + i * kThreads);
+#pragma unroll
+        for (int i = 0; i < kGradVecs; ++i) {
+            if (v0 + i * kThreads >= vecs) break;
+            const int64_t j = int64_t(v0 + i * kThreads) * E - shift;
+            float f[E];
+            unpack<T>(v[i], f);
+#pragma unroll
+            for (int k = 0; k < E; ++k) f[k] = grad(f[k], j + k);
+            if (j >= 0 && j + E <= int64_t(P.vocab)) {
+                uint4 o;
+                if constexpr (sizeof(T) == 4) {
+                    o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+                } else {
+                    __nv_bfloat162 *q = reinterpret_cast<__nv_bfloat162 *>(&o);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) q[k] = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+                }
+                __stcs(reinterpret_cast<uint4 *>(dx + j), o);
+            } else {
+#pragma unroll
+                for (int k = 0; k < E; ++k)
+                    if (j + k >= 0 && j + k < int64_t(P.vocab)) st_f32(dx + j + k, f[k]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kGradVecs; ++i) {
+            const uint32_t j = v0 + i * kThreads;
+            if (j < vecs) st_f32(dx + j, grad(ld_f32(x + j), j));
+        }
     }
+}
+
+template <typename T, bool kTop>
+int launch_forward(const LogprobParams &P, uint32_t n, cudaStream_t stream) {
+    // one CTA per row, or a cluster per row while the GPU has room for more CTAs (two or
+    // more per SM) and every CTA still has a step to do
+    constexpr uint32_t kStep = kThreads * kVecs * kPer<T>;
+    static std::atomic<uint64_t> wide{0};
+    const int rc = once_per_device(wide, [] { return cudaFuncSetAttribute(logprob_kernel<T, kTop>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
+    if (rc) return rc;
+    uint32_t C = 1;
+    while (C < uint32_t(kMaxCluster) && n * C < 304 && P.vocab / kStep >= 2 * C) C *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n * C);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_rc(cudaLaunchKernelEx(&cfg, logprob_kernel<T, kTop>, P));
+}
+
+template <typename T>
+int launch_backward(const GradParams &P, uint32_t n, cudaStream_t stream) {
+    const bool vec = (reinterpret_cast<uintptr_t>(P.x) - reinterpret_cast<uintptr_t>(P.dx)) % 16 == 0 &&
+                     (P.stride - P.dx_stride) * sizeof(T) % 16 == 0;
+    const uint32_t per = kThreads * kGradVecs * (vec ? kPer<T> : 1);
+    // (a row that starts inside a 16-byte block may need one vector more)
+    const uint32_t bx = uint32_t((uint64_t(P.vocab) + (vec ? kPer<T> - 1 : 0) + per - 1) / per);
+    for (uint32_t r0 = 0; r0 < n; r0 += 65535) {
+        GradParams Q = P;
+        Q.x = static_cast<const T *>(P.x) + uint64_t(r0) * P.stride;
+        Q.dx = static_cast<T *>(P.dx) + uint64_t(r0) * P.dx_stride;
+        Q.tokens = static_cast<const uint8_t *>(P.tokens) + uint64_t(r0) * P.id_bytes;
+        Q.lse += r0;
+        Q.g_logprob += r0;
+        if (Q.entropy) Q.entropy += r0;
+        if (Q.g_entropy) Q.g_entropy += r0;
+        const dim3 grid(bx, min(65535u, n - r0));
+        if (vec) logprob_grad_kernel<T, true><<<grid, kThreads, 0, stream>>>(Q);
+        else logprob_grad_kernel<T, false><<<grid, kThreads, 0, stream>>>(Q);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_rc(e);
+    }
+    return K3HUF_OK;
 }
 
 }  // namespace
@@ -144,11 +512,11 @@ extern "C" int k3huf_token_logprobs(const void *d_logits, uint32_t type, uint64_
         return K3HUF_E_ARG;
     if (n == 0) return K3HUF_OK;
     if (!d_logits || !d_tokens || !d_logprob || (top && (!d_top_ids || !d_top_logprobs))) return K3HUF_E_ARG;
-    LogprobParams P{d_logits, d_tokens, d_logprob, d_entropy, d_lse, d_top_logprobs, d_top_ids, d_status, stride, uint32_t(n), vocab, id_bytes, top, scale};
+    const LogprobParams P{d_logits, d_tokens, d_logprob, d_entropy, d_lse, d_top_logprobs, d_top_ids, d_status, stride, vocab, id_bytes, top, scale};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (type == K3HUF_BF16) logprob_kernel<__nv_bfloat16><<<uint32_t(n), kThreads, 0, st>>>(P);
-    else logprob_kernel<float><<<uint32_t(n), kThreads, 0, st>>>(P);
-    return cuda_rc(cudaGetLastError());
+    if (type == K3HUF_BF16)
+        return top ? launch_forward<__nv_bfloat16, true>(P, uint32_t(n), st) : launch_forward<__nv_bfloat16, false>(P, uint32_t(n), st);
+    return top ? launch_forward<float, true>(P, uint32_t(n), st) : launch_forward<float, false>(P, uint32_t(n), st);
 }
 
 extern "C" int k3huf_token_logprobs_grad(const void *d_logits, uint32_t type, uint64_t stride, uint64_t n, uint32_t vocab, float scale,
@@ -164,9 +532,7 @@ extern "C" int k3huf_token_logprobs_grad(const void *d_logits, uint32_t type, ui
     if (n == 0) return K3HUF_OK;
     if (!d_logits || !d_dlogits || !d_tokens || !d_lse || !d_g_logprob) return K3HUF_E_ARG;
     if (d_logits == d_dlogits && stride != out_stride) return K3HUF_E_ARG;
-    GradParams P{d_logits, d_dlogits, d_tokens, d_lse, d_entropy, d_g_logprob, d_g_entropy, d_status, stride, out_stride, uint32_t(n), vocab, id_bytes, scale};
+    const GradParams P{d_logits, d_dlogits, d_tokens, d_lse, d_entropy, d_g_logprob, d_g_entropy, d_status, stride, out_stride, vocab, id_bytes, scale};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (type == K3HUF_BF16) logprob_grad_kernel<__nv_bfloat16><<<uint32_t(n), kThreads, 0, st>>>(P);
-    else logprob_grad_kernel<float><<<uint32_t(n), kThreads, 0, st>>>(P);
-    return cuda_rc(cudaGetLastError());
+    return type == K3HUF_BF16 ? launch_backward<__nv_bfloat16>(P, uint32_t(n), st) : launch_backward<float>(P, uint32_t(n), st);
 }

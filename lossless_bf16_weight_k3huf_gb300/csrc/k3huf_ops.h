@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "k3huf_internal.h"
@@ -40,6 +41,19 @@ inline int cuda_rc(cudaError_t e) {
     if (e == cudaSuccess) return K3HUF_OK;
     set_cuda_error(int(e));
     return K3HUF_E_CUDA;
+}
+
+// Runs f (a cudaFuncSetAttribute or the like) at a kernel's first launch on
+// each device; two threads that do so at once set the same.
+template <typename F>
+int once_per_device(std::atomic<uint64_t> &done, F f) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= 64 || !((done.load(std::memory_order_acquire) >> dev) & 1))) {
+        e = f();
+        if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+    }
+    return cuda_rc(e);
 }
 
 }  // namespace k3huf
