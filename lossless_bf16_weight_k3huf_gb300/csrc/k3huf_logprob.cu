@@ -18,14 +18,18 @@
 // one's arithmetic.  What bounds it: the read of the logits from HBM; per
 // value one exponential and about six more instructions, half of them paired.
 //
-// Top alternatives in the same pass: an element can only be among the `top`
-// largest if it is not below the top-th largest of any set of elements.  Each
-// step counts the threads whose largest value reaches the threshold so far;
-// when they are more than a few, the threshold is raised to the top-th largest
-// of the threads' own largest values (bit by bit, one barrier count each).
-// Then few threads' values reach it and go to a list in shared memory, which
-// is cut to its `top` largest before it could overflow and ranked at the end.  Values as whole numbers with the index below
-// them make one order, so ties need no more.
+// Top alternatives in the same pass: a value can only be among the `top`
+// largest if it is not below the top-th largest of any set of values.  The
+// first step takes the top-th largest of 64 groups' largest values as the
+// threshold (bit by bit within a warp); from then on a thread notes the vectors
+// whose largest value reaches the threshold, without a barrier, and after steps
+// 1, 4, 16, ... the CTA reads the noted vectors
+// again, one value per thread, lists the keys that reach the threshold and cuts
+// the list to its `top` largest, the last of which is the new threshold.  Rows
+// that keep growing can fill the notes (ascending values): such a row's
+// alternatives are taken again in a second read that counts and raises the
+// threshold at every step.  A value's order as a whole number with its index
+// below it is one key, so ties need no more.
 //
 // Backward: elementwise, 16 bytes per thread and load, one read and one write.
 #include <cooperative_groups.h>
@@ -43,8 +47,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kVecs = 4;                      // 16-byte vectors per thread and step
 constexpr int kMaxCluster = 16;
-constexpr uint32_t kList = 4096;              // candidates held in shared memory
-constexpr uint32_t kMostPerStep = (K3HUF_MAX_TOP + 8) * kVecs * 8;
+constexpr uint32_t kNotes = 1024;             // vectors noted in shared memory, and keys listed
+constexpr uint32_t kList = 3072;
+static_assert((K3HUF_MAX_TOP + 8) * kVecs <= int(kNotes) && K3HUF_MAX_TOP + (K3HUF_MAX_TOP + 8) * kVecs * 8 <= int(kList), "a counted step's notes and keys");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // (value, index) order of the top alternatives: larger values first, ties to
@@ -106,6 +111,17 @@ __device__ __forceinline__ void unpack(const uint4 v, float (&f)[kPer<T>]) {
     }
 }
 
+template <typename T>
+__device__ __forceinline__ float vec_max(const uint4 v) {
+    if constexpr (sizeof(T) == 4) {
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    } else {
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
+        const __nv_bfloat162 a = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return fmaxf(__low2float(a), __high2float(a));
+    }
+}
+
 // Vector v of a row whose first value sits `shift` values into its 16-byte
 // block: values [v E - shift, v E - shift + E) of the row; those outside the
 // row read as -infinity.
@@ -150,21 +166,28 @@ struct LogprobParams {
     float scale;
 };
 
-// Cuts the list to its `top` largest keys.
-__device__ void cut_list(uint64_t *list, uint32_t *count, uint32_t top) {
+// Cuts the list to its `top` largest keys, the smallest of them last, and
+// notes whether keys were lost because it was full.
+__device__ void cut_list(uint64_t *list, uint32_t *count, uint32_t *lost, uint32_t top) {
     constexpr int kMine = kList / kThreads;
     __shared__ uint32_t s_above[2];
     __syncthreads();
-    const uint32_t n = *count;
-    if (n <= top) return;
+    const uint32_t n = min(*count, kList);
+    if (n < *count && threadIdx.x == 0) *lost = 1;
+    if (n < top) return;
     if (n <= 2 * kThreads) {
         // few: every key's rank is its place
         const uint64_t a = threadIdx.x < n ? list[threadIdx.x] : 0, b = threadIdx.x + kThreads < n ? list[threadIdx.x + kThreads] : 0;
         uint32_t above_a = 0, above_b = 0;
-        for (uint32_t i = 0; i < n; ++i) {
-            const uint64_t k = list[i];
-            above_a += k > a;
-            above_b += k > b;
+        if (n <= kThreads) {
+            if (a)
+                for (uint32_t i = 0; i < n; ++i) above_a += list[i] > a;
+        } else {
+            for (uint32_t i = 0; i < n; ++i) {
+                const uint64_t k = list[i];
+                above_a += k > a;
+                above_b += k > b;
+            }
         }
         __syncthreads();
         if (a && above_a < top) list[above_a] = a;
@@ -194,15 +217,17 @@ __device__ void cut_list(uint64_t *list, uint32_t *count, uint32_t top) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kMine; ++i)
-        if (mine[i] >= t) list[atomicAdd(count, 1u)] = mine[i];       // (keys differ: exactly `top` of them)
+        if (mine[i] > t) list[atomicAdd(count, 1u)] = mine[i];        // (keys differ: t is one, and the last)
+    __syncthreads();
+    if (threadIdx.x == 0) list[(*count)++] = t;
     __syncthreads();
 }
 
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) logprob_kernel(const LogprobParams P) {
+__global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParams P) {
     constexpr int E = kPer<T>;
     __shared__ State s_part[kWarps], s_all[kMaxCluster];
-    __shared__ uint32_t s_count, s_counts[kMaxCluster];
+    __shared__ uint32_t s_count, s_noted, s_lost, s_counts[kMaxCluster], s_notes[kTop ? kNotes : 1], s_group[kTop ? 64 : 1];
     __shared__ uint64_t s_list[kTop ? kList : 1], s_sent[kTop ? (kMaxCluster - 1) * K3HUF_MAX_TOP : 1];
     const cg::cluster_group cluster = cg::this_cluster();
     const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank(), row = blockIdx.x / C;
@@ -215,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) logprob_kernel(const L
     const uint32_t steps = (vecs + kThreads * kVecs - 1) / (kThreads * kVecs);
     const uint32_t step0 = uint32_t(uint64_t(steps) * rank / C), step1 = uint32_t(uint64_t(steps) * (rank + 1) / C);
     if (C > 1) cluster_arrive();                           // (waited for before the first remote store)
-    if (kTop && tid == 0) s_count = 0;
+    if (kTop && tid == 0) s_count = s_noted = s_lost = 0;
     if (kTop) __syncthreads();
 
     uint4 v[kVecs], next[kVecs];
@@ -231,24 +256,83 @@ __global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) logprob_kernel(const L
     // (-FLT_MAX, not -infinity: then -infinity minus it is -infinity)
     State s{-3.402823466e38f, 0.f, 0.f};
     uint64_t threshold = 0;
+    // Notes this step's vectors that reach the threshold; `first`: sets it first; `count`: raises
+    // it first where many do, so that at most top + 8 threads note any.
+    auto note = [&](uint32_t step, const float (&top_of)[kVecs], float big, bool first, bool count) {
+        const uint32_t few = P.top + 8, v0 = step * (kVecs * kThreads) + tid;
+        const uint32_t mine = v0 < vecs ? order_of(big) : 0u;
+        // (no value of this thread's step has a lower index than its first vector's first)
+        const uint32_t low = 0xFFFFFFFFu - (v0 ? v0 * E - shift : 0u);
+        auto reaches = [&](uint64_t t) { return mine && ((uint64_t(mine) << 32) | low) >= t; };
+        bool raised = false;
+        uint64_t t = 0;
+        if (first) {
+            // the top-th largest of the largest values of 64 groups of 4 threads
+            uint32_t of4 = max(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
+            of4 = max(of4, __shfl_xor_sync(0xffffffffu, of4, 2));
+            if (tid % 4 == 0) s_group[tid / 4] = of4;
+            __syncthreads();
+            const uint32_t a = s_group[lane], b = s_group[lane + 32];
+            uint32_t hi = 0;
+            for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1)
+                if (uint32_t(__popc(__ballot_sync(0xffffffffu, a >= (hi | bit))) + __popc(__ballot_sync(0xffffffffu, b >= (hi | bit)))) >= P.top) hi |= bit;
+            t = uint64_t(hi) << 32;
+            raised = true;
+        } else if (count && uint32_t(__syncthreads_count(reaches(threshold))) > few) {
+            // (the 16 high bits are a bf16 value; for fp32 a little lower a threshold)
+            t = kth_largest(uint64_t(mine) << 32, P.top, 0, 63, 48);
+            raised = true;
+        }
+        if (raised) {
+            // (0: fewer than `top` groups or threads have values at all)
+            if (t && uint32_t(__syncthreads_count((uint64_t(mine) << 32) >= t)) > (count ? few : 4 * few)) {
+                // many equal ones: the whole key of each thread's first largest value decides
+                uint64_t key = 0;
+#pragma unroll 1
+                for (int i = 0; i < kVecs; ++i)
+                    for (int k = 0; k < E; ++k) {
+                        const int64_t j = int64_t(v0 + i * kThreads) * E + k - shift;
+                        if (j >= 0 && j < int64_t(P.vocab)) key = max(key, key_of(ld_f32(x + j), uint32_t(j)));
+                    }
+                t = kth_largest(key, P.top, 0, 63, 0);
+            }
+            threshold = max(threshold, t);
+        }
+        if (reaches(threshold)) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                if (v0 + i * kThreads < vecs && order_of(top_of[i]) >= uint32_t(threshold >> 32)) {
+                    const uint32_t at = atomicAdd(&s_noted, 1u);
+                    if (at < kNotes) s_notes[at] = v0 + i * kThreads;
+                }
+        }
+    };
+    // Lists the noted vectors' keys and raises the threshold to the top-th largest so far.
+    auto raise = [&]() {
+        __syncthreads();
+        const uint32_t noted = min(s_noted, kNotes);
+        if (tid == 0 && s_noted > kNotes) s_lost = 1;
+        for (uint32_t i = tid; i < noted * E; i += kThreads) {
+            const int64_t j = int64_t(s_notes[i / E]) * E + i % E - shift;
+            if (j < 0 || j >= int64_t(P.vocab)) continue;
+            const uint64_t key = key_of(ld_f32(x + j), uint32_t(j));
+            if (key < threshold) continue;
+            const uint32_t at = atomicAdd(&s_count, 1u);
+            if (at < kList) s_list[at] = key;
+        }
+        cut_list(s_list, &s_count, &s_lost, P.top);
+        if (s_count >= P.top) threshold = max(threshold, s_list[P.top - 1]);
+        if (tid == 0) s_noted = 0;
+        __syncthreads();
+    };
     load(next, step0);
     for (uint32_t step = step0; step < step1; ++step) {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) v[i] = next[i];
         load(next, step + 1);
-        float big = -INFINITY;
+        float top_of[kVecs], big = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            if constexpr (sizeof(T) == 4) {
-                float f[E];
-                unpack<T>(v[i], f);
-                big = fmaxf(big, fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])));
-            } else {
-                const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v[i]);
-                const __nv_bfloat162 a = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-                big = fmaxf(big, fmaxf(__low2float(a), __high2float(a)));
-            }
-        }
+        for (int i = 0; i < kVecs; ++i) big = fmaxf(big, top_of[i] = vec_max<T>(v[i]));
         rescale(s, fmaxf(s.m, big), c);
         const float2 minus_m = make_float2(-s.m, -s.m), cc = make_float2(c, c);
         float2 sum = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
@@ -269,57 +353,31 @@ __global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) logprob_kernel(const L
         s.sum += sum.x + sum.y;
         s.dot += dot.x + dot.y;
         if constexpr (kTop) {
-            const uint32_t mine = step * (kVecs * kThreads) + tid < vecs ? order_of(big) : 0u;
-            const uint32_t reach = uint32_t(__syncthreads_count(mine >= uint32_t(threshold >> 32)));
-            if (reach == 0) continue;
-            const uint32_t few = P.top + 8;
-            if (reach > few) {
-                // (the 16 high bits are a bf16 value; for fp32 a little lower a threshold)
-                uint64_t t = kth_largest(uint64_t(mine) << 32, P.top, 0, 63, 48);
-                // (0: fewer than `top` threads have values at all)
-                if (t && uint32_t(__syncthreads_count((uint64_t(mine) << 32) >= t)) > few) {
-                    // many equal ones: the whole key of each thread's first largest value decides
-                    uint64_t key = 0;
+            note(step, top_of, big, step == step0, false);
+            const uint32_t done = step - step0;
+            if (step + 1 < step1 && done && (done & (done - 1)) == 0 && (done & 0x55555555u)) raise();
+        }
+    }
+    if constexpr (kTop) {
+        raise();
+        if (s_lost) {
+            threshold = 0;
+            if (tid == 0) s_count = 0;
+#pragma unroll 1
+            for (uint32_t step = step0; step < step1; ++step) {
+                load(v, step);
+                float top_of[kVecs], big = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < kVecs; ++i) {
-                        float f[E];
-                        unpack<T>(v[i], f);
-#pragma unroll
-                        for (int k = 0; k < E; ++k) {
-                            const int64_t j = int64_t((step * kVecs + i) * kThreads + tid) * E + k - shift;
-                            if (j >= 0 && j < int64_t(P.vocab)) key = max(key, key_of(f[k], uint32_t(j)));
-                        }
-                    }
-                    t = kth_largest(key, P.top, t, 47, 0);
-                }
-                threshold = max(threshold, t);
+                for (int i = 0; i < kVecs; ++i) big = fmaxf(big, top_of[i] = vec_max<T>(v[i]));
+                note(step, top_of, big, false, true);
+                raise();
             }
-            if (mine >= uint32_t(threshold >> 32)) {
-#pragma unroll
-                for (int i = 0; i < kVecs; ++i) {
-                    float f[E];
-                    unpack<T>(v[i], f);
-#pragma unroll
-                    for (int k = 0; k < E; ++k) {
-                        const int64_t j = int64_t((step * kVecs + i) * kThreads + tid) * E + k - shift;
-                        if (j < 0 || j >= int64_t(P.vocab)) continue;
-                        const uint64_t key = key_of(f[k], uint32_t(j));
-                        if (key < threshold) continue;
-                        s_list[atomicAdd(&s_count, 1u)] = key;
-
-                    }
-                }
-            }
-            // at most top + 8 <= 72 threads, of 32 values or fewer each, add to the list in a step
-            __syncthreads();
-            if (s_count > kList - kMostPerStep) cut_list(s_list, &s_count, P.top);
         }
     }
     // the CTA's state, and its candidates
 #pragma unroll
     for (int d = 16; d; d >>= 1) s = join(s, State{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d), __shfl_xor_sync(0xffffffffu, s.dot, d)}, c);
     if (lane == 0) s_part[warp] = s;
-    if (kTop && C > 1) cut_list(s_list, &s_count, P.top);
     __syncthreads();
     s = s_part[0];
 #pragma unroll
@@ -362,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) logprob_kernel(const L
     }
     if constexpr (kTop) {
         if (count > 2 * kThreads) {
-            cut_list(s_list, &s_count, P.top);
+            cut_list(s_list, &s_count, &s_lost, P.top);
             count = s_count;
         }
         for (uint32_t i = tid; i < count; i += kThreads) {
