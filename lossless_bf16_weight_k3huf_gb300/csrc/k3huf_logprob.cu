@@ -461,11 +461,17 @@ __global__ void __launch_bounds__(kThreads) logprob_grad_kernel(const GradParams
     if (!scored && t >= 0 && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(P.status, K3HUF_ST_TOKEN);
     const float g = scored ? P.g_logprob[row] : 0.f;
     const float h = P.g_entropy ? P.g_entropy[row] : 0.f, ent = P.g_entropy ? P.entropy[row] : 0.f, lse = P.lse[row];
-    auto grad = [&](float v, int64_t j) {
-        const float z = v * P.scale, lp = z == -INFINITY ? z : z - lse, p = exp2_fast(lp * kLog2e);
-        const float d = p == 0.f ? 0.f : -p * fmaf(h, lp + ent, g);       // (0 times infinity)
-        return P.scale * (j == t ? d + g : d);
+    // dx_j = p_j (hs lp_j + gs), and scale g more at the token; two values at a time.  A logit of
+    // -infinity, and one so low that p_j is 0, stop at kFloor: 0 times infinity is not 0.
+    const float hs = -h * P.scale, gs = -P.scale * fmaf(h, ent, g), base = lse == -INFINITY ? 0.f : -lse;
+    auto grad = [&](float2 v) {
+        float2 lp = __ffma2_rn(v, make_float2(P.scale, P.scale), make_float2(base, base));
+        lp.x = max_nan(lp.x, kFloor);
+        lp.y = max_nan(lp.y, kFloor);
+        const float2 a = __fmul2_rn(lp, make_float2(kLog2e, kLog2e));
+        return __fmul2_rn(make_float2(exp2_fast(a.x), exp2_fast(a.y)), __ffma2_rn(make_float2(hs, hs), lp, make_float2(gs, gs)));
     };
+    const uint32_t token = scored ? uint32_t(t) : 0xFFFFFFFFu;
     const uint32_t vecs = (P.vocab + shift + E - 1) / E;
     const uint32_t v0 = blockIdx.x * (kThreads * kGradVecs) + threadIdx.x;
     if constexpr (kVec) {
@@ -480,7 +486,16 @@ __global__ void __launch_bounds__(kThreads) logprob_grad_kernel(const GradParams
             float f[E];
             unpack<T>(v[i], f);
 #pragma unroll
-            for (int k = 0; k < E; ++k) f[k] = grad(f[k], j + k);
+            for (int k = 0; k < E; k += 2) {
+                const float2 d = grad(make_float2(f[k], f[k + 1]));
+                f[k] = d.x;
+                f[k + 1] = d.y;
+            }
+            if (token - uint32_t(j) < uint32_t(E)) {
+#pragma unroll
+                for (int k = 0; k < E; ++k)
+                    if (token == uint32_t(j) + k) f[k] = fmaf(P.scale, g, f[k]);
+            }
             if (j >= 0 && j + E <= int64_t(P.vocab)) {
                 uint4 o;
                 if constexpr (sizeof(T) == 4) {
@@ -501,7 +516,9 @@ __global__ void __launch_bounds__(kThreads) logprob_grad_kernel(const GradParams
 #pragma unroll
         for (int i = 0; i < kGradVecs; ++i) {
             const uint32_t j = v0 + i * kThreads;
-            if (j < vecs) st_f32(dx + j, grad(ld_f32(x + j), j));
+            if (j >= vecs) break;
+            const float d = grad(make_float2(ld_f32(x + j), 0.f)).x;
+            st_f32(dx + j, j == token ? fmaf(P.scale, g, d) : d);
         }
     }
 }
