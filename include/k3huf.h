@@ -475,7 +475,7 @@ int k3huf_ring_run_file(k3huf_ring *ring, k3huf_feed *feed, int n_layers, const 
 /* out[t] = scale * W[ids[t]] for tensor `tensor` of the layer as a row-major
  * table of `cols` columns: only the sub-streams that the rows meet are
  * decoded.  Any container (chunk and sub-stream sizes, rows that start
- * anywhere in a chunk); tables of up to 256 stripes.
+ * anywhere in a chunk); tables of up to 256 stripes and 2^31 - 1 columns.
  *  h_layer_hdr .. layer_bytes: as for k3huf_decode_layer;
  *  d_ids: n_tokens ids; a row of zeros is written for "none";
  *  d_out: n_tokens rows of `cols` elements of out_type, out_stride apart.

@@ -6,8 +6,16 @@
 //
 // Lookup: the container's chunk and sub-stream indexes give the first bit of
 // every run of sub_syms values, so the sub-streams that a row meets are
-// decoded and no others.  One thread decodes one sub-stream of one row, from
-// its recorded offset, a symbol per table lookup.
+// decoded and no others.  A unit is one sub-stream of one row; a warp takes up
+// to 32 of them (one per lane; fewer when a call has few, so that they spread
+// over the SMs), copies their bits to shared memory with 16-byte asynchronous
+// copies, and decodes 64 values of each at a time.  A lookup of the next 12
+// bits gives up to four whole codes (their mean length is under 3 bits), so a
+// sub-stream of 256 values takes about 70 dependent lookups instead of 256.
+// The warp then joins the 64 high bytes of each unit with the raw low bytes
+// (loaded before the decode), scales in fp32 and stores 16 bytes per lane.
+// What bounds it: a few units, the chain of lookups (about 55 cycles each)
+// after the table's build; many, the instructions of both halves.
 #include <algorithm>
 
 #include "k3huf_ops.h"
@@ -16,7 +24,12 @@ namespace k3huf {
 namespace {
 
 constexpr int kMaxStripes = 256;              // stripes of the tensor (kernel parameter space)
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;                 // (gradient and one-symbol lookup kernels)
+constexpr int kWarps = 16, kEmbedThreads = 32 * kWarps;
+constexpr uint32_t kPieces = 384;             // 16-byte pieces of bits staged per warp
+constexpr int kRound = 64;                    // values per unit between joins
+constexpr int kRowWords = kRound / 4 + 1;     // a unit's high bytes of one round; the odd stride spreads the banks
+constexpr uint32_t kMaxStagedSub = 1024;      // longest sub-stream whose bits surely fit a warp's pieces
 
 struct EmbedParams {
     const uint8_t *blob;
@@ -26,9 +39,11 @@ struct EmbedParams {
     uint64_t n_tokens, n_values, rows, cols, out_stride;
     uint64_t units;                           // work units per row: an upper bound of the sub-streams it meets
     uint32_t chunk_syms, sub_syms, id_bytes, n_stripes, table;
+    uint32_t lanes;                           // units per warp
     float scale;
     // canonical code of the tensor's table: codes of length l take the 12-bit
-    // windows [lo[l], hi[l]), in the order of sorted[adj[l] + (window >> (12 - l))]
+    // windows [lo[l], hi[l]), in the order of sorted[adj[l] + (window >> (12 - l))];
+    // longer codes take the lower windows
     uint16_t lo[K3HUF_MAXLEN + 1], hi[K3HUF_MAXLEN + 1];
     int16_t adj[K3HUF_MAXLEN + 1];
     uint8_t sorted[256];
@@ -41,72 +56,357 @@ __device__ __forceinline__ uint32_t bswap32(uint32_t x) { return __byte_perm(x, 
 // The 12-bit table, entry (symbol << 4) | length; 0 where no code is.
 __device__ void build_lut(const EmbedParams &P, uint16_t *lut) {
     for (uint32_t e = threadIdx.x; e < K3HUF_TABLE_ENTRIES; e += blockDim.x) {
-        uint32_t v = 0;
-        for (int l = 1; l <= K3HUF_MAXLEN && !v; ++l)
-            if (e >= P.lo[l] && e < P.hi[l]) v = (uint32_t(P.sorted[P.adj[l] + int(e >> (K3HUF_MAXLEN - l))]) << 4) | uint32_t(l);
-        lut[e] = uint16_t(v);
+        uint32_t l = K3HUF_MAXLEN;
+#pragma unroll
+        for (int k = 1; k < K3HUF_MAXLEN; ++k) l -= e >= P.lo[k];
+        lut[e] = uint16_t(e >= P.lo[l] && e < P.hi[l] ? (uint32_t(P.sorted[P.adj[l] + int(e >> (K3HUF_MAXLEN - l))]) << 4) | l : 0u);
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__ EmbedParams P) {
-    __shared__ uint16_t lut[K3HUF_TABLE_ENTRIES];
-    build_lut(P, lut);
-    __syncthreads();
-    const uint64_t w = uint64_t(blockIdx.x) * kThreads + threadIdx.x;
-    if (w >= P.n_tokens * P.units) return;
-    const uint64_t t = w / P.units, k = w - t * P.units;
-    const int64_t id = ld_id(P.ids, P.id_bytes, t);
-    T *out = static_cast<T *>(P.out) + t * P.out_stride;
-    if (id < 0 || uint64_t(id) >= P.rows) {
-        // no row: zeros, and the status bit for an id past the table
-        if (id >= 0 && k == 0) atomicOr(P.status, K3HUF_ST_TOKEN);
-        for (uint64_t c = k; c < P.cols; c += P.units) st_f32(out + c, 0.f);
-        return;
+// The table of up to four codes, from the 12-bit table: .x their symbols, .y
+// their bits [3:0], their number [6:4], and kBad where no code starts (which
+// counts as one symbol 0 of one bit).
+constexpr uint32_t kBad = 1u << 31;
+__device__ void build_lut4(const uint16_t *lut, uint2 *lut4) {
+    for (uint32_t e = threadIdx.x; e < K3HUF_TABLE_ENTRIES; e += blockDim.x) {
+        uint32_t syms = 0, bits = 0, count = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t v = lut[(e << bits) & (K3HUF_TABLE_ENTRIES - 1)], l = v & 15u;
+            if (count == uint32_t(k) && l && bits + l <= K3HUF_MAXLEN) {
+                syms |= (v >> 4) << (8 * k);
+                bits += l;
+                ++count;
+            }
+        }
+        lut4[e] = count ? make_uint2(syms, bits | (count << 4)) : make_uint2(0u, kBad | 17u);
     }
-    const uint32_t cs = P.chunk_syms, ss = P.sub_syms, S = cs / ss;
+}
+
+// One sub-stream of one row.
+struct Unit {
+    const uint8_t *bits, *even;               // the stripe's stream and low bytes
+    uint32_t a, len;                          // first value in the stripe, values
+    uint32_t off, end;                        // first bit, and the one after the last
+    uint32_t huff_bits;
+    int64_t col;                              // column of its first value (negative: the row starts inside)
+    uint64_t token;
+    bool any, none;                           // there is one; its row is zeros
+};
+
+// Unit k of token t.  Sets status bits for what it finds wrong.
+template <bool kFixed>
+__device__ Unit unit_of(const EmbedParams &P, uint64_t t, uint32_t k) {
+    Unit q{};
+    int64_t id = ld_id(P.ids, P.id_bytes, t);
+    q.token = t;
+    if (id < 0 || uint64_t(id) >= P.rows) {
+        if (id >= 0 && k == 0) atomicOr(P.status, K3HUF_ST_TOKEN);
+        q.none = true;                        // (the columns are dealt out as the first row's)
+        id = 0;
+    }
+    const uint32_t cs = kFixed ? 4096u : P.chunk_syms, ss = kFixed ? 256u : P.sub_syms, S = cs / ss;
     const uint32_t full = (K3HUF_STRIPE_VALUES + cs - 1) / cs * S;       // sub-streams of a full stripe
     const uint64_t v0 = uint64_t(id) * P.cols;
     const uint32_t l0 = uint32_t(v0 % K3HUF_STRIPE_VALUES);
     const uint64_t u = v0 / K3HUF_STRIPE_VALUES * full + uint64_t(l0 / cs) * S + l0 % cs / ss + k;
     const uint32_t si = uint32_t(u / full), g = uint32_t(u % full);
-    if (si >= P.n_stripes) return;
+    if (si >= P.n_stripes) return q;
     const uint64_t base = uint64_t(si) * K3HUF_STRIPE_VALUES;
     const uint32_t n = uint32_t(min(uint64_t(K3HUF_STRIPE_VALUES), P.n_values - base));
     const uint32_t c = g / S, j = g % S, nch = (n + cs - 1) / cs;
     // this sub-stream's values in the stripe, [a, b), and those of the row
-    const uint64_t a = uint64_t(c) * cs + uint64_t(j) * ss, b = min(a + ss, uint64_t(n));
-    if (a >= b || base + a >= v0 + P.cols || base + b <= v0) return;
+    const uint64_t a = uint64_t(c) * cs + uint64_t(j) * ss;
+    uint64_t b = min(min(a + ss, uint64_t(c) * cs + cs), uint64_t(n));
+    if (a >= b || base + a >= v0 + P.cols || base + b <= v0) return q;
+    q.any = true;
+    q.a = uint32_t(a);
+    q.len = uint32_t(b - a);
+    q.col = int64_t(base + a) - int64_t(v0);
+    if (q.none) return q;
     const uint8_t *stripe = P.blob + P.stripe[si];
-    const uint32_t *h = reinterpret_cast<const uint32_t *>(stripe);
-    const uint64_t region = si + 1 < P.n_stripes ? P.stripe[si + 1] - P.stripe[si] : P.last_bytes;
-    const uint64_t bits_need = ((uint64_t(h[4]) + 7) / 8 + 15) / 16 * 16 + kBitsSlack;
-    const uint64_t index = 4ull * nch + 2ull * nch * (S - 1);
-    if (h[0] != kStripeMagic || h[1] != P.table || h[2] != n || h[3] != nch || h[5] != 0 ||
-        h[6] != (K3HUF_STRIPE_HDR_BYTES + index + 15) / 16 * 16 || h[7] < h[6] + bits_need || uint64_t(h[7]) + n > region) {
-        atomicOr(P.status, K3HUF_ST_HEADER);
-        return;
-    }
-    const uint32_t huff_bits = h[4];
-    const uint32_t *chunk_off = h + K3HUF_STRIPE_HDR_BYTES / 4;
+    const uint4 *hv = reinterpret_cast<const uint4 *>(stripe);
+    const uint4 h0 = __ldg(hv), h1 = __ldg(hv + 1);
+    // (the index is read along with the header that says whether it is there: it
+    // lies inside the stripe by the host's check of the layer header)
+    const uint32_t *chunk_off = reinterpret_cast<const uint32_t *>(stripe + K3HUF_STRIPE_HDR_BYTES);
     const uint16_t *sub_off = reinterpret_cast<const uint16_t *>(chunk_off + nch);
-    const uint32_t *words = reinterpret_cast<const uint32_t *>(stripe + h[6]);
-    const uint8_t *even = stripe + h[7];
-    const uint32_t cb = chunk_off[c];
-    uint32_t pos = cb + (j ? uint32_t(sub_off[size_t(c) * (S - 1) + j - 1]) : 0u);
-    const uint32_t end = j + 1 < S ? cb + sub_off[size_t(c) * (S - 1) + j] : c + 1 < nch ? chunk_off[c + 1] : huff_bits;
-    uint32_t bad = 0;
-    for (uint64_t v = a; v < b; ++v) {
-        // (the stream is followed by 32 zero bytes, so word huff_bits / 32 + 1 is inside)
-        const uint32_t p = min(pos, huff_bits);
-        const uint32_t e = lut[__funnelshift_l(bswap32(words[p / 32 + 1]), bswap32(words[p / 32]), p) >> 20];
-        if (!(e & 15u)) bad = K3HUF_ST_BADCODE;
-        pos += max(e & 15u, 1u);
-        if (base + v >= v0 && base + v < v0 + P.cols)
-            st_f32(out + (base + v - v0), P.scale * __uint_as_float(((e >> 4) << 24) | (uint32_t(even[v]) << 16)));
+    const uint32_t cb = __ldg(chunk_off + c), ce = c + 1 < nch ? __ldg(chunk_off + c + 1) : h1.x;
+    const uint32_t sb = j ? uint32_t(__ldg(sub_off + size_t(c) * (S - 1) + j - 1)) : 0u;
+    const uint32_t se = j + 1 < S ? uint32_t(__ldg(sub_off + size_t(c) * (S - 1) + j)) : 0u;
+    const uint64_t region = si + 1 < P.n_stripes ? P.stripe[si + 1] - P.stripe[si] : P.last_bytes;
+    const uint64_t bits_need = ((uint64_t(h1.x) + 7) / 8 + 15) / 16 * 16 + kBitsSlack;
+    const uint64_t index = 4ull * nch + 2ull * nch * (S - 1);
+    if (h0.x != kStripeMagic || h0.y != P.table || h0.z != n || h0.w != nch || h1.y != 0 ||
+        h1.z != (K3HUF_STRIPE_HDR_BYTES + index + 15) / 16 * 16 || h1.w < h1.z + bits_need || h1.w % 16 != 0 || uint64_t(h1.w) + n > region) {
+        atomicOr(P.status, K3HUF_ST_HEADER);
+        q.none = true;                        // (zeros are written)
+        return q;
     }
-    if (pos != end) bad |= pos > huff_bits ? K3HUF_ST_OVERRUN : K3HUF_ST_INDEX;
+    q.huff_bits = h1.x;
+    q.bits = stripe + h1.z;
+    q.even = stripe + h1.w;
+    q.off = cb + sb;
+    q.end = j + 1 < S ? cb + se : ce;
+    return q;
+}
+
+// What the join needs of a unit, in shared memory.
+struct Join {
+    const uint8_t *even;                      // low byte of its first value (null: zeros)
+    uint8_t *out;                             // the row's first element
+    int32_t col;                              // column of its first value, at least -sub_syms
+    uint32_t len;
+};
+static_assert(sizeof(Join) == 24, "");
+
+constexpr size_t kWarpBytes = kPieces * 16 + 32 * kRowWords * 4 + 32 * sizeof(Join);
+constexpr size_t kEmbedSmem = K3HUF_TABLE_ENTRIES * (8 + 2) + kWarps * kWarpBytes;
+static_assert(kWarpBytes % 16 == 0, "16-byte pieces");
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src) : "memory");
+}
+
+// Eight values: their high bytes (two words) and low bytes, scaled.
+__device__ __forceinline__ void scaled8(uint32_t h0, uint32_t h1, uint2 even, float scale, float (&f)[8]) {
+    const uint32_t w[4] = {__byte_perm(even.x, h0, 0x5140), __byte_perm(even.x, h0, 0x7362), __byte_perm(even.y, h1, 0x5140), __byte_perm(even.y, h1, 0x7362)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = __fmul2_rn(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), make_float2(scale, scale));
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+    }
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&f)[8]) {
+    uint4 o;
+    __nv_bfloat162 *q = reinterpret_cast<__nv_bfloat162 *>(&o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    __stcs(reinterpret_cast<uint4 *>(p), o);
+}
+__device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(f[0], f[1], f[2], f[3]));
+    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+}
+
+// kVec: whole 8-value pieces (rows, sub-streams and output rows all start on them)
+template <typename T, bool kFixed, bool kVec>
+__global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_constant__ EmbedParams P) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint2 *lut4 = reinterpret_cast<uint2 *>(smem);
+    uint16_t *lut = reinterpret_cast<uint16_t *>(smem + K3HUF_TABLE_ENTRIES * 8);
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    uint8_t *slot = smem + K3HUF_TABLE_ENTRIES * 10 + warp * kWarpBytes;
+    uint32_t *row = reinterpret_cast<uint32_t *>(slot + kPieces * 16);
+    Join *join = reinterpret_cast<Join *>(slot + kPieces * 16 + 32 * kRowWords * 4);
+    const uint64_t total = P.n_tokens * P.units, items = (total + P.lanes - 1) / P.lanes;
+    uint64_t item = blockIdx.x + uint64_t(gridDim.x) * warp;
+    auto fetch = [&](uint64_t i) {
+        const uint64_t w = i * P.lanes + lane;
+        if (i >= items || lane >= P.lanes || w >= total) return Unit{};
+        const uint64_t t = w / P.units;
+        return unit_of<kFixed>(P, t, uint32_t(w - t * P.units));
+    };
+    Unit q = fetch(item);                     // (its loads are in flight while the tables are built)
+    build_lut(P, lut);
+    __syncthreads();
+    build_lut4(lut, lut4);
+    __syncthreads();
+    uint32_t bad = 0;
+    for (; item < items; item += uint64_t(gridDim.x) * kWarps) {
+        // what of the unit is wanted: decoding stops there
+        const uint32_t want = q.any ? uint32_t(min(int64_t(q.len), int64_t(P.cols) - q.col)) : 0u;
+        join[lane] = Join{q.none ? nullptr : q.even + q.a, static_cast<uint8_t *>(P.out) + q.token * P.out_stride * sizeof(T), int32_t(q.col), want};
+        const uint32_t live = q.none ? 0u : want;
+        // clamped, so that a corrupt index cannot move a read outside the stream
+        const uint32_t off = min(q.off, q.huff_bits), end = min(max(q.end, off), q.huff_bits);
+        const uint32_t byte0 = (off >> 7) << 4;
+        // (the last bits' piece and one more: a window reads two words ahead, and the stream
+        // has 32 bytes past its end; no more than the longest codes would take)
+        const uint32_t pieces = live ? min((end + 127) / 128 - byte0 / 16 + 1, (q.len * K3HUF_MAXLEN + 127) / 128 + 2) : 0u;
+        uint32_t before = pieces;             // pieces of the lanes up to this one
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, before, d);
+            if (lane >= uint32_t(d)) before += v;
+        }
+        __syncwarp();
+        const uint32_t longest = __reduce_max_sync(0xffffffffu, want);
+        uint32_t done = 0, first = 0;         // pieces and lanes of the passes so far
+        while (first < 32) {                  // one pass, unless the codes are long
+            const uint32_t over = __ballot_sync(0xffffffffu, lane >= first && before - done > kPieces);
+            const uint32_t last = over ? uint32_t(__ffs(over)) - 1 : 32u;
+            const bool in = lane >= first && lane < last;
+            const uint32_t mine = in ? live : 0u;
+            const uint32_t at = in ? before - done - pieces : 0u;
+            uint8_t *buf = slot + at * 16;
+            const uint32_t most = in ? pieces : 0u, copies = __reduce_max_sync(0xffffffffu, most);
+            for (uint32_t p = 0; p < copies; ++p)
+                if (p < most) cp_async16(buf + p * 16, q.bits + byte0 + p * 16);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            // low bytes of a round's pieces: unit 4 i + lane / 8, values 8 (lane % 8) ..
+            uint2 even[8];
+            auto load_even = [&](uint32_t v0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t u = 4 * i + lane / 8, v = v0 + lane % 8 * 8;
+                    const Join &J = join[u];
+                    even[i] = u >= first && u < last && v < J.len && J.even ? __ldg(reinterpret_cast<const uint2 *>(J.even + v)) : make_uint2(0, 0);
+                }
+            };
+            if (kVec) load_even(0);
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+            const uint32_t *words = reinterpret_cast<const uint32_t *>(buf);
+            const uint32_t max_word = most ? most * 4 - 1 : 0u;
+            uint32_t cur = off - byte0 * 8, next = cur / 32 + 2;
+            uint32_t w0 = most ? bswap32(words[cur / 32]) : 0u, w1 = most ? bswap32(words[min(cur / 32 + 1, max_word)]) : 0u;
+            uint32_t used = 0, pos = 0, fill = 0;
+            uint64_t acc = 0;
+            cur &= 31u;
+            auto advance = [&](uint32_t bits) {
+                used += bits;
+                cur += bits;
+                if (cur >= 32) {
+                    cur -= 32;
+                    w0 = w1;
+                    w1 = bswap32(words[min(next, max_word)]);
+                    ++next;
+                }
+            };
+            uint32_t *my_row = row + lane * kRowWords;
+            for (uint32_t r = 0; r < longest; r += kRound) {
+                const uint32_t stop = min(r + kRound, mine);
+                // up to four codes a lookup while four are wanted of the unit, then one
+                while (pos < stop) {
+                    const uint32_t window = __funnelshift_l(w1, w0, cur) >> 20;
+                    uint2 e;
+                    if (pos + 4 <= mine) {
+                        e = lut4[window];
+                    } else {
+                        const uint32_t v = lut[window];
+                        e = v ? make_uint2(v >> 4, (v & 15u) | 16u) : make_uint2(0u, kBad | 17u);
+                    }
+                    bad |= e.y;
+                    acc |= uint64_t(e.x) << (8 * fill);
+                    const uint32_t count = (e.y >> 4) & 7u;
+                    fill += count;
+                    pos += count;
+                    if (fill >= 4) {
+                        my_row[((pos - fill) - r) >> 2] = uint32_t(acc);
+                        acc >>= 32;
+                        fill -= 4;
+                    }
+                    advance(e.y & 15u);
+                }
+                if (pos == mine && fill && pos - fill >= r) my_row[((pos - fill) - r) >> 2] = uint32_t(acc);   // the last, partial word
+                __syncwarp();
+                // the join
+                if constexpr (kVec) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t u = 4 * i + lane / 8, s8 = lane % 8, v = r + s8 * 8;
+                        const Join J = join[u];
+                        const int32_t c = J.col + int32_t(v);
+                        if (u >= first && u < last && v < J.len && c >= 0) {
+                            const uint32_t *h = row + u * kRowWords + 2 * s8;
+                            float f[8] = {};
+                            if (J.even) scaled8(h[0], h[1], even[i], P.scale, f);
+                            store8(reinterpret_cast<T *>(J.out) + c, f);
+                        }
+                    }
+                    if (r + kRound < longest) load_even(r + kRound);
+                } else {
+                    for (uint32_t u = first; u < min(last, P.lanes); ++u) {
+                        const Join J = join[u];
+#pragma unroll
+                        for (int i = 0; i < kRound / 32; ++i) {
+                            const uint32_t s = i * 32 + lane, v = r + s;
+                            const int32_t c = J.col + int32_t(v);
+                            if (v < J.len && c >= 0) {
+                                float f = 0.f;
+                                if (J.even) f = P.scale * __uint_as_float((uint32_t(reinterpret_cast<const uint8_t *>(row + u * kRowWords)[s]) << 24) | (uint32_t(__ldg(J.even + v)) << 16));
+                                st_f32(reinterpret_cast<T *>(J.out) + c, f);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            // a whole sub-stream ends where the next one begins
+            if (mine && mine == q.len && off + used != q.end) bad |= off + used > q.huff_bits ? kBad >> 1 : kBad >> 2;
+            first = last;
+            done = __shfl_sync(0xffffffffu, before, last - 1);
+        }
+        __syncwarp();
+        q = fetch(item + uint64_t(gridDim.x) * kWarps);
+    }
+    const uint32_t found = (bad & kBad ? K3HUF_ST_BADCODE : 0u) | (bad & kBad >> 1 ? K3HUF_ST_OVERRUN : 0u) | (bad & kBad >> 2 ? K3HUF_ST_INDEX : 0u);
+    if (found) atomicOr(P.status, found);
+}
+
+// Containers with sub-streams longer than kMaxStagedSub: one thread decodes
+// one of them straight from global memory, a symbol per lookup.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) embed_long_kernel(const __grid_constant__ EmbedParams P) {
+    __shared__ uint16_t lut[K3HUF_TABLE_ENTRIES];
+    build_lut(P, lut);
+    __syncthreads();
+    const uint64_t w = uint64_t(blockIdx.x) * kThreads + threadIdx.x;
+    if (w >= P.n_tokens * P.units) return;
+    const uint64_t t = w / P.units;
+    const Unit q = unit_of<false>(P, t, uint32_t(w - t * P.units));
+    if (!q.any) return;
+    T *out = static_cast<T *>(P.out) + q.token * P.out_stride;
+    const uint32_t want = uint32_t(min(int64_t(q.len), int64_t(P.cols) - q.col));
+    const uint32_t *words = reinterpret_cast<const uint32_t *>(q.bits);
+    uint32_t pos = q.off, bad = 0;
+    for (uint32_t v = 0; v < want; ++v) {
+        float f = 0.f;
+        if (!q.none) {
+            // (the stream is followed by 32 zero bytes, so word huff_bits / 32 + 1 is inside)
+            const uint32_t p = min(pos, q.huff_bits);
+            const uint32_t e = lut[__funnelshift_l(bswap32(words[p / 32 + 1]), bswap32(words[p / 32]), p) >> 20];
+            if (!(e & 15u)) bad = K3HUF_ST_BADCODE;
+            pos += max(e & 15u, 1u);
+            f = P.scale * __uint_as_float(((e >> 4) << 24) | (uint32_t(q.even[q.a + v]) << 16));
+        }
+        if (q.col + int64_t(v) >= 0) st_f32(out + q.col + int64_t(v), f);
+    }
+    if (!q.none && want == q.len && pos != q.end) bad |= pos > q.huff_bits ? K3HUF_ST_OVERRUN : K3HUF_ST_INDEX;
     if (bad) atomicOr(P.status, bad);
+}
+
+template <typename T, bool kFixed, bool kVec>
+int launch_embed(const EmbedParams &P, uint32_t grid, cudaStream_t stream) {
+    static std::atomic<uint64_t> once{0};
+    const int rc = once_per_device(once, [] { return cudaFuncSetAttribute(embed_kernel<T, kFixed, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kEmbedSmem)); });
+    if (rc) return rc;
+    embed_kernel<T, kFixed, kVec><<<grid, kEmbedThreads, kEmbedSmem, stream>>>(P);
+    return cuda_rc(cudaGetLastError());
+}
+
+template <typename T>
+int launch_rows(EmbedParams &P, cudaStream_t stream) {
+    const uint64_t total = P.n_tokens * P.units;
+    if (P.sub_syms > kMaxStagedSub) {
+        const uint64_t blocks = (total + kThreads - 1) / kThreads;
+        if (blocks > 0x7FFFFFFFull) return K3HUF_E_ARG;
+        embed_long_kernel<T><<<uint32_t(blocks), kThreads, 0, stream>>>(P);
+        return cuda_rc(cudaGetLastError());
+    }
+    // as many units per warp as still give every SM a warp
+    uint64_t sms = 0;
+    const int rc = sm_count(&sms);
+    if (rc) return rc;
+    P.lanes = 32;
+    while (P.lanes > 4 && total < P.lanes * sms) P.lanes /= 2;
+    const uint32_t grid = uint32_t(std::min<uint64_t>(sms, (total + P.lanes - 1) / P.lanes));
+    const bool fixed = P.chunk_syms == 4096 && P.sub_syms == 256;
+    const bool vec = P.cols % 8 == 0 && P.sub_syms % 8 == 0 && aligned_to(P.out, 16) && P.out_stride * sizeof(T) % 16 == 0;
+    if (fixed) return vec ? launch_embed<T, true, true>(P, grid, stream) : launch_embed<T, true, false>(P, grid, stream);
+    return vec ? launch_embed<T, false, true>(P, grid, stream) : launch_embed<T, false, false>(P, grid, stream);
 }
 
 // One CTA per token; the first token of each id adds up all of that id, in
@@ -157,7 +457,7 @@ extern "C" int k3huf_embed_layer(const void *h_layer_hdr, size_t hdr_bytes, cons
     }
     if (layer_bytes < L.info.blob_bytes || tensor >= L.tensors.size()) return K3HUF_E_ARG;
     const TensorEntry &te = L.tensors[tensor];
-    if (te.n_values % cols != 0 || te.n_stripes > uint32_t(kMaxStripes) || out_stride < cols) return K3HUF_E_ARG;
+    if (te.n_values % cols != 0 || te.n_stripes > uint32_t(kMaxStripes) || out_stride < cols || cols >= (1ull << 31)) return K3HUF_E_ARG;
     if (n_tokens == 0) return K3HUF_OK;
     if (!d_ids || !d_out || n_tokens > (1ull << 31)) return K3HUF_E_ARG;
     EmbedParams P{};
@@ -194,12 +494,9 @@ extern "C" int k3huf_embed_layer(const void *h_layer_hdr, size_t hdr_bytes, cons
     }
     for (uint32_t s = 0; s < te.n_stripes; ++s) P.stripe[s] = L.stripes[te.first_stripe + s].blob_offset;
     P.last_bytes = L.info.blob_bytes - P.stripe[te.n_stripes - 1];
-    const uint64_t blocks = (n_tokens * P.units + kThreads - 1) / kThreads;
-    if (blocks > 0x7FFFFFFFull) return K3HUF_E_ARG;
+    if (P.units > 0xFFFFFFFFull || n_tokens > (1ull << 62) / P.units) return K3HUF_E_ARG;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (out_type == K3HUF_BF16) embed_kernel<__nv_bfloat16><<<uint32_t(blocks), kThreads, 0, st>>>(P);
-    else embed_kernel<float><<<uint32_t(blocks), kThreads, 0, st>>>(P);
-    return cuda_rc(cudaGetLastError());
+    return out_type == K3HUF_BF16 ? launch_rows<__nv_bfloat16>(P, st) : launch_rows<float>(P, st);
 }
 
 extern "C" int k3huf_embed_grad_scratch_bytes(uint64_t n_tokens, uint64_t rows, uint64_t cols, size_t *scratch_bytes) {

@@ -56,4 +56,17 @@ int once_per_device(std::atomic<uint64_t> &done, F f) {
     return cuda_rc(e);
 }
 
+// SMs of the current device.
+inline int sm_count(uint64_t *sms) {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) == 0) {
+        e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess) known[dev].store(n, std::memory_order_relaxed);
+    }
+    *sms = uint64_t(n > 0 ? n : 1);
+    return cuda_rc(e);
+}
+
 }  // namespace k3huf
