@@ -25,8 +25,8 @@ namespace {
 
 constexpr int kMaxStripes = 256;              // stripes of the tensor (kernel parameter space)
 constexpr int kThreads = 128;                 // (gradient and one-symbol lookup kernels)
-constexpr int kWarps = 16, kEmbedThreads = 32 * kWarps;
-constexpr uint32_t kPieces = 384;             // 16-byte pieces of bits staged per warp
+constexpr int kWarps = 24, kEmbedThreads = 32 * kWarps;
+constexpr uint32_t kPieces = 256;             // 16-byte pieces of bits staged per warp
 constexpr int kRound = 64;                    // values per unit between joins
 constexpr int kRowWords = kRound / 4 + 1;     // a unit's high bytes of one round; the odd stride spreads the banks
 constexpr uint32_t kMaxStagedSub = 1024;      // longest sub-stream whose bits surely fit a warp's pieces
@@ -46,41 +46,60 @@ struct EmbedParams {
     // longer codes take the lower windows
     uint16_t lo[K3HUF_MAXLEN + 1], hi[K3HUF_MAXLEN + 1];
     int16_t adj[K3HUF_MAXLEN + 1];
-    uint8_t sorted[256];
+    alignas(4) uint8_t sorted[256];
     uint64_t stripe[kMaxStripes];             // offset of each stripe in the container
     uint64_t last_bytes;                      // container bytes from the last stripe on
 };
 
 __device__ __forceinline__ uint32_t bswap32(uint32_t x) { return __byte_perm(x, 0, 0x0123); }
 
-// The 12-bit table, entry (symbol << 4) | length; 0 where no code is.
-__device__ void build_lut(const EmbedParams &P, uint16_t *lut) {
-    for (uint32_t e = threadIdx.x; e < K3HUF_TABLE_ENTRIES; e += blockDim.x) {
+// The canonical code in shared memory (its lookups differ from lane to lane,
+// which parameter space would serialise).
+struct Code {
+    uint32_t lo[K3HUF_MAXLEN + 1], hi[K3HUF_MAXLEN + 1];
+    int32_t adj[K3HUF_MAXLEN + 1];
+    uint8_t sorted[256];
+};
+
+// The 12-bit table, entry (symbol << 4) | length; 0 where no code is.  All of the CTA.
+__device__ void build_lut(const EmbedParams &P, Code &code, uint16_t *lut) {
+    const uint32_t t = threadIdx.x;
+    if (t <= K3HUF_MAXLEN) {
+        code.lo[t] = P.lo[t];
+        code.hi[t] = P.hi[t];
+        code.adj[t] = P.adj[t];
+    }
+    if (t < 64) reinterpret_cast<uint32_t *>(code.sorted)[t] = reinterpret_cast<const uint32_t *>(P.sorted)[t];
+    __syncthreads();
+    for (uint32_t e = t; e < K3HUF_TABLE_ENTRIES; e += blockDim.x) {
         uint32_t l = K3HUF_MAXLEN;
 #pragma unroll
         for (int k = 1; k < K3HUF_MAXLEN; ++k) l -= e >= P.lo[k];
-        lut[e] = uint16_t(e >= P.lo[l] && e < P.hi[l] ? (uint32_t(P.sorted[P.adj[l] + int(e >> (K3HUF_MAXLEN - l))]) << 4) | l : 0u);
+        lut[e] = uint16_t(e >= code.lo[l] && e < code.hi[l] ? (uint32_t(code.sorted[code.adj[l] + int(e >> (K3HUF_MAXLEN - l))]) << 4) | l : 0u);
     }
+    __syncthreads();
 }
 
 // The table of up to four codes, from the 12-bit table: .x their symbols, .y
-// their bits [3:0], their number [6:4], and kBad where no code starts (which
-// counts as one symbol 0 of one bit).
+// their bits [4:0], eight times their number [15:8], and kBad where no code
+// starts (which counts as one symbol 0 of one bit).
 constexpr uint32_t kBad = 1u << 31;
+__device__ __forceinline__ uint2 one_code(uint32_t v) { return v ? make_uint2(v >> 4, (v & 15u) | 0x800u) : make_uint2(0u, kBad | 0x801u); }
 __device__ void build_lut4(const uint16_t *lut, uint2 *lut4) {
     for (uint32_t e = threadIdx.x; e < K3HUF_TABLE_ENTRIES; e += blockDim.x) {
-        uint32_t syms = 0, bits = 0, count = 0;
+        uint2 f = one_code(lut[e]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t v = lut[(e << bits) & (K3HUF_TABLE_ENTRIES - 1)], l = v & 15u;
-            if (count == uint32_t(k) && l && bits + l <= K3HUF_MAXLEN) {
-                syms |= (v >> 4) << (8 * k);
-                bits += l;
-                ++count;
+        for (int k = 1; k < 4; ++k) {
+            // (a code that does not fit leaves the entry as it is, now and for the next k)
+            const uint32_t bits = f.y & 31u, v = lut[(e << bits) & (K3HUF_TABLE_ENTRIES - 1)], l = v & 15u;
+            if (l && bits + l <= K3HUF_MAXLEN && (f.y & 0xFF00u) == uint32_t(k) << 11) {
+                f.x |= (v >> 4) << (8 * k);
+                f.y += l + 0x800u;
             }
         }
-        lut4[e] = count ? make_uint2(syms, bits | (count << 4)) : make_uint2(0u, kBad | 17u);
+        lut4[e] = f;
     }
+    __syncthreads();
 }
 
 // One sub-stream of one row.
@@ -154,14 +173,14 @@ __device__ Unit unit_of(const EmbedParams &P, uint64_t t, uint32_t k) {
 // What the join needs of a unit, in shared memory.
 struct Join {
     const uint8_t *even;                      // low byte of its first value (null: zeros)
-    uint8_t *out;                             // the row's first element
-    int32_t col;                              // column of its first value, at least -sub_syms
-    uint32_t len;
+    uint8_t *out;                             // where its first value goes (before the row if it starts inside)
+    uint32_t skip, len;                       // its values [skip, len) are the row's
 };
 static_assert(sizeof(Join) == 24, "");
 
 constexpr size_t kWarpBytes = kPieces * 16 + 32 * kRowWords * 4 + 32 * sizeof(Join);
 constexpr size_t kEmbedSmem = K3HUF_TABLE_ENTRIES * (8 + 2) + kWarps * kWarpBytes;
+static_assert(kEmbedSmem + sizeof(Code) + 1024 + 64 <= 227 * 1024, "shared memory of one CTA");
 static_assert(kWarpBytes % 16 == 0, "16-byte pieces");
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
@@ -200,31 +219,36 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
     uint8_t *slot = smem + K3HUF_TABLE_ENTRIES * 10 + warp * kWarpBytes;
     uint32_t *row = reinterpret_cast<uint32_t *>(slot + kPieces * 16);
     Join *join = reinterpret_cast<Join *>(slot + kPieces * 16 + 32 * kRowWords * 4);
+    __shared__ Code code;
+    __shared__ uint32_t s_next;
     const uint64_t total = P.n_tokens * P.units, items = (total + P.lanes - 1) / P.lanes;
-    uint64_t item = blockIdx.x + uint64_t(gridDim.x) * warp;
     auto fetch = [&](uint64_t i) {
         const uint64_t w = i * P.lanes + lane;
         if (i >= items || lane >= P.lanes || w >= total) return Unit{};
-        const uint64_t t = w / P.units;
+        const uint64_t t = total <= 0xFFFFFFFFull ? uint32_t(w) / uint32_t(P.units) : w / P.units;
         return unit_of<kFixed>(P, t, uint32_t(w - t * P.units));
     };
+    // the CTA's items are every gridDim.x-th, handed out to its warps one by one
+    uint64_t item = blockIdx.x + uint64_t(gridDim.x) * warp;
     Unit q = fetch(item);                     // (its loads are in flight while the tables are built)
-    build_lut(P, lut);
-    __syncthreads();
+    if (threadIdx.x == 0) s_next = kWarps;
+    build_lut(P, code, lut);
     build_lut4(lut, lut4);
-    __syncthreads();
     uint32_t bad = 0;
-    for (; item < items; item += uint64_t(gridDim.x) * kWarps) {
+    while (item < items) {
         // what of the unit is wanted: decoding stops there
         const uint32_t want = q.any ? uint32_t(min(int64_t(q.len), int64_t(P.cols) - q.col)) : 0u;
-        join[lane] = Join{q.none ? nullptr : q.even + q.a, static_cast<uint8_t *>(P.out) + q.token * P.out_stride * sizeof(T), int32_t(q.col), want};
+        const uint32_t skip = q.col < 0 ? uint32_t(-q.col) : 0u;
+        join[lane] = Join{q.none ? nullptr : q.even + q.a, static_cast<uint8_t *>(P.out) + (int64_t(q.token * P.out_stride) + q.col) * int64_t(sizeof(T)), skip, want};
+        // nothing to check in the join: whole units of rows that are there
+        const bool plain = __all_sync(0xffffffffu, q.any && !q.none && q.col >= 0 && want == (kFixed ? 256u : P.sub_syms));
         const uint32_t live = q.none ? 0u : want;
         // clamped, so that a corrupt index cannot move a read outside the stream
         const uint32_t off = min(q.off, q.huff_bits), end = min(max(q.end, off), q.huff_bits);
         const uint32_t byte0 = (off >> 7) << 4;
-        // (the last bits' piece and one more: a window reads two words ahead, and the stream
-        // has 32 bytes past its end; no more than the longest codes would take)
-        const uint32_t pieces = live ? min((end + 127) / 128 - byte0 / 16 + 1, (q.len * K3HUF_MAXLEN + 127) / 128 + 2) : 0u;
+        // (a window may reach past the last piece, but no code that is taken does; no more than
+        // the longest codes would take, and one at least: the stream has 32 bytes past its end)
+        const uint32_t pieces = live ? min(max((end + 127) / 128 - byte0 / 16, 1u), (q.len * K3HUF_MAXLEN + 127) / 128 + 1) : 0u;
         uint32_t before = pieces;             // pieces of the lanes up to this one
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -245,6 +269,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
             for (uint32_t p = 0; p < copies; ++p)
                 if (p < most) cp_async16(buf + p * 16, q.bits + byte0 + p * 16);
             asm volatile("cp.async.commit_group;" ::: "memory");
+            const bool whole = plain && first == 0 && last == 32;
             // low bytes of a round's pieces: unit 4 i + lane / 8, values 8 (lane % 8) ..
             uint2 even[8];
             auto load_even = [&](uint32_t v0) {
@@ -252,7 +277,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
                 for (int i = 0; i < 8; ++i) {
                     const uint32_t u = 4 * i + lane / 8, v = v0 + lane % 8 * 8;
                     const Join &J = join[u];
-                    even[i] = u >= first && u < last && v < J.len && J.even ? __ldg(reinterpret_cast<const uint2 *>(J.even + v)) : make_uint2(0, 0);
+                    even[i] = whole || (u >= first && u < last && v < J.len && J.even) ? __ldg(reinterpret_cast<const uint2 *>(J.even + v)) : make_uint2(0, 0);
                 }
             };
             if (kVec) load_even(0);
@@ -260,60 +285,57 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
 
             const uint32_t *words = reinterpret_cast<const uint32_t *>(buf);
             const uint32_t max_word = most ? most * 4 - 1 : 0u;
-            uint32_t cur = off - byte0 * 8, next = cur / 32 + 2;
+            uint32_t cur = off - byte0 * 8;   // (the window's first bit, from the buffer's)
             uint32_t w0 = most ? bswap32(words[cur / 32]) : 0u, w1 = most ? bswap32(words[min(cur / 32 + 1, max_word)]) : 0u;
-            uint32_t used = 0, pos = 0, fill = 0;
-            uint64_t acc = 0;
-            cur &= 31u;
-            auto advance = [&](uint32_t bits) {
-                used += bits;
-                cur += bits;
-                if (cur >= 32) {
-                    cur -= 32;
+            const uint32_t cur0 = cur;
+            // high bytes that wait for a whole word: fill bits of them (0, 8, 16 or 24)
+            uint32_t acc = 0, fill = 0;
+            uint32_t *const my_row = row + lane * kRowWords;
+            auto take = [&](uint2 e, uint32_t *&to) {
+                bad |= e.y;
+                const uint32_t more = __funnelshift_l(e.x, 0u, fill);     // what does not fit in the word
+                acc |= e.x << fill;
+                fill += __byte_perm(e.y, 0u, 0x4441);
+                if (fill >= 32) {
+                    *to++ = acc;
+                    acc = more;
+                    fill -= 32;
+                }
+                const uint32_t was = cur;
+                cur += e.y & 31u;
+                if ((cur ^ was) & 32u) {
                     w0 = w1;
-                    w1 = bswap32(words[min(next, max_word)]);
-                    ++next;
+                    w1 = bswap32(words[min(cur / 32 + 1, max_word)]);
                 }
             };
-            uint32_t *my_row = row + lane * kRowWords;
             for (uint32_t r = 0; r < longest; r += kRound) {
-                const uint32_t stop = min(r + kRound, mine);
-                // up to four codes a lookup while four are wanted of the unit, then one
-                while (pos < stop) {
-                    const uint32_t window = __funnelshift_l(w1, w0, cur) >> 20;
-                    uint2 e;
-                    if (pos + 4 <= mine) {
-                        e = lut4[window];
+                if (r < mine) {
+                    uint32_t *to = my_row;
+                    if (r + kRound + 4 <= mine) {
+                        while (to < my_row + kRound / 4) take(lut4[__funnelshift_l(w1, w0, cur) >> 20], to);
                     } else {
-                        const uint32_t v = lut[window];
-                        e = v ? make_uint2(v >> 4, (v & 15u) | 16u) : make_uint2(0u, kBad | 17u);
+                        // the last rounds: four codes a lookup while four are wanted, then one
+                        for (;;) {
+                            const uint32_t pos = r + uint32_t(to - my_row) * 4 + fill / 8;
+                            if (pos >= mine || to >= my_row + kRound / 4) break;
+                            const uint32_t window = __funnelshift_l(w1, w0, cur) >> 20;
+                            take(pos + 4 <= mine ? lut4[window] : one_code(lut[window]), to);
+                        }
+                        if (to < my_row + kRound / 4) *to = acc;          // a partial word
                     }
-                    bad |= e.y;
-                    acc |= uint64_t(e.x) << (8 * fill);
-                    const uint32_t count = (e.y >> 4) & 7u;
-                    fill += count;
-                    pos += count;
-                    if (fill >= 4) {
-                        my_row[((pos - fill) - r) >> 2] = uint32_t(acc);
-                        acc >>= 32;
-                        fill -= 4;
-                    }
-                    advance(e.y & 15u);
                 }
-                if (pos == mine && fill && pos - fill >= r) my_row[((pos - fill) - r) >> 2] = uint32_t(acc);   // the last, partial word
                 __syncwarp();
                 // the join
                 if constexpr (kVec) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const uint32_t u = 4 * i + lane / 8, s8 = lane % 8, v = r + s8 * 8;
-                        const Join J = join[u];
-                        const int32_t c = J.col + int32_t(v);
-                        if (u >= first && u < last && v < J.len && c >= 0) {
+                        const Join &J = join[u];
+                        if (whole || (u >= first && u < last && v >= J.skip && v < J.len)) {
                             const uint32_t *h = row + u * kRowWords + 2 * s8;
                             float f[8] = {};
-                            if (J.even) scaled8(h[0], h[1], even[i], P.scale, f);
-                            store8(reinterpret_cast<T *>(J.out) + c, f);
+                            if (whole || J.even) scaled8(h[0], h[1], even[i], P.scale, f);
+                            store8(reinterpret_cast<T *>(J.out) + v, f);
                         }
                     }
                     if (r + kRound < longest) load_even(r + kRound);
@@ -323,11 +345,10 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
 #pragma unroll
                         for (int i = 0; i < kRound / 32; ++i) {
                             const uint32_t s = i * 32 + lane, v = r + s;
-                            const int32_t c = J.col + int32_t(v);
-                            if (v < J.len && c >= 0) {
+                            if (v >= J.skip && v < J.len) {
                                 float f = 0.f;
                                 if (J.even) f = P.scale * __uint_as_float((uint32_t(reinterpret_cast<const uint8_t *>(row + u * kRowWords)[s]) << 24) | (uint32_t(__ldg(J.even + v)) << 16));
-                                st_f32(reinterpret_cast<T *>(J.out) + c, f);
+                                st_f32(reinterpret_cast<T *>(J.out) + v, f);
                             }
                         }
                     }
@@ -335,12 +356,15 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
                 __syncwarp();
             }
             // a whole sub-stream ends where the next one begins
-            if (mine && mine == q.len && off + used != q.end) bad |= off + used > q.huff_bits ? kBad >> 1 : kBad >> 2;
+            const uint32_t past = off + (cur - cur0);
+            if (mine && mine == q.len && past != q.end) bad |= past > q.huff_bits ? kBad >> 1 : kBad >> 2;
             first = last;
             done = __shfl_sync(0xffffffffu, before, last - 1);
         }
         __syncwarp();
-        q = fetch(item + uint64_t(gridDim.x) * kWarps);
+        uint32_t k = lane == 0 ? atomicAdd(&s_next, 1u) : 0u;
+        item = blockIdx.x + uint64_t(gridDim.x) * __shfl_sync(0xffffffffu, k, 0);
+        q = fetch(item);
     }
     const uint32_t found = (bad & kBad ? K3HUF_ST_BADCODE : 0u) | (bad & kBad >> 1 ? K3HUF_ST_OVERRUN : 0u) | (bad & kBad >> 2 ? K3HUF_ST_INDEX : 0u);
     if (found) atomicOr(P.status, found);
@@ -351,8 +375,8 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
 template <typename T>
 __global__ void __launch_bounds__(kThreads) embed_long_kernel(const __grid_constant__ EmbedParams P) {
     __shared__ uint16_t lut[K3HUF_TABLE_ENTRIES];
-    build_lut(P, lut);
-    __syncthreads();
+    __shared__ Code code;
+    build_lut(P, code, lut);
     const uint64_t w = uint64_t(blockIdx.x) * kThreads + threadIdx.x;
     if (w >= P.n_tokens * P.units) return;
     const uint64_t t = w / P.units;
