@@ -39,7 +39,8 @@ struct EmbedParams {
     uint64_t n_tokens, n_values, rows, cols, out_stride;
     uint64_t units;                           // work units per row: an upper bound of the sub-streams it meets
     uint32_t chunk_syms, sub_syms, id_bytes, n_stripes, table;
-    uint32_t lanes;                           // units per warp
+    uint32_t lanes;                           // units per warp and item
+    uint64_t total, items;                    // units and items of the call
     float scale;
     // canonical code of the tensor's table: codes of length l take the 12-bit
     // windows [lo[l], hi[l]), in the order of sorted[adj[l] + (window >> (12 - l))];
@@ -61,45 +62,68 @@ struct Code {
     uint8_t sorted[256];
 };
 
-// The 12-bit table, entry (symbol << 4) | length; 0 where no code is.  All of the CTA.
-__device__ void build_lut(const EmbedParams &P, Code &code, uint16_t *lut) {
-    const uint32_t t = threadIdx.x;
+// Barrier 1 of the threads that build tables.
+__device__ __forceinline__ void build_sync(uint32_t threads) { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
+
+// The 12-bit table, entry (symbol << 4) | length; 0 where no code is.  By
+// threads 0 .. n - 1 (n a multiple of 32, at least 64); t < n is this one.
+// Eight entries per thread and step: a code of 9 bits or fewer that holds the
+// first of them holds all.  (Rolled loops here and in build_lut4: every
+// instruction runs once or a few times, and fresh ones cost instruction-cache
+// fills, which took most of an unrolled build's time.)
+__device__ void build_lut(const EmbedParams &P, Code &code, uint16_t *lut, uint32_t t, uint32_t n) {
     if (t <= K3HUF_MAXLEN) {
         code.lo[t] = P.lo[t];
         code.hi[t] = P.hi[t];
         code.adj[t] = P.adj[t];
     }
     if (t < 64) reinterpret_cast<uint32_t *>(code.sorted)[t] = reinterpret_cast<const uint32_t *>(P.sorted)[t];
-    __syncthreads();
-    for (uint32_t e = t; e < K3HUF_TABLE_ENTRIES; e += blockDim.x) {
-        uint32_t l = K3HUF_MAXLEN;
+    build_sync(n);
+    for (uint32_t m = t; m < K3HUF_TABLE_ENTRIES / 8; m += n) {
+        uint32_t v = 0;
+        bool whole = false;
+#pragma unroll 1
+        for (uint32_t e = 8 * m; e < 8 * m + 8 && !whole; ++e) {
+            uint32_t l = K3HUF_MAXLEN;
 #pragma unroll
-        for (int k = 1; k < K3HUF_MAXLEN; ++k) l -= e >= P.lo[k];
-        lut[e] = uint16_t(e >= code.lo[l] && e < code.hi[l] ? (uint32_t(code.sorted[code.adj[l] + int(e >> (K3HUF_MAXLEN - l))]) << 4) | l : 0u);
+            for (int k = 1; k < K3HUF_MAXLEN; ++k) l -= e >= P.lo[k];
+            v = e >= code.lo[l] && e < code.hi[l] ? (uint32_t(code.sorted[code.adj[l] + int(e >> (K3HUF_MAXLEN - l))]) << 4) | l : 0u;
+            lut[e] = uint16_t(v);
+            whole = e == 8 * m && v && l <= K3HUF_MAXLEN - 3;
+        }
+        v |= v << 16;
+        if (whole) reinterpret_cast<uint4 *>(lut)[m] = make_uint4(v, v, v, v);
     }
-    __syncthreads();
+    build_sync(n);
 }
 
 // The table of up to four codes, from the 12-bit table: .x their symbols, .y
 // their bits [4:0], eight times their number [15:8], and kBad where no code
-// starts (which counts as one symbol 0 of one bit).
+// starts (which counts as one symbol 0 of one bit).  Eight entries per thread
+// and step share the codes of their common 9 bits; each then takes up to two
+// more (a third would seldom fit, and an entry need not be full).
 constexpr uint32_t kBad = 1u << 31;
 __device__ __forceinline__ uint2 one_code(uint32_t v) { return v ? make_uint2(v >> 4, (v & 15u) | 0x800u) : make_uint2(0u, kBad | 0x801u); }
-__device__ void build_lut4(const uint16_t *lut, uint2 *lut4) {
-    for (uint32_t e = threadIdx.x; e < K3HUF_TABLE_ENTRIES; e += blockDim.x) {
-        uint2 f = one_code(lut[e]);
-#pragma unroll
-        for (int k = 1; k < 4; ++k) {
-            // (a code that does not fit leaves the entry as it is, now and for the next k)
-            const uint32_t bits = f.y & 31u, v = lut[(e << bits) & (K3HUF_TABLE_ENTRIES - 1)], l = v & 15u;
-            if (l && bits + l <= K3HUF_MAXLEN && (f.y & 0xFF00u) == uint32_t(k) << 11) {
-                f.x |= (v >> 4) << (8 * k);
-                f.y += l + 0x800u;
-            }
-        }
-        lut4[e] = f;
+// f with the code that starts after its bits of window e, if there is one within `room` bits and four are not there yet
+__device__ __forceinline__ uint2 one_more(uint2 f, uint32_t e, uint32_t room, const uint16_t *lut) {
+    const uint32_t bits = f.y & 31u, v = lut[(e << bits) & (K3HUF_TABLE_ENTRIES - 1)], l = v & 15u, at = f.y >> 8;
+    if (l && bits + l <= room && at < 32) {
+        f.x |= (v >> 4) << at;
+        f.y += l + 0x800u;
     }
-    __syncthreads();
+    return f;
+}
+__device__ void build_lut4(const uint16_t *lut, uint2 *lut4, uint32_t t, uint32_t n) {
+    for (uint32_t m = t; m < K3HUF_TABLE_ENTRIES / 8; m += n) {
+        uint2 shared = make_uint2(0u, 0u);
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) shared = one_more(shared, 8 * m, K3HUF_MAXLEN - 3, lut);
+#pragma unroll 1
+        for (uint32_t e = 8 * m; e < 8 * m + 8; ++e) {
+            const uint2 f = one_more(one_more(shared, e, K3HUF_MAXLEN, lut), e, K3HUF_MAXLEN, lut);
+            lut4[e] = f.y ? f : one_code(0);
+        }
+    }
 }
 
 // One sub-stream of one row.
@@ -221,7 +245,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
     Join *join = reinterpret_cast<Join *>(slot + kPieces * 16 + 32 * kRowWords * 4);
     __shared__ Code code;
     __shared__ uint32_t s_next;
-    const uint64_t total = P.n_tokens * P.units, items = (total + P.lanes - 1) / P.lanes;
+    const uint64_t total = P.total, items = P.items;
     auto fetch = [&](uint64_t i) {
         const uint64_t w = i * P.lanes + lane;
         if (i >= items || lane >= P.lanes || w >= total) return Unit{};
@@ -230,10 +254,20 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
     };
     // the CTA's items are every gridDim.x-th, handed out to its warps one by one
     uint64_t item = blockIdx.x + uint64_t(gridDim.x) * warp;
-    Unit q = fetch(item);                     // (its loads are in flight while the tables are built)
     if (threadIdx.x == 0) s_next = kWarps;
-    build_lut(P, code, lut);
-    build_lut4(lut, lut4);
+    // the tables; where only one warp has an item, it looks that up meanwhile
+    const bool few = items <= gridDim.x;
+    Unit q;
+    if (few && warp == 0) {
+        q = fetch(item);
+    } else {
+        const uint32_t n = few ? kEmbedThreads - 32 : kEmbedThreads, t = threadIdx.x - (kEmbedThreads - n);
+        if (!few) q = fetch(item);
+        build_lut(P, code, lut, t, n);
+        build_lut4(lut, lut4, t, n);
+    }
+    __syncthreads();
+    if (few && warp > 0) return;
     uint32_t bad = 0;
     while (item < items) {
         // what of the unit is wanted: decoding stops there
@@ -275,6 +309,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
             auto load_even = [&](uint32_t v0) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
+                    if (4u * i >= P.lanes) break;
                     const uint32_t u = 4 * i + lane / 8, v = v0 + lane % 8 * 8;
                     const Join &J = join[u];
                     even[i] = whole || (u >= first && u < last && v < J.len && J.even) ? __ldg(reinterpret_cast<const uint2 *>(J.even + v)) : make_uint2(0, 0);
@@ -284,42 +319,75 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
             asm volatile("cp.async.wait_group 0;" ::: "memory");
 
             const uint32_t *words = reinterpret_cast<const uint32_t *>(buf);
-            const uint32_t max_word = most ? most * 4 - 1 : 0u;
-            uint32_t cur = off - byte0 * 8;   // (the window's first bit, from the buffer's)
-            uint32_t w0 = most ? bswap32(words[cur / 32]) : 0u, w1 = most ? bswap32(words[min(cur / 32 + 1, max_word)]) : 0u;
+            const uint32_t max_word = most ? most * 4 - 1 : 0u;       // (a window's words past it hold no bit that is taken)
+            uint32_t cur = off - byte0 * 8;   // the next bit, from the buffer's first
             const uint32_t cur0 = cur;
+            // the 64 bits from `cur` on
+            auto window = [&](uint32_t &hi, uint32_t &lo) {
+                const uint32_t i = cur / 32;
+                const uint32_t w0 = bswap32(words[min(i, max_word)]), w1 = bswap32(words[min(i + 1, max_word)]), w2 = bswap32(words[min(i + 2, max_word)]);
+                hi = __funnelshift_l(w1, w0, cur);
+                lo = __funnelshift_l(w2, w1, cur);
+            };
             // high bytes that wait for a whole word: fill bits of them (0, 8, 16 or 24)
             uint32_t acc = 0, fill = 0;
             uint32_t *const my_row = row + lane * kRowWords;
+            // (selects, not branches: in most steps some lane fills a word)
             auto take = [&](uint2 e, uint32_t *&to) {
                 bad |= e.y;
                 const uint32_t more = __funnelshift_l(e.x, 0u, fill);     // what does not fit in the word
                 acc |= e.x << fill;
                 fill += __byte_perm(e.y, 0u, 0x4441);
-                if (fill >= 32) {
-                    *to++ = acc;
-                    acc = more;
-                    fill -= 32;
-                }
-                const uint32_t was = cur;
-                cur += e.y & 31u;
-                if ((cur ^ was) & 32u) {
-                    w0 = w1;
-                    w1 = bswap32(words[min(cur / 32 + 1, max_word)]);
-                }
+                const bool full = fill >= 32;
+                if (full) *to = acc;
+                to += full;
+                acc = full ? more : acc;
+                fill &= 31u;
             };
             for (uint32_t r = 0; r < longest; r += kRound) {
                 if (r < mine) {
                     uint32_t *to = my_row;
                     if (r + kRound + 4 <= mine) {
-                        while (to < my_row + kRound / 4) take(lut4[__funnelshift_l(w1, w0, cur) >> 20], to);
+                        // 16 lookups give 64 values at most, so they need no test for the round's end.
+                        // A window holds the bits of four of them (48 at most); an entry's low five bits
+                        // are the shift, and its low byte adds up
+#pragma unroll 2
+                        for (int k = 0; k < kRound / 16; ++k) {
+                            uint32_t hi, lo, sum = 0;
+                            window(hi, lo);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint2 e = lut4[hi >> 20];
+                                hi = __funnelshift_l(lo, hi, e.y);
+                                lo <<= e.y & 31u;
+                                sum += e.y;
+                                take(e, to);
+                            }
+                            cur += sum & 255u;
+                        }
+                        while (to < my_row + kRound / 4) {
+                            uint32_t hi, lo;
+                            window(hi, lo);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (to >= my_row + kRound / 4) break;
+                                const uint2 e = lut4[hi >> 20];
+                                hi = __funnelshift_l(lo, hi, e.y);
+                                lo <<= e.y & 31u;
+                                cur += e.y & 31u;
+                                take(e, to);
+                            }
+                        }
                     } else {
                         // the last rounds: four codes a lookup while four are wanted, then one
                         for (;;) {
                             const uint32_t pos = r + uint32_t(to - my_row) * 4 + fill / 8;
                             if (pos >= mine || to >= my_row + kRound / 4) break;
-                            const uint32_t window = __funnelshift_l(w1, w0, cur) >> 20;
-                            take(pos + 4 <= mine ? lut4[window] : one_code(lut[window]), to);
+                            uint32_t hi, lo;
+                            window(hi, lo);
+                            const uint2 e = pos + 4 <= mine ? lut4[hi >> 20] : one_code(lut[hi >> 20]);
+                            cur += e.y & 31u;
+                            take(e, to);
                         }
                         if (to < my_row + kRound / 4) *to = acc;          // a partial word
                     }
@@ -329,6 +397,7 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
                 if constexpr (kVec) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
+                        if (4u * i >= P.lanes) break;
                         const uint32_t u = 4 * i + lane / 8, s8 = lane % 8, v = r + s8 * 8;
                         const Join &J = join[u];
                         if (whole || (u >= first && u < last && v >= J.skip && v < J.len)) {
@@ -376,7 +445,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) embed_long_kernel(const __grid_constant__ EmbedParams P) {
     __shared__ uint16_t lut[K3HUF_TABLE_ENTRIES];
     __shared__ Code code;
-    build_lut(P, code, lut);
+    build_lut(P, code, lut, threadIdx.x, kThreads);
     const uint64_t w = uint64_t(blockIdx.x) * kThreads + threadIdx.x;
     if (w >= P.n_tokens * P.units) return;
     const uint64_t t = w / P.units;
@@ -413,20 +482,21 @@ int launch_embed(const EmbedParams &P, uint32_t grid, cudaStream_t stream) {
 
 template <typename T>
 int launch_rows(EmbedParams &P, cudaStream_t stream) {
-    const uint64_t total = P.n_tokens * P.units;
+    const uint64_t total = P.total = P.n_tokens * P.units;
     if (P.sub_syms > kMaxStagedSub) {
         const uint64_t blocks = (total + kThreads - 1) / kThreads;
         if (blocks > 0x7FFFFFFFull) return K3HUF_E_ARG;
         embed_long_kernel<T><<<uint32_t(blocks), kThreads, 0, stream>>>(P);
         return cuda_rc(cudaGetLastError());
     }
-    // as many units per warp as still give every SM a warp
+    // units per item: 32, fewer while the call has one item per SM or less
     uint64_t sms = 0;
     const int rc = sm_count(&sms);
     if (rc) return rc;
     P.lanes = 32;
-    while (P.lanes > 4 && total < P.lanes * sms) P.lanes /= 2;
-    const uint32_t grid = uint32_t(std::min<uint64_t>(sms, (total + P.lanes - 1) / P.lanes));
+    while (P.lanes > 4 && total <= P.lanes / 2 * sms) P.lanes /= 2;
+    P.items = (total + P.lanes - 1) / P.lanes;
+    const uint32_t grid = uint32_t(std::min<uint64_t>(sms, P.items));
     const bool fixed = P.chunk_syms == 4096 && P.sub_syms == 256;
     const bool vec = P.cols % 8 == 0 && P.sub_syms % 8 == 0 && aligned_to(P.out, 16) && P.out_stride * sizeof(T) % 16 == 0;
     if (fixed) return vec ? launch_embed<T, true, true>(P, grid, stream) : launch_embed<T, true, false>(P, grid, stream);
