@@ -89,6 +89,8 @@ def library_path() -> str:
 def _lib():
     """Load the library; raises if it was not built (no fallback)."""
     global _lib_handle
+    if _lib_handle is not None:
+        return _lib_handle
     with _lock:
         if _lib_handle is None:
             if not os.path.exists(_build.LIB):
@@ -179,9 +181,18 @@ def _nbytes(x) -> int:
     return int(x.numel() * x.element_size())
 
 
+_raw_stream = None
+
+
 def _stream(stream) -> int:
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = torch.cuda.is_initialized() and hasattr(torch._C, "_cuda_getCurrentRawStream")
     if stream is None:
         import torch
+        if _raw_stream:                                  # (the address without a Stream object: 2 us less per call)
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return int(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return stream
@@ -404,41 +415,41 @@ ACCUMULATE = 4
 _BF16, _F32 = 0, 1
 
 
-def _elem(t) -> int:
-    """Element type of a bf16 or fp32 tensor."""
-    name = str(t.dtype)
-    if name == "torch.bfloat16":
-        return _BF16
-    if name == "torch.float32":
-        return _F32
-    raise TypeError(f"expected a bf16 or fp32 tensor, got {name}")
+_types = None           # (element types by dtype, id sizes by dtype, fp32, int32, bf16), filled at the first call
 
 
-def _matrix(t, shape, what: str, elem: int | None = None):
-    """(address, element type, row stride) of a CUDA matrix of this shape."""
+def _dtypes():
+    global _types
+    if _types is None:
+        import torch
+        _types = ({torch.bfloat16: _BF16, torch.float32: _F32}, {torch.int32: 4, torch.int64: 8}, torch.float32, torch.int32,
+                  torch.bfloat16)
+    return _types
+
+
+def _matrix(t, n: int, cols: int, what: str, elem: int | None = None):
+    """(address, element type, row stride) of a bf16 or fp32 CUDA matrix of n rows."""
     if not t.is_cuda:
         raise TypeError(f"{what}: expected a CUDA tensor")
-    e = _elem(t)
-    if elem is not None and e != elem:
+    e = _dtypes()[0].get(t.dtype)
+    if e is None or (elem is not None and e != elem):
         raise TypeError(f"{what}: wrong element type {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
-    rows, cols = t.stride()
-    if cols != 1 and shape[1] > 1:
+    if t.shape != (n, cols):
+        raise ValueError(f"{what}: expected shape {(n, cols)}, got {tuple(t.shape)}")
+    rows, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{what}: columns must be adjacent")
-    return t.data_ptr(), e, rows if shape[0] > 1 else max(rows, shape[1])
+    return t.data_ptr(), e, rows if n > 1 else max(rows, cols)
 
 
-def _dense(t, shape, what: str, dtype: str, optional: bool = False):
-    """Address of a contiguous CUDA tensor of this shape and dtype (None if optional and None)."""
-    if t is None and optional:
-        return None
+def _dense(t, shape, what: str, dtype):
+    """Address of a contiguous CUDA tensor of this shape and dtype."""
     if not t.is_cuda:
         raise TypeError(f"{what}: expected a CUDA tensor")
-    if str(t.dtype) != dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous tensor of shape {shape}, got {tuple(t.shape)}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
@@ -446,7 +457,7 @@ def _ids(t, what: str = "ids"):
     """(address, bytes per id, count) of a contiguous int32 or int64 CUDA vector."""
     if not t.is_cuda:
         raise TypeError(f"{what}: expected a CUDA tensor")
-    size = {"torch.int32": 4, "torch.int64": 8}.get(str(t.dtype))
+    size = _dtypes()[1].get(t.dtype)
     if size is None:
         raise TypeError(f"{what}: expected int32 or int64, got {t.dtype}")
     if t.dim() != 1 or not t.is_contiguous():
@@ -463,7 +474,7 @@ def embed_layer(hdr, d_layer, tensor: int, cols: int, ids, out, d_status, scale:
     h = _host(hdr)
     lb = _nbytes(d_layer) if layer_bytes is None else layer_bytes
     ip, ib, n = _ids(ids)
-    op, oe, os_ = _matrix(out, (n, cols), "out")
+    op, oe, os_ = _matrix(out, n, cols, "out")
     _check(_lib().k3huf_embed_layer(h.ctypes.data, h.size, _dptr(d_layer), lb, int(tensor), cols, ip, ib, n, scale,
                                     op, oe, os_, _dptr(d_status), _stream(stream)), "k3huf_embed_layer")
 
@@ -482,8 +493,8 @@ def embed_grad(ids, dy, grad, scratch, d_status, scale: float = 1.0, accumulate:
     ``dy``: bf16 or fp32, len(ids) x cols; ``grad``: fp32, rows x cols."""
     ip, ib, n = _ids(ids)
     rows, cols = grad.shape
-    gp = _dense(grad, (rows, cols), "grad", "torch.float32")
-    dp, de, ds = _matrix(dy, (n, cols), "dy")
+    gp = _dense(grad, (rows, cols), "grad", _dtypes()[2])
+    dp, de, ds = _matrix(dy, n, cols, "dy")
     _check(_lib().k3huf_embed_grad(ip, ib, n, dp, de, ds, rows, cols, scale, gp, _dptr(scratch), _nbytes(scratch),
                                    _dptr(d_status), ACCUMULATE if accumulate else 0, _stream(stream)),
            "k3huf_embed_grad")
@@ -500,8 +511,9 @@ def adapter_scratch_bytes(n_tokens: int, n_adapters: int, rank: int, cols: int, 
 def _adapters(a, b, scales) -> Adapters:
     n, rank, cols = a.shape
     rows = b.shape[2]
-    return Adapters(_dense(a, (n, rank, cols), "a", "torch.bfloat16"), _dense(b, (n, rank, rows), "b", "torch.bfloat16"),
-                    _dense(scales, (n,), "scales", "torch.float32"), n, rank, cols, rows)
+    _, _, f32, _, bf16 = _dtypes()
+    return Adapters(_dense(a, (n, rank, cols), "a", bf16), _dense(b, (n, rank, rows), "b", bf16), _dense(scales, (n,), "scales", f32),
+                    n, rank, cols, rows)
 
 
 def adapter_apply(x, a, b, ids, scales, y, scratch, d_status, base=None, stream=None) -> None:
@@ -511,10 +523,10 @@ def adapter_apply(x, a, b, ids, scales, y, scratch, d_status, base=None, stream=
     ``base``: of y's type, may be y, None for zero."""
     ad = _adapters(a, b, scales)
     n = ids.numel()
-    ip = _dense(ids, (n,), "ids", "torch.int32")
-    xp, _, xs = _matrix(x, (n, ad.cols), "x", _BF16)
-    yp, ye, ys = _matrix(y, (n, ad.rows), "y")
-    bp, _, bs = (None, ye, 0) if base is None else _matrix(base, (n, ad.rows), "base", ye)
+    ip = _dense(ids, (n,), "ids", _dtypes()[3])
+    xp, _, xs = _matrix(x, n, ad.cols, "x", _BF16)
+    yp, ye, ys = _matrix(y, n, ad.rows, "y")
+    bp, _, bs = (None, ye, 0) if base is None else _matrix(base, n, ad.rows, "base", ye)
     _check(_lib().k3huf_adapter_apply(ctypes.addressof(ad), xp, xs, ip, n, bp, bs, yp, ys, ye, _dptr(scratch),
                                       _nbytes(scratch), _dptr(d_status), _stream(stream)), "k3huf_adapter_apply")
 
@@ -526,16 +538,17 @@ def adapter_grad(x, a, b, ids, scales, dy, da, db, scratch, d_status, dx=None, d
     or bf16, None if not wanted) = dx_base + the adapters' part."""
     ad = _adapters(a, b, scales)
     n = ids.numel()
-    ip = _dense(ids, (n,), "ids", "torch.int32")
-    xp, _, xs = _matrix(x, (n, ad.cols), "x", _BF16)
-    yp, _, ys = _matrix(dy, (n, ad.rows), "dy", _BF16)
+    _, _, f32, i32, _ = _dtypes()
+    ip = _dense(ids, (n,), "ids", i32)
+    xp, _, xs = _matrix(x, n, ad.cols, "x", _BF16)
+    yp, _, ys = _matrix(dy, n, ad.rows, "dy", _BF16)
     if dx is None and dx_base is not None:
         raise ValueError("dx_base without dx")
-    dp, de, ds = (None, _BF16, 0) if dx is None else _matrix(dx, (n, ad.cols), "dx")
-    bp, _, bs = (None, de, 0) if dx_base is None else _matrix(dx_base, (n, ad.cols), "dx_base", de)
+    dp, de, ds = (None, _BF16, 0) if dx is None else _matrix(dx, n, ad.cols, "dx")
+    bp, _, bs = (None, de, 0) if dx_base is None else _matrix(dx_base, n, ad.cols, "dx_base", de)
     _check(_lib().k3huf_adapter_grad(ctypes.addressof(ad), xp, xs, ip, n, yp, ys, bp, bs, dp, ds, de,
-                                     _dense(da, tuple(a.shape), "da", "torch.float32"),
-                                     _dense(db, tuple(b.shape), "db", "torch.float32"), _dptr(scratch),
+                                     _dense(da, a.shape, "da", f32),
+                                     _dense(db, b.shape, "db", f32), _dptr(scratch),
                                      _nbytes(scratch), _dptr(d_status), ACCUMULATE if accumulate else 0,
                                      _stream(stream)), "k3huf_adapter_grad")
 
@@ -549,16 +562,18 @@ def token_logprobs(logits, tokens, logprob, d_status, entropy=None, lse=None, to
     of n x top (both or neither)."""
     tp, tb, n = _ids(tokens, "tokens")
     vocab = logits.shape[1]
-    xp, xe, xs = _matrix(logits, (n, vocab), "logits")
-    f32 = "torch.float32"
+    xp, xe, xs = _matrix(logits, n, vocab, "logits")
+    _, _, f32, i32, _ = _dtypes()
     if (top_ids is None) != (top_logprobs is None):
         raise ValueError("top_ids and top_logprobs go together")
-    top = 0 if top_ids is None else top_ids.shape[1]
+    top, ti, tl = 0, None, None
+    if top_ids is not None:
+        top = top_ids.shape[1]
+        ti, tl = _dense(top_ids, (n, top), "top_ids", i32), _dense(top_logprobs, (n, top), "top_logprobs", f32)
     _check(_lib().k3huf_token_logprobs(xp, xe, xs, n, vocab, scale, tp, tb, _dense(logprob, (n,), "logprob", f32),
-                                       _dense(entropy, (n,), "entropy", f32, True), _dense(lse, (n,), "lse", f32, True),
-                                       top, _dense(top_ids, (n, top), "top_ids", "torch.int32", True),
-                                       _dense(top_logprobs, (n, top), "top_logprobs", f32, True), _dptr(d_status),
-                                       _stream(stream)), "k3huf_token_logprobs")
+                                       None if entropy is None else _dense(entropy, (n,), "entropy", f32),
+                                       None if lse is None else _dense(lse, (n,), "lse", f32), top, ti, tl,
+                                       _dptr(d_status), _stream(stream)), "k3huf_token_logprobs")
 
 
 def token_logprobs_grad(logits, tokens, lse, g_logprob, dlogits, d_status, entropy=None, g_entropy=None,
@@ -569,14 +584,14 @@ def token_logprobs_grad(logits, tokens, lse, g_logprob, dlogits, d_status, entro
     logits, may be logits itself."""
     tp, tb, n = _ids(tokens, "tokens")
     vocab = logits.shape[1]
-    xp, xe, xs = _matrix(logits, (n, vocab), "logits")
-    dp, _, ds = _matrix(dlogits, (n, vocab), "dlogits", xe)
-    f32 = "torch.float32"
+    xp, xe, xs = _matrix(logits, n, vocab, "logits")
+    dp, _, ds = _matrix(dlogits, n, vocab, "dlogits", xe)
+    f32 = _dtypes()[2]
     _check(_lib().k3huf_token_logprobs_grad(xp, xe, xs, n, vocab, scale, tp, tb, _dense(lse, (n,), "lse", f32),
-                                            _dense(entropy, (n,), "entropy", f32, True),
+                                            None if entropy is None else _dense(entropy, (n,), "entropy", f32),
                                             _dense(g_logprob, (n,), "g_logprob", f32),
-                                            _dense(g_entropy, (n,), "g_entropy", f32, True), dp, ds,
-                                            _dptr(d_status), _stream(stream)), "k3huf_token_logprobs_grad")
+                                            None if g_entropy is None else _dense(g_entropy, (n,), "g_entropy", f32),
+                                            dp, ds, _dptr(d_status), _stream(stream)), "k3huf_token_logprobs_grad")
 
 
 class Feed:

@@ -194,6 +194,10 @@ expand_few_kernel(const float *h, const __nv_bfloat16 *w, const int32_t *ids, ui
 constexpr uint32_t kTile = 128;               // tokens per tile
 constexpr uint32_t kStep = 64;                // contraction per staged step: one 128-byte row
 constexpr uint32_t kTileBytes = kTile * 128;  // one staged tile of 128 rows
+// Additions in the tensor core before a sum moves to registers.  One of them
+// errs by about 1.3e-8 of the sum, always to the same side (measured: 2e-5 after
+// 1536), while fp32 additions in registers round to nearest.
+constexpr uint32_t kChain = 32;
 
 // The adapters of a tile's tokens, each once, in the order of their first
 // token: of[t] the place of token t's adapter (-1: none), list the adapters.
@@ -294,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
     const uint32_t a0 = blockIdx.y * per, na = a0 < count ? min(per, count - a0) : 0u;
     if (na == 0) return;                      // (the whole cluster)
     const uint32_t cols = na * rp;            // <= 128, a multiple of 16
-    if (warp == 0) tmem_alloc(smem_addr(&s_tmem), 128);
+    if (warp == 0) tmem_alloc(smem_addr(&s_tmem), 256);
     if (tid == 0)
         for (uint32_t i = 0; i < kShrinkStages; ++i) mbar_init(smem_addr(&s_bar[i]), 1);
     if (tid == 0) fence_async_shared();
@@ -320,6 +324,22 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
     };
     const uint32_t desc = mma_desc(kTile, cols, 0, 0);
     bool ok = true;
+    // this thread's sums: token (lane) warp % 4 * 32 + lane, columns warp / 4 * 64 on.  Runs of
+    // kRun steps take turns in the two halves of TMEM
+    constexpr uint32_t kRun = kChain / (kStep / 16);
+    float sum[64] = {};
+    auto drain = [&](uint32_t run) {
+        tc_fence_after();
+#pragma unroll
+        for (uint32_t c = 0; c < 64; c += 16)
+            if (warp / 4 * 64 + c < cols) {
+                float v[16];
+                tmem_load16(tmem + ((warp % 4) << 21) + (run & 1) * 128 + warp / 4 * 64 + c, v);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) sum[c + k] += v[k];
+            }
+        tc_fence_before();
+    };
     for (uint32_t k = k0; k < k0 + kShrinkStages - 1; ++k) {
         if (k < k1) load(k);
         cp_async_commit();
@@ -333,35 +353,35 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
             tc_fence_after();
             const uint64_t a = tile_desc(base + stage * kShrinkStage, 16, 1024), b = tile_desc(base + stage * kShrinkStage + kTileBytes, 16, 1024);
 #pragma unroll
-            for (uint32_t s = 0; s < kStep / 16; ++s) mma(tmem, a + 2 * s, b + 2 * s, desc, i || s);
+            for (uint32_t s = 0; s < kStep / 16; ++s) mma(tmem + (i / kRun & 1) * 128, a + 2 * s, b + 2 * s, desc, i % kRun || s);
             mma_commit(smem_addr(&s_bar[stage]));
         }
         // the stage before this one is free once its products are done
         if (i > 0 && ok) ok = mbar_wait(smem_addr(&s_bar[(i - 1) % kShrinkStages]), (i - 1) / kShrinkStages & 1);
         if (k + kShrinkStages - 1 < k1 && ok) load(k + kShrinkStages - 1);
         cp_async_commit();
+        if (i > 0 && i % kRun == 0) drain(i / kRun - 1);
     }
     if (k1 > k0 && ok) ok = mbar_wait(smem_addr(&s_bar[(k1 - k0 - 1) % kShrinkStages]), (k1 - k0 - 1) / kShrinkStages & 1);
     cp_async_wait<0>();
     if (!ok) atomicOr(P.status, K3HUF_ST_TIMEOUT);
+    if (k1 > k0) drain((k1 - k0 - 1) / kRun);
     __syncthreads();
     tc_fence_after();
 
     // each token's own columns, to shared memory (odd stride: one bank per lane)
     float *part = reinterpret_cast<float *>(smem);
     const uint32_t pitch = rp + 1;
-    if (warp < 4) {
-        const uint32_t t = warp * 32 + lane;
+    {
+        const uint32_t t = warp % 4 * 32 + lane;
         const int32_t of = tile.of[t];
-        for (uint32_t c = 0; c < cols; c += 16) {
-            float v[16];
-            tmem_load16(tmem + (warp << 21) + c, v);
-            const int32_t a = int32_t(a0 + c / rp);
-            if (of == a)
 #pragma unroll
-                for (uint32_t k = 0; k < 16; ++k) part[t * pitch + c % rp + k] = k1 > k0 ? v[k] : 0.f;
+        for (uint32_t c = 0; c < 64; c += 16) {
+            const uint32_t q = warp / 4 * 64 + c;
+            if (q < cols && of == int32_t(a0 + q / rp))
+#pragma unroll
+                for (uint32_t k = 0; k < 16; ++k) part[t * pitch + q % rp + k] = sum[c + k];
         }
-        tc_fence_before();
     }
     if (P.splits > 1) {
         cluster_arrive();
@@ -387,8 +407,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
     } else {
         __syncthreads();
     }
-    tc_fence_after();
-    if (warp == 0) tmem_free(tmem, 128);
+    if (warp == 0) tmem_free(tmem, 256);
 }
 
 struct ExpandParams {
@@ -616,7 +635,7 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
     const bool second = blockIdx.x >= P.col_tiles0;
     const OuterJob &J = P.job[second];
     const uint32_t col = (blockIdx.x - (second ? P.col_tiles0 : 0)) * 128;
-    if (warp == 0) tmem_alloc(smem_addr(&s_tmem), 128);
+    if (warp == 0) tmem_alloc(smem_addr(&s_tmem), kBlocks * 128);
     if (tid == 0)
         for (uint32_t i = 0; i < kOuterStages; ++i) mbar_init(smem_addr(&s_bar[i]), 1);
     if (tid == 0) fence_async_shared();
@@ -628,7 +647,22 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
     bool ok = true;
     uint32_t step = 0;                        // steps of this CTA so far: stage step % 2, phase step / 2 % 2
     for (uint32_t a = blockIdx.y; a < P.n_adapters; a += gridDim.y) {
-        uint32_t first = step;
+        const uint32_t first = step;
+        // this thread's sums: column (lane) warp % 4 * 32 + lane, rank rows warp / 4 * 16 + 32 b on
+        constexpr uint32_t kRun = kChain / (kMaxParts * kStep / 16);
+        float sum[2 * kBlocks][16] = {};
+        auto drain = [&](uint32_t run) {
+            tc_fence_after();
+#pragma unroll
+            for (uint32_t b = 0; b < 2 * kBlocks; ++b)
+                if (warp / 4 * 16 + b * 32 < rp) {
+                    float v[16];
+                    tmem_load16(tmem + ((warp % 4) << 21) + (run & 1) * (kBlocks * 64) + warp / 4 * 16 + b * 32, v);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) sum[b][k] += v[k];
+                }
+            tc_fence_before();
+        };
         for (uint64_t w0 = 0; w0 < P.n; w0 += kWindow) {
             // the window's tokens of this adapter, in order
             const uint32_t size = uint32_t(min(uint64_t(kWindow), P.n - w0));
@@ -693,39 +727,36 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
                     for (uint32_t q = 0; q < kMaxParts; ++q) {
                         const uint64_t hb = tile_desc(at + kStep * 256 + q * kBlocks * (kStep * 128), kStep * 128, 1024);
 #pragma unroll
-                        for (uint32_t k = 0; k < kStep / 16; ++k) mma(tmem, va + k * 128, hb + k * 128, desc, g != first || q || k);
+                        for (uint32_t k = 0; k < kStep / 16; ++k) mma(tmem + ((g - first) / kRun & 1) * (kBlocks * 64), va + k * 128, hb + k * 128, desc, (g - first) % kRun || q || k);
                     }
                     mma_commit(smem_addr(&s_bar[g % kOuterStages]));
                 }
+                // the run before is done: its last step was waited for above, or with its window
+                if (g != first && (g - first) % kRun == 0) drain((g - first) / kRun - 1);
             }
             if (steps && ok) ok = mbar_wait(smem_addr(&s_bar[(step + steps - 1) % kOuterStages]), (step + steps - 1) / kOuterStages & 1);
             cp_async_wait<0>();
             step += steps;
         }
-        __syncthreads();
-        tc_fence_after();
+        if (step != first) drain((step - first - 1) / kRun);
         // lane: column; a warp's stores of one rank row are 128 adjacent bytes
         const uint32_t c = col + warp % 4 * 32 + lane;
-        for (uint32_t j0 = warp / 4 * 16; j0 < rp; j0 += 32) {
-            float v[16];
-            if (step != first) tmem_load16(tmem + ((warp % 4) << 21) + j0, v);
-            else
+        if (c < J.len)
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = 0.f;
-            if (c < J.len)
+            for (uint32_t b = 0; b < 2 * kBlocks; ++b)
 #pragma unroll
-                for (uint32_t k = 0; k < 16; ++k)
-                    if (j0 + k < P.rank) {
-                        float *o = J.g + (uint64_t(a) * P.rank + j0 + k) * J.len + c;
-                        *o = P.add ? *o + v[k] : v[k];
-                    }
-        }
+                for (uint32_t k = 0; k < 16; ++k) {
+                    const uint32_t j = warp / 4 * 16 + b * 32 + k;
+                    if (j >= P.rank) break;
+                    float *o = J.g + (uint64_t(a) * P.rank + j) * J.len + c;
+                    *o = P.add ? *o + sum[b][k] : sum[b][k];
+                }
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
     }
     if (!ok) atomicOr(P.status, K3HUF_ST_TIMEOUT);
-    if (warp == 0) tmem_free(tmem, 128);
+    if (warp == 0) tmem_free(tmem, kBlocks * 128);
 }
 
 // --- host -----------------------------------------------------------------------
