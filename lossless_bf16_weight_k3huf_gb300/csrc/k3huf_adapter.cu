@@ -309,17 +309,31 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
     const uint32_t steps = (J.len + kStep - 1) / kStep;
     const uint32_t k0 = steps * split / P.splits, k1 = steps * (split + 1) / P.splits;
 
+    // this thread's part of a step: chunk tid % 8 of rows tid / 8 + 32 m of both operands, their
+    // addresses worked out once (null: zeros)
+    const uint32_t chunk = tid % 8;
+    const __nv_bfloat16 *v_row[4], *w_row[4];
+    uint32_t to[4];
+#pragma unroll
+    for (uint32_t m = 0; m < 4; ++m) {
+        const uint32_t r = tid / 8 + 32 * m, j = r % rp;
+        to[m] = tile_at(r, chunk);
+        v_row[m] = t0 + r < P.n && tile.of[r] >= 0 ? J.v + (t0 + r) * J.stride + chunk * 8 : nullptr;
+        w_row[m] = r < cols && j < P.rank ? J.w + (uint64_t(tile.list[a0 + r / rp]) * P.rank + j) * J.len + chunk * 8 : nullptr;
+    }
     auto load = [&](uint32_t k) {
-        const uint32_t at = base + (k - k0) % kShrinkStages * kShrinkStage;
-        for (uint32_t i = tid; i < kTile * 8; i += kThreads) {
-            const uint32_t r = i / 8, c = i % 8, col = k * kStep + c * 8;
-            const bool in = t0 + r < P.n && col < J.len && tile.of[r] >= 0;
-            cp_async16z(at + tile_at(r, c), in ? J.v + (t0 + r) * J.stride + col : J.v, in ? 16 : 0);
+        const uint32_t at = base + (k - k0) % kShrinkStages * kShrinkStage, col = k * kStep;
+        const bool in = col + chunk * 8 < J.len;
+#pragma unroll
+        for (uint32_t m = 0; m < 4; ++m) {
+            const bool some = in && v_row[m];
+            cp_async16z(at + to[m], some ? v_row[m] + col : J.v, some ? 16 : 0);
         }
-        for (uint32_t i = tid; i < cols * 8; i += kThreads) {
-            const uint32_t q = i / 8, c = i % 8, col = k * kStep + c * 8, r = q % rp;
-            const bool in = r < P.rank && col < J.len;
-            cp_async16z(at + kTileBytes + tile_at(q, c), in ? J.w + (uint64_t(tile.list[a0 + q / rp]) * P.rank + r) * J.len + col : J.w, in ? 16 : 0);
+#pragma unroll
+        for (uint32_t m = 0; m < 4; ++m) {
+            if (tid / 8 + 32 * m >= cols) break;
+            const bool some = in && w_row[m];
+            cp_async16z(at + kTileBytes + to[m], some ? w_row[m] + col : J.w, some ? 16 : 0);
         }
     };
     const uint32_t desc = mma_desc(kTile, cols, 0, 0);
@@ -494,15 +508,24 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
                 cp_async16z(h_at + place * E::h_bytes + q * E::part_bytes + tile_at(t, c), in ? src + q * P.n * rp : src, in ? 16 : 0);
         }
     };
+    // this thread's part of a step: chunk tid % 16 of rows tid / 16 + 16 m
+    const uint32_t w_chunk = tid % 16;
+    uint32_t w_a[4], w_j[4], w_to[4];
+#pragma unroll
+    for (uint32_t m = 0; m < 4; ++m) {
+        const uint32_t r = tid / 16 + 16 * m;
+        w_a[m] = rp <= kStep ? r / rp : 0;
+        w_j[m] = rp <= kStep ? r % rp : 0;
+        w_to[m] = w_chunk / 8 * (kStep * 128) + tile_at(r, w_chunk % 8);
+    }
     // step s: column tile c0 + s / chunks, chunk s % chunks
     auto load_step = [&](uint32_t s) {
-        const uint32_t chunk = s % chunks, col = (c0 + s / chunks) * 128;
-        for (uint32_t i = tid; i < kStep * 16; i += kThreads) {
-            const uint32_t r = i / 16, c = i % 16;
-            uint32_t a, j;
-            const bool in = row_of(chunk, r, a, j) && j < P.rank && col + c * 8 < P.len;
-            cp_async16z(w_at + (s & 1) * E::w_bytes + c / 8 * (kStep * 128) + tile_at(r, c % 8),
-                        in ? P.w + (uint64_t(tile.list[a]) * P.rank + j) * P.len + col + c * 8 : P.w, in ? 16 : 0);
+        const uint32_t chunk = s % chunks, col = (c0 + s / chunks) * 128 + w_chunk * 8;
+#pragma unroll
+        for (uint32_t m = 0; m < 4; ++m) {
+            const uint32_t a = rp <= kStep ? chunk * per + w_a[m] : chunk / blocks, j = rp <= kStep ? w_j[m] : chunk % blocks * kStep + tid / 16 + 16 * m;
+            const bool in = w_a[m] < per && a < count && j < P.rank && col < P.len;
+            cp_async16z(w_at + (s & 1) * E::w_bytes + w_to[m], in ? P.w + (uint64_t(tile.list[a]) * P.rank + j) * P.len + col : P.w, in ? 16 : 0);
         }
         if (!resident) load_h(chunk, s & 1);
     };
@@ -569,17 +592,27 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
         if (ok) ok = mbar_wait(smem_addr(&s_io[i & 1]), i / 2 & 1);
         tc_fence_after();
         T *mine = reinterpret_cast<T *>(io + (i & 1) * E::io_bytes) + warp % 4 * 32 + lane;
-        for (uint32_t t = warp / 4 * (NT / 2); t < min((warp / 4 + 1) * (NT / 2), rows); t += 16) {
-            float v[16];
-            if (chunks) tmem_load16(tmem + ((warp % 4) << 21) + (i & 1) * 128 + t, v);
-            else
+        const uint32_t t_end = min((warp / 4 + 1) * (NT / 2), rows);
+        for (uint32_t t = warp / 4 * (NT / 2); t < t_end; t += 32) {
+            // (the base's values are fetched while the product comes from TMEM)
+            uint32_t r[32];
+            float b[32];
+            if (chunks) tmem_load32(tmem + ((warp % 4) << 21) + (i & 1) * 128 + t, r);
+            T *q = mine + t * 128;
+            if (P.base) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = 0.f;
+                for (uint32_t k = 0; k < 32; ++k) b[k] = ld_f32(q + k * 128);
+            } else {
 #pragma unroll
-            for (uint32_t k = 0; k < 16; ++k) {
-                T *q = mine + (t + k) * 128;
-                st_f32(q, P.base ? ld_f32(q) + v[k] : v[k]);
+                for (uint32_t k = 0; k < 32; ++k) b[k] = 0.f;
             }
+            if (chunks) {
+                tmem_wait32(r);
+#pragma unroll
+                for (uint32_t k = 0; k < 32; ++k) b[k] += __uint_as_float(r[k]);
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < 32; ++k) st_f32(q + k * 128, b[k]);
         }
         tc_fence_before();
         fence_async_shared();
@@ -693,19 +726,21 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
             __syncthreads();
             const uint32_t steps = (total + kStep - 1) / kStep;
             auto load = [&](uint32_t s) {
-                const uint32_t to = base + (step + s) % kOuterStages * kStage;
-                for (uint32_t i = tid; i < kStep * 16; i += kThreads) {
-                    const uint32_t r = i / 16, c = i % 16, k = s * kStep + r;
-                    const bool in = k < total && col + c * 8 < J.len;
-                    cp_async16z(to + c / 8 * (kStep * 128) + tile_at(r, c % 8), in ? J.v + (w0 + s_token[k]) * J.stride + col + c * 8 : J.v, in ? 16 : 0);
-                }
-                for (uint32_t i = tid; i < kStep * (rp / 8); i += kThreads) {
-                    const uint32_t r = i / (rp / 8), c = i % (rp / 8), k = s * kStep + r;
-                    const bool in = k < total;
-                    const __nv_bfloat16 *src = in ? J.h + (w0 + s_token[k]) * rp + c * 8 : J.h;
+                // chunk tid % 16 of rows tid / 16 + 16 m: of the rows' 128 columns, and, where
+                // there is one, of each part's rank rows
+                const uint32_t to = base + (step + s) % kOuterStages * kStage, c = tid % 16;
+                const bool v_in = col + c * 8 < J.len, h_in = c * 8 < rp;
 #pragma unroll
-                    for (uint32_t q = 0; q < kMaxParts; ++q)
-                        cp_async16z(to + kStep * 256 + (q * kBlocks + c / 8) * (kStep * 128) + tile_at(r, c % 8), in ? src + q * P.n * rp : src, in ? 16 : 0);
+                for (uint32_t m = 0; m < 4; ++m) {
+                    const uint32_t r = tid / 16 + 16 * m, k = s * kStep + r, at = c / 8 * (kStep * 128) + tile_at(r, c % 8);
+                    const uint64_t t = w0 + (k < total ? s_token[k] : 0u);
+                    const bool in = k < total;
+                    cp_async16z(to + at, in && v_in ? J.v + t * J.stride + col + c * 8 : J.v, in && v_in ? 16 : 0);
+                    if (h_in) {
+                        const __nv_bfloat16 *src = J.h + t * rp + c * 8;
+#pragma unroll
+                        for (uint32_t q = 0; q < kMaxParts; ++q) cp_async16z(to + kStep * 256 + q * (kBlocks * kStep * 128) + at, src + q * P.n * rp, in ? 16 : 0);
+                    }
                 }
             };
             if (steps) load(0);
