@@ -192,6 +192,7 @@ expand_few_kernel(const float *h, const __nv_bfloat16 *w, const int32_t *ids, ui
 // --- many tokens: tensor cores --------------------------------------------------
 
 constexpr uint32_t kTile = 128;               // tokens per tile
+constexpr uint32_t kMaxParts = 3;             // bf16 parts of a rank-wide intermediate
 constexpr uint32_t kStep = 64;                // contraction per staged step: one 128-byte row
 constexpr uint32_t kTileBytes = kTile * 128;  // one staged tile of 128 rows
 // Additions in the tensor core before a sum moves to registers.  One of them
@@ -257,10 +258,9 @@ __device__ __forceinline__ void parts_of(float x, __nv_bfloat16 (&p)[3]) {
 }
 
 struct ShrinkJob {
-    const __nv_bfloat16 *v, *w;
-    uint64_t stride;
+    CUtensorMap v, w;                         // tokens x len, boxes of 64 x kTile; rank rows x len, boxes of 64 x rank
     uint32_t len;
-    __nv_bfloat16 *h;                         // parts x tokens x rank_pad
+    __nv_bfloat16 *h;                         // parts x tokens x pitch
 };
 struct ShrinkParams {
     ShrinkJob job[2];
@@ -268,17 +268,19 @@ struct ShrinkParams {
     const int32_t *ids;
     uint32_t *status;
     uint64_t n;
-    uint32_t n_adapters, rank, rank_pad, parts, splits;
+    uint32_t n_adapters, rank, rank_pad, pitch, parts, splits;
 };
 
 // The shrink.  D[128 tokens, rank rows of the tile's adapters] = V W^T, both
-// operands K-major, kStep of the contraction per stage; every token keeps the
-// columns of its own adapter.  CTAs: a tile of tokens x a group of adapters
-// whose rank rows fill 128 columns (all but the first few groups of a tile
-// whose tokens share adapters end at once) x a split of the contraction; the
-// splits are a cluster, whose partial sums meet through shared memory in the
-// order of the splits.  Bound by the read of V (and of the factors when every
-// token has its own).
+// operands K-major tiles brought by TMA, kStep of the contraction per stage;
+// every token keeps the columns of its own adapter.  CTAs: a tile of tokens x a
+// group of adapters whose rank rows fill 128 columns (all but the first few
+// groups of a tile whose tokens share adapters end at once) x a split of the
+// contraction; the splits are a cluster, whose partial sums meet through shared
+// memory in the order of the splits.  One thread keeps copies and products
+// going for a run of kRun steps while the CTA moves the run before it from the
+// other half of TMEM to registers.  Bound by the read of V (and of the factors
+// when every token has its own).
 constexpr uint32_t kShrinkStages = 3, kShrinkStage = 2 * kTileBytes;
 constexpr size_t kShrinkSmem = kShrinkStages * kShrinkStage + 1024;
 constexpr uint32_t kMaxSplits = 8;
@@ -286,7 +288,7 @@ constexpr uint32_t kMaxSplits = 8;
 __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant__ ShrinkParams P) {
     extern __shared__ uint8_t raw[];
     __shared__ TileAdapters tile;
-    __shared__ __align__(8) uint64_t s_bar[kShrinkStages];
+    __shared__ __align__(8) uint64_t s_full[kShrinkStages], s_free[kShrinkStages], s_run[2];
     __shared__ uint32_t s_tmem;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32, base = smem_addr(smem);
@@ -299,93 +301,82 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
     if (na == 0) return;                      // (the whole cluster)
     const uint32_t cols = na * rp;            // <= 128, a multiple of 16
     if (warp == 0) tmem_alloc(smem_addr(&s_tmem), 256);
-    if (tid == 0)
-        for (uint32_t i = 0; i < kShrinkStages; ++i) mbar_init(smem_addr(&s_bar[i]), 1);
-    if (tid == 0) fence_async_shared();
+    if (tid == 0) {
+        for (uint32_t i = 0; i < kShrinkStages; ++i) {
+            mbar_init(smem_addr(&s_full[i]), 1);
+            mbar_init(smem_addr(&s_free[i]), 1);
+        }
+        mbar_init(smem_addr(&s_run[0]), 1);
+        mbar_init(smem_addr(&s_run[1]), 1);
+        fence_async_shared();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     const uint32_t steps = (J.len + kStep - 1) / kStep;
-    const uint32_t k0 = steps * split / P.splits, k1 = steps * (split + 1) / P.splits;
-
-    // this thread's part of a step: chunk tid % 8 of rows tid / 8 + 32 m of both operands, their
-    // addresses worked out once (null: zeros)
-    const uint32_t chunk = tid % 8;
-    const __nv_bfloat16 *v_row[4], *w_row[4];
-    uint32_t to[4];
-#pragma unroll
-    for (uint32_t m = 0; m < 4; ++m) {
-        const uint32_t r = tid / 8 + 32 * m, j = r % rp;
-        to[m] = tile_at(r, chunk);
-        v_row[m] = t0 + r < P.n && tile.of[r] >= 0 ? J.v + (t0 + r) * J.stride + chunk * 8 : nullptr;
-        w_row[m] = r < cols && j < P.rank ? J.w + (uint64_t(tile.list[a0 + r / rp]) * P.rank + j) * J.len + chunk * 8 : nullptr;
-    }
-    auto load = [&](uint32_t k) {
-        const uint32_t at = base + (k - k0) % kShrinkStages * kShrinkStage, col = k * kStep;
-        const bool in = col + chunk * 8 < J.len;
-#pragma unroll
-        for (uint32_t m = 0; m < 4; ++m) {
-            const bool some = in && v_row[m];
-            cp_async16z(at + to[m], some ? v_row[m] + col : J.v, some ? 16 : 0);
-        }
-#pragma unroll
-        for (uint32_t m = 0; m < 4; ++m) {
-            if (tid / 8 + 32 * m >= cols) break;
-            const bool some = in && w_row[m];
-            cp_async16z(at + kTileBytes + to[m], some ? w_row[m] + col : J.w, some ? 16 : 0);
-        }
+    const uint32_t k0 = steps * split / P.splits, n_steps = steps * (split + 1) / P.splits - k0;
+    constexpr uint32_t kRun = kChain / (kStep / 16);
+    const uint32_t runs = (n_steps + kRun - 1) / kRun;
+    bool ok = true;
+    auto load = [&](uint32_t i) {             // by one thread
+        const uint32_t stage = i % kShrinkStages, at = base + stage * kShrinkStage, bar = smem_addr(&s_full[stage]);
+        mbar_expect(bar, kTileBytes + na * P.rank * 128);
+        tma_load(at, &J.v, int32_t((k0 + i) * kStep), int32_t(t0), bar);
+        for (uint32_t a = 0; a < na; ++a) tma_load(at + kTileBytes + a * rp * 128, &J.w, int32_t((k0 + i) * kStep), tile.list[a0 + a] * int32_t(P.rank), bar);
     };
     const uint32_t desc = mma_desc(kTile, cols, 0, 0);
-    bool ok = true;
-    // this thread's sums: token (lane) warp % 4 * 32 + lane, columns warp / 4 * 64 on.  Runs of
-    // kRun steps take turns in the two halves of TMEM
-    constexpr uint32_t kRun = kChain / (kStep / 16);
+    uint32_t loaded = 0;
+    if (tid == 0)
+        for (; loaded < min(kShrinkStages - 1, n_steps); ++loaded) load(loaded);
+    // this thread's sums: token (lane) warp % 4 * 32 + lane, columns warp / 4 * 64 on
     float sum[64] = {};
-    auto drain = [&](uint32_t run) {
-        tc_fence_after();
+    for (uint32_t run = 0; run <= runs; ++run) {
+        if (tid == 0 && run < runs) {
+            for (uint32_t i = run * kRun; i < min((run + 1) * kRun, n_steps) && ok; ++i) {
+                const uint32_t stage = i % kShrinkStages;
+                ok = mbar_wait(smem_addr(&s_full[stage]), i / kShrinkStages & 1);
+                tc_fence_after();
+                const uint64_t a = tile_desc(base + stage * kShrinkStage, 16, 1024), b = tile_desc(base + stage * kShrinkStage + kTileBytes, 16, 1024);
 #pragma unroll
-        for (uint32_t c = 0; c < 64; c += 16)
-            if (warp / 4 * 64 + c < cols) {
-                float v[16];
-                tmem_load16(tmem + ((warp % 4) << 21) + (run & 1) * 128 + warp / 4 * 64 + c, v);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) sum[c + k] += v[k];
+                for (uint32_t s = 0; s < kStep / 16; ++s) mma(tmem + (run & 1) * 128, a + 2 * s, b + 2 * s, desc, i % kRun || s);
+                mma_commit(smem_addr(&s_free[stage]));
+                // the stage before this one is free once its products are done
+                if (loaded < n_steps && ok) {
+                    if (i > 0) ok = mbar_wait(smem_addr(&s_free[(i - 1) % kShrinkStages]), (i - 1) / kShrinkStages & 1);
+                    if (ok) load(loaded++);
+                }
             }
-        tc_fence_before();
-    };
-    for (uint32_t k = k0; k < k0 + kShrinkStages - 1; ++k) {
-        if (k < k1) load(k);
-        cp_async_commit();
-    }
-    for (uint32_t k = k0; k < k1; ++k) {
-        const uint32_t i = k - k0, stage = i % kShrinkStages;
-        cp_async_wait<kShrinkStages - 2>();
-        fence_async_shared();
-        __syncthreads();
-        if (tid == 0 && ok) {
-            tc_fence_after();
-            const uint64_t a = tile_desc(base + stage * kShrinkStage, 16, 1024), b = tile_desc(base + stage * kShrinkStage + kTileBytes, 16, 1024);
-#pragma unroll
-            for (uint32_t s = 0; s < kStep / 16; ++s) mma(tmem + (i / kRun & 1) * 128, a + 2 * s, b + 2 * s, desc, i % kRun || s);
-            mma_commit(smem_addr(&s_bar[stage]));
+            mma_commit(smem_addr(&s_run[run & 1]));
         }
-        // the stage before this one is free once its products are done
-        if (i > 0 && ok) ok = mbar_wait(smem_addr(&s_bar[(i - 1) % kShrinkStages]), (i - 1) / kShrinkStages & 1);
-        if (k + kShrinkStages - 1 < k1 && ok) load(k + kShrinkStages - 1);
-        cp_async_commit();
-        if (i > 0 && i % kRun == 0) drain(i / kRun - 1);
+        __syncwarp();
+        if (run > 0) {
+            const uint32_t r = run - 1;
+            if (!mbar_wait(smem_addr(&s_run[r & 1]), r / 2 & 1)) ok = false;
+            tc_fence_after();
+#pragma unroll
+            for (uint32_t c = 0; c < 64; c += 16)
+                if (warp / 4 * 64 + c < cols) {
+                    float v[16];
+                    tmem_load16(tmem + ((warp % 4) << 21) + (r & 1) * 128 + warp / 4 * 64 + c, v);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) sum[c + k] += v[k];
+                }
+            tc_fence_before();
+        }
+        __syncthreads();                      // (the run after the next writes this half)
     }
-    if (k1 > k0 && ok) ok = mbar_wait(smem_addr(&s_bar[(k1 - k0 - 1) % kShrinkStages]), (k1 - k0 - 1) / kShrinkStages & 1);
-    cp_async_wait<0>();
-    if (!ok) atomicOr(P.status, K3HUF_ST_TIMEOUT);
-    if (k1 > k0) drain((k1 - k0 - 1) / kRun);
+    if (!ok) {
+        atomicOr(P.status, K3HUF_ST_TIMEOUT);
+        // copies still in flight, if any, land first
+        if (tid == 0)
+            for (uint32_t i = loaded > kShrinkStages ? loaded - kShrinkStages : 0; i < loaded; ++i) mbar_wait(smem_addr(&s_full[i % kShrinkStages]), i / kShrinkStages & 1);
+    }
     __syncthreads();
-    tc_fence_after();
 
     // each token's own columns, to shared memory (odd stride: one bank per lane)
     float *part = reinterpret_cast<float *>(smem);
-    const uint32_t pitch = rp + 1;
+    const uint32_t stride = rp + 1;
     {
         const uint32_t t = warp % 4 * 32 + lane;
         const int32_t of = tile.of[t];
@@ -394,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
             const uint32_t q = warp / 4 * 64 + c;
             if (q < cols && of == int32_t(a0 + q / rp))
 #pragma unroll
-                for (uint32_t k = 0; k < 16; ++k) part[t * pitch + q % rp + k] = sum[c + k];
+                for (uint32_t k = 0; k < 16; ++k) part[t * stride + q % rp + k] = sum[c + k];
         }
     }
     if (P.splits > 1) {
@@ -403,17 +394,19 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
     } else {
         __syncthreads();
     }
-    // a share of the tile's tokens per split: sum over the splits, scale, parts
+    // a share of the tile's tokens per split: sum over the splits, scale, parts; zeros for the
+    // rank's padding (whose columns of D hold the next adapter's)
     const uint32_t r0 = kTile * split / P.splits, r1 = kTile * (split + 1) / P.splits;
     for (uint32_t i = r0 * rp + tid; i < r1 * rp; i += kThreads) {
         const uint32_t t = i / rp, j = i % rp;
         const int32_t of = tile.of[t];
         if (of < int32_t(a0) || of >= int32_t(a0 + na)) continue;
-        float sum = 0.f;
-        for (uint32_t q = 0; q < P.splits; ++q) sum += P.splits > 1 ? cluster_load(smem_addr(part + t * pitch + j), q) : part[t * pitch + j];
+        float total = 0.f;
+        if (j < P.rank)
+            for (uint32_t q = 0; q < P.splits; ++q) total += P.splits > 1 ? cluster_load(smem_addr(part + t * stride + j), q) : part[t * stride + j];
         __nv_bfloat16 p[3];
-        parts_of(P.scales[tile.list[of]] * sum, p);
-        for (uint32_t q = 0; q < P.parts; ++q) J.h[(q * P.n + t0 + t) * rp + j] = p[q];
+        parts_of(j < P.rank ? P.scales[tile.list[of]] * total : 0.f, p);
+        for (uint32_t q = 0; q < P.parts; ++q) J.h[(q * P.n + t0 + t) * P.pitch + j] = p[q];
     }
     if (P.splits > 1) {
         cluster_arrive();
@@ -425,203 +418,185 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
 }
 
 struct ExpandParams {
-    const __nv_bfloat16 *h, *w;
-    const void *base;
-    void *y;
+    CUtensorMap h, w, base, y;                // parts x tokens rows of 64-value blocks; rank rows x len, boxes of 64 x rank; boxes of 128 x tokens
     const int32_t *ids;
     uint32_t *status;
-    uint64_t n, base_stride, y_stride;
+    uint64_t n;
     uint32_t n_adapters, rank, rank_pad, len, groups;
+    bool has_base;
 };
 
-// The expand.  D[128 columns, 128 tokens] = W^T H^T with the adapters of the
-// tile one after another along the contraction and H zero where a token has
-// another one: W is read MN-major as it lies in memory, H K-major, in kParts
+// The expand.  D[128 columns, tokens] = W_a^T H^T for one adapter a of the tile
+// after another, each added only where a token has that adapter: no token meets
+// another adapter's values, not even as zero times infinity.  W is read
+// MN-major as it lies in memory, H (the same for all of them) K-major, in
 // parts.  With columns as the operand's rows a warp holds 32 neighbouring
-// columns of a token, so the additions to the base run along shared memory rows
-// that bulk copies bring and take away.  CTAs: a tile of tokens x a range of
-// column tiles.  While one column tile is added, the next one's product runs
-// and the one after is loaded.  Bound by the read of the base and the write of y.
-constexpr uint32_t kMaxParts = 3;
-template <typename T> struct Expand {
-    static constexpr uint32_t tokens = sizeof(T) == 4 ? 64 : 128;         // (two tiles of the base in 64 KB)
+// columns of a token, so the additions to the base run along rows in shared
+// memory, whose tiles TMA brings and takes away.  CTAs: a tile of tokens x a
+// range of column tiles; a step is one adapter of one column tile.  Warps 0 to 7
+// add; a thread of warp 8 brings W and issues the products, two steps ahead
+// of the additions; one of warp 9 brings the base and takes y away.
+// Bound by the read of the base and the write of y.
+constexpr uint32_t kExpandThreads = kThreads + 64;
+template <typename T, uint32_t kBlocks> struct Expand {       // kBlocks: blocks of 64 rank rows
+    static constexpr uint32_t tokens = sizeof(T) == 4 ? 64 : 128;         // (a tile of the base takes 32 KB)
     static constexpr uint32_t parts = sizeof(T) == 4 ? 3 : 2, part_bytes = tokens * 128;
-    static constexpr uint32_t h_bytes = parts * part_bytes, w_bytes = kTileBytes;
-    static constexpr uint32_t io_bytes = tokens * 128 * sizeof(T);
-    static constexpr size_t smem = 2 * (h_bytes + w_bytes + io_bytes) + 1024;
+    static constexpr uint32_t h_bytes = parts * kBlocks * part_bytes, w_bytes = kBlocks * kTileBytes, w_stages = kBlocks == 1 ? 3 : 2;
+    static constexpr uint32_t io_bytes = tokens * 128 * sizeof(T), io_stages = kBlocks == 1 ? 3 : 2;
+    static constexpr size_t smem = h_bytes + w_stages * w_bytes + io_stages * io_bytes + 1024;
     static_assert(smem <= 220 * 1024, "shared memory of one CTA");
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant__ ExpandParams P) {
-    using E = Expand<T>;
-    constexpr uint32_t NT = E::tokens;
+template <typename T, uint32_t kBlocks>
+__global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_constant__ ExpandParams P) {
+    using E = Expand<T, kBlocks>;
+    constexpr uint32_t NT = E::tokens, WS = E::w_stages, IS = E::io_stages;
     extern __shared__ uint8_t raw[];
     __shared__ TileAdapters tile;
-    __shared__ __align__(8) uint64_t s_mma[2], s_io[2];
+    __shared__ uint32_t s_mask[NT][NT / 32];  // tokens of each adapter of the tile
+    __shared__ __align__(8) uint64_t s_h, s_w[WS], s_wfree[WS], s_d[2], s_dfree[2], s_io[IS], s_iodone[IS];
     __shared__ uint32_t s_tmem;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const uint32_t h_at = smem_addr(smem), w_at = h_at + 2 * E::h_bytes, io_at = w_at + 2 * E::w_bytes;
-    uint8_t *io = smem + 2 * (E::h_bytes + E::w_bytes);
+    const uint32_t h_at = smem_addr(smem), w_at = h_at + E::h_bytes, io_at = w_at + WS * E::w_bytes;
+    uint8_t *io = smem + E::h_bytes + WS * E::w_bytes;
     const uint32_t rp = P.rank_pad;
     const uint64_t t0 = uint64_t(blockIdx.x / P.groups) * NT;
     const uint32_t group = blockIdx.x % P.groups, col_tiles = (P.len + 127) / 128;
-    const uint32_t c0 = uint32_t(uint64_t(col_tiles) * group / P.groups), c1 = uint32_t(uint64_t(col_tiles) * (group + 1) / P.groups);
+    const uint32_t c0 = uint32_t(uint64_t(col_tiles) * group / P.groups), tiles = uint32_t(uint64_t(col_tiles) * (group + 1) / P.groups) - c0;
     if (warp == 0) tmem_alloc(smem_addr(&s_tmem), 256);
-    if (tid == 0)
-        for (uint32_t i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&s_mma[i]), 1);
-            mbar_init(smem_addr(&s_io[i]), NT);
+    if (tid == 0) {
+        mbar_init(smem_addr(&s_h), 1);
+        for (uint32_t i = 0; i < WS; ++i) {
+            mbar_init(smem_addr(&s_w[i]), 1);
+            mbar_init(smem_addr(&s_wfree[i]), 1);
         }
-    if (tid == 0) fence_async_shared();
+        for (uint32_t i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&s_d[i]), 1);
+            mbar_init(smem_addr(&s_dfree[i]), kThreads / 32);
+        }
+        for (uint32_t i = 0; i < IS; ++i) {
+            mbar_init(smem_addr(&s_io[i]), 1);
+            mbar_init(smem_addr(&s_iodone[i]), kThreads / 32);
+        }
+    }
+    // the rank's padding in the stages of W, which no copy writes
+    for (uint32_t i = tid; i < WS * 2 * (rp - P.rank) * 8; i += kExpandThreads) {
+        const uint32_t c = i % 8, j = P.rank + i / 8 % (rp - P.rank), half = i / 8 / (rp - P.rank);
+        *reinterpret_cast<uint4 *>(smem + E::h_bytes + half / 2 * E::w_bytes + half % 2 * (kBlocks * kStep * 128) + j * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_async_shared();
     grid_dep_wait();
     const uint32_t count = tile_adapters(tile, P.ids, t0, P.n, NT, P.n_adapters, nullptr);
+    if (warp < NT / 32) {
+        const int32_t of = tile.of[warp * 32 + lane];
+        for (uint32_t a = 0; a < count; ++a) {
+            const uint32_t m = __ballot_sync(0xffffffffu, of == int32_t(a));
+            if (lane == 0) s_mask[a][warp] = m;
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
-    // the contraction in chunks of 64 rank rows: whole adapters, or 64 rows of one
-    const uint32_t per = rp <= kStep ? kStep / rp : 1, blocks = rp <= kStep ? 1 : (rp + kStep - 1) / kStep;
-    const uint32_t chunks = rp <= kStep ? (count + per - 1) / per : count * blocks;
-    const uint32_t tiles = c1 - c0, steps = tiles * max(chunks, 1u);
-    const bool resident = chunks <= 2;        // H of both chunks stays in its two places
-    // place of a chunk's row: adapter (in the tile's list), rank row
-    auto row_of = [&](uint32_t chunk, uint32_t r, uint32_t &a, uint32_t &j) {
-        if (rp <= kStep) {
-            a = chunk * per + r / rp;
-            j = r % rp;
-            return r < per * rp && a < count;
-        }
-        a = chunk / blocks;
-        j = chunk % blocks * kStep + r;
-        return j < rp;
-    };
-    auto load_h = [&](uint32_t chunk, uint32_t place) {
-        for (uint32_t i = tid; i < NT * 8; i += kThreads) {
-            const uint32_t t = i / 8, c = i % 8;
-            uint32_t a, j;
-            const bool in = row_of(chunk, c * 8, a, j) && t0 + t < P.n && tile.of[t] == int32_t(a);
-            const __nv_bfloat16 *src = in ? P.h + (t0 + t) * rp + j : P.h;
-#pragma unroll
-            for (uint32_t q = 0; q < E::parts; ++q)
-                cp_async16z(h_at + place * E::h_bytes + q * E::part_bytes + tile_at(t, c), in ? src + q * P.n * rp : src, in ? 16 : 0);
-        }
-    };
-    // this thread's part of a step: chunk tid % 16 of rows tid / 16 + 16 m
-    const uint32_t w_chunk = tid % 16;
-    uint32_t w_a[4], w_j[4], w_to[4];
-#pragma unroll
-    for (uint32_t m = 0; m < 4; ++m) {
-        const uint32_t r = tid / 16 + 16 * m;
-        w_a[m] = rp <= kStep ? r / rp : 0;
-        w_j[m] = rp <= kStep ? r % rp : 0;
-        w_to[m] = w_chunk / 8 * (kStep * 128) + tile_at(r, w_chunk % 8);
-    }
-    // step s: column tile c0 + s / chunks, chunk s % chunks
-    auto load_step = [&](uint32_t s) {
-        const uint32_t chunk = s % chunks, col = (c0 + s / chunks) * 128 + w_chunk * 8;
-#pragma unroll
-        for (uint32_t m = 0; m < 4; ++m) {
-            const uint32_t a = rp <= kStep ? chunk * per + w_a[m] : chunk / blocks, j = rp <= kStep ? w_j[m] : chunk % blocks * kStep + tid / 16 + 16 * m;
-            const bool in = w_a[m] < per && a < count && j < P.rank && col < P.len;
-            cp_async16z(w_at + (s & 1) * E::w_bytes + w_to[m], in ? P.w + (uint64_t(tile.list[a]) * P.rank + j) * P.len + col : P.w, in ? 16 : 0);
-        }
-        if (!resident) load_h(chunk, s & 1);
-    };
-    const uint32_t desc = mma_desc(128, NT, 1, 0);
-    auto multiply = [&](uint32_t s) {         // by one thread
-        const uint32_t chunk = s % chunks, d = tmem + (s / chunks & 1) * 128;
-        const uint64_t a = tile_desc(w_at + (s & 1) * E::w_bytes, kStep * 128, 1024);
-        const uint32_t h = h_at + (resident ? chunk : s & 1) * E::h_bytes;
-        tc_fence_after();
-#pragma unroll
-        for (uint32_t q = 0; q < E::parts; ++q) {
-            const uint64_t b = tile_desc(h + q * E::part_bytes, 16, 1024);
-#pragma unroll
-            for (uint32_t k = 0; k < kStep / 16; ++k) mma(d, a + k * 128, b + 2 * k, desc, chunk || q || k);
-        }
-        mma_commit(smem_addr(&s_mma[s & 1]));
-    };
-    // the base's rows of a column tile: thread t brings and takes away row t
-    const uint32_t rows = uint32_t(min(uint64_t(NT), P.n - t0));
-    auto row_bytes = [&](uint32_t i) { return min(128u, P.len - (c0 + i) * 128) * uint32_t(sizeof(T)); };
-    auto load_io = [&](uint32_t i) {
-        const uint32_t bar = smem_addr(&s_io[i & 1]);
-        if (tid < NT) {
-            const bool in = P.base && tid < rows;
-            mbar_expect(bar, in ? row_bytes(i) : 0);
-            if (in)
-                bulk_load(io_at + (i & 1) * E::io_bytes + tid * (128 * sizeof(T)), static_cast<const T *>(P.base) + (t0 + tid) * P.base_stride + (c0 + i) * 128, row_bytes(i), bar);
-        }
-    };
+    const uint32_t tmem = s_tmem, steps = tiles * count;
     bool ok = true;
-    load_io(0);
-    if (chunks) {
-        if (resident)
-            for (uint32_t c = 0; c < chunks; ++c) load_h(c, c);
-        load_step(0);
-        cp_async_commit();
-        if (steps > 1) load_step(1);
-        cp_async_commit();
-        cp_async_wait<1>();
-        fence_async_shared();
-        __syncthreads();
-        if (tid == 0) multiply(0);
-    }
-    for (uint32_t s = 0; s < steps; ++s) {
-        const uint32_t i = chunks ? s / chunks : s;
-        if (chunks) {
-            if (s + 1 < steps) {
-                cp_async_wait<0>();
-                fence_async_shared();
+    if (warp == 8) {
+        if (lane == 0 && steps) {
+            mbar_expect(smem_addr(&s_h), E::h_bytes);
+            for (uint32_t q = 0; q < E::parts; ++q)
+                for (uint32_t b = 0; b < kBlocks; ++b) tma_load(h_at + (q * kBlocks + b) * E::part_bytes, &P.h, int32_t(b * 64), int32_t(q * P.n + t0), smem_addr(&s_h));
+            // W of step s: two blocks of 64 columns, each the adapter's rank rows
+            auto load = [&](uint32_t s) {
+                const uint32_t bar = smem_addr(&s_w[s % WS]), at = w_at + s % WS * E::w_bytes;
+                mbar_expect(bar, 2 * P.rank * 128);
+                for (uint32_t half = 0; half < 2; ++half)
+                    tma_load(at + half * (kBlocks * kStep * 128), &P.w, int32_t((c0 + s / count) * 128 + half * 64), tile.list[s % count] * int32_t(P.rank), bar);
+            };
+            const uint32_t desc = mma_desc(128, NT, 1, 0);
+            uint32_t loaded = 0;
+            for (; loaded < min(WS, steps); ++loaded) load(loaded);
+            ok = mbar_wait(smem_addr(&s_h), 0);
+            for (uint32_t s = 0; s < steps && ok; ++s) {
+                ok = mbar_wait(smem_addr(&s_w[s % WS]), s / WS & 1);
+                if (s >= 2 && ok) ok = mbar_wait(smem_addr(&s_dfree[s & 1]), (s / 2 - 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t w = tile_desc(w_at + s % WS * E::w_bytes, kBlocks * kStep * 128, 1024);
+                for (uint32_t q = 0; q < E::parts; ++q)
+                    for (uint32_t k = 0; k < rp / 16; ++k)
+                        mma(tmem + (s & 1) * 128, w + k * 128, tile_desc(h_at + (q * kBlocks + k / 4) * E::part_bytes, 16, 1024) + 2 * (k % 4), desc, q || k);
+                mma_commit(smem_addr(&s_wfree[s % WS]));
+                mma_commit(smem_addr(&s_d[s & 1]));
+                // (a stage is free once the products before these are done)
+                if (s > 0 && loaded < steps) {
+                    ok = mbar_wait(smem_addr(&s_wfree[(s - 1) % WS]), (s - 1) / WS & 1);
+                    if (ok) load(loaded++);
+                }
+            }
+            if (!ok)                          // copies still in flight land first
+                for (uint32_t s = loaded > WS ? loaded - WS : 0; s < loaded; ++s) mbar_wait(smem_addr(&s_w[s % WS]), s / WS & 1);
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            auto load = [&](uint32_t i) {
+                const uint32_t bar = smem_addr(&s_io[i % IS]);
+                mbar_expect(bar, P.has_base ? E::io_bytes : 0);
+                if (P.has_base) tma_load(io_at + i % IS * E::io_bytes, &P.base, int32_t((c0 + i) * 128), int32_t(t0), bar);
+            };
+            for (uint32_t i = 0; i < min(IS, tiles); ++i) load(i);
+            for (uint32_t i = 0; i < tiles && ok; ++i) {
+                ok = mbar_wait(smem_addr(&s_iodone[i % IS]), i / IS & 1);
+                if (!ok) break;
+                tma_store(&P.y, int32_t((c0 + i) * 128), int32_t(t0), io_at + i % IS * E::io_bytes);
+                bulk_commit();
+                if (i + IS < tiles) {
+                    bulk_wait_read<0>();
+                    load(i + IS);
+                }
+            }
+            bulk_wait_all();
+        }
+    } else {
+        for (uint32_t i = 0; i < tiles; ++i) {
+            if (ok) ok = mbar_wait(smem_addr(&s_io[i % IS]), i / IS & 1);
+            T *mine = reinterpret_cast<T *>(io + i % IS * E::io_bytes) + warp % 4 * 32 + lane;
+            if (!P.has_base)
+                for (uint32_t t = warp / 4 * (NT / 2); t < (warp / 4 + 1) * (NT / 2); ++t)
+                    if (tile.of[t] < 0) st_f32(mine + t * 128, 0.f);
+            for (uint32_t a = 0; a < count; ++a) {
+                const uint32_t s = i * count + a;
+                if (ok) ok = mbar_wait(smem_addr(&s_d[s & 1]), s / 2 & 1);
+                tc_fence_after();
+#pragma unroll
+                for (uint32_t g = 0; g < NT / 64; ++g) {
+                    const uint32_t t = warp / 4 * (NT / 2) + g * 32, mask = s_mask[a][t / 32];
+                    if (mask == 0) continue;
+                    // (the base's values are fetched while the product comes from TMEM)
+                    uint32_t r[32];
+                    float b[32];
+                    tmem_load32(tmem + ((warp % 4) << 21) + (s & 1) * 128 + t, r);
+                    T *q = mine + t * 128;
+#pragma unroll
+                    for (uint32_t k = 0; k < 32; ++k) b[k] = P.has_base ? ld_f32(q + k * 128) : 0.f;
+                    tmem_wait32(r);
+                    if (mask == 0xffffffffu) {
+#pragma unroll
+                        for (uint32_t k = 0; k < 32; ++k) st_f32(q + k * 128, b[k] + __uint_as_float(r[k]));
+                    } else {
+#pragma unroll
+                        for (uint32_t k = 0; k < 32; ++k)
+                            if (mask >> k & 1) st_f32(q + k * 128, b[k] + __uint_as_float(r[k]));
+                    }
+                }
                 tc_fence_before();
-                __syncthreads();
-                if (tid == 0 && ok) multiply(s + 1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&s_dfree[s & 1]));
             }
-            if (ok) ok = mbar_wait(smem_addr(&s_mma[s & 1]), s / 2 & 1);
-            if (s + 2 < steps && ok) load_step(s + 2);
-            cp_async_commit();
-            if (s % chunks + 1 < chunks) continue;
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&s_iodone[i % IS]));
         }
-        // column tile i: the product is in its half of TMEM
-        if (i + 1 < tiles) {
-            if (tid < NT) bulk_wait_read<0>();          // (tile i - 1 has left the other buffer)
-            load_io(i + 1);
-        }
-        if (ok) ok = mbar_wait(smem_addr(&s_io[i & 1]), i / 2 & 1);
-        tc_fence_after();
-        T *mine = reinterpret_cast<T *>(io + (i & 1) * E::io_bytes) + warp % 4 * 32 + lane;
-        const uint32_t t_end = min((warp / 4 + 1) * (NT / 2), rows);
-        for (uint32_t t = warp / 4 * (NT / 2); t < t_end; t += 32) {
-            // (the base's values are fetched while the product comes from TMEM)
-            uint32_t r[32];
-            float b[32];
-            if (chunks) tmem_load32(tmem + ((warp % 4) << 21) + (i & 1) * 128 + t, r);
-            T *q = mine + t * 128;
-            if (P.base) {
-#pragma unroll
-                for (uint32_t k = 0; k < 32; ++k) b[k] = ld_f32(q + k * 128);
-            } else {
-#pragma unroll
-                for (uint32_t k = 0; k < 32; ++k) b[k] = 0.f;
-            }
-            if (chunks) {
-                tmem_wait32(r);
-#pragma unroll
-                for (uint32_t k = 0; k < 32; ++k) b[k] += __uint_as_float(r[k]);
-            }
-#pragma unroll
-            for (uint32_t k = 0; k < 32; ++k) st_f32(q + k * 128, b[k]);
-        }
-        tc_fence_before();
-        fence_async_shared();
-        __syncthreads();
-        if (tid < rows) bulk_store(static_cast<T *>(P.y) + (t0 + tid) * P.y_stride + (c0 + i) * 128, io_at + (i & 1) * E::io_bytes + tid * (128 * sizeof(T)), row_bytes(i));
-        if (tid < NT) bulk_commit();
     }
-    if (tid < NT) bulk_wait_all();
-    cp_async_wait<0>();
     if (!ok) atomicOr(P.status, K3HUF_ST_TIMEOUT);
     tc_fence_before();
     __syncthreads();
@@ -630,7 +605,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
 }
 
 struct OuterJob {
-    const __nv_bfloat16 *h, *v;               // parts x tokens x rank_pad; the rows that it multiplies
+    const __nv_bfloat16 *h, *v;               // parts x tokens x pitch; the rows that it multiplies
     float *g;
     uint64_t stride;
     uint32_t len;
@@ -640,7 +615,7 @@ struct OuterParams {
     const int32_t *ids;
     uint32_t *status;
     uint64_t n;
-    uint32_t n_adapters, rank, rank_pad, col_tiles0;       // column tiles of job 0
+    uint32_t n_adapters, rank, rank_pad, pitch, col_tiles0;        // column tiles of job 0
     bool add;
 };
 
@@ -737,9 +712,9 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
                     const bool in = k < total;
                     cp_async16z(to + at, in && v_in ? J.v + t * J.stride + col + c * 8 : J.v, in && v_in ? 16 : 0);
                     if (h_in) {
-                        const __nv_bfloat16 *src = J.h + t * rp + c * 8;
+                        const __nv_bfloat16 *src = J.h + t * P.pitch + c * 8;
 #pragma unroll
-                        for (uint32_t q = 0; q < kMaxParts; ++q) cp_async16z(to + kStep * 256 + q * (kBlocks * kStep * 128) + at, src + q * P.n * rp, in ? 16 : 0);
+                        for (uint32_t q = 0; q < kMaxParts; ++q) cp_async16z(to + kStep * 256 + q * (kBlocks * kStep * 128) + at, src + q * P.n * P.pitch, in ? 16 : 0);
                     }
                 }
             };
@@ -797,14 +772,15 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
 // --- host -----------------------------------------------------------------------
 
 bool adapters_ok(const k3huf_adapters_t *ad, uint64_t n) {
-    return ad && ad->a && ad->b && ad->scales && ad->n_adapters && ad->n_adapters < (1u << 24) && ad->rank && ad->rank <= K3HUF_MAX_RANK &&
-           ad->cols && ad->rows && ad->cols < (1ull << 31) && ad->rows < (1ull << 31) && n < (1ull << 31) && aligned_to(ad->a, 2) &&
+    return ad && ad->a && ad->b && ad->scales && ad->n_adapters && uint64_t(ad->n_adapters) * ad->rank < (1ull << 31) && ad->rank && ad->rank <= K3HUF_MAX_RANK &&
+           ad->cols && ad->rows && ad->cols < (1ull << 31) && ad->rows < (1ull << 31) && n < (1ull << 29) && aligned_to(ad->a, 2) &&
            aligned_to(ad->b, 2) && aligned_to(ad->scales, 4);
 }
 
 uint32_t padded(uint32_t rank) { return (rank + 15) / 16 * 16; }
-// Bytes of one rank-wide intermediate: fp32, or three bf16 parts of the padded rank.
-uint64_t h_bytes(uint64_t n, uint32_t rank) { return align_up(n * std::max<uint64_t>(4 * rank, 2 * kMaxParts * padded(rank)), 256); }
+// A rank-wide intermediate: fp32, or three bf16 parts in blocks of 64 values.
+uint32_t h_pitch(uint32_t rank) { return (rank + 63) / 64 * 64; }
+uint64_t h_bytes(uint64_t n, uint32_t rank) { return align_up(n * 2 * kMaxParts * h_pitch(rank), 256); }
 
 enum class Form { any, few, many };
 bool rows16(const void *p, uint64_t stride, uint32_t type) { return aligned_to(p, 16) && stride * elem_bytes(type) % 16 == 0; }
@@ -827,6 +803,13 @@ int launch_after(void (*kernel)(Args...), dim3 grid, uint32_t threads, size_t sm
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cuda_rc(cudaLaunchKernelEx(&cfg, kernel, Args(args)...));
+}
+
+int shrink_job(ShrinkParams &P, uint32_t j, const void *v, uint64_t stride, const void *w, uint64_t len, __nv_bfloat16 *h) {
+    P.job[j].len = uint32_t(len);
+    P.job[j].h = h;
+    const int rc = tensor_map(&P.job[j].v, v, K3HUF_BF16, P.n, len, stride, kTile, kStep, true);
+    return rc ? rc : tensor_map(&P.job[j].w, w, K3HUF_BF16, uint64_t(P.n_adapters) * P.rank, len, len, P.rank, kStep, true);
 }
 
 int launch_shrink(ShrinkParams &P, uint32_t jobs, uint64_t sms, cudaStream_t stream) {
@@ -855,23 +838,38 @@ int launch_shrink(ShrinkParams &P, uint32_t jobs, uint64_t sms, cudaStream_t str
     return cuda_rc(cudaLaunchKernelEx(&cfg, shrink_kernel, P));
 }
 
-template <typename T>
-int launch_expand(ExpandParams &P, uint64_t sms, cudaStream_t stream) {
+template <typename T, uint32_t kBlocks>
+int launch_expand(ExpandParams &P, const void *h, const void *w, const void *base, uint64_t base_stride, void *y, uint64_t y_stride, uint64_t sms, cudaStream_t stream) {
+    using E = Expand<T, kBlocks>;
     static std::atomic<uint64_t> once{0};
-    const int rc = once_per_device(once, [] { return cudaFuncSetAttribute(expand_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Expand<T>::smem)); });
+    int rc = once_per_device(once, [] { return cudaFuncSetAttribute(expand_kernel<T, kBlocks>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(E::smem)); });
     if (rc) return rc;
-    const uint64_t tiles = (P.n + Expand<T>::tokens - 1) / Expand<T>::tokens, cols = (P.len + 127) / 128;
+    constexpr uint32_t type = sizeof(T) == 4 ? K3HUF_F32 : K3HUF_BF16;
+    rc = tensor_map(&P.h, h, K3HUF_BF16, E::parts * P.n, kBlocks * 64, kBlocks * 64, E::tokens, 64, true);
+    if (!rc) rc = tensor_map(&P.w, w, K3HUF_BF16, uint64_t(P.n_adapters) * P.rank, P.len, P.len, P.rank, 64, true);
+    if (!rc) rc = tensor_map(&P.y, y, type, P.n, P.len, y_stride, E::tokens, 128, false);
+    if (!rc) rc = base ? tensor_map(&P.base, base, type, P.n, P.len, base_stride, E::tokens, 128, false) : K3HUF_OK;
+    if (rc) return rc;
+    P.has_base = base != nullptr;
+    const uint64_t tiles = (P.n + E::tokens - 1) / E::tokens, cols = (P.len + 127) / 128;
     // column ranges per token tile: the count whose last wave of CTAs (one per SM) is fullest,
     // among those that give an SM up to three waves
     uint64_t best = 1;
     double waste = 1e30;
     for (uint64_t g = 1; g <= cols && g <= std::max<uint64_t>(1, 3 * sms / tiles); ++g) {
         const uint64_t waves = (tiles * g + sms - 1) / sms, per = (cols + g - 1) / g;
-        const double w = double(waves * (per + 1));        // (a CTA's start costs about one column tile)
-        if (w < waste) waste = w, best = g;
+        const double cost = double(waves * (per + 2));     // (a CTA's start costs about two column tiles)
+        if (cost < waste) waste = cost, best = g;
     }
     P.groups = uint32_t(best);
-    return launch_after(expand_kernel<T>, dim3(uint32_t(tiles * best)), kThreads, Expand<T>::smem, stream, P);
+    return launch_after(expand_kernel<T, kBlocks>, dim3(uint32_t(tiles * best)), kExpandThreads, E::smem, stream, P);
+}
+int launch_expand(ExpandParams &P, const void *h, const void *w, const void *base, uint64_t base_stride, void *y, uint64_t y_stride, uint32_t type, uint64_t sms, cudaStream_t stream) {
+    if (P.rank_pad <= kStep)
+        return type == K3HUF_BF16 ? launch_expand<__nv_bfloat16, 1>(P, h, w, base, base_stride, y, y_stride, sms, stream)
+                                  : launch_expand<float, 1>(P, h, w, base, base_stride, y, y_stride, sms, stream);
+    return type == K3HUF_BF16 ? launch_expand<__nv_bfloat16, 2>(P, h, w, base, base_stride, y, y_stride, sms, stream)
+                              : launch_expand<float, 2>(P, h, w, base, base_stride, y, y_stride, sms, stream);
 }
 
 int launch_outer(const OuterParams &P, uint32_t col_tiles, cudaStream_t stream) {
@@ -892,7 +890,7 @@ int launch_outer(const OuterParams &P, uint32_t col_tiles, cudaStream_t stream) 
 using namespace k3huf;
 
 extern "C" int k3huf_adapter_scratch_bytes(uint64_t n_tokens, uint32_t n_adapters, uint32_t rank, uint64_t cols, uint64_t rows, int grad, size_t *scratch_bytes) {
-    if (!scratch_bytes || n_adapters == 0 || rank == 0 || rank > K3HUF_MAX_RANK || cols == 0 || rows == 0 || n_tokens >= (1ull << 31)) return K3HUF_E_ARG;
+    if (!scratch_bytes || n_adapters == 0 || rank == 0 || rank > K3HUF_MAX_RANK || cols == 0 || rows == 0 || n_tokens >= (1ull << 29)) return K3HUF_E_ARG;
     *scratch_bytes = 256 + h_bytes(n_tokens, rank) * (grad ? 2 : 1);
     return K3HUF_OK;
 }
@@ -940,11 +938,15 @@ extern "C" int k3huf_adapter_apply(const k3huf_adapters_t *ad, const void *d_x, 
     int rc = sm_count(&sms);
     if (rc) return rc;
     auto *h = static_cast<__nv_bfloat16 *>(d_scratch);
-    ShrinkParams sp{{{x, a, x_stride, uint32_t(ad->cols), h}}, ad->scales, d_ids, d_status, n, S, r, padded(r), y_type == K3HUF_F32 ? 3u : 2u, 1};
-    rc = launch_shrink(sp, 1, sms, st);
+    ShrinkParams sp{};
+    sp.scales = ad->scales, sp.ids = d_ids, sp.status = d_status, sp.n = n;
+    sp.n_adapters = S, sp.rank = r, sp.rank_pad = padded(r), sp.pitch = h_pitch(r), sp.parts = y_type == K3HUF_F32 ? 3 : 2;
+    rc = shrink_job(sp, 0, x, x_stride, a, ad->cols, h);
+    if (!rc) rc = launch_shrink(sp, 1, sms, st);
     if (rc) return rc;
-    ExpandParams ep{h, b, d_base, d_y, d_ids, d_status, n, base_stride, y_stride, S, r, padded(r), uint32_t(ad->rows), 1};
-    return y_type == K3HUF_BF16 ? launch_expand<__nv_bfloat16>(ep, sms, st) : launch_expand<float>(ep, sms, st);
+    ExpandParams ep{};
+    ep.ids = d_ids, ep.status = d_status, ep.n = n, ep.n_adapters = S, ep.rank = r, ep.rank_pad = padded(r), ep.len = uint32_t(ad->rows);
+    return launch_expand(ep, h, b, d_base, base_stride, d_y, y_stride, y_type, sms, st);
 }
 
 extern "C" int k3huf_adapter_grad(const k3huf_adapters_t *ad, const void *d_x, uint64_t x_stride, const int32_t *d_ids, uint64_t n_tokens,
@@ -985,15 +987,20 @@ extern "C" int k3huf_adapter_grad(const k3huf_adapters_t *ad, const void *d_x, u
     int rc = sm_count(&sms);
     if (rc) return rc;
     auto *h = reinterpret_cast<__nv_bfloat16 *>(h0), *dh = reinterpret_cast<__nv_bfloat16 *>(h1);
-    ShrinkParams sp{{{x, a, x_stride, uint32_t(ad->cols), h}, {dy, b, dy_stride, uint32_t(ad->rows), dh}}, ad->scales, d_ids, d_status, n, S, r, padded(r), kMaxParts, 1};
-    rc = launch_shrink(sp, 2, sms, st);
+    ShrinkParams sp{};
+    sp.scales = ad->scales, sp.ids = d_ids, sp.status = d_status, sp.n = n;
+    sp.n_adapters = S, sp.rank = r, sp.rank_pad = padded(r), sp.pitch = h_pitch(r), sp.parts = kMaxParts;
+    rc = shrink_job(sp, 0, x, x_stride, a, ad->cols, h);
+    if (!rc) rc = shrink_job(sp, 1, dy, dy_stride, b, ad->rows, dh);
+    if (!rc) rc = launch_shrink(sp, 2, sms, st);
     if (rc) return rc;
     if (d_dx) {
-        ExpandParams ep{dh, a, d_dx_base, d_dx, d_ids, d_status, n, dx_base_stride, dx_stride, S, r, padded(r), uint32_t(ad->cols), 1};
-        rc = dx_type == K3HUF_BF16 ? launch_expand<__nv_bfloat16>(ep, sms, st) : launch_expand<float>(ep, sms, st);
+        ExpandParams ep{};
+        ep.ids = d_ids, ep.status = d_status, ep.n = n, ep.n_adapters = S, ep.rank = r, ep.rank_pad = padded(r), ep.len = uint32_t(ad->cols);
+        rc = launch_expand(ep, dh, a, d_dx_base, dx_base_stride, d_dx, dx_stride, dx_type, sms, st);
         if (rc) return rc;
     }
     const uint32_t tiles_a = uint32_t((ad->cols + 127) / 128), tiles_b = uint32_t((ad->rows + 127) / 128);
-    const OuterParams op{{{dh, x, d_da, x_stride, uint32_t(ad->cols)}, {h, dy, d_db, dy_stride, uint32_t(ad->rows)}}, d_ids, d_status, n, S, r, padded(r), tiles_a, add};
+    const OuterParams op{{{dh, x, d_da, x_stride, uint32_t(ad->cols)}, {h, dy, d_db, dy_stride, uint32_t(ad->rows)}}, d_ids, d_status, n, S, r, padded(r), h_pitch(r), tiles_a, add};
     return launch_outer(op, tiles_a + tiles_b, st);
 }
