@@ -18,13 +18,13 @@
 // after the table's build; many, the instructions of both halves.
 #include <algorithm>
 
-#include "k3huf_ops.h"
+#include "k3huf_tc.h"
 
 namespace k3huf {
 namespace {
 
 constexpr int kMaxStripes = 256;              // stripes of the tensor (kernel parameter space)
-constexpr int kThreads = 128;                 // (gradient and one-symbol lookup kernels)
+constexpr int kThreads = 128;                 // (one-symbol lookup kernel)
 constexpr int kWarps = 24, kEmbedThreads = 32 * kWarps;
 constexpr uint32_t kPieces = 256;             // 16-byte pieces of bits staged per warp
 constexpr int kRound = 64;                    // values per unit between joins
@@ -503,30 +503,330 @@ int launch_rows(EmbedParams &P, cudaStream_t stream) {
     return vec ? launch_embed<T, false, true>(P, grid, stream) : launch_embed<T, false, false>(P, grid, stream);
 }
 
-// One CTA per token; the first token of each id adds up all of that id, in
-// the order of the tokens.
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-embed_grad_kernel(const void *ids, uint32_t id_bytes, uint64_t n, const T *dy, uint64_t dy_stride, uint64_t rows, uint64_t cols, float scale, float *grad, uint32_t *status) {
-    const uint64_t t = blockIdx.x;
-    const int64_t id = ld_id(ids, id_bytes, t);
-    if (id < 0 || uint64_t(id) >= rows) {
-        if (id >= 0 && threadIdx.x == 0) atomicOr(status, K3HUF_ST_TOKEN);
+// --- the gradient ---------------------------------------------------------------
+//
+// Blocks of up to kBlock tokens.  A CTA sorts a block's tokens by id in shared
+// memory (stable, so equal ids keep the tokens' order), while the other CTAs of
+// the launch write the zeros of a gradient that is not accumulated.  The second
+// launch adds up each id's rows: a warp per id and 1024 columns, 16 bytes per
+// lane and load, or, for an id with more than kHeavy tokens, a CTA per 256
+// columns whose warps take a share of the tokens each and meet in shared memory.
+// One such launch per block, in order, so that every sum has one order.  Bound
+// by the write of the gradient, or by the read of dY and the rows that it meets.
+constexpr uint32_t kBlock = 16384, kSortThreads = 1024, kHeavy = 64, kDigit = 9;
+constexpr uint32_t kItems = kBlock / kSortThreads;
+constexpr uint32_t kSumThreads = 256, kHeavyCols = 256;
+constexpr size_t kSortSmem = kBlock * (4 + 2) + (kSortThreads / 32) * (1u << kDigit) * 2;
+
+// A block's outcome in the scratch.
+struct Sorted {
+    uint32_t ids, heavy, pad[62];             // numbers of distinct ids and of those with many tokens
+    uint32_t order[kBlock];                   // tokens by id
+    uint32_t id[kBlock], start[kBlock + 1];   // each id and its first place in `order`; start[ids] is the end
+    uint32_t many[kBlock / kHeavy];           // places in `id` of those with many tokens
+    uint32_t pad1[63];
+};
+static_assert(sizeof(Sorted) % 256 == 0, "");
+
+struct GradSortParams {
+    const void *ids;
+    Sorted *out;
+    float4 *zero;                             // gradient to zero, or null
+    uint64_t zero_vecs, n, rows;
+    uint32_t *status;
+    uint32_t id_bytes, blocks, bits;          // bits of a key: the id, or `rows` for none
+};
+
+__global__ void __launch_bounds__(kSortThreads) grad_sort_kernel(const GradSortParams P) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint32_t s_base[1u << kDigit], s_warp[kSortThreads / 32 + 1], s_heavy;
+    grid_dep_launch();
+    const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    if (blockIdx.x >= P.blocks) {
+        const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (uint64_t i = uint64_t(blockIdx.x - P.blocks) * kSortThreads + tid; i < P.zero_vecs; i += uint64_t(gridDim.x - P.blocks) * kSortThreads) __stcs(P.zero + i, none);
         return;
     }
-    int seen = 0;
-    for (uint64_t u = threadIdx.x; u < t; u += kThreads) seen |= ld_id(ids, id_bytes, u) == id;
-    if (__syncthreads_or(seen)) return;
-    for (uint64_t c = threadIdx.x; c < cols; c += kThreads) {
-        float sum = 0.f;
-        for (uint64_t u = t; u < n; ++u)
-            if (ld_id(ids, id_bytes, u) == id) sum += ld_f32(dy + u * dy_stride + c);
-        grad[uint64_t(id) * cols + c] += scale * sum;
+    uint32_t *keys = reinterpret_cast<uint32_t *>(smem);
+    uint16_t *places = reinterpret_cast<uint16_t *>(smem + kBlock * 4);
+    uint16_t(*hist)[1u << kDigit] = reinterpret_cast<uint16_t(*)[1u << kDigit]>(smem + kBlock * 6);
+    const uint64_t t0 = uint64_t(blockIdx.x) * kBlock;
+    const uint32_t n = uint32_t(min(uint64_t(kBlock), P.n - t0));
+    Sorted &out = P.out[blockIdx.x];
+    // item k of a thread is number (warp * items + k) * 32 + lane: warps hold runs
+    const uint32_t items = (n + kSortThreads - 1) / kSortThreads;
+    uint32_t key[kItems], place[kItems];
+#pragma unroll
+    for (uint32_t k = 0; k < kItems; ++k) {
+        const uint32_t i = (warp * items + k) * 32 + lane;
+        key[k] = 0xFFFFFFFFu;                 // (past the block: after everything)
+        place[k] = i;
+        if (k < items && i < n) {
+            const int64_t id = ld_id(P.ids, P.id_bytes, t0 + i);
+            key[k] = id >= 0 && uint64_t(id) < P.rows ? uint32_t(id) : uint32_t(P.rows);
+            if (id >= 0 && uint64_t(id) >= P.rows) atomicOr(P.status, K3HUF_ST_TOKEN);
+        }
+    }
+    // sums over the CTA's threads before this one
+    auto before = [&](uint32_t v, uint32_t &total) {
+        uint32_t incl = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= uint32_t(d)) incl += o;
+        }
+        __syncthreads();
+        if (lane == 31) s_warp[warp] = incl;
+        __syncthreads();
+        if (warp == 0) {
+            const uint32_t w = s_warp[lane];
+            uint32_t all = w;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t o = __shfl_up_sync(0xffffffffu, all, d);
+                if (lane >= uint32_t(d)) all += o;
+            }
+            s_warp[lane] = all - w;
+            if (lane == 31) s_warp[32] = all;
+        }
+        __syncthreads();
+        total = s_warp[32];
+        return s_warp[warp] + incl - v;
+    };
+    const uint32_t passes = (P.bits + kDigit - 1) / kDigit, width = (P.bits + passes - 1) / passes, bins = 1u << width;
+    for (uint32_t pass = 0; pass < passes; ++pass) {
+        // places within the warp's items of equal digit, in order
+        uint32_t rank[kItems];
+        for (uint32_t d = lane; d < bins; d += 32) hist[warp][d] = 0;
+        __syncwarp();
+#pragma unroll
+        for (uint32_t k = 0; k < kItems; ++k) {
+            if (k >= items) break;
+            const uint32_t d = key[k] >> (pass * width) & (bins - 1);
+            const uint32_t same = __match_any_sync(0xffffffffu, d), below = __popc(same & ((1u << lane) - 1u));
+            const uint32_t had = hist[warp][d];
+            __syncwarp();
+            if (below == 0) hist[warp][d] = uint16_t(had + __popc(same));
+            __syncwarp();
+            rank[k] = had + below;
+        }
+        __syncthreads();
+        // counts to first places: by digit, then by warp
+        uint32_t mine = 0;
+        if (tid < bins)
+            for (uint32_t w = 0; w < kSortThreads / 32; ++w) {
+                const uint32_t c = hist[w][tid];
+                hist[w][tid] = uint16_t(mine);
+                mine += c;
+            }
+        uint32_t total;
+        const uint32_t first = before(mine, total);
+        if (tid < bins) s_base[tid] = first;
+        __syncthreads();
+#pragma unroll
+        for (uint32_t k = 0; k < kItems; ++k) {
+            if (k >= items) break;
+            const uint32_t d = key[k] >> (pass * width) & (bins - 1), to = s_base[d] + hist[warp][d] + rank[k];
+            keys[to] = key[k];
+            places[to] = uint16_t(place[k]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (uint32_t k = 0; k < kItems; ++k) {
+            if (k >= items) break;
+            const uint32_t i = (warp * items + k) * 32 + lane;
+            key[k] = keys[i];
+            place[k] = places[i];
+        }
+    }
+    // the distinct ids: thread t looks at places t * items and on
+    if (tid == 0) s_heavy = 0;
+    uint32_t heads = 0;
+    for (uint32_t k = 0; k < items; ++k) {
+        const uint32_t i = tid * items + k;
+        if (i < n && keys[i] < P.rows && (i == 0 || keys[i - 1] != keys[i])) ++heads;
+    }
+    uint32_t total;
+    uint32_t at = before(heads, total);
+    for (uint32_t k = 0; k < items; ++k) {
+        const uint32_t i = tid * items + k;
+        if (i >= n) break;
+        out.order[i] = places[i];
+        if (keys[i] < P.rows && (i == 0 || keys[i - 1] != keys[i])) {
+            out.id[at] = keys[i];
+            out.start[at] = i;
+            // (equal keys are adjacent: more than kHeavy of them reach kHeavy places on)
+            if (i + kHeavy < n && keys[i + kHeavy] == keys[i]) out.many[atomicAdd(&s_heavy, 1u)] = at;
+            ++at;
+        }
+        if (keys[i] < P.rows && (i + 1 == n || keys[i + 1] >= P.rows)) out.start[total] = i + 1;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        out.ids = total;
+        out.heavy = s_heavy;
     }
 }
 
+struct GradSumParams {
+    const Sorted *block;
+    const void *dy;                           // the block's first token's row
+    float *grad;
+    uint64_t dy_stride, cols;
+    uint32_t slabs, heavy_slabs, heavy_blocks;             // of 1024 columns; of kHeavyCols; CTAs for ids with many tokens
+    float scale;
+    bool add;
+};
+
+// kVec: 16-byte loads and stores; eight adjacent columns per lane
+template <typename T, bool kVec>
+__device__ __forceinline__ void add8(const T *p, uint64_t left, float (&acc)[8]) {
+    if constexpr (kVec && sizeof(T) == 2) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            acc[2 * i] += __uint_as_float(w[i] << 16);
+            acc[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else if constexpr (kVec) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+        acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w, acc[4] += b.x, acc[5] += b.y, acc[6] += b.z, acc[7] += b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (uint64_t(i) < left) acc[i] += ld_f32(p + i);
+    }
+}
+template <bool kVec>
+__device__ __forceinline__ void put8(float *g, uint64_t left, const float (&v)[8], float scale, bool add) {
+    if constexpr (kVec) {
+        float4 *q = reinterpret_cast<float4 *>(g);
+        float4 a = make_float4(scale * v[0], scale * v[1], scale * v[2], scale * v[3]), b = make_float4(scale * v[4], scale * v[5], scale * v[6], scale * v[7]);
+        if (add) {
+            const float4 x = q[0], y = q[1];
+            a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w, b.x += y.x, b.y += y.y, b.z += y.z, b.w += y.w;
+        }
+        q[0] = a;
+        q[1] = b;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (uint64_t(i) < left) g[i] = add ? g[i] + scale * v[i] : scale * v[i];
+    }
+}
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kSumThreads) grad_sum_kernel(const GradSumParams P) {
+    __shared__ float s_part[kSumThreads / 32][kHeavyCols];
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const Sorted &S = *P.block;
+    const T *dy = static_cast<const T *>(P.dy);
+    grid_dep_launch();
+    grid_dep_wait();
+    if (blockIdx.x < P.heavy_blocks) {
+        const uint32_t h = blockIdx.x / P.heavy_slabs;
+        if (h >= S.heavy) return;
+        const uint32_t u = S.many[h], begin = S.start[u], count = S.start[u + 1] - begin;
+        const uint64_t c = uint64_t(blockIdx.x % P.heavy_slabs) * kHeavyCols + lane * 8;
+        const uint64_t left = c < P.cols ? P.cols - c : 0;
+        float acc[8] = {};
+        const uint32_t j1 = begin + uint32_t(uint64_t(count) * (warp + 1) / 8);
+        if (left)
+#pragma unroll 8
+            for (uint32_t j = begin + uint32_t(uint64_t(count) * warp / 8); j < j1; ++j) add8<T, kVec>(dy + S.order[j] * P.dy_stride + c, left, acc);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s_part[warp][i * 32 + lane] = acc[i];
+        __syncthreads();
+        if (warp == 0 && left) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float sum = 0.f;
+                for (uint32_t w = 0; w < kSumThreads / 32; ++w) sum += s_part[w][i * 32 + lane];
+                acc[i] = sum;
+            }
+            put8<kVec>(P.grad + uint64_t(S.id[u]) * P.cols + c, left, acc, P.scale, P.add);
+        }
+        return;
+    }
+    const uint64_t unit = uint64_t(blockIdx.x - P.heavy_blocks) * (kSumThreads / 32) + warp;
+    const uint64_t u = unit / P.slabs;
+    if (u >= S.ids) return;
+    const uint32_t begin = S.start[u], end = S.start[u + 1];
+    if (end - begin > kHeavy) return;
+    const uint64_t c0 = unit % P.slabs * 1024 + lane * 8;
+    float *g = P.grad + uint64_t(S.id[u]) * P.cols;
+    float acc[4][8] = {};
+#pragma unroll 2
+    for (uint32_t j = begin; j < end; ++j) {
+        const T *row = dy + S.order[j] * P.dy_stride;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (c0 + k * 256 < P.cols) add8<T, kVec>(row + c0 + k * 256, P.cols - (c0 + k * 256), acc[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (c0 + k * 256 < P.cols) put8<kVec>(g + c0 + k * 256, P.cols - (c0 + k * 256), acc[k], P.scale, P.add);
+}
+
+// Fewer than four gradient elements, or an address that is not 16-byte aligned: the zeros that
+// whole vectors leave out.
 __global__ void zero_kernel(float *g, uint64_t n) {
     for (uint64_t i = uint64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += uint64_t(gridDim.x) * blockDim.x) g[i] = 0.f;
+}
+
+template <typename T>
+int launch_grad(const void *d_ids, uint32_t id_bytes, uint64_t n, const T *dy, uint64_t dy_stride, uint64_t rows, uint64_t cols, float scale, float *grad, Sorted *sorted,
+                uint32_t *status, bool add, cudaStream_t stream) {
+    static std::atomic<uint64_t> once{0};
+    int rc = once_per_device(once, [] { return cudaFuncSetAttribute(grad_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSortSmem)); });
+    if (rc) return rc;
+    uint64_t sms = 0;
+    rc = sm_count(&sms);
+    if (rc) return rc;
+    GradSortParams Q{};
+    Q.ids = d_ids, Q.out = sorted, Q.n = n, Q.rows = rows, Q.status = status, Q.id_bytes = id_bytes;
+    Q.blocks = uint32_t((n + kBlock - 1) / kBlock);
+    for (Q.bits = 1; (rows >> Q.bits) != 0; ++Q.bits) {}
+    uint32_t zero_blocks = 0;
+    if (!add) {
+        const uint64_t all = rows * cols, vecs = aligned_to(grad, 16) ? all / 4 : 0;
+        Q.zero = reinterpret_cast<float4 *>(grad);
+        Q.zero_vecs = vecs;
+        zero_blocks = uint32_t(std::min<uint64_t>(sms, (vecs + kSortThreads - 1) / kSortThreads));
+        if (vecs * 4 < all) {
+            zero_kernel<<<uint32_t(std::min<uint64_t>(8 * sms, (all - vecs * 4 + 255) / 256)), 256, 0, stream>>>(grad + vecs * 4, all - vecs * 4);
+            rc = cuda_rc(cudaGetLastError());
+            if (rc) return rc;
+        }
+    }
+    if (Q.blocks + zero_blocks == 0) return K3HUF_OK;
+    grad_sort_kernel<<<Q.blocks + zero_blocks, kSortThreads, kSortSmem, stream>>>(Q);
+    rc = cuda_rc(cudaGetLastError());
+    const bool vec = cols % 8 == 0 && aligned_to(dy, 16) && dy_stride * sizeof(T) % 16 == 0 && aligned_to(grad, 16);
+    for (uint32_t b = 0; b < Q.blocks && !rc; ++b) {
+        const uint64_t size = std::min<uint64_t>(kBlock, n - uint64_t(b) * kBlock);
+        GradSumParams P{};
+        P.block = sorted + b;
+        P.dy = dy + uint64_t(b) * kBlock * dy_stride;
+        P.grad = grad, P.dy_stride = dy_stride, P.cols = cols, P.scale = scale, P.add = add || b > 0;
+        P.slabs = uint32_t((cols + 1023) / 1024);
+        P.heavy_slabs = uint32_t((cols + kHeavyCols - 1) / kHeavyCols);
+        const uint64_t heavy = size / (kHeavy + 1) * P.heavy_slabs, light = (std::min(size, rows) * P.slabs + kSumThreads / 32 - 1) / (kSumThreads / 32);
+        if (heavy + light > 0x7FFFFFFFull) return K3HUF_E_ARG;
+        P.heavy_blocks = uint32_t(heavy);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(uint32_t(heavy + light));
+        cfg.blockDim = dim3(kSumThreads);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        rc = cuda_rc(vec ? cudaLaunchKernelEx(&cfg, grad_sum_kernel<T, true>, P) : cudaLaunchKernelEx(&cfg, grad_sum_kernel<T, false>, P));
+    }
+    return rc;
 }
 
 }  // namespace
@@ -594,8 +894,8 @@ extern "C" int k3huf_embed_layer(const void *h_layer_hdr, size_t hdr_bytes, cons
 }
 
 extern "C" int k3huf_embed_grad_scratch_bytes(uint64_t n_tokens, uint64_t rows, uint64_t cols, size_t *scratch_bytes) {
-    if (!scratch_bytes || rows == 0 || cols == 0) return K3HUF_E_ARG;
-    *scratch_bytes = 256;
+    if (!scratch_bytes || rows == 0 || rows >= (1ull << 31) || cols == 0 || cols >= (1ull << 31) || n_tokens > 0x7FFFFFFFull) return K3HUF_E_ARG;
+    *scratch_bytes = std::max<uint64_t>(1, (n_tokens + kBlock - 1) / kBlock) * sizeof(Sorted);
     return K3HUF_OK;
 }
 
@@ -611,13 +911,9 @@ extern "C" int k3huf_embed_grad(const void *d_ids, uint32_t id_bytes, uint64_t n
         return K3HUF_E_ARG;
     if (n_tokens == 0 && (flags & K3HUF_ACCUMULATE)) return K3HUF_OK;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (!(flags & K3HUF_ACCUMULATE)) {
-        const uint64_t n = rows * cols;
-        zero_kernel<<<uint32_t(std::min<uint64_t>(1216, (n + 255) / 256)), 256, 0, st>>>(d_grad, n);
-    }
-    if (n_tokens && dy_type == K3HUF_BF16)
-        embed_grad_kernel<<<uint32_t(n_tokens), kThreads, 0, st>>>(d_ids, id_bytes, n_tokens, static_cast<const __nv_bfloat16 *>(d_dy), dy_stride, rows, cols, scale, d_grad, d_status);
-    else if (n_tokens)
-        embed_grad_kernel<<<uint32_t(n_tokens), kThreads, 0, st>>>(d_ids, id_bytes, n_tokens, static_cast<const float *>(d_dy), dy_stride, rows, cols, scale, d_grad, d_status);
-    return cuda_rc(cudaGetLastError());
+    const bool add = (flags & K3HUF_ACCUMULATE) != 0;
+    Sorted *sorted = static_cast<Sorted *>(d_scratch);
+    if (dy_type == K3HUF_BF16)
+        return launch_grad(d_ids, id_bytes, n_tokens, static_cast<const __nv_bfloat16 *>(d_dy), dy_stride, rows, cols, scale, d_grad, sorted, d_status, add, st);
+    return launch_grad(d_ids, id_bytes, n_tokens, static_cast<const float *>(d_dy), dy_stride, rows, cols, scale, d_grad, sorted, d_status, add, st);
 }
