@@ -769,6 +769,62 @@ __global__ void __launch_bounds__(kSumThreads) grad_sum_kernel(const GradSumPara
         if (c0 + k * 256 < P.cols) put8<kVec>(g + c0 + k * 256, P.cols - (c0 + k * 256), acc[k], P.scale, P.add);
 }
 
+// Up to kFewTokens tokens, without a sort: a CTA per token and 2048 columns
+// compares its id with all others; the id's first token's CTA adds up all of
+// them, a warp per 256 columns, eight tokens' loads in flight.
+constexpr uint32_t kFewTokens = 1024;
+struct GradFewParams {
+    const void *ids, *dy;
+    float *grad;
+    uint32_t *status;
+    uint64_t dy_stride, rows, cols;
+    uint32_t n, id_bytes;
+    float scale;
+    bool add;
+};
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kSumThreads) grad_few_kernel(const GradFewParams P) {
+    __shared__ uint32_t s_same[kFewTokens / 32];
+    __shared__ uint16_t s_token[kFewTokens];
+    const uint32_t t = blockIdx.x, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int64_t id = ld_id(P.ids, P.id_bytes, t);
+    if (id < 0 || uint64_t(id) >= P.rows) {
+        if (id >= 0 && tid == 0 && blockIdx.y == 0) atomicOr(P.status, K3HUF_ST_TOKEN);
+        return;
+    }
+    int earlier = 0;
+#pragma unroll
+    for (uint32_t k = 0; k < kFewTokens / kSumThreads; ++k) {
+        const uint32_t u = k * kSumThreads + tid;
+        const bool same = u < P.n && ld_id(P.ids, P.id_bytes, u) == id;
+        earlier |= same && u < t;
+        const uint32_t m = __ballot_sync(0xffffffffu, same);
+        if (lane == 0) s_same[k * (kSumThreads / 32) + warp] = m;
+    }
+    if (__syncthreads_or(earlier)) return;
+    // the tokens in order: word `lane` of the matches goes behind the words before it
+    const uint32_t mine = s_same[lane];
+    uint32_t at = __popc(mine);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, at, d);
+        if (lane >= uint32_t(d)) at += v;
+    }
+    const uint32_t count = __shfl_sync(0xffffffffu, at, 31);
+    if (warp == 0) {
+        at -= __popc(mine);
+        for (uint32_t m = mine; m; m &= m - 1) s_token[at++] = uint16_t(lane * 32 + __ffs(m) - 1);
+    }
+    __syncthreads();
+    const uint64_t c = uint64_t(blockIdx.y) * 2048 + warp * 256 + lane * 8;
+    if (c >= P.cols) return;
+    const T *dy = static_cast<const T *>(P.dy) + c;
+    float acc[8] = {};
+#pragma unroll 8
+    for (uint32_t j = 0; j < count; ++j) add8<T, kVec>(dy + s_token[j] * P.dy_stride, P.cols - c, acc);
+    put8<kVec>(P.grad + uint64_t(id) * P.cols + c, P.cols - c, acc, P.scale, P.add);
+}
+
 // Fewer than four gradient elements, or an address that is not 16-byte aligned: the zeros that
 // whole vectors leave out.
 __global__ void zero_kernel(float *g, uint64_t n) {
@@ -784,9 +840,11 @@ int launch_grad(const void *d_ids, uint32_t id_bytes, uint64_t n, const T *dy, u
     uint64_t sms = 0;
     rc = sm_count(&sms);
     if (rc) return rc;
+    const bool vec = cols % 8 == 0 && aligned_to(dy, 16) && dy_stride * sizeof(T) % 16 == 0 && aligned_to(grad, 16);
+    const bool few = n <= kFewTokens;
     GradSortParams Q{};
     Q.ids = d_ids, Q.out = sorted, Q.n = n, Q.rows = rows, Q.status = status, Q.id_bytes = id_bytes;
-    Q.blocks = uint32_t((n + kBlock - 1) / kBlock);
+    Q.blocks = few ? 0 : uint32_t((n + kBlock - 1) / kBlock);
     for (Q.bits = 1; (rows >> Q.bits) != 0; ++Q.bits) {}
     uint32_t zero_blocks = 0;
     if (!add) {
@@ -800,10 +858,18 @@ int launch_grad(const void *d_ids, uint32_t id_bytes, uint64_t n, const T *dy, u
             if (rc) return rc;
         }
     }
-    if (Q.blocks + zero_blocks == 0) return K3HUF_OK;
-    grad_sort_kernel<<<Q.blocks + zero_blocks, kSortThreads, kSortSmem, stream>>>(Q);
-    rc = cuda_rc(cudaGetLastError());
-    const bool vec = cols % 8 == 0 && aligned_to(dy, 16) && dy_stride * sizeof(T) % 16 == 0 && aligned_to(grad, 16);
+    if (Q.blocks + zero_blocks) {
+        grad_sort_kernel<<<Q.blocks + zero_blocks, kSortThreads, kSortSmem, stream>>>(Q);
+        rc = cuda_rc(cudaGetLastError());
+    }
+    if (few && n && !rc) {
+        const GradFewParams F{d_ids, dy, grad, status, dy_stride, rows, cols, uint32_t(n), id_bytes, scale, add};
+        const dim3 grid(uint32_t(n), uint32_t((cols + 2047) / 2048));
+        if (grid.y > 65535) return K3HUF_E_ARG;
+        if (vec) grad_few_kernel<T, true><<<grid, kSumThreads, 0, stream>>>(F);
+        else grad_few_kernel<T, false><<<grid, kSumThreads, 0, stream>>>(F);
+        rc = cuda_rc(cudaGetLastError());
+    }
     for (uint32_t b = 0; b < Q.blocks && !rc; ++b) {
         const uint64_t size = std::min<uint64_t>(kBlock, n - uint64_t(b) * kBlock);
         GradSumParams P{};
@@ -894,7 +960,7 @@ extern "C" int k3huf_embed_layer(const void *h_layer_hdr, size_t hdr_bytes, cons
 }
 
 extern "C" int k3huf_embed_grad_scratch_bytes(uint64_t n_tokens, uint64_t rows, uint64_t cols, size_t *scratch_bytes) {
-    if (!scratch_bytes || rows == 0 || rows >= (1ull << 31) || cols == 0 || cols >= (1ull << 31) || n_tokens > 0x7FFFFFFFull) return K3HUF_E_ARG;
+    if (!scratch_bytes || rows == 0 || rows >= (1ull << 31) || cols == 0 || cols >= (1ull << 27) || n_tokens > 0x7FFFFFFFull) return K3HUF_E_ARG;
     *scratch_bytes = std::max<uint64_t>(1, (n_tokens + kBlock - 1) / kBlock) * sizeof(Sorted);
     return K3HUF_OK;
 }
