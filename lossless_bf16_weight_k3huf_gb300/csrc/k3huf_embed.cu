@@ -67,10 +67,8 @@ __device__ __forceinline__ void build_sync(uint32_t threads) { asm volatile("bar
 
 // The 12-bit table, entry (symbol << 4) | length; 0 where no code is.  By
 // threads 0 .. n - 1 (n a multiple of 32, at least 64); t < n is this one.
-// Eight entries per thread and step: a code of 9 bits or fewer that holds the
-// first of them holds all.  (Rolled loops here and in build_lut4: every
-// instruction runs once or a few times, and fresh ones cost instruction-cache
-// fills, which took most of an unrolled build's time.)
+// The builds take a few entries per thread: their dependent lookups are what
+// they cost, so each table is built from the one before in one step.
 __device__ void build_lut(const EmbedParams &P, Code &code, uint16_t *lut, uint32_t t, uint32_t n) {
     if (t <= K3HUF_MAXLEN) {
         code.lo[t] = P.lo[t];
@@ -79,50 +77,44 @@ __device__ void build_lut(const EmbedParams &P, Code &code, uint16_t *lut, uint3
     }
     if (t < 64) reinterpret_cast<uint32_t *>(code.sorted)[t] = reinterpret_cast<const uint32_t *>(P.sorted)[t];
     build_sync(n);
-    for (uint32_t m = t; m < K3HUF_TABLE_ENTRIES / 8; m += n) {
-        uint32_t v = 0;
-        bool whole = false;
-#pragma unroll 1
-        for (uint32_t e = 8 * m; e < 8 * m + 8 && !whole; ++e) {
-            uint32_t l = K3HUF_MAXLEN;
+#pragma unroll 2
+    for (uint32_t e = t; e < K3HUF_TABLE_ENTRIES; e += n) {
+        uint32_t l = K3HUF_MAXLEN;
 #pragma unroll
-            for (int k = 1; k < K3HUF_MAXLEN; ++k) l -= e >= P.lo[k];
-            v = e >= code.lo[l] && e < code.hi[l] ? (uint32_t(code.sorted[code.adj[l] + int(e >> (K3HUF_MAXLEN - l))]) << 4) | l : 0u;
-            lut[e] = uint16_t(v);
-            whole = e == 8 * m && v && l <= K3HUF_MAXLEN - 3;
-        }
-        v |= v << 16;
-        if (whole) reinterpret_cast<uint4 *>(lut)[m] = make_uint4(v, v, v, v);
+        for (int k = 1; k < K3HUF_MAXLEN; ++k) l -= e >= P.lo[k];
+        const uint32_t v = (uint32_t(code.sorted[(code.adj[l] + int(e >> (K3HUF_MAXLEN - l))) & 255]) << 4) | l;
+        lut[e] = uint16_t(e >= code.lo[l] && e < code.hi[l] ? v : 0u);
     }
     build_sync(n);
 }
 
-// The table of up to four codes, from the 12-bit table: .x their symbols, .y
-// their bits [4:0], eight times their number [15:8], and kBad where no code
-// starts (which counts as one symbol 0 of one bit).  Eight entries per thread
-// and step share the codes of their common 9 bits; each then takes up to two
-// more (a third would seldom fit, and an entry need not be full).
-constexpr uint32_t kBad = 1u << 31;
-__device__ __forceinline__ uint2 one_code(uint32_t v) { return v ? make_uint2(v >> 4, (v & 15u) | 0x800u) : make_uint2(0u, kBad | 0x801u); }
-// f with the code that starts after its bits of window e, if there is one within `room` bits and four are not there yet
-__device__ __forceinline__ uint2 one_more(uint2 f, uint32_t e, uint32_t room, const uint16_t *lut) {
-    const uint32_t bits = f.y & 31u, v = lut[(e << bits) & (K3HUF_TABLE_ENTRIES - 1)], l = v & 15u, at = f.y >> 8;
-    if (l && bits + l <= room && at < 32) {
-        f.x |= (v >> 4) << at;
-        f.y += l + 0x800u;
+// The table of up to two codes: symbols [7:0] and [15:8], the first code's bits
+// [19:16], all bits [24:20], bit 25 for two codes; 0 where no code is.
+constexpr uint32_t kTwo = 1u << 25;
+__device__ void build_lut2(const uint16_t *lut, uint32_t *lut2, uint32_t t, uint32_t n) {
+#pragma unroll 2
+    for (uint32_t e = t; e < K3HUF_TABLE_ENTRIES; e += n) {
+        const uint32_t a = lut[e], l = a & 15u, b = lut[(e << l) & (K3HUF_TABLE_ENTRIES - 1)], m = b & 15u;
+        const uint32_t one = (a >> 4) | (l << 16) | (l << 20);
+        lut2[e] = !l ? 0u : m && l + m <= K3HUF_MAXLEN ? (one + (m << 20)) | (b >> 4) << 8 | kTwo : one;
     }
-    return f;
+    build_sync(n);
 }
-__device__ void build_lut4(const uint16_t *lut, uint2 *lut4, uint32_t t, uint32_t n) {
-    for (uint32_t m = t; m < K3HUF_TABLE_ENTRIES / 8; m += n) {
-        uint2 shared = make_uint2(0u, 0u);
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) shared = one_more(shared, 8 * m, K3HUF_MAXLEN - 3, lut);
-#pragma unroll 1
-        for (uint32_t e = 8 * m; e < 8 * m + 8; ++e) {
-            const uint2 f = one_more(one_more(shared, e, K3HUF_MAXLEN, lut), e, K3HUF_MAXLEN, lut);
-            lut4[e] = f.y ? f : one_code(0);
+
+// The table of up to four codes, two by two: .x their symbols, .y their bits
+// [4:0], eight times their number [15:8], and kBad where no code starts (which
+// counts as one symbol 0 of one bit).
+constexpr uint32_t kBad = 1u << 31;
+__device__ void build_lut4(const uint32_t *lut2, uint2 *lut4, uint32_t t, uint32_t n) {
+#pragma unroll 2
+    for (uint32_t e = t; e < K3HUF_TABLE_ENTRIES; e += n) {
+        const uint32_t a = lut2[e], l = a >> 20 & 31u, b = lut2[(e << l) & (K3HUF_TABLE_ENTRIES - 1)], m1 = b >> 16 & 15u, m = b >> 20 & 31u;
+        uint2 f = make_uint2(a & 0xFFFFu, l | (a & kTwo ? 0x1000u : 0x800u));
+        if ((a & kTwo) && b) {
+            if (l + m <= K3HUF_MAXLEN) f = make_uint2(f.x | (b & 0xFFFFu) << 16, f.y + m + (b & kTwo ? 0x1000u : 0x800u));
+            else if (l + m1 <= K3HUF_MAXLEN) f = make_uint2(f.x | (b & 0xFFu) << 16, f.y + m1 + 0x800u);
         }
+        lut4[e] = a ? f : make_uint2(0u, kBad | 0x801u);
     }
 }
 
@@ -263,8 +255,11 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
     } else {
         const uint32_t n = few ? kEmbedThreads - 32 : kEmbedThreads, t = threadIdx.x - (kEmbedThreads - n);
         if (!few) q = fetch(item);
+        // (the table of two lies in the warps' slots, which are not in use yet)
+        uint32_t *lut2 = reinterpret_cast<uint32_t *>(smem + K3HUF_TABLE_ENTRIES * 10);
         build_lut(P, code, lut, t, n);
-        build_lut4(lut, lut4, t, n);
+        build_lut2(lut, lut2, t, n);
+        build_lut4(lut2, lut4, t, n);
     }
     __syncthreads();
     if (few && warp > 0) return;
@@ -274,20 +269,46 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
         const uint32_t want = q.any ? uint32_t(min(int64_t(q.len), int64_t(P.cols) - q.col)) : 0u;
         const uint32_t skip = q.col < 0 ? uint32_t(-q.col) : 0u;
         join[lane] = Join{q.none ? nullptr : q.even + q.a, static_cast<uint8_t *>(P.out) + (int64_t(q.token * P.out_stride) + q.col) * int64_t(sizeof(T)), skip, want};
-        // nothing to check in the join: whole units of rows that are there
-        const bool plain = __all_sync(0xffffffffu, q.any && !q.none && q.col >= 0 && want == (kFixed ? 256u : P.sub_syms));
+        // nothing to check in the join: whole units of rows that are there; and nothing to look up where
+        // they follow one another in one row (row_even, row_out: this lane's place in the first of four)
+        constexpr uint32_t kSub = 256;
+        const bool there = q.any && !q.none && q.col >= 0 && want == (kFixed ? kSub : P.sub_syms);
+        const bool plain = __all_sync(0xffffffffu, there);
+        const uint8_t *row_even = nullptr;
+        T *row_out = nullptr;
+        if (kFixed && kVec) {
+            const uint8_t *e = q.even + q.a;
+            T *o = static_cast<T *>(P.out) + q.token * P.out_stride + q.col;
+            const uint64_t e0 = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(e), 0), o0 = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(o), 0);
+            if (__all_sync(0xffffffffu, lane >= P.lanes || (there && reinterpret_cast<uint64_t>(e) == e0 + lane * kSub && reinterpret_cast<uint64_t>(o) == o0 + lane * kSub * sizeof(T)))) {
+                row_even = reinterpret_cast<const uint8_t *>(e0) + lane / 8 * kSub + lane % 8 * 8;
+                row_out = reinterpret_cast<T *>(o0) + lane / 8 * kSub + lane % 8 * 8;
+            }
+        }
         const uint32_t live = q.none ? 0u : want;
         // clamped, so that a corrupt index cannot move a read outside the stream
         const uint32_t off = min(q.off, q.huff_bits), end = min(max(q.end, off), q.huff_bits);
-        const uint32_t byte0 = (off >> 7) << 4;
-        // (a window may reach past the last piece, but no code that is taken does; no more than
-        // the longest codes would take, and one at least: the stream has 32 bytes past its end)
-        const uint32_t pieces = live ? min(max((end + 127) / 128 - byte0 / 16, 1u), (q.len * K3HUF_MAXLEN + 127) / 128 + 1) : 0u;
-        uint32_t before = pieces;             // pieces of the lanes up to this one
+        // its 16-byte pieces of the stream, [p0, p1) (a window may reach past the last one, but no code
+        // that is taken does; no more than the longest codes would take, and one at least: the
+        // stream has 32 bytes past its end)
+        const uint32_t p0 = off >> 7, p1 = min(max((end + 127) >> 7, p0 + 1), p0 + (q.len * K3HUF_MAXLEN + 127) / 128 + 1);
+        // a unit that goes on where the lane before ends shares that one's last piece
+        const uint32_t last_p1 = __shfl_up_sync(0xffffffffu, p1, 1), last_end = __shfl_up_sync(0xffffffffu, end, 1);
+        const uint64_t last_bits = __shfl_up_sync(0xffffffffu, live ? reinterpret_cast<uint64_t>(q.bits) : 0ull, 1);
+        bool on = live && lane > 0 && last_bits == reinterpret_cast<uint64_t>(q.bits) && last_end == off && last_p1 - p0 <= 1 && p1 >= last_p1;
+        uint32_t pieces = 0, before = 0;      // of this lane; of the lanes up to this one
+        auto count_pieces = [&]() {
+            before = pieces = live ? p1 - (on ? last_p1 : p0) : 0u;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, before, d);
-            if (lane >= uint32_t(d)) before += v;
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, before, d);
+                if (lane >= uint32_t(d)) before += v;
+            }
+        };
+        count_pieces();
+        if (__shfl_sync(0xffffffffu, before, 31) > kPieces) {  // several passes: every lane for itself
+            on = false;
+            count_pieces();
         }
         __syncwarp();
         const uint32_t longest = __reduce_max_sync(0xffffffffu, want);
@@ -297,13 +318,20 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
             const uint32_t last = over ? uint32_t(__ffs(over)) - 1 : 32u;
             const bool in = lane >= first && lane < last;
             const uint32_t mine = in ? live : 0u;
-            const uint32_t at = in ? before - done - pieces : 0u;
-            uint8_t *buf = slot + at * 16;
-            const uint32_t most = in ? pieces : 0u, copies = __reduce_max_sync(0xffffffffu, most);
-            for (uint32_t p = 0; p < copies; ++p)
-                if (p < most) cp_async16(buf + p * 16, q.bits + byte0 + p * 16);
+            const uint32_t at = before - done - pieces;            // where its own pieces start
+            // the pass's runs of pieces, each copied by the whole warp
+            for (uint32_t heads = __ballot_sync(0xffffffffu, in && live && !on); heads; ) {
+                const uint32_t h = __ffs(heads) - 1;
+                heads &= heads - 1;
+                const uint32_t from = __shfl_sync(0xffffffffu, at, h), to = heads ? __shfl_sync(0xffffffffu, at, (__ffs(heads) - 1) & 31) : __shfl_sync(0xffffffffu, before, last - 1) - done;
+                const uint8_t *src = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(q.bits) + uint64_t(p0) * 16, h));
+                for (uint32_t p = from + lane; p < to; p += 32) cp_async16(slot + p * 16, src + (p - from) * 16);
+            }
+            const uint8_t *buf = slot + (in && live ? at - (on ? last_p1 - p0 : 0u) : 0u) * 16;
+            const uint32_t most = in && live ? p1 - p0 : 0u;
             asm volatile("cp.async.commit_group;" ::: "memory");
             const bool whole = plain && first == 0 && last == 32;
+            if (first > 0 || last < 32) row_even = nullptr;
             // low bytes of a round's pieces: unit 4 i + lane / 8, values 8 (lane % 8) ..
             uint2 even[8];
             auto load_even = [&](uint32_t v0) {
@@ -311,17 +339,23 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
                 for (int i = 0; i < 8; ++i) {
                     if (4u * i >= P.lanes) break;
                     const uint32_t u = 4 * i + lane / 8, v = v0 + lane % 8 * 8;
+                    if (row_even) {
+                        even[i] = __ldg(reinterpret_cast<const uint2 *>(row_even + i * (4 * kSub) + v0));
+                        continue;
+                    }
                     const Join &J = join[u];
                     even[i] = whole || (u >= first && u < last && v < J.len && J.even) ? __ldg(reinterpret_cast<const uint2 *>(J.even + v)) : make_uint2(0, 0);
                 }
             };
             if (kVec) load_even(0);
             asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncwarp();                     // (copies by other lanes)
 
             const uint32_t *words = reinterpret_cast<const uint32_t *>(buf);
             const uint32_t max_word = most ? most * 4 - 1 : 0u;       // (a window's words past it hold no bit that is taken)
-            uint32_t cur = off - byte0 * 8;   // the next bit, from the buffer's first
+            uint32_t cur = off - p0 * 128;    // the next bit, from the buffer's first
             const uint32_t cur0 = cur;
+            uint32_t last_window = 0, last_entry = 0;
             // the 64 bits from `cur` on
             auto window = [&](uint32_t &hi, uint32_t &lo) {
                 const uint32_t i = cur / 32;
@@ -346,50 +380,49 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
             };
             for (uint32_t r = 0; r < longest; r += kRound) {
                 if (r < mine) {
+                    // Until 64 values, or the unit's last, are there.  n lookups give 4 n values at most,
+                    // so the first ones need no test for the end.  A window holds the bits of four
+                    // lookups (48 at most); an entry's low five bits are the shift, and its low byte
+                    // adds up.  The last lookup may give up to three values too many, the next round's
+                    // first or, past the unit, nobody's
                     uint32_t *to = my_row;
-                    if (r + kRound + 4 <= mine) {
-                        // 16 lookups give 64 values at most, so they need no test for the round's end.
-                        // A window holds the bits of four of them (48 at most); an entry's low five bits
-                        // are the shift, and its low byte adds up
-#pragma unroll 2
-                        for (int k = 0; k < kRound / 16; ++k) {
-                            uint32_t hi, lo, sum = 0;
-                            window(hi, lo);
+                    const uint32_t stop = min(uint32_t(kRound), mine - r);
+                    uint32_t hi = 0, lo = 0;
+                    auto look = [&]() {
+                        const uint2 e = lut4[hi >> 20];
+                        last_window = hi;
+                        last_entry = e.y;
+                        hi = __funnelshift_l(lo, hi, e.y);
+                        lo <<= e.y & 31u;
+                        take(e, to);
+                        return e.y;
+                    };
+                    for (uint32_t k = 0; k < stop / 16; ++k) {
+                        window(hi, lo);
+                        uint32_t sum = 0;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint2 e = lut4[hi >> 20];
-                                hi = __funnelshift_l(lo, hi, e.y);
-                                lo <<= e.y & 31u;
-                                sum += e.y;
-                                take(e, to);
-                            }
-                            cur += sum & 255u;
-                        }
-                        while (to < my_row + kRound / 4) {
-                            uint32_t hi, lo;
-                            window(hi, lo);
+                        for (int i = 0; i < 4; ++i) sum += look();
+                        cur += sum & 255u;
+                    }
+                    auto more = [&]() { return uint32_t(to - my_row) * 4 + fill / 8 < stop; };
+                    while (more()) {
+                        window(hi, lo);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if (to >= my_row + kRound / 4) break;
-                                const uint2 e = lut4[hi >> 20];
-                                hi = __funnelshift_l(lo, hi, e.y);
-                                lo <<= e.y & 31u;
-                                cur += e.y & 31u;
-                                take(e, to);
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            if (i && !more()) break;
+                            cur += look() & 31u;
                         }
-                    } else {
-                        // the last rounds: four codes a lookup while four are wanted, then one
-                        for (;;) {
-                            const uint32_t pos = r + uint32_t(to - my_row) * 4 + fill / 8;
-                            if (pos >= mine || to >= my_row + kRound / 4) break;
-                            uint32_t hi, lo;
-                            window(hi, lo);
-                            const uint2 e = pos + 4 <= mine ? lut4[hi >> 20] : one_code(lut[hi >> 20]);
-                            cur += e.y & 31u;
-                            take(e, to);
+                    }
+                    if (r + kRound >= mine) {
+                        if (to < my_row + kRowWords) *to = acc;            // a partial word
+                        // the bits of the values too many do not count
+                        uint32_t codes = (last_entry >> 11 & 31u) - (uint32_t(to - my_row) * 4 + fill / 8 - stop);
+                        cur -= last_entry & 31u;
+                        for (; codes; --codes) {
+                            const uint32_t l = max(lut[last_window >> 20] & 15u, 1u);
+                            last_window <<= l;
+                            cur += l;
                         }
-                        if (to < my_row + kRound / 4) *to = acc;          // a partial word
                     }
                 }
                 __syncwarp();
@@ -399,11 +432,19 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
                     for (int i = 0; i < 8; ++i) {
                         if (4u * i >= P.lanes) break;
                         const uint32_t u = 4 * i + lane / 8, s8 = lane % 8, v = r + s8 * 8;
+                        const uint32_t *h = row + u * kRowWords + 2 * s8;
+                        float f[8];
+                        if (row_even) {
+                            scaled8(h[0], h[1], even[i], P.scale, f);
+                            store8(row_out + i * (4 * kSub) + r, f);
+                            continue;
+                        }
                         const Join &J = join[u];
                         if (whole || (u >= first && u < last && v >= J.skip && v < J.len)) {
-                            const uint32_t *h = row + u * kRowWords + 2 * s8;
-                            float f[8] = {};
                             if (whole || J.even) scaled8(h[0], h[1], even[i], P.scale, f);
+                            else
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) f[k] = 0.f;
                             store8(reinterpret_cast<T *>(J.out) + v, f);
                         }
                     }
