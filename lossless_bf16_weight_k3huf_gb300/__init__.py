@@ -159,6 +159,8 @@ def _check(rc: int, what: str):
 
 
 def _host(a) -> np.ndarray:
+    if type(a) is np.ndarray and a.dtype == np.uint8 and a.ndim == 1 and a.flags.c_contiguous:
+        return a
     if isinstance(a, (bytes, bytearray, memoryview)):
         return np.frombuffer(a, dtype=np.uint8)
     if hasattr(a, "numpy") and not isinstance(a, np.ndarray):      # torch CPU tensor
@@ -475,7 +477,7 @@ def embed_layer(hdr, d_layer, tensor: int, cols: int, ids, out, d_status, scale:
     lb = _nbytes(d_layer) if layer_bytes is None else layer_bytes
     ip, ib, n = _ids(ids)
     op, oe, os_ = _matrix(out, n, cols, "out")
-    _check(_lib().k3huf_embed_layer(h.ctypes.data, h.size, _dptr(d_layer), lb, int(tensor), cols, ip, ib, n, scale,
+    _check(_lib().k3huf_embed_layer(h.__array_interface__["data"][0], h.size, _dptr(d_layer), lb, int(tensor), cols, ip, ib, n, scale,
                                     op, oe, os_, _dptr(d_status), _stream(stream)), "k3huf_embed_layer")
 
 

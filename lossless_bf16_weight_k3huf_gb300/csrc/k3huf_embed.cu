@@ -65,38 +65,49 @@ struct Code {
 // Barrier 1 of the threads that build tables.
 __device__ __forceinline__ void build_sync(uint32_t threads) { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
 
-// The 12-bit table, entry (symbol << 4) | length; 0 where no code is.  By
-// threads 0 .. n - 1 (n a multiple of 32, at least 64); t < n is this one.
-// The builds take a few entries per thread: their dependent lookups are what
-// they cost, so each table is built from the one before in one step.
-__device__ void build_lut(const EmbedParams &P, Code &code, uint16_t *lut, uint32_t t, uint32_t n) {
+// Place of entry e in the tables that a build reads.  Neighbouring entries
+// mostly start with the same code, of l bits say, so a warp looks entries up
+// that lie 2^l apart: straight tables would put up to 32 of them in one bank.
+__device__ __forceinline__ uint32_t spread(uint32_t e) { return e ^ (e >> 5 & 31u) ^ (e >> 10); }
+
+// The 12-bit table, entry (symbol << 4) | length; 0 where no code is; also
+// spread out, for the builds.  By threads 0 .. n - 1 (n a multiple of 32, at
+// least 64); t < n is this one.  The builds take a few entries per thread:
+// their dependent lookups are what they cost, so each table is built from the
+// one before in one step.
+__device__ void build_lut(const EmbedParams &P, Code &code, uint16_t *lut, uint32_t *lut1, uint32_t t, uint32_t n) {
     if (t <= K3HUF_MAXLEN) {
         code.lo[t] = P.lo[t];
         code.hi[t] = P.hi[t];
         code.adj[t] = P.adj[t];
     }
     if (t < 64) reinterpret_cast<uint32_t *>(code.sorted)[t] = reinterpret_cast<const uint32_t *>(P.sorted)[t];
+    uint32_t lo[K3HUF_MAXLEN];
+#pragma unroll
+    for (int k = 1; k < K3HUF_MAXLEN; ++k) lo[k] = P.lo[k];
     build_sync(n);
-#pragma unroll 2
+#pragma unroll 1
     for (uint32_t e = t; e < K3HUF_TABLE_ENTRIES; e += n) {
         uint32_t l = K3HUF_MAXLEN;
 #pragma unroll
-        for (int k = 1; k < K3HUF_MAXLEN; ++k) l -= e >= P.lo[k];
-        const uint32_t v = (uint32_t(code.sorted[(code.adj[l] + int(e >> (K3HUF_MAXLEN - l))) & 255]) << 4) | l;
-        lut[e] = uint16_t(e >= code.lo[l] && e < code.hi[l] ? v : 0u);
+        for (int k = 1; k < K3HUF_MAXLEN; ++k) l -= e >= lo[k];
+        const uint32_t s = (uint32_t(code.sorted[(code.adj[l] + int(e >> (K3HUF_MAXLEN - l))) & 255]) << 4) | l;
+        const uint32_t v = e >= code.lo[l] && e < code.hi[l] ? s : 0u;
+        lut[e] = uint16_t(v);
+        if (lut1) lut1[spread(e)] = v;
     }
     build_sync(n);
 }
 
-// The table of up to two codes: symbols [7:0] and [15:8], the first code's bits
-// [19:16], all bits [24:20], bit 25 for two codes; 0 where no code is.
+// The table of up to two codes, spread out: symbols [7:0] and [15:8], the first
+// code's bits [19:16], all bits [24:20], bit 25 for two codes; 0 where no code is.
 constexpr uint32_t kTwo = 1u << 25;
-__device__ void build_lut2(const uint16_t *lut, uint32_t *lut2, uint32_t t, uint32_t n) {
-#pragma unroll 2
+__device__ void build_lut2(const uint32_t *lut1, uint32_t *lut2, uint32_t t, uint32_t n) {
+#pragma unroll 1
     for (uint32_t e = t; e < K3HUF_TABLE_ENTRIES; e += n) {
-        const uint32_t a = lut[e], l = a & 15u, b = lut[(e << l) & (K3HUF_TABLE_ENTRIES - 1)], m = b & 15u;
+        const uint32_t a = lut1[spread(e)], l = a & 15u, b = lut1[spread((e << l) & (K3HUF_TABLE_ENTRIES - 1))], m = b & 15u;
         const uint32_t one = (a >> 4) | (l << 16) | (l << 20);
-        lut2[e] = !l ? 0u : m && l + m <= K3HUF_MAXLEN ? (one + (m << 20)) | (b >> 4) << 8 | kTwo : one;
+        lut2[spread(e)] = !l ? 0u : m && l + m <= K3HUF_MAXLEN ? (one + (m << 20)) | (b >> 4) << 8 | kTwo : one;
     }
     build_sync(n);
 }
@@ -106,9 +117,9 @@ __device__ void build_lut2(const uint16_t *lut, uint32_t *lut2, uint32_t t, uint
 // counts as one symbol 0 of one bit).
 constexpr uint32_t kBad = 1u << 31;
 __device__ void build_lut4(const uint32_t *lut2, uint2 *lut4, uint32_t t, uint32_t n) {
-#pragma unroll 2
+#pragma unroll 1
     for (uint32_t e = t; e < K3HUF_TABLE_ENTRIES; e += n) {
-        const uint32_t a = lut2[e], l = a >> 20 & 31u, b = lut2[(e << l) & (K3HUF_TABLE_ENTRIES - 1)], m1 = b >> 16 & 15u, m = b >> 20 & 31u;
+        const uint32_t a = lut2[spread(e)], l = a >> 20 & 31u, b = lut2[spread((e << l) & (K3HUF_TABLE_ENTRIES - 1))], m1 = b >> 16 & 15u, m = b >> 20 & 31u;
         uint2 f = make_uint2(a & 0xFFFFu, l | (a & kTwo ? 0x1000u : 0x800u));
         if ((a & kTwo) && b) {
             if (l + m <= K3HUF_MAXLEN) f = make_uint2(f.x | (b & 0xFFFFu) << 16, f.y + m + (b & kTwo ? 0x1000u : 0x800u));
@@ -255,10 +266,10 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
     } else {
         const uint32_t n = few ? kEmbedThreads - 32 : kEmbedThreads, t = threadIdx.x - (kEmbedThreads - n);
         if (!few) q = fetch(item);
-        // (the table of two lies in the warps' slots, which are not in use yet)
-        uint32_t *lut2 = reinterpret_cast<uint32_t *>(smem + K3HUF_TABLE_ENTRIES * 10);
-        build_lut(P, code, lut, t, n);
-        build_lut2(lut, lut2, t, n);
+        // (two more tables lie in the warps' slots, which are not in use yet)
+        uint32_t *lut1 = reinterpret_cast<uint32_t *>(smem + K3HUF_TABLE_ENTRIES * 10), *lut2 = lut1 + K3HUF_TABLE_ENTRIES;
+        build_lut(P, code, lut, lut1, t, n);
+        build_lut2(lut1, lut2, t, n);
         build_lut4(lut2, lut4, t, n);
     }
     __syncthreads();
@@ -486,7 +497,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) embed_long_kernel(const __grid_constant__ EmbedParams P) {
     __shared__ uint16_t lut[K3HUF_TABLE_ENTRIES];
     __shared__ Code code;
-    build_lut(P, code, lut, threadIdx.x, kThreads);
+    build_lut(P, code, lut, nullptr, threadIdx.x, kThreads);
     const uint64_t w = uint64_t(blockIdx.x) * kThreads + threadIdx.x;
     if (w >= P.n_tokens * P.units) return;
     const uint64_t t = w / P.units;
@@ -985,14 +996,16 @@ extern "C" int k3huf_embed_layer(const void *h_layer_hdr, size_t hdr_bytes, cons
     uint32_t code[256], first[K3HUF_MAXLEN + 1], count[K3HUF_MAXLEN + 1];
     const uint8_t *len = L.tables + 256ull * te.table;
     canonical_codes(len, code, first, count);
-    int off = 0;
+    int at[K3HUF_MAXLEN + 1], off = 0;
     for (int l = 1; l <= K3HUF_MAXLEN; ++l) {
         P.lo[l] = uint16_t(first[l] << (K3HUF_MAXLEN - l));
         P.hi[l] = uint16_t((first[l] + count[l]) << (K3HUF_MAXLEN - l));
         P.adj[l] = int16_t(off - int(first[l]));
-        for (int s = 0; s < 256; ++s)
-            if (len[s] == l) P.sorted[off++] = uint8_t(s);
+        at[l] = off;
+        off += int(count[l]);
     }
+    for (int s = 0; s < 256; ++s)
+        if (len[s]) P.sorted[at[len[s]]++] = uint8_t(s);
     for (uint32_t s = 0; s < te.n_stripes; ++s) P.stripe[s] = L.stripes[te.first_stripe + s].blob_offset;
     P.last_bytes = L.info.blob_bytes - P.stripe[te.n_stripes - 1];
     if (P.units > 0xFFFFFFFFull || n_tokens > (1ull << 62) / P.units) return K3HUF_E_ARG;
