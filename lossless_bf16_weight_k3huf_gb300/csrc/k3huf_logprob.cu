@@ -43,13 +43,12 @@ namespace cg = cooperative_groups;
 namespace k3huf {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kGradThreads = 256;
 constexpr int kVecs = 4;                      // 16-byte vectors per thread and step
 constexpr int kMaxCluster = 16;
-constexpr uint32_t kNotes = 1024;             // vectors noted in shared memory, and keys listed
-constexpr uint32_t kList = 3072;
-static_assert((K3HUF_MAX_TOP + 8) * kVecs <= int(kNotes) && K3HUF_MAX_TOP + (K3HUF_MAX_TOP + 8) * kVecs * 8 <= int(kList), "a counted step's notes and keys");
+constexpr uint32_t kList = 2432;              // keys listed in shared memory
+template <int kThreads> constexpr uint32_t kNotes = kVecs * kThreads;     // vectors noted: a step's
+static_assert(K3HUF_MAX_TOP + (K3HUF_MAX_TOP + 8) * kVecs * 8 <= int(kList), "a counted step's notes and keys");
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // (value, index) order of the top alternatives: larger values first, ties to
@@ -168,6 +167,7 @@ struct LogprobParams {
 
 // Cuts the list to its `top` largest keys, the smallest of them last, and
 // notes whether keys were lost because it was full.
+template <int kThreads>
 __device__ void cut_list(uint64_t *list, uint32_t *count, uint32_t *lost, uint32_t top) {
     constexpr int kMine = kList / kThreads;
     __shared__ uint32_t s_above[2];
@@ -223,12 +223,14 @@ __device__ void cut_list(uint64_t *list, uint32_t *count, uint32_t *lost, uint32
     __syncthreads();
 }
 
-template <typename T, bool kTop>
-__global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParams P) {
-    constexpr int E = kPer<T>;
+template <typename T, bool kTop, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(const LogprobParams P) {
+    constexpr int E = kPer<T>, kWarps = kThreads / 32;
+    constexpr uint32_t kMaxNotes = kNotes<kThreads>;
     __shared__ State s_part[kWarps], s_all[kMaxCluster];
-    __shared__ uint32_t s_count, s_noted, s_lost, s_counts[kMaxCluster], s_notes[kTop ? kNotes : 1], s_group[kTop ? 64 : 1];
-    __shared__ uint64_t s_list[kTop ? kList : 1], s_sent[kTop ? (kMaxCluster - 1) * K3HUF_MAX_TOP : 1];
+    __shared__ uint32_t s_count, s_noted, s_lost, s_counts[kMaxCluster], s_notes[kTop ? kMaxNotes : 1], s_group[kTop ? 64 : 1];
+    __shared__ uint64_t s_list[kTop ? kList : 1];
+    extern __shared__ uint64_t s_sent[];                   // (of the other CTAs of a cluster)
     const cg::cluster_group cluster = cg::this_cluster();
     const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank(), row = blockIdx.x / C;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -267,10 +269,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
         bool raised = false;
         uint64_t t = 0;
         if (first) {
-            // the top-th largest of the largest values of 64 groups of 4 threads
-            uint32_t of4 = max(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
-            of4 = max(of4, __shfl_xor_sync(0xffffffffu, of4, 2));
-            if (tid % 4 == 0) s_group[tid / 4] = of4;
+            // the top-th largest of the largest values of 64 groups of threads
+            constexpr int kGroup = kThreads / 64;
+            uint32_t most = mine;
+#pragma unroll
+            for (int d = 1; d < kGroup; d <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+            if (tid % kGroup == 0) s_group[tid / kGroup] = most;
             __syncthreads();
             const uint32_t a = s_group[lane], b = s_group[lane + 32];
             uint32_t hi = 0;
@@ -303,15 +307,15 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
             for (int i = 0; i < kVecs; ++i)
                 if (v0 + i * kThreads < vecs && order_of(top_of[i]) >= uint32_t(threshold >> 32)) {
                     const uint32_t at = atomicAdd(&s_noted, 1u);
-                    if (at < kNotes) s_notes[at] = v0 + i * kThreads;
+                    if (at < kMaxNotes) s_notes[at] = v0 + i * kThreads;
                 }
         }
     };
     // Lists the noted vectors' keys and raises the threshold to the top-th largest so far.
     auto raise = [&]() {
         __syncthreads();
-        const uint32_t noted = min(s_noted, kNotes);
-        if (tid == 0 && s_noted > kNotes) s_lost = 1;
+        const uint32_t noted = min(s_noted, kMaxNotes);
+        if (tid == 0 && s_noted > kMaxNotes) s_lost = 1;
         for (uint32_t i = tid; i < noted * E; i += kThreads) {
             const int64_t j = int64_t(s_notes[i / E]) * E + i % E - shift;
             if (j < 0 || j >= int64_t(P.vocab)) continue;
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
             const uint32_t at = atomicAdd(&s_count, 1u);
             if (at < kList) s_list[at] = key;
         }
-        cut_list(s_list, &s_count, &s_lost, P.top);
+        cut_list<kThreads>(s_list, &s_count, &s_lost, P.top);
         if (s_count >= P.top) threshold = max(threshold, s_list[P.top - 1]);
         if (tid == 0) s_noted = 0;
         __syncthreads();
@@ -420,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobParam
     }
     if constexpr (kTop) {
         if (count > 2 * kThreads) {
-            cut_list(s_list, &s_count, &s_lost, P.top);
+            cut_list<kThreads>(s_list, &s_count, &s_lost, P.top);
             count = s_count;
         }
         for (uint32_t i = tid; i < count; i += kThreads) {
@@ -450,7 +454,7 @@ constexpr int kGradVecs = 4;
 
 // kVec: logits and gradients sit alike in their 16-byte blocks
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads) logprob_grad_kernel(const GradParams P) {
+__global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const GradParams P) {
     constexpr int E = kVec ? kPer<T> : 1;
     const uint32_t row = blockIdx.y;
     const T *x = static_cast<const T *>(P.x) + uint64_t(row) * P.stride;
@@ -473,16 +477,16 @@ __global__ void __launch_bounds__(kThreads) logprob_grad_kernel(const GradParams
     };
     const uint32_t token = scored ? uint32_t(t) : 0xFFFFFFFFu;
     const uint32_t vecs = (P.vocab + shift + E - 1) / E;
-    const uint32_t v0 = blockIdx.x * (kThreads * kGradVecs) + threadIdx.x;
+    const uint32_t v0 = blockIdx.x * (kGradThreads * kGradVecs) + threadIdx.x;
     if constexpr (kVec) {
         uint4 v[kGradVecs];
 #pragma unroll
         for (int i = 0; i < kGradVecs; ++i)
-            if (v0 + i * kThreads < vecs) v[i] = load_vec(x, shift, P.vocab, v0 + i * kThreads);
+            if (v0 + i * kGradThreads < vecs) v[i] = load_vec(x, shift, P.vocab, v0 + i * kGradThreads);
 #pragma unroll
         for (int i = 0; i < kGradVecs; ++i) {
-            if (v0 + i * kThreads >= vecs) break;
-            const int64_t j = int64_t(v0 + i * kThreads) * E - shift;
+            if (v0 + i * kGradThreads >= vecs) break;
+            const int64_t j = int64_t(v0 + i * kGradThreads) * E - shift;
             float f[E];
             unpack<T>(v[i], f);
 #pragma unroll
@@ -515,7 +519,7 @@ __global__ void __launch_bounds__(kThreads) logprob_grad_kernel(const GradParams
     } else {
 #pragma unroll
         for (int i = 0; i < kGradVecs; ++i) {
-            const uint32_t j = v0 + i * kThreads;
+            const uint32_t j = v0 + i * kGradThreads;
             if (j >= vecs) break;
             const float d = grad(make_float2(ld_f32(x + j), 0.f)).x;
             st_f32(dx + j, j == token ? fmaf(P.scale, g, d) : d);
@@ -523,34 +527,45 @@ __global__ void __launch_bounds__(kThreads) logprob_grad_kernel(const GradParams
     }
 }
 
-template <typename T, bool kTop>
+template <typename T, bool kTop, int kThreads>
 int launch_forward(const LogprobParams &P, uint32_t n, cudaStream_t stream) {
     // one CTA per row, or a cluster per row while the GPU has room for more CTAs (two or
     // more per SM) and every CTA still has a step to do
     constexpr uint32_t kStep = kThreads * kVecs * kPer<T>;
     static std::atomic<uint64_t> wide{0};
-    const int rc = once_per_device(wide, [] { return cudaFuncSetAttribute(logprob_kernel<T, kTop>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
+    const int rc = once_per_device(wide, [] { return cudaFuncSetAttribute(logprob_kernel<T, kTop, kThreads>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
     if (rc) return rc;
     uint32_t C = 1;
-    while (C < uint32_t(kMaxCluster) && n * C < 304 && P.vocab / kStep >= 2 * C) C *= 2;
+    while (C < uint32_t(kMaxCluster) && n * C < 152u * 512 / kThreads && P.vocab / kStep >= 2 * C) C *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n * C);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
+    cfg.dynamicSmemBytes = kTop && C > 1 ? (kMaxCluster - 1) * K3HUF_MAX_TOP * sizeof(uint64_t) : 0;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = C;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cuda_rc(cudaLaunchKernelEx(&cfg, logprob_kernel<T, kTop>, P));
+    return cuda_rc(cudaLaunchKernelEx(&cfg, logprob_kernel<T, kTop, kThreads>, P));
+}
+
+// CTAs of 128 threads, twice as many rows at once, up to this vocabulary, of 256
+// above it.  4000 rows of bf16 logits with 20 alternatives, 128 and 256 threads:
+// 35 and 52 us at 4096, 115 and 117 at 32768, 177 both at 65536, 289 and 279 at
+// 131072; without alternatives 19 and 29, 54 and 60, 93 and 98, 177 and 175.
+constexpr uint32_t kSmallVocab = 65536;
+template <typename T, bool kTop>
+int launch_forward(const LogprobParams &P, uint32_t n, cudaStream_t stream) {
+    return P.vocab <= kSmallVocab ? launch_forward<T, kTop, 128>(P, n, stream) : launch_forward<T, kTop, 256>(P, n, stream);
 }
 
 template <typename T>
 int launch_backward(const GradParams &P, uint32_t n, cudaStream_t stream) {
     const bool vec = (reinterpret_cast<uintptr_t>(P.x) - reinterpret_cast<uintptr_t>(P.dx)) % 16 == 0 &&
                      (P.stride - P.dx_stride) * sizeof(T) % 16 == 0;
-    const uint32_t per = kThreads * kGradVecs * (vec ? kPer<T> : 1);
+    const uint32_t per = kGradThreads * kGradVecs * (vec ? kPer<T> : 1);
     // (a row that starts inside a 16-byte block may need one vector more)
     const uint32_t bx = uint32_t((uint64_t(P.vocab) + (vec ? kPer<T> - 1 : 0) + per - 1) / per);
     for (uint32_t r0 = 0; r0 < n; r0 += 65535) {
@@ -563,8 +578,8 @@ int launch_backward(const GradParams &P, uint32_t n, cudaStream_t stream) {
         if (Q.entropy) Q.entropy += r0;
         if (Q.g_entropy) Q.g_entropy += r0;
         const dim3 grid(bx, min(65535u, n - r0));
-        if (vec) logprob_grad_kernel<T, true><<<grid, kThreads, 0, stream>>>(Q);
-        else logprob_grad_kernel<T, false><<<grid, kThreads, 0, stream>>>(Q);
+        if (vec) logprob_grad_kernel<T, true><<<grid, kGradThreads, 0, stream>>>(Q);
+        else logprob_grad_kernel<T, false><<<grid, kGradThreads, 0, stream>>>(Q);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_rc(e);
     }
