@@ -624,17 +624,24 @@ struct OuterParams {
 // token by token, so both are read MN-major.  CTAs: a tile of columns (of
 // either gradient) x an adapter; the tokens' indexes come from the ids,
 // kWindow at a time, in order.  Bound by the read of V.
-constexpr uint32_t kWindow = 4096;
-constexpr uint32_t kOuterStages = 2;
-
-template <uint32_t kBlocks>                   // blocks of 64 rank rows
-constexpr uint32_t kOuterStage = kStep * 256 + kMaxParts * kBlocks * kStep * 128;
-template <uint32_t kBlocks>
-constexpr size_t kOuterSmem = kOuterStages * kOuterStage<kBlocks> + 1024;
+//
+// Ranks up to 32 (kBlocks 0) stage the parts side by side and multiply them at
+// once into columns of their own, which takes a third of the products and
+// leaves room for a third stage; above, a part is kBlocks blocks of 64 rank rows
+// and the parts add up in the same columns.
+constexpr uint32_t kWindow = 2048;
+template <uint32_t kBlocks> struct Outer {
+    static constexpr uint32_t stages = kBlocks == 0 ? 3 : 2, h_bytes = (kBlocks == 0 ? 2 : kMaxParts * kBlocks) * kStep * 128;
+    static constexpr uint32_t stage = kStep * 256 + h_bytes, half = kBlocks == 0 ? 128 : kBlocks * 64;      // (half: columns of TMEM)
+    static constexpr uint32_t run = kChain / (kBlocks == 0 ? kStep / 16 : kMaxParts * kStep / 16);
+    static constexpr uint32_t pieces = kBlocks == 0 ? 1 : 2 * kBlocks;      // of 16 columns per thread
+    static constexpr size_t smem = stages * stage + 1024;
+};
 
 template <uint32_t kBlocks>
 __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__ OuterParams P) {
-    constexpr uint32_t kStage = kOuterStage<kBlocks>;
+    using O = Outer<kBlocks>;
+    constexpr uint32_t kStage = O::stage, kOuterStages = O::stages;
     extern __shared__ uint8_t raw[];
     __shared__ uint32_t s_token[kWindow], s_count[kThreads / 32 + 1], s_tmem;
     __shared__ __align__(8) uint64_t s_bar[kOuterStages];
@@ -643,7 +650,7 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
     const bool second = blockIdx.x >= P.col_tiles0;
     const OuterJob &J = P.job[second];
     const uint32_t col = (blockIdx.x - (second ? P.col_tiles0 : 0)) * 128;
-    if (warp == 0) tmem_alloc(smem_addr(&s_tmem), kBlocks * 128);
+    if (warp == 0) tmem_alloc(smem_addr(&s_tmem), 2 * O::half);
     if (tid == 0)
         for (uint32_t i = 0; i < kOuterStages; ++i) mbar_init(smem_addr(&s_bar[i]), 1);
     if (tid == 0) fence_async_shared();
@@ -651,24 +658,26 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem, desc = mma_desc(128, rp, 1, 1);
+    const uint32_t tmem = s_tmem, desc = mma_desc(128, kBlocks == 0 ? kMaxParts * rp : rp, 1, 1);
     bool ok = true;
-    uint32_t step = 0;                        // steps of this CTA so far: stage step % 2, phase step / 2 % 2
+    uint32_t step = 0;                        // steps of this CTA so far: their stages and phases follow
     for (uint32_t a = blockIdx.y; a < P.n_adapters; a += gridDim.y) {
         const uint32_t first = step;
         // this thread's sums: column (lane) warp % 4 * 32 + lane, rank rows warp / 4 * 16 + 32 b on
-        constexpr uint32_t kRun = kChain / (kMaxParts * kStep / 16);
-        float sum[2 * kBlocks][16] = {};
+        constexpr uint32_t kRun = O::run;
+        float sum[O::pieces][16] = {};
         auto drain = [&](uint32_t run) {
             tc_fence_after();
 #pragma unroll
-            for (uint32_t b = 0; b < 2 * kBlocks; ++b)
-                if (warp / 4 * 16 + b * 32 < rp) {
-                    float v[16];
-                    tmem_load16(tmem + ((warp % 4) << 21) + (run & 1) * (kBlocks * 64) + warp / 4 * 16 + b * 32, v);
+            for (uint32_t b = 0; b < O::pieces; ++b)
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) sum[b][k] += v[k];
-                }
+                for (uint32_t q = 0; q < (kBlocks == 0 ? kMaxParts : 1); ++q)
+                    if (warp / 4 * 16 + b * 32 < rp) {
+                        float v[16];
+                        tmem_load16(tmem + ((warp % 4) << 21) + (run & 1) * O::half + q * rp + warp / 4 * 16 + b * 32, v);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) sum[b][k] += v[k];
+                    }
             tc_fence_before();
         };
         for (uint64_t w0 = 0; w0 < P.n; w0 += kWindow) {
@@ -714,30 +723,35 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
                     if (h_in) {
                         const __nv_bfloat16 *src = J.h + t * P.pitch + c * 8;
 #pragma unroll
-                        for (uint32_t q = 0; q < kMaxParts; ++q) cp_async16z(to + kStep * 256 + q * (kBlocks * kStep * 128) + at, src + q * P.n * P.pitch, in ? 16 : 0);
+                        for (uint32_t q = 0; q < kMaxParts; ++q) {
+                            const uint32_t hc = kBlocks == 0 ? q * (rp / 8) + c : c;
+                            cp_async16z(to + kStep * 256 + q * (kBlocks * kStep * 128) + hc / 8 * (kStep * 128) + tile_at(r, hc % 8), src + q * P.n * P.pitch, in ? 16 : 0);
+                        }
                     }
                 }
             };
-            if (steps) load(0);
-            cp_async_commit();
+            for (uint32_t s = 0; s < kOuterStages - 1; ++s) {
+                if (s < steps) load(s);
+                cp_async_commit();
+            }
             for (uint32_t s = 0; s < steps; ++s) {
                 const uint32_t g = step + s;
-                // the other stage is free once the step before is done
+                // the stage before this one is free once its products are done
                 if (s > 0 && ok) ok = mbar_wait(smem_addr(&s_bar[(g - 1) % kOuterStages]), (g - 1) / kOuterStages & 1);
-                if (s + 1 < steps && ok) load(s + 1);
+                if (s + kOuterStages - 1 < steps && ok) load(s + kOuterStages - 1);
                 cp_async_commit();
-                cp_async_wait<1>();
+                cp_async_wait<kOuterStages - 1>();
                 fence_async_shared();
                 __syncthreads();
                 if (tid == 0 && ok) {
                     tc_fence_after();
-                    const uint32_t at = base + g % kOuterStages * kStage;
+                    const uint32_t at = base + g % kOuterStages * kStage, d = tmem + ((g - first) / kRun & 1) * O::half;
                     const uint64_t va = tile_desc(at, kStep * 128, 1024);
 #pragma unroll
-                    for (uint32_t q = 0; q < kMaxParts; ++q) {
+                    for (uint32_t q = 0; q < (kBlocks == 0 ? 1 : kMaxParts); ++q) {
                         const uint64_t hb = tile_desc(at + kStep * 256 + q * kBlocks * (kStep * 128), kStep * 128, 1024);
 #pragma unroll
-                        for (uint32_t k = 0; k < kStep / 16; ++k) mma(tmem + ((g - first) / kRun & 1) * (kBlocks * 64), va + k * 128, hb + k * 128, desc, (g - first) % kRun || q || k);
+                        for (uint32_t k = 0; k < kStep / 16; ++k) mma(d, va + k * 128, hb + k * 128, desc, (g - first) % kRun || q || k);
                     }
                     mma_commit(smem_addr(&s_bar[g % kOuterStages]));
                 }
@@ -753,7 +767,7 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
         const uint32_t c = col + warp % 4 * 32 + lane;
         if (c < J.len)
 #pragma unroll
-            for (uint32_t b = 0; b < 2 * kBlocks; ++b)
+            for (uint32_t b = 0; b < O::pieces; ++b)
 #pragma unroll
                 for (uint32_t k = 0; k < 16; ++k) {
                     const uint32_t j = warp / 4 * 16 + b * 32 + k;
@@ -766,7 +780,7 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
         tc_fence_after();
     }
     if (!ok) atomicOr(P.status, K3HUF_ST_TIMEOUT);
-    if (warp == 0) tmem_free(tmem, kBlocks * 128);
+    if (warp == 0) tmem_free(tmem, 2 * O::half);
 }
 
 // --- host -----------------------------------------------------------------------
@@ -875,13 +889,15 @@ int launch_expand(ExpandParams &P, const void *h, const void *w, const void *bas
 int launch_outer(const OuterParams &P, uint32_t col_tiles, cudaStream_t stream) {
     static std::atomic<uint64_t> once{0};
     const int rc = once_per_device(once, [] {
-        const cudaError_t e = cudaFuncSetAttribute(outer_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kOuterSmem<1>));
-        return e != cudaSuccess ? e : cudaFuncSetAttribute(outer_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kOuterSmem<2>));
+        cudaError_t e = cudaFuncSetAttribute(outer_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Outer<0>::smem));
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(outer_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Outer<1>::smem));
+        return e != cudaSuccess ? e : cudaFuncSetAttribute(outer_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Outer<2>::smem));
     });
     if (rc) return rc;
     const dim3 grid(col_tiles, std::min(P.n_adapters, 65535u));
-    return P.rank_pad <= kStep ? launch_after(outer_kernel<1>, grid, kThreads, kOuterSmem<1>, stream, P)
-                               : launch_after(outer_kernel<2>, grid, kThreads, kOuterSmem<2>, stream, P);
+    if (P.rank_pad <= 32) return launch_after(outer_kernel<0>, grid, kThreads, Outer<0>::smem, stream, P);
+    return P.rank_pad <= kStep ? launch_after(outer_kernel<1>, grid, kThreads, Outer<1>::smem, stream, P)
+                               : launch_after(outer_kernel<2>, grid, kThreads, Outer<2>::smem, stream, P);
 }
 
 }  // namespace
