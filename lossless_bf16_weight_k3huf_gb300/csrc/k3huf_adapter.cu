@@ -202,19 +202,19 @@ constexpr uint32_t kChain = 32;
 
 // The adapters of a tile's tokens, each once, in the order of their first
 // token: of[t] the place of token t's adapter (-1: none), list the adapters.
-// All threads of the CTA (at least 128) for `size` tokens; returns their number.
+// All threads of the CTA (at least 128); returns their number.
 struct TileAdapters {
     int32_t id[kTile], list[kTile];
     int16_t of[kTile];
     uint32_t count[4];
 };
-__device__ uint32_t tile_adapters(TileAdapters &s, const int32_t *ids, uint64_t t0, uint64_t n, uint32_t size, uint32_t n_adapters, uint32_t *status) {
+__device__ uint32_t tile_adapters(TileAdapters &s, const int32_t *ids, uint64_t t0, uint64_t n, uint32_t n_adapters, uint32_t *status) {
     const uint32_t t = threadIdx.x, lane = t % 32, warp = t / 32;
     int32_t id = -1;
     bool first = false;
     uint32_t below = 0;
     if (t < kTile) {
-        if (t < size && t0 + t < n) id = ids[t0 + t];
+        if (t0 + t < n) id = ids[t0 + t];
         if (id >= 0 && uint32_t(id) >= n_adapters) {
             if (status) atomicOr(status, K3HUF_ST_TOKEN);
             id = -1;
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
     const uint32_t split = blockIdx.x % P.splits, rp = P.rank_pad;
     const uint64_t t0 = uint64_t(blockIdx.x / P.splits) * kTile;
     grid_dep_launch();
-    const uint32_t per = kTile / rp, count = tile_adapters(tile, P.ids, t0, P.n, kTile, P.n_adapters, split + blockIdx.y + blockIdx.z == 0 ? P.status : nullptr);
+    const uint32_t per = kTile / rp, count = tile_adapters(tile, P.ids, t0, P.n, P.n_adapters, split + blockIdx.y + blockIdx.z == 0 ? P.status : nullptr);
     const uint32_t a0 = blockIdx.y * per, na = a0 < count ? min(per, count - a0) : 0u;
     if (na == 0) return;                      // (the whole cluster)
     const uint32_t cols = na * rp;            // <= 128, a multiple of 16
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
 }
 
 struct ExpandParams {
-    CUtensorMap h, w, base, y;                // parts x tokens rows of 64-value blocks; rank rows x len, boxes of 64 x rank; boxes of 128 x tokens
+    CUtensorMap h, w, base, y;                // parts x tokens rows of 64-value blocks; rank rows x len, boxes of 64 x rank; boxes of 128 bytes x 128 tokens
     const int32_t *ids;
     uint32_t *status;
     uint64_t n;
@@ -426,34 +426,49 @@ struct ExpandParams {
     bool has_base;
 };
 
-// The expand.  D[128 columns, tokens] = W_a^T H^T for one adapter a of the tile
-// after another, each added only where a token has that adapter: no token meets
-// another adapter's values, not even as zero times infinity.  W is read
-// MN-major as it lies in memory, H (the same for all of them) K-major, in
-// parts.  With columns as the operand's rows a warp holds 32 neighbouring
-// columns of a token, so the additions to the base run along rows in shared
-// memory, whose tiles TMA brings and takes away.  CTAs: a tile of tokens x a
-// range of column tiles; a step is one adapter of one column tile.  Warps 0 to 7
-// add; a thread of warp 8 brings W and issues the products, two steps ahead
-// of the additions; one of warp 9 brings the base and takes y away.
-// Bound by the read of the base and the write of y.
+// The expand.  D[128 tokens, columns] = H W_a for one adapter a of the tile after
+// another, each added only where a token has that adapter: no token meets
+// another adapter's values, not even as zero times infinity.  H (the same for
+// all of them) is read K-major, in parts, W MN-major as it lies in memory.  A
+// thread holds a token's neighbouring columns, so it adds 16 bytes of the base
+// at a time, in tiles of 128-byte rows that TMA brings and takes away swizzled.
+// CTAs: a tile of tokens x a range of column tiles; a step is one adapter of
+// one column tile.  Warps 0 to 7 add; a thread of warp 8 brings W and issues
+// the products, two steps ahead of the additions; one of warp 9 brings the base
+// and takes y away.  Bound by the read of the base and the write of y.  (With
+// columns as the lanes, 2 bytes at a time, the additions took five times the
+// instructions: 184 us instead of 138 for 8192 x 24576 bf16.)
 constexpr uint32_t kExpandThreads = kThreads + 64;
 template <typename T, uint32_t kBlocks> struct Expand {       // kBlocks: blocks of 64 rank rows
-    static constexpr uint32_t tokens = sizeof(T) == 4 ? 64 : 128;         // (a tile of the base takes 32 KB)
-    static constexpr uint32_t parts = sizeof(T) == 4 ? 3 : 2, part_bytes = tokens * 128;
-    static constexpr uint32_t h_bytes = parts * kBlocks * part_bytes, w_bytes = kBlocks * kTileBytes, w_stages = kBlocks == 1 ? 3 : 2;
-    static constexpr uint32_t io_bytes = tokens * 128 * sizeof(T), io_stages = kBlocks == 1 ? 3 : 2;
+    static constexpr uint32_t row = 128 / sizeof(T), cols = 2 * row;      // columns of a 128-byte row; of a tile of two of them
+    static constexpr uint32_t parts = sizeof(T) == 4 ? 3 : 2;
+    static constexpr uint32_t h_bytes = parts * kBlocks * kTileBytes, w_block = kBlocks * kStep * 128, w_bytes = cols / 64 * w_block, w_stages = kBlocks == 1 ? 3 : 2;
+    static constexpr uint32_t io_bytes = 2 * kTileBytes, io_stages = kBlocks == 1 ? 3 : 2;
     static constexpr size_t smem = h_bytes + w_stages * w_bytes + io_stages * io_bytes + 1024;
     static_assert(smem <= 220 * 1024, "shared memory of one CTA");
 };
 
+__device__ __forceinline__ void add_chunk(uint4 &v, const uint32_t *r, __nv_bfloat16) {
+    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __fadd2_rn(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])));
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+__device__ __forceinline__ void add_chunk(uint4 &v, const uint32_t *r, float) {
+    uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) + __uint_as_float(r[i]));
+}
+
 template <typename T, uint32_t kBlocks>
 __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_constant__ ExpandParams P) {
     using E = Expand<T, kBlocks>;
-    constexpr uint32_t NT = E::tokens, WS = E::w_stages, IS = E::io_stages;
+    constexpr uint32_t WS = E::w_stages, IS = E::io_stages;
     extern __shared__ uint8_t raw[];
     __shared__ TileAdapters tile;
-    __shared__ uint32_t s_mask[NT][NT / 32];  // tokens of each adapter of the tile
     __shared__ __align__(8) uint64_t s_h, s_w[WS], s_wfree[WS], s_d[2], s_dfree[2], s_io[IS], s_iodone[IS];
     __shared__ uint32_t s_tmem;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -461,8 +476,8 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
     const uint32_t h_at = smem_addr(smem), w_at = h_at + E::h_bytes, io_at = w_at + WS * E::w_bytes;
     uint8_t *io = smem + E::h_bytes + WS * E::w_bytes;
     const uint32_t rp = P.rank_pad;
-    const uint64_t t0 = uint64_t(blockIdx.x / P.groups) * NT;
-    const uint32_t group = blockIdx.x % P.groups, col_tiles = (P.len + 127) / 128;
+    const uint64_t t0 = uint64_t(blockIdx.x / P.groups) * kTile;
+    const uint32_t group = blockIdx.x % P.groups, col_tiles = (P.len + E::cols - 1) / E::cols;
     const uint32_t c0 = uint32_t(uint64_t(col_tiles) * group / P.groups), tiles = uint32_t(uint64_t(col_tiles) * (group + 1) / P.groups) - c0;
     if (warp == 0) tmem_alloc(smem_addr(&s_tmem), 256);
     if (tid == 0) {
@@ -481,38 +496,31 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
         }
     }
     // the rank's padding in the stages of W, which no copy writes
-    for (uint32_t i = tid; i < WS * 2 * (rp - P.rank) * 8; i += kExpandThreads) {
-        const uint32_t c = i % 8, j = P.rank + i / 8 % (rp - P.rank), half = i / 8 / (rp - P.rank);
-        *reinterpret_cast<uint4 *>(smem + E::h_bytes + half / 2 * E::w_bytes + half % 2 * (kBlocks * kStep * 128) + j * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+    for (uint32_t i = tid; i < WS * (E::cols / 64) * (rp - P.rank) * 8; i += kExpandThreads) {
+        const uint32_t c = i % 8, j = P.rank + i / 8 % (rp - P.rank), block = i / 8 / (rp - P.rank);
+        *reinterpret_cast<uint4 *>(smem + E::h_bytes + block * E::w_block + j * 128 + c * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_async_shared();
     grid_dep_wait();
-    const uint32_t count = tile_adapters(tile, P.ids, t0, P.n, NT, P.n_adapters, nullptr);
-    if (warp < NT / 32) {
-        const int32_t of = tile.of[warp * 32 + lane];
-        for (uint32_t a = 0; a < count; ++a) {
-            const uint32_t m = __ballot_sync(0xffffffffu, of == int32_t(a));
-            if (lane == 0) s_mask[a][warp] = m;
-        }
-    }
+    const uint32_t count = tile_adapters(tile, P.ids, t0, P.n, P.n_adapters, nullptr);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem, steps = tiles * count;
     bool ok = true;
-    if (warp == 8) {
+    if (warp == kThreads / 32) {
         if (lane == 0 && steps) {
             mbar_expect(smem_addr(&s_h), E::h_bytes);
             for (uint32_t q = 0; q < E::parts; ++q)
-                for (uint32_t b = 0; b < kBlocks; ++b) tma_load(h_at + (q * kBlocks + b) * E::part_bytes, &P.h, int32_t(b * 64), int32_t(q * P.n + t0), smem_addr(&s_h));
-            // W of step s: two blocks of 64 columns, each the adapter's rank rows
+                for (uint32_t b = 0; b < kBlocks; ++b) tma_load(h_at + (q * kBlocks + b) * kTileBytes, &P.h, int32_t(b * 64), int32_t(q * P.n + t0), smem_addr(&s_h));
+            // W of step s: blocks of 64 columns, each the adapter's rank rows
             auto load = [&](uint32_t s) {
                 const uint32_t bar = smem_addr(&s_w[s % WS]), at = w_at + s % WS * E::w_bytes;
-                mbar_expect(bar, 2 * P.rank * 128);
-                for (uint32_t half = 0; half < 2; ++half)
-                    tma_load(at + half * (kBlocks * kStep * 128), &P.w, int32_t((c0 + s / count) * 128 + half * 64), tile.list[s % count] * int32_t(P.rank), bar);
+                mbar_expect(bar, E::cols / 64 * P.rank * 128);
+                for (uint32_t b = 0; b < E::cols / 64; ++b)
+                    tma_load(at + b * E::w_block, &P.w, int32_t((c0 + s / count) * E::cols + b * 64), tile.list[s % count] * int32_t(P.rank), bar);
             };
-            const uint32_t desc = mma_desc(128, NT, 1, 0);
+            const uint32_t desc = mma_desc(kTile, E::cols, 0, 1);
             uint32_t loaded = 0;
             for (; loaded < min(WS, steps); ++loaded) load(loaded);
             ok = mbar_wait(smem_addr(&s_h), 0);
@@ -521,10 +529,10 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
                 if (s >= 2 && ok) ok = mbar_wait(smem_addr(&s_dfree[s & 1]), (s / 2 - 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t w = tile_desc(w_at + s % WS * E::w_bytes, kBlocks * kStep * 128, 1024);
+                const uint64_t w = tile_desc(w_at + s % WS * E::w_bytes, E::w_block, 1024);
                 for (uint32_t q = 0; q < E::parts; ++q)
                     for (uint32_t k = 0; k < rp / 16; ++k)
-                        mma(tmem + (s & 1) * 128, w + k * 128, tile_desc(h_at + (q * kBlocks + k / 4) * E::part_bytes, 16, 1024) + 2 * (k % 4), desc, q || k);
+                        mma(tmem + (s & 1) * 128, tile_desc(h_at + (q * kBlocks + k / 4) * kTileBytes, 16, 1024) + 2 * (k % 4), w + k * 128, desc, q || k);
                 mma_commit(smem_addr(&s_wfree[s % WS]));
                 mma_commit(smem_addr(&s_d[s & 1]));
                 // (a stage is free once the products before these are done)
@@ -536,18 +544,20 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
             if (!ok)                          // copies still in flight land first
                 for (uint32_t s = loaded > WS ? loaded - WS : 0; s < loaded; ++s) mbar_wait(smem_addr(&s_w[s % WS]), s / WS & 1);
         }
-    } else if (warp == 9) {
+    } else if (warp == kThreads / 32 + 1) {
         if (lane == 0) {
             auto load = [&](uint32_t i) {
                 const uint32_t bar = smem_addr(&s_io[i % IS]);
                 mbar_expect(bar, P.has_base ? E::io_bytes : 0);
-                if (P.has_base) tma_load(io_at + i % IS * E::io_bytes, &P.base, int32_t((c0 + i) * 128), int32_t(t0), bar);
+                if (P.has_base)
+                    for (uint32_t b = 0; b < 2; ++b) tma_load(io_at + i % IS * E::io_bytes + b * kTileBytes, &P.base, int32_t((c0 + i) * E::cols + b * E::row), int32_t(t0), bar);
             };
             for (uint32_t i = 0; i < min(IS, tiles); ++i) load(i);
             for (uint32_t i = 0; i < tiles && ok; ++i) {
                 ok = mbar_wait(smem_addr(&s_iodone[i % IS]), i / IS & 1);
                 if (!ok) break;
-                tma_store(&P.y, int32_t((c0 + i) * 128), int32_t(t0), io_at + i % IS * E::io_bytes);
+                for (uint32_t b = 0; b < 2; ++b)
+                    if ((c0 + i) * E::cols + b * E::row < P.len) tma_store(&P.y, int32_t((c0 + i) * E::cols + b * E::row), int32_t(t0), io_at + i % IS * E::io_bytes + b * kTileBytes);
                 bulk_commit();
                 if (i + IS < tiles) {
                     bulk_wait_read<0>();
@@ -557,35 +567,37 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
             bulk_wait_all();
         }
     } else {
+        // this thread: token warp % 4 * 32 + lane, the tile's columns of row block warp / 4
+        const uint32_t t = warp % 4 * 32 + lane;
+        const int32_t mine = tile.of[t];
+        constexpr uint32_t kPer = 16 / sizeof(T);              // columns of a 16-byte chunk
         for (uint32_t i = 0; i < tiles; ++i) {
             if (ok) ok = mbar_wait(smem_addr(&s_io[i % IS]), i / IS & 1);
-            T *mine = reinterpret_cast<T *>(io + i % IS * E::io_bytes) + warp % 4 * 32 + lane;
-            if (!P.has_base)
-                for (uint32_t t = warp / 4 * (NT / 2); t < (warp / 4 + 1) * (NT / 2); ++t)
-                    if (tile.of[t] < 0) st_f32(mine + t * 128, 0.f);
+            uint8_t *rows = io + i % IS * E::io_bytes + warp / 4 * kTileBytes;
+            if (!P.has_base && mine < 0)
+#pragma unroll
+                for (uint32_t c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(rows + tile_at(t, c)) = make_uint4(0, 0, 0, 0);
             for (uint32_t a = 0; a < count; ++a) {
                 const uint32_t s = i * count + a;
                 if (ok) ok = mbar_wait(smem_addr(&s_d[s & 1]), s / 2 & 1);
                 tc_fence_after();
+                if (__any_sync(0xffffffffu, mine == int32_t(a))) {
 #pragma unroll
-                for (uint32_t g = 0; g < NT / 64; ++g) {
-                    const uint32_t t = warp / 4 * (NT / 2) + g * 32, mask = s_mask[a][t / 32];
-                    if (mask == 0) continue;
-                    // (the base's values are fetched while the product comes from TMEM)
-                    uint32_t r[32];
-                    float b[32];
-                    tmem_load32(tmem + ((warp % 4) << 21) + (s & 1) * 128 + t, r);
-                    T *q = mine + t * 128;
+                    for (uint32_t piece = 0; piece < E::row / 32; ++piece) {
+                        // (the base's chunks are fetched while the product comes from TMEM)
+                        uint32_t r[32];
+                        tmem_load32(tmem + ((warp % 4) << 21) + (s & 1) * 128 + warp / 4 * E::row + piece * 32, r);
+                        uint4 b[32 / kPer];
 #pragma unroll
-                    for (uint32_t k = 0; k < 32; ++k) b[k] = P.has_base ? ld_f32(q + k * 128) : 0.f;
-                    tmem_wait32(r);
-                    if (mask == 0xffffffffu) {
+                        for (uint32_t c = 0; c < 32 / kPer; ++c)
+                            b[c] = P.has_base ? *reinterpret_cast<const uint4 *>(rows + tile_at(t, piece * (32 / kPer) + c)) : make_uint4(0, 0, 0, 0);
+                        tmem_wait32(r);
+                        if (mine == int32_t(a))
 #pragma unroll
-                        for (uint32_t k = 0; k < 32; ++k) st_f32(q + k * 128, b[k] + __uint_as_float(r[k]));
-                    } else {
-#pragma unroll
-                        for (uint32_t k = 0; k < 32; ++k)
-                            if (mask >> k & 1) st_f32(q + k * 128, b[k] + __uint_as_float(r[k]));
+                            for (uint32_t c = 0; c < 32 / kPer; ++c) {
+                                add_chunk(b[c], r + c * kPer, T());
+                                *reinterpret_cast<uint4 *>(rows + tile_at(t, piece * (32 / kPer) + c)) = b[c];
+                            }
                     }
                 }
                 tc_fence_before();
@@ -859,13 +871,13 @@ int launch_expand(ExpandParams &P, const void *h, const void *w, const void *bas
     int rc = once_per_device(once, [] { return cudaFuncSetAttribute(expand_kernel<T, kBlocks>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(E::smem)); });
     if (rc) return rc;
     constexpr uint32_t type = sizeof(T) == 4 ? K3HUF_F32 : K3HUF_BF16;
-    rc = tensor_map(&P.h, h, K3HUF_BF16, E::parts * P.n, kBlocks * 64, kBlocks * 64, E::tokens, 64, true);
+    rc = tensor_map(&P.h, h, K3HUF_BF16, E::parts * P.n, kBlocks * 64, kBlocks * 64, kTile, 64, true);
     if (!rc) rc = tensor_map(&P.w, w, K3HUF_BF16, uint64_t(P.n_adapters) * P.rank, P.len, P.len, P.rank, 64, true);
-    if (!rc) rc = tensor_map(&P.y, y, type, P.n, P.len, y_stride, E::tokens, 128, false);
-    if (!rc) rc = base ? tensor_map(&P.base, base, type, P.n, P.len, base_stride, E::tokens, 128, false) : K3HUF_OK;
+    if (!rc) rc = tensor_map(&P.y, y, type, P.n, P.len, y_stride, kTile, E::row, true);
+    if (!rc) rc = base ? tensor_map(&P.base, base, type, P.n, P.len, base_stride, kTile, E::row, true) : K3HUF_OK;
     if (rc) return rc;
     P.has_base = base != nullptr;
-    const uint64_t tiles = (P.n + E::tokens - 1) / E::tokens, cols = (P.len + 127) / 128;
+    const uint64_t tiles = (P.n + kTile - 1) / kTile, cols = (P.len + E::cols - 1) / E::cols;
     // column ranges per token tile: the count whose last wave of CTAs (one per SM) is fullest,
     // among those that give an SM up to three waves
     uint64_t best = 1;
