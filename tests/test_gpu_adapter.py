@@ -236,6 +236,32 @@ def test_gradients_against_differences():
         assert abs(float((got.double() * step[k]).sum()) - slope) <= room + 1e-8 * abs(slope)
 
 
+@pytest.mark.parametrize("n,r", [(12, 16), (300, 16), (300, 96), (300, 5)])
+def test_no_token_meets_another_adapters_values(n, r):
+    """Infinities and NaN in one adapter, and in the inputs of the tokens that use it, stay with those tokens: the
+    others' results are the very ones that finite values there give."""
+    S, cols, rows = 5, 264, 328
+    good = make(n, S, r, cols, rows, 40 + r)
+    bad = {k: v.clone() for k, v in good.items()}
+    bad["a"][2, :, 7] = float("inf")
+    bad["b"][2, r - 1] = float("nan")
+    hit = good["ids"] == 2
+    bad["x"][hit] = float("nan")
+    bad["dy"][hit] = float("-inf")
+    none = good["ids"] < 0
+    bad["x"][none], bad["dy"][none] = float("nan"), float("inf")
+    for dtype in (torch.float32, torch.bfloat16):
+        base = torch.randn(n, rows, device="cuda").to(dtype)
+        y, z = torch.empty_like(base), torch.empty_like(base)
+        assert apply(good, y, base) == 0 and apply(bad, z, base) == 0
+        assert torch.equal(y[~hit], z[~hit]) and torch.equal(z[none], base[none])
+        want, got = grads(good, dtype), grads(bad, dtype)
+        keep = [i for i in range(S) if i != 2]
+        assert torch.equal(want[0][keep], got[0][keep]) and torch.equal(want[1][keep], got[1][keep])
+        assert torch.equal(want[2][~hit], got[2][~hit])
+        assert bool((got[2][none] == 0).all())
+
+
 def test_refusals():
     s = make(4, 2, 8, 64, 32, 1)
     y, st, sc = torch.empty(4, 32, device="cuda"), status(), scratch_for(s)
