@@ -560,12 +560,12 @@ int launch_rows(EmbedParams &P, cudaStream_t stream) {
 // Blocks of up to kBlock tokens.  A CTA sorts a block's tokens by id in shared
 // memory (stable, so equal ids keep the tokens' order), while the other CTAs of
 // the launch write the zeros of a gradient that is not accumulated.  The second
-// launch adds up each id's rows: a warp per id and 1024 columns, 16 bytes per
-// lane and load, or, for an id with more than kHeavy tokens, a CTA per 256
+// launch adds up each id's rows: a warp per id and 1024 columns (256 of narrow
+// tables), 16 bytes per lane and load, eight of them in flight, or, for an id with more than kHeavy tokens, a CTA per 256
 // columns whose warps take a share of the tokens each and meet in shared memory.
 // One such launch per block, in order, so that every sum has one order.  Bound
 // by the write of the gradient, or by the read of dY and the rows that it meets.
-constexpr uint32_t kBlock = 16384, kSortThreads = 1024, kHeavy = 64, kDigit = 9;
+constexpr uint32_t kBlock = 16384, kSortThreads = 1024, kHeavy = 32, kDigit = 9;
 constexpr uint32_t kItems = kBlock / kSortThreads;
 constexpr uint32_t kSumThreads = 256, kHeavyCols = 256;
 constexpr size_t kSortSmem = kBlock * (4 + 2) + (kSortThreads / 32) * (1u << kDigit) * 2;
@@ -596,7 +596,11 @@ __global__ void __launch_bounds__(kSortThreads) grad_sort_kernel(const GradSortP
     const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (blockIdx.x >= P.blocks) {
         const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (uint64_t i = uint64_t(blockIdx.x - P.blocks) * kSortThreads + tid; i < P.zero_vecs; i += uint64_t(gridDim.x - P.blocks) * kSortThreads) __stcs(P.zero + i, none);
+        // (four vectors per thread and step)
+        for (uint64_t i = uint64_t(blockIdx.x - P.blocks) * (4 * kSortThreads) + tid; i < P.zero_vecs; i += uint64_t(gridDim.x - P.blocks) * (4 * kSortThreads))
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k)
+                if (i + k * kSortThreads < P.zero_vecs) __stcs(P.zero + i + k * kSortThreads, none);
         return;
     }
     uint32_t *keys = reinterpret_cast<uint32_t *>(smem);
@@ -655,8 +659,13 @@ __global__ void __launch_bounds__(kSortThreads) grad_sort_kernel(const GradSortP
         for (uint32_t k = 0; k < kItems; ++k) {
             if (k >= items) break;
             const uint32_t d = key[k] >> (pass * width) & (bins - 1);
-            const uint32_t same = __match_any_sync(0xffffffffu, d), below = __popc(same & ((1u << lane) - 1u));
-            const uint32_t had = hist[warp][d];
+            // lanes of the same digit, bit by bit
+            uint32_t same = 0xffffffffu;
+            for (uint32_t b = 0; b < width; ++b) {
+                const uint32_t ones = __ballot_sync(0xffffffffu, d >> b & 1u);
+                same &= d >> b & 1u ? ones : ~ones;
+            }
+            const uint32_t below = __popc(same & ((1u << lane) - 1u)), had = hist[warp][d];
             __syncwarp();
             if (below == 0) hist[warp][d] = uint16_t(had + __popc(same));
             __syncwarp();
@@ -666,10 +675,15 @@ __global__ void __launch_bounds__(kSortThreads) grad_sort_kernel(const GradSortP
         // counts to first places: by digit, then by warp
         uint32_t mine = 0;
         if (tid < bins)
-            for (uint32_t w = 0; w < kSortThreads / 32; ++w) {
-                const uint32_t c = hist[w][tid];
-                hist[w][tid] = uint16_t(mine);
-                mine += c;
+            for (uint32_t w0 = 0; w0 < kSortThreads / 32; w0 += 16) {
+                uint16_t c[16];               // (all loads before the stores, which could be to the same place for all the compiler knows)
+#pragma unroll
+                for (uint32_t w = 0; w < 16; ++w) c[w] = hist[w0 + w][tid];
+#pragma unroll
+                for (uint32_t w = 0; w < 16; ++w) {
+                    hist[w0 + w][tid] = uint16_t(mine);
+                    mine += c[w];
+                }
             }
         uint32_t total;
         const uint32_t first = before(mine, total);
@@ -691,27 +705,30 @@ __global__ void __launch_bounds__(kSortThreads) grad_sort_kernel(const GradSortP
             place[k] = places[i];
         }
     }
-    // the distinct ids: thread t looks at places t * items and on
+    // the distinct ids, in order: each warp looks at its items' places, 32 at a time
     if (tid == 0) s_heavy = 0;
     uint32_t heads = 0;
     for (uint32_t k = 0; k < items; ++k) {
-        const uint32_t i = tid * items + k;
-        if (i < n && keys[i] < P.rows && (i == 0 || keys[i - 1] != keys[i])) ++heads;
+        const uint32_t i = (warp * items + k) * 32 + lane;
+        heads += __popc(__ballot_sync(0xffffffffu, i < n && keys[i] < P.rows && (i == 0 || keys[i - 1] != keys[i])));
     }
     uint32_t total;
-    uint32_t at = before(heads, total);
+    uint32_t at = before(lane == 0 ? heads : 0u, total);       // (lane 0's: the warps before)
+    at = __shfl_sync(0xffffffffu, at, 0);
     for (uint32_t k = 0; k < items; ++k) {
-        const uint32_t i = tid * items + k;
-        if (i >= n) break;
-        out.order[i] = places[i];
-        if (keys[i] < P.rows && (i == 0 || keys[i - 1] != keys[i])) {
-            out.id[at] = keys[i];
-            out.start[at] = i;
+        const uint32_t i = (warp * items + k) * 32 + lane;
+        const bool valid = i < n && keys[i] < P.rows, head = valid && (i == 0 || keys[i - 1] != keys[i]);
+        const uint32_t all = __ballot_sync(0xffffffffu, head);
+        if (i < n) out.order[i] = places[i];
+        if (head) {
+            const uint32_t u = at + __popc(all & ((1u << lane) - 1u));
+            out.id[u] = keys[i];
+            out.start[u] = i;
             // (equal keys are adjacent: more than kHeavy of them reach kHeavy places on)
-            if (i + kHeavy < n && keys[i + kHeavy] == keys[i]) out.many[atomicAdd(&s_heavy, 1u)] = at;
-            ++at;
+            if (i + kHeavy < n && keys[i + kHeavy] == keys[i]) out.many[atomicAdd(&s_heavy, 1u)] = u;
         }
-        if (keys[i] < P.rows && (i + 1 == n || keys[i + 1] >= P.rows)) out.start[total] = i + 1;
+        if (valid && (i + 1 == n || keys[i + 1] >= P.rows)) out.start[total] = i + 1;
+        at += __popc(all);
     }
     __syncthreads();
     if (tid == 0) {
@@ -725,7 +742,7 @@ struct GradSumParams {
     const void *dy;                           // the block's first token's row
     float *grad;
     uint64_t dy_stride, cols;
-    uint32_t slabs, heavy_slabs, heavy_blocks;             // of 1024 columns; of kHeavyCols; CTAs for ids with many tokens
+    uint32_t slabs, heavy_slabs, heavy_blocks;             // of a warp's columns; of kHeavyCols; CTAs for ids with many tokens
     float scale;
     bool add;
 };
@@ -768,7 +785,8 @@ __device__ __forceinline__ void put8(float *g, uint64_t left, const float (&v)[8
     }
 }
 
-template <typename T, bool kVec>
+// kVecs: vectors of eight columns per lane and id
+template <typename T, bool kVec, int kVecs>
 __global__ void __launch_bounds__(kSumThreads) grad_sum_kernel(const GradSumParams P) {
     __shared__ float s_part[kSumThreads / 32][kHeavyCols];
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -806,18 +824,19 @@ __global__ void __launch_bounds__(kSumThreads) grad_sum_kernel(const GradSumPara
     if (u >= S.ids) return;
     const uint32_t begin = S.start[u], end = S.start[u + 1];
     if (end - begin > kHeavy) return;
-    const uint64_t c0 = unit % P.slabs * 1024 + lane * 8;
+    const uint64_t c0 = unit % P.slabs * (256 * kVecs) + lane * 8;
+    if (c0 >= P.cols) return;
     float *g = P.grad + uint64_t(S.id[u]) * P.cols;
-    float acc[4][8] = {};
-#pragma unroll 2
+    float acc[kVecs][8] = {};
+#pragma unroll(8 / kVecs)
     for (uint32_t j = begin; j < end; ++j) {
         const T *row = dy + S.order[j] * P.dy_stride;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < kVecs; ++k)
             if (c0 + k * 256 < P.cols) add8<T, kVec>(row + c0 + k * 256, P.cols - (c0 + k * 256), acc[k]);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < kVecs; ++k)
         if (c0 + k * 256 < P.cols) put8<kVec>(g + c0 + k * 256, P.cols - (c0 + k * 256), acc[k], P.scale, P.add);
 }
 
@@ -928,7 +947,8 @@ int launch_grad(const void *d_ids, uint32_t id_bytes, uint64_t n, const T *dy, u
         P.block = sorted + b;
         P.dy = dy + uint64_t(b) * kBlock * dy_stride;
         P.grad = grad, P.dy_stride = dy_stride, P.cols = cols, P.scale = scale, P.add = add || b > 0;
-        P.slabs = uint32_t((cols + 1023) / 1024);
+        const bool wide = cols > 1024;
+        P.slabs = uint32_t((cols + (wide ? 1023 : 255)) / (wide ? 1024 : 256));
         P.heavy_slabs = uint32_t((cols + kHeavyCols - 1) / kHeavyCols);
         const uint64_t heavy = size / (kHeavy + 1) * P.heavy_slabs, light = (std::min(size, rows) * P.slabs + kSumThreads / 32 - 1) / (kSumThreads / 32);
         if (heavy + light > 0x7FFFFFFFull) return K3HUF_E_ARG;
@@ -942,7 +962,8 @@ int launch_grad(const void *d_ids, uint32_t id_bytes, uint64_t n, const T *dy, u
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        rc = cuda_rc(vec ? cudaLaunchKernelEx(&cfg, grad_sum_kernel<T, true>, P) : cudaLaunchKernelEx(&cfg, grad_sum_kernel<T, false>, P));
+        rc = cuda_rc(vec ? cudaLaunchKernelEx(&cfg, wide ? grad_sum_kernel<T, true, 4> : grad_sum_kernel<T, true, 1>, P)
+                         : cudaLaunchKernelEx(&cfg, wide ? grad_sum_kernel<T, false, 4> : grad_sum_kernel<T, false, 1>, P));
     }
     return rc;
 }
