@@ -747,26 +747,34 @@ struct GradSumParams {
     bool add;
 };
 
-// kVec: 16-byte loads and stores; eight adjacent columns per lane
-template <typename T, bool kVec>
-__device__ __forceinline__ void add8(const T *p, uint64_t left, float (&acc)[8]) {
-    if constexpr (kVec && sizeof(T) == 2) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Eight adjacent columns of a row as they were loaded: 16-byte loads (kVec), or fp32 values one by one.
+template <typename T, bool kVec> struct Row8 {
+    static constexpr int words = kVec && sizeof(T) == 2 ? 4 : 8;
+    uint32_t w[words];
+    __device__ __forceinline__ void load(const T *p, uint64_t left) {
+        if constexpr (kVec) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            acc[2 * i] += __uint_as_float(w[i] << 16);
-            acc[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
+            for (int i = 0; i < words / 4; ++i) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = uint64_t(i) < left ? __float_as_uint(ld_f32(p + i)) : 0u;
         }
-    } else if constexpr (kVec) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-        acc[0] += a.x, acc[1] += a.y, acc[2] += a.z, acc[3] += a.w, acc[4] += b.x, acc[5] += b.y, acc[6] += b.z, acc[7] += b.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (uint64_t(i) < left) acc[i] += ld_f32(p + i);
     }
-}
+    __device__ __forceinline__ void add_to(float (&acc)[8]) const {
+#pragma unroll
+        for (int i = 0; i < words; ++i) {
+            if constexpr (words == 4) {
+                acc[2 * i] += __uint_as_float(w[i] << 16);
+                acc[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
+            } else {
+                acc[i] += __uint_as_float(w[i]);
+            }
+        }
+    }
+};
 template <bool kVec>
 __device__ __forceinline__ void put8(float *g, uint64_t left, const float (&v)[8], float scale, bool add) {
     if constexpr (kVec) {
@@ -785,6 +793,34 @@ __device__ __forceinline__ void put8(float *g, uint64_t left, const float (&v)[8
     }
 }
 
+// Adds up rows `token(j)` of dy for j in [j0, j1), in order, kVecs vectors of eight
+// columns per lane: 32 tokens' numbers are fetched at once, and 8 / kVecs rows are
+// in flight together.
+template <typename T, bool kVec, int kVecs, typename F>
+__device__ __forceinline__ void add_rows(const T *dy, uint64_t stride, uint64_t c0, uint64_t cols, uint32_t j0, uint32_t j1, F token, float (&acc)[kVecs][8]) {
+    constexpr uint32_t kRows = 8 / kVecs;
+    const uint32_t lane = threadIdx.x % 32;
+    for (uint32_t j = j0; j < j1; j += 32) {
+        const uint32_t mine = j + lane < j1 ? token(j + lane) : 0u, n = min(32u, j1 - j);
+        for (uint32_t k = 0; k < n; k += kRows) {
+            Row8<T, kVec> rows[kRows][kVecs] = {};
+#pragma unroll
+            for (uint32_t r = 0; r < kRows; ++r) {
+                const uint32_t t = __shfl_sync(0xffffffffu, mine, (k + r) & 31u);
+#pragma unroll
+                for (int v = 0; v < kVecs; ++v) {
+                    const uint64_t c = c0 + v * 256;
+                    if (k + r < n && c < cols) rows[r][v].load(dy + t * stride + c, cols - c);
+                }
+            }
+#pragma unroll
+            for (uint32_t r = 0; r < kRows; ++r)
+#pragma unroll
+                for (int v = 0; v < kVecs; ++v) rows[r][v].add_to(acc[v]);
+        }
+    }
+}
+
 // kVecs: vectors of eight columns per lane and id
 template <typename T, bool kVec, int kVecs>
 __global__ void __launch_bounds__(kSumThreads) grad_sum_kernel(const GradSumParams P) {
@@ -800,11 +836,9 @@ __global__ void __launch_bounds__(kSumThreads) grad_sum_kernel(const GradSumPara
         const uint32_t u = S.many[h], begin = S.start[u], count = S.start[u + 1] - begin;
         const uint64_t c = uint64_t(blockIdx.x % P.heavy_slabs) * kHeavyCols + lane * 8;
         const uint64_t left = c < P.cols ? P.cols - c : 0;
-        float acc[8] = {};
-        const uint32_t j1 = begin + uint32_t(uint64_t(count) * (warp + 1) / 8);
-        if (left)
-#pragma unroll 8
-            for (uint32_t j = begin + uint32_t(uint64_t(count) * warp / 8); j < j1; ++j) add8<T, kVec>(dy + S.order[j] * P.dy_stride + c, left, acc);
+        float sum[1][8] = {};
+        add_rows<T, kVec, 1>(dy, P.dy_stride, c, P.cols, begin + uint32_t(uint64_t(count) * warp / 8), begin + uint32_t(uint64_t(count) * (warp + 1) / 8), [&](uint32_t j) { return S.order[j]; }, sum);
+        float(&acc)[8] = sum[0];
 #pragma unroll
         for (int i = 0; i < 8; ++i) s_part[warp][i * 32 + lane] = acc[i];
         __syncthreads();
@@ -825,16 +859,9 @@ __global__ void __launch_bounds__(kSumThreads) grad_sum_kernel(const GradSumPara
     const uint32_t begin = S.start[u], end = S.start[u + 1];
     if (end - begin > kHeavy) return;
     const uint64_t c0 = unit % P.slabs * (256 * kVecs) + lane * 8;
-    if (c0 >= P.cols) return;
     float *g = P.grad + uint64_t(S.id[u]) * P.cols;
     float acc[kVecs][8] = {};
-#pragma unroll(8 / kVecs)
-    for (uint32_t j = begin; j < end; ++j) {
-        const T *row = dy + S.order[j] * P.dy_stride;
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k)
-            if (c0 + k * 256 < P.cols) add8<T, kVec>(row + c0 + k * 256, P.cols - (c0 + k * 256), acc[k]);
-    }
+    add_rows<T, kVec, kVecs>(dy, P.dy_stride, c0, P.cols, begin, end, [&](uint32_t j) { return S.order[j]; }, acc);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k)
         if (c0 + k * 256 < P.cols) put8<kVec>(g + c0 + k * 256, P.cols - (c0 + k * 256), acc[k], P.scale, P.add);
@@ -888,12 +915,9 @@ __global__ void __launch_bounds__(kSumThreads) grad_few_kernel(const GradFewPara
     }
     __syncthreads();
     const uint64_t c = uint64_t(blockIdx.y) * 2048 + warp * 256 + lane * 8;
-    if (c >= P.cols) return;
-    const T *dy = static_cast<const T *>(P.dy) + c;
-    float acc[8] = {};
-#pragma unroll 8
-    for (uint32_t j = 0; j < count; ++j) add8<T, kVec>(dy + s_token[j] * P.dy_stride, P.cols - c, acc);
-    put8<kVec>(P.grad + uint64_t(id) * P.cols + c, P.cols - c, acc, P.scale, P.add);
+    float acc[1][8] = {};
+    add_rows<T, kVec, 1>(static_cast<const T *>(P.dy), P.dy_stride, c, P.cols, 0, count, [&](uint32_t j) { return uint32_t(s_token[j]); }, acc);
+    if (c < P.cols) put8<kVec>(P.grad + uint64_t(id) * P.cols + c, P.cols - c, acc[0], P.scale, P.add);
 }
 
 // Fewer than four gradient elements, or an address that is not 16-byte aligned: the zeros that
