@@ -541,12 +541,14 @@ int launch_rows(EmbedParams &P, cudaStream_t stream) {
         embed_long_kernel<T><<<uint32_t(blocks), kThreads, 0, stream>>>(P);
         return cuda_rc(cudaGetLastError());
     }
-    // units per item: 32, fewer while the call has one item per SM or less
+    // units per item: 32, fewer while every warp of the GPU still gets one item at most (a warp's
+    // latency then counts, not its instructions: 4000 rows of 577 values 30 us, 54 with 32 units
+    // per item; 8000 rows of 8192 values are the same 85 us, since they keep 32)
     uint64_t sms = 0;
     const int rc = sm_count(&sms);
     if (rc) return rc;
     P.lanes = 32;
-    while (P.lanes > 4 && total <= P.lanes / 2 * sms) P.lanes /= 2;
+    while (P.lanes > 4 && total <= P.lanes / 2 * sms * kWarps) P.lanes /= 2;
     P.items = (total + P.lanes - 1) / P.lanes;
     const uint32_t grid = uint32_t(std::min<uint64_t>(sms, P.items));
     const bool fixed = P.chunk_syms == 4096 && P.sub_syms == 256;
