@@ -9,7 +9,7 @@
 // "expand" (a sum of a factor's rows) and "outer" (a sum over tokens).
 //
 // Three forms, by a rule on sizes and alignment (run_form):
-//  - few tokens (tokens x rank up to kFewWork): fp32 arithmetic, a CTA per
+//  - few tokens (their factor rows up to kFewBytes): fp32 arithmetic, a CTA per
 //    token and part of the factor; every factor row is read once per token,
 //    mostly from L2;
 //  - many: tcgen05.mma on tiles of 128 tokens, described at each kernel;
@@ -25,7 +25,7 @@ namespace k3huf {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr uint64_t kFewWork = 4096;           // tokens x rank
+constexpr uint64_t kFewBytes = 300'000'000;    // of factor rows, read once per token
 
 __device__ __forceinline__ bool adapter_of(const int32_t *ids, uint64_t t, uint32_t n_adapters, int32_t &i) {
     i = ids[t];
@@ -810,10 +810,14 @@ uint64_t h_bytes(uint64_t n, uint32_t rank) { return align_up(n * 2 * kMaxParts 
 
 enum class Form { any, few, many };
 bool rows16(const void *p, uint64_t stride, uint32_t type) { return aligned_to(p, 16) && stride * elem_bytes(type) % 16 == 0; }
-// Tokens x rank up to kFewWork: each token's factor rows are read on their own,
-// about 100 MB from L2 at 4096 x (8192 + 8192) in 14 us; the tiles take about 20 us
-// for 192 tokens of as many adapters.
-Form run_form(uint64_t n, uint32_t rank, bool rows_ok) { return !rows_ok ? Form::any : n * rank <= kFewWork ? Form::few : Form::many; }
+// Few tokens: each reads its factor rows on its own, at about 10 TB/s from L2.
+// Per call, few and many, fp32 and bf16 results: 256 tokens x 64 x (4096 +
+// 4096), 268 MB, 27 us and 31 or 30; 250 x 32 x (8192 + 8192) of 64 adapters,
+// 262 MB, 42 or 39 and 152 or 91; 1000 x 32 x (4096 + 4096) of 32 adapters, 524
+// MB, 48 and 59 or 41; 2000 x 16 x (8192 + 8192), 1 GB, 118 or 113 and 69 or 46.
+Form run_form(uint64_t n, const k3huf_adapters_t *ad, bool rows_ok) {
+    return !rows_ok ? Form::any : n <= 65535 && n * ad->rank * (ad->cols + ad->rows) * 2 <= kFewBytes ? Form::few : Form::many;
+}
 
 // A launch that may begin while the kernel before it ends (its blocks wait for that one themselves).
 template <typename... Args, typename... Given>
@@ -940,7 +944,7 @@ extern "C" int k3huf_adapter_apply(const k3huf_adapters_t *ad, const void *d_x, 
     const auto *a = static_cast<const __nv_bfloat16 *>(ad->a), *b = static_cast<const __nv_bfloat16 *>(ad->b), *x = static_cast<const __nv_bfloat16 *>(d_x);
     const bool rows_ok = rows16(a, ad->cols, K3HUF_BF16) && rows16(b, ad->rows, K3HUF_BF16) && rows16(x, x_stride, K3HUF_BF16) &&
                          rows16(d_y, y_stride, y_type) && (!d_base || rows16(d_base, base_stride, y_type));
-    switch (run_form(n, r, rows_ok)) {
+    switch (run_form(n, ad, rows_ok)) {
         case Form::any: {
             float *h = static_cast<float *>(d_scratch);
             shrink_any_kernel<<<n, kThreads, 0, st>>>(x, x_stride, a, ad->scales, d_ids, S, r, ad->cols, h, d_status);

@@ -102,6 +102,26 @@ def test_apply_matches_the_formula(n, S, r, cols, rows, kind, dtype):
         assert torch.equal(again, y)                     # the same bits every time
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["mixed", "runs", "one"])
+@pytest.mark.parametrize("n,S,r,cols,rows", [(2100, 3, 64, 1024, 1032), (1300, 40, 128, 520, 776), (4001, 2, 48, 600, 264), (9000, 6, 16, 512, 576)])
+def test_apply_to_many_tokens(n, S, r, cols, rows, kind, dtype):
+    """Enough factor rows for the tensor-core tiles (over 300 MB): several adapters per tile, ranks of one and two
+    blocks, padded ranks, ragged last tiles."""
+    s = make(n, S, r, cols, rows, n + cols, kind)
+    base = torch.randn(n, rows, device="cuda").to(dtype)
+    for b in (base, None):
+        y = torch.full((n, rows), float("nan"), device="cuda", dtype=dtype)
+        assert apply(s, y, b) == 0
+        want, tol = reference(s, b)
+        assert bool(((y.double() - want).abs() <= tol + rounding(dtype) * want.abs()).all())
+        again = torch.empty_like(y)
+        apply(s, again, b)
+        assert torch.equal(again, y)
+        if dtype == torch.float32:
+            assert float((y.double() - want).norm() / want.norm()) < 2e-6
+
+
 def test_fp32_result_keeps_fp32_precision():
     """The rank-wide intermediate is not rounded to 16 bits on the way to an fp32 result: the whole output is within
     2e-6 of the formula in the 2-norm (fp32 sums of 1024 terms err by about 1e-6 or less; a bf16 intermediate by 2e-3,
