@@ -502,6 +502,7 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
     }
     fence_async_shared();
     grid_dep_wait();
+    grid_dep_launch();                        // (the outer products need the shrink only, which is done)
     const uint32_t count = tile_adapters(tile, P.ids, t0, P.n, P.n_adapters, nullptr);
     tc_fence_before();
     __syncthreads();
@@ -628,7 +629,7 @@ struct OuterParams {
     uint32_t *status;
     uint64_t n;
     uint32_t n_adapters, rank, rank_pad, pitch, col_tiles0;        // column tiles of job 0
-    bool add;
+    bool add, beside;                         // add to g; launched beside an expand (see the kernel's first wait)
 };
 
 // The outer product.  D[128 columns, rank] = V^T H over the tokens of one
@@ -666,7 +667,9 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
     if (tid == 0)
         for (uint32_t i = 0; i < kOuterStages; ++i) mbar_init(smem_addr(&s_bar[i]), 1);
     if (tid == 0) fence_async_shared();
-    grid_dep_wait();
+    // Behind an expand this kernel's CTAs start once all of that one's have seen the shrink end, so
+    // nothing that they read is still being written; they wait for the expand at their end
+    if (!P.beside) grid_dep_wait();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -792,6 +795,7 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
         tc_fence_after();
     }
     if (!ok) atomicOr(P.status, K3HUF_ST_TIMEOUT);
+    if (P.beside) grid_dep_wait();
     if (warp == 0) tmem_free(tmem, 2 * O::half);
 }
 
@@ -1033,6 +1037,6 @@ extern "C" int k3huf_adapter_grad(const k3huf_adapters_t *ad, const void *d_x, u
         if (rc) return rc;
     }
     const uint32_t tiles_a = uint32_t((ad->cols + 127) / 128), tiles_b = uint32_t((ad->rows + 127) / 128);
-    const OuterParams op{{{dh, x, d_da, x_stride, uint32_t(ad->cols)}, {h, dy, d_db, dy_stride, uint32_t(ad->rows)}}, d_ids, d_status, n, S, r, padded(r), h_pitch(r), tiles_a, add};
+    const OuterParams op{{{dh, x, d_da, x_stride, uint32_t(ad->cols)}, {h, dy, d_db, dy_stride, uint32_t(ad->rows)}}, d_ids, d_status, n, S, r, padded(r), h_pitch(r), tiles_a, add, d_dx != nullptr};
     return launch_outer(op, tiles_a + tiles_b, st);
 }
