@@ -433,12 +433,12 @@ struct ExpandParams {
 // thread holds a token's neighbouring columns, so it adds 16 bytes of the base
 // at a time, in tiles of 128-byte rows that TMA brings and takes away swizzled.
 // CTAs: a tile of tokens x a range of column tiles; a step is one adapter of
-// one column tile.  Warps 0 to 7 add; a thread of warp 8 brings W and issues
-// the products, two steps ahead of the additions; one of warp 9 brings the base
-// and takes y away.  Bound by the read of the base and the write of y: 158 us for
+// one column tile.  Warps 0 to 7 add; a thread of warp 8 issues the products, two
+// steps ahead of the additions; one of warp 9 brings the base and takes y away;
+// one of warp 10 brings W.  Bound by the read of the base and the write of y: 158 us for
 // 8192 tokens x 24576 bf16 columns, 5.1 TB/s.  (With columns as the lanes, 2 bytes
 // at a time, the additions took five times the instructions, 184 us.)
-constexpr uint32_t kExpandThreads = kThreads + 64;
+constexpr uint32_t kExpandThreads = kThreads + 96;
 template <typename T, uint32_t kBlocks> struct Expand {       // kBlocks: blocks of 64 rank rows
     static constexpr uint32_t row = 128 / sizeof(T), cols = 2 * row;      // columns of a 128-byte row; of a tile of two of them
     static constexpr uint32_t parts = sizeof(T) == 4 ? 3 : 2;
@@ -514,36 +514,48 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
             mbar_expect(smem_addr(&s_h), E::h_bytes);
             for (uint32_t q = 0; q < E::parts; ++q)
                 for (uint32_t b = 0; b < kBlocks; ++b) tma_load(h_at + (q * kBlocks + b) * kTileBytes, &P.h, int32_t(b * 64), int32_t(q * P.n + t0), smem_addr(&s_h));
-            // W of step s: blocks of 64 columns, each the adapter's rank rows
-            auto load = [&](uint32_t s) {
-                const uint32_t bar = smem_addr(&s_w[s % WS]), at = w_at + s % WS * E::w_bytes;
-                mbar_expect(bar, E::cols / 64 * P.rank * 128);
-                for (uint32_t b = 0; b < E::cols / 64; ++b)
-                    tma_load(at + b * E::w_block, &P.w, int32_t((c0 + s / count) * E::cols + b * 64), tile.list[s % count] * int32_t(P.rank), bar);
-            };
-            const uint32_t desc = mma_desc(kTile, E::cols, 0, 1);
-            uint32_t loaded = 0;
-            for (; loaded < min(WS, steps); ++loaded) load(loaded);
+            // (descriptors and places kept up to date, not worked out: one thread issues for all)
+            constexpr uint32_t desc = mma_desc(kTile, E::cols, 0, 1);
+            const uint64_t h0 = tile_desc(h_at, 16, 1024), w0 = tile_desc(w_at, E::w_block, 1024);
+            const uint32_t subs = rp / 16;
+            uint32_t stage = 0, round = 0;    // of W: s % WS and s / WS & 1
             ok = mbar_wait(smem_addr(&s_h), 0);
             for (uint32_t s = 0; s < steps && ok; ++s) {
-                ok = mbar_wait(smem_addr(&s_w[s % WS]), s / WS & 1);
+                ok = mbar_wait(smem_addr(&s_w[stage]), round);
                 if (s >= 2 && ok) ok = mbar_wait(smem_addr(&s_dfree[s & 1]), (s / 2 - 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t w = tile_desc(w_at + s % WS * E::w_bytes, E::w_block, 1024);
+                const uint64_t w = w0 + stage * (E::w_bytes >> 4);
+                const uint32_t d = tmem + (s & 1) * 128;
+#pragma unroll
                 for (uint32_t q = 0; q < E::parts; ++q)
-                    for (uint32_t k = 0; k < rp / 16; ++k)
-                        mma(tmem + (s & 1) * 128, tile_desc(h_at + (q * kBlocks + k / 4) * kTileBytes, 16, 1024) + 2 * (k % 4), w + k * 128, desc, q || k);
-                mma_commit(smem_addr(&s_wfree[s % WS]));
+#pragma unroll
+                    for (uint32_t k = 0; k < 4 * kBlocks; ++k)
+                        if (k < subs) mma(d, h0 + (((q * kBlocks + k / 4) * kTileBytes) >> 4) + 2 * (k % 4), w + k * 128, desc, q || k);
+                mma_commit(smem_addr(&s_wfree[stage]));
                 mma_commit(smem_addr(&s_d[s & 1]));
-                // (a stage is free once the products before these are done)
-                if (s > 0 && loaded < steps) {
-                    ok = mbar_wait(smem_addr(&s_wfree[(s - 1) % WS]), (s - 1) / WS & 1);
-                    if (ok) load(loaded++);
-                }
+                if (++stage == WS) stage = 0, round ^= 1u;
             }
+        }
+    } else if (warp == kThreads / 32 + 2) {
+        if (lane == 0) {
+            // W of a step: blocks of 64 columns, each the adapter's rank rows
+            uint32_t stage = 0, round = 1, s = 0;      // (the first round's stages are free)
+            for (uint32_t i = 0; i < tiles && ok; ++i)
+                for (uint32_t a = 0; a < count && ok; ++a, ++s) {
+                    const uint32_t bar = smem_addr(&s_w[stage]), at = w_at + stage * E::w_bytes;
+                    if (s >= WS) ok = mbar_wait(smem_addr(&s_wfree[stage]), round);
+                    if (!ok) break;
+                    mbar_expect(bar, E::cols / 64 * P.rank * 128);
+#pragma unroll
+                    for (uint32_t b = 0; b < E::cols / 64; ++b) tma_load(at + b * E::w_block, &P.w, int32_t((c0 + i) * E::cols + b * 64), tile.list[a] * int32_t(P.rank), bar);
+                    if (++stage == WS) stage = 0, round ^= 1u;
+                }
             if (!ok)                          // copies still in flight land first
-                for (uint32_t s = loaded > WS ? loaded - WS : 0; s < loaded; ++s) mbar_wait(smem_addr(&s_w[s % WS]), s / WS & 1);
+                for (uint32_t k = 0; k < min(s, WS); ++k) {
+                    stage = stage ? stage - 1 : WS - 1;
+                    mbar_wait(smem_addr(&s_w[stage]), (s - 1 - k) / WS & 1);
+                }
         }
     } else if (warp == kThreads / 32 + 1) {
         if (lane == 0) {
