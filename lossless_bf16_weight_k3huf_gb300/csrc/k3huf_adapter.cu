@@ -277,9 +277,9 @@ struct ShrinkParams {
 // group of adapters whose rank rows fill 128 columns (all but the first few
 // groups of a tile whose tokens share adapters end at once) x a split of the
 // contraction; the splits are a cluster, whose partial sums meet through shared
-// memory in the order of the splits.  One thread keeps copies and products
-// going for a run of kRun steps while the CTA moves the run before it from the
-// other half of TMEM to registers.  Bound by the read of V (and of the factors
+// memory in the order of the splits.  One thread keeps the products and one the
+// copies going for a run of kRun steps while the CTA moves the run before it from
+// the other half of TMEM to registers.  Bound by the read of V (and of the factors
 // when every token has its own).
 constexpr uint32_t kShrinkStages = 3, kShrinkStage = 2 * kTileBytes;
 constexpr size_t kShrinkSmem = kShrinkStages * kShrinkStage + 1024;
@@ -326,29 +326,32 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
         for (uint32_t a = 0; a < na; ++a) tma_load(at + kTileBytes + a * rp * 128, &J.w, int32_t((k0 + i) * kStep), tile.list[a0 + a] * int32_t(P.rank), bar);
     };
     const uint32_t desc = mma_desc(kTile, cols, 0, 0);
+    const uint64_t d0 = tile_desc(base, 16, 1024);
     uint32_t loaded = 0;
-    if (tid == 0)
+    if (tid == 32)
         for (; loaded < min(kShrinkStages - 1, n_steps); ++loaded) load(loaded);
     // this thread's sums: token (lane) warp % 4 * 32 + lane, columns warp / 4 * 64 on
     float sum[64] = {};
     for (uint32_t run = 0; run <= runs; ++run) {
+        const uint32_t last = min((run + 1) * kRun, n_steps);
         if (tid == 0 && run < runs) {
-            for (uint32_t i = run * kRun; i < min((run + 1) * kRun, n_steps) && ok; ++i) {
+            for (uint32_t i = run * kRun; i < last && ok; ++i) {
                 const uint32_t stage = i % kShrinkStages;
                 ok = mbar_wait(smem_addr(&s_full[stage]), i / kShrinkStages & 1);
                 tc_fence_after();
-                const uint64_t a = tile_desc(base + stage * kShrinkStage, 16, 1024), b = tile_desc(base + stage * kShrinkStage + kTileBytes, 16, 1024);
+                const uint64_t a = d0 + stage * (kShrinkStage >> 4), b = a + (kTileBytes >> 4);
 #pragma unroll
                 for (uint32_t s = 0; s < kStep / 16; ++s) mma(tmem + (run & 1) * 128, a + 2 * s, b + 2 * s, desc, i % kRun || s);
                 mma_commit(smem_addr(&s_free[stage]));
-                // the stage before this one is free once its products are done
-                if (loaded < n_steps && ok) {
-                    if (i > 0) ok = mbar_wait(smem_addr(&s_free[(i - 1) % kShrinkStages]), (i - 1) / kShrinkStages & 1);
-                    if (ok) load(loaded++);
-                }
             }
             mma_commit(smem_addr(&s_run[run & 1]));
         }
+        if (tid == 32 && run < runs)
+            // a stage is free once the products of the step before are done
+            for (uint32_t i = run * kRun; i < last && loaded < n_steps && ok; ++i) {
+                if (i > 0) ok = mbar_wait(smem_addr(&s_free[(i - 1) % kShrinkStages]), (i - 1) / kShrinkStages & 1);
+                if (ok) load(loaded++);
+            }
         __syncwarp();
         if (run > 0) {
             const uint32_t r = run - 1;
@@ -369,7 +372,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
     if (!ok) {
         atomicOr(P.status, K3HUF_ST_TIMEOUT);
         // copies still in flight, if any, land first
-        if (tid == 0)
+        if (tid == 32)
             for (uint32_t i = loaded > kShrinkStages ? loaded - kShrinkStages : 0; i < loaded; ++i) mbar_wait(smem_addr(&s_full[i % kShrinkStages]), i / kShrinkStages & 1);
     }
     __syncthreads();
