@@ -25,8 +25,8 @@ namespace {
 
 constexpr int kMaxStripes = 256;              // stripes of the tensor (kernel parameter space)
 constexpr int kThreads = 128;                 // (one-symbol lookup kernel)
-constexpr int kWarps = 24, kEmbedThreads = 32 * kWarps;
-constexpr uint32_t kPieces = 256;             // 16-byte pieces of bits staged per warp
+constexpr int kWarps = 18, kEmbedThreads = 32 * kWarps;
+constexpr uint32_t kPieces = 464;             // 16-byte pieces of bits staged per warp
 constexpr int kRound = 64;                    // values per unit between joins
 constexpr int kRowWords = kRound / 4 + 1;     // a unit's high bytes of one round; the odd stride spreads the banks
 constexpr uint32_t kMaxStagedSub = 1024;      // longest sub-stream whose bits surely fit a warp's pieces
