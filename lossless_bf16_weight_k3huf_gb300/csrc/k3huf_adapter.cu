@@ -273,10 +273,9 @@ struct ShrinkParams {
 
 // The shrink.  D[128 tokens, rank rows of the tile's adapters] = V W^T, both
 // operands K-major tiles brought by TMA, kStep of the contraction per stage;
-// every token keeps the columns of its own adapter.  CTAs: a tile of tokens x a
-// group of adapters whose rank rows fill 128 columns (all but the first few
-// groups of a tile whose tokens share adapters end at once) x a split of the
-// contraction; the splits are a cluster, whose partial sums meet through shared
+// every token keeps the columns of its own adapter.  CTAs: a tile of tokens x some
+// of its groups of adapters, whose rank rows fill 128 columns (a tile whose tokens
+// share adapters has one or two groups), x a split of the contraction; the splits are a cluster, whose partial sums meet through shared
 // memory in the order of the splits.  One thread keeps the products and one the
 // copies going for a run of kRun steps while the CTA moves the run before it from
 // the other half of TMEM to registers.  Bound by the read of V (and of the factors
@@ -297,9 +296,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
     const uint64_t t0 = uint64_t(blockIdx.x / P.splits) * kTile;
     grid_dep_launch();
     const uint32_t per = kTile / rp, count = tile_adapters(tile, P.ids, t0, P.n, P.n_adapters, split + blockIdx.y + blockIdx.z == 0 ? P.status : nullptr);
-    const uint32_t a0 = blockIdx.y * per, na = a0 < count ? min(per, count - a0) : 0u;
-    if (na == 0) return;                      // (the whole cluster)
-    const uint32_t cols = na * rp;            // <= 128, a multiple of 16
+    if (blockIdx.y * per >= count) return;    // (the whole cluster)
     if (warp == 0) tmem_alloc(smem_addr(&s_tmem), 256);
     if (tid == 0) {
         for (uint32_t i = 0; i < kShrinkStages; ++i) {
@@ -319,103 +316,108 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
     constexpr uint32_t kRun = kChain / (kStep / 16);
     const uint32_t runs = (n_steps + kRun - 1) / kRun;
     bool ok = true;
-    auto load = [&](uint32_t i) {             // by one thread
-        const uint32_t stage = i % kShrinkStages, at = base + stage * kShrinkStage, bar = smem_addr(&s_full[stage]);
-        mbar_expect(bar, kTileBytes + na * P.rank * 128);
-        tma_load(at, &J.v, int32_t((k0 + i) * kStep), int32_t(t0), bar);
-        for (uint32_t a = 0; a < na; ++a) tma_load(at + kTileBytes + a * rp * 128, &J.w, int32_t((k0 + i) * kStep), tile.list[a0 + a] * int32_t(P.rank), bar);
-    };
-    const uint32_t desc = mma_desc(kTile, cols, 0, 0);
-    const uint64_t d0 = tile_desc(base, 16, 1024);
-    uint32_t loaded = 0;
-    if (tid == 32)
-        for (; loaded < min(kShrinkStages - 1, n_steps); ++loaded) load(loaded);
-    // this thread's sums: token (lane) warp % 4 * 32 + lane, columns warp / 4 * 64 on
-    float sum[64] = {};
-    for (uint32_t run = 0; run <= runs; ++run) {
-        const uint32_t last = min((run + 1) * kRun, n_steps);
-        if (tid == 0 && run < runs) {
-            for (uint32_t i = run * kRun; i < last && ok; ++i) {
-                const uint32_t stage = i % kShrinkStages;
-                ok = mbar_wait(smem_addr(&s_full[stage]), i / kShrinkStages & 1);
-                tc_fence_after();
-                const uint64_t a = d0 + stage * (kShrinkStage >> 4), b = a + (kTileBytes >> 4);
-#pragma unroll
-                for (uint32_t s = 0; s < kStep / 16; ++s) mma(tmem + (run & 1) * 128, a + 2 * s, b + 2 * s, desc, i % kRun || s);
-                mma_commit(smem_addr(&s_free[stage]));
-            }
-            mma_commit(smem_addr(&s_run[run & 1]));
-        }
-        if (tid == 32 && run < runs)
-            // a stage is free once the products of the step before are done
-            for (uint32_t i = run * kRun; i < last && loaded < n_steps && ok; ++i) {
-                if (i > 0) ok = mbar_wait(smem_addr(&s_free[(i - 1) % kShrinkStages]), (i - 1) / kShrinkStages & 1);
-                if (ok) load(loaded++);
-            }
-        __syncwarp();
-        if (run > 0) {
-            const uint32_t r = run - 1;
-            if (!mbar_wait(smem_addr(&s_run[r & 1]), r / 2 & 1)) ok = false;
-            tc_fence_after();
-#pragma unroll
-            for (uint32_t c = 0; c < 64; c += 16)
-                if (warp / 4 * 64 + c < cols) {
-                    float v[16];
-                    tmem_load16(tmem + ((warp % 4) << 21) + (r & 1) * 128 + warp / 4 * 64 + c, v);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) sum[c + k] += v[k];
-                }
-            tc_fence_before();
-        }
-        __syncthreads();                      // (the run after the next writes this half)
-    }
-    if (!ok) {
-        atomicOr(P.status, K3HUF_ST_TIMEOUT);
-        // copies still in flight, if any, land first
+    // the tile's groups of adapters that fall to this cluster; steps and runs count on (step0, run0)
+    for (uint32_t a0 = blockIdx.y * per, step0 = 0, run0 = 0; a0 < count; a0 += gridDim.y * per, step0 += n_steps, run0 += runs) {
+        const uint32_t na = min(per, count - a0), cols = na * rp;          // (<= 128, a multiple of 16)
+        auto load = [&](uint32_t i) {             // by one thread
+            const uint32_t stage = (step0 + i) % kShrinkStages, at = base + stage * kShrinkStage, bar = smem_addr(&s_full[stage]);
+            mbar_expect(bar, kTileBytes + na * P.rank * 128);
+            tma_load(at, &J.v, int32_t((k0 + i) * kStep), int32_t(t0), bar);
+            for (uint32_t a = 0; a < na; ++a) tma_load(at + kTileBytes + a * rp * 128, &J.w, int32_t((k0 + i) * kStep), tile.list[a0 + a] * int32_t(P.rank), bar);
+        };
+        const uint32_t desc = mma_desc(kTile, cols, 0, 0);
+        const uint64_t d0 = tile_desc(base, 16, 1024);
+        uint32_t loaded = 0;
         if (tid == 32)
-            for (uint32_t i = loaded > kShrinkStages ? loaded - kShrinkStages : 0; i < loaded; ++i) mbar_wait(smem_addr(&s_full[i % kShrinkStages]), i / kShrinkStages & 1);
-    }
-    __syncthreads();
-
-    // each token's own columns, to shared memory (odd stride: one bank per lane)
-    float *part = reinterpret_cast<float *>(smem);
-    const uint32_t stride = rp + 1;
-    {
-        const uint32_t t = warp % 4 * 32 + lane;
-        const int32_t of = tile.of[t];
+            for (; loaded < min(kShrinkStages - 1, n_steps); ++loaded) load(loaded);
+        // this thread's sums: token (lane) warp % 4 * 32 + lane, columns warp / 4 * 64 on
+        float sum[64] = {};
+        for (uint32_t run = 0; run <= runs; ++run) {
+            const uint32_t last = min((run + 1) * kRun, n_steps);
+            if (tid == 0 && run < runs) {
+                for (uint32_t i = run * kRun; i < last && ok; ++i) {
+                    const uint32_t stage = (step0 + i) % kShrinkStages;
+                    ok = mbar_wait(smem_addr(&s_full[stage]), (step0 + i) / kShrinkStages & 1);
+                    tc_fence_after();
+                    const uint64_t a = d0 + stage * (kShrinkStage >> 4), b = a + (kTileBytes >> 4);
 #pragma unroll
-        for (uint32_t c = 0; c < 64; c += 16) {
-            const uint32_t q = warp / 4 * 64 + c;
-            if (q < cols && of == int32_t(a0 + q / rp))
+                    for (uint32_t s = 0; s < kStep / 16; ++s) mma(tmem + ((run0 + run) & 1) * 128, a + 2 * s, b + 2 * s, desc, i % kRun || s);
+                    mma_commit(smem_addr(&s_free[stage]));
+                }
+                mma_commit(smem_addr(&s_run[(run0 + run) & 1]));
+            }
+            if (tid == 32 && run < runs)
+                // a stage is free once the products of the step before are done
+                for (uint32_t i = run * kRun; i < last && loaded < n_steps && ok; ++i) {
+                    if (i > 0) ok = mbar_wait(smem_addr(&s_free[(step0 + i - 1) % kShrinkStages]), (step0 + i - 1) / kShrinkStages & 1);
+                    if (ok) load(loaded++);
+                }
+            __syncwarp();
+            if (run > 0) {
+                const uint32_t r = run0 + run - 1;
+                if (!mbar_wait(smem_addr(&s_run[r & 1]), r / 2 & 1)) ok = false;
+                tc_fence_after();
 #pragma unroll
-                for (uint32_t k = 0; k < 16; ++k) part[t * stride + q % rp + k] = sum[c + k];
+                for (uint32_t c = 0; c < 64; c += 16)
+                    if (warp / 4 * 64 + c < cols) {
+                        float v[16];
+                        tmem_load16(tmem + ((warp % 4) << 21) + (r & 1) * 128 + warp / 4 * 64 + c, v);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) sum[c + k] += v[k];
+                    }
+                tc_fence_before();
+            }
+            __syncthreads();                      // (the run after the next writes this half)
         }
-    }
-    if (P.splits > 1) {
-        cluster_arrive();
-        cluster_wait();
-    } else {
+        if (!ok) {
+            atomicOr(P.status, K3HUF_ST_TIMEOUT);
+            // copies still in flight, if any, land first
+            if (tid == 32)
+                for (uint32_t i = loaded > kShrinkStages ? loaded - kShrinkStages : 0; i < loaded; ++i) mbar_wait(smem_addr(&s_full[(step0 + i) % kShrinkStages]), (step0 + i) / kShrinkStages & 1);
+        }
         __syncthreads();
-    }
-    // a share of the tile's tokens per split: sum over the splits, scale, parts; zeros for the
-    // rank's padding (whose columns of D hold the next adapter's)
-    const uint32_t r0 = kTile * split / P.splits, r1 = kTile * (split + 1) / P.splits;
-    for (uint32_t i = r0 * rp + tid; i < r1 * rp; i += kThreads) {
-        const uint32_t t = i / rp, j = i % rp;
-        const int32_t of = tile.of[t];
-        if (of < int32_t(a0) || of >= int32_t(a0 + na)) continue;
-        float total = 0.f;
-        if (j < P.rank)
-            for (uint32_t q = 0; q < P.splits; ++q) total += P.splits > 1 ? cluster_load(smem_addr(part + t * stride + j), q) : part[t * stride + j];
-        __nv_bfloat16 p[3];
-        parts_of(j < P.rank ? P.scales[tile.list[of]] * total : 0.f, p);
-        for (uint32_t q = 0; q < P.parts; ++q) J.h[(q * P.n + t0 + t) * P.pitch + j] = p[q];
-    }
-    if (P.splits > 1) {
-        cluster_arrive();
-        cluster_wait();
-    } else {
-        __syncthreads();
+
+        // each token's own columns, to shared memory (odd stride: one bank per lane)
+        float *part = reinterpret_cast<float *>(smem);
+        const uint32_t stride = rp + 1;
+        {
+            const uint32_t t = warp % 4 * 32 + lane;
+            const int32_t of = tile.of[t];
+#pragma unroll
+            for (uint32_t c = 0; c < 64; c += 16) {
+                const uint32_t q = warp / 4 * 64 + c;
+                if (q < cols && of == int32_t(a0 + q / rp))
+#pragma unroll
+                    for (uint32_t k = 0; k < 16; ++k) part[t * stride + q % rp + k] = sum[c + k];
+            }
+        }
+        if (P.splits > 1) {
+            cluster_arrive();
+            cluster_wait();
+        } else {
+            __syncthreads();
+        }
+        // a share of the tile's tokens per split: sum over the splits, scale, parts; zeros for the
+        // rank's padding (whose columns of D hold the next adapter's)
+        const uint32_t r0 = kTile * split / P.splits, r1 = kTile * (split + 1) / P.splits;
+        for (uint32_t i = r0 * rp + tid; i < r1 * rp; i += kThreads) {
+            const uint32_t t = i / rp, j = i % rp;
+            const int32_t of = tile.of[t];
+            if (of < int32_t(a0) || of >= int32_t(a0 + na)) continue;
+            float total = 0.f;
+            if (j < P.rank)
+                for (uint32_t q = 0; q < P.splits; ++q) total += P.splits > 1 ? cluster_load(smem_addr(part + t * stride + j), q) : part[t * stride + j];
+            __nv_bfloat16 p[3];
+            parts_of(j < P.rank ? P.scales[tile.list[of]] * total : 0.f, p);
+            for (uint32_t q = 0; q < P.parts; ++q) J.h[(q * P.n + t0 + t) * P.pitch + j] = p[q];
+        }
+        fence_async_shared();                     // (the next group's copies overwrite what was read here)
+        if (P.splits > 1) {
+            cluster_arrive();
+            cluster_wait();
+        } else {
+            __syncthreads();
+        }
     }
     if (warp == 0) tmem_free(tmem, 256);
 }
@@ -874,7 +876,9 @@ int launch_shrink(ShrinkParams &P, uint32_t jobs, uint64_t sms, cudaStream_t str
     P.splits = 1;
     while (P.splits < kMaxSplits && tiles * jobs * P.splits * 2 <= 2 * sms && steps >= 8 * P.splits) P.splits *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(uint32_t(tiles * P.splits), groups, jobs);
+    // clusters per tile: as many as its groups may be, but no more than fill the GPU
+    const uint64_t clusters = tiles * P.splits * jobs;
+    cfg.gridDim = dim3(uint32_t(tiles * P.splits), std::min<uint32_t>(groups, uint32_t((2 * sms + clusters - 1) / clusters)), jobs);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kShrinkSmem;
     cfg.stream = stream;
