@@ -491,7 +491,8 @@ int k3huf_embed_layer(const void *h_layer_hdr, size_t hdr_bytes, const void *d_l
  * are added to grad and the other rows are left alone.
  *  d_dy: n_tokens rows of `cols` elements of dy_type, dy_stride apart;
  *  d_grad: rows x cols floats, contiguous;
- *  d_scratch: k3huf_embed_grad_scratch_bytes(...) bytes. */
+ *  d_scratch: k3huf_embed_grad_scratch_bytes(...) bytes.
+ * Up to 2^31 - 1 tokens and rows, and 2^26 columns. */
 int k3huf_embed_grad_scratch_bytes(uint64_t n_tokens, uint64_t rows, uint64_t cols, size_t *scratch_bytes);
 int k3huf_embed_grad(const void *d_ids, uint32_t id_bytes, uint64_t n_tokens, const void *d_dy, uint32_t dy_type,
                      uint64_t dy_stride, uint64_t rows, uint64_t cols, float scale, float *d_grad, void *d_scratch,
@@ -501,7 +502,8 @@ int k3huf_embed_grad(const void *d_ids, uint32_t id_bytes, uint64_t n_tokens, co
  * device: a is n_adapters x rank x cols and b is n_adapters x rank x rows,
  * bf16, contiguous (both rank-major: b holds the transpose of the output
  * factor); scales holds n_adapters floats.  Adapters of a smaller rank are
- * padded with zero rows. */
+ * padded with zero rows.  Calls take up to 2^29 - 1 tokens; n_adapters x rank,
+ * cols and rows stay below 2^31. */
 #define K3HUF_MAX_RANK 128u
 typedef struct {
     const void *a, *b;

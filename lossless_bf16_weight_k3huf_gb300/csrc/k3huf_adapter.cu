@@ -275,11 +275,12 @@ struct ShrinkParams {
 // operands K-major tiles brought by TMA, kStep of the contraction per stage;
 // every token keeps the columns of its own adapter.  CTAs: a tile of tokens x some
 // of its groups of adapters, whose rank rows fill 128 columns (a tile whose tokens
-// share adapters has one or two groups), x a split of the contraction; the splits are a cluster, whose partial sums meet through shared
-// memory in the order of the splits.  One thread keeps the products and one the
+// share adapters has one or two groups), x a split of the contraction; the splits
+// are a cluster, whose partial sums meet through shared memory in the order of
+// the splits.  One thread keeps the products and one the
 // copies going for a run of kRun steps while the CTA moves the run before it from
 // the other half of TMEM to registers.  Bound by the read of V (and of the factors
-// when every token has its own).
+// when every token has its own): 30 us for 8192 tokens x 8192 to rank 64, 4.5 TB/s.
 constexpr uint32_t kShrinkStages = 3, kShrinkStage = 2 * kTileBytes;
 constexpr size_t kShrinkSmem = kShrinkStages * kShrinkStage + 1024;
 constexpr uint32_t kMaxSplits = 8;
@@ -440,8 +441,8 @@ struct ExpandParams {
 // CTAs: a tile of tokens x a range of column tiles; a step is one adapter of
 // one column tile.  Warps 0 to 7 add; a thread of warp 8 issues the products, two
 // steps ahead of the additions; one of warp 9 brings the base and takes y away;
-// one of warp 10 brings W.  Bound by the read of the base and the write of y: 158 us for
-// 8192 tokens x 24576 bf16 columns, 5.1 TB/s.  (With columns as the lanes, 2 bytes
+// one of warp 10 brings W.  Bound by the read of the base and the write of y: 144 us for
+// 8192 tokens x 24576 bf16 columns, 5.6 TB/s.  (With columns as the lanes, 2 bytes
 // at a time, the additions took five times the instructions, 184 us.)
 constexpr uint32_t kExpandThreads = kThreads + 96;
 template <typename T, uint32_t kBlocks> struct Expand {       // kBlocks: blocks of 64 rank rows
@@ -653,7 +654,8 @@ struct OuterParams {
 // adapter, 64 of them per step, gathered by their indexes: both operands lie
 // token by token, so both are read MN-major.  CTAs: a tile of columns (of
 // either gradient) x an adapter; the tokens' indexes come from the ids,
-// kWindow at a time, in order.  Bound by the read of V.
+// kWindow at a time, in order.  Bound by the read of V, in pieces of 256 bytes:
+// 35 us for 4096 tokens x 32 x (8192 + 8192) of 4 adapters, 3.8 TB/s.
 //
 // Ranks up to 32 (kBlocks 0) stage the parts side by side and multiply them at
 // once into columns of their own, which takes a third of the products and
@@ -832,10 +834,11 @@ uint64_t h_bytes(uint64_t n, uint32_t rank) { return align_up(n * 2 * kMaxParts 
 enum class Form { any, few, many };
 bool rows16(const void *p, uint64_t stride, uint32_t type) { return aligned_to(p, 16) && stride * elem_bytes(type) % 16 == 0; }
 // Few tokens: each reads its factor rows on its own, at about 10 TB/s from L2.
-// Per call, few and many, fp32 and bf16 results: 256 tokens x 64 x (4096 +
-// 4096), 268 MB, 27 us and 31 or 30; 250 x 32 x (8192 + 8192) of 64 adapters,
-// 262 MB, 42 or 39 and 152 or 91; 1000 x 32 x (4096 + 4096) of 32 adapters, 524
-// MB, 48 and 59 or 41; 2000 x 16 x (8192 + 8192), 1 GB, 118 or 113 and 69 or 46.
+// Per call, few and many, fp32 or bf16 results: 128 tokens x 32 x (8192 + 8192)
+// of 32 adapters, 134 MB, 19 us and 50 or 48; 256 x 64 x (4096 + 4096) of 8, 268
+// MB, 27 us both; 250 x 32 x (8192 + 8192) of 64, 262 MB, 42 or 39 and 115 or 72;
+// 1000 x 32 x (4096 + 4096) of 32, 524 MB, 48 and 48 or 34; 2000 x 16 x (8192 +
+// 8192) of 8, 1 GB, 118 or 113 and 60 or 39.
 Form run_form(uint64_t n, const k3huf_adapters_t *ad, bool rows_ok) {
     return !rows_ok ? Form::any : n <= 65535 && n * ad->rank * (ad->cols + ad->rows) * 2 <= kFewBytes ? Form::few : Form::many;
 }

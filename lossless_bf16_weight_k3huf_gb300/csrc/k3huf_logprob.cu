@@ -10,28 +10,30 @@
 //   dx_j = s (g (1[j = token] - p_j) - h p_j (log p_j + entropy))
 // Logits of -infinity take no part (p_j = 0).
 //
-// Forward, one read of the logits: a CTA of 256 threads streams a row (or, when
-// there are fewer rows than the GPU holds CTAs, the CTAs of a cluster take a
+// Forward, one read of the logits: a CTA (128 threads, 256 for the largest
+// vocabularies) streams a row (or, when there are fewer rows than the GPU holds CTAs, the CTAs of a cluster take a
 // slice each and their results meet in the first one's shared memory).  Every
 // thread keeps a running maximum with sum and dot rescaled to it (in base 2);
 // 4 x 16 bytes per thread and step, the next step's loads issued before this
 // one's arithmetic.  What bounds it: the read of the logits from HBM; per
-// value one exponential and about six more instructions, half of them paired.
+// value one exponential and about six more instructions, half of them paired:
+// 4095 rows of 131072 bf16 175 us, 6.1 TB/s;
+// 277 us with 20 alternatives.
 //
 // Top alternatives in the same pass: a value can only be among the `top`
 // largest if it is not below the top-th largest of any set of values.  The
 // first step takes the top-th largest of 64 groups' largest values as the
 // threshold (bit by bit within a warp); from then on a thread notes the vectors
 // whose largest value reaches the threshold, without a barrier, and after steps
-// 1, 4, 16, ... the CTA reads the noted vectors
-// again, one value per thread, lists the keys that reach the threshold and cuts
-// the list to its `top` largest, the last of which is the new threshold.  Rows
-// that keep growing can fill the notes (ascending values): such a row's
+// 1, 4, 16, ... the CTA reads the noted vectors again, one value per thread, lists
+// the keys that reach the threshold and cuts the list to its `top` largest, the
+// last of which is the new threshold.  Rows that keep growing can fill the notes (ascending values): such a row's
 // alternatives are taken again in a second read that counts and raises the
 // threshold at every step.  A value's order as a whole number with its index
 // below it is one key, so ties need no more.
 //
-// Backward: elementwise, 16 bytes per thread and load, one read and one write.
+// Backward: elementwise, 16 bytes per thread and load, one read and one write,
+// at the rate of a copy: 2047 rows of 131072 bf16 157 us, 6.8 TB/s.
 #include <cooperative_groups.h>
 
 #include <cmath>
