@@ -171,7 +171,7 @@ struct LogprobParams {
 // notes whether keys were lost because it was full.
 template <int kThreads>
 __device__ void cut_list(uint64_t *list, uint32_t *count, uint32_t *lost, uint32_t top) {
-    constexpr int kMine = kList / kThreads;
+    constexpr int kMine = (kList + kThreads - 1) / kThreads;
     __shared__ uint32_t s_above[2];
     __syncthreads();
     const uint32_t n = min(*count, kList);

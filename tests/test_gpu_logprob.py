@@ -111,6 +111,18 @@ def test_ties_go_to_the_lower_index(dtype):
         check(x, torch.arange(6, device="cuda"), top)
 
 
+@pytest.mark.parametrize("many", [400, 1000, 2300, 2336, 2368, 2400, 2500, 4096])
+def test_many_values_above_the_first_ones(many):
+    """A part of a row that rises above all before it: up to that many candidates at once."""
+    n, V = 640, 70000
+    gen = torch.Generator("cuda").manual_seed(many)
+    x = -torch.rand(n, V, generator=gen, device="cuda")
+    x[:, 4096:4096 + many] = 1 + torch.rand(n, many, generator=gen, device="cuda").argsort(1).float() / 64
+    _, _, _, ti, _, st = forward(x, torch.zeros(n, dtype=torch.int64, device="cuda"), 20)
+    assert st == 0
+    assert torch.equal(ti.long(), torch.topk(x, 20, dim=1).indices)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_masked_rows_and_lowest_values(dtype):
     V = 5000
