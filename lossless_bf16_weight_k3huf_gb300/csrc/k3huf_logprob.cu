@@ -18,11 +18,11 @@
 // one's arithmetic.  What bounds it: the read of the logits from HBM; per
 // value one exponential and about six more instructions, half of them paired:
 // 4095 rows of 131072 bf16 175 us, 6.1 TB/s;
-// 277 us with 20 alternatives.
+// 272 us with 20 alternatives.
 //
 // Top alternatives in the same pass: a value can only be among the `top`
 // largest if it is not below the top-th largest of any set of values.  The
-// first step takes the top-th largest of 64 groups' largest values as the
+// first step takes the top-th largest of 64 or 128 groups' largest values as the
 // threshold (bit by bit within a warp); from then on a thread notes the vectors
 // whose largest value reaches the threshold, without a barrier, and after steps
 // 1, 4, 16, ... the CTA reads the noted vectors again, one value per thread, lists
@@ -225,12 +225,17 @@ __device__ void cut_list(uint64_t *list, uint32_t *count, uint32_t *lost, uint32
     __syncthreads();
 }
 
-template <typename T, bool kTop, int kThreads>
+// kTop: 0 without alternatives, 1 for up to kNarrow (the first threshold is taken
+// from 64 groups of threads), 2 for more (from 128; the 64th largest of 64 would be
+// the smallest, and let 300 of a step's values through instead of 90: 1000 rows
+// of 131072 with 64 alternatives 168 and 115 us, of 32000 124 and 60).
+constexpr uint32_t kNarrow = 24;
+template <typename T, int kTop, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(const LogprobParams P) {
     constexpr int E = kPer<T>, kWarps = kThreads / 32;
     constexpr uint32_t kMaxNotes = kNotes<kThreads>;
     __shared__ State s_part[kWarps], s_all[kMaxCluster];
-    __shared__ uint32_t s_count, s_noted, s_lost, s_counts[kMaxCluster], s_notes[kTop ? kMaxNotes : 1], s_group[kTop ? 64 : 1];
+    __shared__ uint32_t s_count, s_noted, s_lost, s_counts[kMaxCluster], s_notes[kTop ? kMaxNotes : 1], s_group[kTop ? 64 * kTop : 1];
     __shared__ uint64_t s_list[kTop ? kList : 1];
     extern __shared__ uint64_t s_sent[];                   // (of the other CTAs of a cluster)
     const cg::cluster_group cluster = cg::this_cluster();
@@ -271,17 +276,22 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
         bool raised = false;
         uint64_t t = 0;
         if (first) {
-            // the top-th largest of the largest values of 64 groups of threads
-            constexpr int kGroup = kThreads / 64;
+            // the top-th largest of the largest values of 64 or 128 groups of threads
+            constexpr int kSets = kTop ? 2 * kTop : 1, kGroup = kThreads / (32 * kSets);
             uint32_t most = mine;
 #pragma unroll
             for (int d = 1; d < kGroup; d <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
             if (tid % kGroup == 0) s_group[tid / kGroup] = most;
             __syncthreads();
-            const uint32_t a = s_group[lane], b = s_group[lane + 32];
-            uint32_t hi = 0;
-            for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1)
-                if (uint32_t(__popc(__ballot_sync(0xffffffffu, a >= (hi | bit))) + __popc(__ballot_sync(0xffffffffu, b >= (hi | bit)))) >= P.top) hi |= bit;
+            uint32_t g[kSets], hi = 0;
+#pragma unroll
+            for (int i = 0; i < kSets; ++i) g[i] = s_group[lane + 32 * i];
+            for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1) {
+                uint32_t above = 0;
+#pragma unroll
+                for (int i = 0; i < kSets; ++i) above += __popc(__ballot_sync(0xffffffffu, g[i] >= (hi | bit)));
+                if (above >= P.top) hi |= bit;
+            }
             t = uint64_t(hi) << 32;
             raised = true;
         } else if (count && uint32_t(__syncthreads_count(reaches(threshold))) > few) {
@@ -529,7 +539,7 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const GradPa
     }
 }
 
-template <typename T, bool kTop, int kThreads>
+template <typename T, int kTop, int kThreads>
 int launch_forward(const LogprobParams &P, uint32_t n, cudaStream_t stream) {
     // one CTA per row, or a cluster per row while the GPU has room for more CTAs (two or
     // more per SM) and every CTA still has a step to do
@@ -558,9 +568,14 @@ int launch_forward(const LogprobParams &P, uint32_t n, cudaStream_t stream) {
 // 35 and 52 us at 4096, 115 and 117 at 32768, 177 both at 65536, 289 and 279 at
 // 131072; without alternatives 19 and 29, 54 and 60, 93 and 98, 177 and 175.
 constexpr uint32_t kSmallVocab = 65536;
-template <typename T, bool kTop>
+template <typename T, int kTop>
 int launch_forward(const LogprobParams &P, uint32_t n, cudaStream_t stream) {
     return P.vocab <= kSmallVocab ? launch_forward<T, kTop, 128>(P, n, stream) : launch_forward<T, kTop, 256>(P, n, stream);
+}
+
+template <typename T>
+int launch_forward(const LogprobParams &P, uint32_t n, cudaStream_t stream) {
+    return P.top == 0 ? launch_forward<T, 0>(P, n, stream) : P.top <= kNarrow ? launch_forward<T, 1>(P, n, stream) : launch_forward<T, 2>(P, n, stream);
 }
 
 template <typename T>
@@ -607,8 +622,8 @@ extern "C" int k3huf_token_logprobs(const void *d_logits, uint32_t type, uint64_
     const LogprobParams P{d_logits, d_tokens, d_logprob, d_entropy, d_lse, d_top_logprobs, d_top_ids, d_status, stride, vocab, id_bytes, top, scale};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (type == K3HUF_BF16)
-        return top ? launch_forward<__nv_bfloat16, true>(P, uint32_t(n), st) : launch_forward<__nv_bfloat16, false>(P, uint32_t(n), st);
-    return top ? launch_forward<float, true>(P, uint32_t(n), st) : launch_forward<float, false>(P, uint32_t(n), st);
+        return launch_forward<__nv_bfloat16>(P, uint32_t(n), st);
+    return launch_forward<float>(P, uint32_t(n), st);
 }
 
 extern "C" int k3huf_token_logprobs_grad(const void *d_logits, uint32_t type, uint64_t stride, uint64_t n, uint32_t vocab, float scale,

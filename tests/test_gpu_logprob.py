@@ -111,6 +111,20 @@ def test_ties_go_to_the_lower_index(dtype):
         check(x, torch.arange(6, device="cuda"), top)
 
 
+@pytest.mark.parametrize("top", [24, 25, 64])
+@pytest.mark.parametrize("n,V", [(700, 9000), (20, 70000), (650, 70000), (5, 64), (4, 200)])
+def test_many_alternatives(n, V, top):
+    gen = torch.Generator("cuda").manual_seed(n + V + top)
+    x = torch.rand(n, V, generator=gen, device="cuda").argsort(1).float() / V          # (no two alike)
+    _, _, _, ti, tl, st = forward(x, torch.zeros(n, dtype=torch.int64, device="cuda"), top)
+    want = torch.topk(x, top, dim=1)
+    assert st == 0
+    assert torch.equal(ti.long(), want.indices)
+    got = torch.log_softmax(x.double(), 1).gather(1, want.indices)
+    # (as in the docstring, with Z = 1 and values up to 1 + log V)
+    assert (tl - got).abs().max() <= (6 + V / 64 + 16 + 4 * (2 + np.log(V))) * E
+
+
 @pytest.mark.parametrize("many", [400, 1000, 2300, 2336, 2368, 2400, 2500, 4096])
 def test_many_values_above_the_first_ones(many):
     """A part of a row that rises above all before it: up to that many candidates at once."""
