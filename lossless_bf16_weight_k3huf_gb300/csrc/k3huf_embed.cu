@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(kEmbedThreads, 1) embed_kernel(const __grid_co
         // they follow one another in one row (row_even, row_out: this lane's place in the first of four)
         constexpr uint32_t kSub = 256;
         const bool there = q.any && !q.none && q.col >= 0 && want == (kFixed ? kSub : P.sub_syms);
-        const bool plain = __all_sync(0xffffffffu, there);
+        // (whole rounds of them: a shorter sub-stream's last round holds less than the 64 values that the join takes)
+        const bool plain = __all_sync(0xffffffffu, there) && (kFixed || P.sub_syms % kRound == 0);
         const uint8_t *row_even = nullptr;
         T *row_out = nullptr;
         if (kFixed && kVec) {

@@ -172,6 +172,26 @@ def test_on_a_stream_of_its_own():
     assert st.item() == 0 and same_bits(out.cpu(), expect(table_of(blob, 0, 1024), np.arange(100)[::-1].copy(), 1.0, torch.bfloat16))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("chunk,sub", [(4096, 32), (4096, 8), (1024, 16), (960, 96), (3000, 24)])
+def test_sub_streams_that_are_no_whole_rounds(chunk, sub, dtype):
+    """Sub-streams whose length is not a multiple of the 64 values that are decoded and stored at a time, enough of
+    them that warps take 32 whole ones at once: nothing beyond a sub-stream is written, in the rows or behind them."""
+    rows, cols = 64, 9600
+    w = workloads.normal_tensor((rows, cols), 0.02, chunk + sub)
+    blob = k3.encode_layer([w], chunk_syms=chunk, sub_syms=sub)
+    n = 200 if sub <= 32 else 600                        # 600 rows of 100 or more: over 45000 units
+    ids = np.random.default_rng(sub).integers(0, rows, n)
+    buf = torch.full(((n + 1) * cols,), 7.0, dtype=dtype, device="cuda")
+    out, st = buf[: n * cols].view(n, cols), status()
+    k3.embed_layer(blob[: k3.layer_info(blob)["hdr_bytes"]], torch.from_numpy(blob).cuda(), 0, cols, torch.as_tensor(ids).cuda(), out, st, scale=1.7)
+    torch.cuda.synchronize()
+    table = torch.from_numpy(w.view(np.int16)).view(torch.bfloat16).reshape(rows, cols)
+    assert st.item() == 0
+    assert bool((buf[n * cols:] == 7.0).all())
+    assert same_bits(out.cpu(), expect(table, ids, 1.7, dtype))
+
+
 # --- gradient -----------------------------------------------------------------
 
 def grad_of(ids, dy, rows, scale, held=None, id_dtype=torch.int64):
