@@ -1034,8 +1034,10 @@ extern "C" int k3huf_embed_layer(const void *h_layer_hdr, size_t hdr_bytes, cons
     P.rows = te.n_values / cols;
     P.cols = cols;
     P.out_stride = out_stride;
-    P.chunk_syms = L.info.chunk_syms;
-    P.sub_syms = L.info.sub_syms;
+    // (a chunk is no longer than its stripe: the same layout, and sums with it stay in 32 bits; such chunks
+    // are one sub-stream each)
+    P.chunk_syms = std::min(L.info.chunk_syms, K3HUF_STRIPE_VALUES);
+    P.sub_syms = std::min(L.info.sub_syms, P.chunk_syms);
     P.id_bytes = id_bytes;
     P.n_stripes = te.n_stripes;
     P.table = te.table;

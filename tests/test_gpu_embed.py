@@ -192,6 +192,18 @@ def test_sub_streams_that_are_no_whole_rounds(chunk, sub, dtype):
     assert same_bits(out.cpu(), expect(table, ids, 1.7, dtype))
 
 
+@pytest.mark.parametrize("chunk", [(1 << 25) + 1, 1 << 31, (1 << 32) - (1 << 25), (1 << 32) - (1 << 25) + 1, (1 << 32) - 1])
+def test_chunks_longer_than_a_stripe(chunk):
+    """One chunk and one sub-stream per stripe, up to the largest chunk size that the header holds."""
+    w = workloads.normal_tensor((10, 64), 0.02, 17)
+    blob = oracle.encode_layer([w], chunk_syms=chunk, sub_syms=256)
+    ids = [9, 0, 3, -1, 3]
+    for dtype in (torch.bfloat16, torch.float32):
+        got, st = lookup(blob, 0, 64, ids, scale=0.5, dtype=dtype)
+        assert st == 0
+        assert same_bits(got, expect(table_of(blob, 0, 64), ids, 0.5, dtype))
+
+
 # --- gradient -----------------------------------------------------------------
 
 def grad_of(ids, dy, rows, scale, held=None, id_dtype=torch.int64):
