@@ -99,10 +99,15 @@ outer_any_kernel(const float *h, const __nv_bfloat16 *v, uint64_t stride, const 
     for (uint64_t row = blockIdx.y; row < uint64_t(n_adapters) * rank; row += gridDim.y) {
         const uint32_t i = uint32_t(row / rank), r = uint32_t(row % rank);
         float acc = 0.f;
+        bool used = false;
         for (uint64_t t = 0; t < n; ++t)
-            if (ids[t] == int32_t(i)) acc = fmaf(h[t * rank + r], ld_f32(v + t * stride + c), acc);
+            if (ids[t] == int32_t(i)) {
+                acc = fmaf(h[t * rank + r], ld_f32(v + t * stride + c), acc);
+                used = true;
+            }
         float *out = g + row * len + c;
-        *out = add ? *out + acc : acc;
+        // (adapters without a token are left alone: another call may be adding to them)
+        if (used || !add) *out = add ? *out + acc : acc;
     }
 }
 
@@ -797,9 +802,10 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
             step += steps;
         }
         if (step != first) drain((step - first - 1) / kRun);
-        // lane: column; a warp's stores of one rank row are 128 adjacent bytes
+        // lane: column; a warp's stores of one rank row are 128 adjacent bytes.  (Added to: adapters
+        // without a token are left alone, another call may be adding to them)
         const uint32_t c = col + warp % 4 * 32 + lane;
-        if (c < J.len)
+        if (c < J.len && (step != first || !P.add))
 #pragma unroll
             for (uint32_t b = 0; b < O::pieces; ++b)
 #pragma unroll

@@ -307,3 +307,27 @@ def test_refusals():
     with pytest.raises(ValueError):
         k3.adapter_grad(*args, s["dy"], torch.empty(2, 8, 64, device="cuda"), torch.empty(2, 8, 32, device="cuda"), scratch_for(s, True), st,
                         dx_base=torch.empty(4, 64, device="cuda"))
+
+
+@pytest.mark.parametrize("rank", [16, 33, 96, 5])
+def test_accumulating_leaves_unused_adapters_alone(rank):
+    """Adapters without a token keep every bit of what is held (-0 too, which adding 0 would make +0), whatever the
+    form; those with one get held + their sum."""
+    S, n, cols, rows = 9, 300, 264, 328
+    s = make(n, S, rank, cols, rows, rank)
+    s["ids"] = torch.where(s["ids"] % 4 == 1, s["ids"], torch.full_like(s["ids"], -1))         # adapters 1 and 5
+    wide_x = torch.zeros(n, cols + 1, dtype=torch.bfloat16, device="cuda")
+    wide_x[:, 1:] = s["x"]
+    for x in (s["x"], wide_x[:, 1:]):                    # on 16 bytes, and not
+        s["x"] = x
+        held = tuple(torch.randn(s[k].shape, device="cuda") for k in ("a", "b"))
+        for h in held:
+            h[:, :, ::3] = -0.0
+        da, db, _, st = grads(s, held=held, want_dx=False)
+        ra, rb, _ = grad_reference(s, held=held)
+        assert st == 0 and close(da, ra) and close(db, rb)
+        unused = [i for i in range(S) if i not in (1, 5)]
+        for got, h in ((da, held[0]), (db, held[1])):
+            assert torch.equal(got[unused].view(torch.int32), h[unused].view(torch.int32))
+        da, db, _, st = grads(s, want_dx=False)          # not accumulating, they get zeros
+        assert st == 0 and bool((da[unused] == 0).all()) and bool((db[unused] == 0).all())
