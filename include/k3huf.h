@@ -503,7 +503,10 @@ int k3huf_embed_grad(const void *d_ids, uint32_t id_bytes, uint64_t n_tokens, co
  * bf16, contiguous (both rank-major: b holds the transpose of the output
  * factor); scales holds n_adapters floats.  Adapters of a smaller rank are
  * padded with zero rows.  Calls take up to 2^29 - 1 tokens; n_adapters x rank,
- * cols and rows stay below 2^31. */
+ * cols and rows stay below 2^31.  A rank-wide intermediate that overflows is an
+ * infinity, as the formula's; where a factor, x or dy holds an infinity, the
+ * results that it takes part in are infinite or NaN (never another adapter's or
+ * another token's). */
 #define K3HUF_MAX_RANK 128u
 typedef struct {
     const void *a, *b;

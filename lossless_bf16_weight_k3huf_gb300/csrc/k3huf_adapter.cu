@@ -18,6 +18,7 @@
 // sum of bf16 parts: three parts (24 bits) where the result is fp32, two (16
 // bits) where it is rounded to bf16.
 #include <algorithm>
+#include <cmath>
 
 #include "k3huf_tc.h"
 
@@ -254,10 +255,13 @@ __device__ uint32_t tile_adapters(TileAdapters &s, const int32_t *ids, uint64_t 
     return count;
 }
 
-// x as a sum of bf16 parts
+// x as a sum of bf16 parts.  A finite one that would round to an infinity starts with the largest
+// bf16 instead, whose rest the other parts hold; an infinity is the first part and zeros.
 __device__ __forceinline__ void parts_of(float x, __nv_bfloat16 (&p)[3]) {
-    p[0] = __float2bfloat16_rn(x);
-    const float a = x - __bfloat162float(p[0]);
+    const float most = __uint_as_float(0x7F7F0000u);          // the largest bf16
+    const bool infinite = fabsf(x) == INFINITY;
+    p[0] = __float2bfloat16_rn(fabsf(x) > most && !infinite ? copysignf(most, x) : x);
+    const float a = infinite ? 0.f : x - __bfloat162float(p[0]);
     p[1] = __float2bfloat16_rn(a);
     p[2] = __float2bfloat16_rn(a - __bfloat162float(p[1]));
 }

@@ -331,3 +331,61 @@ def test_accumulating_leaves_unused_adapters_alone(rank):
             assert torch.equal(got[unused].view(torch.int32), h[unused].view(torch.int32))
         da, db, _, st = grads(s, want_dx=False)          # not accumulating, they get zeros
         assert st == 0 and bool((da[unused] == 0).all()) and bool((db[unused] == 0).all())
+
+
+@pytest.mark.parametrize("form", ["few", "tiles", "any"])
+def test_intermediates_beyond_the_largest_bf16(form):
+    """A rank-wide intermediate that overflows fp32 is an infinity, and so is what it gives with finite factors; one
+    between the largest bf16 and the largest fp32 value is finite, and so is what it gives."""
+    n, S, r, cols, rows = (2100, 3, 64, 1024, 1032) if form == "tiles" else (40, 3, 64, 1024, 1032)
+    s = make(n, S, r, cols, rows, 77)
+    s["scales"].fill_(1.0)
+    s["ids"][5], s["ids"][6] = 1, 2
+    # token 5: 2^120 2^10; token 6: 2^127 (2 - 2^-7 + 2^-8 + 2^-9), rounded to bf16 an infinity
+    s["x"][5], s["x"][6] = 0, 0
+    s["a"][1, :, 0], s["a"][2, :, :3] = 0, 0
+    s["x"][5, 0], s["a"][1, 0, 0] = 2.0 ** 120, 2.0 ** 10
+    s["x"][6, :3] = 2.0 ** 127
+    s["a"][2, 0, :3] = torch.tensor([2 - 2.0 ** -7, 2.0 ** -8, 2.0 ** -9], device="cuda").to(torch.bfloat16)
+    s["b"][2] *= 2.0 ** -100
+    s["b"][1][s["b"][1] == 0] = 1.0                      # (0 times infinity is NaN)
+    s["dy"][5], s["dy"][6] = 0, 0
+    if form == "any":
+        wide = torch.zeros(n, cols + 1, dtype=torch.bfloat16, device="cuda")
+        wide[:, 1:] = s["x"]
+        s["x"] = wide[:, 1:]
+    for dtype in (torch.float32, torch.bfloat16):
+        y = torch.full((n, rows), float("nan"), device="cuda", dtype=dtype)
+        assert apply(s, y) == 0
+        assert torch.equal(y[5].float(), torch.sign(s["b"][1, 0].float()) * float("inf"))
+        want = float(np.float32(2.0 ** 127 * (2 - 2.0 ** -9))) * s["b"][2, 0].double()
+        # (the other rank rows' factors are 0 times theirs)
+        got = y[6].double()
+        assert bool(((got - want).abs() <= (2.0 ** -15 + rounding(dtype)) * want.abs()).all())
+    # the same in the gradients: dh of token 5 overflows, of token 6 lies in between
+    s = make(n, S, r, cols, rows, 78)
+    s["scales"].fill_(1.0)
+    s["ids"][s["ids"] == 1] = 0                          # token 5 alone has adapter 1, token 6 adapter 2
+    s["ids"][s["ids"] == 2] = 0
+    s["ids"][5], s["ids"][6] = 1, 2
+    s["dy"][5], s["dy"][6] = 0, 0
+    s["b"][1, :, 0], s["b"][2, :, :3] = 0, 0
+    s["dy"][5, 0], s["b"][1, 0, 0] = 2.0 ** 120, 2.0 ** 10
+    s["dy"][6, :3] = 2.0 ** 127
+    s["b"][2, 0, :3] = torch.tensor([2 - 2.0 ** -7, 2.0 ** -8, 2.0 ** -9], device="cuda").to(torch.bfloat16)
+    s["a"][2] *= 2.0 ** -100
+    s["x"][6] *= 2.0 ** -100
+    s["a"][1][s["a"][1] == 0] = 1.0
+    s["x"][5][s["x"][5] == 0] = 1.0
+    if form == "any":
+        wide = torch.zeros(n, cols + 1, dtype=torch.bfloat16, device="cuda")
+        wide[:, 1:] = s["x"]
+        s["x"] = wide[:, 1:]
+    da, db, dx, st = grads(s)
+    dh = float(np.float32(2.0 ** 127 * (2 - 2.0 ** -9)))
+    assert st == 0
+    assert torch.equal(dx[5], torch.sign(s["a"][1, 0].float()) * float("inf"))
+    assert torch.equal(da[1, 0], torch.sign(s["x"][5].float()) * float("inf")) and bool((da[1, 1:] == 0).all())
+    for got, factor in ((dx[6], s["a"][2, 0]), (da[2, 0], s["x"][6])):
+        want = dh * factor.double()
+        assert bool(((got.double() - want).abs() <= 2.0 ** -15 * want.abs()).all())
