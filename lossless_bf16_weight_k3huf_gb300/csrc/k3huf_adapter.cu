@@ -115,6 +115,7 @@ outer_any_kernel(const float *h, const __nv_bfloat16 *v, uint64_t stride, const 
 // --- few tokens ---------------------------------------------------------------
 
 constexpr int kRows = 4;                      // factor rows per CTA
+constexpr uint32_t kFewCols = 512;            // columns of y per CTA
 
 // h[t, r] = s_i v[t] . w[i, r], zero without an adapter, for kRows rows r: one
 // CTA per token and group of rows, 16-byte loads.  At 4 tokens x 16 x 8192 it
@@ -161,14 +162,14 @@ shrink_few_kernel(const __nv_bfloat16 *v, uint64_t stride, const __nv_bfloat16 *
     }
 }
 
-// y[t] = base[t] + sum_r h[t, r] w[i, r]: one CTA per token and 512 columns,
+// y[t] = base[t] + sum_r h[t, r] w[i, r]: one CTA per token and kFewCols columns,
 // four per thread.
 template <typename T>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kFewCols / 4)
 expand_few_kernel(const float *h, const __nv_bfloat16 *w, const int32_t *ids, uint32_t n_adapters, uint32_t rank, uint32_t len, const T *base, uint64_t base_stride, T *y, uint64_t y_stride) {
     __shared__ float s_h[K3HUF_MAX_RANK];
     const uint64_t t = blockIdx.x;
-    const uint32_t c = blockIdx.y * 512 + threadIdx.x * 4;
+    const uint32_t c = blockIdx.y * kFewCols + threadIdx.x * 4;
     grid_dep_wait();
     int32_t i;
     const bool any = adapter_of(ids, t, n_adapters, i);
@@ -849,8 +850,11 @@ bool rows16(const void *p, uint64_t stride, uint32_t type) { return aligned_to(p
 // MB, 27 us both; 250 x 32 x (8192 + 8192) of 64, 262 MB, 42 or 39 and 115 or 72;
 // 1000 x 32 x (4096 + 4096) of 32, 524 MB, 48 and 48 or 34; 2000 x 16 x (8192 +
 // 8192) of 8, 1 GB, 118 or 113 and 60 or 39.
+// (A grid's second dimension takes 65535 blocks: more rows than that many blocks of
+// kFewCols run as many tokens.)
 Form run_form(uint64_t n, const k3huf_adapters_t *ad, bool rows_ok) {
-    return !rows_ok ? Form::any : n <= 65535 && n * ad->rank * (ad->cols + ad->rows) * 2 <= kFewBytes ? Form::few : Form::many;
+    const bool few = n <= 65535 && n * ad->rank * (ad->cols + ad->rows) * 2 <= kFewBytes && (ad->rows + kFewCols - 1) / kFewCols <= 65535;
+    return !rows_ok ? Form::any : few ? Form::few : Form::many;
 }
 
 // A launch that may begin while the kernel before it ends (its blocks wait for that one themselves).
@@ -995,10 +999,10 @@ extern "C" int k3huf_adapter_apply(const k3huf_adapters_t *ad, const void *d_x, 
             shrink_few_kernel<<<dim3(n, (r + kRows - 1) / kRows), kThreads, 0, st>>>(x, x_stride, a, ad->scales, d_ids, S, r, uint32_t(ad->cols), h, d_status);
             const int rc = cuda_rc(cudaGetLastError());
             if (rc) return rc;
-            const dim3 grid(n, uint32_t((ad->rows + 511) / 512));
+            const dim3 grid(n, uint32_t((ad->rows + kFewCols - 1) / kFewCols));
             if (y_type == K3HUF_BF16)
-                return launch_after(expand_few_kernel<__nv_bfloat16>, grid, 128, 0, st, h, b, d_ids, S, r, uint32_t(ad->rows), static_cast<const __nv_bfloat16 *>(d_base), base_stride, static_cast<__nv_bfloat16 *>(d_y), y_stride);
-            return launch_after(expand_few_kernel<float>, grid, 128, 0, st, h, b, d_ids, S, r, uint32_t(ad->rows), static_cast<const float *>(d_base), base_stride, static_cast<float *>(d_y), y_stride);
+                return launch_after(expand_few_kernel<__nv_bfloat16>, grid, kFewCols / 4, 0, st, h, b, d_ids, S, r, uint32_t(ad->rows), static_cast<const __nv_bfloat16 *>(d_base), base_stride, static_cast<__nv_bfloat16 *>(d_y), y_stride);
+            return launch_after(expand_few_kernel<float>, grid, kFewCols / 4, 0, st, h, b, d_ids, S, r, uint32_t(ad->rows), static_cast<const float *>(d_base), base_stride, static_cast<float *>(d_y), y_stride);
         }
         case Form::many: break;
     }

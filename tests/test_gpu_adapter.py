@@ -389,3 +389,24 @@ def test_intermediates_beyond_the_largest_bf16(form):
     for got, factor in ((dx[6], s["a"][2, 0]), (da[2, 0], s["x"][6])):
         want = dh * factor.double()
         assert bool(((got.double() - want).abs() <= 2.0 ** -15 * want.abs()).all())
+
+
+def test_more_rows_than_a_grid_has_column_blocks():
+    """One token and 34 million rows: few enough factor bytes for the form of few tokens, whose grid takes 65535
+    blocks of 512 rows."""
+    rows = 65535 * 512 + 8
+    s = make(1, 1, 1, 8, 8, 3)
+    s["ids"].fill_(0)
+    s["b"] = (torch.arange(rows, device="cuda") % 251 - 125).to(torch.bfloat16).view(1, 1, rows)
+    h = float((s["x"].double() @ s["a"][0].double().T * s["scales"].double()[0]).item())
+    for dtype in (torch.float32, torch.bfloat16):
+        y = torch.full((1, rows), float("nan"), device="cuda", dtype=dtype)
+        st = status()
+        k3.adapter_apply(s["x"], s["a"], s["b"], s["ids"], s["scales"], y, scratch_for(s), st)
+        torch.cuda.synchronize()
+        want = s["b"][0].double() * h
+        assert st.item() == 0
+        # (eight products; see the docstring at the top)
+        scale = float(s["scales"][0].double() * (s["x"].double().abs() @ s["a"][0].double().abs().T).item())
+        tol = s["b"][0].double().abs() * ((slack(8) + slack(1)) * scale + 2.0 ** -15 * abs(h)) + rounding(dtype) * want.abs()
+        assert bool(((y.double() - want).abs() <= tol).all())
