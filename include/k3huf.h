@@ -560,6 +560,9 @@ int k3huf_token_logprobs(const void *d_logits, uint32_t type, uint64_t stride, u
  * gradient of the log probability (not read for "none") and h that of the
  * entropy (d_g_entropy NULL: zero, and d_entropy is not read),
  *   dlogits[j] = scale (g (1[j = token] - p_j) - h p_j (log p_j + entropy)).
+ * p is taken as 1 at most: of a row whose largest scaled logit is beyond 2^24 in
+ * magnitude (a mask of the type's lowest value over all of it) the fp32 lse does
+ * not hold the sum, and p is some value from 0 to 1.
  *  d_lse, d_entropy: as k3huf_token_logprobs gave them;
  *  d_dlogits: of the logits' type, out_stride apart; may be d_logits itself
  *    (then out_stride = stride). */

@@ -61,10 +61,15 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 }
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t j) { return (uint64_t(order_of(x)) << 32) | (0xFFFFFFFFu - j); }
 
-// max that keeps a NaN
+// max and min that keep a NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -478,12 +483,14 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const GradPa
     const float g = scored ? P.g_logprob[row] : 0.f;
     const float h = P.g_entropy ? P.g_entropy[row] : 0.f, ent = P.g_entropy ? P.entropy[row] : 0.f, lse = P.lse[row];
     // dx_j = p_j (hs lp_j + gs), and scale g more at the token; two values at a time.  A logit of
-    // -infinity, and one so low that p_j is 0, stop at kFloor: 0 times infinity is not 0.
+    // -infinity, and one so low that p_j is 0, stop at kFloor: 0 times infinity is not 0.  p_j is 1 at
+    // most: where logits are so large (masks of the type's lowest value in a whole row) that lse is
+    // off by more than 1, a log of p_j above 0 would give infinities.
     const float hs = -h * P.scale, gs = -P.scale * fmaf(h, ent, g), base = lse == -INFINITY ? 0.f : -lse;
     auto grad = [&](float2 v) {
         float2 lp = __ffma2_rn(v, make_float2(P.scale, P.scale), make_float2(base, base));
-        lp.x = max_nan(lp.x, kFloor);
-        lp.y = max_nan(lp.y, kFloor);
+        lp.x = min_nan(max_nan(lp.x, kFloor), 0.f);
+        lp.y = min_nan(max_nan(lp.y, kFloor), 0.f);
         const float2 a = __fmul2_rn(lp, make_float2(kLog2e, kLog2e));
         return __fmul2_rn(make_float2(exp2_fast(a.x), exp2_fast(a.y)), __ffma2_rn(make_float2(hs, hs), lp, make_float2(gs, gs)));
     };

@@ -290,3 +290,29 @@ def test_refusals():
         k3.token_logprobs_grad(x, tokens, lp, lp, x.to(torch.bfloat16), st)
     with pytest.raises(k3.K3HufError):
         k3.token_logprobs_grad(x, tokens, lp, lp, torch.empty_like(x), st, g_entropy=lp)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale", [0.8, 1.0, 1.7, 0.3])
+def test_gradient_of_rows_at_the_lowest_value(dtype, scale):
+    """Rows whose mask leaves nothing, with the type's lowest value for the mask.  lse, about -3e38, does not hold the
+    log of the count, so p is known to lie in [0, 1] only; a row that nothing is asked of has gradient 0, and no
+    gradient is beyond scale (|g| + |h| entropy + |h|)."""
+    n, V = 64, 777
+    x, tokens = logits(n, V, dtype, 5)
+    low = torch.finfo(dtype).min
+    x[:32] = low
+    if dtype == torch.float32:                           # masks near the lowest value, whose products round either way
+        x[:32] = low * torch.linspace(0.5, 1.0, 32, device="cuda")[:, None]
+    tokens[::2] = -1
+    lp, ent, lse, *_ = forward(x, tokens, 0, scale)
+    g, h = torch.full((n,), 2.0, device="cuda"), torch.full((n,), -3.0, device="cuda")
+    for hh in (None, h):
+        d, st = backward(x, tokens, lse, ent, g, hh, scale)
+        assert st == 0 and bool(d.isfinite().all())
+        if hh is None:
+            assert bool((d[::2] == 0).all())
+        room = scale * (2.0 + (3.0 * (ent.double() + 1) if hh is not None else 0.0)) * (1 + 2.0 ** -8)
+        assert bool((d.double().abs() <= (room[:, None] if hh is not None else room)).all())
+    want, tol = backward_ref(x[32:], tokens[32:], lse[32:], ent[32:], g[32:], h[32:], scale)
+    assert bool(((d[32:].double() - want).abs() <= tol + (2.0 ** -8 if dtype == torch.bfloat16 else E) * want.abs()).all())
