@@ -550,7 +550,7 @@ int k3huf_adapter_grad(const k3huf_adapters_t *adapters, const void *d_x, uint64
  *    d_top_logprobs, n x top.
  * Logits of -infinity have probability 0 and take no part in the entropy; a
  * row with no other logits has lse -infinity and entropy 0.  A NaN, or
- * +infinity, makes the row's statistics NaN. */
+ * +infinity, makes the row's statistics and log probabilities NaN. */
 #define K3HUF_MAX_TOP 64u
 int k3huf_token_logprobs(const void *d_logits, uint32_t type, uint64_t stride, uint64_t n, uint32_t vocab, float scale,
                          const void *d_tokens, uint32_t id_bytes, float *d_logprob, float *d_entropy, float *d_lse,

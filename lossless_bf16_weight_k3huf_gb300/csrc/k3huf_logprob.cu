@@ -429,7 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     // a row with no finite logit: sum is 0, lse -infinity
     const bool none = s.sum == 0.f;
     const float log2sum = log2f(s.sum), logsum = log2sum * kLn2;
-    auto log_prob = [&](float z) { return z == -INFINITY ? z : fmaf(z - s.m, P.scale, -logsum); };
+    // (a logit of -infinity where the sum is 0, whose log is -infinity too; a NaN sum goes on)
+    auto log_prob = [&](float z) { return z == -INFINITY && s.sum == s.sum ? z : fmaf(z - s.m, P.scale, -logsum); };
     if (tid == 0) {
         const int64_t t = ld_id(P.tokens, P.id_bytes, row);
         float lp = 0.f;

@@ -316,3 +316,21 @@ def test_gradient_of_rows_at_the_lowest_value(dtype, scale):
         assert bool((d.double().abs() <= (room[:, None] if hh is not None else room)).all())
     want, tol = backward_ref(x[32:], tokens[32:], lse[32:], ent[32:], g[32:], h[32:], scale)
     assert bool(((d[32:].double() - want).abs() <= tol + (2.0 ** -8 if dtype == torch.bfloat16 else E) * want.abs()).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [40, 3000, 70000])
+def test_a_nan_or_infinity_reaches_every_statistic(dtype, V):
+    """Also the log probability of a token whose own logit is -infinity, and those of the alternatives."""
+    x, _ = logits(4, V, dtype, 6)
+    x[:3, 1::2] = -INF
+    x[0, 5] = float("nan")
+    x[1, V // 2] = INF
+    tokens = torch.tensor([3, 3, 3, 3], device="cuda")   # (a banned one, but in the last row)
+    for top in (0, 4):
+        lp, ent, lse, ti, tl, st = forward(x, tokens, top)
+        assert st == 0
+        for v in (lp, ent, lse) + ((tl,) if top else ()):
+            assert bool(v[:2].isnan().all())
+            assert not bool(v[2:].isnan().any())
+        assert lp[2].item() == -INF
