@@ -247,7 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank(), row = blockIdx.x / C;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const T *x = static_cast<const T *>(P.x) + uint64_t(row) * P.stride;
-    const float c = P.scale * kLog2e;
+    // (finite for every scale: infinity times a difference of 0 is NaN)
+    const float c = fminf(P.scale * kLog2e, 3.402823466e38f);
     const uint32_t shift = uint32_t(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
     const uint32_t vecs = (P.vocab + shift + E - 1) / E;
     // this CTA's vectors: whole steps, as even as they come

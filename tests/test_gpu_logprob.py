@@ -334,3 +334,22 @@ def test_a_nan_or_infinity_reaches_every_statistic(dtype, V):
             assert bool(v[:2].isnan().all())
             assert not bool(v[2:].isnan().any())
         assert lp[2].item() == -INF
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_largest_scales(dtype):
+    """Any finite scale: at the largest every logit below the largest one has probability 0."""
+    x = torch.zeros(3, 500, device="cuda", dtype=dtype)
+    x[0, :] = -1.0
+    x[0, 7] = 0.0
+    x[2, 100:] = -0.5
+    tokens = torch.tensor([7, 3, 99], device="cuda")
+    for scale in (1e38, 2.4e38, 3.4e38):
+        lp, ent, lse, ti, tl, st = forward(x, tokens, 2, scale)
+        assert st == 0 and lp[0].item() == 0.0 and ent[0].item() == 0.0 and lse[0].item() == 0.0
+        for row, count in ((1, 500), (2, 100)):
+            want = np.log(count)
+            for got in (-lp[row].item(), ent[row].item(), lse[row].item()):
+                # (a sum of ones; see the docstring at the top with Z = 0)
+                assert abs(got - want) <= (4 + 500 / 64 + 32) * E * (1 + want)
+        assert ti[0].tolist() == [7, 0] and ti[1].tolist() == [0, 1]
