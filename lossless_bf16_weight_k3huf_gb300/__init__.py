@@ -183,22 +183,21 @@ def _nbytes(x) -> int:
     return int(x.numel() * x.element_size())
 
 
-_raw_stream = None
+_raw_stream = None      # torch's call for the current stream's address, once CUDA is initialised
 
 
 def _stream(stream) -> int:
     global _raw_stream
-    if _raw_stream is None:
-        import torch
-        _raw_stream = torch.cuda.is_initialized() and hasattr(torch._C, "_cuda_getCurrentRawStream")
-    if stream is None:
-        import torch
-        if _raw_stream:                                  # (the address without a Stream object: 2 us less per call)
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-        return int(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return stream
-    return int(stream.cuda_stream)
+    if stream is not None:
+        return int(stream.cuda_stream)
+    import torch
+    if _raw_stream is None and torch.cuda.is_initialized():
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if _raw_stream is not None:                          # (the address without a Stream object: 2 us less per call)
+        return _raw_stream(torch._C._cuda_getDevice())
+    return int(torch.cuda.current_stream().cuda_stream)
 
 
 # ---------------------------------------------------------------------------
