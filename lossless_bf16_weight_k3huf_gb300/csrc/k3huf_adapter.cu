@@ -380,9 +380,9 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
             }
             __syncthreads();                      // (the run after the next writes this half)
         }
-        if (!ok) {
-            atomicOr(P.status, K3HUF_ST_TIMEOUT);
-            // copies still in flight, if any, land first
+        // a wait gave up, in any thread: copies still in flight, if any, land first
+        if (!ok) atomicOr(P.status, K3HUF_ST_TIMEOUT);
+        if (__syncthreads_or(!ok)) {
             if (tid == 32)
                 for (uint32_t i = loaded > kShrinkStages ? loaded - kShrinkStages : 0; i < loaded; ++i) mbar_wait(smem_addr(&s_full[(step0 + i) % kShrinkStages]), (step0 + i) / kShrinkStages & 1);
         }
@@ -525,8 +525,10 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
     tc_fence_after();
     const uint32_t tmem = s_tmem, steps = tiles * count;
     bool ok = true;
+    uint32_t issued = 0;                      // of this thread's copies: of H, of W's stages or of the base's
     if (warp == kThreads / 32) {
         if (lane == 0 && steps) {
+            issued = 1;
             mbar_expect(smem_addr(&s_h), E::h_bytes);
             for (uint32_t q = 0; q < E::parts; ++q)
                 for (uint32_t b = 0; b < kBlocks; ++b) tma_load(h_at + (q * kBlocks + b) * kTileBytes, &P.h, int32_t(b * 64), int32_t(q * P.n + t0), smem_addr(&s_h));
@@ -567,11 +569,7 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
                     for (uint32_t b = 0; b < E::cols / 64; ++b) tma_load(at + b * E::w_block, &P.w, int32_t((c0 + i) * E::cols + b * 64), tile.list[a] * int32_t(P.rank), bar);
                     if (++stage == WS) stage = 0, round ^= 1u;
                 }
-            if (!ok)                          // copies still in flight land first
-                for (uint32_t k = 0; k < min(s, WS); ++k) {
-                    stage = stage ? stage - 1 : WS - 1;
-                    mbar_wait(smem_addr(&s_w[stage]), (s - 1 - k) / WS & 1);
-                }
+            issued = s;
         }
     } else if (warp == kThreads / 32 + 1) {
         if (lane == 0) {
@@ -581,7 +579,7 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
                 if (P.has_base)
                     for (uint32_t b = 0; b < 2; ++b) tma_load(io_at + i % IS * E::io_bytes + b * kTileBytes, &P.base, int32_t((c0 + i) * E::cols + b * E::row), int32_t(t0), bar);
             };
-            for (uint32_t i = 0; i < min(IS, tiles); ++i) load(i);
+            for (; issued < min(IS, tiles); ++issued) load(issued);
             for (uint32_t i = 0; i < tiles && ok; ++i) {
                 ok = mbar_wait(smem_addr(&s_iodone[i % IS]), i / IS & 1);
                 if (!ok) break;
@@ -590,7 +588,7 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
                 bulk_commit();
                 if (i + IS < tiles) {
                     bulk_wait_read<0>();
-                    load(i + IS);
+                    load(issued++);
                 }
             }
             bulk_wait_all();
@@ -640,7 +638,13 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
     }
     if (!ok) atomicOr(P.status, K3HUF_ST_TIMEOUT);
     tc_fence_before();
-    __syncthreads();
+    // a wait gave up, in any thread: each issuer's last copies, those of its stages, land first
+    if (__syncthreads_or(!ok)) {
+        const uint32_t stages = warp == kThreads / 32 ? 1 : warp == kThreads / 32 + 2 ? WS : IS;
+        uint64_t *bars = warp == kThreads / 32 ? &s_h : warp == kThreads / 32 + 2 ? s_w : s_io;
+        for (uint32_t i = issued > stages ? issued - stages : 0; i < issued; ++i) mbar_wait(smem_addr(&bars[i % stages]), i / stages & 1);
+        __syncthreads();
+    }
     tc_fence_after();
     if (warp == 0) tmem_free(tmem, 256);
 }
