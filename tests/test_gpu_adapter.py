@@ -410,3 +410,98 @@ def test_more_rows_than_a_grid_has_column_blocks():
         scale = float(s["scales"][0].double() * (s["x"].double().abs() @ s["a"][0].double().abs().T).item())
         tol = s["b"][0].double().abs() * ((slack(8) + slack(1)) * scale + 2.0 ** -15 * abs(h)) + rounding(dtype) * want.abs()
         assert bool(((y.double() - want).abs() <= tol).all())
+
+
+# --- the tensor-core forms where the tests above run the others: over 300 MB of factor rows -------------------------
+
+MANY = (2100, 4, 64, 1024, 1032)                         # 553 MB; a ragged last tile, rows that end inside a column tile
+
+
+@pytest.mark.parametrize("dtype,pad", [(torch.float32, 4), (torch.bfloat16, 8), (torch.float32, 64)])
+def test_tiles_in_place_strides_and_ids_past_the_pool(dtype, pad):
+    n, S, r, cols, rows = MANY
+    s = make(n, S, r, cols, rows, 81)
+    wide_x = torch.randn(n, cols + 8, device="cuda").to(torch.bfloat16)
+    s["x"] = wide_x[:, :cols]
+    wide_y = torch.randn(n, rows + pad, device="cuda").to(dtype)
+    y, before = wide_y[:, :rows], wide_y.clone()
+    past = torch.tensor([1, 130, 2099], device="cuda")
+    s["ids"][past] = torch.tensor([S, 1 << 20, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    assert apply(s, y, y) == k3.ST_TOKEN
+    want, tol = reference(s, before[:, :rows])
+    assert bool(((y.double() - want).abs() <= tol + rounding(dtype) * want.abs()).all())
+    assert torch.equal(wide_y[:, rows:], before[:, rows:])
+    assert torch.equal(y[past], before[past, :rows])
+
+
+@pytest.mark.parametrize("kind", ["one", "none"])
+def test_tiles_of_one_adapter_or_none(kind):
+    n, S, r, cols, rows = MANY
+    s = make(n, S, r, cols, rows, 82, kind)
+    for dtype in (torch.float32, torch.bfloat16):
+        base = torch.randn(n, rows, device="cuda").to(dtype)
+        for b in (base, None):
+            y = torch.full_like(base, float("nan"))
+            assert apply(s, y, b) == 0
+            want, tol = reference(s, b)
+            assert bool(((y.double() - want).abs() <= tol + rounding(dtype) * want.abs()).all())
+            if kind == "none":
+                assert torch.equal(y, base if b is not None else torch.zeros_like(base))
+
+
+@pytest.mark.parametrize("r", [64, 96, 50])
+def test_tiles_keep_adapters_apart(r):
+    """As test_no_token_meets_another_adapters_values, forward."""
+    n, S, _, cols, rows = MANY
+    good = make(n, S, r, cols, rows, 83 + r)
+    bad = {k: v.clone() for k, v in good.items()}
+    bad["a"][2, :, 7] = float("inf")
+    bad["b"][2, r - 1] = float("nan")
+    hit, none = good["ids"] == 2, good["ids"] < 0
+    bad["x"][hit] = float("nan")
+    bad["x"][none] = float("inf")
+    for dtype in (torch.float32, torch.bfloat16):
+        base = torch.randn(n, rows, device="cuda").to(dtype)
+        y, z = torch.empty_like(base), torch.empty_like(base)
+        assert apply(good, y, base) == 0 and apply(bad, z, base) == 0
+        assert torch.equal(y[~hit], z[~hit]) and torch.equal(z[none], base[none])
+
+
+def test_tiles_keep_fp32_precision():
+    """As test_fp32_result_keeps_fp32_precision: two bf16 parts of a normal intermediate are off by 2.4e-6 of it in the
+    2-norm, and so is what they give; three hold all of its 24 bits.  dx is the same product."""
+    n, S, r, cols, rows = MANY
+    s = make(n, S, r, cols, rows, 84, "runs")
+    s["ids"].clamp_(min=0)
+    y = torch.empty(n, rows, device="cuda")
+    assert apply(s, y) == 0
+    want, _ = reference(s, None)
+    assert float((y.double() - want).norm() / want.norm()) < 2e-6
+    for shape in (MANY, (300, 3, 32, 1024, 1032), (260, 2, 128, 520, 264)):
+        s = make(*shape, 85, "runs")
+        s["ids"].clamp_(min=0)
+        _, _, dx, st = grads(s)
+        want, _ = grad_reference(s)[2]
+        assert st == 0 and float((dx.double() - want).norm() / want.norm()) < 2e-6
+
+
+@pytest.mark.parametrize("dtype,pad", [(torch.float32, 4), (torch.bfloat16, 8)])
+@pytest.mark.parametrize("n,r", [(300, 16), (270, 80)])
+def test_gradients_in_place_strides_and_ids_past_the_pool(n, r, dtype, pad):
+    """dx_base is dx; rows of x, dy and dx further apart than their columns; ids past the pool, which take no part."""
+    S, cols, rows = 5, 264, 328
+    s = make(n, S, r, cols, rows, 86)
+    s["x"] = torch.randn(n, cols + 8, device="cuda").to(torch.bfloat16)[:, :cols]
+    s["dy"] = torch.randn(n, rows + 16, device="cuda").to(torch.bfloat16)[:, :rows]
+    past = torch.tensor([0, 129, n - 1], device="cuda")
+    s["ids"][past] = torch.tensor([S, 1 << 20, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    wide = torch.randn(n, cols + pad, device="cuda").to(dtype)
+    dx, before = wide[:, :cols], wide.clone()
+    da, db = (torch.full(s[k].shape, float("nan"), device="cuda") for k in ("a", "b"))
+    st = status()
+    k3.adapter_grad(s["x"], s["a"], s["b"], s["ids"], s["scales"], s["dy"], da, db, scratch_for(s, True), st, dx=dx, dx_base=dx)
+    torch.cuda.synchronize()
+    ra, rb, rx = grad_reference(s, before[:, :cols])
+    assert st.item() == k3.ST_TOKEN
+    assert close(da, ra) and close(db, rb) and close(dx, rx, dtype)
+    assert torch.equal(wide[:, cols:], before[:, cols:]) and torch.equal(dx[past], before[past, :cols])
