@@ -204,6 +204,63 @@ def test_chunks_longer_than_a_stripe(chunk):
         assert same_bits(got, expect(table_of(blob, 0, 64), ids, 0.5, dtype))
 
 
+def big_table(rows, cols, kind):
+    if kind == "normal":
+        return workloads.normal_tensor((rows, cols), 0.02, rows + cols)
+    w = np.random.default_rng(rows).integers(0, 1 << 16, (rows, cols)).astype(np.uint16)   # 8-bit codes
+    w[(w & 0x7F80) == 0x7F80] &= 0x3FFF                  # (no NaN)
+    return w
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,cols,kind", [(400, 8192, "normal"), (1000, 8192, "normal"), (1500, 8192, "normal"), (4000, 8192, "normal"),
+                                         (1500, 8191, "normal"), (3000, 8192, "bytes"), (1500, 8200, "bytes"), (1500, 8191, "bytes")])
+def test_calls_that_fill_the_gpu(n, cols, kind, dtype):
+    """8, 16 and 32 units per item, items past a warp's first, whole rows or rows that start anywhere, and bits that
+    take several passes ("bytes": 32 units of 16 pieces), some of them of no row."""
+    rows = 500
+    w = big_table(rows, cols, kind)
+    blob = k3.encode_layer([w])
+    rng = np.random.default_rng(n)
+    ids = rng.integers(0, rows, n)
+    for none in (False, True):
+        if none:
+            ids[rng.random(n) < 0.1] = -1
+        buf = torch.full(((n + 1) * cols,), 7.0, dtype=dtype, device="cuda")
+        out, st = buf[: n * cols].view(n, cols), status()
+        k3.embed_layer(blob[: k3.layer_info(blob)["hdr_bytes"]], torch.from_numpy(blob).cuda(), 0, cols, torch.as_tensor(ids).cuda(), out, st, scale=0.5)
+        torch.cuda.synchronize()
+        table = torch.from_numpy(w.view(np.int16)).view(torch.bfloat16).reshape(rows, cols)
+        assert st.item() == 0 and bool((buf[n * cols:] == 7.0).all())
+        assert same_bits(out.cpu(), expect(table, ids, 0.5, dtype))
+
+
+def test_corrupt_indexes_are_found():
+    """Every flipped bit of a chunk's or a sub-stream's first bit sets a status bit where the rows meet the whole of
+    it (the sub-stream before it, or the chunk's last, does not end where the next begins); nothing behind the rows is
+    written, with these or with flipped bits of the stream."""
+    rows, cols = 64, 1024
+    w = workloads.heavy_tail(seed=8, n=rows * cols).reshape(rows, cols)
+    blob = oracle.encode_layer([w])
+    hdr = k3.layer_info(blob)["hdr_bytes"]
+    chunks, subs = rows * cols // 4096, 15               # 15 recorded starts in each chunk of 16 sub-streams
+    first = hdr + 32
+    index = first + 4 * chunks + 2 * chunks * subs
+    rng = np.random.default_rng(9)
+    flips = [(first + 4 * c, 1 << int(rng.integers(0, 8))) for c in range(chunks)]
+    flips += [(int(at), 1 << int(rng.integers(0, 8))) for at in rng.integers(first + 4 * chunks, index, 40)]
+    stream = [(int(at), 0xFF) for at in rng.integers(index + 16, index + 4000, 20)]
+    for at, mask in flips + stream:
+        bad = blob.copy()
+        bad[at] ^= mask
+        buf = torch.full(((rows + 1) * cols,), 7.0, dtype=torch.bfloat16, device="cuda")
+        st = status()
+        k3.embed_layer(blob[:hdr], torch.from_numpy(bad).cuda(), 0, cols, torch.arange(rows, device="cuda"), buf[: rows * cols].view(rows, cols), st)
+        torch.cuda.synchronize()
+        assert bool((buf[rows * cols:] == 7.0).all())
+        assert at >= index or st.item() != 0, (at - first, mask)
+
+
 # --- gradient -----------------------------------------------------------------
 
 def grad_of(ids, dy, rows, scale, held=None, id_dtype=torch.int64):
@@ -264,6 +321,28 @@ def test_gradient_of_one_repeated_id_and_of_none():
     assert st == 0 and bool((g == 0).all())
     held = torch.ones(9, 72, device="cuda")
     assert torch.equal(grad_of([], dy[:0], 9, 1.0, held)[0], held)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,rows,cols", [(1100, 60, 1032), (3000, 4000, 2056), (2000, 37, 3001), (17000, 300, 1056)])
+def test_gradient_of_wide_tables(n, rows, cols, dtype):
+    """More than 1024 tokens and columns: several slabs of columns, for ids with few tokens and for those with many;
+    17000 tokens take two blocks."""
+    rng = np.random.default_rng(n + cols)
+    ids = long_tail(rng, n, rows)
+    ids[rng.random(n) < 0.05] = -1
+    ids[: 40] = rows - 1                                 # (more than 32 of the last id too)
+    dy = torch.from_numpy(rng.standard_normal((n, cols)).astype(np.float32)).to(dtype).cuda()
+    for held in (None, torch.from_numpy(rng.standard_normal((rows, cols)).astype(np.float32)).cuda()):
+        g, st = grad_of(ids, dy, rows, 0.7, held)
+        assert st == 0
+        want, tol = grad_ref(ids, dy, rows, 0.7, held)
+        assert np.all(np.abs(g.double().cpu().numpy() - want) <= tol)
+        again, _ = grad_of(ids, dy, rows, 0.7, held)
+        assert torch.equal(again, g)
+        if held is not None:
+            unused = np.setdiff1d(np.arange(rows), ids)
+            assert torch.equal(g[unused], held[unused])
 
 
 def test_gradient_strides_and_int32_ids():
