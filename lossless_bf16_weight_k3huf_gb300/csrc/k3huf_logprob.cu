@@ -78,10 +78,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return r;
 }
 
-// The cluster's barrier in its two halves; the stores before the one are seen after the other.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
 // A running softmax state: e_j = 2^((x_j - m) c), sum of e_j, sum of e_j (x_j - m) c.
 struct State {
     float m, sum, dot;
@@ -556,8 +552,11 @@ int launch_forward(const LogprobParams &P, uint32_t n, cudaStream_t stream) {
     static std::atomic<uint64_t> wide{0};
     const int rc = once_per_device(wide, [] { return cudaFuncSetAttribute(logprob_kernel<T, kTop, kThreads>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
     if (rc) return rc;
+    uint64_t sms = 0;
+    const int sm_rc = sm_count(&sms);
+    if (sm_rc) return sm_rc;
     uint32_t C = 1;
-    while (C < uint32_t(kMaxCluster) && n * C < 152u * 512 / kThreads && P.vocab / kStep >= 2 * C) C *= 2;
+    while (C < uint32_t(kMaxCluster) && n * C < sms * 512 / kThreads && P.vocab / kStep >= 2 * C) C *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n * C);
     cfg.blockDim = dim3(kThreads);

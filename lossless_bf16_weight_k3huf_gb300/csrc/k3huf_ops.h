@@ -32,6 +32,10 @@ __device__ __forceinline__ int64_t ld_id(const void *ids, uint32_t id_bytes, uin
     return id_bytes == 8 ? static_cast<const int64_t *>(ids)[i] : int64_t(static_cast<const int32_t *>(ids)[i]);
 }
 
+// The cluster's barrier in its two halves; the stores before the one are seen after the other.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // --- host -------------------------------------------------------------------
 inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline bool elem_ok(uint32_t type) { return type == K3HUF_BF16 || type == K3HUF_F32; }
