@@ -165,7 +165,7 @@ struct LogprobParams {
     uint32_t *status;
     uint64_t stride;
     uint32_t vocab, id_bytes, top;
-    float scale;
+    float scale, c;                           // c: scale log2 e, finite for every scale (infinity times a difference of 0 is NaN)
 };
 
 // Cuts the list to its `top` largest keys, the smallest of them last, and
@@ -243,8 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) logprob_kernel(cons
     const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank(), row = blockIdx.x / C;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const T *x = static_cast<const T *>(P.x) + uint64_t(row) * P.stride;
-    // (finite for every scale: infinity times a difference of 0 is NaN)
-    const float c = fminf(P.scale * kLog2e, 3.402823466e38f);
+    const float c = P.c;
     const uint32_t shift = uint32_t(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
     const uint32_t vecs = (P.vocab + shift + E - 1) / E;
     // this CTA's vectors: whole steps, as even as they come
@@ -627,7 +626,7 @@ extern "C" int k3huf_token_logprobs(const void *d_logits, uint32_t type, uint64_
         return K3HUF_E_ARG;
     if (n == 0) return K3HUF_OK;
     if (!d_logits || !d_tokens || !d_logprob || (top && (!d_top_ids || !d_top_logprobs))) return K3HUF_E_ARG;
-    const LogprobParams P{d_logits, d_tokens, d_logprob, d_entropy, d_lse, d_top_logprobs, d_top_ids, d_status, stride, vocab, id_bytes, top, scale};
+    const LogprobParams P{d_logits, d_tokens, d_logprob, d_entropy, d_lse, d_top_logprobs, d_top_ids, d_status, stride, vocab, id_bytes, top, scale, fminf(scale * kLog2e, 3.402823466e38f)};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (type == K3HUF_BF16)
         return launch_forward<__nv_bfloat16>(P, uint32_t(n), st);
