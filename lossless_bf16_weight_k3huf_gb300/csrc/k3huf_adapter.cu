@@ -259,10 +259,14 @@ __device__ uint32_t tile_adapters(TileAdapters &s, const int32_t *ids, uint64_t 
 // x as a sum of bf16 parts.  A finite one that would round to an infinity starts with the largest
 // bf16 instead, whose rest the other parts hold; an infinity is the first part and zeros.
 __device__ __forceinline__ void parts_of(float x, __nv_bfloat16 (&p)[3]) {
+    p[0] = __float2bfloat16_rn(x);
+    float a = x - __bfloat162float(p[0]);
     const float most = __uint_as_float(0x7F7F0000u);          // the largest bf16
-    const bool infinite = fabsf(x) == INFINITY;
-    p[0] = __float2bfloat16_rn(fabsf(x) > most && !infinite ? copysignf(most, x) : x);
-    const float a = infinite ? 0.f : x - __bfloat162float(p[0]);
+    if (fabsf(x) > most) {
+        const bool infinite = fabsf(x) == INFINITY;
+        p[0] = __float2bfloat16_rn(infinite ? x : copysignf(most, x));
+        a = infinite ? 0.f : x - copysignf(most, x);
+    }
     p[1] = __float2bfloat16_rn(a);
     p[2] = __float2bfloat16_rn(a - __bfloat162float(p[1]));
 }
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
     extern __shared__ uint8_t raw[];
     __shared__ TileAdapters tile;
     __shared__ __align__(8) uint64_t s_full[kShrinkStages], s_free[kShrinkStages], s_run[2];
-    __shared__ uint32_t s_tmem;
+    __shared__ uint32_t s_tmem, s_gave_up;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32, base = smem_addr(smem);
     const ShrinkJob &J = P.job[blockIdx.z];
@@ -314,6 +318,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
             mbar_init(smem_addr(&s_full[i]), 1);
             mbar_init(smem_addr(&s_free[i]), 1);
         }
+        s_gave_up = 0;
         mbar_init(smem_addr(&s_run[0]), 1);
         mbar_init(smem_addr(&s_run[1]), 1);
         fence_async_shared();
@@ -380,13 +385,14 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant_
             }
             __syncthreads();                      // (the run after the next writes this half)
         }
-        // a wait gave up, in any thread: copies still in flight, if any, land first
-        if (!ok) atomicOr(P.status, K3HUF_ST_TIMEOUT);
-        if (__syncthreads_or(!ok)) {
-            if (tid == 32)
-                for (uint32_t i = loaded > kShrinkStages ? loaded - kShrinkStages : 0; i < loaded; ++i) mbar_wait(smem_addr(&s_full[(step0 + i) % kShrinkStages]), (step0 + i) / kShrinkStages & 1);
+        if (!ok) {
+            atomicOr(P.status, K3HUF_ST_TIMEOUT);
+            s_gave_up = 1;
         }
         __syncthreads();
+        // a wait gave up, in any thread: copies still in flight, if any, land before the CTA ends
+        if (tid == 32 && s_gave_up)
+            for (uint32_t i = loaded > kShrinkStages ? loaded - kShrinkStages : 0; i < loaded; ++i) mbar_wait(smem_addr(&s_full[(step0 + i) % kShrinkStages]), (step0 + i) / kShrinkStages & 1);
 
         // each token's own columns, to shared memory (odd stride: one bank per lane)
         float *part = reinterpret_cast<float *>(smem);
@@ -525,10 +531,8 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
     tc_fence_after();
     const uint32_t tmem = s_tmem, steps = tiles * count;
     bool ok = true;
-    uint32_t issued = 0;                      // of this thread's copies: of H, of W's stages or of the base's
     if (warp == kThreads / 32) {
         if (lane == 0 && steps) {
-            issued = 1;
             mbar_expect(smem_addr(&s_h), E::h_bytes);
             for (uint32_t q = 0; q < E::parts; ++q)
                 for (uint32_t b = 0; b < kBlocks; ++b) tma_load(h_at + (q * kBlocks + b) * kTileBytes, &P.h, int32_t(b * 64), int32_t(q * P.n + t0), smem_addr(&s_h));
@@ -554,6 +558,7 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
                 mma_commit(smem_addr(&s_d[s & 1]));
                 if (++stage == WS) stage = 0, round ^= 1u;
             }
+            if (!ok) mbar_wait(smem_addr(&s_h), 0);   // (a copy in flight lands before the CTA ends)
         }
     } else if (warp == kThreads / 32 + 2) {
         if (lane == 0) {
@@ -569,7 +574,11 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
                     for (uint32_t b = 0; b < E::cols / 64; ++b) tma_load(at + b * E::w_block, &P.w, int32_t((c0 + i) * E::cols + b * 64), tile.list[a] * int32_t(P.rank), bar);
                     if (++stage == WS) stage = 0, round ^= 1u;
                 }
-            issued = s;
+            // the last copies land before the CTA ends, whichever thread's wait may have given up
+            for (uint32_t k = 0; k < min(s, WS); ++k) {
+                stage = stage ? stage - 1 : WS - 1;
+                mbar_wait(smem_addr(&s_w[stage]), (s - 1 - k) / WS & 1);
+            }
         }
     } else if (warp == kThreads / 32 + 1) {
         if (lane == 0) {
@@ -579,7 +588,8 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
                 if (P.has_base)
                     for (uint32_t b = 0; b < 2; ++b) tma_load(io_at + i % IS * E::io_bytes + b * kTileBytes, &P.base, int32_t((c0 + i) * E::cols + b * E::row), int32_t(t0), bar);
             };
-            for (; issued < min(IS, tiles); ++issued) load(issued);
+            uint32_t loaded = min(IS, tiles);
+            for (uint32_t i = 0; i < loaded; ++i) load(i);
             for (uint32_t i = 0; i < tiles && ok; ++i) {
                 ok = mbar_wait(smem_addr(&s_iodone[i % IS]), i / IS & 1);
                 if (!ok) break;
@@ -588,10 +598,11 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
                 bulk_commit();
                 if (i + IS < tiles) {
                     bulk_wait_read<0>();
-                    load(issued++);
+                    load(loaded++);
                 }
             }
             bulk_wait_all();
+            for (uint32_t i = loaded > IS ? loaded - IS : 0; i < loaded; ++i) mbar_wait(smem_addr(&s_io[i % IS]), i / IS & 1);
         }
     } else {
         // this thread: token warp % 4 * 32 + lane, the tile's columns of row block warp / 4
@@ -638,13 +649,7 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const __grid_con
     }
     if (!ok) atomicOr(P.status, K3HUF_ST_TIMEOUT);
     tc_fence_before();
-    // a wait gave up, in any thread: each issuer's last copies, those of its stages, land first
-    if (__syncthreads_or(!ok)) {
-        const uint32_t stages = warp == kThreads / 32 ? 1 : warp == kThreads / 32 + 2 ? WS : IS;
-        uint64_t *bars = warp == kThreads / 32 ? &s_h : warp == kThreads / 32 + 2 ? s_w : s_io;
-        for (uint32_t i = issued > stages ? issued - stages : 0; i < issued; ++i) mbar_wait(smem_addr(&bars[i % stages]), i / stages & 1);
-        __syncthreads();
-    }
+    __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_free(tmem, 256);
 }
@@ -814,7 +819,8 @@ __global__ void __launch_bounds__(kThreads) outer_kernel(const __grid_constant__
         // lane: column; a warp's stores of one rank row are 128 adjacent bytes.  (Added to: adapters
         // without a token are left alone, another call may be adding to them)
         const uint32_t c = col + warp % 4 * 32 + lane;
-        if (c < J.len && (step != first || !P.add))
+        const bool alone = P.add && step == first;
+        if (c < J.len && !alone)
 #pragma unroll
             for (uint32_t b = 0; b < O::pieces; ++b)
 #pragma unroll
