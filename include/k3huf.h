@@ -459,9 +459,13 @@ int k3huf_ring_run_file(k3huf_ring *ring, k3huf_feed *feed, int n_layers, const 
  *  - ids are int32 or int64 (id_bytes 4 or 8).  A negative id means "none"
  *    (padding, an unscored token, a request without an adapter); one past
  *    the range is taken as none too and sets K3HUF_ST_TOKEN in *d_status;
- *  - sums, softmax statistics and rank-wide intermediates are fp32; bf16
- *    results are rounded once, to nearest.  Results do not depend on timing:
- *    the same call on the same inputs gives the same bits;
+ *  - sums, softmax statistics and rank-wide intermediates are fp32 sums; bf16
+ *    results are rounded once, to nearest.  (One more rounding: for bf16 results
+ *    of many tokens the rank-wide intermediate enters the second product to
+ *    2^-17 of itself.  That is far below the result's own 2^-9, but shows where
+ *    base and the adapter's part cancel; fp32 results take all of its bits.)
+ *    Results do not depend on timing: the same call on the same inputs gives
+ *    the same bits;
  *  - scratch is the caller's, need not be initialised, and must not be given
  *    to two calls that may run at the same time;
  *  - a call over zero tokens launches nothing that reads or writes them. */
@@ -486,9 +490,11 @@ int k3huf_embed_layer(const void *h_layer_hdr, size_t hdr_bytes, const void *d_l
                       void *stream);
 
 /* The gradient of such a lookup: grad[v] = scale * (sum of dY[t] over the
- * tokens t with ids[t] = v, in the order of the tokens), for a table of
- * `rows` rows; rows without a token are zero.  With K3HUF_ACCUMULATE the sums
- * are added to grad and the other rows are left alone.
+ * tokens t with ids[t] = v), for a table of `rows` rows; rows without a token
+ * are zero.  The sum's order is fixed by the ids: that of the tokens, but above
+ * 1024 tokens more than 32 of one id are added in shares, and every 16384 tokens
+ * by themselves.  With K3HUF_ACCUMULATE the sums are added to grad and the other
+ * rows are left alone.
  *  d_dy: n_tokens rows of `cols` elements of dy_type, dy_stride apart;
  *  d_grad: rows x cols floats, contiguous;
  *  d_scratch: k3huf_embed_grad_scratch_bytes(...) bytes.

@@ -15,8 +15,10 @@
 //  - many: tcgen05.mma on tiles of 128 tokens, described at each kernel;
 //  - rows that do not start on 16 bytes: one CTA per token, element by element.
 // The rank-wide intermediates are fp32 sums.  The tensor cores take them as a
-// sum of bf16 parts: three parts (24 bits) where the result is fp32, two (16
-// bits) where it is rounded to bf16.
+// sum of bf16 parts: three parts (24 bits) where the result is fp32, two (to
+// 2^-17 of themselves) where it is rounded to bf16, to 2^-9.  Three there too
+// cost 8192 tokens x 64 x (8192 + 24576) 202 us instead of 194, 4000 tokens of
+// 64 adapters in any order, rank 16, 139 instead of 125.
 #include <algorithm>
 #include <cmath>
 
