@@ -61,6 +61,10 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&f)[4]) {
 }
 
 // --- rows of any alignment --------------------------------------------------------
+//
+// Bound by their loads of one element each: 192 tokens x 16 x (8192 + 8192) 133 us (15
+// with rows on 16 bytes); gradients of 515 tokens x 32 1044 us (43), most of it the
+// outer product's search through the ids for every element.
 
 // h[t, r] = s_i v[t] . w[i, r]; zero without an adapter.  One CTA per token, one warp per row of the factor.
 __global__ void __launch_bounds__(kThreads)
@@ -296,7 +300,7 @@ struct ShrinkParams {
 // the splits.  One thread keeps the products and one the
 // copies going for a run of kRun steps while the CTA moves the run before it from
 // the other half of TMEM to registers.  Bound by the read of V (and of the factors
-// when every token has its own): 30 us for 8192 tokens x 8192 to rank 64, 4.5 TB/s.
+// when every token has its own): 36 us for 8192 tokens x 8192 to rank 64, 3.7 TB/s.
 constexpr uint32_t kShrinkStages = 3, kShrinkStage = 2 * kTileBytes;
 constexpr size_t kShrinkSmem = kShrinkStages * kShrinkStage + 1024;
 constexpr uint32_t kMaxSplits = 8;
@@ -459,8 +463,8 @@ struct ExpandParams {
 // CTAs: a tile of tokens x a range of column tiles; a step is one adapter of
 // one column tile.  Warps 0 to 7 add; a thread of warp 8 issues the products, two
 // steps ahead of the additions; one of warp 9 brings the base and takes y away;
-// one of warp 10 brings W.  Bound by the read of the base and the write of y: 144 us for
-// 8192 tokens x 24576 bf16 columns, 5.6 TB/s.  (With columns as the lanes, 2 bytes
+// one of warp 10 brings W.  Bound by the read of the base and the write of y: 142 us for
+// 8192 tokens x 24576 bf16 columns, 5.7 TB/s.  (With columns as the lanes, 2 bytes
 // at a time, the additions took five times the instructions, 184 us.)
 constexpr uint32_t kExpandThreads = kThreads + 96;
 template <typename T, uint32_t kBlocks> struct Expand {       // kBlocks: blocks of 64 rank rows
@@ -676,7 +680,7 @@ struct OuterParams {
 // token by token, so both are read MN-major.  CTAs: a tile of columns (of
 // either gradient) x an adapter; the tokens' indexes come from the ids,
 // kWindow at a time, in order.  Bound by the read of V, in pieces of 256 bytes:
-// 35 us for 4096 tokens x 32 x (8192 + 8192) of 4 adapters, 3.8 TB/s.
+// 46 us for 4096 tokens x 32 x (8192 + 8192) of 4 adapters, 2.9 TB/s.
 //
 // Ranks up to 32 (kBlocks 0) stage the parts side by side and multiply them at
 // once into columns of their own, which takes a third of the products and

@@ -16,7 +16,8 @@
 // (loaded before the decode), scales in fp32 and stores 16 bytes per lane.
 // What bounds it: a few units, the chain of lookups (about 55 cycles each)
 // after the table's build (14 us for 32 rows of 8192); many, the lookups'
-// wavefronts and the instructions of both halves (70 us for 8192 such rows).
+// wavefronts and the instructions of both halves (66 to 76 us for 8192 such
+// rows, by their ids; 78 us in fp32).
 #include <algorithm>
 
 #include "k3huf_tc.h"
