@@ -94,7 +94,9 @@ expand_any_kernel(const float *h, const __nv_bfloat16 *w, const int32_t *ids, ui
         float acc = 0.f;
         if (any)
             for (uint32_t r = 0; r < rank; ++r) acc = fmaf(h[t * rank + r], ld_f32(w + (uint64_t(i) * rank + r) * len + c), acc);
-        st_f32(y + t * y_stride + c, base ? ld_f32(base + t * base_stride + c) + acc : acc);
+        // (without an adapter the base as it is: -0 + 0 would be +0)
+        const float b = base ? ld_f32(base + t * base_stride + c) : 0.f;
+        st_f32(y + t * y_stride + c, any ? b + acc : b);
     }
 }
 
@@ -198,7 +200,7 @@ expand_few_kernel(const float *h, const __nv_bfloat16 *w, const int32_t *ids, ui
         }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] += sum[k];
+    for (int k = 0; k < 4; ++k) acc[k] = any ? acc[k] + sum[k] : acc[k];       // (the base as it is: -0 + 0 would be +0)
     store4(y + t * y_stride + c, acc);
 }
 

@@ -505,3 +505,24 @@ def test_gradients_in_place_strides_and_ids_past_the_pool(n, r, dtype, pad):
     assert st.item() == k3.ST_TOKEN
     assert close(da, ra) and close(db, rb) and close(dx, rx, dtype)
     assert torch.equal(wide[:, cols:], before[:, cols:]) and torch.equal(dx[past], before[past, :cols])
+
+
+@pytest.mark.parametrize("form", ["few", "tiles", "any"])
+def test_tokens_without_an_adapter_keep_the_base_bits(form):
+    """y = base, to the sign of its zeros; the same of dx."""
+    n, S, r, cols, rows = MANY if form == "tiles" else (40, 3, 16, 264, 328)
+    s = make(n, S, r, cols, rows, 91)
+    s["ids"][::3] = -1
+    if form == "any":
+        wide = torch.zeros(n, cols + 1, dtype=torch.bfloat16, device="cuda")
+        wide[:, 1:] = s["x"]
+        s["x"] = wide[:, 1:]
+    none = s["ids"] < 0
+    for dtype, bits in ((torch.float32, torch.int32), (torch.bfloat16, torch.int16)):
+        base, dx_base = torch.randn(n, rows, device="cuda").to(dtype), torch.randn(n, cols, device="cuda").to(dtype)
+        base[:, ::5], dx_base[:, ::5] = -0.0, -0.0
+        y = torch.empty_like(base)
+        assert apply(s, y, base) == 0
+        assert torch.equal(y[none].view(bits), base[none].view(bits))
+        dx = grads(s, dtype, dx_base)[2]
+        assert torch.equal(dx[none].view(bits), dx_base[none].view(bits))
