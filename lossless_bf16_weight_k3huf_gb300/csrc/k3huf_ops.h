@@ -41,9 +41,11 @@ inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintp
 inline bool elem_ok(uint32_t type) { return type == K3HUF_BF16 || type == K3HUF_F32; }
 inline size_t elem_bytes(uint32_t type) { return type == K3HUF_F32 ? 4 : 2; }
 
+// (the runtime's record of the error is cleared: the call returns it, nobody else should meet it)
 inline int cuda_rc(cudaError_t e) {
     if (e == cudaSuccess) return K3HUF_OK;
     set_cuda_error(int(e));
+    (void)cudaGetLastError();
     return K3HUF_E_CUDA;
 }
 

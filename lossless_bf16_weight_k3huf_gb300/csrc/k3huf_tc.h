@@ -145,8 +145,7 @@ inline int tensor_map(CUtensorMap *map, const void *p, uint32_t type, uint64_t r
         cudaDriverEntryPointQueryResult found{};
         const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
         if (e != cudaSuccess || found != cudaDriverEntryPointSuccess || !f) {
-            set_cuda_error(int(e != cudaSuccess ? e : cudaErrorNotSupported));
-            return K3HUF_E_CUDA;
+            return cuda_rc(e != cudaSuccess ? e : cudaErrorNotSupported);
         }
         encode = reinterpret_cast<Encode>(f);
         known.store(encode, std::memory_order_release);
