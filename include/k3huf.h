@@ -552,8 +552,8 @@ int k3huf_adapter_grad(const k3huf_adapters_t *adapters, const void *d_x, uint64
  *  d_logprob: n floats, 0 for "none"; d_entropy, d_lse (log of the sum of
  *    exponentials of the scaled logits): n floats, or NULL;
  *  top (0 .. K3HUF_MAX_TOP, at most vocab): the `top` largest logits of every
- *    row, largest first, ties to the lower index: d_top_ids and
- *    d_top_logprobs, n x top.
+ *    row, largest first, ties to the lower index (a NaN ranks as -infinity):
+ *    d_top_ids and d_top_logprobs, n x top.
  * Logits of -infinity have probability 0 and take no part in the entropy; a
  * row with no other logits has lse -infinity and entropy 0.  A NaN, or
  * +infinity, makes the row's statistics and log probabilities NaN. */
