@@ -577,6 +577,63 @@ int k3huf_token_logprobs_grad(const void *d_logits, uint32_t type, uint64_t stri
                               const float *d_entropy, const float *d_g_logprob, const float *d_g_entropy,
                               void *d_dlogits, uint64_t out_stride, uint32_t *d_status, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * From a decoded weight to its logits and what is done with them: the product of
+ * many tokens with a bf16 weight (k3huf_decode_tensor's output), the control of
+ * logits before a token is chosen, distillation from a teacher's alternatives.
+ * The conventions of the operators above hold here too. */
+
+/* act(z): z; max(z, 0); z / (1 + exp(-z)); the tanh form of GELU,
+ * z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))). */
+#define K3HUF_ACT_NONE 0u
+#define K3HUF_ACT_RELU 1u
+#define K3HUF_ACT_SILU 2u
+#define K3HUF_ACT_GELU 3u
+
+/* Scratch of k3huf_linear (grad 0) and k3huf_linear_grad (grad 1): room for copies
+ * of the operands whose rows do not start on 16-byte boundaries.  any 0: for
+ * contiguous operands from 16-byte aligned addresses (0 bytes when rows and cols
+ * are multiples of 8); any 1: for operands of every stride and alignment.  A call
+ * that needs no copy takes NULL and 0. */
+int k3huf_linear_scratch_bytes(uint64_t n_tokens, uint64_t rows, uint64_t cols, int grad, int any,
+                               size_t *scratch_bytes);
+
+/* y[t] = act(z[t]) + residual[t], z[t] = x[t] W^T + bias, for a row-major weight W
+ * of `rows` rows (outputs) and `cols` columns (inputs).
+ *  d_x: n_tokens rows of cols bf16; d_w: rows of cols bf16;
+ *  d_bias: rows elements of bias_type, or NULL;
+ *  d_residual: rows of y's type, or NULL; may be d_y itself (then
+ *    residual_stride = y_stride);
+ *  d_y: n_tokens rows of `rows` elements of y_type;
+ *  d_z: where a backward pass wants z, rows of z_type; or NULL.
+ * Sums are fp32: for fp32 y they leave the tensor core every 512 values of the
+ * contraction, whose additions round to one side.  Up to 2^31 - 1 tokens, rows
+ * and columns. */
+int k3huf_linear(const void *d_x, uint64_t x_stride, uint64_t n_tokens, const void *d_w, uint64_t w_stride,
+                 uint64_t rows, uint64_t cols, const void *d_bias, uint32_t bias_type, uint32_t act,
+                 const void *d_residual, uint64_t residual_stride, void *d_y, uint64_t y_stride, uint32_t y_type,
+                 void *d_z, uint64_t z_stride, uint32_t z_type, void *d_scratch, size_t scratch_bytes,
+                 uint32_t *d_status, void *stream);
+
+/* What the epilogue passes back: dz[t] = dy[t] act'(z[t]), rounded to bf16, and
+ * dbias = sum over the tokens of dz before that rounding (NULL: not wanted; with
+ * K3HUF_ACCUMULATE added to).  The residual's gradient is dy itself; without
+ * activation dz is dy.  d_dz may be d_dy or d_z, where that is bf16 of the same
+ * stride. */
+int k3huf_linear_dz(const void *d_z, uint32_t z_type, uint64_t z_stride, const void *d_dy, uint32_t dy_type,
+                    uint64_t dy_stride, uint64_t n_tokens, uint64_t rows, uint32_t act, void *d_dz,
+                    uint64_t dz_stride, float *d_dbias, uint32_t flags, void *stream);
+
+/* The gradients of the product for dz (n_tokens rows of `rows` bf16):
+ *  dx[t] = dz[t] W: rows of cols elements of dx_type (d_dx NULL: not wanted, and
+ *    d_w is not read), the dx_base of k3huf_adapter_grad;
+ *  dW = sum over the tokens of dz[t]^T x[t]: rows x cols floats, contiguous (d_dw
+ *    NULL: not wanted, and d_x is not read); with K3HUF_ACCUMULATE added to. */
+int k3huf_linear_grad(const void *d_x, uint64_t x_stride, uint64_t n_tokens, const void *d_w, uint64_t w_stride,
+                      uint64_t rows, uint64_t cols, const void *d_dz, uint64_t dz_stride, void *d_dx,
+                      uint64_t dx_stride, uint32_t dx_type, float *d_dw, void *d_scratch, size_t scratch_bytes,
+                      uint32_t *d_status, uint32_t flags, void *stream);
+
 /* Last CUDA error code seen by this library on the calling thread. */
 int k3huf_last_cuda_error(void);
 /* Static description of a K3HUF_E_* code. */

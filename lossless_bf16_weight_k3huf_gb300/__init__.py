@@ -34,7 +34,8 @@ EXPORTS = [
     "k3huf_encode_scratch_bytes", "k3huf_encode_bound", "k3huf_encode_layer_gpu", "k3huf_gemv_layer",
     "k3huf_gemv_layer_ex", "k3huf_gemv_layer_batch", "k3huf_embed_layer", "k3huf_embed_grad_scratch_bytes",
     "k3huf_embed_grad", "k3huf_adapter_scratch_bytes", "k3huf_adapter_apply", "k3huf_adapter_grad",
-    "k3huf_token_logprobs", "k3huf_token_logprobs_grad",
+    "k3huf_token_logprobs", "k3huf_token_logprobs_grad", "k3huf_linear_scratch_bytes", "k3huf_linear",
+    "k3huf_linear_dz", "k3huf_linear_grad",
 ]
 FILE_ALIGN = 4096
 
@@ -147,6 +148,12 @@ def _lib():
                                                _vp, _vp]
             L.k3huf_token_logprobs_grad.argtypes = [_vp, u32, u64, u64, u32, f32, _vp, u32, _vp, _vp, _vp, _vp, _vp,
                                                     u64, _vp, _vp]
+            L.k3huf_linear_scratch_bytes.argtypes = [u64, u64, u64, ctypes.c_int, ctypes.c_int, ctypes.POINTER(_sz)]
+            L.k3huf_linear.argtypes = [_vp, u64, u64, _vp, u64, u64, u64, _vp, u32, u32, _vp, u64, _vp, u64, u32, _vp, u64,
+                                       u32, _vp, _sz, _vp, _vp]
+            L.k3huf_linear_dz.argtypes = [_vp, u32, u64, _vp, u32, u64, u64, u64, u32, _vp, u64, _vp, u32, _vp]
+            L.k3huf_linear_grad.argtypes = [_vp, u64, u64, _vp, u64, u64, u64, _vp, u64, _vp, u64, u32, _vp, _vp, _sz, _vp,
+                                            u32, _vp]
             L.k3huf_strerror.restype = ctypes.c_char_p
             L.k3huf_strerror.argtypes = [ctypes.c_int]
             _lib_handle = L
@@ -593,6 +600,89 @@ def token_logprobs_grad(logits, tokens, lse, g_logprob, dlogits, d_status, entro
                                             _dense(g_logprob, (n,), "g_logprob", f32),
                                             None if g_entropy is None else _dense(g_entropy, (n,), "g_entropy", f32),
                                             dp, ds, _dptr(d_status), _stream(stream)), "k3huf_token_logprobs_grad")
+
+
+_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+
+
+def _act(act: str) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"act: expected one of {tuple(_ACTS)}, got {act!r}")
+    return _ACTS[act]
+
+
+def _given(scratch):
+    """(address, bytes) of a scratch tensor, or of none."""
+    return (None, 0) if scratch is None else (_dptr(scratch), _nbytes(scratch))
+
+
+def linear_scratch_bytes(n_tokens: int, rows: int, cols: int, grad: bool = False, any: bool = False) -> int:
+    """Device scratch bytes of linear, or of linear_grad: 0 for contiguous operands
+    whose rows start on 16 bytes.  ``any``: for operands of every stride and
+    alignment."""
+    out = _sz(0)
+    _check(_lib().k3huf_linear_scratch_bytes(n_tokens, rows, cols, int(grad), int(any), ctypes.byref(out)),
+           "k3huf_linear_scratch_bytes")
+    return int(out.value)
+
+
+def linear(x, w, y, d_status, bias=None, residual=None, act: str = "none", z=None, scratch=None, stream=None) -> None:
+    """y[t] = act(x[t] w^T + bias) + residual[t] (k3huf_linear).  ``x``, ``w``: bf16,
+    tokens x cols and rows x cols; ``bias``: bf16 or fp32 of rows; ``act``: none,
+    relu, silu or gelu (tanh form); ``y``: bf16 or fp32, tokens x rows; ``residual``:
+    of y's type, may be y; ``z``: bf16 or fp32, takes what act is applied to."""
+    n, cols = x.shape
+    rows = w.shape[0]
+    xp, _, xs = _matrix(x, n, cols, "x", _BF16)
+    wp, _, ws = _matrix(w, rows, cols, "w", _BF16)
+    yp, ye, ys = _matrix(y, n, rows, "y")
+    bp, be = None, 0
+    if bias is not None:
+        be = _dtypes()[0].get(bias.dtype)
+        if be is None:
+            raise TypeError(f"bias: wrong element type {bias.dtype}")
+        bp = _dense(bias, (rows,), "bias", bias.dtype)
+    rp, _, rs = (None, ye, 0) if residual is None else _matrix(residual, n, rows, "residual", ye)
+    zp, ze, zs = (None, 0, 0) if z is None else _matrix(z, n, rows, "z")
+    sp, sb = _given(scratch)
+    _check(_lib().k3huf_linear(xp, xs, n, wp, ws, rows, cols, bp, be, _act(act), rp, rs, yp, ys, ye, zp, zs, ze, sp, sb,
+                               _dptr(d_status), _stream(stream)), "k3huf_linear")
+
+
+def linear_dz(z, dy, dz, act: str = "none", dbias=None, accumulate: bool = False, stream=None) -> None:
+    """dz = dy act'(z), rounded to bf16, and ``dbias`` (fp32 of rows), its sum over the
+    tokens (k3huf_linear_dz); ``accumulate``: added to dbias.  ``z``, ``dy``: bf16 or
+    fp32, tokens x rows."""
+    n, rows = z.shape
+    zp, ze, zs = _matrix(z, n, rows, "z")
+    gp, ge, gs = _matrix(dy, n, rows, "dy")
+    op, _, os_ = _matrix(dz, n, rows, "dz", _BF16)
+    _check(_lib().k3huf_linear_dz(zp, ze, zs, gp, ge, gs, n, rows, _act(act), op, os_,
+                                  None if dbias is None else _dense(dbias, (rows,), "dbias", _dtypes()[2]),
+                                  ACCUMULATE if accumulate else 0, _stream(stream)), "k3huf_linear_dz")
+
+
+def linear_grad(x, w, dz, d_status, dx=None, dw=None, scratch=None, accumulate: bool = False, stream=None) -> None:
+    """Gradients of the product for the bf16 gradient ``dz`` (k3huf_linear_grad):
+    ``dx`` = dz w (fp32 or bf16, tokens x cols) and ``dw`` = dz^T x (fp32, rows x
+    cols; ``accumulate``: added to), each None if not wanted; then w, or x, may be
+    None too."""
+    n, rows = dz.shape
+    if dx is None and dw is None:
+        raise ValueError("dx or dw")
+    cols = (dx if dx is not None else dw).shape[1]
+    gp, _, gs = _matrix(dz, n, rows, "dz", _BF16)
+    wp, ws, dp, ds, de = None, 0, None, 0, 0
+    if dx is not None:
+        wp, _, ws = _matrix(w, rows, cols, "w", _BF16)
+        dp, de, ds = _matrix(dx, n, cols, "dx")
+    xp, xs, qp = None, 0, None
+    if dw is not None:
+        xp, _, xs = _matrix(x, n, cols, "x", _BF16)
+        qp = _dense(dw, (rows, cols), "dw", _dtypes()[2])
+    sp, sb = _given(scratch)
+    _check(_lib().k3huf_linear_grad(xp, xs, n, wp, ws, rows, cols, gp, gs, dp, ds, de, qp, sp, sb, _dptr(d_status),
+                                    ACCUMULATE if accumulate else 0, _stream(stream)), "k3huf_linear_grad")
 
 
 class Feed:

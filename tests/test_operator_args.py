@@ -116,3 +116,44 @@ def test_scratch_sizes_grow_with_the_tokens():
     for args in ((4, 0, 64), (4, 10, 0)):
         with pytest.raises(k3.K3HufError):
             k3.embed_grad_scratch_bytes(*args)
+
+
+def test_linear(lib):
+    def call(x=P, xs=64, n=4, w=P, ws=64, rows=32, cols=64, bias=P, bt=0, act=1, res=P, rs=32, y=P, ys=32, yt=1, z=P, zs=32, zt=0, scratch=None, size=0, st=P):
+        return lib.k3huf_linear(x, xs, n, w, ws, rows, cols, bias, bt, act, res, rs, y, ys, yt, z, zs, zt, scratch, size, st, None)
+
+    assert call(n=0) == k3.OK and call(n=0, x=None, w=None, y=None, z=None, res=None, bias=None) == k3.OK
+    for kw in (dict(x=None), dict(x=P + 1), dict(xs=63), dict(n=1 << 31), dict(w=None), dict(w=P + 1), dict(ws=63), dict(rows=0), dict(rows=1 << 31),
+               dict(cols=0), dict(cols=1 << 31, xs=1 << 31, ws=1 << 31), dict(bias=P + 1), dict(bt=1, bias=P + 2), dict(bt=2), dict(act=4), dict(res=P + 2),
+               dict(rs=31), dict(rs=40), dict(y=None), dict(y=P + 2), dict(ys=31), dict(yt=2), dict(z=P + 1), dict(zs=31), dict(zt=2), dict(zt=1, z=P + 2),
+               dict(st=None), dict(st=P + 2), dict(scratch=P + 16, size=1 << 20)):
+        assert call(**kw) == k3.E_ARG, kw
+    # rows that do not start on 16 bytes need their copies' room
+    need = k3.linear_scratch_bytes(4, 32, 64, any=True)
+    assert k3.linear_scratch_bytes(4, 32, 64) == 0 and k3.linear_scratch_bytes(4, 32, 63) == need
+    for kw in (dict(xs=65, ws=65), dict(xs=65, ws=65, scratch=P, size=need - 1), dict(xs=65), dict(ws=65), dict(x=P + 2), dict(w=P + 8)):
+        assert call(**kw) == k3.E_ARG, kw
+
+
+def test_linear_dz(lib):
+    def call(z=P, zt=0, zs=32, dy=P + 64, dyt=0, dys=32, n=4, rows=32, act=2, dz=P + 128, dzs=32, db=P, flags=0):
+        return lib.k3huf_linear_dz(z, zt, zs, dy, dyt, dys, n, rows, act, dz, dzs, db, flags, None)
+
+    assert call(n=0, db=None) == k3.OK and call(n=0, flags=k3.ACCUMULATE) == k3.OK
+    for kw in (dict(z=None), dict(z=P + 1), dict(zt=1, z=P + 2), dict(zt=2), dict(zs=31), dict(dy=None), dict(dy=P + 1), dict(dyt=3), dict(dys=31),
+               dict(n=1 << 31), dict(rows=0), dict(act=4), dict(dz=None), dict(dz=P + 1), dict(dzs=31), dict(db=P + 2), dict(flags=1), dict(dz=P, zs=40),
+               dict(dz=P, zt=1), dict(dz=P + 64, dys=40), dict(dz=P + 64, dyt=1)):
+        assert call(**kw) == k3.E_ARG, kw
+
+
+def test_linear_grad(lib):
+    def call(x=P, xs=64, n=4, w=P, ws=64, rows=32, cols=64, dz=P, dzs=32, dx=P, dxs=64, dxt=0, dw=P, scratch=None, size=0, st=P, flags=0):
+        return lib.k3huf_linear_grad(x, xs, n, w, ws, rows, cols, dz, dzs, dx, dxs, dxt, dw, scratch, size, st, flags, None)
+
+    assert call(n=0, dw=None) == k3.OK and call(n=0, flags=k3.ACCUMULATE) == k3.OK
+    for kw in (dict(x=None), dict(x=P + 1), dict(xs=63), dict(n=1 << 31), dict(w=None), dict(w=P + 1), dict(ws=63), dict(rows=0), dict(cols=0), dict(dz=None),
+               dict(dz=P + 1), dict(dzs=31), dict(dx=P + 1), dict(dxt=1, dx=P + 2), dict(dxt=2), dict(dxs=63), dict(dw=P + 2), dict(dx=None, dw=None), dict(st=None),
+               dict(flags=8), dict(scratch=P + 16, size=1 << 20), dict(xs=65), dict(ws=65), dict(dzs=33)):
+        assert call(**kw) == k3.E_ARG, kw
+    need = k3.linear_scratch_bytes(4, 32, 64, grad=True, any=True)
+    assert call(xs=65, ws=65, dzs=33, scratch=P, size=need - 1) == k3.E_ARG
