@@ -634,6 +634,76 @@ int k3huf_linear_grad(const void *d_x, uint64_t x_stride, uint64_t n_tokens, con
                       uint64_t dx_stride, uint32_t dx_type, float *d_dw, void *d_scratch, size_t scratch_bytes,
                       uint32_t *d_status, uint32_t flags, void *stream);
 
+/* What is done to the logits of a batch's rows before a token is chosen.  Each part
+ * is left out by a NULL list (penalties need a history).  Lists lie on the device
+ * and are shared by rows as their spans say (drafted tokens over one history, one
+ * list of biases for many requests); a span outside its list counts as empty and
+ * sets K3HUF_ST_INDEX. */
+typedef struct {
+    const void *history;          /* n_history token ids, prompts and outputs of the requests */
+    const int64_t *spans;         /* n x 3: from, split, to: row t's prompt lies at [from, split) of the history, its output at [split, to) */
+    uint64_t n_history;           /* up to 2^31 - 1, as n_bias */
+    uint32_t history_id_bytes, bias_id_bytes;
+    const float *repetition, *frequency, *presence;      /* n floats each, or NULL (1, 0, 0) */
+    const void *bias_ids;         /* n_bias token ids ... */
+    const float *bias_values;     /* ... and what is added to their logits */
+    const int64_t *bias_spans;    /* n x 2; a token listed twice in a row's span takes its last value */
+    uint64_t n_bias;
+    const uint32_t *mask;         /* n_masks rows of mask_stride words; bit j % 32 of word j / 32: token j is allowed */
+    const int32_t *mask_rows;     /* n: row t's mask, negative for none (past n_masks: none, K3HUF_ST_INDEX); NULL: mask t */
+    uint64_t n_masks, mask_stride;
+} k3huf_control_t;
+
+/* out[t][j]: with `seen` whether row t's prompt or output holds token j and c how
+ * often its output does,
+ *   v = logits[t][j];  if seen: v = v > 0 ? v / repetition[t] : v repetition[t];
+ *   v -= frequency[t] c;  if c > 0: v -= presence[t];  v += bias;
+ *   -infinity where the mask does not allow j (whatever the logit was).
+ * Sums are fp32, the result of out_type rounded once; a token that nothing touches
+ * keeps its bits where the types are the same.  d_out may be d_logits (then of the
+ * same type and stride): only what changes is read and written. */
+int k3huf_logits_control(const k3huf_control_t *control, const void *d_logits, uint32_t type, uint64_t stride,
+                         uint64_t n, uint32_t vocab, void *d_out, uint32_t out_type, uint64_t out_stride,
+                         uint32_t *d_status, void *stream);
+
+/* Distillation of rows of logits (the student's: type, stride) from a teacher's top
+ * alternatives, as k3huf_token_logprobs gives them, under p = softmax(scale *
+ * logits), scale > 0:
+ *   loss[t] = sum over the alternatives i of q_i (log q_i - log p_i)
+ *  d_top_ids, d_top_logprobs: n x top (1 .. K3HUF_MAX_TOP); a negative id is no
+ *    alternative; one listed twice counts twice in the sums over i;
+ *  mode: what q is.
+ *   K3HUF_DISTILL_GIVEN: exp(d_top_logprobs), a part of a distribution;
+ *   K3HUF_DISTILL_NORMALISED: their softmax over the row's alternatives (logits of
+ *     the teacher do as well);
+ *   K3HUF_DISTILL_REST: as given, and the mass that they leave is one alternative
+ *     more, the rest, against the mass that p leaves: q_r (log q_r - log p_r) with
+ *     q_r = 1 - sum q (0 if that is negative), p_r the sum of p over the other tokens;
+ *  d_loss: n floats, 0 for a row without alternatives; d_lse (log of the sum of
+ *    exponentials of the scaled logits), d_log_rest (log p_r; K3HUF_DISTILL_REST
+ *    only): n floats, or NULL.
+ * A term of q 0 is 0; a q above 0 against p 0 gives an infinite loss.  Logits of
+ * -infinity have p 0; a NaN or +infinity makes the row's results NaN.  Up to
+ * 2^27 - 1 rows. */
+#define K3HUF_DISTILL_GIVEN      0u
+#define K3HUF_DISTILL_NORMALISED 1u
+#define K3HUF_DISTILL_REST       2u
+int k3huf_distill(const void *d_logits, uint32_t type, uint64_t stride, uint64_t n, uint32_t vocab, float scale,
+                  const int32_t *d_top_ids, const float *d_top_logprobs, uint32_t top, uint32_t mode, float *d_loss,
+                  float *d_lse, float *d_log_rest, uint32_t *d_status, void *stream);
+
+/* Its gradient with respect to the logits for the gradient g of the loss (not read
+ * for a row without alternatives, whose gradient is 0): with Q = sum q (+ q_r),
+ *   dlogits[j] = scale g (Q p_j - q_j) for an alternative,
+ *                scale g (Q - q_r / p_r) p_j for another token.
+ *  d_lse, d_log_rest (K3HUF_DISTILL_REST, else NULL): as k3huf_distill gave them;
+ *  d_dlogits: of the logits' type, out_stride apart; may be d_logits itself (then
+ *    out_stride = stride). */
+int k3huf_distill_grad(const void *d_logits, uint32_t type, uint64_t stride, uint64_t n, uint32_t vocab, float scale,
+                       const int32_t *d_top_ids, const float *d_top_logprobs, uint32_t top, uint32_t mode,
+                       const float *d_lse, const float *d_log_rest, const float *d_g_loss, void *d_dlogits,
+                       uint64_t out_stride, uint32_t *d_status, void *stream);
+
 /* Last CUDA error code seen by this library on the calling thread. */
 int k3huf_last_cuda_error(void);
 /* Static description of a K3HUF_E_* code. */

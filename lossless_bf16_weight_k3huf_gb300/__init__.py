@@ -35,7 +35,7 @@ EXPORTS = [
     "k3huf_gemv_layer_ex", "k3huf_gemv_layer_batch", "k3huf_embed_layer", "k3huf_embed_grad_scratch_bytes",
     "k3huf_embed_grad", "k3huf_adapter_scratch_bytes", "k3huf_adapter_apply", "k3huf_adapter_grad",
     "k3huf_token_logprobs", "k3huf_token_logprobs_grad", "k3huf_linear_scratch_bytes", "k3huf_linear",
-    "k3huf_linear_dz", "k3huf_linear_grad",
+    "k3huf_linear_dz", "k3huf_linear_grad", "k3huf_logits_control", "k3huf_distill", "k3huf_distill_grad",
 ]
 FILE_ALIGN = 4096
 
@@ -75,6 +75,15 @@ class Adapters(ctypes.Structure):
     _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("n_adapters", ctypes.c_uint32), ("rank", ctypes.c_uint32), ("cols", ctypes.c_uint64),
                 ("rows", ctypes.c_uint64)]
+
+
+class Control(ctypes.Structure):
+    _fields_ = [("history", ctypes.c_void_p), ("spans", ctypes.c_void_p), ("n_history", ctypes.c_uint64),
+                ("history_id_bytes", ctypes.c_uint32), ("bias_id_bytes", ctypes.c_uint32),
+                ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("bias_ids", ctypes.c_void_p), ("bias_values", ctypes.c_void_p), ("bias_spans", ctypes.c_void_p),
+                ("n_bias", ctypes.c_uint64), ("mask", ctypes.c_void_p), ("mask_rows", ctypes.c_void_p),
+                ("n_masks", ctypes.c_uint64), ("mask_stride", ctypes.c_uint64)]
 
 
 _lib_handle = None
@@ -154,6 +163,10 @@ def _lib():
             L.k3huf_linear_dz.argtypes = [_vp, u32, u64, _vp, u32, u64, u64, u64, u32, _vp, u64, _vp, u32, _vp]
             L.k3huf_linear_grad.argtypes = [_vp, u64, u64, _vp, u64, u64, u64, _vp, u64, _vp, u64, u32, _vp, _vp, _sz, _vp,
                                             u32, _vp]
+            L.k3huf_logits_control.argtypes = [_vp, _vp, u32, u64, u64, u32, _vp, u32, u64, _vp, _vp]
+            L.k3huf_distill.argtypes = [_vp, u32, u64, u64, u32, f32, _vp, _vp, u32, u32, _vp, _vp, _vp, _vp, _vp]
+            L.k3huf_distill_grad.argtypes = [_vp, u32, u64, u64, u32, f32, _vp, _vp, u32, u32, _vp, _vp, _vp, _vp, u64,
+                                             _vp, _vp]
             L.k3huf_strerror.restype = ctypes.c_char_p
             L.k3huf_strerror.argtypes = [ctypes.c_int]
             _lib_handle = L
@@ -432,6 +445,7 @@ def _dtypes():
         import torch
         _types = ({torch.bfloat16: _BF16, torch.float32: _F32}, {torch.int32: 4, torch.int64: 8}, torch.float32, torch.int32,
                   torch.bfloat16)
+
     return _types
 
 
@@ -683,6 +697,96 @@ def linear_grad(x, w, dz, d_status, dx=None, dw=None, scratch=None, accumulate: 
     sp, sb = _given(scratch)
     _check(_lib().k3huf_linear_grad(xp, xs, n, wp, ws, rows, cols, gp, gs, dp, ds, de, qp, sp, sb, _dptr(d_status),
                                     ACCUMULATE if accumulate else 0, _stream(stream)), "k3huf_linear_grad")
+
+
+def logits_control(logits, out, d_status, history=None, spans=None, repetition=None, frequency=None, presence=None,
+                   bias_ids=None, bias_values=None, bias_spans=None, mask=None, mask_rows=None, stream=None) -> None:
+    """Penalties for repeated tokens, biases and grammar masks on the rows of
+    ``logits`` (k3huf_logits_control; bf16 or fp32, n x vocab), into ``out`` (bf16 or
+    fp32, may be logits itself).
+    ``history``: int32 or int64 token ids; ``spans``: int64, n x 3 (from, split, to):
+    row t's prompt is history[from:split], its output history[split:to];
+    ``repetition``, ``frequency``, ``presence``: fp32 of n; ``bias_ids`` (int32 or
+    int64), ``bias_values`` (fp32), ``bias_spans`` (int64, n x 2): row t's biases;
+    ``mask``: int32, states x words, bit j % 32 of word j // 32 allows token j;
+    ``mask_rows``: int32 of n, a row's state, negative for none (None: state t)."""
+    n, vocab = logits.shape
+    xp, xe, xs = _matrix(logits, n, vocab, "logits")
+    yp, ye, ys = _matrix(out, n, vocab, "out")
+    _, sizes, f32, i32, _ = _dtypes()
+    i64 = next(t for t, size in sizes.items() if size == 8)
+    c = Control()
+    if (history is None) != (spans is None):
+        raise ValueError("history and spans go together")
+    if history is None and (repetition is not None or frequency is not None or presence is not None):
+        raise ValueError("penalties need a history")
+    if len({v is None for v in (bias_ids, bias_values, bias_spans)}) != 1:
+        raise ValueError("bias_ids, bias_values and bias_spans go together")
+    if mask is None and mask_rows is not None:
+        raise ValueError("mask_rows without mask")
+    if history is not None:
+        c.history, c.history_id_bytes, c.n_history = _ids(history, "history")
+        c.spans = _dense(spans, (n, 3), "spans", i64)
+        for name, v in (("repetition", repetition), ("frequency", frequency), ("presence", presence)):
+            if v is not None:
+                setattr(c, name, _dense(v, (n,), name, f32))
+    if bias_ids is not None:
+        c.bias_ids, c.bias_id_bytes, c.n_bias = _ids(bias_ids, "bias_ids")
+        c.bias_values = _dense(bias_values, (c.n_bias,), "bias_values", f32)
+        c.bias_spans = _dense(bias_spans, (n, 2), "bias_spans", i64)
+    if mask is not None:
+        c.n_masks, c.mask_stride = mask.shape
+        c.mask = _dense(mask, mask.shape, "mask", i32)
+        if mask_rows is not None:
+            c.mask_rows = _dense(mask_rows, (n,), "mask_rows", i32)
+    _check(_lib().k3huf_logits_control(ctypes.addressof(c), xp, xe, xs, n, vocab, yp, ye, ys, _dptr(d_status),
+                                       _stream(stream)), "k3huf_logits_control")
+
+
+_MODES = {"given": 0, "normalised": 1, "rest": 2}
+
+
+def _mode(mode: str) -> int:
+    if mode not in _MODES:
+        raise ValueError(f"mode: expected one of {tuple(_MODES)}, got {mode!r}")
+    return _MODES[mode]
+
+
+def distill(logits, top_ids, top_logprobs, loss, d_status, lse=None, log_rest=None, mode: str = "given",
+            scale: float = 1.0, stream=None) -> None:
+    """Divergence of softmax(scale * logits) from a teacher's top alternatives, per row
+    (k3huf_distill).  ``logits``: bf16 or fp32, n x vocab; ``top_ids`` (int32, negative
+    for none), ``top_logprobs`` (fp32): n x top, as token_logprobs gives them; ``mode``:
+    their probabilities as given, normalised over the row's alternatives, or with the
+    rest of the mass as one alternative more; ``loss``, ``lse``, ``log_rest`` (mode rest):
+    fp32 of n."""
+    n, vocab = logits.shape
+    xp, xe, xs = _matrix(logits, n, vocab, "logits")
+    _, _, f32, i32, _ = _dtypes()
+    top = top_ids.shape[1]
+    _check(_lib().k3huf_distill(xp, xe, xs, n, vocab, scale, _dense(top_ids, (n, top), "top_ids", i32),
+                                _dense(top_logprobs, (n, top), "top_logprobs", f32), top, _mode(mode),
+                                _dense(loss, (n,), "loss", f32), None if lse is None else _dense(lse, (n,), "lse", f32),
+                                None if log_rest is None else _dense(log_rest, (n,), "log_rest", f32), _dptr(d_status),
+                                _stream(stream)), "k3huf_distill")
+
+
+def distill_grad(logits, top_ids, top_logprobs, lse, g_loss, dlogits, d_status, log_rest=None, mode: str = "given",
+                 scale: float = 1.0, stream=None) -> None:
+    """Gradient of distill with respect to the logits (k3huf_distill_grad), for the
+    gradients of the losses; ``lse`` and (mode rest) ``log_rest`` as the forward gave
+    them.  ``dlogits``: as logits, may be logits itself."""
+    n, vocab = logits.shape
+    xp, xe, xs = _matrix(logits, n, vocab, "logits")
+    dp, _, ds = _matrix(dlogits, n, vocab, "dlogits", xe)
+    _, _, f32, i32, _ = _dtypes()
+    top = top_ids.shape[1]
+    _check(_lib().k3huf_distill_grad(xp, xe, xs, n, vocab, scale, _dense(top_ids, (n, top), "top_ids", i32),
+                                     _dense(top_logprobs, (n, top), "top_logprobs", f32), top, _mode(mode),
+                                     _dense(lse, (n,), "lse", f32),
+                                     None if log_rest is None else _dense(log_rest, (n,), "log_rest", f32),
+                                     _dense(g_loss, (n,), "g_loss", f32), dp, ds, _dptr(d_status), _stream(stream)),
+           "k3huf_distill_grad")
 
 
 class Feed:

@@ -1,0 +1,482 @@
+// Distillation of a row of logits from a teacher's top alternatives, and its gradient.
+//
+// With z = s x the student's scaled logits, p = softmax(z), and q_i = exp(t_i) the teacher's probabilities of its
+// alternatives i (t_i as given, or less their log-sum-exp where the alternatives are taken as the whole):
+//   loss = sum_i q_i (t_i - log p_i)  [ + q_r (log q_r - log p_r) ]
+// where the bracket is the rest's share if it is wanted: q_r = 1 - sum_i q_i, p_r = 1 - sum_i p_i, the sum of the
+// other tokens' p.  With Q = sum_i q_i (+ q_r), g the upstream gradient:
+//   dx_j = s g (Q p_j - q_j) for an alternative,   s g (Q - q_r / p_r) p_j for another token.
+//
+// A loss is what is left of terms far larger than itself, so what there are few of (the alternatives' terms, the
+// rest's mass, the logarithms) is computed in 64 bits; the sum over the vocabulary in 32.  p_r is summed over the
+// other tokens alone, never taken as a difference: a small rest keeps its digits.
+//
+// Forward, one read of the logits: a CTA streams a row, or the CTAs of a cluster when there are fewer rows than the
+// GPU holds CTAs.  To leave the alternatives out of the rest's sum, a filter of one bit per vector (modulo its size)
+// sends the few vectors that may hold one to a comparison with the list.
+//
+// Backward: elementwise; every other token's gradient is s g (Q p_r - q_r) exp(z_j - lse - log p_r), the
+// alternatives' are written over it behind a barrier.
+#include <cooperative_groups.h>
+
+#include <cmath>
+
+#include "k3huf_rows.h"
+
+namespace cg = cooperative_groups;
+
+namespace k3huf {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVecs = 4;                      // 16-byte vectors per thread and step
+constexpr int kMaxCluster = 16;
+constexpr uint32_t kFilterBits = 16384;
+
+struct Sum {
+    float m, sum;                             // sum of 2^((x - m) c)
+};
+__device__ __forceinline__ void rescale(Sum &s, float m, float c) {
+    s.sum *= exp2_fast(max_nan((s.m - m) * c, kFloor));
+    s.m = m;
+}
+__device__ __forceinline__ Sum join(Sum a, Sum b, float c) {
+    const float m = fmaxf(a.m, b.m);
+    rescale(a, m, c);
+    rescale(b, m, c);
+    return {m, a.sum + b.sum};
+}
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+__device__ __forceinline__ double warp_max(double v) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+}
+
+struct Teacher {
+    const int32_t *ids;
+    const float *top;
+    uint32_t count, mode;                     // alternatives per row
+};
+
+// A row's alternatives, by one warp, two per lane (entries lane and lane + 32; id -1: none, q 0).
+struct Alternatives {
+    int32_t id[2];
+    double t[2], q[2];                        // log q (0 for none), q
+    double mass, rest;                        // sum of q; what is left of 1, where that is wanted
+    bool any;
+};
+__device__ __forceinline__ Alternatives alternatives(const Teacher &T, uint64_t row, uint32_t vocab, uint32_t lane, uint32_t *status) {
+    Alternatives A;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const uint32_t i = lane + 32 * e;
+        A.id[e] = i < T.count ? T.ids[row * T.count + i] : -1;
+        if (A.id[e] >= 0 && uint32_t(A.id[e]) >= vocab) {
+            if (status) atomicOr(status, K3HUF_ST_TOKEN);
+            A.id[e] = -1;
+        }
+        A.t[e] = A.id[e] >= 0 ? double(T.top[row * T.count + i]) : -INFINITY;
+    }
+    A.any = __any_sync(0xffffffffu, A.id[0] >= 0 || A.id[1] >= 0);
+    if (T.mode == K3HUF_DISTILL_NORMALISED) {
+        // (largest -infinity: every q is 0; NaN, and +infinity, make the row NaN)
+        const double m = warp_max(fmax(A.t[0], A.t[1]));
+        double sum = 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (A.id[e] >= 0 && !(A.t[e] == -INFINITY)) sum += exp(A.t[e] - m);
+        sum = warp_sum(sum);
+        if (sum > 0 || sum != sum) {
+            const double lse = m + log(sum);
+            A.t[0] -= lse;
+            A.t[1] -= lse;
+        }
+    }
+    double mass = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        A.q[e] = A.id[e] < 0 || A.t[e] == -INFINITY ? 0. : exp(A.t[e]);
+        mass += A.q[e];
+    }
+    A.mass = warp_sum(mass);
+    A.rest = T.mode != K3HUF_DISTILL_REST ? 0. : A.mass > 1. ? 0. : 1. - A.mass;
+    return A;
+}
+
+struct DistillParams {
+    const void *x;
+    Teacher teacher;
+    float *loss, *lse, *log_rest;
+    uint32_t *status;
+    uint64_t stride;
+    uint32_t vocab;
+    float scale, c;                           // c: scale log2 e, finite for every scale
+};
+
+template <typename T, bool kRest>
+__global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillParams P) {
+    constexpr int E = kPer<T>, kWarps = kThreads / 32;
+    __shared__ Sum s_part[kWarps], s_all[kMaxCluster];
+    __shared__ uint32_t s_filter[kRest ? kFilterBits / 32 : 1];
+    __shared__ int32_t s_ids[kRest ? K3HUF_MAX_TOP : 1];
+    const cg::cluster_group cluster = cg::this_cluster();
+    const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank(), row = blockIdx.x / C;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const T *x = static_cast<const T *>(P.x) + uint64_t(row) * P.stride;
+    const float c = P.c;
+    const uint32_t shift = uint32_t(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
+    const uint32_t vecs = (P.vocab + shift + E - 1) / E, K = P.teacher.count;
+    const uint32_t steps = (vecs + kThreads * kVecs - 1) / (kThreads * kVecs);
+    const uint32_t step0 = uint32_t(uint64_t(steps) * rank / C), step1 = uint32_t(uint64_t(steps) * (rank + 1) / C);
+    if (C > 1) cluster_arrive();              // (waited for before the first remote store)
+    uint4 v[kVecs], next[kVecs];
+    auto load = [&](uint4 (&to)[kVecs], uint32_t step) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            const uint32_t at = (step * kVecs + i) * kThreads + tid;
+            to[i] = step < step1 && at < vecs ? load_vec(x, shift, P.vocab, at)
+                                              : (sizeof(T) == 4 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
+                                                                : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u));
+        }
+    };
+    load(next, step0);
+    if constexpr (kRest) {
+        for (uint32_t i = tid; i < kFilterBits / 32; i += kThreads) s_filter[i] = 0;
+        __syncthreads();
+        if (uint32_t(tid) < K) {
+            const int32_t id = P.teacher.ids[uint64_t(row) * K + tid];
+            s_ids[tid] = id;
+            if (id >= 0 && uint32_t(id) < P.vocab) {
+                const uint32_t at = (uint32_t(id) + shift) / E % kFilterBits;
+                atomicOr(&s_filter[at / 32], 1u << (at % 32));
+            }
+        }
+        __syncthreads();
+    }
+    Sum s{-3.402823466e38f, 0.f};             // (not -infinity: then -infinity minus it is -infinity)
+    for (uint32_t step = step0; step < step1; ++step) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) v[i] = next[i];
+        load(next, step + 1);
+        if constexpr (kRest) {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) {
+                const uint32_t at = (step * kVecs + i) * kThreads + tid, bit = at % kFilterBits;
+                if (s_filter[bit / 32] >> (bit % 32) & 1) {
+                    uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    for (uint32_t k = 0; k < K; ++k) {
+                        const int64_t d = int64_t(s_ids[k]) + shift - int64_t(at) * E;
+                        if (s_ids[k] < 0 || d < 0 || d >= E) continue;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            if constexpr (sizeof(T) == 4) {
+                                if (d == u) w[u] = 0xFF800000u;
+                            } else {
+                                if (d == 2 * u) w[u] = (w[u] & 0xFFFF0000u) | 0xFF80u;
+                                if (d == 2 * u + 1) w[u] = (w[u] & 0xFFFFu) | 0xFF800000u;
+                            }
+                        }
+                    }
+                    v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+        float big = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) big = fmaxf(big, vec_max<T>(v[i]));
+        rescale(s, fmaxf(s.m, big), c);
+        const float2 minus_m = make_float2(-s.m, -s.m), cc = make_float2(c, c);
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+            float f[E];
+            unpack<T>(v[i], f);
+#pragma unroll
+            for (int k = 0; k < E; k += 2) {
+                float2 t = __fmul2_rn(__fadd2_rn(make_float2(f[k], f[k + 1]), minus_m), cc);
+                t.x = max_nan(t.x, kFloor);
+                t.y = max_nan(t.y, kFloor);
+                sum = __fadd2_rn(sum, make_float2(exp2_fast(t.x), exp2_fast(t.y)));
+            }
+        }
+        s.sum += sum.x + sum.y;
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d)}, c);
+    if (lane == 0) s_part[warp] = s;
+    __syncthreads();
+    if (C > 1) {
+        cluster_wait();
+        if (tid == 0) {
+            s = s_part[0];
+            for (int w = 1; w < kWarps; ++w) s = join(s, s_part[w], c);
+            cluster.map_shared_rank(s_all, 0)[rank] = s;
+        }
+        cluster_arrive();
+        cluster_wait();
+    }
+    if (rank > 0 || warp > 0) return;
+    if (C == 1) {
+        s = s_part[0];
+        for (int w = 1; w < kWarps; ++w) s = join(s, s_part[w], c);
+    } else {
+        s = s_all[0];
+        for (uint32_t r = 1; r < C; ++r) s = join(s, s_all[r], c);
+    }
+    // one warp: the alternatives' terms
+    const Alternatives A = alternatives(P.teacher, row, P.vocab, lane, P.status);
+    float f[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) f[e] = A.id[e] >= 0 ? ld_f32(x + A.id[e]) : -INFINITY;
+    double m = s.m, total = s.sum, rest = s.sum;
+    if constexpr (kRest) {
+        // the alternatives join the sum, each token once (it counts at its first place)
+        float top = fmaxf(f[0], f[1]);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        if (double(top) > m) {
+            rest *= exp((m - double(top)) * P.scale);
+            m = top;
+        }
+        bool first[2] = {A.id[0] >= 0, A.id[1] >= 0};
+        for (uint32_t k = 0; k + 1 < K; ++k) {
+            const int32_t id = __shfl_sync(0xffffffffu, k < 32 ? A.id[0] : A.id[1], k % 32);
+            if (k < uint32_t(lane) && id == A.id[0]) first[0] = false;
+            if (k < uint32_t(lane) + 32 && id == A.id[1]) first[1] = false;
+        }
+        double mine = 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (first[e] && f[e] != -INFINITY) mine += exp((double(f[e]) - m) * P.scale);
+        total = rest + warp_sum(mine);
+    }
+    const double log_total = log(total);
+    // (a row of -infinity alone: every log p is -infinity)
+    double loss = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (A.id[e] >= 0 && !(A.q[e] == 0.)) loss += A.q[e] * (A.t[e] - (f[e] == -INFINITY && total == total ? -INFINITY : (double(f[e]) - m) * P.scale - log_total));
+    loss = warp_sum(loss);
+    if (lane) return;
+    if constexpr (kRest) {
+        const double log_rest = total == 0. ? -INFINITY : log(rest / total);
+        if (P.log_rest) P.log_rest[row] = float(log_rest);
+        if (A.rest > 0.) loss += A.rest * (log(A.rest) - log_rest);
+    }
+    P.loss[row] = A.any ? float(loss) : 0.f;
+    if (P.lse) P.lse[row] = total == 0. ? -INFINITY : float(m * P.scale + log_total);
+}
+
+struct GradParams {
+    const void *x;
+    void *dx;
+    Teacher teacher;
+    const float *lse, *log_rest, *g;
+    uint32_t *status;
+    uint64_t stride, dx_stride;
+    uint32_t vocab;
+    float scale;
+};
+
+constexpr int kGradVecs = 4;
+
+// kVec: logits and gradients sit alike in their 16-byte blocks
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kThreads) distill_grad_kernel(const GradParams P) {
+    constexpr int E = kVec ? kPer<T> : 1;
+    __shared__ float s_of[3];                 // of every other token: what exp(z - s_of[0]) is multiplied by; whether there is a teacher
+    const uint32_t row = blockIdx.y, lane = threadIdx.x % 32;
+    const T *x = static_cast<const T *>(P.x) + uint64_t(row) * P.stride;
+    T *dx = static_cast<T *>(P.dx) + uint64_t(row) * P.dx_stride;
+    const uint32_t shift = kVec ? uint32_t(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T)) : 0u;
+    const uint32_t vecs = (P.vocab + shift + E - 1) / E;
+    const uint32_t v0 = blockIdx.x * (kThreads * kGradVecs) + threadIdx.x;
+    uint4 v[kGradVecs];
+    float one[kGradVecs];
+#pragma unroll
+    for (int i = 0; i < kGradVecs; ++i)
+        if (v0 + i * kThreads < vecs) {
+            if constexpr (kVec) v[i] = load_vec(x, shift, P.vocab, v0 + i * kThreads);
+            else one[i] = ld_f32(x + v0 + i * kThreads);
+        }
+    // the first warp: the row's factors, and the gradients of the alternatives in this CTA's part
+    float d_top[2];
+    int32_t at_top[2] = {-1, -1};
+    if (threadIdx.x < 32) {
+        const Alternatives A = alternatives(P.teacher, row, P.vocab, lane, blockIdx.x == 0 ? P.status : nullptr);
+        const bool rest = P.teacher.mode == K3HUF_DISTILL_REST;
+        const double lse = P.lse[row], log_rest = rest ? double(P.log_rest[row]) : 0., sg = A.any ? double(P.scale) * P.g[row] : 0., Q = A.mass + A.rest;
+        if (lane == 0) {
+            // (no other token: every p of the rest is 0)
+            const bool some = lse != -INFINITY && log_rest != -INFINITY;
+            s_of[0] = some ? float(lse + log_rest) : 0.f;
+            s_of[1] = !some ? 0.f : float(rest ? sg * (Q * exp(log_rest) - A.rest) : sg * Q);
+            s_of[2] = A.any ? 1.f : 0.f;
+        }
+        const int64_t j0 = int64_t(blockIdx.x) * (kThreads * kGradVecs) * E - shift, j1 = j0 + kThreads * kGradVecs * E;
+        double q[2] = {A.q[0], A.q[1]};
+        bool mine[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) mine[e] = A.id[e] >= 0 && A.id[e] >= j0 && A.id[e] < j1;
+        // a token that is listed more than once: its first place takes all of its q, in their order
+        for (uint32_t k = 0; k < P.teacher.count; ++k) {
+            const int32_t id = __shfl_sync(0xffffffffu, k < 32 ? A.id[0] : A.id[1], k % 32);
+            const double other = __shfl_sync(0xffffffffu, k < 32 ? A.q[0] : A.q[1], k % 32);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (id != A.id[e] || k == lane + 32 * e) continue;
+                if (k < lane + 32 * e) mine[e] = false;
+                else q[e] += other;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (mine[e]) {
+                const float f = ld_f32(x + A.id[e]);
+                const double lp = double(f) * P.scale - lse;
+                const double p = f == -INFINITY ? 0. : lp > 0. ? 1. : exp(lp);
+                at_top[e] = A.id[e];
+                d_top[e] = float(sg * (Q * p - q[e]));
+            }
+    }
+    __syncthreads();
+    const float base = -s_of[0], coef = s_of[1];
+    const bool any = s_of[2] != 0.f;
+    // exp(z - s_of[0]) is 1 at most, as a probability is (see the log probabilities' gradient)
+    auto grad = [&](float2 f) {
+        float2 lp = __ffma2_rn(f, make_float2(P.scale, P.scale), make_float2(base, base));
+        lp.x = min_nan(max_nan(lp.x, kFloor), 0.f);
+        lp.y = min_nan(max_nan(lp.y, kFloor), 0.f);
+        const float2 a = __fmul2_rn(lp, make_float2(kLog2e, kLog2e));
+        return any ? __fmul2_rn(make_float2(exp2_fast(a.x), exp2_fast(a.y)), make_float2(coef, coef)) : make_float2(0.f, 0.f);
+    };
+#pragma unroll
+    for (int i = 0; i < kGradVecs; ++i) {
+        if (v0 + i * kThreads >= vecs) break;
+        if constexpr (kVec) {
+            const int64_t j = int64_t(v0 + i * kThreads) * E - shift;
+            float f[E];
+            unpack<T>(v[i], f);
+#pragma unroll
+            for (int k = 0; k < E; k += 2) {
+                const float2 d = grad(make_float2(f[k], f[k + 1]));
+                f[k] = d.x;
+                f[k + 1] = d.y;
+            }
+            if (j >= 0 && j + E <= int64_t(P.vocab)) {
+                uint4 o;
+                if constexpr (sizeof(T) == 4) {
+                    o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+                } else {
+                    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&o);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) h[k] = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+                }
+                __stcs(reinterpret_cast<uint4 *>(dx + j), o);
+            } else {
+#pragma unroll
+                for (int k = 0; k < E; ++k)
+                    if (j + k >= 0 && j + k < int64_t(P.vocab)) st_f32(dx + j + k, f[k]);
+            }
+        } else {
+            st_f32(dx + v0 + i * kThreads, grad(make_float2(one[i], 0.f)).x);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (at_top[e] >= 0) st_f32(dx + at_top[e], d_top[e]);
+}
+
+template <typename T, bool kRest>
+int launch_forward(const DistillParams &P, uint32_t n, cudaStream_t stream) {
+    constexpr uint32_t kStep = kThreads * kVecs * kPer<T>;
+    static std::atomic<uint64_t> wide{0};
+    uint64_t sms = 0;
+    int rc = once_per_device(wide, [] { return cudaFuncSetAttribute(distill_kernel<T, kRest>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
+    if (!rc) rc = sm_count(&sms);
+    if (rc) return rc;
+    // one CTA per row, or a cluster per row while the GPU has room for more CTAs and every CTA still has a step to do
+    uint32_t C = 1;
+    while (C < uint32_t(kMaxCluster) && uint64_t(n) * C < sms * 2 && P.vocab / kStep >= 2 * C) C *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n * C);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_rc(cudaLaunchKernelEx(&cfg, distill_kernel<T, kRest>, P));
+}
+
+template <typename T>
+int launch_backward(const GradParams &P, uint32_t n, cudaStream_t stream) {
+    const bool vec = (reinterpret_cast<uintptr_t>(P.x) - reinterpret_cast<uintptr_t>(P.dx)) % 16 == 0 && (P.stride - P.dx_stride) * sizeof(T) % 16 == 0;
+    const uint32_t per = kThreads * kGradVecs * (vec ? kPer<T> : 1);
+    // (a row that starts inside a 16-byte block may need one vector more)
+    const uint32_t bx = uint32_t((uint64_t(P.vocab) + (vec ? kPer<T> - 1 : 0) + per - 1) / per);
+    for (uint32_t r0 = 0; r0 < n; r0 += 65535) {
+        GradParams Q = P;
+        Q.x = static_cast<const T *>(P.x) + uint64_t(r0) * P.stride;
+        Q.dx = static_cast<T *>(P.dx) + uint64_t(r0) * P.dx_stride;
+        Q.teacher.ids += uint64_t(r0) * P.teacher.count;
+        Q.teacher.top += uint64_t(r0) * P.teacher.count;
+        Q.lse += r0;
+        if (Q.log_rest) Q.log_rest += r0;
+        Q.g += r0;
+        const dim3 grid(bx, min(65535u, n - r0));
+        if (vec) distill_grad_kernel<T, true><<<grid, kThreads, 0, stream>>>(Q);
+        else distill_grad_kernel<T, false><<<grid, kThreads, 0, stream>>>(Q);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_rc(e);
+    }
+    return K3HUF_OK;
+}
+
+bool common_ok(const void *d_logits, uint32_t type, uint64_t stride, uint64_t n, uint32_t vocab, float scale, const int32_t *d_top_ids, const float *d_top, uint32_t top,
+               uint32_t mode, const uint32_t *d_status) {
+    return elem_ok(type) && vocab && vocab <= 0x7FFFFFFFu && stride >= vocab && d_status && scale > 0.f && std::isfinite(scale) && top && top <= K3HUF_MAX_TOP &&
+           n <= 0x7FFFFFFFull / kMaxCluster && mode <= K3HUF_DISTILL_REST && aligned_to(d_logits, elem_bytes(type)) && aligned_to(d_top_ids, 4) && aligned_to(d_top, 4) &&
+           aligned_to(d_status, 4);
+}
+
+}  // namespace
+}  // namespace k3huf
+
+using namespace k3huf;
+
+extern "C" int k3huf_distill(const void *d_logits, uint32_t type, uint64_t stride, uint64_t n, uint32_t vocab, float scale, const int32_t *d_top_ids,
+                             const float *d_top_logprobs, uint32_t top, uint32_t mode, float *d_loss, float *d_lse, float *d_log_rest, uint32_t *d_status, void *stream) {
+    if (!common_ok(d_logits, type, stride, n, vocab, scale, d_top_ids, d_top_logprobs, top, mode, d_status) || !aligned_to(d_loss, 4) || !aligned_to(d_lse, 4) ||
+        !aligned_to(d_log_rest, 4) || (d_log_rest && mode != K3HUF_DISTILL_REST))
+        return K3HUF_E_ARG;
+    if (n == 0) return K3HUF_OK;
+    if (!d_logits || !d_top_ids || !d_top_logprobs || !d_loss) return K3HUF_E_ARG;
+    const DistillParams P{d_logits, {d_top_ids, d_top_logprobs, top, mode}, d_loss, d_lse, d_log_rest, d_status, stride, vocab, scale, fminf(scale * kLog2e, 3.402823466e38f)};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool rest = mode == K3HUF_DISTILL_REST;
+    if (type == K3HUF_BF16) return rest ? launch_forward<__nv_bfloat16, true>(P, uint32_t(n), st) : launch_forward<__nv_bfloat16, false>(P, uint32_t(n), st);
+    return rest ? launch_forward<float, true>(P, uint32_t(n), st) : launch_forward<float, false>(P, uint32_t(n), st);
+}
+
+extern "C" int k3huf_distill_grad(const void *d_logits, uint32_t type, uint64_t stride, uint64_t n, uint32_t vocab, float scale, const int32_t *d_top_ids,
+                                  const float *d_top_logprobs, uint32_t top, uint32_t mode, const float *d_lse, const float *d_log_rest, const float *d_g_loss, void *d_dlogits,
+                                  uint64_t out_stride, uint32_t *d_status, void *stream) {
+    if (!common_ok(d_logits, type, stride, n, vocab, scale, d_top_ids, d_top_logprobs, top, mode, d_status) || out_stride < vocab || !aligned_to(d_dlogits, elem_bytes(type)) ||
+        !aligned_to(d_lse, 4) || !aligned_to(d_log_rest, 4) || !aligned_to(d_g_loss, 4) || (d_log_rest != nullptr) != (mode == K3HUF_DISTILL_REST))
+        return K3HUF_E_ARG;
+    if (n == 0) return K3HUF_OK;
+    if (!d_logits || !d_dlogits || !d_top_ids || !d_top_logprobs || !d_lse || !d_g_loss || (d_logits == d_dlogits && stride != out_stride)) return K3HUF_E_ARG;
+    const GradParams P{d_logits, d_dlogits, {d_top_ids, d_top_logprobs, top, mode}, d_lse, d_log_rest, d_g_loss, d_status, stride, out_stride, vocab, scale};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return type == K3HUF_BF16 ? launch_backward<__nv_bfloat16>(P, uint32_t(n), st) : launch_backward<float>(P, uint32_t(n), st);
+}

@@ -38,7 +38,7 @@
 
 #include <cmath>
 
-#include "k3huf_ops.h"
+#include "k3huf_rows.h"
 
 namespace cg = cooperative_groups;
 
@@ -51,7 +51,6 @@ constexpr int kMaxCluster = 16;
 constexpr uint32_t kList = 2432;              // keys listed in shared memory
 template <int kThreads> constexpr uint32_t kNotes = kVecs * kThreads;     // vectors noted: a step's
 static_assert(K3HUF_MAX_TOP + (K3HUF_MAX_TOP + 8) * kVecs * 8 <= int(kList), "a counted step's notes and keys");
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // (value, index) order of the top alternatives: larger values first, ties to
 // the lower index.  +0 and -0 are equal and a NaN ranks as -infinity; never 0.
@@ -61,29 +60,10 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 }
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t j) { return (uint64_t(order_of(x)) << 32) | (0xFFFFFFFFu - j); }
 
-// max and min that keep a NaN
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float min_nan(float a, float b) {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // A running softmax state: e_j = 2^((x_j - m) c), sum of e_j, sum of e_j (x_j - m) c.
 struct State {
     float m, sum, dot;
 };
-// An exponent below which 2^x is 0 in fp32, and which times 0 is 0 (minus infinity is not).
-constexpr float kFloor = -2000.f;
 __device__ __forceinline__ void rescale(State &s, float m, float c) {
     const float d = max_nan((s.m - m) * c, kFloor), f = exp2_fast(d);
     s.dot = f * fmaf(d, s.sum, s.dot);
@@ -95,55 +75,6 @@ __device__ __forceinline__ State join(State a, State b, float c) {
     rescale(a, m, c);
     rescale(b, m, c);
     return {m, a.sum + b.sum, a.dot + b.dot};
-}
-
-template <typename T> constexpr int kPer = 16 / int(sizeof(T));       // values per vector
-
-template <typename T>
-__device__ __forceinline__ void unpack(const uint4 v, float (&f)[kPer<T>]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 4) {
-            f[i] = __uint_as_float(w[i]);
-        } else {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ float vec_max(const uint4 v) {
-    if constexpr (sizeof(T) == 4) {
-        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
-    } else {
-        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
-        const __nv_bfloat162 a = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
-        return fmaxf(__low2float(a), __high2float(a));
-    }
-}
-
-// Vector v of a row whose first value sits `shift` values into its 16-byte
-// block: values [v E - shift, v E - shift + E) of the row; those outside the
-// row read as -infinity.
-template <typename T>
-__device__ __forceinline__ uint4 load_vec(const T *row, uint32_t shift, uint32_t n, uint32_t v) {
-    constexpr int E = kPer<T>;
-    const int64_t j = int64_t(v) * E - shift;
-    if (j >= 0 && j + E <= int64_t(n)) return __ldcs(reinterpret_cast<const uint4 *>(row + j));
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (sizeof(T) == 4) {
-            w[i] = j + i >= 0 && j + i < int64_t(n) ? __float_as_uint(row[j + i]) : 0xFF800000u;
-        } else {
-            const uint16_t *p = reinterpret_cast<const uint16_t *>(row);
-            const int64_t a = j + 2 * i, b = a + 1;
-            w[i] = (a >= 0 && a < int64_t(n) ? p[a] : 0xFF80u) | (b >= 0 && b < int64_t(n) ? uint32_t(p[b]) << 16 : 0xFF800000u);
-        }
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // The `k`-th largest key of the CTA's threads (mine: each thread's own), down

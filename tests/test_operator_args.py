@@ -157,3 +157,42 @@ def test_linear_grad(lib):
         assert call(**kw) == k3.E_ARG, kw
     need = k3.linear_scratch_bytes(4, 32, 64, grad=True, any=True)
     assert call(xs=65, ws=65, dzs=33, scratch=P, size=need - 1) == k3.E_ARG
+
+
+def test_logits_control(lib):
+    full = dict(history=P, spans=P, n_history=100, history_id_bytes=8, bias_id_bytes=4, repetition=P, frequency=P, presence=P, bias_ids=P, bias_values=P,
+                bias_spans=P, n_bias=9, mask=P, mask_rows=P, n_masks=2, mask_stride=2)
+
+    def call(x=P, t=1, stride=50, n=3, vocab=50, out=P + 4096, ot=0, os=50, st=P, control=True, **kw):
+        c = k3.Control(**{**full, **kw})
+        return lib.k3huf_logits_control(ctypes.addressof(c) if control else None, x, t, stride, n, vocab, out, ot, os, st, None)
+
+    assert call(n=0) == k3.OK and call(n=0, x=None, out=None) == k3.OK
+    for kw in (dict(control=False), dict(x=None), dict(x=P + 2), dict(t=2), dict(stride=49), dict(vocab=0), dict(vocab=1 << 31, stride=1 << 31, os=1 << 31),
+               dict(n=1 << 31), dict(out=None), dict(out=P + 1), dict(ot=2), dict(os=49), dict(out=P), dict(out=P, ot=1, os=60), dict(st=None), dict(st=P + 2),
+               dict(spans=None), dict(spans=P + 4), dict(n_history=1 << 31), dict(history_id_bytes=2), dict(history=P + 4), dict(repetition=P + 2),
+               dict(frequency=P + 1), dict(presence=P + 2), dict(bias_ids=P + 2), dict(bias_id_bytes=3), dict(bias_values=None), dict(bias_values=P + 2),
+               dict(bias_spans=None), dict(bias_spans=P + 4), dict(n_bias=1 << 31), dict(mask=P + 2), dict(mask_rows=P + 2), dict(mask_stride=1), dict(mask_rows=None)):
+        assert call(**kw) == k3.E_ARG, kw
+
+
+def test_distill(lib):
+    def call(x=P, t=1, stride=50, n=3, vocab=50, scale=1.0, ids=P, lp=P, top=5, mode=2, loss=P, lse=P, rest=P, st=P):
+        return lib.k3huf_distill(x, t, stride, n, vocab, scale, ids, lp, top, mode, loss, lse, rest, st, None)
+
+    assert call(n=0) == k3.OK
+    for kw in (dict(x=None), dict(x=P + 2), dict(t=2), dict(stride=49), dict(n=1 << 27), dict(vocab=0), dict(vocab=1 << 31, stride=1 << 31), dict(scale=0.0),
+               dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(ids=None), dict(ids=P + 2), dict(lp=None), dict(lp=P + 1), dict(top=0),
+               dict(top=65), dict(mode=3), dict(mode=0), dict(mode=1), dict(loss=None), dict(loss=P + 2), dict(lse=P + 2), dict(rest=P + 2), dict(st=None)):
+        assert call(**kw) == k3.E_ARG, kw
+
+
+def test_distill_grad(lib):
+    def call(x=P, t=1, stride=50, n=3, vocab=50, scale=1.0, ids=P, lp=P, top=5, mode=2, lse=P, rest=P, g=P, d=P, ds=50, st=P):
+        return lib.k3huf_distill_grad(x, t, stride, n, vocab, scale, ids, lp, top, mode, lse, rest, g, d, ds, st, None)
+
+    assert call(n=0) == k3.OK
+    for kw in (dict(x=None), dict(x=P + 2), dict(t=2), dict(stride=49), dict(n=1 << 27), dict(vocab=0), dict(scale=0.0), dict(ids=None), dict(lp=None), dict(top=0),
+               dict(top=65), dict(mode=3), dict(mode=0), dict(rest=None), dict(rest=P + 2), dict(lse=None), dict(lse=P + 1), dict(g=None), dict(g=P + 2),
+               dict(d=None), dict(d=P + 2), dict(ds=49), dict(ds=60), dict(st=None)):
+        assert call(**kw) == k3.E_ARG, kw
