@@ -642,7 +642,7 @@ int k3huf_linear_grad(const void *d_x, uint64_t x_stride, uint64_t n_tokens, con
 typedef struct {
     const void *history;          /* n_history token ids, prompts and outputs of the requests */
     const int64_t *spans;         /* n x 3: from, split, to: row t's prompt lies at [from, split) of the history, its output at [split, to) */
-    uint64_t n_history;           /* up to 2^31 - 1, as n_bias */
+    uint64_t n_history;           /* up to 2^30, as n_bias */
     uint32_t history_id_bytes, bias_id_bytes;
     const float *repetition, *frequency, *presence;      /* n floats each, or NULL (1, 0, 0) */
     const void *bias_ids;         /* n_bias token ids ... */

@@ -19,6 +19,7 @@
 // alternatives' are written over it behind a barrier.
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "k3huf_rows.h"
@@ -28,7 +29,8 @@ namespace cg = cooperative_groups;
 namespace k3huf {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;                 // that stream; one warp more sees to the alternatives
+constexpr int kAll = kThreads + 32;
 constexpr int kVecs = 4;                      // 16-byte vectors per thread and step
 constexpr int kMaxCluster = 16;
 constexpr uint32_t kFilterBits = 16384;
@@ -119,10 +121,49 @@ struct DistillParams {
     float scale, c;                           // c: scale log2 e, finite for every scale
 };
 
+// What the alternatives give to the loss, by the warp that does not stream, while the others do.
+struct Terms {
+    double sum, mass, rest;                   // sum of q (t - s (x - from)); of q; the rest's q
+    double top, from, top_sum;                // the largest of their logits; the same if it is finite, else 0; sum of exp(s (x - top)), each token once
+    uint32_t any;
+};
 template <typename T, bool kRest>
-__global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillParams P) {
+__device__ Terms terms(const DistillParams &P, const T *x, uint64_t row, uint32_t lane) {
+    const Alternatives A = alternatives(P.teacher, row, P.vocab, lane, P.status);
+    Terms R{0., A.mass, A.rest, 0., 0., 0., A.any};
+    float f[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) f[e] = A.id[e] >= 0 ? ld_f32(x + A.id[e]) : -INFINITY;
+    float top = fmaxf(f[0], f[1]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    R.top = top;
+    R.from = isfinite(top) ? R.top : 0.;      // (logits of 1e38 would leave nothing of t beside them)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (A.id[e] >= 0 && !(A.q[e] == 0.)) R.sum += A.q[e] * (A.t[e] - (double(f[e]) - R.from) * P.scale);
+    R.sum = warp_sum(R.sum);
+    if constexpr (kRest) {
+        // (a token that is listed twice counts at its first place)
+        bool first[2] = {A.id[0] >= 0, A.id[1] >= 0};
+        for (uint32_t k = 0; k + 1 < P.teacher.count; ++k) {
+            const int32_t id = __shfl_sync(0xffffffffu, k < 32 ? A.id[0] : A.id[1], k % 32);
+            if (k < lane && id == A.id[0]) first[0] = false;
+            if (k < lane + 32 && id == A.id[1]) first[1] = false;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (first[e] && f[e] != -INFINITY) R.top_sum += exp((double(f[e]) - R.top) * P.scale);
+        R.top_sum = warp_sum(R.top_sum);
+    }
+    return R;
+}
+
+template <typename T, bool kRest>
+__global__ void __launch_bounds__(kAll, 3) distill_kernel(const DistillParams P) {
     constexpr int E = kPer<T>, kWarps = kThreads / 32;
     __shared__ Sum s_part[kWarps], s_all[kMaxCluster];
+    __shared__ Terms s_terms;
     __shared__ uint32_t s_filter[kRest ? kFilterBits / 32 : 1];
     __shared__ int32_t s_ids[kRest ? K3HUF_MAX_TOP : 1];
     const cg::cluster_group cluster = cg::this_cluster();
@@ -145,9 +186,9 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillParam
                                                                 : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u));
         }
     };
-    load(next, step0);
+    if (warp < kWarps) load(next, step0);
     if constexpr (kRest) {
-        for (uint32_t i = tid; i < kFilterBits / 32; i += kThreads) s_filter[i] = 0;
+        for (uint32_t i = tid; i < kFilterBits / 32; i += kAll) s_filter[i] = 0;
         __syncthreads();
         if (uint32_t(tid) < K) {
             const int32_t id = P.teacher.ids[uint64_t(row) * K + tid];
@@ -159,118 +200,102 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const DistillParam
         }
         __syncthreads();
     }
-    Sum s{-3.402823466e38f, 0.f};             // (not -infinity: then -infinity minus it is -infinity)
-    for (uint32_t step = step0; step < step1; ++step) {
+    if (warp == kWarps) {
+        if (rank == 0) {
+            const Terms R = terms<T, kRest>(P, x, row, lane);
+            if (lane == 0) s_terms = R;
+        }
+    } else {
+        Sum s{-3.402823466e38f, 0.f};         // (not -infinity: then -infinity minus it is -infinity)
+        for (uint32_t step = step0; step < step1; ++step) {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) v[i] = next[i];
-        load(next, step + 1);
-        if constexpr (kRest) {
+            for (int i = 0; i < kVecs; ++i) v[i] = next[i];
+            load(next, step + 1);
+            if constexpr (kRest) {
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                const uint32_t at = (step * kVecs + i) * kThreads + tid, bit = at % kFilterBits;
-                if (s_filter[bit / 32] >> (bit % 32) & 1) {
-                    uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                    for (uint32_t k = 0; k < K; ++k) {
-                        const int64_t d = int64_t(s_ids[k]) + shift - int64_t(at) * E;
-                        if (s_ids[k] < 0 || d < 0 || d >= E) continue;
+                for (int i = 0; i < kVecs; ++i) {
+                    const uint32_t at = (step * kVecs + i) * kThreads + tid, bit = at % kFilterBits;
+                    if (s_filter[bit / 32] >> (bit % 32) & 1) {
+                        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        for (uint32_t k = 0; k < K; ++k) {
+                            const int64_t d = int64_t(s_ids[k]) + shift - int64_t(at) * E;
+                            if (s_ids[k] < 0 || d < 0 || d >= E) continue;
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            if constexpr (sizeof(T) == 4) {
-                                if (d == u) w[u] = 0xFF800000u;
-                            } else {
-                                if (d == 2 * u) w[u] = (w[u] & 0xFFFF0000u) | 0xFF80u;
-                                if (d == 2 * u + 1) w[u] = (w[u] & 0xFFFFu) | 0xFF800000u;
+                            for (int u = 0; u < 4; ++u) {
+                                if constexpr (sizeof(T) == 4) {
+                                    if (d == u) w[u] = 0xFF800000u;
+                                } else {
+                                    if (d == 2 * u) w[u] = (w[u] & 0xFFFF0000u) | 0xFF80u;
+                                    if (d == 2 * u + 1) w[u] = (w[u] & 0xFFFFu) | 0xFF800000u;
+                                }
                             }
                         }
+                        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    v[i] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
-        }
-        float big = -INFINITY;
+            float big = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) big = fmaxf(big, vec_max<T>(v[i]));
-        rescale(s, fmaxf(s.m, big), c);
-        const float2 minus_m = make_float2(-s.m, -s.m), cc = make_float2(c, c);
-        float2 sum = make_float2(0.f, 0.f);
+            for (int i = 0; i < kVecs; ++i) big = fmaxf(big, vec_max<T>(v[i]));
+            rescale(s, fmaxf(s.m, big), c);
+            const float2 minus_m = make_float2(-s.m, -s.m), cc = make_float2(c, c);
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            float f[E];
-            unpack<T>(v[i], f);
+            for (int i = 0; i < kVecs; ++i) {
+                float f[E];
+                unpack<T>(v[i], f);
 #pragma unroll
-            for (int k = 0; k < E; k += 2) {
-                float2 t = __fmul2_rn(__fadd2_rn(make_float2(f[k], f[k + 1]), minus_m), cc);
-                t.x = max_nan(t.x, kFloor);
-                t.y = max_nan(t.y, kFloor);
-                sum = __fadd2_rn(sum, make_float2(exp2_fast(t.x), exp2_fast(t.y)));
+                for (int k = 0; k < E; k += 2) {
+                    float2 t = __fmul2_rn(__fadd2_rn(make_float2(f[k], f[k + 1]), minus_m), cc);
+                    t.x = max_nan(t.x, kFloor);
+                    t.y = max_nan(t.y, kFloor);
+                    sum = __fadd2_rn(sum, make_float2(exp2_fast(t.x), exp2_fast(t.y)));
+                }
             }
+            s.sum += sum.x + sum.y;
         }
-        s.sum += sum.x + sum.y;
-    }
 #pragma unroll
-    for (int d = 16; d; d >>= 1) s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d)}, c);
-    if (lane == 0) s_part[warp] = s;
+        for (int d = 16; d; d >>= 1) s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d)}, c);
+        if (lane == 0) s_part[warp] = s;
+    }
     __syncthreads();
+    if (C == 1 && warp > 0) return;
+    // one warp: the warps' sums, then the CTAs'
+    Sum s = s_part[lane % kWarps];
+#pragma unroll
+    for (int d = kWarps / 2; d; d >>= 1) s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d)}, c);
     if (C > 1) {
         cluster_wait();
-        if (tid == 0) {
-            s = s_part[0];
-            for (int w = 1; w < kWarps; ++w) s = join(s, s_part[w], c);
-            cluster.map_shared_rank(s_all, 0)[rank] = s;
-        }
+        if (tid == 0) cluster.map_shared_rank(s_all, 0)[rank] = s;
         cluster_arrive();
         cluster_wait();
-    }
-    if (rank > 0 || warp > 0) return;
-    if (C == 1) {
-        s = s_part[0];
-        for (int w = 1; w < kWarps; ++w) s = join(s, s_part[w], c);
-    } else {
-        s = s_all[0];
-        for (uint32_t r = 1; r < C; ++r) s = join(s, s_all[r], c);
-    }
-    // one warp: the alternatives' terms
-    const Alternatives A = alternatives(P.teacher, row, P.vocab, lane, P.status);
-    float f[2];
+        if (rank > 0 || warp > 0) return;
+        s = uint32_t(lane) < C ? s_all[lane] : Sum{-3.402823466e38f, 0.f};
 #pragma unroll
-    for (int e = 0; e < 2; ++e) f[e] = A.id[e] >= 0 ? ld_f32(x + A.id[e]) : -INFINITY;
-    double m = s.m, total = s.sum, rest = s.sum;
+        for (int d = kMaxCluster / 2; d; d >>= 1) s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d)}, c);
+    }
+    const Terms R = s_terms;
+    double m = s.m, rest = s.sum, total = rest;
     if constexpr (kRest) {
-        // the alternatives join the sum, each token once (it counts at its first place)
-        float top = fmaxf(f[0], f[1]);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        if (double(top) > m) {
-            rest *= exp((m - double(top)) * P.scale);
-            m = top;
-        }
-        bool first[2] = {A.id[0] >= 0, A.id[1] >= 0};
-        for (uint32_t k = 0; k + 1 < K; ++k) {
-            const int32_t id = __shfl_sync(0xffffffffu, k < 32 ? A.id[0] : A.id[1], k % 32);
-            if (k < uint32_t(lane) && id == A.id[0]) first[0] = false;
-            if (k < uint32_t(lane) + 32 && id == A.id[1]) first[1] = false;
-        }
-        double mine = 0;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (first[e] && f[e] != -INFINITY) mine += exp((double(f[e]) - m) * P.scale);
-        total = rest + warp_sum(mine);
+        m = fmax(m, R.top);
+        // (a lane each: the two sums, then the logarithms)
+        const double f = exp(((lane ? R.top : double(s.m)) - m) * P.scale), scaled = lane ? (R.top_sum == 0. ? 0. : R.top_sum * f) : rest * f;
+        rest = __shfl_sync(0xffffffffu, scaled, 0);
+        total = rest + __shfl_sync(0xffffffffu, scaled, 1);
     }
-    const double log_total = log(total);
-    // (a row of -infinity alone: every log p is -infinity)
-    double loss = 0;
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-        if (A.id[e] >= 0 && !(A.q[e] == 0.)) loss += A.q[e] * (A.t[e] - (f[e] == -INFINITY && total == total ? -INFINITY : (double(f[e]) - m) * P.scale - log_total));
-    loss = warp_sum(loss);
+    const double logs = log(lane == 0 ? total : lane == 1 ? rest / total : R.rest);
+    const double log_total = __shfl_sync(0xffffffffu, logs, 0), log_q = __shfl_sync(0xffffffffu, logs, 2);
+    const double log_rest = total == 0. ? -INFINITY : __shfl_sync(0xffffffffu, logs, 1);
     if (lane) return;
+    const double lse = total == 0. ? -INFINITY : m * P.scale + log_total;
+    // (a row of -infinity alone: every log p is -infinity)
+    double loss = total != 0. ? R.sum + R.mass * ((m - R.from) * P.scale + log_total) : R.mass == 0. ? 0. : R.mass * INFINITY;
     if constexpr (kRest) {
-        const double log_rest = total == 0. ? -INFINITY : log(rest / total);
         if (P.log_rest) P.log_rest[row] = float(log_rest);
-        if (A.rest > 0.) loss += A.rest * (log(A.rest) - log_rest);
+        if (R.rest > 0.) loss += R.rest * (log_q - log_rest);
     }
-    P.loss[row] = A.any ? float(loss) : 0.f;
-    if (P.lse) P.lse[row] = total == 0. ? -INFINITY : float(m * P.scale + log_total);
+    P.loss[row] = R.any ? float(loss) : 0.f;
+    if (P.lse) P.lse[row] = float(lse);
 }
 
 struct GradParams {
@@ -279,119 +304,180 @@ struct GradParams {
     Teacher teacher;
     const float *lse, *log_rest, *g;
     uint32_t *status;
-    uint64_t stride, dx_stride;
-    uint32_t vocab;
+    uint64_t stride, dx_stride, n;
+    uint32_t vocab, steps, parts, per;        // steps of a row, in so many pieces of so many
     float scale;
 };
 
-constexpr int kGradVecs = 4;
+constexpr int kGradVecs = 4, kGradPerSm = 3;
+constexpr uint32_t kGradSteps = 4;            // steps of a CTA on one row
+
+// One piece of work: some steps of a row.
+struct Piece {
+    uint64_t row;
+    uint32_t step, steps;                     // the first, and the one behind the last
+};
 
 // kVec: logits and gradients sit alike in their 16-byte blocks
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads) distill_grad_kernel(const GradParams P) {
+__global__ void __launch_bounds__(kAll, kGradPerSm) distill_grad_kernel(const GradParams P) {
     constexpr int E = kVec ? kPer<T> : 1;
-    __shared__ float s_of[3];                 // of every other token: what exp(z - s_of[0]) is multiplied by; whether there is a teacher
-    const uint32_t row = blockIdx.y, lane = threadIdx.x % 32;
-    const T *x = static_cast<const T *>(P.x) + uint64_t(row) * P.stride;
-    T *dx = static_cast<T *>(P.dx) + uint64_t(row) * P.dx_stride;
-    const uint32_t shift = kVec ? uint32_t(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T)) : 0u;
-    const uint32_t vecs = (P.vocab + shift + E - 1) / E;
-    const uint32_t v0 = blockIdx.x * (kThreads * kGradVecs) + threadIdx.x;
-    uint4 v[kGradVecs];
-    float one[kGradVecs];
-#pragma unroll
-    for (int i = 0; i < kGradVecs; ++i)
-        if (v0 + i * kThreads < vecs) {
-            if constexpr (kVec) v[i] = load_vec(x, shift, P.vocab, v0 + i * kThreads);
-            else one[i] = ld_f32(x + v0 + i * kThreads);
-        }
-    // the first warp: the row's factors, and the gradients of the alternatives in this CTA's part
-    float d_top[2];
-    int32_t at_top[2] = {-1, -1};
-    if (threadIdx.x < 32) {
-        const Alternatives A = alternatives(P.teacher, row, P.vocab, lane, blockIdx.x == 0 ? P.status : nullptr);
-        const bool rest = P.teacher.mode == K3HUF_DISTILL_REST;
-        const double lse = P.lse[row], log_rest = rest ? double(P.log_rest[row]) : 0., sg = A.any ? double(P.scale) * P.g[row] : 0., Q = A.mass + A.rest;
-        if (lane == 0) {
-            // (no other token: every p of the rest is 0)
-            const bool some = lse != -INFINITY && log_rest != -INFINITY;
-            s_of[0] = some ? float(lse + log_rest) : 0.f;
-            s_of[1] = !some ? 0.f : float(rest ? sg * (Q * exp(log_rest) - A.rest) : sg * Q);
-            s_of[2] = A.any ? 1.f : 0.f;
-        }
-        const int64_t j0 = int64_t(blockIdx.x) * (kThreads * kGradVecs) * E - shift, j1 = j0 + kThreads * kGradVecs * E;
-        double q[2] = {A.q[0], A.q[1]};
-        bool mine[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) mine[e] = A.id[e] >= 0 && A.id[e] >= j0 && A.id[e] < j1;
-        // a token that is listed more than once: its first place takes all of its q, in their order
-        for (uint32_t k = 0; k < P.teacher.count; ++k) {
-            const int32_t id = __shfl_sync(0xffffffffu, k < 32 ? A.id[0] : A.id[1], k % 32);
-            const double other = __shfl_sync(0xffffffffu, k < 32 ? A.q[0] : A.q[1], k % 32);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (id != A.id[e] || k == lane + 32 * e) continue;
-                if (k < lane + 32 * e) mine[e] = false;
-                else q[e] += other;
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (mine[e]) {
-                const float f = ld_f32(x + A.id[e]);
-                const double lp = double(f) * P.scale - lse;
-                const double p = f == -INFINITY ? 0. : lp > 0. ? 1. : exp(lp);
-                at_top[e] = A.id[e];
-                d_top[e] = float(sg * (Q * p - q[e]));
-            }
-    }
-    __syncthreads();
-    const float base = -s_of[0], coef = s_of[1];
-    const bool any = s_of[2] != 0.f;
-    // exp(z - s_of[0]) is 1 at most, as a probability is (see the log probabilities' gradient)
-    auto grad = [&](float2 f) {
-        float2 lp = __ffma2_rn(f, make_float2(P.scale, P.scale), make_float2(base, base));
-        lp.x = min_nan(max_nan(lp.x, kFloor), 0.f);
-        lp.y = min_nan(max_nan(lp.y, kFloor), 0.f);
-        const float2 a = __fmul2_rn(lp, make_float2(kLog2e, kLog2e));
-        return any ? __fmul2_rn(make_float2(exp2_fast(a.x), exp2_fast(a.y)), make_float2(coef, coef)) : make_float2(0.f, 0.f);
+    constexpr uint32_t kStep = kThreads * kGradVecs;          // vectors of a step
+    // of every other token: what exp(z - the first) is multiplied by; whether there is a teacher.  (This piece's and the next one's)
+    __shared__ float s_of[2][3];
+    const uint32_t tid = threadIdx.x, lane = tid % 32;
+    auto row_of = [&](uint64_t row) { return static_cast<const T *>(P.x) + row * P.stride; };
+    auto out_of = [&](uint64_t row) { return static_cast<T *>(P.dx) + row * P.dx_stride; };
+    auto shift_of = [&](const T *x) { return kVec ? uint32_t(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T)) : 0u; };
+    const uint64_t pieces = P.n * P.parts;
+    auto piece_of = [&](uint64_t i) {
+        const uint32_t part = uint32_t(i % P.parts);
+        return Piece{i / P.parts, part * P.per, min((part + 1) * P.per, P.steps)};
     };
-#pragma unroll
-    for (int i = 0; i < kGradVecs; ++i) {
-        if (v0 + i * kThreads >= vecs) break;
-        if constexpr (kVec) {
-            const int64_t j = int64_t(v0 + i * kThreads) * E - shift;
-            float f[E];
-            unpack<T>(v[i], f);
-#pragma unroll
-            for (int k = 0; k < E; k += 2) {
-                const float2 d = grad(make_float2(f[k], f[k + 1]));
-                f[k] = d.x;
-                f[k + 1] = d.y;
+    if (tid >= kThreads) {
+        // this warp: a piece's factors, and the gradients of the alternatives in it, a piece ahead of the others;
+        // those of the alternatives are written when the others are done with the piece
+        float d_top[2], d_next[2];
+        int32_t at_top[2] = {-1, -1}, at_next[2];
+        uint64_t row = 0;
+        auto prepare = [&](uint64_t i) {
+            at_next[0] = at_next[1] = -1;
+            if (i >= pieces) return;
+            const Piece p = piece_of(i);
+            const T *x = row_of(p.row);
+            const Alternatives A = alternatives(P.teacher, p.row, P.vocab, lane, p.step == 0 ? P.status : nullptr);
+            const bool rest = P.teacher.mode == K3HUF_DISTILL_REST;
+            const double lse = P.lse[p.row], log_rest = rest ? double(P.log_rest[p.row]) : 0., sg = A.any ? double(P.scale) * P.g[p.row] : 0., Q = A.mass + A.rest;
+            if (lane == 0) {
+                // (no other token: every p of the rest is 0)
+                const bool some = lse != -INFINITY && log_rest != -INFINITY;
+                float *of = s_of[i / gridDim.x & 1];
+                of[0] = some ? float(lse + log_rest) : 0.f;
+                of[1] = !some ? 0.f : float(rest ? sg * (Q * exp(log_rest) - A.rest) : sg * Q);
+                of[2] = A.any ? 1.f : 0.f;
             }
-            if (j >= 0 && j + E <= int64_t(P.vocab)) {
-                uint4 o;
-                if constexpr (sizeof(T) == 4) {
-                    o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-                } else {
-                    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&o);
+            const int64_t shift = shift_of(x), j0 = int64_t(p.step) * kStep * E - shift, j1 = int64_t(p.steps) * kStep * E - shift;
+            double q[2] = {A.q[0], A.q[1]};
+            bool mine[2];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) h[k] = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+            for (int e = 0; e < 2; ++e) mine[e] = A.id[e] >= 0 && A.id[e] >= j0 && A.id[e] < j1;
+            // a token that is listed more than once: its first place takes all of its q, in their order
+            for (uint32_t k = 0; k < P.teacher.count; ++k) {
+                const int32_t id = __shfl_sync(0xffffffffu, k < 32 ? A.id[0] : A.id[1], k % 32);
+                const double other = __shfl_sync(0xffffffffu, k < 32 ? A.q[0] : A.q[1], k % 32);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (id != A.id[e] || k == lane + 32 * e) continue;
+                    if (k < lane + 32 * e) mine[e] = false;
+                    else q[e] += other;
                 }
-                __stcs(reinterpret_cast<uint4 *>(dx + j), o);
-            } else {
-#pragma unroll
-                for (int k = 0; k < E; ++k)
-                    if (j + k >= 0 && j + k < int64_t(P.vocab)) st_f32(dx + j + k, f[k]);
             }
-        } else {
-            st_f32(dx + v0 + i * kThreads, grad(make_float2(one[i], 0.f)).x);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (mine[e]) {
+                    const float f = ld_f32(x + A.id[e]);
+                    const double lp = double(f) * P.scale - lse;
+                    const double prob = f == -INFINITY ? 0. : lp > 0. ? 1. : exp(lp);
+                    at_next[e] = A.id[e];
+                    d_next[e] = float(sg * (Q * prob - q[e]));
+                }
+        };
+        auto write = [&]() {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (at_top[e] >= 0) st_f32(out_of(row) + at_top[e], d_top[e]);
+        };
+        prepare(blockIdx.x);
+        for (uint64_t i = blockIdx.x; i < pieces; i += gridDim.x) {
+            __syncthreads();
+            write();                          // (of the piece before)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) at_top[e] = at_next[e], d_top[e] = d_next[e];
+            row = i / P.parts;
+            prepare(i + gridDim.x);
+        }
+        __syncthreads();
+        write();
+        return;
+    }
+    uint4 v[kGradVecs], next[kGradVecs];
+    auto load = [&](uint4 (&to)[kGradVecs], uint64_t row, uint32_t step) {
+        const T *x = row_of(row);
+        const uint32_t shift = shift_of(x), vecs = (P.vocab + shift + E - 1) / E;
+#pragma unroll
+        for (int i = 0; i < kGradVecs; ++i) {
+            const uint32_t at = step * kStep + i * kThreads + tid;
+            if (at >= vecs) continue;
+            if constexpr (kVec) to[i] = load_vec(x, shift, P.vocab, at);
+            else to[i].x = __float_as_uint(ld_f32(x + at));
+        }
+    };
+    if (blockIdx.x < pieces) {
+        const Piece p = piece_of(blockIdx.x);
+        load(next, p.row, p.step);
+    }
+    for (uint64_t i = blockIdx.x; i < pieces; i += gridDim.x) {
+        const Piece p = piece_of(i);
+        const T *x = row_of(p.row);
+        T *dx = out_of(p.row);
+        const uint32_t shift = shift_of(x), vecs = (P.vocab + shift + E - 1) / E;
+        __syncthreads();
+        const float *of = s_of[i / gridDim.x & 1];
+        const float base = -of[0], coef = of[1];
+        const bool any = of[2] != 0.f;
+        // exp(z - the sum's logarithm) is 1 at most, as a probability is (see the log probabilities' gradient)
+        auto grad = [&](float2 f) {
+            float2 lp = __ffma2_rn(f, make_float2(P.scale, P.scale), make_float2(base, base));
+            lp.x = min_nan(max_nan(lp.x, kFloor), 0.f);
+            lp.y = min_nan(max_nan(lp.y, kFloor), 0.f);
+            const float2 a = __fmul2_rn(lp, make_float2(kLog2e, kLog2e));
+            return any ? __fmul2_rn(make_float2(exp2_fast(a.x), exp2_fast(a.y)), make_float2(coef, coef)) : make_float2(0.f, 0.f);
+        };
+        for (uint32_t step = p.step; step < p.steps; ++step) {
+#pragma unroll
+            for (int k = 0; k < kGradVecs; ++k) v[k] = next[k];
+            if (step + 1 < p.steps) {
+                load(next, p.row, step + 1);
+            } else if (i + gridDim.x < pieces) {
+                const Piece q = piece_of(i + gridDim.x);
+                load(next, q.row, q.step);
+            }
+#pragma unroll
+            for (int m = 0; m < kGradVecs; ++m) {
+                const uint32_t at = step * kStep + m * kThreads + tid;
+                if (at >= vecs) break;
+                if constexpr (kVec) {
+                    const int64_t j = int64_t(at) * E - shift;
+                    float f[E];
+                    unpack<T>(v[m], f);
+#pragma unroll
+                    for (int k = 0; k < E; k += 2) {
+                        const float2 d = grad(make_float2(f[k], f[k + 1]));
+                        f[k] = d.x;
+                        f[k + 1] = d.y;
+                    }
+                    if (j >= 0 && j + E <= int64_t(P.vocab)) {
+                        uint4 o;
+                        if constexpr (sizeof(T) == 4) {
+                            o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+                        } else {
+                            __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&o);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) h[k] = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+                        }
+                        __stcs(reinterpret_cast<uint4 *>(dx + j), o);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < E; ++k)
+                            if (j + k >= 0 && j + k < int64_t(P.vocab)) st_f32(dx + j + k, f[k]);
+                    }
+                } else {
+                    st_f32(dx + at, grad(make_float2(__uint_as_float(v[m].x), 0.f)).x);
+                }
+            }
         }
     }
     __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-        if (at_top[e] >= 0) st_f32(dx + at_top[e], d_top[e]);
 }
 
 template <typename T, bool kRest>
@@ -407,7 +493,7 @@ int launch_forward(const DistillParams &P, uint32_t n, cudaStream_t stream) {
     while (C < uint32_t(kMaxCluster) && uint64_t(n) * C < sms * 2 && P.vocab / kStep >= 2 * C) C *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n * C);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kAll);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -419,27 +505,22 @@ int launch_forward(const DistillParams &P, uint32_t n, cudaStream_t stream) {
 }
 
 template <typename T>
-int launch_backward(const GradParams &P, uint32_t n, cudaStream_t stream) {
+int launch_backward(GradParams P, cudaStream_t stream) {
     const bool vec = (reinterpret_cast<uintptr_t>(P.x) - reinterpret_cast<uintptr_t>(P.dx)) % 16 == 0 && (P.stride - P.dx_stride) * sizeof(T) % 16 == 0;
-    const uint32_t per = kThreads * kGradVecs * (vec ? kPer<T> : 1);
+    uint64_t sms = 0;
+    const int rc = sm_count(&sms);
+    if (rc) return rc;
+    const uint64_t per = uint64_t(kThreads) * kGradVecs * (vec ? kPer<T> : 1);
     // (a row that starts inside a 16-byte block may need one vector more)
-    const uint32_t bx = uint32_t((uint64_t(P.vocab) + (vec ? kPer<T> - 1 : 0) + per - 1) / per);
-    for (uint32_t r0 = 0; r0 < n; r0 += 65535) {
-        GradParams Q = P;
-        Q.x = static_cast<const T *>(P.x) + uint64_t(r0) * P.stride;
-        Q.dx = static_cast<T *>(P.dx) + uint64_t(r0) * P.dx_stride;
-        Q.teacher.ids += uint64_t(r0) * P.teacher.count;
-        Q.teacher.top += uint64_t(r0) * P.teacher.count;
-        Q.lse += r0;
-        if (Q.log_rest) Q.log_rest += r0;
-        Q.g += r0;
-        const dim3 grid(bx, min(65535u, n - r0));
-        if (vec) distill_grad_kernel<T, true><<<grid, kThreads, 0, stream>>>(Q);
-        else distill_grad_kernel<T, false><<<grid, kThreads, 0, stream>>>(Q);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return cuda_rc(e);
-    }
-    return K3HUF_OK;
+    P.steps = uint32_t((uint64_t(P.vocab) + (vec ? kPer<T> - 1 : 0) + per - 1) / per);
+    // pieces of kGradSteps steps, or fewer while the GPU's CTAs would not all have one
+    P.per = std::min(kGradSteps, P.steps);
+    while (P.per > 1 && P.n * ((P.steps + P.per - 1) / P.per) < sms * kGradPerSm) --P.per;
+    P.parts = (P.steps + P.per - 1) / P.per;
+    const uint32_t grid = uint32_t(std::min<uint64_t>(P.n * P.parts, sms * kGradPerSm));
+    if (vec) distill_grad_kernel<T, true><<<grid, kAll, 0, stream>>>(P);
+    else distill_grad_kernel<T, false><<<grid, kAll, 0, stream>>>(P);
+    return cuda_rc(cudaGetLastError());
 }
 
 bool common_ok(const void *d_logits, uint32_t type, uint64_t stride, uint64_t n, uint32_t vocab, float scale, const int32_t *d_top_ids, const float *d_top, uint32_t top,
@@ -476,7 +557,7 @@ extern "C" int k3huf_distill_grad(const void *d_logits, uint32_t type, uint64_t 
         return K3HUF_E_ARG;
     if (n == 0) return K3HUF_OK;
     if (!d_logits || !d_dlogits || !d_top_ids || !d_top_logprobs || !d_lse || !d_g_loss || (d_logits == d_dlogits && stride != out_stride)) return K3HUF_E_ARG;
-    const GradParams P{d_logits, d_dlogits, {d_top_ids, d_top_logprobs, top, mode}, d_lse, d_log_rest, d_g_loss, d_status, stride, out_stride, vocab, scale};
+    const GradParams P{d_logits, d_dlogits, {d_top_ids, d_top_logprobs, top, mode}, d_lse, d_log_rest, d_g_loss, d_status, stride, out_stride, n, vocab, 0, 0, 0, scale};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return type == K3HUF_BF16 ? launch_backward<__nv_bfloat16>(P, uint32_t(n), st) : launch_backward<float>(P, uint32_t(n), st);
+    return type == K3HUF_BF16 ? launch_backward<__nv_bfloat16>(P, st) : launch_backward<float>(P, st);
 }

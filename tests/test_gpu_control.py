@@ -152,6 +152,18 @@ def test_histories_of_every_length(history):
         assert check(x, c, bits, in_place=in_place) == 0
 
 
+def test_every_token_touched():
+    """More touched tokens than are looked after at once, and more than 2^16 of a part."""
+    r = np.random.default_rng(3)
+    for V in (131072, 150001):
+        x, c, _ = case(2, V, seed=11, history=10, bias=4)
+        all_of_them = np.concatenate([r.permutation(V), r.integers(0, V, 5000)])
+        c["history"] = torch.from_numpy(all_of_them.astype(np.int32)).cuda()
+        c["spans"] = torch.tensor([[0, 60000, len(all_of_them)], [V // 3, V // 2, V]], device="cuda")
+        for in_place in (False, True):
+            assert check(x, c, None, in_place=in_place) == 0
+
+
 def test_each_part_alone():
     for drop in (("repetition",), ("frequency",), ("presence",), ("repetition", "frequency", "presence"), ("bias_ids", "bias_values", "bias_spans"),
                  ("history", "spans", "repetition", "frequency", "presence"), ("mask", "mask_rows")):

@@ -170,9 +170,9 @@ def test_logits_control(lib):
     assert call(n=0) == k3.OK and call(n=0, x=None, out=None) == k3.OK
     for kw in (dict(control=False), dict(x=None), dict(x=P + 2), dict(t=2), dict(stride=49), dict(vocab=0), dict(vocab=1 << 31, stride=1 << 31, os=1 << 31),
                dict(n=1 << 31), dict(out=None), dict(out=P + 1), dict(ot=2), dict(os=49), dict(out=P), dict(out=P, ot=1, os=60), dict(st=None), dict(st=P + 2),
-               dict(spans=None), dict(spans=P + 4), dict(n_history=1 << 31), dict(history_id_bytes=2), dict(history=P + 4), dict(repetition=P + 2),
+               dict(spans=None), dict(spans=P + 4), dict(n_history=(1 << 30) + 1), dict(history_id_bytes=2), dict(history=P + 4), dict(repetition=P + 2),
                dict(frequency=P + 1), dict(presence=P + 2), dict(bias_ids=P + 2), dict(bias_id_bytes=3), dict(bias_values=None), dict(bias_values=P + 2),
-               dict(bias_spans=None), dict(bias_spans=P + 4), dict(n_bias=1 << 31), dict(mask=P + 2), dict(mask_rows=P + 2), dict(mask_stride=1), dict(mask_rows=None)):
+               dict(bias_spans=None), dict(bias_spans=P + 4), dict(n_bias=(1 << 30) + 1), dict(mask=P + 2), dict(mask_rows=P + 2), dict(mask_stride=1), dict(mask_rows=None)):
         assert call(**kw) == k3.E_ARG, kw
 
 
