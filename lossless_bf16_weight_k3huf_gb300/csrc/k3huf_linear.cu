@@ -28,7 +28,7 @@ constexpr uint32_t kChain = 32;
 template <uint32_t kTileJ> struct Shape {
     static constexpr uint32_t a_bytes = kTileI * 128, b_bytes = kTileJ * 128, stage = a_bytes + b_bytes;
     static constexpr uint32_t per_sm = kTileJ <= 64 ? 2 : 1;                 // CTAs
-    static constexpr uint32_t stages = kTileJ == 256 ? 4 : kTileJ == 128 ? 6 : kTileJ == 64 ? 4 : kTileJ == 32 ? 5 : 6;
+    static constexpr uint32_t stages = kTileJ == 128 ? 6 : kTileJ == 64 ? 4 : kTileJ == 32 ? 5 : 6;
     static constexpr uint32_t part = kTileJ >= 32 ? kTileJ / 2 : kTileJ;     // columns of TMEM per epilogue thread
     static constexpr size_t smem = stages * stage + 1024;
     static_assert(smem * per_sm <= 220 * 1024, "shared memory of an SM");
@@ -50,12 +50,92 @@ struct ProductParams {
     uint32_t size_i, size_j, steps, tiles_i, tiles_j, splits, run;     // run: steps added up in TMEM
 };
 
-__device__ __forceinline__ float activate(float z, uint32_t act) {
-    if (act == K3HUF_ACT_RELU) return z < 0.f ? 0.f : z;
-    if (act == K3HUF_ACT_SILU) return z / (1.f + expf(-z));
-    // (1 + tanh u) / 2 is the logistic function of 2 u
-    if (act == K3HUF_ACT_GELU) return z / (1.f + expf(-1.5957691216057308f * fmaf(0.044715f * z * z, z, z)));
-    return z;
+__device__ __forceinline__ float bias_at(const Epilogue &e, uint32_t i) {
+    return !e.bias ? 0.f : e.bias_type == K3HUF_F32 ? static_cast<const float *>(e.bias)[i] : ld_f32(static_cast<const __nv_bfloat16 *>(e.bias) + i);
+}
+
+// kCount neighbouring columns j of the thread's i: sums to results.
+template <int kCount>
+__device__ __forceinline__ void finish(const Epilogue &e, uint32_t i, uint32_t j, uint32_t size_j, float (&v)[kCount], float bias) {
+    const bool f32 = e.out_type == K3HUF_F32;
+    float res[kCount];
+    if (e.residual) {
+        const uint64_t at = uint64_t(j) * e.residual_stride + i;
+        if (f32) {
+            const float *r = static_cast<const float *>(e.residual) + at;
+#pragma unroll
+            for (int c = 0; c < kCount; ++c, r += e.residual_stride) res[c] = j + c < size_j ? *r : 0.f;
+        } else {
+            const __nv_bfloat16 *r = static_cast<const __nv_bfloat16 *>(e.residual) + at;
+#pragma unroll
+            for (int c = 0; c < kCount; ++c, r += e.residual_stride) res[c] = j + c < size_j ? ld_f32(r) : 0.f;
+        }
+    }
+    if (e.bias) {
+#pragma unroll
+        for (int c = 0; c < kCount; ++c) v[c] += bias;
+    }
+    if (e.z) {
+#pragma unroll
+        for (int c = 0; c < kCount; ++c) {
+            const uint64_t at = uint64_t(j + c) * e.z_stride + i;
+            if (j + c >= size_j) break;
+            if (e.z_type == K3HUF_F32) static_cast<float *>(e.z)[at] = v[c];
+            else st_f32(static_cast<__nv_bfloat16 *>(e.z) + at, v[c]);
+        }
+    }
+    if (e.act == K3HUF_ACT_RELU) {
+#pragma unroll
+        for (int c = 0; c < kCount; ++c) v[c] = v[c] < 0.f ? 0.f : v[c];
+    } else if (e.act == K3HUF_ACT_SILU) {
+#pragma unroll
+        for (int c = 0; c < kCount; ++c) v[c] = v[c] / (1.f + expf(-v[c]));
+    } else if (e.act == K3HUF_ACT_GELU) {
+        // (1 + tanh u) / 2 is the logistic function of 2 u
+#pragma unroll
+        for (int c = 0; c < kCount; ++c) v[c] = v[c] / (1.f + expf(-1.5957691216057308f * fmaf(0.044715f * v[c] * v[c], v[c], v[c])));
+    }
+    if (e.residual) {
+#pragma unroll
+        for (int c = 0; c < kCount; ++c) v[c] += res[c];
+    }
+    const uint64_t at = uint64_t(j) * e.out_stride + i;
+    if (f32) {
+        float *o = static_cast<float *>(e.out) + at;
+#pragma unroll
+        for (int c = 0; c < kCount; ++c, o += e.out_stride)
+            if (j + c < size_j) *o = v[c];
+    } else {
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(e.out) + at;
+#pragma unroll
+        for (int c = 0; c < kCount; ++c, o += e.out_stride)
+            if (j + c < size_j) st_f32(o, v[c]);
+    }
+}
+
+// A tile's sums of several runs are added up in registers, and go back to TMEM, to where the last run's were.
+template <uint32_t kPart>
+__device__ __forceinline__ void add_run(uint32_t from, float (&sum)[kPart], bool first, bool last) {
+#pragma unroll
+    for (uint32_t c = 0; c < kPart; c += 16) {
+        float v[16];
+        tmem_load16(from + c, v);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sum[c + k] = first ? v[k] : sum[c + k] + v[k];
+        if (last) tmem_store16(from + c, &sum[c]);
+    }
+    if (last) asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// ... and from there, 16 columns at a time, to the result.
+template <uint32_t kPart>
+__device__ __forceinline__ void finish_tile(const Epilogue &e, uint32_t from, uint32_t i, uint32_t size_i, uint32_t j, uint32_t size_j, float bias) {
+#pragma unroll 1
+    for (uint32_t c = 0; c < kPart; c += 16) {
+        float v[16];
+        tmem_load16(from + c, v);
+        if (i < size_i) finish(e, i, j + c, size_j, v, bias);
+        __syncwarp();
+    }
 }
 
 // Order of the tiles: kGroup rows of tiles at a time, so that the CTAs at work at once share operands.
@@ -100,38 +180,6 @@ __global__ void __launch_bounds__(kThreads, Shape<kTileJ>::per_sm) product_kerne
     float sum[S::part];
     const uint32_t quarter = warp % 4, c_first = warp / 4 * S::part;         // (epilogue warps)
     const bool reads = warp < kEpilogue / 32 && c_first < kTileJ;
-
-    // (out, z: the column j, a row of the result, at the thread's i)
-    const Epilogue &e = P.e;
-    auto finish = [&](uint32_t i, uint32_t j, const float *v, int count, float bias) {       // count (<= 16) neighbouring j
-        float res[16];
-        if (e.residual) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                if (c >= count) break;
-                const uint64_t at = uint64_t(j + c) * e.residual_stride + i;
-                res[c] = j + c >= P.size_j ? 0.f : e.out_type == K3HUF_F32 ? static_cast<const float *>(e.residual)[at] : ld_f32(static_cast<const __nv_bfloat16 *>(e.residual) + at);
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-            if (c >= count || j + c >= P.size_j) break;
-            const float z = e.bias ? v[c] + bias : v[c];
-            if (e.z) {
-                const uint64_t at = uint64_t(j + c) * e.z_stride + i;
-                if (e.z_type == K3HUF_F32) static_cast<float *>(e.z)[at] = z;
-                else st_f32(static_cast<__nv_bfloat16 *>(e.z) + at, z);
-            }
-            float y = activate(z, e.act);
-            if (e.residual) y += res[c];
-            const uint64_t at = uint64_t(j + c) * e.out_stride + i;
-            if (e.out_type == K3HUF_F32) static_cast<float *>(e.out)[at] = y;
-            else st_f32(static_cast<__nv_bfloat16 *>(e.out) + at, y);
-        }
-    };
-    auto bias_at = [&](uint32_t i) {
-        return !e.bias ? 0.f : e.bias_type == K3HUF_F32 ? static_cast<const float *>(e.bias)[i] : ld_f32(static_cast<const __nv_bfloat16 *>(e.bias) + i);
-    };
 
     if (warp == kEpilogue / 32) {
         if (lane == 0) {
@@ -206,27 +254,17 @@ __global__ void __launch_bounds__(kThreads, Shape<kTileJ>::per_sm) product_kerne
             uint32_t ti, tj;
             tile_place(P, t, ti, tj);
             const uint32_t i = ti * kTileI + quarter * 32 + lane;
-            const float bias = i < P.size_i ? bias_at(i) : 0.f;
+            const float bias = i < P.size_i ? bias_at(P.e, i) : 0.f;
             for (uint32_t q = 0; q < runs; ++q, ++r) {
                 if (ok) ok = mbar_wait(smem_addr(&s_sum[r & 1]), r / 2 & 1);
                 tc_fence_after();
-                if (reads) {
-                    const uint32_t from = tmem + (quarter << 21) + (r & 1) * kTileJ + c_first;
-#pragma unroll
-                    for (uint32_t c = 0; c < S::part; c += 16) {
-                        float v[16];
-                        tmem_load16(from + c, v);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) sum[c + k] = q ? sum[c + k] + v[k] : v[k];
-                    }
-                }
+                const bool last = q + 1 == runs && P.splits == 1;
+                const uint32_t from = tmem + (quarter << 21) + (r & 1) * kTileJ + c_first;
+                if (reads && (runs > 1 || !last)) add_run<S::part>(from, sum, q == 0, last);
+                if (reads && last) finish_tile<S::part>(P.e, from, i, P.size_i, tj * kTileJ + c_first, P.size_j, bias);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&s_read[r & 1]));
-            }
-            if (P.splits == 1 && reads && i < P.size_i) {
-#pragma unroll
-                for (uint32_t c = 0; c < S::part; c += 16) finish(i, tj * kTileJ + c_first + c, sum + c, 16, bias);
             }
         }
     }
@@ -244,17 +282,17 @@ __global__ void __launch_bounds__(kThreads, Shape<kTileJ>::per_sm) product_kerne
         tile_place(P, t_first, ti, tj);
         const uint32_t i = ti * kTileI + quarter * 32 + lane;
         if (warp < kEpilogue / 32 && i < P.size_i) {
-            const float bias = bias_at(i);
+            const float bias = bias_at(P.e, i);
             const uint32_t c0 = kTileJ * split / P.splits, c1 = kTileJ * (split + 1) / P.splits;
             for (uint32_t c = c0 + warp / 4; c < c1 && tj * kTileJ + c < P.size_j; c += 2) {
-                float part[kMaxSplits], v = 0.f;
+                float part[kMaxSplits], v[1] = {0.f};
 #pragma unroll
                 for (uint32_t q = 0; q < kMaxSplits; ++q)
                     if (q < P.splits) part[q] = cluster_load(smem_addr(parts + c * kTileI + quarter * 32 + lane), q);
 #pragma unroll
                 for (uint32_t q = 0; q < kMaxSplits; ++q)
-                    if (q < P.splits) v += part[q];
-                finish(i, tj * kTileJ + c, &v, 1, bias);
+                    if (q < P.splits) v[0] += part[q];
+                finish(P.e, i, tj * kTileJ + c, P.size_j, v, bias);
             }
         }
         __syncwarp();
@@ -266,6 +304,185 @@ __global__ void __launch_bounds__(kThreads, Shape<kTileJ>::per_sm) product_kerne
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_free(tmem, 2 * kTileJ);
+}
+
+// The same for large results: the two CTAs of a pair work on one tile of 256 x kTileJ.  Each holds 128 of its rows (and
+// their sums, in its own TMEM) and half of its columns' operand, which both use: per product a CTA's shared memory is
+// filled with and read for half as much of B.  The first CTA's threads issue the products of both; the copies of both
+// complete on its barriers, the products' ends on barriers of both.
+constexpr uint32_t kPairThreads = kEpilogue + 128;       // (whole warpgroups: registers move from the last one to the others)
+constexpr uint32_t kPairMoreRegs = 232, kPairFewRegs = 40;
+static_assert(kPairMoreRegs * kEpilogue + kPairFewRegs * 128 <= 168 * kPairThreads, "registers that the CTA is launched with");
+template <uint32_t kTileJ> struct Pair {
+    static constexpr uint32_t a_bytes = kTileI * 128, b_bytes = kTileJ / 2 * 128, stage = a_bytes + b_bytes;
+    static constexpr uint32_t stages = kTileJ == 256 ? 6 : 8;
+    static constexpr uint32_t part = kTileJ / 2;
+    static constexpr size_t smem = stages * stage + 1024;
+    static_assert(smem <= 220 * 1024, "shared memory of an SM");
+};
+
+__device__ __forceinline__ uint32_t in_cta(uint32_t at, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, uint32_t cluster_bar) {
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y),
+                 "r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(desc),
+                 "r"(uint32_t(add)) : "memory");
+}
+// the barrier at this address of both CTAs completes when all products issued before have
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"(uint16_t(3)) : "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_bar) { asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory"); }
+// a wait for arrivals of the other CTA's threads
+__device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kTcPolls; ++i) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+        if (done) return true;
+    }
+    return false;
+}
+
+template <uint32_t kTileJ, bool kMnA, bool kMnB>
+__global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_constant__ ProductParams P) {
+    using S = Pair<kTileJ>;
+    constexpr uint32_t NS = S::stages;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t s_full[NS], s_free[NS], s_sum[2], s_read[2];
+    __shared__ uint32_t s_tmem;
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32, base = smem_addr(smem), rank = blockIdx.x % 2;
+    const uint64_t t_first = blockIdx.x / 2, t_step = gridDim.x / 2;
+    const uint32_t runs = (P.steps + P.run - 1) / P.run;
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)), "r"(2 * kTileJ) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    if (tid == 0) {
+        for (uint32_t i = 0; i < NS; ++i) {
+            mbar_init(smem_addr(&s_full[i]), 1);
+            mbar_init(smem_addr(&s_free[i]), 1);
+        }
+        for (uint32_t i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&s_sum[i]), 1);
+            mbar_init(smem_addr(&s_read[i]), 2 * kEpilogue / 32);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async_shared();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    bool ok = true;
+    if (warp >= kEpilogue / 32) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairFewRegs));
+        if (warp == kEpilogue / 32 && lane == 0) {
+            uint32_t stage = 0, round = 0;    // copies so far: round * NS + stage
+            for (uint64_t t = t_first; t < P.tiles && ok; t += t_step) {
+                uint32_t ti, tj;
+                tile_place(P, t, ti, tj);
+                const int32_t i0 = int32_t((ti * 2 + rank) * kTileI), j0 = int32_t(tj * kTileJ + rank * (kTileJ / 2));
+                for (uint32_t s = 0; s < P.steps; ++s) {
+                    if (round) ok = mbar_wait(smem_addr(&s_free[stage]), (round - 1) & 1);
+                    if (!ok) break;
+                    const uint32_t at = base + stage * S::stage, bar = in_cta(smem_addr(&s_full[stage]), 0);
+                    const int32_t k = int32_t(s * kStep);
+                    if (rank == 0) mbar_expect(smem_addr(&s_full[stage]), 2 * S::stage);
+                    if constexpr (kMnA) {
+                        pair_load(at, &P.a, i0, k, bar);
+                        pair_load(at + kStep * 128, &P.a, i0 + 64, k, bar);
+                    } else {
+                        pair_load(at, &P.a, k, i0, bar);
+                    }
+                    if constexpr (kMnB) {
+#pragma unroll
+                        for (uint32_t b = 0; b < kTileJ / 128; ++b) pair_load(at + S::a_bytes + b * (kStep * 128), &P.b, j0 + int32_t(b * 64), k, bar);
+                    } else {
+                        pair_load(at + S::a_bytes, &P.b, k, j0, bar);
+                    }
+                    if (++stage == NS) stage = 0, ++round;
+                }
+            }
+            // the last copies of both CTAs land before either ends (the barrier below), whichever thread's wait may have
+            // given up; if one has, the second CTA, whose own barriers nothing completes, waits until its limit
+            if (rank == 0) {
+                for (uint32_t q = 0; q < NS && (round || stage); ++q) {
+                    if (stage == 0) stage = NS, --round;
+                    --stage;
+                    mbar_wait_pair(smem_addr(&s_full[stage]), round & 1);
+                }
+            } else if (!ok) {
+                mbar_wait(smem_addr(&s_full[0]), 0);
+            }
+        } else if (warp == kEpilogue / 32 + 1 && lane == 0 && rank == 0) {
+            constexpr uint32_t desc = mma_desc(2 * kTileI, kTileJ, kMnA, kMnB);
+            const uint64_t a0 = tile_desc(base, kMnA ? kStep * 128 : 16, 1024), b0 = tile_desc(base + S::a_bytes, kMnB ? kStep * 128 : 16, 1024);
+            uint32_t stage = 0, round = 0, r = 0;      // r: runs so far
+            for (uint64_t t = t_first; t < P.tiles && ok; t += t_step)
+                for (uint32_t s = 0, in_run = 0; s < P.steps; ++s) {
+                    if (in_run == 0 && r >= 2) ok = mbar_wait_pair(smem_addr(&s_read[r & 1]), (r / 2 - 1) & 1);
+                    if (ok) ok = mbar_wait_pair(smem_addr(&s_full[stage]), round & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t a = a0 + stage * (S::stage >> 4), b = b0 + stage * (S::stage >> 4);
+                    const uint32_t d = tmem + (r & 1) * kTileJ;
+#pragma unroll
+                    for (uint32_t q = 0; q < kStep / 16; ++q) pair_mma(d, a + q * (kMnA ? 128 : 2), b + q * (kMnB ? 128 : 2), desc, in_run || q);
+                    pair_commit(smem_addr(&s_free[stage]));
+                    if (++stage == NS) stage = 0, ++round;
+                    if (++in_run == P.run || s + 1 == P.steps) {
+                        pair_commit(smem_addr(&s_sum[r & 1]));
+                        in_run = 0;
+                        ++r;
+                    }
+                }
+            // (products whose end nobody waited for, if a wait gave up, end before the CTAs do)
+            for (uint32_t q = 0; q < NS && (round || stage); ++q) {
+                if (stage == 0) stage = NS, --round;
+                --stage;
+                mbar_wait(smem_addr(&s_free[stage]), round & 1);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairMoreRegs));
+        const uint32_t quarter = warp % 4, c_first = warp / 4 * S::part;
+        uint32_t r = 0;
+        for (uint64_t t = t_first; t < P.tiles; t += t_step) {
+            uint32_t ti, tj;
+            tile_place(P, t, ti, tj);
+            const uint32_t i = (ti * 2 + rank) * kTileI + quarter * 32 + lane;
+            const float bias = i < P.size_i ? bias_at(P.e, i) : 0.f;
+            float sum[S::part];
+            for (uint32_t q = 0; q < runs; ++q, ++r) {
+                if (ok) ok = mbar_wait(smem_addr(&s_sum[r & 1]), r / 2 & 1);
+                tc_fence_after();
+                const uint32_t from = tmem + (quarter << 21) + (r & 1) * kTileJ + c_first;
+                if (runs > 1) add_run<S::part>(from, sum, q == 0, q + 1 == runs);
+                if (q + 1 == runs) finish_tile<S::part>(P.e, from, i, P.size_i, tj * kTileJ + c_first, P.size_j, bias);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_at(in_cta(smem_addr(&s_read[r & 1]), 0));
+            }
+        }
+    }
+    __syncwarp();
+    if (!ok) atomicOr(P.status, K3HUF_ST_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    tc_fence_after();
+    if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kTileJ) : "memory");
 }
 
 // Rows that do not start on 16 bytes, copied to rows that do (TMA reads no others): 8 values per thread.
@@ -427,35 +644,68 @@ int aligned_rows(Operand &o, uint8_t *&scratch, uint64_t sms, cudaStream_t strea
     return cuda_rc(cudaGetLastError());
 }
 
-template <uint32_t kTileJ, bool kMnA, bool kMnB>
-int launch_product(ProductParams &P, const Operand &a, const Operand &b, uint64_t sms, cudaStream_t stream) {
-    using S = Shape<kTileJ>;
-    static std::atomic<uint64_t> once{0};
-    int rc = once_per_device(once, [] { return cudaFuncSetAttribute(product_kernel<kTileJ, kMnA, kMnB>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::smem)); });
-    if (!rc) rc = tensor_map(&P.a, a.p, K3HUF_BF16, a.rows, a.cols, a.stride, kMnA ? kStep : kTileI, kStep, true);
-    if (!rc) rc = tensor_map(&P.b, b.p, K3HUF_BF16, b.rows, b.cols, b.stride, kMnB ? kStep : kTileJ, kStep, true);
+// How a result is cut: tiles of `pair` CTAs, 128 pair x tile_j, the contraction in `splits`.
+struct Cut {
+    uint32_t tile_j, pair, splits;
+    uint64_t tiles;
+};
+// The cut of the lowest cost by this count of cycles: a step of 64 of the contraction takes the tensor core 128 x tile_j x 64
+// / 4096 cycles per CTA and the copies their bytes at kLoadRate; CTAs that share an SM share both; a tile costs kTileCost more.
+constexpr uint64_t kLoadRate = 48, kTileCost = 3000;
+template <bool kMnB>
+Cut choose(uint64_t size_i, uint64_t size_j, uint64_t steps, uint64_t sms) {
+    Cut best{};
+    uint64_t least = ~0ull;
+    auto consider = [&](uint32_t tile_j, uint32_t pair, uint64_t per_sm) {
+        Cut c{tile_j, pair, 1, (size_i + kTileI * pair - 1) / (kTileI * pair) * ((size_j + tile_j - 1) / tile_j)};
+        const uint64_t slots = sms * per_sm / pair;
+        if (pair == 1) c.splits = uint32_t(std::max<uint64_t>(1, std::min<uint64_t>({kMaxSplits, slots / c.tiles, steps / 4})));
+        const uint64_t step = per_sm * std::max<uint64_t>(2 * tile_j, (kTileI + tile_j / pair) * 128 / kLoadRate);
+        const uint64_t waves = (c.tiles * c.splits + slots - 1) / slots, cost = waves * ((steps + c.splits - 1) / c.splits * step + kTileCost);
+        if (cost < least) least = cost, best = c;
+    };
+    if constexpr (!kMnB) {
+        consider(16, 1, Shape<16>::per_sm);
+        consider(32, 1, Shape<32>::per_sm);
+    }
+    consider(64, 1, Shape<64>::per_sm);
+    consider(128, 1, Shape<128>::per_sm);
+    consider(128, 2, 1);
+    consider(256, 2, 1);
+    return best;
+}
+
+template <typename Kernel>
+int launch_product(Kernel kernel, std::atomic<uint64_t> &once, uint32_t threads, size_t smem, uint64_t slots, const Cut &cut, ProductParams &P, cudaStream_t stream) {
+    const int rc = once_per_device(once, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)); });
     if (rc) return rc;
-    P.tiles_i = (P.size_i + kTileI - 1) / kTileI;
-    P.tiles_j = (P.size_j + kTileJ - 1) / kTileJ;
-    P.tiles = uint64_t(P.tiles_i) * P.tiles_j;
-    const bool e_f32 = P.e.out_type == K3HUF_F32 || (P.e.z && P.e.z_type == K3HUF_F32);
-    // fewer tiles than the GPU holds CTAs: the CTAs of a cluster share a tile's contraction
-    const uint64_t slots = sms * S::per_sm;
-    P.splits = uint32_t(std::max<uint64_t>(1, std::min<uint64_t>({kMaxSplits, slots / P.tiles, P.steps / 4})));
-    P.run = e_f32 ? kChain / (kStep / 16) : P.steps;
-    const uint64_t ctas = P.splits > 1 ? P.tiles * P.splits : std::min(P.tiles, slots);
+    P.tiles = cut.tiles;
+    P.tiles_i = (P.size_i + kTileI * cut.pair - 1) / (kTileI * cut.pair);
+    P.tiles_j = (P.size_j + cut.tile_j - 1) / cut.tile_j;
+    P.splits = cut.splits;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(uint32_t(ctas));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = S::smem;
+    cfg.gridDim = dim3(uint32_t(std::min(cut.tiles * cut.splits, slots) * cut.pair));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = P.splits;
+    attr[0].val.clusterDim.x = cut.pair * cut.splits;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cuda_rc(cudaLaunchKernelEx(&cfg, product_kernel<kTileJ, kMnA, kMnB>, P));
+    cfg.numAttrs = cut.pair == 1 ? 1 : 0;     // (a pair's kernel has its cluster in its declaration)
+    return cuda_rc(cudaLaunchKernelEx(&cfg, kernel, P));
+}
+
+template <uint32_t kTileJ, bool kMnA, bool kMnB>
+int launch_one(const Cut &cut, ProductParams &P, uint64_t sms, cudaStream_t stream) {
+    static std::atomic<uint64_t> once{0};
+    return launch_product(product_kernel<kTileJ, kMnA, kMnB>, once, kThreads, Shape<kTileJ>::smem, sms * Shape<kTileJ>::per_sm, cut, P, stream);
+}
+template <uint32_t kTileJ, bool kMnA, bool kMnB>
+int launch_pair(const Cut &cut, ProductParams &P, uint64_t sms, cudaStream_t stream) {
+    static std::atomic<uint64_t> once{0};
+    return launch_product(pair_kernel<kTileJ, kMnA, kMnB>, once, kPairThreads, Pair<kTileJ>::smem, sms / 2, cut, P, stream);
 }
 
 // out[j][i] = sum_k A[i][k] B[j][k]
@@ -465,13 +715,18 @@ int product(const Operand &a, const Operand &b, uint64_t size_i, uint64_t size_j
     P.e = e;
     P.status = status;
     P.size_i = uint32_t(size_i), P.size_j = uint32_t(size_j), P.steps = uint32_t((size_k + kStep - 1) / kStep);
+    const bool f32 = e.out_type == K3HUF_F32 || (e.z && e.z_type == K3HUF_F32);
+    P.run = f32 ? kChain / (kStep / 16) : P.steps;
+    const Cut cut = choose<kMnB>(size_i, size_j, P.steps, sms);
+    int rc = tensor_map(&P.a, a.p, K3HUF_BF16, a.rows, a.cols, a.stride, kMnA ? kStep : kTileI, kStep, true);
+    if (!rc) rc = tensor_map(&P.b, b.p, K3HUF_BF16, b.rows, b.cols, b.stride, kMnB ? kStep : cut.tile_j / cut.pair, kStep, true);
+    if (rc) return rc;
+    if (cut.pair == 2) return cut.tile_j == 256 ? launch_pair<256, kMnA, kMnB>(cut, P, sms, stream) : launch_pair<128, kMnA, kMnB>(cut, P, sms, stream);
     if constexpr (!kMnB) {
-        if (size_j <= 16) return launch_product<16, kMnA, kMnB>(P, a, b, sms, stream);
-        if (size_j <= 32) return launch_product<32, kMnA, kMnB>(P, a, b, sms, stream);
+        if (cut.tile_j == 16) return launch_one<16, kMnA, kMnB>(cut, P, sms, stream);
+        if (cut.tile_j == 32) return launch_one<32, kMnA, kMnB>(cut, P, sms, stream);
     }
-    if (size_j <= 64) return launch_product<64, kMnA, kMnB>(P, a, b, sms, stream);
-    if (size_j <= 128) return launch_product<128, kMnA, kMnB>(P, a, b, sms, stream);
-    return launch_product<256, kMnA, kMnB>(P, a, b, sms, stream);
+    return cut.tile_j == 64 ? launch_one<64, kMnA, kMnB>(cut, P, sms, stream) : launch_one<128, kMnA, kMnB>(cut, P, sms, stream);
 }
 
 bool sizes_ok(uint64_t n, uint64_t rows, uint64_t cols) { return rows && cols && n < (1ull << 31) && rows < (1ull << 31) && cols < (1ull << 31); }
