@@ -89,11 +89,11 @@ __device__ __forceinline__ void finish(const Epilogue &e, uint32_t i, uint32_t j
         for (int c = 0; c < kCount; ++c) v[c] = v[c] < 0.f ? 0.f : v[c];
     } else if (e.act == K3HUF_ACT_SILU) {
 #pragma unroll
-        for (int c = 0; c < kCount; ++c) v[c] = v[c] / (1.f + expf(-v[c]));
+        for (int c = 0; c < kCount; ++c) v[c] = __fdividef(v[c], 1.f + __expf(-v[c]));
     } else if (e.act == K3HUF_ACT_GELU) {
         // (1 + tanh u) / 2 is the logistic function of 2 u
 #pragma unroll
-        for (int c = 0; c < kCount; ++c) v[c] = v[c] / (1.f + expf(-1.5957691216057308f * fmaf(0.044715f * v[c] * v[c], v[c], v[c])));
+        for (int c = 0; c < kCount; ++c) v[c] = __fdividef(v[c], 1.f + __expf(-1.5957691216057308f * fmaf(0.044715f * v[c] * v[c], v[c], v[c])));
     }
     if (e.residual) {
 #pragma unroll
@@ -501,16 +501,16 @@ __global__ void __launch_bounds__(kCopyThreads) align_rows_kernel(const uint16_t
 }
 
 // act'(z).  Far out, where it no longer changes in 32 bits, z stops: infinities give the limit.
-__device__ __forceinline__ float slope(float z, uint32_t act) {
-    if (act == K3HUF_ACT_RELU) return z > 0.f ? 1.f : 0.f;
-    if (act == K3HUF_ACT_SILU) {
+template <uint32_t kAct> __device__ __forceinline__ float slope(float z) {
+    if constexpr (kAct == K3HUF_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+    if constexpr (kAct == K3HUF_ACT_SILU) {
         z = z > 80.f ? 80.f : z < -80.f ? -80.f : z;
-        const float x = expf(-z), q = 1.f / (1.f + x);
+        const float x = __expf(-z), q = __fdividef(1.f, 1.f + x);
         return fmaf(z * q, x * q, q);
     }
-    if (act == K3HUF_ACT_GELU) {
+    if constexpr (kAct == K3HUF_ACT_GELU) {
         z = z > 10.f ? 10.f : z < -10.f ? -10.f : z;
-        const float x = expf(-1.5957691216057308f * fmaf(0.044715f * z * z, z, z)), q = 1.f / (1.f + x);
+        const float x = __expf(-1.5957691216057308f * fmaf(0.044715f * z * z, z, z)), q = __fdividef(1.f, 1.f + x);
         return fmaf(z * q, x * q * 1.5957691216057308f * fmaf(3.f * 0.044715f * z, z, 1.f), q);
     }
     return 1.f;
@@ -521,69 +521,90 @@ struct SlopeParams {
     __nv_bfloat16 *dz;
     float *dbias;
     uint64_t n, z_stride, dy_stride, dz_stride;
-    uint32_t rows, z_type, dy_type, act;
+    uint32_t rows, act;
     bool add;
 };
 
-// dz and the columns' sums in one read of z and dy.  A CTA takes kSlopeCols columns (kPer neighbouring ones per thread)
-// and its share of the tokens; the CTAs of a cluster, which share the columns, add up in the order of their tokens.
-constexpr int kSlopeThreads = 256, kSlopeLanes = 16, kSlopeDepth = 4;        // threads along the columns; tokens in flight per thread
-template <int kPer> __device__ __forceinline__ void load_row(const void *p, uint32_t type, uint64_t at, float (&f)[kPer]) {
-    if constexpr (kPer == 8) {
-        if (type == K3HUF_F32) {
-            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
-            const float4 a = __ldcs(q), b = __ldcs(q + 1);
-            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-        } else {
-            const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) + at));
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) f[2 * k] = __uint_as_float(w[k] << 16), f[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-        }
+// dz and the columns' sums in one read of z and dy.  A CTA takes kSlopeLanes x kPer columns (kPer neighbouring ones per
+// thread) and its share of the tokens; the CTAs of a cluster, which share the columns, add up in the order of their tokens.
+constexpr int kSlopeThreads = 256, kSlopeLanes = 16, kSlopePerSm = 4;        // threads along the columns
+template <typename T, int kPer> struct Few {              // neighbouring values as loaded
+    T v[kPer];
+};
+template <typename T> struct Few<T, 8> {
+    uint4 v[8 * sizeof(T) / 16];
+};
+template <typename T, int kPer> __device__ __forceinline__ void load_few(const T *p, Few<T, kPer> &f) {
+    if constexpr (kPer == 1) {
+        f.v[0] = *p;
     } else {
-        f[0] = type == K3HUF_F32 ? static_cast<const float *>(p)[at] : ld_f32(static_cast<const __nv_bfloat16 *>(p) + at);
+#pragma unroll
+        for (int h = 0; h < int(8 * sizeof(T) / 16); ++h) f.v[h] = __ldcs(reinterpret_cast<const uint4 *>(p) + h);
+    }
+}
+template <typename T, int kPer> __device__ __forceinline__ void unpack_few(const Few<T, kPer> &f, float (&o)[kPer]) {
+    if constexpr (kPer == 1) {
+        o[0] = ld_f32(&f.v[0]);
+    } else {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(f.v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = sizeof(T) == 4 ? __uint_as_float(w[k]) : __uint_as_float(k % 2 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
     }
 }
 
-template <int kPer>
-__global__ void __launch_bounds__(kSlopeThreads) slope_kernel(const SlopeParams P, uint32_t splits) {
+// dz of a thread's columns for the tokens t0 + down, + kDown, ... and their sums
+template <uint32_t kAct, typename Z, typename D, int kPer>
+__device__ __forceinline__ void slope_rows(const SlopeParams &P, uint64_t c, uint64_t t0, uint64_t t1, float (&sum)[kPer]) {
+    constexpr int kDown = kSlopeThreads / kSlopeLanes, kDepth = kPer == 1 || sizeof(Z) + sizeof(D) == 4 ? 4 : 2;      // tokens in flight
+    for (uint64_t t = t0; t < t1; t += uint64_t(kDown) * kDepth) {
+        Few<Z, kPer> z[kDepth];
+        Few<D, kPer> g[kDepth];
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            const uint64_t at = t + uint64_t(d) * kDown;
+            if (at >= t1) break;
+            load_few(static_cast<const Z *>(P.z) + at * P.z_stride + c, z[d]);
+            load_few(static_cast<const D *>(P.dy) + at * P.dy_stride + c, g[d]);
+        }
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            const uint64_t at = t + uint64_t(d) * kDown;
+            if (at >= t1) break;
+            float a[kPer], b[kPer];
+            unpack_few(z[d], a);
+            unpack_few(g[d], b);
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                b[k] *= slope<kAct>(a[k]);
+                sum[k] += b[k];
+            }
+            __nv_bfloat16 *o = P.dz + at * P.dz_stride + c;
+            if constexpr (kPer == 8) {
+                uint4 v;
+                __nv_bfloat162 *q = reinterpret_cast<__nv_bfloat162 *>(&v);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) q[k] = __floats2bfloat162_rn(b[2 * k], b[2 * k + 1]);
+                __stcs(reinterpret_cast<uint4 *>(o), v);
+            } else {
+                st_f32(o, b[0]);
+            }
+        }
+    }
+}
+
+template <typename Z, typename D, int kPer>
+__global__ void __launch_bounds__(kSlopeThreads, kSlopePerSm) slope_kernel(const SlopeParams P, uint32_t splits) {
     constexpr int kCols = kSlopeLanes * kPer, kDown = kSlopeThreads / kSlopeLanes;
     __shared__ float s_sum[kDown][kCols + 1], s_cta[kCols];
     const uint32_t split = blockIdx.x % splits, lane = threadIdx.x % kSlopeLanes, down = threadIdx.x / kSlopeLanes;
     const uint64_t c0 = uint64_t(blockIdx.x / splits) * kCols, c = c0 + lane * kPer;
-    const uint64_t t0 = P.n * split / splits, t1 = P.n * (split + 1) / splits;
+    const uint64_t t0 = P.n * split / splits + down, t1 = P.n * (split + 1) / splits;
     float sum[kPer] = {};
     if (c < P.rows) {
-        for (uint64_t t = t0 + down; t < t1; t += uint64_t(kDown) * kSlopeDepth) {
-            float z[kSlopeDepth][kPer], g[kSlopeDepth][kPer];
-#pragma unroll
-            for (int d = 0; d < kSlopeDepth; ++d) {
-                const uint64_t at = t + uint64_t(d) * kDown;
-                if (at >= t1) break;
-                load_row<kPer>(P.z, P.z_type, at * P.z_stride + c, z[d]);
-                load_row<kPer>(P.dy, P.dy_type, at * P.dy_stride + c, g[d]);
-            }
-#pragma unroll
-            for (int d = 0; d < kSlopeDepth; ++d) {
-                const uint64_t at = t + uint64_t(d) * kDown;
-                if (at >= t1) break;
-#pragma unroll
-                for (int k = 0; k < kPer; ++k) {
-                    g[d][k] *= slope(z[d][k], P.act);
-                    sum[k] += g[d][k];
-                }
-                __nv_bfloat16 *o = P.dz + at * P.dz_stride + c;
-                if constexpr (kPer == 8) {
-                    uint4 v;
-                    __nv_bfloat162 *q = reinterpret_cast<__nv_bfloat162 *>(&v);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) q[k] = __floats2bfloat162_rn(g[d][2 * k], g[d][2 * k + 1]);
-                    *reinterpret_cast<uint4 *>(o) = v;
-                } else {
-                    st_f32(o, g[d][0]);
-                }
-            }
-        }
+        if (P.act == K3HUF_ACT_NONE) slope_rows<K3HUF_ACT_NONE, Z, D, kPer>(P, c, t0, t1, sum);
+        else if (P.act == K3HUF_ACT_RELU) slope_rows<K3HUF_ACT_RELU, Z, D, kPer>(P, c, t0, t1, sum);
+        else if (P.act == K3HUF_ACT_SILU) slope_rows<K3HUF_ACT_SILU, Z, D, kPer>(P, c, t0, t1, sum);
+        else slope_rows<K3HUF_ACT_GELU, Z, D, kPer>(P, c, t0, t1, sum);
     }
     if (!P.dbias) return;                     // (the whole grid)
 #pragma unroll
@@ -784,14 +805,17 @@ extern "C" int k3huf_linear_dz(const void *d_z, uint32_t z_type, uint64_t z_stri
     uint64_t sms = 0;
     const int rc = sm_count(&sms);
     if (rc) return rc;
-    const SlopeParams P{d_z, d_dy, static_cast<__nv_bfloat16 *>(d_dz), d_dbias, n_tokens, z_stride, dy_stride, dz_stride, uint32_t(rows), z_type, dy_type, act, add};
+    const SlopeParams P{d_z, d_dy, static_cast<__nv_bfloat16 *>(d_dz), d_dbias, n_tokens, z_stride, dy_stride, dz_stride, uint32_t(rows), act, add};
     auto on16 = [](const void *p, uint64_t stride, uint32_t type) { return aligned_to(p, 16) && stride * elem_bytes(type) % 16 == 0; };
     const bool vec = rows % 8 == 0 && on16(d_z, z_stride, z_type) && on16(d_dy, dy_stride, dy_type) && on16(d_dz, dz_stride, K3HUF_BF16);
     const uint32_t cols = kSlopeLanes * (vec ? 8 : 1);
     const uint64_t blocks = (rows + cols - 1) / cols;
-    // tokens split over a cluster until the GPU is full (four CTAs per SM)
+    // the tokens split over a cluster of up to eight CTAs, so that the GPU's places (four per SM) are filled best
+    const uint64_t slots = sms * kSlopePerSm;
     uint32_t splits = 1;
-    while (splits < 8 && blocks * splits < sms * 4 && n_tokens / splits > kSlopeThreads / kSlopeLanes * kSlopeDepth) splits *= 2;
+    auto idle = [&](uint64_t k) { return double((blocks * k + slots - 1) / slots) * double(slots) / double(blocks * k); };      // places taken per CTA
+    for (uint32_t k = 2; k <= 8 && n_tokens / k >= 64; ++k)
+        if (idle(k) < idle(splits) - 0.02) splits = k;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(uint32_t(blocks * splits));
     cfg.blockDim = dim3(kSlopeThreads);
@@ -802,7 +826,10 @@ extern "C" int k3huf_linear_dz(const void *d_z, uint32_t z_type, uint64_t z_stri
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cuda_rc(vec ? cudaLaunchKernelEx(&cfg, slope_kernel<8>, P, splits) : cudaLaunchKernelEx(&cfg, slope_kernel<1>, P, splits));
+    using BF = __nv_bfloat16;
+    auto run = [&](auto vec8, auto one) { return cuda_rc(vec ? cudaLaunchKernelEx(&cfg, vec8, P, splits) : cudaLaunchKernelEx(&cfg, one, P, splits)); };
+    if (z_type == K3HUF_BF16) return dy_type == K3HUF_BF16 ? run(slope_kernel<BF, BF, 8>, slope_kernel<BF, BF, 1>) : run(slope_kernel<BF, float, 8>, slope_kernel<BF, float, 1>);
+    return dy_type == K3HUF_BF16 ? run(slope_kernel<float, BF, 8>, slope_kernel<float, BF, 1>) : run(slope_kernel<float, float, 8>, slope_kernel<float, float, 1>);
 }
 
 extern "C" int k3huf_linear_grad(const void *d_x, uint64_t x_stride, uint64_t n_tokens, const void *d_w, uint64_t w_stride, uint64_t rows, uint64_t cols,
