@@ -25,6 +25,29 @@ constexpr uint32_t kMaxSplits = 8;
 // of the sum, always to the same side.
 constexpr uint32_t kChain = 32;
 
+// Place in a ring of stages: the stage, and the parity of the phase that its barrier is in this time round.
+template <uint32_t kStages> struct Ring {
+    uint32_t stage = 0, parity = 0, used = 0;
+    __device__ __forceinline__ void next() {
+        used = min(used + 1, kStages);
+        if (++stage == kStages) stage = 0, parity ^= 1;
+    }
+    // Back by one stage, of those that were used last; false when all have been gone through.
+    __device__ __forceinline__ bool back() {
+        if (used == 0) return false;
+        --used;
+        if (stage == 0) stage = kStages, parity ^= 1;
+        --stage;
+        return true;
+    }
+};
+// The same thread of a converged warp, each time.
+__device__ __forceinline__ bool one_thread() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 template <uint32_t kTileJ> struct Shape {
     static constexpr uint32_t a_bytes = kTileI * 128, b_bytes = kTileJ * 128, stage = a_bytes + b_bytes;
     static constexpr uint32_t per_sm = kTileJ <= 64 ? 2 : 1;                 // CTAs
@@ -182,17 +205,20 @@ __global__ void __launch_bounds__(kThreads, Shape<kTileJ>::per_sm) product_kerne
     const bool reads = warp < kEpilogue / 32 && c_first < kTileJ;
 
     if (warp == kEpilogue / 32) {
-        if (lane == 0) {
-            uint32_t stage = 0, round = 0;    // copies so far: round * NS + stage
-            for (uint64_t t = t_first; t < P.tiles && ok; t += t_step) {
-                uint32_t ti, tj;
-                tile_place(P, t, ti, tj);
-                const int32_t i0 = int32_t(ti * kTileI), j0 = int32_t(tj * kTileJ);
-                for (uint32_t s = 0; s < n_steps; ++s) {
-                    if (round) ok = mbar_wait(smem_addr(&s_free[stage]), (round - 1) & 1);
-                    if (!ok) break;
-                    const uint32_t at = base + stage * S::stage, bar = smem_addr(&s_full[stage]);
-                    const int32_t k = int32_t((k0 + s) * kStep);
+        // (the whole warp goes through the loop, one thread issues: addresses stay in uniform registers)
+        const bool issues = one_thread();
+        Ring<NS> ring;
+        const uint32_t full = smem_addr(&s_full[0]), free = smem_addr(&s_free[0]);
+        for (uint64_t t = t_first; t < P.tiles && ok; t += t_step) {
+            uint32_t ti, tj;
+            tile_place(P, t, ti, tj);
+            const int32_t i0 = int32_t(ti * kTileI), j0 = int32_t(tj * kTileJ);
+            int32_t k = int32_t(k0 * kStep);
+            for (uint32_t s = 0; s < n_steps; ++s, k += int32_t(kStep)) {
+                ok = mbar_wait(free + ring.stage * 8, ring.parity ^ 1);       // (the first round's stages are free)
+                if (!ok) break;
+                if (issues) {
+                    const uint32_t at = base + ring.stage * S::stage, bar = full + ring.stage * 8;
                     mbar_expect(bar, S::stage);
                     if constexpr (kMnA) {
                         tma_load(at, &P.a, i0, k, bar);
@@ -206,48 +232,40 @@ __global__ void __launch_bounds__(kThreads, Shape<kTileJ>::per_sm) product_kerne
                     } else {
                         tma_load(at + S::a_bytes, &P.b, k, j0, bar);
                     }
-                    if (++stage == NS) stage = 0, ++round;
                 }
-            }
-            // the last copies land before the CTA ends, whichever thread's wait may have given up
-            for (uint32_t q = 0; q < NS && (round || stage); ++q) {
-                if (stage == 0) stage = NS, --round;
-                --stage;
-                mbar_wait(smem_addr(&s_full[stage]), round & 1);
+                ring.next();
             }
         }
-        __syncwarp();
+        // the last copies land before the CTA ends, whichever thread's wait may have given up
+        while (ring.back()) mbar_wait(full + ring.stage * 8, ring.parity);
     } else if (warp == kEpilogue / 32 + 1) {
-        if (lane == 0) {
-            constexpr uint32_t desc = mma_desc(kTileI, kTileJ, kMnA, kMnB);
-            const uint64_t a0 = tile_desc(base, kMnA ? kStep * 128 : 16, 1024), b0 = tile_desc(base + S::a_bytes, kMnB ? kStep * 128 : 16, 1024);
-            uint32_t stage = 0, round = 0, r = 0;      // r: runs so far
-            for (uint64_t t = t_first; t < P.tiles && ok; t += t_step)
-                for (uint32_t s = 0, in_run = 0; s < n_steps; ++s) {
-                    if (in_run == 0 && r >= 2) ok = mbar_wait(smem_addr(&s_read[r & 1]), (r / 2 - 1) & 1);
-                    if (ok) ok = mbar_wait(smem_addr(&s_full[stage]), round & 1);
+        const bool issues = one_thread();
+        constexpr uint32_t desc = mma_desc(kTileI, kTileJ, kMnA, kMnB);
+        const uint64_t a0 = tile_desc(base, kMnA ? kStep * 128 : 16, 1024), b0 = tile_desc(base + S::a_bytes, kMnB ? kStep * 128 : 16, 1024);
+        const uint32_t full = smem_addr(&s_full[0]), free = smem_addr(&s_free[0]);
+        Ring<NS> ring;
+        Ring<2> run;
+        for (uint64_t t = t_first; t < P.tiles && ok; t += t_step)
+            for (uint32_t s0 = 0; s0 < n_steps && ok; s0 += P.run) {
+                ok = mbar_wait(smem_addr(&s_read[run.stage]), run.parity ^ 1);
+                const uint32_t d = tmem + run.stage * kTileJ, s1 = min(s0 + P.run, n_steps);
+                for (uint32_t s = s0; s < s1 && ok; ++s) {
+                    ok = mbar_wait(full + ring.stage * 8, ring.parity);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t a = a0 + stage * (S::stage >> 4), b = b0 + stage * (S::stage >> 4);
-                    const uint32_t d = tmem + (r & 1) * kTileJ;
+                    if (issues) {
+                        const uint64_t a = a0 + ring.stage * (S::stage >> 4), b = b0 + ring.stage * (S::stage >> 4);
 #pragma unroll
-                    for (uint32_t q = 0; q < kStep / 16; ++q) mma(d, a + q * (kMnA ? 128 : 2), b + q * (kMnB ? 128 : 2), desc, in_run || q);
-                    mma_commit(smem_addr(&s_free[stage]));
-                    if (++stage == NS) stage = 0, ++round;
-                    if (++in_run == P.run || s + 1 == n_steps) {
-                        mma_commit(smem_addr(&s_sum[r & 1]));
-                        in_run = 0;
-                        ++r;
+                        for (uint32_t q = 0; q < kStep / 16; ++q) mma(d, a + q * (kMnA ? 128 : 2), b + q * (kMnB ? 128 : 2), desc, s > s0 || q);
+                        mma_commit(free + ring.stage * 8);
                     }
+                    ring.next();
                 }
-            // (products whose end nobody waited for, if a wait gave up, end before the CTA does)
-            for (uint32_t q = 0; q < NS && (round || stage); ++q) {
-                if (stage == 0) stage = NS, --round;
-                --stage;
-                mbar_wait(smem_addr(&s_free[stage]), round & 1);
+                if (issues) mma_commit(smem_addr(&s_sum[run.stage]));
+                run.next();
             }
-        }
-        __syncwarp();
+        // (products whose end nobody waited for, if a wait gave up, end before the CTA does)
+        while (ring.back()) mbar_wait(free + ring.stage * 8, ring.parity);
     } else {
         uint32_t r = 0;
         for (uint64_t t = t_first; t < P.tiles; t += t_step) {
@@ -386,72 +404,72 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1) pair_kern
     bool ok = true;
     if (warp >= kEpilogue / 32) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairFewRegs));
-        if (warp == kEpilogue / 32 && lane == 0) {
-            uint32_t stage = 0, round = 0;    // copies so far: round * NS + stage
+        if (warp == kEpilogue / 32) {
+            const bool issues = one_thread();
+            Ring<NS> ring;
+            const uint32_t full = smem_addr(&s_full[0]), first_full = in_cta(full, 0), free = smem_addr(&s_free[0]);
             for (uint64_t t = t_first; t < P.tiles && ok; t += t_step) {
                 uint32_t ti, tj;
                 tile_place(P, t, ti, tj);
                 const int32_t i0 = int32_t((ti * 2 + rank) * kTileI), j0 = int32_t(tj * kTileJ + rank * (kTileJ / 2));
-                for (uint32_t s = 0; s < P.steps; ++s) {
-                    if (round) ok = mbar_wait(smem_addr(&s_free[stage]), (round - 1) & 1);
+                int32_t k = 0;
+                for (uint32_t s = 0; s < P.steps; ++s, k += int32_t(kStep)) {
+                    ok = mbar_wait(free + ring.stage * 8, ring.parity ^ 1);       // (the first round's stages are free)
                     if (!ok) break;
-                    const uint32_t at = base + stage * S::stage, bar = in_cta(smem_addr(&s_full[stage]), 0);
-                    const int32_t k = int32_t(s * kStep);
-                    if (rank == 0) mbar_expect(smem_addr(&s_full[stage]), 2 * S::stage);
-                    if constexpr (kMnA) {
-                        pair_load(at, &P.a, i0, k, bar);
-                        pair_load(at + kStep * 128, &P.a, i0 + 64, k, bar);
-                    } else {
-                        pair_load(at, &P.a, k, i0, bar);
-                    }
-                    if constexpr (kMnB) {
+                    if (issues) {
+                        const uint32_t at = base + ring.stage * S::stage, bar = first_full + ring.stage * 8;
+                        if (rank == 0) mbar_expect(full + ring.stage * 8, 2 * S::stage);
+                        if constexpr (kMnA) {
+                            pair_load(at, &P.a, i0, k, bar);
+                            pair_load(at + kStep * 128, &P.a, i0 + 64, k, bar);
+                        } else {
+                            pair_load(at, &P.a, k, i0, bar);
+                        }
+                        if constexpr (kMnB) {
 #pragma unroll
-                        for (uint32_t b = 0; b < kTileJ / 128; ++b) pair_load(at + S::a_bytes + b * (kStep * 128), &P.b, j0 + int32_t(b * 64), k, bar);
-                    } else {
-                        pair_load(at + S::a_bytes, &P.b, k, j0, bar);
+                            for (uint32_t b = 0; b < kTileJ / 128; ++b) pair_load(at + S::a_bytes + b * (kStep * 128), &P.b, j0 + int32_t(b * 64), k, bar);
+                        } else {
+                            pair_load(at + S::a_bytes, &P.b, k, j0, bar);
+                        }
                     }
-                    if (++stage == NS) stage = 0, ++round;
+                    ring.next();
                 }
             }
             // the last copies of both CTAs land before either ends (the barrier below), whichever thread's wait may have
             // given up; if one has, the second CTA, whose own barriers nothing completes, waits until its limit
             if (rank == 0) {
-                for (uint32_t q = 0; q < NS && (round || stage); ++q) {
-                    if (stage == 0) stage = NS, --round;
-                    --stage;
-                    mbar_wait_pair(smem_addr(&s_full[stage]), round & 1);
-                }
+                while (ring.back()) mbar_wait_pair(full + ring.stage * 8, ring.parity);
             } else if (!ok) {
-                mbar_wait(smem_addr(&s_full[0]), 0);
+                mbar_wait(full, 0);
             }
-        } else if (warp == kEpilogue / 32 + 1 && lane == 0 && rank == 0) {
+        } else if (warp == kEpilogue / 32 + 1 && rank == 0) {
+            const bool issues = one_thread();
             constexpr uint32_t desc = mma_desc(2 * kTileI, kTileJ, kMnA, kMnB);
             const uint64_t a0 = tile_desc(base, kMnA ? kStep * 128 : 16, 1024), b0 = tile_desc(base + S::a_bytes, kMnB ? kStep * 128 : 16, 1024);
-            uint32_t stage = 0, round = 0, r = 0;      // r: runs so far
+            const uint32_t full = smem_addr(&s_full[0]), free = smem_addr(&s_free[0]);
+            Ring<NS> ring;
+            Ring<2> run;
             for (uint64_t t = t_first; t < P.tiles && ok; t += t_step)
-                for (uint32_t s = 0, in_run = 0; s < P.steps; ++s) {
-                    if (in_run == 0 && r >= 2) ok = mbar_wait_pair(smem_addr(&s_read[r & 1]), (r / 2 - 1) & 1);
-                    if (ok) ok = mbar_wait_pair(smem_addr(&s_full[stage]), round & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t a = a0 + stage * (S::stage >> 4), b = b0 + stage * (S::stage >> 4);
-                    const uint32_t d = tmem + (r & 1) * kTileJ;
+                for (uint32_t s0 = 0; s0 < P.steps && ok; s0 += P.run) {
+                    ok = mbar_wait_pair(smem_addr(&s_read[run.stage]), run.parity ^ 1);
+                    const uint32_t d = tmem + run.stage * kTileJ, s1 = min(s0 + P.run, P.steps);
+                    for (uint32_t s = s0; s < s1 && ok; ++s) {
+                        ok = mbar_wait(full + ring.stage * 8, ring.parity);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (issues) {
+                            const uint64_t a = a0 + ring.stage * (S::stage >> 4), b = b0 + ring.stage * (S::stage >> 4);
 #pragma unroll
-                    for (uint32_t q = 0; q < kStep / 16; ++q) pair_mma(d, a + q * (kMnA ? 128 : 2), b + q * (kMnB ? 128 : 2), desc, in_run || q);
-                    pair_commit(smem_addr(&s_free[stage]));
-                    if (++stage == NS) stage = 0, ++round;
-                    if (++in_run == P.run || s + 1 == P.steps) {
-                        pair_commit(smem_addr(&s_sum[r & 1]));
-                        in_run = 0;
-                        ++r;
+                            for (uint32_t q = 0; q < kStep / 16; ++q) pair_mma(d, a + q * (kMnA ? 128 : 2), b + q * (kMnB ? 128 : 2), desc, s > s0 || q);
+                            pair_commit(free + ring.stage * 8);
+                        }
+                        ring.next();
                     }
+                    if (issues) pair_commit(smem_addr(&s_sum[run.stage]));
+                    run.next();
                 }
             // (products whose end nobody waited for, if a wait gave up, end before the CTAs do)
-            for (uint32_t q = 0; q < NS && (round || stage); ++q) {
-                if (stage == 0) stage = NS, --round;
-                --stage;
-                mbar_wait(smem_addr(&s_free[stage]), round & 1);
-            }
+            while (ring.back()) mbar_wait(free + ring.stage * 8, ring.parity);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairMoreRegs));
