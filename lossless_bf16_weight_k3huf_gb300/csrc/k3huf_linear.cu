@@ -123,16 +123,27 @@ __device__ __forceinline__ void finish(const Epilogue &e, uint32_t i, uint32_t j
         for (int c = 0; c < kCount; ++c) v[c] += res[c];
     }
     const uint64_t at = uint64_t(j) * e.out_stride + i;
+    const bool whole = j + kCount <= size_j;
     if (f32) {
         float *o = static_cast<float *>(e.out) + at;
+        if (whole) {
 #pragma unroll
-        for (int c = 0; c < kCount; ++c, o += e.out_stride)
-            if (j + c < size_j) *o = v[c];
+            for (int c = 0; c < kCount; ++c, o += e.out_stride) *o = v[c];
+        } else {
+#pragma unroll
+            for (int c = 0; c < kCount; ++c, o += e.out_stride)
+                if (j + c < size_j) *o = v[c];
+        }
     } else {
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(e.out) + at;
+        if (whole) {
 #pragma unroll
-        for (int c = 0; c < kCount; ++c, o += e.out_stride)
-            if (j + c < size_j) st_f32(o, v[c]);
+            for (int c = 0; c < kCount; ++c, o += e.out_stride) st_f32(o, v[c]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < kCount; ++c, o += e.out_stride)
+                if (j + c < size_j) st_f32(o, v[c]);
+        }
     }
 }
 
@@ -149,13 +160,18 @@ __device__ __forceinline__ void add_run(uint32_t from, float (&sum)[kPart], bool
     }
     if (last) asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// ... and from there, 16 columns at a time, to the result.
+// ... and from there, 16 columns at a time, to the result; the next columns are on their way from TMEM meanwhile.
 template <uint32_t kPart>
 __device__ __forceinline__ void finish_tile(const Epilogue &e, uint32_t from, uint32_t i, uint32_t size_i, uint32_t j, uint32_t size_j, float bias) {
+    uint32_t next[16];
+    tmem_start16(from, next);
 #pragma unroll 1
     for (uint32_t c = 0; c < kPart; c += 16) {
         float v[16];
-        tmem_load16(from + c, v);
+        tmem_wait16(next);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(next[k]);
+        if (c + 16 < kPart) tmem_start16(from + c + 16, next);
         if (i < size_i) finish(e, i, j + c, size_j, v, bias);
         __syncwarp();
     }
@@ -356,7 +372,9 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uin
 __device__ __forceinline__ void pair_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"(uint16_t(3)) : "memory");
 }
-__device__ __forceinline__ void arrive_at(uint32_t cluster_bar) { asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory"); }
+// (nothing but the sums in TMEM is handed back, and their loads are complete: a release would wait for every store of the
+// results, 110 us instead of 88 for 8192 x 8192 x 576 fp32)
+__device__ __forceinline__ void arrive_at(uint32_t cluster_bar) { asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory"); }
 // a wait for arrivals of the other CTA's threads
 __device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity) {
     for (uint32_t i = 0; i < kTcPolls; ++i) {

@@ -114,6 +114,26 @@ def test_rows_of_any_alignment(pad):
     assert int(st) == 0
 
 
+def test_what_lies_between_rows_is_not_read_or_written():
+    """Rows that start on 16 bytes and end inside a block of 16: NaN behind them takes no part, and stays."""
+    for n, rows, cols in ((300, 261, 333), (5, 261, 333), (300, 515, 1001), (2000, 1030, 77)):
+        x, w, dz = (normal(a, b, seed=a + b, std=0.3) for a, b in ((n, cols), (rows, cols), (n, rows)))
+        def spread(v):
+            held = torch.full((v.shape[0], (v.shape[1] + 15) // 8 * 8), float("nan"), dtype=BF, device="cuda")
+            held[:, : v.shape[1]] = v
+            return held[:, : v.shape[1]]
+        for y_type in (BF, F32):
+            y, st = torch.full((n, (rows + 15) // 8 * 8), 7.0, dtype=y_type, device="cuda"), status()
+            k3.linear(spread(x), spread(w), y[:, :rows], st)
+            check(y[:, :rows], x.double() @ w.double().T, sum_bound(x, w), "y")
+            assert bool((y[:, rows:] == 7.0).all())
+            dx, dw = torch.full((n, (cols + 15) // 8 * 8), 7.0, dtype=y_type, device="cuda"), torch.empty(rows, cols, device="cuda")
+            k3.linear_grad(spread(x), spread(w), spread(dz), st, dx=dx[:, :cols], dw=dw)
+            check(dx[:, :cols], dz.double() @ w.double(), sum_bound(dz, w.T), "dx")
+            check(dw, dz.double().T @ x.double(), sum_bound(dz.T, x.T), "dw")
+            assert bool((dx[:, cols:] == 7.0).all()) and int(st) == 0
+
+
 def test_residual_in_place_and_one_row():
     x, w = normal(40, 320, seed=1), normal(200, 320, seed=2, std=0.05)
     for y_type in (BF, F32):
