@@ -77,9 +77,11 @@ __device__ __forceinline__ float bias_at(const Epilogue &e, uint32_t i) {
     return !e.bias ? 0.f : e.bias_type == K3HUF_F32 ? static_cast<const float *>(e.bias)[i] : ld_f32(static_cast<const __nv_bfloat16 *>(e.bias) + i);
 }
 
-// kCount neighbouring columns j of the thread's i: sums to results.
+__device__ __forceinline__ bool aligned_to_device(const void *p, uint32_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// kCount neighbouring columns j of the thread's i: sums to values of the result ...
 template <int kCount>
-__device__ __forceinline__ void finish(const Epilogue &e, uint32_t i, uint32_t j, uint32_t size_j, float (&v)[kCount], float bias) {
+__device__ __forceinline__ void apply(const Epilogue &e, uint32_t i, uint32_t j, uint32_t size_j, float (&v)[kCount], float bias) {
     const bool f32 = e.out_type == K3HUF_F32;
     float res[kCount];
     if (e.residual) {
@@ -122,9 +124,13 @@ __device__ __forceinline__ void finish(const Epilogue &e, uint32_t i, uint32_t j
 #pragma unroll
         for (int c = 0; c < kCount; ++c) v[c] += res[c];
     }
+}
+// ... which are stored.
+template <int kCount>
+__device__ __forceinline__ void store(const Epilogue &e, uint32_t i, uint32_t j, uint32_t size_j, const float (&v)[kCount]) {
     const uint64_t at = uint64_t(j) * e.out_stride + i;
     const bool whole = j + kCount <= size_j;
-    if (f32) {
+    if (e.out_type == K3HUF_F32) {
         float *o = static_cast<float *>(e.out) + at;
         if (whole) {
 #pragma unroll
@@ -144,6 +150,33 @@ __device__ __forceinline__ void finish(const Epilogue &e, uint32_t i, uint32_t j
             for (int c = 0; c < kCount; ++c, o += e.out_stride)
                 if (j + c < size_j) st_f32(o, v[c]);
         }
+    }
+}
+
+// Four neighbouring i of one column: sums to results.
+__device__ __forceinline__ void finish_four(const Epilogue &e, uint32_t i, uint32_t size_i, uint32_t j, const float (&v)[4], const float (&bias)[4]) {
+    Epilogue at = e;                          // (as a row of columns: i and j change places)
+    at.out_stride = at.residual_stride = at.z_stride = 1;
+    const uint32_t w = e.out_type == K3HUF_F32 ? 4 : 2;
+    at.out = static_cast<uint8_t *>(e.out) + (uint64_t(j) * e.out_stride + i) * w;
+    if (e.residual) at.residual = static_cast<const uint8_t *>(e.residual) + (uint64_t(j) * e.residual_stride + i) * w;
+    if (e.z) at.z = static_cast<uint8_t *>(e.z) + (uint64_t(j) * e.z_stride + i) * (e.z_type == K3HUF_F32 ? 4 : 2);
+    at.bias = nullptr;
+    float u[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) u[k] = e.bias ? v[k] + bias[k] : v[k];
+    const uint32_t count = i < size_i ? min(size_i - i, 4u) : 0u;
+    if (count == 0) return;
+    apply(at, 0, 0, count, u, 0.f);
+    if (count == 4 && e.out_type == K3HUF_F32 && aligned_to_device(at.out, 16)) *static_cast<float4 *>(at.out) = make_float4(u[0], u[1], u[2], u[3]);
+    else if (count == 4 && e.out_type == K3HUF_BF16 && aligned_to_device(at.out, 8)) {
+        uint2 o;
+        __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&o);
+        h[0] = __floats2bfloat162_rn(u[0], u[1]);
+        h[1] = __floats2bfloat162_rn(u[2], u[3]);
+        *static_cast<uint2 *>(at.out) = o;
+    } else {
+        store(at, 0, 0, count, u);
     }
 }
 
@@ -172,7 +205,10 @@ __device__ __forceinline__ void finish_tile(const Epilogue &e, uint32_t from, ui
 #pragma unroll
         for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(next[k]);
         if (c + 16 < kPart) tmem_start16(from + c + 16, next);
-        if (i < size_i) finish(e, i, j + c, size_j, v, bias);
+        if (i < size_i) {
+            apply(e, i, j + c, size_j, v, bias);
+            store(e, i, j + c, size_j, v);
+        }
         __syncwarp();
     }
 }
@@ -184,6 +220,34 @@ __device__ __forceinline__ void tile_place(const ProductParams &P, uint64_t t, u
     const uint32_t g = uint32_t(t / whole), rest = uint32_t(t % whole), rows = min(kGroup, P.tiles_i - g * kGroup);
     ti = g * kGroup + rest % rows;
     tj = rest / rows;
+}
+
+// Sums of the splits' partial sums, in their order, to results: columns c, c + 8, ... below c1 of the tile that begins at
+// column j, four neighbouring i of each; the loads of kBatch columns from kMost (or fewer) CTAs are in flight at once.
+template <uint32_t kBatch, uint32_t kMost>
+__device__ __forceinline__ void join(const ProductParams &P, const float *mine, uint32_t i, uint32_t j, uint32_t c, uint32_t c1) {
+    constexpr uint32_t kWarps = kEpilogue / 32;
+    float bias[4];
+#pragma unroll
+    for (uint32_t u = 0; u < 4; ++u) bias[u] = i + u < P.size_i ? bias_at(P.e, i + u) : 0.f;
+    for (; c < c1; c += kBatch * kWarps) {
+        float4 part[kBatch][kMost];
+#pragma unroll
+        for (uint32_t k = 0; k < kBatch; ++k)
+#pragma unroll
+            for (uint32_t q = 0; q < kMost; ++q)
+                if (q < P.splits && c + k * kWarps < c1) part[k][q] = cluster_load4(smem_addr(mine + (c + k * kWarps) * kTileI), q);
+#pragma unroll
+        for (uint32_t k = 0; k < kBatch; ++k) {
+            const uint32_t col = c + k * kWarps;
+            if (col >= c1) break;
+            float v[4] = {part[k][0].x, part[k][0].y, part[k][0].z, part[k][0].w};
+#pragma unroll
+            for (uint32_t q = 1; q < kMost; ++q)
+                if (q < P.splits) v[0] += part[k][q].x, v[1] += part[k][q].y, v[2] += part[k][q].z, v[3] += part[k][q].w;
+            finish_four(P.e, i, P.size_i, j + col, v, bias);
+        }
+    }
 }
 
 template <uint32_t kTileJ, bool kMnA, bool kMnB>
@@ -314,20 +378,12 @@ __global__ void __launch_bounds__(kThreads, Shape<kTileJ>::per_sm) product_kerne
         cluster_wait();
         uint32_t ti, tj;
         tile_place(P, t_first, ti, tj);
-        const uint32_t i = ti * kTileI + quarter * 32 + lane;
-        if (warp < kEpilogue / 32 && i < P.size_i) {
-            const float bias = bias_at(P.e, i);
-            const uint32_t c0 = kTileJ * split / P.splits, c1 = kTileJ * (split + 1) / P.splits;
-            for (uint32_t c = c0 + warp / 4; c < c1 && tj * kTileJ + c < P.size_j; c += 2) {
-                float part[kMaxSplits], v[1] = {0.f};
-#pragma unroll
-                for (uint32_t q = 0; q < kMaxSplits; ++q)
-                    if (q < P.splits) part[q] = cluster_load(smem_addr(parts + c * kTileI + quarter * 32 + lane), q);
-#pragma unroll
-                for (uint32_t q = 0; q < kMaxSplits; ++q)
-                    if (q < P.splits) v[0] += part[q];
-                finish(P.e, i, tj * kTileJ + c, P.size_j, v, bias);
-            }
+        if (warp < kEpilogue / 32) {
+            const uint32_t c0 = kTileJ * split / P.splits, c1 = min(kTileJ * (split + 1) / P.splits, P.size_j - tj * kTileJ);
+            const float *mine = parts + lane * 4;             // four neighbouring i of a column per thread, a column per warp
+            if (P.splits <= 2) join<8, 2>(P, mine, ti * kTileI + lane * 4, tj * kTileJ, c0 + warp, c1);
+            else if (P.splits <= 4) join<4, 4>(P, mine, ti * kTileI + lane * 4, tj * kTileJ, c0 + warp, c1);
+            else join<2, 8>(P, mine, ti * kTileI + lane * 4, tj * kTileJ, c0 + warp, c1);
         }
         __syncwarp();
         cluster_arrive();
@@ -706,29 +762,39 @@ struct Cut {
     uint32_t tile_j, pair, splits;
     uint64_t tiles;
 };
-// The cut of the lowest cost by this count of cycles: a step of 64 of the contraction takes the tensor core 128 x tile_j x 64
-// / 4096 cycles per CTA and the copies their bytes at kLoadRate; CTAs that share an SM share both; a tile costs kTileCost more.
-constexpr uint64_t kLoadRate = 48, kTileCost = 3000;
+// The cut of the lowest cost by this count of cycles.  A step of 64 of the contraction takes the tensor core 128 x tile_j x
+// 64 / 4096 cycles per CTA, a tenth more where it is kept busiest, and the copies their bytes at kLoadRate; CTAs that share
+// an SM share both.  The epilogue takes kColumnCost for each of a thread's columns, beside the next tile's steps and after
+// the last tile; partial sums that meet cost kJoinCost; and the operands come from memory at kMemoryRate.  (Times of the
+// cuts it chooses between, us: 777 x 8192 x 576 in pairs of 128 columns 12, of 256 16, single CTAs of 128 15; 256 x 8192 x
+// 8192 32, 43, 36; 8192 x 576 x 8192 70, 78, 90; 4096 x 4096 x 4096 83, 80, 105; 100 x 1000 x 1000 in CTAs of 32 columns
+// 6.7 with four splits, 7.7 without.)
+constexpr uint64_t kLoadRate = 64, kColumnCost = 75, kJoinCost = 4500, kMemoryRate = 3344;
 template <bool kMnB>
 Cut choose(uint64_t size_i, uint64_t size_j, uint64_t steps, uint64_t sms) {
     Cut best{};
     uint64_t least = ~0ull;
+    const uint64_t memory = (size_i + size_j) * steps * kStep * 2 / kMemoryRate;
     auto consider = [&](uint32_t tile_j, uint32_t pair, uint64_t per_sm) {
         Cut c{tile_j, pair, 1, (size_i + kTileI * pair - 1) / (kTileI * pair) * ((size_j + tile_j - 1) / tile_j)};
-        const uint64_t slots = sms * per_sm / pair;
-        if (pair == 1) c.splits = uint32_t(std::max<uint64_t>(1, std::min<uint64_t>({kMaxSplits, slots / c.tiles, steps / 4})));
-        const uint64_t step = per_sm * std::max<uint64_t>(2 * tile_j, (kTileI + tile_j / pair) * 128 / kLoadRate);
-        const uint64_t waves = (c.tiles * c.splits + slots - 1) / slots, cost = waves * ((steps + c.splits - 1) / c.splits * step + kTileCost);
-        if (cost < least) least = cost, best = c;
+        const uint64_t busy = tile_j == 256 ? 560 : 2 * tile_j;
+        const uint64_t slots = sms * per_sm / pair, step = per_sm * std::max<uint64_t>(busy, (kTileI + tile_j / pair) * 128 / kLoadRate);
+        const uint64_t epilogue = kColumnCost * std::max(tile_j / 2, 16u);
+        const uint64_t most = pair == 2 ? 1 : std::max<uint64_t>(1, std::min<uint64_t>({kMaxSplits, slots / c.tiles, steps / 2}));
+        for (c.splits = 1; c.splits <= most; ++c.splits) {
+            const uint64_t waves = (c.tiles * c.splits + slots - 1) / slots;
+            const uint64_t cost = std::max(memory, waves * std::max((steps + c.splits - 1) / c.splits * step, epilogue)) + epilogue + (c.splits > 1 ? kJoinCost : 0);
+            if (cost < least || (cost == least && c.tile_j == best.tile_j)) least = cost, best = c;
+        }
     };
-    if constexpr (!kMnB) {
-        consider(16, 1, Shape<16>::per_sm);
-        consider(32, 1, Shape<32>::per_sm);
-    }
-    consider(64, 1, Shape<64>::per_sm);
-    consider(128, 1, Shape<128>::per_sm);
-    consider(128, 2, 1);
     consider(256, 2, 1);
+    consider(128, 2, 1);
+    consider(128, 1, Shape<128>::per_sm);
+    consider(64, 1, Shape<64>::per_sm);
+    if constexpr (!kMnB) {
+        consider(32, 1, Shape<32>::per_sm);
+        consider(16, 1, Shape<16>::per_sm);
+    }
     return best;
 }
 

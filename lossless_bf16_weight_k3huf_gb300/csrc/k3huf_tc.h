@@ -68,6 +68,13 @@ __device__ __forceinline__ float cluster_load(uint32_t at, uint32_t rank) {
     return v;
 }
 
+__device__ __forceinline__ float4 cluster_load4(uint32_t at, uint32_t rank) {
+    float4 v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at), "r"(rank) : "memory");
+    return v;
+}
+
 // Where chunk c (16 bytes) of row r lies in a tile.
 __device__ __forceinline__ uint32_t tile_at(uint32_t r, uint32_t c) { return r * 128 + ((c ^ (r & 7u)) << 4); }
 
