@@ -69,8 +69,7 @@ struct ProductParams {
     CUtensorMap a, b;
     Epilogue e;
     uint32_t *status;
-    uint64_t tiles;
-    uint32_t size_i, size_j, steps, tiles_i, tiles_j, splits, run;     // run: steps added up in TMEM
+    uint32_t tiles, size_i, size_j, steps, tiles_i, tiles_j, splits, run;     // run: steps added up in TMEM
 };
 
 __device__ __forceinline__ float bias_at(const Epilogue &e, uint32_t i) {
@@ -215,9 +214,8 @@ __device__ __forceinline__ void finish_tile(const Epilogue &e, uint32_t from, ui
 
 // Order of the tiles: kGroup rows of tiles at a time, so that the CTAs at work at once share operands.
 constexpr uint32_t kGroup = 16;
-__device__ __forceinline__ void tile_place(const ProductParams &P, uint64_t t, uint32_t &ti, uint32_t &tj) {
-    const uint64_t whole = uint64_t(kGroup) * P.tiles_j;
-    const uint32_t g = uint32_t(t / whole), rest = uint32_t(t % whole), rows = min(kGroup, P.tiles_i - g * kGroup);
+__device__ __forceinline__ void tile_place(const ProductParams &P, uint32_t t, uint32_t &ti, uint32_t &tj) {
+    const uint32_t whole = kGroup * P.tiles_j, g = t / whole, rest = t % whole, rows = min(kGroup, P.tiles_i - g * kGroup);
     ti = g * kGroup + rest % rows;
     tj = rest / rows;
 }
@@ -260,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kTileJ>::per_sm) product_kerne
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32, base = smem_addr(smem);
     const uint32_t split = blockIdx.x % P.splits;
-    const uint64_t t_first = blockIdx.x / P.splits, t_step = gridDim.x / P.splits;
+    const uint32_t t_first = blockIdx.x / P.splits, t_step = gridDim.x / P.splits;
     const uint32_t k0 = uint32_t(uint64_t(P.steps) * split / P.splits), n_steps = uint32_t(uint64_t(P.steps) * (split + 1) / P.splits) - k0;
     const uint32_t runs = (n_steps + P.run - 1) / P.run;
     if (warp == 0) tmem_alloc(smem_addr(&s_tmem), 2 * kTileJ);
@@ -289,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kTileJ>::per_sm) product_kerne
         const bool issues = one_thread();
         Ring<NS> ring;
         const uint32_t full = smem_addr(&s_full[0]), free = smem_addr(&s_free[0]);
-        for (uint64_t t = t_first; t < P.tiles && ok; t += t_step) {
+        for (uint32_t t = t_first; t < P.tiles && ok; t += t_step) {
             uint32_t ti, tj;
             tile_place(P, t, ti, tj);
             const int32_t i0 = int32_t(ti * kTileI), j0 = int32_t(tj * kTileJ);
@@ -325,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kTileJ>::per_sm) product_kerne
         const uint32_t full = smem_addr(&s_full[0]), free = smem_addr(&s_free[0]);
         Ring<NS> ring;
         Ring<2> run;
-        for (uint64_t t = t_first; t < P.tiles && ok; t += t_step)
+        for (uint32_t t = t_first; t < P.tiles && ok; t += t_step)
             for (uint32_t s0 = 0; s0 < n_steps && ok; s0 += P.run) {
                 ok = mbar_wait(smem_addr(&s_read[run.stage]), run.parity ^ 1);
                 const uint32_t d = tmem + run.stage * kTileJ, s1 = min(s0 + P.run, n_steps);
@@ -348,11 +346,20 @@ __global__ void __launch_bounds__(kThreads, Shape<kTileJ>::per_sm) product_kerne
         while (ring.back()) mbar_wait(free + ring.stage * 8, ring.parity);
     } else {
         uint32_t r = 0;
-        for (uint64_t t = t_first; t < P.tiles; t += t_step) {
+        auto bias_of = [&](uint32_t t) {
+            uint32_t ti, tj;
+            if (t >= P.tiles || !P.e.bias) return 0.f;
+            tile_place(P, t, ti, tj);
+            const uint32_t i = ti * kTileI + quarter * 32 + lane;
+            return i < P.size_i ? bias_at(P.e, i) : 0.f;
+        };
+        float next_bias = bias_of(t_first);
+        for (uint32_t t = t_first; t < P.tiles; t += t_step) {
             uint32_t ti, tj;
             tile_place(P, t, ti, tj);
             const uint32_t i = ti * kTileI + quarter * 32 + lane;
-            const float bias = i < P.size_i ? bias_at(P.e, i) : 0.f;
+            const float bias = next_bias;
+            next_bias = bias_of(t + t_step);  // (on its way while this tile is finished)
             for (uint32_t q = 0; q < runs; ++q, ++r) {
                 if (ok) ok = mbar_wait(smem_addr(&s_sum[r & 1]), r / 2 & 1);
                 tc_fence_after();
@@ -451,7 +458,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1) pair_kern
     __shared__ uint32_t s_tmem;
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const uint32_t tid = threadIdx.x, warp = tid / 32, lane = tid % 32, base = smem_addr(smem), rank = blockIdx.x % 2;
-    const uint64_t t_first = blockIdx.x / 2, t_step = gridDim.x / 2;
+    const uint32_t t_first = blockIdx.x / 2, t_step = gridDim.x / 2;
     const uint32_t runs = (P.steps + P.run - 1) / P.run;
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)), "r"(2 * kTileJ) : "memory");
@@ -482,7 +489,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1) pair_kern
             const bool issues = one_thread();
             Ring<NS> ring;
             const uint32_t full = smem_addr(&s_full[0]), first_full = in_cta(full, 0), free = smem_addr(&s_free[0]);
-            for (uint64_t t = t_first; t < P.tiles && ok; t += t_step) {
+            for (uint32_t t = t_first; t < P.tiles && ok; t += t_step) {
                 uint32_t ti, tj;
                 tile_place(P, t, ti, tj);
                 const int32_t i0 = int32_t((ti * 2 + rank) * kTileI), j0 = int32_t(tj * kTileJ + rank * (kTileJ / 2));
@@ -523,7 +530,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1) pair_kern
             const uint32_t full = smem_addr(&s_full[0]), free = smem_addr(&s_free[0]);
             Ring<NS> ring;
             Ring<2> run;
-            for (uint64_t t = t_first; t < P.tiles && ok; t += t_step)
+            for (uint32_t t = t_first; t < P.tiles && ok; t += t_step)
                 for (uint32_t s0 = 0; s0 < P.steps && ok; s0 += P.run) {
                     ok = mbar_wait_pair(smem_addr(&s_read[run.stage]), run.parity ^ 1);
                     const uint32_t d = tmem + run.stage * kTileJ, s1 = min(s0 + P.run, P.steps);
@@ -549,11 +556,20 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1) pair_kern
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairMoreRegs));
         const uint32_t quarter = warp % 4, c_first = warp / 4 * S::part;
         uint32_t r = 0;
-        for (uint64_t t = t_first; t < P.tiles; t += t_step) {
+        auto bias_of = [&](uint32_t t) {
+            uint32_t ti, tj;
+            if (t >= P.tiles || !P.e.bias) return 0.f;
+            tile_place(P, t, ti, tj);
+            const uint32_t i = (ti * 2 + rank) * kTileI + quarter * 32 + lane;
+            return i < P.size_i ? bias_at(P.e, i) : 0.f;
+        };
+        float next_bias = bias_of(t_first);
+        for (uint32_t t = t_first; t < P.tiles; t += t_step) {
             uint32_t ti, tj;
             tile_place(P, t, ti, tj);
             const uint32_t i = (ti * 2 + rank) * kTileI + quarter * 32 + lane;
-            const float bias = i < P.size_i ? bias_at(P.e, i) : 0.f;
+            const float bias = next_bias;
+            next_bias = bias_of(t + t_step);  // (on its way while this tile is finished)
             float sum[S::part];
             for (uint32_t q = 0; q < runs; ++q, ++r) {
                 if (ok) ok = mbar_wait(smem_addr(&s_sum[r & 1]), r / 2 & 1);
@@ -764,22 +780,21 @@ struct Cut {
 };
 // The cut of the lowest cost by this count of cycles.  A step of 64 of the contraction takes the tensor core 128 x tile_j x
 // 64 / 4096 cycles per CTA, a tenth more where it is kept busiest, and the copies their bytes at kLoadRate; CTAs that share
-// an SM share both.  The epilogue takes kColumnCost for each of a thread's columns, beside the next tile's steps and after
-// the last tile; partial sums that meet cost kJoinCost; and the operands come from memory at kMemoryRate.  (Times of the
-// cuts it chooses between, us: 777 x 8192 x 576 in pairs of 128 columns 12, of 256 16, single CTAs of 128 15; 256 x 8192 x
-// 8192 32, 43, 36; 8192 x 576 x 8192 70, 78, 90; 4096 x 4096 x 4096 83, 80, 105; 100 x 1000 x 1000 in CTAs of 32 columns
-// 6.7 with four splits, 7.7 without.)
-constexpr uint64_t kLoadRate = 64, kColumnCost = 75, kJoinCost = 4500, kMemoryRate = 3344;
+// an SM share both.  The epilogue's time (of all the SM's CTAs; fitted to 8192 x 8192 x 64) passes beside the next tile's
+// steps, and after the last tile; partial sums that meet cost kJoinCost; and the operands come from memory at kMemoryRate.
+// (Times of the cuts it chooses between, us: 777 x 8192 x 576 in pairs of 128 columns 12, of 256 15, single CTAs of 128 15;
+// 256 x 8192 x 8192 32, 43, 36; 8192 x 8192 x 576 62, 61, 87; 8192 x 576 x 8192 70, 78, 90; 4096 x 4096 x 4096 83, 80,
+// 105; 100 x 1000 x 1000 in CTAs of 32 columns 6.7 with four splits, 7.7 without.)
+constexpr uint64_t kLoadRate = 64, kJoinCost = 4500, kMemoryRate = 3344;
 template <bool kMnB>
 Cut choose(uint64_t size_i, uint64_t size_j, uint64_t steps, uint64_t sms) {
     Cut best{};
     uint64_t least = ~0ull;
     const uint64_t memory = (size_i + size_j) * steps * kStep * 2 / kMemoryRate;
-    auto consider = [&](uint32_t tile_j, uint32_t pair, uint64_t per_sm) {
+    auto consider = [&](uint32_t tile_j, uint32_t pair, uint64_t per_sm, uint64_t epilogue) {
         Cut c{tile_j, pair, 1, (size_i + kTileI * pair - 1) / (kTileI * pair) * ((size_j + tile_j - 1) / tile_j)};
-        const uint64_t busy = tile_j == 256 ? 560 : 2 * tile_j;
+        const uint64_t busy = tile_j == 256 ? 580 : 2 * tile_j;
         const uint64_t slots = sms * per_sm / pair, step = per_sm * std::max<uint64_t>(busy, (kTileI + tile_j / pair) * 128 / kLoadRate);
-        const uint64_t epilogue = kColumnCost * std::max(tile_j / 2, 16u);
         const uint64_t most = pair == 2 ? 1 : std::max<uint64_t>(1, std::min<uint64_t>({kMaxSplits, slots / c.tiles, steps / 2}));
         for (c.splits = 1; c.splits <= most; ++c.splits) {
             const uint64_t waves = (c.tiles * c.splits + slots - 1) / slots;
@@ -787,13 +802,13 @@ Cut choose(uint64_t size_i, uint64_t size_j, uint64_t steps, uint64_t sms) {
             if (cost < least || (cost == least && c.tile_j == best.tile_j)) least = cost, best = c;
         }
     };
-    consider(256, 2, 1);
-    consider(128, 2, 1);
-    consider(128, 1, Shape<128>::per_sm);
-    consider(64, 1, Shape<64>::per_sm);
+    consider(256, 2, 1, 6600);
+    consider(128, 2, 1, 3600);
+    consider(128, 1, Shape<128>::per_sm, 5400);
+    consider(64, 1, Shape<64>::per_sm, 4500);
     if constexpr (!kMnB) {
-        consider(32, 1, Shape<32>::per_sm);
-        consider(16, 1, Shape<16>::per_sm);
+        consider(32, 1, Shape<32>::per_sm, 2300);
+        consider(16, 1, Shape<16>::per_sm, 1900);
     }
     return best;
 }
@@ -802,7 +817,8 @@ template <typename Kernel>
 int launch_product(Kernel kernel, std::atomic<uint64_t> &once, uint32_t threads, size_t smem, uint64_t slots, const Cut &cut, ProductParams &P, cudaStream_t stream) {
     const int rc = once_per_device(once, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)); });
     if (rc) return rc;
-    P.tiles = cut.tiles;
+    if (cut.tiles > 0x3FFFFFFFu) return K3HUF_E_ARG;           // (results of more than 2 x 10^12 elements)
+    P.tiles = uint32_t(cut.tiles);
     P.tiles_i = (P.size_i + kTileI * cut.pair - 1) / (kTileI * cut.pair);
     P.tiles_j = (P.size_j + cut.tile_j - 1) / cut.tile_j;
     P.splits = cut.splits;
