@@ -12,8 +12,8 @@
 // other tokens alone, never taken as a difference: a small rest keeps its digits.
 //
 // Forward, one read of the logits: a CTA streams a row, or the CTAs of a cluster when there are fewer rows than the
-// GPU holds CTAs.  To leave the alternatives out of the rest's sum, a filter of one bit per vector (modulo its size)
-// sends the few vectors that may hold one to a comparison with the list.
+// GPU holds CTAs.  To leave the alternatives out of the rest's sum, every thread has a bit for each of its
+// vectors (modulo 64), which sends the few that may hold one to a comparison with the list.
 //
 // Backward: elementwise; every other token's gradient is s g (Q p_r - q_r) exp(z_j - lse - log p_r), the
 // alternatives' are written over it behind a barrier.
@@ -33,7 +33,7 @@ constexpr int kThreads = 256;                 // that stream; one warp more sees
 constexpr int kAll = kThreads + 32;
 constexpr int kVecs = 4;                      // 16-byte vectors per thread and step
 constexpr int kMaxCluster = 16;
-constexpr uint32_t kFilterBits = 16384;
+static_assert(64 % kVecs == 0, "a step's bits lie side by side in a mask of 64");
 
 struct Sum {
     float m, sum;                             // sum of 2^((x - m) c)
@@ -159,13 +159,43 @@ __device__ Terms terms(const DistillParams &P, const T *x, uint64_t row, uint32_
     return R;
 }
 
-template <typename T, bool kRest>
-__global__ void __launch_bounds__(kAll, 3) distill_kernel(const DistillParams P) {
+// Adds vectors of logits to a running sum.
+template <typename T, int N>
+__device__ __forceinline__ void add_vectors(Sum &s, const uint4 (&v)[N], float c) {
+    constexpr int E = kPer<T>;
+    float big = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) big = fmaxf(big, vec_max<T>(v[i]));
+    rescale(s, fmaxf(s.m, big), c);
+    const float2 minus_m = make_float2(-s.m, -s.m), cc = make_float2(c, c);
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float f[E];
+        unpack<T>(v[i], f);
+#pragma unroll
+        for (int k = 0; k < E; k += 2) {
+            float2 t = __fmul2_rn(__fadd2_rn(make_float2(f[k], f[k + 1]), minus_m), cc);
+            t.x = max_nan(t.x, kFloor);
+            t.y = max_nan(t.y, kFloor);
+            sum = __fadd2_rn(sum, make_float2(exp2_fast(t.x), exp2_fast(t.y)));
+        }
+    }
+    s.sum += sum.x + sum.y;
+}
+template <typename T> __device__ __forceinline__ uint4 nothing() {       // a vector of -infinity
+    constexpr uint32_t w = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+    return make_uint4(w, w, w, w);
+}
+
+template <typename T, bool kRest, int kThreads>
+__global__ void __launch_bounds__(kThreads + 32, kThreads == 128 ? 6 : 4) distill_kernel(const DistillParams P) {
     constexpr int E = kPer<T>, kWarps = kThreads / 32;
+    constexpr uint32_t kSteps = 64 / kVecs;                // of a mask
     __shared__ Sum s_part[kWarps], s_all[kMaxCluster];
     __shared__ Terms s_terms;
-    __shared__ uint32_t s_filter[kRest ? kFilterBits / 32 : 1];
-    __shared__ int32_t s_ids[kRest ? K3HUF_MAX_TOP : 1];
+    __shared__ unsigned long long s_mask[kRest ? kThreads : 1];
+    __shared__ uint2 s_places[kRest ? K3HUF_MAX_TOP : 1];
     const cg::cluster_group cluster = cg::this_cluster();
     const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank(), row = blockIdx.x / C;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -181,24 +211,48 @@ __global__ void __launch_bounds__(kAll, 3) distill_kernel(const DistillParams P)
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             const uint32_t at = (step * kVecs + i) * kThreads + tid;
-            to[i] = step < step1 && at < vecs ? load_vec(x, shift, P.vocab, at)
-                                              : (sizeof(T) == 4 ? make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u)
-                                                                : make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u));
+            to[i] = step < step1 && at < vecs ? load_vec(x, shift, P.vocab, at) : nothing<T>();
         }
     };
     if (warp < kWarps) load(next, step0);
+    // which of a thread's vectors (modulo 64) may hold an alternative: a bit each, kVecs of a step.  The stream passes these
+    // over; what else they hold is added first, a vector per thread
+    uint64_t mask = 0;
+    Sum s{-3.402823466e38f, 0.f};             // (not -infinity: then -infinity minus it is -infinity)
     if constexpr (kRest) {
-        for (uint32_t i = tid; i < kFilterBits / 32; i += kAll) s_filter[i] = 0;
+        const int32_t id = uint32_t(tid) < K ? P.teacher.ids[uint64_t(row) * K + tid] : -1;
+        if (tid < kThreads) s_mask[tid] = 0;
         __syncthreads();
-        if (uint32_t(tid) < K) {
-            const int32_t id = P.teacher.ids[uint64_t(row) * K + tid];
-            s_ids[tid] = id;
-            if (id >= 0 && uint32_t(id) < P.vocab) {
-                const uint32_t at = (uint32_t(id) + shift) / E % kFilterBits;
-                atomicOr(&s_filter[at / 32], 1u << (at % 32));
+        const bool in = id >= 0 && uint32_t(id) < P.vocab;
+        const uint32_t place = (uint32_t(id) + shift) / E;
+        if (uint32_t(tid) < K) s_places[tid] = in ? make_uint2(place, (uint32_t(id) + shift) % E) : make_uint2(0xFFFFFFFFu, 0);
+        if (in) atomicOr(&s_mask[place % kThreads], 1ull << (place / kThreads % 64));
+        __syncthreads();
+        if (tid < kThreads) mask = s_mask[tid];
+        const uint32_t turns = (vecs + kThreads * 64 - 1) / (kThreads * 64);          // vectors per bit
+        if (tid < kThreads)
+            for (uint32_t e = tid; e < K * turns; e += kThreads) {
+                const uint32_t k = e % K, home = s_places[k].x % (kThreads * 64), at = home + e / K * (kThreads * 64);
+                bool take = s_places[k].x != 0xFFFFFFFFu && at < vecs && at / (kThreads * kVecs) >= step0 && at / (kThreads * kVecs) < step1;
+                for (uint32_t q = 0; q < k; ++q) take = take && (s_places[q].x == 0xFFFFFFFFu || s_places[q].x % (kThreads * 64) != home);
+                if (!take) continue;
+                uint4 one[1] = {load_vec(x, shift, P.vocab, at)};
+                uint32_t out = 0;
+                for (uint32_t q = 0; q < K; ++q)
+                    if (s_places[q].x == at) out |= 1u << s_places[q].y;
+                uint32_t w[4] = {one[0].x, one[0].y, one[0].z, one[0].w};
+#pragma unroll
+                for (uint32_t u = 0; u < 4; ++u) {
+                    if constexpr (sizeof(T) == 4) {
+                        if (out >> u & 1) w[u] = 0xFF800000u;
+                    } else {
+                        if (out >> (2 * u) & 1) w[u] = (w[u] & 0xFFFF0000u) | 0xFF80u;
+                        if (out >> (2 * u + 1) & 1) w[u] = (w[u] & 0xFFFFu) | 0xFF800000u;
+                    }
+                }
+                one[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                add_vectors<T>(s, one, c);
             }
-        }
-        __syncthreads();
     }
     if (warp == kWarps) {
         if (rank == 0) {
@@ -206,53 +260,19 @@ __global__ void __launch_bounds__(kAll, 3) distill_kernel(const DistillParams P)
             if (lane == 0) s_terms = R;
         }
     } else {
-        Sum s{-3.402823466e38f, 0.f};         // (not -infinity: then -infinity minus it is -infinity)
         for (uint32_t step = step0; step < step1; ++step) {
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) v[i] = next[i];
             load(next, step + 1);
             if constexpr (kRest) {
+                const uint32_t some = uint32_t(mask >> (step % kSteps * kVecs)) & ((1u << kVecs) - 1);
+                if (some) {
 #pragma unroll
-                for (int i = 0; i < kVecs; ++i) {
-                    const uint32_t at = (step * kVecs + i) * kThreads + tid, bit = at % kFilterBits;
-                    if (s_filter[bit / 32] >> (bit % 32) & 1) {
-                        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                        for (uint32_t k = 0; k < K; ++k) {
-                            const int64_t d = int64_t(s_ids[k]) + shift - int64_t(at) * E;
-                            if (s_ids[k] < 0 || d < 0 || d >= E) continue;
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                if constexpr (sizeof(T) == 4) {
-                                    if (d == u) w[u] = 0xFF800000u;
-                                } else {
-                                    if (d == 2 * u) w[u] = (w[u] & 0xFFFF0000u) | 0xFF80u;
-                                    if (d == 2 * u + 1) w[u] = (w[u] & 0xFFFFu) | 0xFF800000u;
-                                }
-                            }
-                        }
-                        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                    for (int i = 0; i < kVecs; ++i)
+                        if (some >> i & 1) v[i] = nothing<T>();
                 }
             }
-            float big = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) big = fmaxf(big, vec_max<T>(v[i]));
-            rescale(s, fmaxf(s.m, big), c);
-            const float2 minus_m = make_float2(-s.m, -s.m), cc = make_float2(c, c);
-            float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) {
-                float f[E];
-                unpack<T>(v[i], f);
-#pragma unroll
-                for (int k = 0; k < E; k += 2) {
-                    float2 t = __fmul2_rn(__fadd2_rn(make_float2(f[k], f[k + 1]), minus_m), cc);
-                    t.x = max_nan(t.x, kFloor);
-                    t.y = max_nan(t.y, kFloor);
-                    sum = __fadd2_rn(sum, make_float2(exp2_fast(t.x), exp2_fast(t.y)));
-                }
-            }
-            s.sum += sum.x + sum.y;
+            add_vectors<T>(s, v, c);
         }
 #pragma unroll
         for (int d = 16; d; d >>= 1) s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d)}, c);
@@ -261,7 +281,7 @@ __global__ void __launch_bounds__(kAll, 3) distill_kernel(const DistillParams P)
     __syncthreads();
     if (C == 1 && warp > 0) return;
     // one warp: the warps' sums, then the CTAs'
-    Sum s = s_part[lane % kWarps];
+    s = s_part[lane % kWarps];
 #pragma unroll
     for (int d = kWarps / 2; d; d >>= 1) s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d)}, c);
     if (C > 1) {
@@ -480,20 +500,20 @@ __global__ void __launch_bounds__(kAll, kGradPerSm) distill_grad_kernel(const Gr
     __syncthreads();
 }
 
-template <typename T, bool kRest>
+template <typename T, bool kRest, int kThreads>
 int launch_forward(const DistillParams &P, uint32_t n, cudaStream_t stream) {
     constexpr uint32_t kStep = kThreads * kVecs * kPer<T>;
     static std::atomic<uint64_t> wide{0};
     uint64_t sms = 0;
-    int rc = once_per_device(wide, [] { return cudaFuncSetAttribute(distill_kernel<T, kRest>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
+    int rc = once_per_device(wide, [] { return cudaFuncSetAttribute(distill_kernel<T, kRest, kThreads>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
     if (!rc) rc = sm_count(&sms);
     if (rc) return rc;
     // one CTA per row, or a cluster per row while the GPU has room for more CTAs and every CTA still has a step to do
     uint32_t C = 1;
-    while (C < uint32_t(kMaxCluster) && uint64_t(n) * C < sms * 2 && P.vocab / kStep >= 2 * C) C *= 2;
+    while (C < uint32_t(kMaxCluster) && uint64_t(n) * C < sms * 512 / kThreads && P.vocab / kStep >= 2 * C) C *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n * C);
-    cfg.blockDim = dim3(kAll);
+    cfg.blockDim = dim3(kThreads + 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -501,7 +521,14 @@ int launch_forward(const DistillParams &P, uint32_t n, cudaStream_t stream) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cuda_rc(cudaLaunchKernelEx(&cfg, distill_kernel<T, kRest>, P));
+    return cuda_rc(cudaLaunchKernelEx(&cfg, distill_kernel<T, kRest, kThreads>, P));
+}
+
+// Short rows take CTAs of 128 threads, more of them at once.
+constexpr uint32_t kSmallVocab = 65536;
+template <typename T, bool kRest>
+int launch_forward(const DistillParams &P, uint32_t n, cudaStream_t stream) {
+    return P.vocab <= kSmallVocab ? launch_forward<T, kRest, 128>(P, n, stream) : launch_forward<T, kRest, 256>(P, n, stream);
 }
 
 template <typename T>
