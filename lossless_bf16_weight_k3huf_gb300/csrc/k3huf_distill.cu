@@ -54,27 +54,23 @@ __device__ __forceinline__ double warp_sum(double v) {
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
 }
-__device__ __forceinline__ double warp_max(double v) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, d));
-    return v;
-}
-
 struct Teacher {
     const int32_t *ids;
     const float *top;
     uint32_t count, mode;                     // alternatives per row
 };
 
-// A row's alternatives, by one warp, two per lane (entries lane and lane + 32; id -1: none, q 0).
+// A row's alternatives, by one warp: entry `lane`, and, of more than 32, entry lane + 32 (id -1: none, q 0).  64-bit
+// arithmetic runs at a sixtieth of the 32-bit rate, so nothing is computed twice or for a second entry that is not there.
 struct Alternatives {
     int32_t id[2];
-    double t[2], q[2];                        // log q (0 for none), q
+    double t[2], q[2];                        // log q (-infinity for none), q
     double mass, rest;                        // sum of q; what is left of 1, where that is wanted
     bool any;
 };
 __device__ __forceinline__ Alternatives alternatives(const Teacher &T, uint64_t row, uint32_t vocab, uint32_t lane, uint32_t *status) {
     Alternatives A;
+    const int entries = T.count > 32 ? 2 : 1;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const uint32_t i = lane + 32 * e;
@@ -84,29 +80,31 @@ __device__ __forceinline__ Alternatives alternatives(const Teacher &T, uint64_t 
             A.id[e] = -1;
         }
         A.t[e] = A.id[e] >= 0 ? double(T.top[row * T.count + i]) : -INFINITY;
+        A.q[e] = 0.;
     }
     A.any = __any_sync(0xffffffffu, A.id[0] >= 0 || A.id[1] >= 0);
+    double m = 0.;
     if (T.mode == K3HUF_DISTILL_NORMALISED) {
-        // (largest -infinity: every q is 0; NaN, and +infinity, make the row NaN)
-        const double m = warp_max(fmax(A.t[0], A.t[1]));
-        double sum = 0;
+        // (the largest, of floats; where it is -infinity every q is 0; NaN, and +infinity, make the row NaN)
+        float most = fmaxf(float(A.t[0]), float(A.t[1]));
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (A.id[e] >= 0 && !(A.t[e] == -INFINITY)) sum += exp(A.t[e] - m);
-        sum = warp_sum(sum);
-        if (sum > 0 || sum != sum) {
-            const double lse = m + log(sum);
-            A.t[0] -= lse;
-            A.t[1] -= lse;
-        }
+        for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+        m = most == -INFINITY ? 0. : double(most);
     }
     double mass = 0;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        A.q[e] = A.id[e] < 0 || A.t[e] == -INFINITY ? 0. : exp(A.t[e]);
+        if (e >= entries) break;
+        A.q[e] = A.t[e] == -INFINITY ? 0. : exp(A.t[e] - m);
         mass += A.q[e];
     }
     A.mass = warp_sum(mass);
+    if (T.mode == K3HUF_DISTILL_NORMALISED && !(A.mass == 0.)) {
+        const double lse = m + log(A.mass), one = 1. / A.mass;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) A.t[e] -= lse, A.q[e] *= one;
+        A.mass = A.mass == A.mass ? 1. : A.mass;
+    }
     A.rest = T.mode != K3HUF_DISTILL_REST ? 0. : A.mass > 1. ? 0. : 1. - A.mass;
     return A;
 }
@@ -124,24 +122,27 @@ struct DistillParams {
 // What the alternatives give to the loss, by the warp that does not stream, while the others do.
 struct Terms {
     double sum, mass, rest;                   // sum of q (t - s (x - from)); of q; the rest's q
-    double top, from, top_sum;                // the largest of their logits; the same if it is finite, else 0; sum of exp(s (x - top)), each token once
+    double from;                              // the largest of their logits if it is finite, else 0
+    float top, top_sum;                       // the largest of their logits; sum of exp(s (x - top)), each token once
     uint32_t any;
 };
 template <typename T, bool kRest>
 __device__ Terms terms(const DistillParams &P, const T *x, uint64_t row, uint32_t lane) {
     const Alternatives A = alternatives(P.teacher, row, P.vocab, lane, P.status);
-    Terms R{0., A.mass, A.rest, 0., 0., 0., A.any};
     float f[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) f[e] = A.id[e] >= 0 ? ld_f32(x + A.id[e]) : -INFINITY;
     float top = fmaxf(f[0], f[1]);
 #pragma unroll
     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    R.top = top;
-    R.from = isfinite(top) ? R.top : 0.;      // (logits of 1e38 would leave nothing of t beside them)
+    // (logits of 1e38 would leave nothing of t beside them)
+    Terms R{0., A.mass, A.rest, isfinite(top) ? double(top) : 0., top, 0.f, A.any};
+    const int entries = P.teacher.count > 32 ? 2 : 1;
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int e = 0; e < 2; ++e) {
+        if (e >= entries) break;
         if (A.id[e] >= 0 && !(A.q[e] == 0.)) R.sum += A.q[e] * (A.t[e] - (double(f[e]) - R.from) * P.scale);
+    }
     R.sum = warp_sum(R.sum);
     if constexpr (kRest) {
         // (a token that is listed twice counts at its first place)
@@ -153,7 +154,7 @@ __device__ Terms terms(const DistillParams &P, const T *x, uint64_t row, uint32_
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-            if (first[e] && f[e] != -INFINITY) R.top_sum += exp((double(f[e]) - R.top) * P.scale);
+            if (first[e] && f[e] != -INFINITY) R.top_sum += expf((f[e] - top) * P.scale);
         R.top_sum = warp_sum(R.top_sum);
     }
     return R;
@@ -295,21 +296,19 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == 128 ? 6 : 4) distil
         for (int d = kMaxCluster / 2; d; d >>= 1) s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d)}, c);
     }
     const Terms R = s_terms;
-    double m = s.m, rest = s.sum, total = rest;
+    float m = s.m, rest = s.sum, total = rest;
     if constexpr (kRest) {
-        m = fmax(m, R.top);
-        // (a lane each: the two sums, then the logarithms)
-        const double f = exp(((lane ? R.top : double(s.m)) - m) * P.scale), scaled = lane ? (R.top_sum == 0. ? 0. : R.top_sum * f) : rest * f;
-        rest = __shfl_sync(0xffffffffu, scaled, 0);
-        total = rest + __shfl_sync(0xffffffffu, scaled, 1);
+        m = fmaxf(m, R.top);
+        rest *= expf((s.m - m) * P.scale);
+        total = rest + (R.top_sum == 0.f ? 0.f : R.top_sum * expf((R.top - m) * P.scale));
     }
-    const double logs = log(lane == 0 ? total : lane == 1 ? rest / total : R.rest);
+    const double logs = log(lane == 0 ? double(total) : lane == 1 ? double(rest) : R.rest);       // (a lane each)
     const double log_total = __shfl_sync(0xffffffffu, logs, 0), log_q = __shfl_sync(0xffffffffu, logs, 2);
-    const double log_rest = total == 0. ? -INFINITY : __shfl_sync(0xffffffffu, logs, 1);
+    const double log_sum = __shfl_sync(0xffffffffu, logs, 1), log_rest = rest == 0.f ? -INFINITY : log_sum - log_total;
     if (lane) return;
-    const double lse = total == 0. ? -INFINITY : m * P.scale + log_total;
+    const double lse = total == 0.f ? -INFINITY : double(m) * P.scale + log_total;
     // (a row of -infinity alone: every log p is -infinity)
-    double loss = total != 0. ? R.sum + R.mass * ((m - R.from) * P.scale + log_total) : R.mass == 0. ? 0. : R.mass * INFINITY;
+    double loss = total != 0.f ? R.sum + R.mass * ((double(m) - R.from) * P.scale + log_total) : R.mass == 0. ? 0. : R.mass * INFINITY;
     if constexpr (kRest) {
         if (P.log_rest) P.log_rest[row] = float(log_rest);
         if (R.rest > 0.) loss += R.rest * (log_q - log_rest);
@@ -384,6 +383,7 @@ __global__ void __launch_bounds__(kAll, kGradPerSm) distill_grad_kernel(const Gr
             // a token that is listed more than once: its first place takes all of its q, in their order
             for (uint32_t k = 0; k < P.teacher.count; ++k) {
                 const int32_t id = __shfl_sync(0xffffffffu, k < 32 ? A.id[0] : A.id[1], k % 32);
+                if (!__any_sync(0xffffffffu, (id == A.id[0] && k != lane) || (id == A.id[1] && k != lane + 32))) continue;
                 const double other = __shfl_sync(0xffffffffu, k < 32 ? A.q[0] : A.q[1], k % 32);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -396,8 +396,7 @@ __global__ void __launch_bounds__(kAll, kGradPerSm) distill_grad_kernel(const Gr
             for (int e = 0; e < 2; ++e)
                 if (mine[e]) {
                     const float f = ld_f32(x + A.id[e]);
-                    const double lp = double(f) * P.scale - lse;
-                    const double prob = f == -INFINITY ? 0. : lp > 0. ? 1. : exp(lp);
+                    const float lp = float(double(f) * P.scale - lse), prob = f == -INFINITY ? 0.f : lp > 0.f ? 1.f : expf(lp);
                     at_next[e] = A.id[e];
                     d_next[e] = float(sg * (Q * prob - q[e]));
                 }
