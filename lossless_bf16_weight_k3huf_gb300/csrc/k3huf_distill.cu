@@ -189,11 +189,49 @@ template <typename T> __device__ __forceinline__ uint4 nothing() {       // a ve
     return make_uint4(w, w, w, w);
 }
 
+// The sum of what the vectors that the stream passes over hold beside the alternatives, of the CTA's steps: those that share
+// a bit with an alternative's (`places`: vector and element of each), one per lane of the warp that does not stream.  (Apart
+// from the kernel, whose registers it would take.)
+template <typename T, int kThreads>
+__device__ __noinline__ Sum passed_over(const T *x, uint32_t shift, uint32_t vocab, uint32_t vecs, uint32_t step0, uint32_t step1, const uint2 *places, uint32_t count, float c) {
+    Sum s{-3.402823466e38f, 0.f};
+    const uint32_t turns = (vecs + kThreads * 64 - 1) / (kThreads * 64);          // vectors per bit
+    for (uint32_t e = threadIdx.x % 32; e < count * turns; e += 32) {
+        const uint32_t k = e % count, of = places[k].x, home = of % (kThreads * 64), at = home + e / count * (kThreads * 64);
+        if (of == 0xFFFFFFFFu || at >= vecs || at / (kThreads * kVecs) < step0 || at / (kThreads * kVecs) >= step1) continue;
+        uint4 one[1] = {load_vec(x, shift, vocab, at)};
+        // (its bit is another's, earlier in the list: that one's thread adds it)
+        uint32_t out = 0;
+        bool mine = true;
+#pragma unroll 4
+        for (uint32_t q = 0; q < count; ++q) {
+            const uint2 p = places[q];
+            mine = mine && !(q < k && p.x != 0xFFFFFFFFu && p.x % (kThreads * 64) == home);
+            out |= p.x == at ? 1u << p.y : 0u;
+        }
+        if (!mine) continue;
+        uint32_t w[4] = {one[0].x, one[0].y, one[0].z, one[0].w};
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u) {
+            if constexpr (sizeof(T) == 4) {
+                if (out >> u & 1) w[u] = 0xFF800000u;
+            } else {
+                if (out >> (2 * u) & 1) w[u] = (w[u] & 0xFFFF0000u) | 0xFF80u;
+                if (out >> (2 * u + 1) & 1) w[u] = (w[u] & 0xFFFFu) | 0xFF800000u;
+            }
+        }
+        one[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        add_vectors<T>(s, one, c);
+    }
+    return s;
+}
+
 template <typename T, bool kRest, int kThreads>
-__global__ void __launch_bounds__(kThreads + 32, kThreads == 128 ? 6 : 4) distill_kernel(const DistillParams P) {
+__global__ void __launch_bounds__(kThreads + 32, kThreads == 256 ? 4 : kRest ? 6 : 7) distill_kernel(const DistillParams P) {
     constexpr int E = kPer<T>, kWarps = kThreads / 32;
     constexpr uint32_t kSteps = 64 / kVecs;                // of a mask
-    __shared__ Sum s_part[kWarps], s_all[kMaxCluster];
+    constexpr uint32_t kParts = kRest ? kWarps + 1 : kWarps;
+    __shared__ Sum s_part[kParts], s_all[kMaxCluster];
     __shared__ Terms s_terms;
     __shared__ unsigned long long s_mask[kRest ? kThreads : 1];
     __shared__ uint2 s_places[kRest ? K3HUF_MAX_TOP : 1];
@@ -217,7 +255,7 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == 128 ? 6 : 4) distil
     };
     if (warp < kWarps) load(next, step0);
     // which of a thread's vectors (modulo 64) may hold an alternative: a bit each, kVecs of a step.  The stream passes these
-    // over; what else they hold is added first, a vector per thread
+    // over
     uint64_t mask = 0;
     Sum s{-3.402823466e38f, 0.f};             // (not -infinity: then -infinity minus it is -infinity)
     if constexpr (kRest) {
@@ -230,32 +268,14 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == 128 ? 6 : 4) distil
         if (in) atomicOr(&s_mask[place % kThreads], 1ull << (place / kThreads % 64));
         __syncthreads();
         if (tid < kThreads) mask = s_mask[tid];
-        const uint32_t turns = (vecs + kThreads * 64 - 1) / (kThreads * 64);          // vectors per bit
-        if (tid < kThreads)
-            for (uint32_t e = tid; e < K * turns; e += kThreads) {
-                const uint32_t k = e % K, home = s_places[k].x % (kThreads * 64), at = home + e / K * (kThreads * 64);
-                bool take = s_places[k].x != 0xFFFFFFFFu && at < vecs && at / (kThreads * kVecs) >= step0 && at / (kThreads * kVecs) < step1;
-                for (uint32_t q = 0; q < k; ++q) take = take && (s_places[q].x == 0xFFFFFFFFu || s_places[q].x % (kThreads * 64) != home);
-                if (!take) continue;
-                uint4 one[1] = {load_vec(x, shift, P.vocab, at)};
-                uint32_t out = 0;
-                for (uint32_t q = 0; q < K; ++q)
-                    if (s_places[q].x == at) out |= 1u << s_places[q].y;
-                uint32_t w[4] = {one[0].x, one[0].y, one[0].z, one[0].w};
-#pragma unroll
-                for (uint32_t u = 0; u < 4; ++u) {
-                    if constexpr (sizeof(T) == 4) {
-                        if (out >> u & 1) w[u] = 0xFF800000u;
-                    } else {
-                        if (out >> (2 * u) & 1) w[u] = (w[u] & 0xFFFF0000u) | 0xFF80u;
-                        if (out >> (2 * u + 1) & 1) w[u] = (w[u] & 0xFFFFu) | 0xFF800000u;
-                    }
-                }
-                one[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                add_vectors<T>(s, one, c);
-            }
     }
     if (warp == kWarps) {
+        if constexpr (kRest) {
+            s = passed_over<T, kThreads>(x, shift, P.vocab, vecs, step0, step1, s_places, K, c);
+#pragma unroll
+            for (int d = 16; d; d >>= 1) s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d)}, c);
+            if (lane == 0) s_part[kWarps] = s;
+        }
         if (rank == 0) {
             const Terms R = terms<T, kRest>(P, x, row, lane);
             if (lane == 0) s_terms = R;
@@ -282,9 +302,9 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == 128 ? 6 : 4) distil
     __syncthreads();
     if (C == 1 && warp > 0) return;
     // one warp: the warps' sums, then the CTAs'
-    s = s_part[lane % kWarps];
+    s = uint32_t(lane) < kParts ? s_part[lane] : Sum{-3.402823466e38f, 0.f};
 #pragma unroll
-    for (int d = kWarps / 2; d; d >>= 1) s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d)}, c);
+    for (int d = kParts > 8 ? 8 : 4; d; d >>= 1) s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d)}, c);
     if (C > 1) {
         cluster_wait();
         if (tid == 0) cluster.map_shared_rank(s_all, 0)[rank] = s;
@@ -509,7 +529,7 @@ int launch_forward(const DistillParams &P, uint32_t n, cudaStream_t stream) {
     if (rc) return rc;
     // one CTA per row, or a cluster per row while the GPU has room for more CTAs and every CTA still has a step to do
     uint32_t C = 1;
-    while (C < uint32_t(kMaxCluster) && uint64_t(n) * C < sms * 512 / kThreads && P.vocab / kStep >= 2 * C) C *= 2;
+    while (C < uint32_t(kMaxCluster) && uint64_t(n) * C * 2 <= sms * (kThreads == 256 ? 4 : kRest ? 6 : 7) && P.vocab / kStep >= 2 * C) C *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(n * C);
     cfg.blockDim = dim3(kThreads + 32);
