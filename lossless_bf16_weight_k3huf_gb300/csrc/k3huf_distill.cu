@@ -42,11 +42,26 @@ __device__ __forceinline__ void rescale(Sum &s, float m, float c) {
     s.sum *= exp2_fast(max_nan((s.m - m) * c, kFloor));
     s.m = m;
 }
-__device__ __forceinline__ Sum join(Sum a, Sum b, float c) {
-    const float m = fmaxf(a.m, b.m);
-    rescale(a, m, c);
-    rescale(b, m, c);
-    return {m, a.sum + b.sum};
+// A warp's sums as one, its largest value and a 64-bit sum: every lane's is brought to that value once, by an exponent
+// whose rounding is made good, and they are added up without loss (each addition's rounding error in a sum of its own).
+// Sums joined pair by pair, 32 bits each, were 5e-8 off: as much as a loss between near distributions shows.
+struct Part {
+    float m;
+    double sum;
+};
+__device__ __forceinline__ Part warp_part(Sum s, float c) {
+    float m = s.m;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float d = max_nan(s.m - m, -2e4f / c), t = d * c, low = fmaf(d, c, -t);
+    float hi = s.sum * exp2_fast(max_nan(t, kFloor)) * fmaf(low, kLn2, 1.f), lo = 0.f;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) {
+        const float b = __shfl_xor_sync(0xffffffffu, hi, k), sum = hi + b, other = sum - hi;
+        lo += __shfl_xor_sync(0xffffffffu, lo, k) + ((hi - (sum - other)) + (b - other));
+        hi = sum;
+    }
+    return {m, double(hi) + double(lo)};
 }
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -54,6 +69,12 @@ __device__ __forceinline__ double warp_sum(double v) {
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
 }
+// exp of a 64-bit number to 32 bits (the rounding of the argument alone would cost |a| 2^-24 of the result).
+__device__ __forceinline__ float exp_of(double a) {
+    const float hi = float(a), lo = isfinite(hi) ? float(a - double(hi)) : 0.f, e = expf(hi);
+    return fmaf(e, lo, e);
+}
+
 struct Teacher {
     const int32_t *ids;
     const float *top;
@@ -116,14 +137,15 @@ struct DistillParams {
     uint32_t *status;
     uint64_t stride;
     uint32_t vocab;
-    float scale, c;                           // c: scale log2 e, finite for every scale
+    float c;                                  // scale log2 e, finite for every scale
+    double scale;                             // c ln 2: what the sum is taken with, so that c's rounding meets both sides of a loss
 };
 
 // What the alternatives give to the loss, by the warp that does not stream, while the others do.
 struct Terms {
     double sum, mass, rest;                   // sum of q (t - s (x - from)); of q; the rest's q
-    double from;                              // the largest of their logits if it is finite, else 0
-    float top, top_sum;                       // the largest of their logits; sum of exp(s (x - top)), each token once
+    double from, top_sum;                     // the largest of their logits if it is finite, else 0; sum of exp(s (x - top)), each token once
+    float top;                                // the largest of their logits
     uint32_t any;
 };
 template <typename T, bool kRest>
@@ -136,7 +158,7 @@ __device__ Terms terms(const DistillParams &P, const T *x, uint64_t row, uint32_
 #pragma unroll
     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     // (logits of 1e38 would leave nothing of t beside them)
-    Terms R{0., A.mass, A.rest, isfinite(top) ? double(top) : 0., top, 0.f, A.any};
+    Terms R{0., A.mass, A.rest, isfinite(top) ? double(top) : 0., 0., top, A.any};
     const int entries = P.teacher.count > 32 ? 2 : 1;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -153,8 +175,10 @@ __device__ Terms terms(const DistillParams &P, const T *x, uint64_t row, uint32_
             if (k < lane + 32 && id == A.id[1]) first[1] = false;
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (first[e] && f[e] != -INFINITY) R.top_sum += expf((f[e] - top) * P.scale);
+        for (int e = 0; e < 2; ++e) {
+            if (e >= entries) break;
+            if (first[e] && f[e] != -INFINITY) R.top_sum += exp((double(f[e]) - double(top)) * P.scale);
+        }
         R.top_sum = warp_sum(R.top_sum);
     }
     return R;
@@ -231,7 +255,7 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == 256 ? 4 : kRest ? 6
     constexpr int E = kPer<T>, kWarps = kThreads / 32;
     constexpr uint32_t kSteps = 64 / kVecs;                // of a mask
     constexpr uint32_t kParts = kRest ? kWarps + 1 : kWarps;
-    __shared__ Sum s_part[kParts], s_all[kMaxCluster];
+    __shared__ Part s_part[kParts], s_all[kMaxCluster];
     __shared__ Terms s_terms;
     __shared__ unsigned long long s_mask[kRest ? kThreads : 1];
     __shared__ uint2 s_places[kRest ? K3HUF_MAX_TOP : 1];
@@ -272,9 +296,8 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == 256 ? 4 : kRest ? 6
     if (warp == kWarps) {
         if constexpr (kRest) {
             s = passed_over<T, kThreads>(x, shift, P.vocab, vecs, step0, step1, s_places, K, c);
-#pragma unroll
-            for (int d = 16; d; d >>= 1) s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d)}, c);
-            if (lane == 0) s_part[kWarps] = s;
+            const Part part = warp_part(s, c);
+            if (lane == 0) s_part[kWarps] = part;
         }
         if (rank == 0) {
             const Terms R = terms<T, kRest>(P, x, row, lane);
@@ -295,40 +318,44 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == 256 ? 4 : kRest ? 6
             }
             add_vectors<T>(s, v, c);
         }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d)}, c);
-        if (lane == 0) s_part[warp] = s;
+        const Part part = warp_part(s, c);
+        if (lane == 0) s_part[warp] = part;
     }
     __syncthreads();
     if (C == 1 && warp > 0) return;
-    // one warp: the warps' sums, then the CTAs'
-    s = uint32_t(lane) < kParts ? s_part[lane] : Sum{-3.402823466e38f, 0.f};
+    // one warp: the warps' sums, then the CTAs', and (not of the rest) the alternatives'
+    float m;
+    double rest, total;
+    auto add = [&](const Part *parts, uint32_t count, bool tops) {
+        Part p{-3.402823466e38f, 0.};
+        if (uint32_t(lane) < count) p = parts[lane];
+        else if (tops && uint32_t(lane) == count) p = {s_terms.top, s_terms.top_sum};
+        m = p.m;
 #pragma unroll
-    for (int d = kParts > 8 ? 8 : 4; d; d >>= 1) s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d)}, c);
-    if (C > 1) {
+        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const double v = p.sum == 0. ? 0. : p.sum * exp_of((double(p.m) - double(m)) * P.scale);
+        rest = warp_sum(uint32_t(lane) < count ? v : 0.);
+        total = tops ? rest + __shfl_sync(0xffffffffu, v, int(count)) : rest;
+    };
+    if (C == 1) {
+        add(s_part, kParts, kRest);
+    } else {
+        add(s_part, kParts, false);
         cluster_wait();
-        if (tid == 0) cluster.map_shared_rank(s_all, 0)[rank] = s;
+        if (tid == 0) cluster.map_shared_rank(s_all, 0)[rank] = Part{m, rest};
         cluster_arrive();
         cluster_wait();
         if (rank > 0 || warp > 0) return;
-        s = uint32_t(lane) < C ? s_all[lane] : Sum{-3.402823466e38f, 0.f};
-#pragma unroll
-        for (int d = kMaxCluster / 2; d; d >>= 1) s = join(s, Sum{__shfl_xor_sync(0xffffffffu, s.m, d), __shfl_xor_sync(0xffffffffu, s.sum, d)}, c);
+        add(s_all, C, kRest);
     }
     const Terms R = s_terms;
-    float m = s.m, rest = s.sum, total = rest;
-    if constexpr (kRest) {
-        m = fmaxf(m, R.top);
-        rest *= expf((s.m - m) * P.scale);
-        total = rest + (R.top_sum == 0.f ? 0.f : R.top_sum * expf((R.top - m) * P.scale));
-    }
-    const double logs = log(lane == 0 ? double(total) : lane == 1 ? double(rest) : R.rest);       // (a lane each)
+    const double logs = log(lane == 0 ? total : lane == 1 ? rest : R.rest);       // (a lane each)
     const double log_total = __shfl_sync(0xffffffffu, logs, 0), log_q = __shfl_sync(0xffffffffu, logs, 2);
-    const double log_sum = __shfl_sync(0xffffffffu, logs, 1), log_rest = rest == 0.f ? -INFINITY : log_sum - log_total;
+    const double log_sum = __shfl_sync(0xffffffffu, logs, 1), log_rest = rest == 0. ? -INFINITY : log_sum - log_total;
     if (lane) return;
-    const double lse = total == 0.f ? -INFINITY : double(m) * P.scale + log_total;
+    const double lse = total == 0. ? -INFINITY : double(m) * P.scale + log_total;
     // (a row of -infinity alone: every log p is -infinity)
-    double loss = total != 0.f ? R.sum + R.mass * ((double(m) - R.from) * P.scale + log_total) : R.mass == 0. ? 0. : R.mass * INFINITY;
+    double loss = total != 0. ? R.sum + R.mass * ((double(m) - R.from) * P.scale + log_total) : R.mass == 0. ? 0. : R.mass * INFINITY;
     if constexpr (kRest) {
         if (P.log_rest) P.log_rest[row] = float(log_rest);
         if (R.rest > 0.) loss += R.rest * (log_q - log_rest);
@@ -588,7 +615,8 @@ extern "C" int k3huf_distill(const void *d_logits, uint32_t type, uint64_t strid
         return K3HUF_E_ARG;
     if (n == 0) return K3HUF_OK;
     if (!d_logits || !d_top_ids || !d_top_logprobs || !d_loss) return K3HUF_E_ARG;
-    const DistillParams P{d_logits, {d_top_ids, d_top_logprobs, top, mode}, d_loss, d_lse, d_log_rest, d_status, stride, vocab, scale, fminf(scale * kLog2e, 3.402823466e38f)};
+    const float c = float(fmin(double(scale) * 1.4426950408889634074, 3.402823466e38));
+    const DistillParams P{d_logits, {d_top_ids, d_top_logprobs, top, mode}, d_loss, d_lse, d_log_rest, d_status, stride, vocab, c, double(c) * 0.69314718055994530942};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool rest = mode == K3HUF_DISTILL_REST;
     if (type == K3HUF_BF16) return rest ? launch_forward<__nv_bfloat16, true>(P, uint32_t(n), st) : launch_forward<__nv_bfloat16, false>(P, uint32_t(n), st);
