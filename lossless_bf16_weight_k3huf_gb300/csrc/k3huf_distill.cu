@@ -371,12 +371,11 @@ struct GradParams {
     const float *lse, *log_rest, *g;
     uint32_t *status;
     uint64_t stride, dx_stride, n;
-    uint32_t vocab, steps, parts, per;        // steps of a row, in so many pieces of so many
+    uint32_t vocab, steps, parts;             // steps of a row, in so many pieces
     float scale;
 };
 
 constexpr int kGradVecs = 4, kGradPerSm = 3;
-constexpr uint32_t kGradSteps = 4;            // steps of a CTA on one row
 
 // One piece of work: some steps of a row.
 struct Piece {
@@ -398,7 +397,7 @@ __global__ void __launch_bounds__(kAll, kGradPerSm) distill_grad_kernel(const Gr
     const uint64_t pieces = P.n * P.parts;
     auto piece_of = [&](uint64_t i) {
         const uint32_t part = uint32_t(i % P.parts);
-        return Piece{i / P.parts, part * P.per, min((part + 1) * P.per, P.steps)};
+        return Piece{i / P.parts, uint32_t(uint64_t(P.steps) * part / P.parts), uint32_t(uint64_t(P.steps) * (part + 1) / P.parts)};
     };
     if (tid >= kThreads) {
         // this warp: a piece's factors, and the gradients of the alternatives in it, a piece ahead of the others;
@@ -586,10 +585,14 @@ int launch_backward(GradParams P, cudaStream_t stream) {
     const uint64_t per = uint64_t(kThreads) * kGradVecs * (vec ? kPer<T> : 1);
     // (a row that starts inside a 16-byte block may need one vector more)
     P.steps = uint32_t((uint64_t(P.vocab) + (vec ? kPer<T> - 1 : 0) + per - 1) / per);
-    // pieces of kGradSteps steps, or fewer while the GPU's CTAs would not all have one
-    P.per = std::min(kGradSteps, P.steps);
-    while (P.per > 1 && P.n * ((P.steps + P.per - 1) / P.per) < sms * kGradPerSm) --P.per;
-    P.parts = (P.steps + P.per - 1) / P.per;
+    // whole rows, or pieces of three steps or more (one, while the GPU's CTAs would not all have a piece) where the CTAs'
+    // last round of them is fuller: every piece costs its row's factors again (4095 rows of 131072 bf16 whole 332 us, in
+    // halves 341, in quarters 349; 515 of 50021 fp32 47, 43, 42)
+    const uint64_t slots = sms * kGradPerSm;
+    auto rounds = [&](uint32_t parts) { return double((P.n * parts + slots - 1) / slots) / parts; };      // (in rows)
+    P.parts = 1;
+    for (uint32_t parts = 2; parts <= P.steps && (3 * parts <= P.steps || P.n * (parts - 1) < slots) && P.n * parts < 64 * slots; ++parts)
+        if (rounds(parts) < 0.98 * rounds(P.parts)) P.parts = parts;
     const uint32_t grid = uint32_t(std::min<uint64_t>(P.n * P.parts, sms * kGradPerSm));
     if (vec) distill_grad_kernel<T, true><<<grid, kAll, 0, stream>>>(P);
     else distill_grad_kernel<T, false><<<grid, kAll, 0, stream>>>(P);
@@ -631,7 +634,7 @@ extern "C" int k3huf_distill_grad(const void *d_logits, uint32_t type, uint64_t 
         return K3HUF_E_ARG;
     if (n == 0) return K3HUF_OK;
     if (!d_logits || !d_dlogits || !d_top_ids || !d_top_logprobs || !d_lse || !d_g_loss || (d_logits == d_dlogits && stride != out_stride)) return K3HUF_E_ARG;
-    const GradParams P{d_logits, d_dlogits, {d_top_ids, d_top_logprobs, top, mode}, d_lse, d_log_rest, d_g_loss, d_status, stride, out_stride, n, vocab, 0, 0, 0, scale};
+    const GradParams P{d_logits, d_dlogits, {d_top_ids, d_top_logprobs, top, mode}, d_lse, d_log_rest, d_g_loss, d_status, stride, out_stride, n, vocab, 0, 0, scale};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return type == K3HUF_BF16 ? launch_backward<__nv_bfloat16>(P, st) : launch_backward<float>(P, st);
 }
