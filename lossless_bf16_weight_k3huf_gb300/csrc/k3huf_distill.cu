@@ -53,8 +53,9 @@ __device__ __forceinline__ Part warp_part(Sum s, float c) {
     float m = s.m;
 #pragma unroll
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float d = max_nan(s.m - m, -2e4f / c), t = d * c, low = fmaf(d, c, -t);
-    float hi = s.sum * exp2_fast(max_nan(t, kFloor)) * fmaf(low, kLn2, 1.f), lo = 0.f;
+    // (far below the largest there is nothing to make good, and infinities of the difference would give NaN)
+    const float d = s.m - m, t = max_nan(d * c, kFloor), low = t > kFloor ? fmaf(d, c, -t) : 0.f;
+    float hi = s.sum * exp2_fast(t) * fmaf(low, kLn2, 1.f), lo = 0.f;
 #pragma unroll
     for (int k = 16; k; k >>= 1) {
         const float b = __shfl_xor_sync(0xffffffffu, hi, k), sum = hi + b, other = sum - hi;

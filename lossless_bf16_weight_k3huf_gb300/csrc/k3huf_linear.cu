@@ -24,6 +24,8 @@ constexpr uint32_t kMaxSplits = 8;
 // Additions in the tensor core before a sum that ends as fp32 moves to registers: one of them errs by about 1.3e-8
 // of the sum, always to the same side.
 constexpr uint32_t kChain = 32;
+// Steps of a sum that ends as bf16: 65536 values, 5e-5 of the sum, and a wait for them that stays far from its limit.
+constexpr uint32_t kLongRun = 1024;
 
 // Place in a ring of stages: the stage, and the parity of the phase that its barrier is in this time round.
 template <uint32_t kStages> struct Ring {
@@ -855,7 +857,7 @@ int product(const Operand &a, const Operand &b, uint64_t size_i, uint64_t size_j
     P.status = status;
     P.size_i = uint32_t(size_i), P.size_j = uint32_t(size_j), P.steps = uint32_t((size_k + kStep - 1) / kStep);
     const bool f32 = e.out_type == K3HUF_F32 || (e.z && e.z_type == K3HUF_F32);
-    P.run = f32 ? kChain / (kStep / 16) : P.steps;
+    P.run = f32 ? kChain / (kStep / 16) : std::min(P.steps, kLongRun);
     const Cut cut = choose<kMnB>(size_i, size_j, P.steps, sms);
     int rc = tensor_map(&P.a, a.p, K3HUF_BF16, a.rows, a.cols, a.stride, kMnA ? kStep : kTileI, kStep, true);
     if (!rc) rc = tensor_map(&P.b, b.p, K3HUF_BF16, b.rows, b.cols, b.stride, kMnB ? kStep : cut.tile_j / cut.pair, kStep, true);
@@ -891,7 +893,7 @@ extern "C" int k3huf_linear(const void *d_x, uint64_t x_stride, uint64_t n_token
         return K3HUF_E_ARG;
     if (!aligned_to(d_x, 2) || !aligned_to(d_w, 2) || (d_bias && !aligned_to(d_bias, elem_bytes(bias_type))) || !aligned_to(d_residual, elem_bytes(y_type)) ||
         !aligned_to(d_y, elem_bytes(y_type)) || (d_z && !aligned_to(d_z, elem_bytes(z_type))) || !aligned_to(d_scratch, 256) || !aligned_to(d_status, 4) ||
-        (d_residual && d_residual == d_y && residual_stride != y_stride))
+        (d_residual && d_residual == d_y && residual_stride != y_stride) || (d_z && d_z == d_y))
         return K3HUF_E_ARG;
     if (n_tokens == 0) return K3HUF_OK;
     if (!d_x || !d_w || !d_y) return K3HUF_E_ARG;

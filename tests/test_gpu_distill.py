@@ -246,6 +246,17 @@ def test_masks_of_the_lowest_value(dtype):
     assert bool(torch.isfinite(d.float()).all())
 
 
+def test_scales_of_every_size():
+    """The smallest and the largest scales, with logits as far apart as fp32 holds."""
+    x, ids, t = make(3, 3000, 8, 11, none=0.0)
+    x[1, ::2], x[1, 1::2] = -3.4e38, 3.3e38
+    for scale in (1e-44, 1e-38, 1e-36, 1e-20, 1e10, 3e38):
+        for mode in MODES:
+            loss, lse, _, _ = run(x, ids, t, mode, scale)
+            assert not bool(torch.isnan(loss).any()) and not bool(torch.isnan(lse).any()), (scale, mode)
+    check(x[:1], ids[:1].contiguous(), t[:1].contiguous(), "rest", scale=1e-30)
+
+
 def test_status_of_ids_past_the_vocabulary():
     x, ids, t = make(5, 700, 6, 6)
     ids[3, 2] = 700

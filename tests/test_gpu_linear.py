@@ -173,6 +173,23 @@ def test_fp32_results_hold_long_sums():
     assert bool(((y.double() - want).abs() <= ((32 + 4) * 2 + cols / 512) * E * want).all())
 
 
+def test_a_contraction_of_several_runs():
+    n, rows, cols = 20, 130, 66000                              # bf16 results leave the tensor core every 65536 values
+    x, w = normal(n, cols, seed=1), normal(rows, cols, seed=2, std=0.01)
+    y, st = torch.empty(n, rows, dtype=BF, device="cuda"), status()
+    k3.linear(x, w, y, st)
+    check(y, x.double() @ w.double().T, sum_bound(x, w), "y")
+    x, dz = normal(140000, 40, seed=3), normal(140000, 24, seed=4)
+    dw = torch.empty(24, 40, device="cuda")
+    k3.linear_grad(x, None, dz, st, dw=dw)
+    check(dw, dz.double().T @ x.double(), sum_bound(dz.T, x.T), "dw")
+    big, small = normal(300, 140000, seed=5), normal(260, 140000, seed=6, std=0.01)
+    y = torch.empty(300, 260, dtype=BF, device="cuda")
+    k3.linear(big, small, y, st)
+    check(y, big.double() @ small.double().T, sum_bound(big, small), "y of pairs")
+    assert int(st) == 0
+
+
 def grads(n, rows, cols, dx_type=BF, add=False, pad=(0, 0, 0), seed=1, want=("dx", "dw")):
     x, w, dz = normal(n, cols, seed=seed, pad=pad[0]), normal(rows, cols, seed=seed + 1, std=0.1, pad=pad[1]), normal(n, rows, seed=seed + 2, pad=pad[2])
     dx = torch.full((n, cols), 7.0, dtype=dx_type, device="cuda")

@@ -119,14 +119,14 @@ def test_scratch_sizes_grow_with_the_tokens():
 
 
 def test_linear(lib):
-    def call(x=P, xs=64, n=4, w=P, ws=64, rows=32, cols=64, bias=P, bt=0, act=1, res=P, rs=32, y=P, ys=32, yt=1, z=P, zs=32, zt=0, scratch=None, size=0, st=P):
+    def call(x=P, xs=64, n=4, w=P, ws=64, rows=32, cols=64, bias=P, bt=0, act=1, res=P, rs=32, y=P, ys=32, yt=1, z=P + 64, zs=32, zt=0, scratch=None, size=0, st=P):
         return lib.k3huf_linear(x, xs, n, w, ws, rows, cols, bias, bt, act, res, rs, y, ys, yt, z, zs, zt, scratch, size, st, None)
 
     assert call(n=0) == k3.OK and call(n=0, x=None, w=None, y=None, z=None, res=None, bias=None) == k3.OK
     for kw in (dict(x=None), dict(x=P + 1), dict(xs=63), dict(n=1 << 31), dict(w=None), dict(w=P + 1), dict(ws=63), dict(rows=0), dict(rows=1 << 31),
                dict(cols=0), dict(cols=1 << 31, xs=1 << 31, ws=1 << 31), dict(bias=P + 1), dict(bt=1, bias=P + 2), dict(bt=2), dict(act=4), dict(res=P + 2),
                dict(rs=31), dict(rs=40), dict(y=None), dict(y=P + 2), dict(ys=31), dict(yt=2), dict(z=P + 1), dict(zs=31), dict(zt=2), dict(zt=1, z=P + 2),
-               dict(st=None), dict(st=P + 2), dict(scratch=P + 16, size=1 << 20)):
+               dict(st=None), dict(st=P + 2), dict(scratch=P + 16, size=1 << 20), dict(z=P, y=P, zt=1)):
         assert call(**kw) == k3.E_ARG, kw
     # rows that do not start on 16 bytes need their copies' room
     need = k3.linear_scratch_bytes(4, 32, 64, any=True)
