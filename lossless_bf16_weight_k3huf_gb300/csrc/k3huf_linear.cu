@@ -80,7 +80,31 @@ __device__ __forceinline__ float bias_at(const Epilogue &e, uint32_t i) {
 
 __device__ __forceinline__ bool aligned_to_device(const void *p, uint32_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// kCount neighbouring columns j of the thread's i: sums to values of the result ...
+// kCount neighbouring columns j of the thread's i, stored.
+template <int kCount, typename T>
+__device__ __forceinline__ void store_as(T *o, uint64_t stride, uint32_t left, const float (&v)[kCount]) {       // left: columns to the matrix's end
+    if (left >= kCount) {
+#pragma unroll
+        for (int c = 0; c < kCount; ++c, o += stride) st_f32(o, v[c]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < kCount; ++c, o += stride)
+            if (c < left) st_f32(o, v[c]);
+    }
+}
+template <int kCount>
+__device__ __forceinline__ void store_to(void *matrix, uint32_t type, uint64_t stride, uint32_t i, uint32_t j, uint32_t size_j, const float (&v)[kCount]) {
+    const uint64_t at = uint64_t(j) * stride + i;
+    const uint32_t left = j < size_j ? size_j - j : 0u;
+    if (type == K3HUF_F32) store_as(static_cast<float *>(matrix) + at, stride, left, v);
+    else store_as(static_cast<__nv_bfloat16 *>(matrix) + at, stride, left, v);
+}
+template <int kCount>
+__device__ __forceinline__ void store(const Epilogue &e, uint32_t i, uint32_t j, uint32_t size_j, const float (&v)[kCount]) {
+    store_to(e.out, e.out_type, e.out_stride, i, j, size_j, v);
+}
+
+// kCount neighbouring columns j of the thread's i: sums to values of the result.
 template <int kCount>
 __device__ __forceinline__ void apply(const Epilogue &e, uint32_t i, uint32_t j, uint32_t size_j, float (&v)[kCount], float bias) {
     const bool f32 = e.out_type == K3HUF_F32;
@@ -101,15 +125,7 @@ __device__ __forceinline__ void apply(const Epilogue &e, uint32_t i, uint32_t j,
 #pragma unroll
         for (int c = 0; c < kCount; ++c) v[c] += bias;
     }
-    if (e.z) {
-#pragma unroll
-        for (int c = 0; c < kCount; ++c) {
-            const uint64_t at = uint64_t(j + c) * e.z_stride + i;
-            if (j + c >= size_j) break;
-            if (e.z_type == K3HUF_F32) static_cast<float *>(e.z)[at] = v[c];
-            else st_f32(static_cast<__nv_bfloat16 *>(e.z) + at, v[c]);
-        }
-    }
+    if (e.z) store_to(e.z, e.z_type, e.z_stride, i, j, size_j, v);
     if (e.act == K3HUF_ACT_RELU) {
 #pragma unroll
         for (int c = 0; c < kCount; ++c) v[c] = v[c] < 0.f ? 0.f : v[c];
@@ -124,33 +140,6 @@ __device__ __forceinline__ void apply(const Epilogue &e, uint32_t i, uint32_t j,
     if (e.residual) {
 #pragma unroll
         for (int c = 0; c < kCount; ++c) v[c] += res[c];
-    }
-}
-// ... which are stored.
-template <int kCount>
-__device__ __forceinline__ void store(const Epilogue &e, uint32_t i, uint32_t j, uint32_t size_j, const float (&v)[kCount]) {
-    const uint64_t at = uint64_t(j) * e.out_stride + i;
-    const bool whole = j + kCount <= size_j;
-    if (e.out_type == K3HUF_F32) {
-        float *o = static_cast<float *>(e.out) + at;
-        if (whole) {
-#pragma unroll
-            for (int c = 0; c < kCount; ++c, o += e.out_stride) *o = v[c];
-        } else {
-#pragma unroll
-            for (int c = 0; c < kCount; ++c, o += e.out_stride)
-                if (j + c < size_j) *o = v[c];
-        }
-    } else {
-        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(e.out) + at;
-        if (whole) {
-#pragma unroll
-            for (int c = 0; c < kCount; ++c, o += e.out_stride) st_f32(o, v[c]);
-        } else {
-#pragma unroll
-            for (int c = 0; c < kCount; ++c, o += e.out_stride)
-                if (j + c < size_j) st_f32(o, v[c]);
-        }
     }
 }
 
@@ -263,22 +252,28 @@ __global__ void __launch_bounds__(kThreads, Shape<kTileJ>::per_sm) product_kerne
     const uint32_t t_first = blockIdx.x / P.splits, t_step = gridDim.x / P.splits;
     const uint32_t k0 = uint32_t(uint64_t(P.steps) * split / P.splits), n_steps = uint32_t(uint64_t(P.steps) * (split + 1) / P.splits) - k0;
     const uint32_t runs = (n_steps + P.run - 1) / P.run;
+    // (the warp that copies makes the barriers and starts; the others meet behind its back)
     if (warp == 0) tmem_alloc(smem_addr(&s_tmem), 2 * kTileJ);
-    if (tid == 0) {
-        for (uint32_t i = 0; i < NS; ++i) {
-            mbar_init(smem_addr(&s_full[i]), 1);
-            mbar_init(smem_addr(&s_free[i]), 1);
+    if (warp == kEpilogue / 32) {
+        if (lane == 0) {
+            for (uint32_t i = 0; i < NS; ++i) {
+                mbar_init(smem_addr(&s_full[i]), 1);
+                mbar_init(smem_addr(&s_free[i]), 1);
+            }
+            for (uint32_t i = 0; i < 2; ++i) {
+                mbar_init(smem_addr(&s_sum[i]), 1);
+                mbar_init(smem_addr(&s_read[i]), kEpilogue / 32);
+            }
+            fence_async_shared();
         }
-        for (uint32_t i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&s_sum[i]), 1);
-            mbar_init(smem_addr(&s_read[i]), kEpilogue / 32);
-        }
-        fence_async_shared();
+        __syncwarp();
+        asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
+    } else {
+        tc_fence_before();
+        asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+        tc_fence_after();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = warp == kEpilogue / 32 ? 0u : s_tmem;
     bool ok = true;
     float sum[S::part];
     const uint32_t quarter = warp % 4, c_first = warp / 4 * S::part;         // (epilogue warps)
@@ -792,11 +787,12 @@ template <bool kMnB>
 Cut choose(uint64_t size_i, uint64_t size_j, uint64_t steps, uint64_t sms) {
     Cut best{};
     uint64_t least = ~0ull;
-    const uint64_t memory = (size_i + size_j) * steps * kStep * 2 / kMemoryRate;
     auto consider = [&](uint32_t tile_j, uint32_t pair, uint64_t per_sm, uint64_t epilogue) {
         Cut c{tile_j, pair, 1, (size_i + kTileI * pair - 1) / (kTileI * pair) * ((size_j + tile_j - 1) / tile_j)};
         const uint64_t busy = tile_j == 256 ? 580 : 2 * tile_j;
         const uint64_t slots = sms * per_sm / pair, step = per_sm * std::max<uint64_t>(busy, (kTileI + tile_j / pair) * 128 / kLoadRate);
+        // (an operand that several tiles read comes from L2 after the first)
+        const uint64_t memory = (size_i * (3 + (size_j + tile_j - 1) / tile_j) / 4 + size_j) * steps * kStep * 2 / kMemoryRate;
         const uint64_t most = pair == 2 ? 1 : std::max<uint64_t>(1, std::min<uint64_t>({kMaxSplits, slots / c.tiles, steps / 2}));
         for (c.splits = 1; c.splits <= most; ++c.splits) {
             const uint64_t waves = (c.tiles * c.splits + slots - 1) / slots;
