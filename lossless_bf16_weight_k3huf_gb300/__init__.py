@@ -444,7 +444,7 @@ def _dtypes():
     if _types is None:
         import torch
         _types = ({torch.bfloat16: _BF16, torch.float32: _F32}, {torch.int32: 4, torch.int64: 8}, torch.float32, torch.int32,
-                  torch.bfloat16)
+                  torch.bfloat16, torch.int64)
 
     return _types
 
@@ -533,7 +533,7 @@ def adapter_scratch_bytes(n_tokens: int, n_adapters: int, rank: int, cols: int, 
 def _adapters(a, b, scales) -> Adapters:
     n, rank, cols = a.shape
     rows = b.shape[2]
-    _, _, f32, _, bf16 = _dtypes()
+    _, _, f32, _, bf16, _ = _dtypes()
     return Adapters(_dense(a, (n, rank, cols), "a", bf16), _dense(b, (n, rank, rows), "b", bf16), _dense(scales, (n,), "scales", f32),
                     n, rank, cols, rows)
 
@@ -560,7 +560,7 @@ def adapter_grad(x, a, b, ids, scales, dy, da, db, scratch, d_status, dx=None, d
     or bf16, None if not wanted) = dx_base + the adapters' part."""
     ad = _adapters(a, b, scales)
     n = ids.numel()
-    _, _, f32, i32, _ = _dtypes()
+    _, _, f32, i32, _, _ = _dtypes()
     ip = _dense(ids, (n,), "ids", i32)
     xp, _, xs = _matrix(x, n, ad.cols, "x", _BF16)
     yp, _, ys = _matrix(dy, n, ad.rows, "dy", _BF16)
@@ -585,7 +585,7 @@ def token_logprobs(logits, tokens, logprob, d_status, entropy=None, lse=None, to
     tp, tb, n = _ids(tokens, "tokens")
     vocab = logits.shape[1]
     xp, xe, xs = _matrix(logits, n, vocab, "logits")
-    _, _, f32, i32, _ = _dtypes()
+    _, _, f32, i32, _, _ = _dtypes()
     if (top_ids is None) != (top_logprobs is None):
         raise ValueError("top_ids and top_logprobs go together")
     top, ti, tl = 0, None, None
@@ -713,9 +713,8 @@ def logits_control(logits, out, d_status, history=None, spans=None, repetition=N
     n, vocab = logits.shape
     xp, xe, xs = _matrix(logits, n, vocab, "logits")
     yp, ye, ys = _matrix(out, n, vocab, "out")
-    _, sizes, f32, i32, _ = _dtypes()
-    i64 = next(t for t, size in sizes.items() if size == 8)
-    c = Control()
+    types = _dtypes()
+    f32, i32, i64 = types[2], types[3], types[5]
     if (history is None) != (spans is None):
         raise ValueError("history and spans go together")
     if history is None and (repetition is not None or frequency is not None or presence is not None):
@@ -724,21 +723,27 @@ def logits_control(logits, out, d_status, history=None, spans=None, repetition=N
         raise ValueError("bias_ids, bias_values and bias_spans go together")
     if mask is None and mask_rows is not None:
         raise ValueError("mask_rows without mask")
+    hp = sp = rp = fp = pp = bp = vp = wp = mp = qp = None
+    hn = hb = bn = bb = mn = ms = 0
     if history is not None:
-        c.history, c.history_id_bytes, c.n_history = _ids(history, "history")
-        c.spans = _dense(spans, (n, 3), "spans", i64)
-        for name, v in (("repetition", repetition), ("frequency", frequency), ("presence", presence)):
-            if v is not None:
-                setattr(c, name, _dense(v, (n,), name, f32))
+        hp, hb, hn = _ids(history, "history")
+        sp = _dense(spans, (n, 3), "spans", i64)
+        if repetition is not None:
+            rp = _dense(repetition, (n,), "repetition", f32)
+        if frequency is not None:
+            fp = _dense(frequency, (n,), "frequency", f32)
+        if presence is not None:
+            pp = _dense(presence, (n,), "presence", f32)
     if bias_ids is not None:
-        c.bias_ids, c.bias_id_bytes, c.n_bias = _ids(bias_ids, "bias_ids")
-        c.bias_values = _dense(bias_values, (c.n_bias,), "bias_values", f32)
-        c.bias_spans = _dense(bias_spans, (n, 2), "bias_spans", i64)
+        bp, bb, bn = _ids(bias_ids, "bias_ids")
+        vp = _dense(bias_values, (bn,), "bias_values", f32)
+        wp = _dense(bias_spans, (n, 2), "bias_spans", i64)
     if mask is not None:
-        c.n_masks, c.mask_stride = mask.shape
-        c.mask = _dense(mask, mask.shape, "mask", i32)
+        mn, ms = mask.shape
+        mp = _dense(mask, (mn, ms), "mask", i32)
         if mask_rows is not None:
-            c.mask_rows = _dense(mask_rows, (n,), "mask_rows", i32)
+            qp = _dense(mask_rows, (n,), "mask_rows", i32)
+    c = Control(hp, sp, hn, hb, bb, rp, fp, pp, bp, vp, wp, bn, mp, qp, mn, ms)
     _check(_lib().k3huf_logits_control(ctypes.addressof(c), xp, xe, xs, n, vocab, yp, ye, ys, _dptr(d_status),
                                        _stream(stream)), "k3huf_logits_control")
 
@@ -762,7 +767,7 @@ def distill(logits, top_ids, top_logprobs, loss, d_status, lse=None, log_rest=No
     fp32 of n."""
     n, vocab = logits.shape
     xp, xe, xs = _matrix(logits, n, vocab, "logits")
-    _, _, f32, i32, _ = _dtypes()
+    _, _, f32, i32, _, _ = _dtypes()
     top = top_ids.shape[1]
     _check(_lib().k3huf_distill(xp, xe, xs, n, vocab, scale, _dense(top_ids, (n, top), "top_ids", i32),
                                 _dense(top_logprobs, (n, top), "top_logprobs", f32), top, _mode(mode),
@@ -779,7 +784,7 @@ def distill_grad(logits, top_ids, top_logprobs, lse, g_loss, dlogits, d_status, 
     n, vocab = logits.shape
     xp, xe, xs = _matrix(logits, n, vocab, "logits")
     dp, _, ds = _matrix(dlogits, n, vocab, "dlogits", xe)
-    _, _, f32, i32, _ = _dtypes()
+    _, _, f32, i32, _, _ = _dtypes()
     top = top_ids.shape[1]
     _check(_lib().k3huf_distill_grad(xp, xe, xs, n, vocab, scale, _dense(top_ids, (n, top), "top_ids", i32),
                                      _dense(top_logprobs, (n, top), "top_logprobs", f32), top, _mode(mode),

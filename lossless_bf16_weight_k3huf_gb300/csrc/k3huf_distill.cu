@@ -96,6 +96,9 @@ struct Alternatives {
 __device__ __forceinline__ Alternatives alternatives(const Teacher &T, uint64_t row, uint32_t vocab, uint32_t lane, uint32_t *status) {
     Alternatives A;
     const int entries = T.count > 32 ? 2 : 1;
+    float top[2];                             // (fetched beside the ids, not after them)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) top[e] = lane + 32 * e < T.count ? T.top[row * T.count + lane + 32 * e] : 0.f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const uint32_t i = lane + 32 * e;
@@ -104,7 +107,7 @@ __device__ __forceinline__ Alternatives alternatives(const Teacher &T, uint64_t 
             if (status) atomicOr(status, K3HUF_ST_TOKEN);
             A.id[e] = -1;
         }
-        A.t[e] = A.id[e] >= 0 ? double(T.top[row * T.count + i]) : -INFINITY;
+        A.t[e] = A.id[e] >= 0 ? double(top[e]) : -INFINITY;
         A.q[e] = 0.;
     }
     A.any = __any_sync(0xffffffffu, A.id[0] >= 0 || A.id[1] >= 0);

@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kTileJ>::per_sm) product_kerne
             else join<2, 8>(P, mine, ti * kTileI + lane * 4, tj * kTileJ, c0 + warp, c1);
         }
         __syncwarp();
-        cluster_arrive();
+        cluster_arrive_relaxed();             // (nobody reads another CTA's sums any more)
         cluster_wait();
     }
     if (!ok) atomicOr(P.status, K3HUF_ST_TIMEOUT);
@@ -588,7 +588,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1) pair_kern
     if (!ok) atomicOr(P.status, K3HUF_ST_TIMEOUT);
     tc_fence_before();
     __syncthreads();
-    cluster_arrive();
+    cluster_arrive_relaxed();
     cluster_wait();
     tc_fence_after();
     if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kTileJ) : "memory");
@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(kSlopeThreads, kSlopePerSm) slope_kernel(const
     }
     __syncwarp();
     if (splits > 1) {
-        cluster_arrive();
+        cluster_arrive_relaxed();
         cluster_wait();
     }
 }

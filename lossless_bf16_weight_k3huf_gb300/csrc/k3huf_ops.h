@@ -34,6 +34,8 @@ __device__ __forceinline__ int64_t ld_id(const void *ids, uint32_t id_bytes, uin
 
 // The cluster's barrier in its two halves; the stores before the one are seen after the other.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// ... before which nothing is handed over (an exit: a release would wait for every store to memory)
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // --- host -------------------------------------------------------------------
