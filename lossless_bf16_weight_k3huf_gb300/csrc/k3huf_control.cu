@@ -365,7 +365,8 @@ int launch(ControlParams P, uint64_t n, cudaStream_t stream) {
         const int stream_rc = run(std::max(least, std::min(most, sms * 24 / n)), 256, 256, false);
         if (stream_rc || !lists) return stream_rc;
     }
-    return run(least, 256, 0, streams);
+    // (of the lists, as many threads per row as the GPU has for it: 93 rows of 8000 entries 30 us with 256)
+    return run(least, n <= sms ? 1024 : n <= 2 * sms ? 512 : 256, 0, streams);
 }
 
 }  // namespace

@@ -108,23 +108,24 @@ __device__ __forceinline__ void store(const Epilogue &e, uint32_t i, uint32_t j,
     store_to(e.out, e.out_type, e.out_stride, i, j, size_j, v);
 }
 
-// kCount neighbouring columns j of the thread's i: sums to values of the result.
+// The residual's values there.
 template <int kCount>
-__device__ __forceinline__ void apply(const Epilogue &e, uint32_t i, uint32_t j, uint32_t size_j, float (&v)[kCount], float bias) {
-    const bool f32 = e.out_type == K3HUF_F32;
-    float res[kCount];
-    if (e.residual) {
-        const uint64_t at = uint64_t(j) * e.residual_stride + i;
-        if (f32) {
-            const float *r = static_cast<const float *>(e.residual) + at;
+__device__ __forceinline__ void residual_at(const Epilogue &e, uint32_t i, uint32_t j, uint32_t size_j, float (&res)[kCount]) {
+    const uint64_t at = uint64_t(j) * e.residual_stride + i;
+    if (e.out_type == K3HUF_F32) {
+        const float *r = static_cast<const float *>(e.residual) + at;
 #pragma unroll
-            for (int c = 0; c < kCount; ++c, r += e.residual_stride) res[c] = j + c < size_j ? *r : 0.f;
-        } else {
-            const __nv_bfloat16 *r = static_cast<const __nv_bfloat16 *>(e.residual) + at;
+        for (int c = 0; c < kCount; ++c, r += e.residual_stride) res[c] = j + c < size_j ? *r : 0.f;
+    } else {
+        const __nv_bfloat16 *r = static_cast<const __nv_bfloat16 *>(e.residual) + at;
 #pragma unroll
-            for (int c = 0; c < kCount; ++c, r += e.residual_stride) res[c] = j + c < size_j ? ld_f32(r) : 0.f;
-        }
+        for (int c = 0; c < kCount; ++c, r += e.residual_stride) res[c] = j + c < size_j ? ld_f32(r) : 0.f;
     }
+}
+
+// Sums to values of the result.
+template <int kCount>
+__device__ __forceinline__ void apply(const Epilogue &e, uint32_t i, uint32_t j, uint32_t size_j, float (&v)[kCount], float bias, const float (&res)[kCount]) {
     if (e.bias) {
 #pragma unroll
         for (int c = 0; c < kCount; ++c) v[c] += bias;
@@ -161,7 +162,9 @@ __device__ __forceinline__ void finish_four(const Epilogue &e, uint32_t i, uint3
     for (int k = 0; k < 4; ++k) u[k] = e.bias ? v[k] + bias[k] : v[k];
     const uint32_t count = i < size_i ? min(size_i - i, 4u) : 0u;
     if (count == 0) return;
-    apply(at, 0, 0, count, u, 0.f);
+    float res[4];
+    if (e.residual) residual_at(at, 0, 0, count, res);
+    apply(at, 0, 0, count, u, 0.f, res);
     if (count == 4 && e.out_type == K3HUF_F32 && aligned_to_device(at.out, 16)) *static_cast<float4 *>(at.out) = make_float4(u[0], u[1], u[2], u[3]);
     else if (count == 4 && e.out_type == K3HUF_BF16 && aligned_to_device(at.out, 8)) {
         uint2 o;
@@ -187,20 +190,22 @@ __device__ __forceinline__ void add_run(uint32_t from, float (&sum)[kPart], bool
     }
     if (last) asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// ... and from there, 16 columns at a time, to the result; the next columns are on their way from TMEM meanwhile.
+// ... and from there, 16 columns at a time, to the result; the next columns, and their residual, are on
+// their way meanwhile (`res`: the first columns').
 template <uint32_t kPart>
-__device__ __forceinline__ void finish_tile(const Epilogue &e, uint32_t from, uint32_t i, uint32_t size_i, uint32_t j, uint32_t size_j, float bias) {
+__device__ __forceinline__ void finish_tile(const Epilogue &e, uint32_t from, uint32_t i, uint32_t size_i, uint32_t j, uint32_t size_j, float bias, float (&res)[16]) {
     uint32_t next[16];
     tmem_start16(from, next);
 #pragma unroll 1
     for (uint32_t c = 0; c < kPart; c += 16) {
-        float v[16];
+        float v[16], mine[16];
         tmem_wait16(next);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(next[k]);
+        for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(next[k]), mine[k] = res[k];
         if (c + 16 < kPart) tmem_start16(from + c + 16, next);
         if (i < size_i) {
-            apply(e, i, j + c, size_j, v, bias);
+            if (e.residual && c + 16 < kPart) residual_at(e, i, j + c + 16, size_j, res);
+            apply(e, i, j + c, size_j, v, bias, mine);
             store(e, i, j + c, size_j, v);
         }
         __syncwarp();
@@ -361,13 +366,15 @@ __global__ void __launch_bounds__(kThreads, Shape<kTileJ>::per_sm) product_kerne
             const uint32_t i = ti * kTileI + quarter * 32 + lane;
             const float bias = next_bias;
             next_bias = bias_of(t + t_step);  // (on its way while this tile is finished)
+            float res[16];
+            if (P.e.residual && i < P.size_i && reads && P.splits == 1) residual_at(P.e, i, tj * kTileJ + c_first, P.size_j, res);
             for (uint32_t q = 0; q < runs; ++q, ++r) {
                 if (ok) ok = mbar_wait(smem_addr(&s_sum[r & 1]), r / 2 & 1);
                 tc_fence_after();
                 const bool last = q + 1 == runs && P.splits == 1;
                 const uint32_t from = tmem + (quarter << 21) + (r & 1) * kTileJ + c_first;
                 if (reads && (runs > 1 || !last)) add_run<S::part>(from, sum, q == 0, last);
-                if (reads && last) finish_tile<S::part>(P.e, from, i, P.size_i, tj * kTileJ + c_first, P.size_j, bias);
+                if (reads && last) finish_tile<S::part>(P.e, from, i, P.size_i, tj * kTileJ + c_first, P.size_j, bias, res);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&s_read[r & 1]));
@@ -571,13 +578,15 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1) pair_kern
             const uint32_t i = (ti * 2 + rank) * kTileI + quarter * 32 + lane;
             const float bias = next_bias;
             next_bias = bias_of(t + t_step);  // (on its way while this tile is finished)
+            float res[16];
+            if (P.e.residual && i < P.size_i) residual_at(P.e, i, tj * kTileJ + c_first, P.size_j, res);
             float sum[S::part];
             for (uint32_t q = 0; q < runs; ++q, ++r) {
                 if (ok) ok = mbar_wait(smem_addr(&s_sum[r & 1]), r / 2 & 1);
                 tc_fence_after();
                 const uint32_t from = tmem + (quarter << 21) + (r & 1) * kTileJ + c_first;
                 if (runs > 1) add_run<S::part>(from, sum, q == 0, q + 1 == runs);
-                if (q + 1 == runs) finish_tile<S::part>(P.e, from, i, P.size_i, tj * kTileJ + c_first, P.size_j, bias);
+                if (q + 1 == runs) finish_tile<S::part>(P.e, from, i, P.size_i, tj * kTileJ + c_first, P.size_j, bias, res);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_at(in_cta(smem_addr(&s_read[r & 1]), 0));
