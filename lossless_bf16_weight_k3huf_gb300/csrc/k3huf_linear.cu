@@ -212,6 +212,57 @@ __device__ __forceinline__ void finish_tile(const Epilogue &e, uint32_t from, ui
     }
 }
 
+// The same for a warp whose 32 elements of every column lie in the matrix, with a residual whose rows start on 16 bytes: it
+// comes through a buffer in shared memory, kSlots x 16 columns ahead.  (16 columns of loads at a time, in registers, are
+// 8 KB in flight per SM: 3012 x 8192 x 192 with a residual 108 us, and 40 us so.)
+constexpr uint32_t kAheadBytes = 4096;                    // of a warp
+template <typename T> struct Ahead {
+    static constexpr uint32_t slot = 16 * 32 * sizeof(T), slots = kAheadBytes / slot, parts = 32 * sizeof(T) / 16;      // parts: of a column, 16 bytes each
+    // columns j to j + 15, elements i0 to i0 + 31, on their way to the slot
+    __device__ static __forceinline__ void start(const Epilogue &e, uint32_t to, uint32_t i0, uint32_t j, uint32_t size_j, uint32_t lane) {
+        const T *r = static_cast<const T *>(e.residual);
+#pragma unroll
+        for (uint32_t q = 0; q < slot / 512; ++q) {
+            const uint32_t p = lane + 32 * q, col = p / parts, off = p % parts * (16 / sizeof(T));
+            const bool in = j + col < size_j;
+            cp_async16z(to + p * 16, in ? r + uint64_t(j + col) * e.residual_stride + i0 + off : r, in ? 16 : 0);
+        }
+    }
+    // ... the first of a tile's
+    template <uint32_t kPart> __device__ static __forceinline__ void start_tile(const Epilogue &e, uint32_t buffer, uint32_t i0, uint32_t j, uint32_t size_j, uint32_t lane) {
+#pragma unroll
+        for (uint32_t q = 0; q < slots; ++q) {
+            if (q * 16 < kPart) start(e, buffer + q * slot, i0, j + q * 16, size_j, lane);
+            cp_async_commit();
+        }
+    }
+    template <uint32_t kPart>
+    __device__ static __forceinline__ void finish(const Epilogue &e, uint8_t *buffer, uint32_t from, uint32_t i0, uint32_t lane, uint32_t j, uint32_t size_j, float bias) {
+        uint32_t next[16];
+        tmem_start16(from, next);
+#pragma unroll 1
+        for (uint32_t c = 0; c < kPart; c += 16) {
+            float v[16], res[16];
+            const uint32_t at = c / 16 % slots * slot;
+            cp_async_wait<slots - 1>();
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) res[k] = ld_f32(reinterpret_cast<const T *>(buffer + at) + k * 32 + lane);
+            __syncwarp();
+            if (c + 16 * slots < kPart) start(e, smem_addr(buffer + at), i0, j + c + 16 * slots, size_j, lane);
+            cp_async_commit();
+            tmem_wait16(next);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(next[k]);
+            if (c + 16 < kPart) tmem_start16(from + c + 16, next);
+            apply(e, i0 + lane, j + c, size_j, v, bias, res);
+            store(e, i0 + lane, j + c, size_j, v);
+        }
+        cp_async_wait<0>();
+        __syncwarp();
+    }
+};
+
 // Order of the tiles: kGroup rows of tiles at a time, so that the CTAs at work at once share operands.
 constexpr uint32_t kGroup = 16;
 __device__ __forceinline__ void tile_place(const ProductParams &P, uint32_t t, uint32_t &ti, uint32_t &tj) {
@@ -422,8 +473,8 @@ template <uint32_t kTileJ> struct Pair {
     static constexpr uint32_t a_bytes = kTileI * 128, b_bytes = kTileJ / 2 * 128, stage = a_bytes + b_bytes;
     static constexpr uint32_t stages = kTileJ == 256 ? 6 : 8;
     static constexpr uint32_t part = kTileJ / 2;
-    static constexpr size_t smem = stages * stage + 1024;
-    static_assert(smem <= 220 * 1024, "shared memory of an SM");
+    static constexpr size_t smem = stages * stage + 1024, ahead = kEpilogue / 32 * kAheadBytes;
+    static_assert(smem + ahead <= 226 * 1024, "shared memory of a CTA");
 };
 
 __device__ __forceinline__ uint32_t in_cta(uint32_t at, uint32_t rank) {
@@ -457,7 +508,9 @@ __device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity) {
     return false;
 }
 
-template <uint32_t kTileJ, bool kMnA, bool kMnB>
+// (kAhead: a residual whose rows start on 16 bytes; an instantiation of its own, whose code would slow the others' epilogue,
+// 8192 x 8192 x 576 from 69 to 83 us)
+template <uint32_t kTileJ, bool kMnA, bool kMnB, bool kAhead>
 __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1) pair_kernel(const __grid_constant__ ProductParams P) {
     using S = Pair<kTileJ>;
     constexpr uint32_t NS = S::stages;
@@ -579,14 +632,27 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kPairThreads, 1) pair_kern
             const float bias = next_bias;
             next_bias = bias_of(t + t_step);  // (on its way while this tile is finished)
             float res[16];
-            if (P.e.residual && i < P.size_i) residual_at(P.e, i, tj * kTileJ + c_first, P.size_j, res);
+            const bool f32 = P.e.out_type == K3HUF_F32, ahead = kAhead && i - lane + 32 <= P.size_i;
+            uint8_t *buffer = smem + NS * S::stage + warp * kAheadBytes;
+            if (!ahead && P.e.residual && i < P.size_i) residual_at(P.e, i, tj * kTileJ + c_first, P.size_j, res);
+            if constexpr (kAhead) {
+                if (ahead && f32) Ahead<float>::template start_tile<S::part>(P.e, smem_addr(buffer), i - lane, tj * kTileJ + c_first, P.size_j, lane);
+                if (ahead && !f32) Ahead<__nv_bfloat16>::template start_tile<S::part>(P.e, smem_addr(buffer), i - lane, tj * kTileJ + c_first, P.size_j, lane);
+            }
             float sum[S::part];
             for (uint32_t q = 0; q < runs; ++q, ++r) {
                 if (ok) ok = mbar_wait(smem_addr(&s_sum[r & 1]), r / 2 & 1);
                 tc_fence_after();
                 const uint32_t from = tmem + (quarter << 21) + (r & 1) * kTileJ + c_first;
                 if (runs > 1) add_run<S::part>(from, sum, q == 0, q + 1 == runs);
-                if (q + 1 == runs) finish_tile<S::part>(P.e, from, i, P.size_i, tj * kTileJ + c_first, P.size_j, bias, res);
+                if (q + 1 == runs) {
+                    const uint32_t j = tj * kTileJ + c_first;
+                    if constexpr (kAhead) {
+                        if (ahead && f32) Ahead<float>::template finish<S::part>(P.e, buffer, from, i - lane, lane, j, P.size_j, bias);
+                        else if (ahead) Ahead<__nv_bfloat16>::template finish<S::part>(P.e, buffer, from, i - lane, lane, j, P.size_j, bias);
+                    }
+                    if (!ahead) finish_tile<S::part>(P.e, from, i, P.size_i, j, P.size_j, bias, res);
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_at(in_cta(smem_addr(&s_read[r & 1]), 0));
@@ -853,10 +919,10 @@ int launch_one(const Cut &cut, ProductParams &P, uint64_t sms, cudaStream_t stre
     static std::atomic<uint64_t> once{0};
     return launch_product(product_kernel<kTileJ, kMnA, kMnB>, once, kThreads, Shape<kTileJ>::smem, sms * Shape<kTileJ>::per_sm, cut, P, stream);
 }
-template <uint32_t kTileJ, bool kMnA, bool kMnB>
+template <uint32_t kTileJ, bool kMnA, bool kMnB, bool kAhead>
 int launch_pair(const Cut &cut, ProductParams &P, uint64_t sms, cudaStream_t stream) {
     static std::atomic<uint64_t> once{0};
-    return launch_product(pair_kernel<kTileJ, kMnA, kMnB>, once, kPairThreads, Pair<kTileJ>::smem, sms / 2, cut, P, stream);
+    return launch_product(pair_kernel<kTileJ, kMnA, kMnB, kAhead>, once, kPairThreads, Pair<kTileJ>::smem + (kAhead ? Pair<kTileJ>::ahead : 0), sms / 2, cut, P, stream);
 }
 
 // out[j][i] = sum_k A[i][k] B[j][k]
@@ -866,13 +932,18 @@ int product(const Operand &a, const Operand &b, uint64_t size_i, uint64_t size_j
     P.e = e;
     P.status = status;
     P.size_i = uint32_t(size_i), P.size_j = uint32_t(size_j), P.steps = uint32_t((size_k + kStep - 1) / kStep);
+    const uint32_t width = uint32_t(elem_bytes(e.out_type));
+    const bool ahead = e.residual && aligned_to(e.residual, 16) && e.residual_stride * width % 16 == 0;
     const bool f32 = e.out_type == K3HUF_F32 || (e.z && e.z_type == K3HUF_F32);
     P.run = f32 ? kChain / (kStep / 16) : std::min(P.steps, kLongRun);
     const Cut cut = choose<kMnB>(size_i, size_j, P.steps, sms);
     int rc = tensor_map(&P.a, a.p, K3HUF_BF16, a.rows, a.cols, a.stride, kMnA ? kStep : kTileI, kStep, true);
     if (!rc) rc = tensor_map(&P.b, b.p, K3HUF_BF16, b.rows, b.cols, b.stride, kMnB ? kStep : cut.tile_j / cut.pair, kStep, true);
     if (rc) return rc;
-    if (cut.pair == 2) return cut.tile_j == 256 ? launch_pair<256, kMnA, kMnB>(cut, P, sms, stream) : launch_pair<128, kMnA, kMnB>(cut, P, sms, stream);
+    if constexpr (kMnA == kMnB) {             // (dx has no residual)
+        if (cut.pair == 2 && ahead) return cut.tile_j == 256 ? launch_pair<256, kMnA, kMnB, true>(cut, P, sms, stream) : launch_pair<128, kMnA, kMnB, true>(cut, P, sms, stream);
+    }
+    if (cut.pair == 2) return cut.tile_j == 256 ? launch_pair<256, kMnA, kMnB, false>(cut, P, sms, stream) : launch_pair<128, kMnA, kMnB, false>(cut, P, sms, stream);
     if constexpr (!kMnB) {
         if (cut.tile_j == 16) return launch_one<16, kMnA, kMnB>(cut, P, sms, stream);
         if (cut.tile_j == 32) return launch_one<32, kMnA, kMnB>(cut, P, sms, stream);
