@@ -8,7 +8,7 @@
 //   dx_j = s g (Q p_j - q_j) for an alternative,   s g (Q - q_r / p_r) p_j for another token.
 //
 // A loss is what is left of terms far larger than itself, so what there are few of (the alternatives' terms, the
-// rest's mass, the logarithms) is computed in 64 bits; the sum over the vocabulary in 32.  p_r is summed over the
+// rest's mass, the logarithms) is computed in 64 bits or pairs of floats; the sum over the vocabulary in 32.  p_r is summed over the
 // other tokens alone, never taken as a difference: a small rest keeps its digits.
 //
 // Forward, one read of the logits: a CTA streams a row, or the CTAs of a cluster when there are fewer rows than the
@@ -45,12 +45,80 @@ __device__ __forceinline__ void rescale(Sum &s, float m, float c) {
     s.sum *= exp2_fast(max_nan((s.m - m) * c, kFloor));
     s.m = m;
 }
-// A warp's sums as one, its largest value and a 64-bit sum: every lane's is brought to that value once, by an exponent
+// 64-bit arithmetic runs at a sixtieth of the 32-bit rate here: 4992 rows of 1744 logits took 52 us with it throughout, 5 of
+// them for their bytes.  So exponentials, logarithms and sums are taken in pairs of floats, a value and what its rounding left
+// (Dekker's double-length numbers): 45 bits and more.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {               // a + b, without loss
+    const float s = a + b, other = s - a;
+    return {s, (a - (s - other)) + (b - other)};
+}
+__device__ __forceinline__ Two two_fast(float a, float b) {              // ... of |a| >= |b|
+    const float s = a + b;
+    return {s, b - (s - a)};
+}
+__device__ __forceinline__ Two two_mul(Two a, Two b) {
+    const float p = __fmul_rn(a.hi, b.hi);
+    return {p, fmaf(a.hi, b.hi, -p) + fmaf(a.hi, b.lo, a.lo * b.hi)};
+}
+__device__ __forceinline__ double wide(Two a) { return double(a.hi) + double(a.lo); }
+__device__ __forceinline__ Two narrow(double a) {                         // (an infinity's rest would be NaN)
+    const float hi = float(a);
+    return {hi, isfinite(hi) ? float(a - double(hi)) : 0.f};
+}
+
+// e^a for |a| <= 80: a = n ln 2 + 16 u with ln 2 in three parts, whose first two give exact products with n (Cody and Waite's
+// reduction); w = e^u - 1 by its series, whose terms from the third on need but 32 bits (|u| < 0.022: 2e-13 of 1); then four
+// times e^2u - 1 = 2 w + w^2.  In all 4e-12 of the result at most.
+constexpr float kExpMost = 80.f;
+__device__ __forceinline__ Two two_exp(Two a) {
+    constexpr double ln2 = 0.693147180559945309417;
+    constexpr float l1 = float(int(ln2 * 131072)) / 131072.f, l2 = float(int((ln2 - l1) * 17179869184.)) / 17179869184.f, l3 = float(ln2 - l1 - l2);
+    const float n = rintf(a.hi * kLog2e);
+    Two u = two_sum(fmaf(-n, l1, a.hi), -n * l2);
+    u = two_sum(u.hi, u.lo + fmaf(-n, l3, a.lo));
+    const float h = u.hi * 0.0625f, l = u.lo * 0.0625f;
+    const float square = __fmul_rn(h, h), left = fmaf(h, h, -square);
+    const float tail = square * h * fmaf(h, fmaf(h, fmaf(h, 1.f / 720, 1.f / 120), 1.f / 24), 1.f / 6);
+    Two w = two_fast(h, 0.5f * square);
+    w = two_fast(w.hi, w.lo + (tail + (l + fmaf(h, l, 0.5f * left))));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float p = __fmul_rn(w.hi, w.hi), e = fmaf(w.hi, w.hi, -p);
+        const Two s = two_fast(2.f * w.hi, p);
+        w = two_fast(s.hi, s.lo + fmaf(2.f, w.lo, fmaf(2.f * w.hi, w.lo, e)));
+    }
+    const Two one = two_fast(1.f, w.hi);
+    const float power = __int_as_float((int(n) + 127) << 23);
+    return {one.hi * power, (one.lo + w.lo) * power};
+}
+// log v, by a whole warp: y = logf(v) and, as v e^-y is 1 but for 2e-6 at most, what that is off (its square's half beside it)
+__device__ __forceinline__ double log_of(double v) {
+    const float f = float(v);
+    if (__any_sync(0xffffffffu, !(f >= 1e-30f && f <= 1e30f))) return log(v);
+    const float y = logf(f);
+    const double d = fma(v, wide(two_exp({-y, 0.f})), -1.);
+    const float low = float(d);
+    return double(y) + (d - double(0.5f * low * low));
+}
+__device__ __forceinline__ Two warp_sum(Two v) {                          // (of finite values)
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        const float b = __shfl_xor_sync(0xffffffffu, v.hi, d);
+        const Two s = two_sum(v.hi, b);
+        v = {s.hi, v.lo + __shfl_xor_sync(0xffffffffu, v.lo, d) + s.lo};
+    }
+    return v;
+}
+
+// A warp's sums as one, its largest value and the sum: every lane's is brought to that value once, by an exponent
 // whose rounding is made good, and they are added up without loss (each addition's rounding error in a sum of its own).
 // Sums joined pair by pair, 32 bits each, were 5e-8 off: as much as a loss between near distributions shows.
 struct Part {
     float m;
-    double sum;
+    Two sum;
 };
 __device__ __forceinline__ Part warp_part(Sum s, float c) {
     float m = s.m;
@@ -58,14 +126,7 @@ __device__ __forceinline__ Part warp_part(Sum s, float c) {
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     // (far below the largest there is nothing to make good, and infinities of the difference would give NaN)
     const float d = s.m - m, t = max_nan(d * c, kFloor), low = t > kFloor ? fmaf(d, c, -t) : 0.f;
-    float hi = s.sum * exp2_fast(t) * fmaf(low, kLn2, 1.f), lo = 0.f;
-#pragma unroll
-    for (int k = 16; k; k >>= 1) {
-        const float b = __shfl_xor_sync(0xffffffffu, hi, k), sum = hi + b, other = sum - hi;
-        lo += __shfl_xor_sync(0xffffffffu, lo, k) + ((hi - (sum - other)) + (b - other));
-        hi = sum;
-    }
-    return {m, double(hi) + double(lo)};
+    return {m, warp_sum(Two{s.sum * exp2_fast(t) * fmaf(low, kLn2, 1.f), 0.f})};
 }
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -73,10 +134,17 @@ __device__ __forceinline__ double warp_sum(double v) {
     for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
 }
-// exp of a 64-bit number to 32 bits (the rounding of the argument alone would cost |a| 2^-24 of the result).
-__device__ __forceinline__ float exp_of(double a) {
-    const float hi = float(a), lo = isfinite(hi) ? float(a - double(hi)) : 0.f, e = expf(hi);
-    return fmaf(e, lo, e);
+// (x - m) scale
+__device__ __forceinline__ Two below(float x, float m, Two scale) {
+    const Two a = two_mul(two_sum(0.5f * x, -0.5f * m), scale);           // (halves: a difference of 6e38 has its place too)
+    return {2.f * a.hi, 2.f * a.lo};
+}
+// e^a for a <= 0; nothing below e^-80, which no sum with a term of 1 shows
+__device__ __forceinline__ Two weight(Two a) { return a.hi < -kExpMost ? Two{0.f, 0.f} : two_exp(a); }
+// ... to 32 bits, for what is 1 for the largest part (the rounding of a alone would cost |a| 2^-24 of it)
+__device__ __forceinline__ float weight32(Two a) {
+    const float e = a.hi < -kExpMost ? 0.f : expf(a.hi);
+    return e == 0.f ? 0.f : fmaf(e, a.lo, e);
 }
 
 struct Teacher {
@@ -85,17 +153,19 @@ struct Teacher {
     uint32_t count, mode;                     // alternatives per row
 };
 
-// A row's alternatives, by one warp: entry `lane`, and, of more than 32, entry lane + 32 (id -1: none, q 0).  64-bit
-// arithmetic runs at a sixtieth of the 32-bit rate, so nothing is computed twice or for a second entry that is not there.
+// A row's alternatives, by one warp: entry `lane`, and, of more than 32, entry lane + 32 (id -1: none, q 0).  Nothing is
+// computed for a second entry that is not there.
 struct Alternatives {
     int32_t id[2];
-    double t[2], q[2];                        // log q (-infinity for none), q
+    double t[2], q[2];                        // log q + log `whole` (-infinity for none), q
     double mass, rest;                        // sum of q; what is left of 1, where that is wanted
+    double whole;                             // what the q were divided by
     bool any;
 };
 __device__ __forceinline__ Alternatives alternatives(const Teacher &T, uint64_t row, uint32_t vocab, uint32_t lane, uint32_t *status) {
     Alternatives A;
     const int entries = T.count > 32 ? 2 : 1;
+    A.whole = 1.;
     float top[2];                             // (fetched beside the ids, not after them)
 #pragma unroll
     for (int e = 0; e < 2; ++e) top[e] = lane + 32 * e < T.count ? T.top[row * T.count + lane + 32 * e] : 0.f;
@@ -107,30 +177,47 @@ __device__ __forceinline__ Alternatives alternatives(const Teacher &T, uint64_t 
             if (status) atomicOr(status, K3HUF_ST_TOKEN);
             A.id[e] = -1;
         }
-        A.t[e] = A.id[e] >= 0 ? double(top[e]) : -INFINITY;
-        A.q[e] = 0.;
+        if (A.id[e] < 0) top[e] = -INFINITY;
     }
     A.any = __any_sync(0xffffffffu, A.id[0] >= 0 || A.id[1] >= 0);
-    double m = 0.;
+    float m = 0.f;
     if (T.mode == K3HUF_DISTILL_NORMALISED) {
-        // (the largest, of floats; where it is -infinity every q is 0; NaN, and +infinity, make the row NaN)
-        float most = fmaxf(float(A.t[0]), float(A.t[1]));
+        // (the largest; where it is -infinity every q is 0; NaN, and +infinity, make the row NaN)
+        float most = fmaxf(top[0], top[1]);
 #pragma unroll
         for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-        m = most == -INFINITY ? 0. : double(most);
+        m = most == -INFINITY ? 0.f : most;
     }
-    double mass = 0;
+    auto within = [&](float t) { return t == -INFINITY || fabsf(t - m) <= kExpMost; };
+    if (__all_sync(0xffffffffu, within(top[0]) && within(top[1]))) {
+        Two mass{0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        if (e >= entries) break;
-        A.q[e] = A.t[e] == -INFINITY ? 0. : exp(A.t[e] - m);
-        mass += A.q[e];
+        for (int e = 0; e < 2; ++e) {
+            A.t[e] = -INFINITY, A.q[e] = 0.;
+            if (e >= entries) break;
+            if (top[e] == -INFINITY) continue;
+            const Two t = two_sum(top[e], -m), q = two_exp(t), sum = two_sum(mass.hi, q.hi);
+            A.t[e] = wide(t), A.q[e] = wide(q);
+            mass = {sum.hi, sum.lo + mass.lo + q.lo};
+        }
+        A.mass = wide(warp_sum(mass));
+    } else {
+        double mass = 0.;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            A.t[e] = double(top[e]) - double(m);
+            A.q[e] = top[e] == -INFINITY ? 0. : exp(A.t[e]);
+            mass += A.q[e];
+        }
+        A.mass = warp_sum(mass);
     }
-    A.mass = warp_sum(mass);
     if (T.mode == K3HUF_DISTILL_NORMALISED && !(A.mass == 0.)) {
-        const double lse = m + log(A.mass), one = 1. / A.mass;
+        // (the largest q is 1, and of 64 none is larger: a reciprocal, once refined, has 45 bits)
+        const double first = 1.f / float(A.mass), one = fma(first, fma(-A.mass, first, 1.), first);
+        A.whole = A.mass;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) A.t[e] -= lse, A.q[e] *= one;
+        for (int e = 0; e < 2; ++e)
+            if (e < entries) A.q[e] *= one;
         A.mass = A.mass == A.mass ? 1. : A.mass;
     }
     A.rest = T.mode != K3HUF_DISTILL_REST ? 0. : A.mass > 1. ? 0. : 1. - A.mass;
@@ -146,13 +233,14 @@ struct DistillParams {
     uint32_t vocab;
     float c;                                  // scale log2 e, finite for every scale
     double scale;                             // c ln 2: what the sum is taken with, so that c's rounding meets both sides of a loss
+    Two scale2;                               // ... in floats
 };
 
 // What the alternatives give to the loss, by the warp that does not stream, while the others do.
 struct Terms {
-    double sum, mass, rest;                   // sum of q (t - s (x - from)); of q; the rest's q
-    double from, top_sum;                     // the largest of their logits if it is finite, else 0; sum of exp(s (x - top)), each token once
-    float top;                                // the largest of their logits
+    double sum, mass, rest, whole;            // sum of q (t + log whole - s (x - from)); of q; the rest's q
+    float from, top;                          // the largest of their logits, and, where it is not finite, 0
+    Two top_sum;                              // sum of exp(s (x - top)), each token once
     uint32_t any;
 };
 template <typename T, bool kRest>
@@ -165,12 +253,12 @@ __device__ Terms terms(const DistillParams &P, const T *x, uint64_t row, uint32_
 #pragma unroll
     for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     // (logits of 1e38 would leave nothing of t beside them)
-    Terms R{0., A.mass, A.rest, isfinite(top) ? double(top) : 0., 0., top, A.any};
+    Terms R{0., A.mass, A.rest, A.whole, isfinite(top) ? top : 0.f, top, {0.f, 0.f}, A.any};
     const int entries = P.teacher.count > 32 ? 2 : 1;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         if (e >= entries) break;
-        if (A.id[e] >= 0 && !(A.q[e] == 0.)) R.sum += A.q[e] * (A.t[e] - (double(f[e]) - R.from) * P.scale);
+        if (A.id[e] >= 0 && !(A.q[e] == 0.)) R.sum += A.q[e] * (A.t[e] - (double(f[e]) - double(R.from)) * P.scale);
     }
     R.sum = warp_sum(R.sum);
     if constexpr (kRest) {
@@ -184,7 +272,9 @@ __device__ Terms terms(const DistillParams &P, const T *x, uint64_t row, uint32_
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             if (e >= entries) break;
-            if (first[e] && f[e] != -INFINITY) R.top_sum += exp((double(f[e]) - double(top)) * P.scale);
+            if (!first[e] || f[e] == -INFINITY) continue;
+            const Two p = weight(below(f[e], top, P.scale2)), sum = two_sum(R.top_sum.hi, p.hi);
+            R.top_sum = {sum.hi, sum.lo + R.top_sum.lo + p.lo};
         }
         R.top_sum = warp_sum(R.top_sum);
     }
@@ -334,13 +424,13 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == 256 ? 4 : kRest ? 6
     float m;
     double rest, total;
     auto add = [&](const Part *parts, uint32_t count, bool tops) {
-        Part p{-3.402823466e38f, 0.};
+        Part p{-3.402823466e38f, {0.f, 0.f}};
         if (uint32_t(lane) < count) p = parts[lane];
         else if (tops && uint32_t(lane) == count) p = {s_terms.top, s_terms.top_sum};
         m = p.m;
 #pragma unroll
         for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const double v = p.sum == 0. ? 0. : p.sum * exp_of((double(p.m) - double(m)) * P.scale);
+        const double v = p.sum.hi == 0.f ? 0. : wide(two_mul(p.sum, {weight32(below(p.m, m, P.scale2)), 0.f}));
         rest = warp_sum(uint32_t(lane) < count ? v : 0.);
         total = tops ? rest + __shfl_sync(0xffffffffu, v, int(count)) : rest;
     };
@@ -349,20 +439,21 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == 256 ? 4 : kRest ? 6
     } else {
         add(s_part, kParts, false);
         cluster_wait();
-        if (tid == 0) cluster.map_shared_rank(s_all, 0)[rank] = Part{m, rest};
+        if (tid == 0) cluster.map_shared_rank(s_all, 0)[rank] = Part{m, narrow(rest)};
         cluster_arrive();
         cluster_wait();
         if (rank > 0 || warp > 0) return;
         add(s_all, C, kRest);
     }
     const Terms R = s_terms;
-    const double logs = log(lane == 0 ? total : lane == 1 ? rest : R.rest);       // (a lane each)
-    const double log_total = __shfl_sync(0xffffffffu, logs, 0), log_q = __shfl_sync(0xffffffffu, logs, 2);
+    // (a lane each; of what is 0, or not there, no logarithm is used)
+    const double of = lane == 0 ? total : lane == 1 && kRest ? rest : lane == 2 ? R.rest : lane == 3 ? R.whole : 1., logs = log_of(of == 0. ? 1. : of);
+    const double log_total = __shfl_sync(0xffffffffu, logs, 0), log_q = __shfl_sync(0xffffffffu, logs, 2), log_whole = __shfl_sync(0xffffffffu, logs, 3);
     const double log_sum = __shfl_sync(0xffffffffu, logs, 1), log_rest = rest == 0. ? -INFINITY : log_sum - log_total;
     if (lane) return;
     const double lse = total == 0. ? -INFINITY : double(m) * P.scale + log_total;
     // (a row of -infinity alone: every log p is -infinity)
-    double loss = total != 0. ? R.sum + R.mass * ((double(m) - R.from) * P.scale + log_total) : R.mass == 0. ? 0. : R.mass * INFINITY;
+    double loss = total != 0. ? R.sum + R.mass * ((double(m) - double(R.from)) * P.scale + log_total - log_whole) : R.mass == 0. ? 0. : R.mass * INFINITY;
     if constexpr (kRest) {
         if (P.log_rest) P.log_rest[row] = float(log_rest);
         if (R.rest > 0.) loss += R.rest * (log_q - log_rest);
@@ -626,7 +717,8 @@ extern "C" int k3huf_distill(const void *d_logits, uint32_t type, uint64_t strid
     if (n == 0) return K3HUF_OK;
     if (!d_logits || !d_top_ids || !d_top_logprobs || !d_loss) return K3HUF_E_ARG;
     const float c = float(fmin(double(scale) * 1.4426950408889634074, 3.402823466e38));
-    const DistillParams P{d_logits, {d_top_ids, d_top_logprobs, top, mode}, d_loss, d_lse, d_log_rest, d_status, stride, vocab, c, double(c) * 0.69314718055994530942};
+    const double scale_of = double(c) * 0.69314718055994530942;
+    const DistillParams P{d_logits, {d_top_ids, d_top_logprobs, top, mode}, d_loss, d_lse, d_log_rest, d_status, stride, vocab, c, scale_of, {float(scale_of), float(scale_of - double(float(scale_of)))}};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool rest = mode == K3HUF_DISTILL_REST;
     if (type == K3HUF_BF16) return rest ? launch_forward<__nv_bfloat16, true>(P, uint32_t(n), st) : launch_forward<__nv_bfloat16, false>(P, uint32_t(n), st);
