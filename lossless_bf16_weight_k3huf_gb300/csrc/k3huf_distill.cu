@@ -147,6 +147,27 @@ __device__ __forceinline__ float weight32(Two a) {
     return e == 0.f ? 0.f : fmaf(e, a.lo, e);
 }
 
+// Of a warp's list (entry `lane`, and lane + 32 where it has more than 32; below 0: none) the entries that are like another
+// one, a bit each.  There are few, and what depends on an entry's likes looks at those alone.
+__device__ __forceinline__ uint64_t alike(int32_t a, int32_t b, bool more, uint32_t lane) {
+    bool a_like = false, b_like = false;
+#pragma unroll
+    for (uint32_t k = 0; k < 32; ++k) {
+        const int32_t one = __shfl_sync(0xffffffffu, a, k);
+        a_like |= one == a && k != lane;
+        b_like |= one == b;
+    }
+    if (more) {
+#pragma unroll
+        for (uint32_t k = 0; k < 32; ++k) {
+            const int32_t one = __shfl_sync(0xffffffffu, b, k);
+            a_like |= one == a;
+            b_like |= one == b && k != lane;
+        }
+    }
+    return __ballot_sync(0xffffffffu, a_like && a >= 0) | uint64_t(__ballot_sync(0xffffffffu, b_like && b >= 0)) << 32;
+}
+
 struct Teacher {
     const int32_t *ids;
     const float *top;
@@ -264,7 +285,8 @@ __device__ Terms terms(const DistillParams &P, const T *x, uint64_t row, uint32_
     if constexpr (kRest) {
         // (a token that is listed twice counts at its first place)
         bool first[2] = {A.id[0] >= 0, A.id[1] >= 0};
-        for (uint32_t k = 0; k + 1 < P.teacher.count; ++k) {
+        for (uint64_t left = alike(A.id[0], A.id[1], entries > 1, lane); left; left &= left - 1) {
+            const uint32_t k = __ffsll(left) - 1;
             const int32_t id = __shfl_sync(0xffffffffu, k < 32 ? A.id[0] : A.id[1], k % 32);
             if (k < lane && id == A.id[0]) first[0] = false;
             if (k < lane + 32 && id == A.id[1]) first[1] = false;
@@ -316,18 +338,20 @@ template <typename T> __device__ __forceinline__ uint4 nothing() {       // a ve
 template <typename T, int kThreads>
 __device__ __noinline__ Sum passed_over(const T *x, uint32_t shift, uint32_t vocab, uint32_t vecs, uint32_t step0, uint32_t step1, const uint2 *places, uint32_t count, float c) {
     Sum s{-3.402823466e38f, 0.f};
-    const uint32_t turns = (vecs + kThreads * 64 - 1) / (kThreads * 64);          // vectors per bit
-    for (uint32_t e = threadIdx.x % 32; e < count * turns; e += 32) {
+    const uint32_t turns = (vecs + kThreads * 64 - 1) / (kThreads * 64), lane = threadIdx.x % 32;                 // vectors per bit
+    auto bit_of = [&](uint32_t k) { return k >= count || places[k].x == 0xFFFFFFFFu ? -1 : int32_t(places[k].x % (kThreads * 64)); };
+    const uint64_t sharing = alike(bit_of(lane), bit_of(lane + 32), count > 32, lane);
+    for (uint32_t e = lane; e < count * turns; e += 32) {
         const uint32_t k = e % count, of = places[k].x, home = of % (kThreads * 64), at = home + e / count * (kThreads * 64);
         if (of == 0xFFFFFFFFu || at >= vecs || at / (kThreads * kVecs) < step0 || at / (kThreads * kVecs) >= step1) continue;
         uint4 one[1] = {load_vec(x, shift, vocab, at)};
         // (its bit is another's, earlier in the list: that one's thread adds it)
-        uint32_t out = 0;
+        uint32_t out = of == at ? 1u << places[k].y : 0u;
         bool mine = true;
-#pragma unroll 4
-        for (uint32_t q = 0; q < count; ++q) {
+        for (uint64_t left = sharing; left; left &= left - 1) {
+            const uint32_t q = __ffsll(left) - 1;
             const uint2 p = places[q];
-            mine = mine && !(q < k && p.x != 0xFFFFFFFFu && p.x % (kThreads * 64) == home);
+            mine = mine && !(q < k && p.x % (kThreads * 64) == home);
             out |= p.x == at ? 1u << p.y : 0u;
         }
         if (!mine) continue;
@@ -525,9 +549,9 @@ __global__ void __launch_bounds__(kAll, kGradPerSm) distill_grad_kernel(const Gr
 #pragma unroll
             for (int e = 0; e < 2; ++e) mine[e] = A.id[e] >= 0 && A.id[e] >= j0 && A.id[e] < j1;
             // a token that is listed more than once: its first place takes all of its q, in their order
-            for (uint32_t k = 0; k < P.teacher.count; ++k) {
+            for (uint64_t left = alike(A.id[0], A.id[1], P.teacher.count > 32, lane); left; left &= left - 1) {
+                const uint32_t k = __ffsll(left) - 1;
                 const int32_t id = __shfl_sync(0xffffffffu, k < 32 ? A.id[0] : A.id[1], k % 32);
-                if (!__any_sync(0xffffffffu, (id == A.id[0] && k != lane) || (id == A.id[1] && k != lane + 32))) continue;
                 const double other = __shfl_sync(0xffffffffu, k < 32 ? A.q[0] : A.q[1], k % 32);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
