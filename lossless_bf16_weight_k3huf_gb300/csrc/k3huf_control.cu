@@ -26,7 +26,7 @@ constexpr uint32_t kMaxThreads = 1024;
 constexpr uint32_t kUnit = 8;                             // values handled at once
 template <typename T> constexpr int kUnits = 8 / int(sizeof(T));         // units in flight per thread
 constexpr uint32_t kPart = 1u << 17;                      // values per CTA at most
-constexpr uint32_t kPlaces = 2048;                        // touched tokens that are looked after at once
+constexpr uint32_t kPlaces = 2048, kMostPlaces = 12288;   // touched tokens that are looked after at once, by default and at most
 constexpr uint32_t kSeen = 1u << 31;
 
 struct ControlParams {
@@ -36,6 +36,7 @@ struct ControlParams {
     uint32_t *status;
     uint64_t x_stride, y_stride, row0;
     uint32_t vocab, parts, part, streaming;   // CTAs per row; values of each; threads that stream (the others see to the lists)
+    uint32_t places;                          // touched tokens that a CTA looks after at once
     bool after;                               // the stream is the launch before this one
 };
 
@@ -86,7 +87,8 @@ template <typename T, typename U>
 __global__ void __launch_bounds__(kMaxThreads) control_kernel(const __grid_constant__ ControlParams P) {
     extern __shared__ uint32_t s_touched[];   // a bit per token of the part
     uint32_t *s_before = s_touched + P.part / 32;             // touched tokens before the word
-    __shared__ uint32_t s_count[kPlaces], s_bias[kPlaces], s_token[kPlaces], s_warp[kMaxThreads / 32];
+    uint32_t *s_count = s_before + P.part / 32, *s_bias = s_count + P.places, *s_token = s_bias + P.places;
+    __shared__ uint32_t s_warp[kMaxThreads / 32];
     const uint64_t row = P.row0 + blockIdx.x / P.parts;
     const uint32_t part = blockIdx.x % P.parts;
     const T *x = static_cast<const T *>(P.x) + row * P.x_stride;
@@ -266,14 +268,14 @@ __global__ void __launch_bounds__(kMaxThreads) control_kernel(const __grid_const
         before += __popc(s_touched[w]);
     }
     bool streamed = !streams;
-    // windows of kPlaces places (nearly always one)
-    for (uint32_t first = 0; first < all; first += kPlaces) {
-        const uint32_t count = min(all - first, kPlaces);
+    // windows of so many places (nearly always one)
+    for (uint32_t first = 0; first < all; first += P.places) {
+        const uint32_t count = min(all - first, P.places);
         for (uint32_t i = tid; i < count; i += n) s_count[i] = s_bias[i] = 0;
         sync();
         each(false, [&](uint32_t i, uint32_t at) {
             const uint32_t p = s_before[at / 32] + __popc(s_touched[at / 32] & ((1u << (at % 32)) - 1u)) - first;
-            if (p >= kPlaces) return;
+            if (p >= P.places) return;
             s_token[p] = at;
             if (i >= n_history) atomicMax(&s_bias[p], i - n_history + 1);      // (a token that is listed twice takes its last bias)
             else if (i < n_prompt) atomicOr(&s_count[p], kSeen);
@@ -317,7 +319,7 @@ __global__ void __launch_bounds__(kMaxThreads) control_kernel(const __grid_const
         streamed = true;
         for (uint32_t p = tid; p < count; p += n)
             if (s_token[p] != 0xFFFFFFFFu) st_f32(y + j0 + s_token[p], __uint_as_float(s_count[p]));
-        if (first + kPlaces < all) sync();    // (the next window's counts)
+        if (all - first > P.places) sync();    // (the next window's counts)
     }
     if (!streamed) __syncthreads();
     if (P.after) grid_dep_wait();             // (a part without touched tokens too: this launch ends after the stream)
@@ -331,7 +333,7 @@ int launch(ControlParams P, uint64_t n, cudaStream_t stream) {
     const bool streams = P.x != P.y || P.c.mask, lists = P.c.history || P.c.bias_ids;
     if (!streams && !lists) return K3HUF_OK;
     static std::atomic<uint64_t> once{0};
-    const int attr_rc = once_per_device(once, [] { return cudaFuncSetAttribute(control_kernel<T, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kPart / 4)); });
+    const int attr_rc = once_per_device(once, [] { return cudaFuncSetAttribute(control_kernel<T, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kPart / 4 + 12 * kMostPlaces)); });
     if (attr_rc) return attr_rc;
     const uint64_t least = (uint64_t(P.vocab) + kPart - 1) / kPart, most = std::max<uint64_t>(least, P.vocab / 4096);
     auto run = [&](uint64_t parts, uint32_t threads, uint32_t streaming, bool after) {
@@ -345,7 +347,7 @@ int launch(ControlParams P, uint64_t n, cudaStream_t stream) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(uint32_t(std::min(rows, n - r0) * P.parts));
             cfg.blockDim = dim3(threads);
-            cfg.dynamicSmemBytes = streaming == threads ? 0 : P.part / 4;
+            cfg.dynamicSmemBytes = streaming == threads ? 0 : P.part / 4 + 12 * P.places;
             cfg.stream = stream;
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -359,14 +361,21 @@ int launch(ControlParams P, uint64_t n, cudaStream_t stream) {
     };
     // Few rows: one launch, as many parts as there are SMs, a CTA of 1024 threads each, half of which see to the lists
     // (they take a thread's time per entry).  More: a launch for the stream, then one for the lists, which begins while
-    // the first one ends.
-    if (n <= sms / 2) return run(std::max(least, std::min(most, sms / n)), kMaxThreads, !streams ? 0 : lists ? kMaxThreads / 2 : kMaxThreads, false);
+    // the first one ends.  Long lists touch more tokens than kPlaces, and each window reads them all again: such rows get
+    // more places (432 rows of 14338 different tokens 92 us, 128 with 2048 places; 8 rows of 30000 33 us, 48).
+    const uint64_t total = (P.c.history ? P.c.n_history : 0) + (P.c.bias_ids ? P.c.n_bias : 0);
+    auto places = [&](uint64_t list, uint32_t limit) { return uint32_t(std::clamp<uint64_t>((list + kPlaces - 1) / kPlaces * kPlaces, kPlaces, limit)); };
+    if (n <= sms / 2) {
+        P.places = places(total, kMostPlaces);
+        return run(std::max(least, std::min(most, sms / n)), kMaxThreads, !streams ? 0 : lists ? kMaxThreads / 2 : kMaxThreads, false);
+    }
     if (streams) {
         const int stream_rc = run(std::max(least, std::min(most, sms * 24 / n)), 256, 256, false);
         if (stream_rc || !lists) return stream_rc;
     }
+    P.places = places(total / n, kMostPlaces / 2);
     // (of the lists, as many threads per row as the GPU has for it: 93 rows of 8000 entries 30 us with 256)
-    return run(least, n <= sms ? 1024 : n <= 2 * sms ? 512 : 256, 0, streams);
+    return run(least, n <= sms ? 1024 : n <= 2 * sms || P.places > kPlaces ? 512 : 256, 0, streams);
 }
 
 }  // namespace
@@ -387,7 +396,7 @@ extern "C" int k3huf_logits_control(const k3huf_control_t *control, const void *
     if (c.mask && (c.mask_stride < (uint64_t(vocab) + 31) / 32 || (!c.mask_rows && c.n_masks < n))) return K3HUF_E_ARG;
     if (n == 0) return K3HUF_OK;
     if (!d_logits || !d_out || (d_logits == d_out && (type != out_type || stride != out_stride))) return K3HUF_E_ARG;
-    const ControlParams P{d_logits, d_out, c, d_status, stride, out_stride, 0, vocab, 1, 0, 0, false};
+    const ControlParams P{d_logits, d_out, c, d_status, stride, out_stride, 0, vocab, 1, 0, 0, kPlaces, false};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (type == K3HUF_BF16) return out_type == K3HUF_BF16 ? launch<__nv_bfloat16, __nv_bfloat16>(P, n, st) : launch<__nv_bfloat16, float>(P, n, st);
     return out_type == K3HUF_BF16 ? launch<float, __nv_bfloat16>(P, n, st) : launch<float, float>(P, n, st);
