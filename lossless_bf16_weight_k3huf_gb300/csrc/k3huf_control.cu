@@ -199,8 +199,38 @@ __global__ void __launch_bounds__(kMaxThreads) control_kernel(const __grid_const
     const uint32_t size = j1 - j0, words = (size + 31) / 32;
     // places in the part of the entries i0, i0 + n, ... (2^32 - 1: none, or a token of another part)
     auto load = [&](uint32_t i0, bool check, uint32_t (&at)[kAhead]) {
-        // (nothing but loads in the first loop: the use of one before the next is issued would wait for it)
+        // (nothing but loads in the first loops: the use of one before the next is issued would wait for it)
         int32_t lo[kAhead], hi[kAhead];
+        bool past = false;
+        // (where all threads' are of the history, a third of the instructions does: 8 rows of 30000 tokens 25 us, 33 without)
+        const bool whole = i0 - tid + kAhead * n <= n_history;
+        if (whole && wide0 == 1) {
+            const int32_t *q = static_cast<const int32_t *>(ids[0]) + i0;
+#pragma unroll
+            for (uint32_t k = 0; k < kAhead; ++k) lo[k] = __ldg(q + k * n);
+#pragma unroll
+            for (uint32_t k = 0; k < kAhead; ++k) {
+                past = past || lo[k] >= int32_t(P.vocab);
+                at[k] = uint32_t(lo[k]) - j0 < size ? uint32_t(lo[k]) - j0 : 0xFFFFFFFFu;
+            }
+            if (past && check) atomicOr(P.status, K3HUF_ST_TOKEN);
+            return;
+        }
+        if (whole) {
+            const int2 *q = static_cast<const int2 *>(ids[0]) + i0;
+#pragma unroll
+            for (uint32_t k = 0; k < kAhead; ++k) {
+                const int2 v = __ldg(q + k * n);
+                lo[k] = v.x, hi[k] = v.y;
+            }
+#pragma unroll
+            for (uint32_t k = 0; k < kAhead; ++k) {
+                past = past || (hi[k] >= 0 && (hi[k] > 0 || uint32_t(lo[k]) >= P.vocab));
+                at[k] = hi[k] == 0 && uint32_t(lo[k]) - j0 < size ? uint32_t(lo[k]) - j0 : 0xFFFFFFFFu;
+            }
+            if (past && check) atomicOr(P.status, K3HUF_ST_TOKEN);
+            return;
+        }
 #pragma unroll
         for (uint32_t k = 0; k < kAhead; ++k) {
             const uint32_t i = i0 + k * n;
@@ -212,7 +242,6 @@ __global__ void __launch_bounds__(kMaxThreads) control_kernel(const __grid_const
             lo[k] = __ldg(q);
             if (wide == 2) hi[k] = __ldg(q + 1);
         }
-        bool past = false;
 #pragma unroll
         for (uint32_t k = 0; k < kAhead; ++k) {
             if ((i0 + k * n >= n_history ? wide1 : wide0) != 2) hi[k] = lo[k] >> 31;
