@@ -164,6 +164,31 @@ def test_every_token_touched():
             assert check(x, c, None, in_place=in_place) == 0
 
 
+@pytest.mark.parametrize("ids", [torch.int32, torch.int64])
+@pytest.mark.parametrize("n", [3, 200, 400])
+def test_long_rows_of_different_tokens(n, ids):
+    """Rows that differ in how many tokens they touch, fewer and more than are looked after at once; ids that are none, within."""
+    V, r = 40011, np.random.default_rng(n)
+    x, c, bits = case(n, V, seed=n, x_type=BF, history=5, bias=40, allowed=0.6, ids=ids)
+    length = r.integers(0, 7001, n)
+    length[:3] = 30011, 0, 8192
+    ends = np.cumsum(length)
+    tokens = r.integers(0, V, ends[-1])
+    c["history"] = torch.from_numpy(tokens).cuda().to(ids)
+    c["spans"] = torch.from_numpy(np.stack([ends - length, ends - length // 2, ends], 1)).cuda()
+    assert check(x, c, bits) == 0
+    # (an id past the vocabulary is no token, and -1 none either)
+    at = torch.from_numpy(r.choice(20000, 50, replace=False)).cuda()
+    c["history"][at] = -1
+    assert check(x, c, bits) == 0
+    want, got, st = torch.empty_like(x), torch.empty_like(x), status()
+    k3.logits_control(x, want, st, **c)
+    assert int(st) == 0
+    c["history"][at[0]] = V if ids == torch.int32 else 1 << 33
+    k3.logits_control(x, got, st, **c)
+    assert torch.equal(got, want) and int(st) == k3.ST_TOKEN
+
+
 def test_each_part_alone():
     for drop in (("repetition",), ("frequency",), ("presence",), ("repetition", "frequency", "presence"), ("bias_ids", "bias_values", "bias_spans"),
                  ("history", "spans", "repetition", "frequency", "presence"), ("mask", "mask_rows")):
