@@ -677,9 +677,22 @@ __global__ void __launch_bounds__(kCopyThreads) align_rows_kernel(const uint16_t
         const uint64_t r = at / per_row;
         const uint32_t c = uint32_t(at % per_row) * 8;
         const uint16_t *src = from + r * stride + c;
-        uint32_t w[4];
+        const uint32_t past = uint32_t(reinterpret_cast<uintptr_t>(src) % 16 / 2);
+        uint32_t w[8];
+        if (c >= past && c + 16 - past <= cols) {
+            // (two whole 16-byte blocks of the row's own hold them)
+            const uint4 *q = reinterpret_cast<const uint4 *>(src - past), one = __ldg(q), two = __ldg(q + 1);
+            w[0] = one.x, w[1] = one.y, w[2] = one.z, w[3] = one.w, w[4] = two.x, w[5] = two.y, w[6] = two.z, w[7] = two.w;
 #pragma unroll
-        for (uint32_t k = 0; k < 4; ++k) w[k] = (c + 2 * k < cols ? src[2 * k] : 0u) | (c + 2 * k + 1 < cols ? uint32_t(src[2 * k + 1]) << 16 : 0u);
+            for (uint32_t k = 0; k < 6; ++k) w[k] = past & 4 ? w[k + 2] : w[k];
+#pragma unroll
+            for (uint32_t k = 0; k < 5; ++k) w[k] = past & 2 ? w[k + 1] : w[k];
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) w[k] = past & 1 ? __funnelshift_r(w[k], w[k + 1], 16) : w[k];
+        } else {
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) w[k] = (c + 2 * k < cols ? src[2 * k] : 0u) | (c + 2 * k + 1 < cols ? uint32_t(src[2 * k + 1]) << 16 : 0u);
+        }
         reinterpret_cast<uint4 *>(to)[at] = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
