@@ -389,8 +389,10 @@ int launch(ControlParams P, uint64_t n, cudaStream_t stream) {
         return int(K3HUF_OK);
     };
     // Few rows: one launch, as many parts as there are SMs, a CTA of 1024 threads each, half of which see to the lists
-    // (they take a thread's time per entry).  More: a launch for the stream, then one for the lists, which begins while
-    // the first one ends.  Long lists touch more tokens than kPlaces, and each window reads them all again: such rows get
+    // (they take a thread's time per entry).  More, as long as the GPU holds two CTAs of 512 per SM for all: the same with
+    // those (100 rows of 131072 10.7 us, 19 with two launches; 300 rows of 50021 20 and 26).  Many: a launch for the stream,
+    // then one for the lists, which begins while the first one ends (400 rows of 50021 31 us, 33 with one launch; 1024 of
+    // 131072 118 and 127).  Long lists touch more tokens than kPlaces, and each window reads them all again: such rows get
     // more places (432 rows of 14338 different tokens 92 us, 128 with 2048 places; 8 rows of 30000 33 us, 48).
     const uint64_t total = (P.c.history ? P.c.n_history : 0) + (P.c.bias_ids ? P.c.n_bias : 0);
     auto places = [&](uint64_t list, uint32_t limit) { return uint32_t(std::clamp<uint64_t>((list + kPlaces - 1) / kPlaces * kPlaces, kPlaces, limit)); };
@@ -398,11 +400,12 @@ int launch(ControlParams P, uint64_t n, cudaStream_t stream) {
         P.places = places(total, kMostPlaces);
         return run(std::max(least, std::min(most, sms / n)), kMaxThreads, !streams ? 0 : lists ? kMaxThreads / 2 : kMaxThreads, false);
     }
+    P.places = places(total / n, kMostPlaces / 2);
+    if (streams && lists && n <= 2 * sms) return run(std::max(least, std::min(most, sms * 2 / n)), 512, 256, false);
     if (streams) {
         const int stream_rc = run(std::max(least, std::min(most, sms * 24 / n)), 256, 256, false);
         if (stream_rc || !lists) return stream_rc;
     }
-    P.places = places(total / n, kMostPlaces / 2);
     // (of the lists, as many threads per row as the GPU has for it: 93 rows of 8000 entries 30 us with 256)
     return run(least, n <= sms ? 1024 : n <= 2 * sms || P.places > kPlaces ? 512 : 256, 0, streams);
 }
