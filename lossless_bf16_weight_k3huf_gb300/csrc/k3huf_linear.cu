@@ -868,6 +868,33 @@ struct Cut {
     uint32_t tile_j, pair, splits;
     uint64_t tiles;
 };
+// Clusters of so many CTAs, each with an SM of its own, that the GPU holds at once: fewer than its SMs would make room for, as
+// a cluster lies within one of its parts (50 clusters of three do not fit: 186 x 3176 x 9960 57 us with them, 45 in twos).
+uint64_t clusters_of(uint32_t splits, uint64_t sms) {
+    static std::atomic<int> known[kMaxSplits + 1];
+    int n = known[splits];
+    if (n == 0) {
+        constexpr auto kernel = product_kernel<128, false, false>;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(splits);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Shape<128>::smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = splits;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Shape<128>::smem)) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+            (void)cudaGetLastError();         // (only the choice depends on it)
+            n = int(sms / splits);
+        }
+        known[splits] = n;
+    }
+    return uint64_t(n);
+}
+
 // The cut of the lowest cost by this count of cycles.  A step of 64 of the contraction takes the tensor core 128 x tile_j x
 // 64 / 4096 cycles per CTA, a tenth more where it is kept busiest, and the copies their bytes at kLoadRate; CTAs that share
 // an SM share both.  The epilogue's time (of all the SM's CTAs; fitted to 8192 x 8192 x 64) passes beside the next tile's
@@ -888,7 +915,8 @@ Cut choose(uint64_t size_i, uint64_t size_j, uint64_t steps, uint64_t sms) {
         const uint64_t memory = (size_i * (3 + (size_j + tile_j - 1) / tile_j) / 4 + size_j) * steps * kStep * 2 / kMemoryRate;
         const uint64_t most = pair == 2 ? 1 : std::max<uint64_t>(1, std::min<uint64_t>({kMaxSplits, slots / c.tiles, steps / 2}));
         for (c.splits = 1; c.splits <= most; ++c.splits) {
-            const uint64_t waves = (c.tiles * c.splits + slots - 1) / slots;
+            const uint64_t at_once = c.splits > 1 ? clusters_of(c.splits, sms) * per_sm : slots;
+            const uint64_t waves = (c.tiles + at_once - 1) / at_once;
             const uint64_t cost = std::max(memory, waves * std::max((steps + c.splits - 1) / c.splits * step, epilogue)) + epilogue + (c.splits > 1 ? kJoinCost : 0);
             if (cost < least || (cost == least && c.tile_j == best.tile_j)) least = cost, best = c;
         }
