@@ -14,7 +14,7 @@
 // Forward, one read of the logits: a CTA streams a row, or the CTAs of a cluster when there are fewer rows than the
 // GPU holds CTAs.  To leave the alternatives out of the rest's sum, every thread has a bit for each of its
 // vectors (modulo 64); it passes over those that may hold one, and the warp beside the stream adds what else they
-// hold.  What bounds it: the read of the logits, 4095 rows of 131072 bf16 166 us (6.5 TB/s), 188 with the rest, whose
+// hold.  What bounds it: the read of the logits, 4095 rows of 131072 bf16 164 us (6.5 TB/s), 188 with the rest, whose
 // rows cannot start before their alternatives are known.
 //
 // Backward: elementwise; every other token's gradient is s g (Q p_r - q_r) exp(z_j - lse - log p_r), the
