@@ -162,6 +162,19 @@ def test_infinities_and_nan_stay_in_their_rows():
     assert bool(((y.double() - want).abs()[fine] <= (sum_bound(xf, wf) + E * want.abs())[fine]).all())
 
 
+@pytest.mark.parametrize("y_type", [BF, F32])
+@pytest.mark.parametrize("n,rows,cols", [(1003, 4104, 192), (4001, 2056, 576), (300, 8200, 64), (2570, 1000, 1100)])
+def test_residuals_of_large_results(n, rows, cols, y_type):
+    """Rows of a residual that start on 16 bytes and rows that do not, tiles that end inside; in place, bit for bit the same."""
+    for pad in (0, 1):
+        forward(n, rows, cols, act="silu", y_type=y_type, bias=F32, res=True, z_type=BF, pad=(0, 0, pad, 0), seed=n + pad)
+    x, w, r = normal(n, cols, seed=1, dtype=BF), normal(rows, cols, seed=2, dtype=BF), normal(n, rows, seed=3, dtype=y_type)
+    st, y, room = status(), torch.empty_like(r), scratch(n, rows, cols)
+    k3.linear(x, w, y, st, residual=r, act="gelu", scratch=room)
+    k3.linear(x, w, r, st, residual=r, act="gelu", scratch=room)
+    assert torch.equal(y, r) and int(st) == 0
+
+
 def test_fp32_results_hold_long_sums():
     """All products positive: steps that round to one side add up.  Every 32 steps of 16 the sum leaves the tensor core,
     so the error is at most that of 32 steps and of K / 512 additions to nearest."""
