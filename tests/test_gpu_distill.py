@@ -5,6 +5,7 @@ itself, and a sum of V of them by (V / 64 + 16) 2^-24 more (64 or more partial s
 The loss adds, in 64 bits, Q times the error of the row's sum and q_r times that of the rest's, and is rounded once.
 In the gradient the exponent z - lse (- log p_r) of an fp32 lse errs by 2^-24 of each of its terms' magnitudes, a few times
 over; what it multiplies is computed in 64 bits."""
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -179,6 +180,27 @@ def test_a_token_listed_twice(mode, dtype):
     check(x, ids, t, mode)
     check_grad(x, ids, t, mode)
     check_grad(x, ids, t, mode, in_place=True)
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_alternatives_alike_and_far_apart(mode, dtype):
+    """64 alternatives: listed twice, in either half of the list; in neighbouring places, and as far apart as makes a row's
+    vectors fall together; of log-probabilities near 0 to far below what 32 bits hold."""
+    V, r = 262149, np.random.default_rng(17)
+    x, _, _ = make(5, V, 64, seed=23, dtype=dtype)
+    ids = np.zeros((5, 64), dtype=np.int64)
+    for row in range(5):
+        j = r.integers(0, 65000, 8)
+        ids[row] = np.concatenate([j, j + 65536, j + 131072, j + 131073, j + 196608, j + 7, r.permutation(j), r.permutation(j + 131072)])
+        ids[row] = ids[row][r.permutation(64)]
+    t = r.choice([-1000.0, -100.0, -85.5, -79.5, -20.0, -7.0], (5, 64))
+    t[0] = -6.0 + r.random(64)
+    t[1] = -79.0 - r.random(64)
+    t[2, 5], t[3, 40], t[4, 60] = -0.25, -0.5, -INF
+    ids, t = torch.from_numpy(ids).cuda().to(torch.int32), torch.from_numpy(t).cuda().float()
+    check(x, ids, t, mode, scale=1.3)
+    check_grad(x, ids, t, mode, scale=1.3)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
