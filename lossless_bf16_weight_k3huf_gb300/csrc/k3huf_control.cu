@@ -168,7 +168,10 @@ __global__ void __launch_bounds__(kMaxThreads) control_kernel(const __grid_const
     }
     const bool streams = P.streaming > 0;
     const uint32_t n = blockDim.x - P.streaming, tid = threadIdx.x - P.streaming, lane = tid % 32, warp = tid / 32;
-    auto sync = [&]() { asm volatile("bar.sync 1, %0;" ::"r"(n) : "memory"); };      // (of these threads)
+    auto sync = [&]() {                       // (of these threads; a warp's come to it together, wherever they parted before)
+        __syncwarp();
+        asm volatile("bar.sync 1, %0;" ::"r"(n) : "memory");
+    };
     // the two lists, numbered as one: tokens of the history, then of the biases
     const void *ids[2] = {c.history, c.bias_ids};
     uint32_t n_history = 0, n_prompt = 0, entries = 0;

@@ -359,3 +359,28 @@ def test_decoded_weight_and_the_coded_product_agree():
     check(y, want, bound, "linear")
     assert bool(((v.double() - want).abs() <= cols * E * (x.double().abs() @ w.view(rows, cols).double().abs().T)).all())
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("n,rows,cols", [(1, 100, 4096), (9, 200, 3000), (40, 333, 5000), (100, 130, 9000), (1300, 17, 64), (2500, 40, 128)])
+def test_warps_that_part_meet_again_at_the_clusters_barriers(n, rows, cols):
+    """Contractions that clusters share, of tiles whose last columns or lanes lie outside, and sums of slopes over clusters
+    with half a warp of columns: warps part in these before they meet the cluster.  Every call gives the same bits."""
+    x, w, z, dy = normal(n, cols, seed=1), normal(rows, cols, seed=2, std=cols ** -0.5), normal(n, rows, seed=3, dtype=F32), normal(n, rows, seed=4)
+    b, room, st = normal(rows, seed=5, dtype=F32), scratch(n, rows, cols, grad=True), status()
+    first = None
+    for _ in range(10):
+        y, dx, dw = torch.empty(n, rows, device="cuda"), torch.empty(n, cols, device="cuda"), torch.empty(rows, cols, device="cuda")
+        dz, db = torch.empty(n, rows, dtype=BF, device="cuda"), torch.empty(rows, device="cuda")
+        k3.linear(x, w, y, st, bias=b, act="silu", scratch=room)
+        k3.linear_dz(z, dy, dz, act="silu", dbias=db)
+        k3.linear_grad(x, w, dz, st, dx=dx, dw=dw, scratch=room)
+        now = (y, dz, db, dx, dw)
+        first = first or now
+        assert all(torch.equal(a, c) for a, c in zip(first, now))
+    assert int(st) == 0
+    want = x.double() @ w.double().T + b.double()
+    check(first[0], act64(want, "silu"), 1.2 * (sum_bound(x, w) + E * want.abs()) + 8 * E * want.abs(), "y")
+    want = dy.double() * slope64(z.double(), "silu")
+    bound = 16 * E * (1 + z.double().abs()) * dy.double().abs()
+    check(first[1], want, bound, "dz")
+    assert bool(((first[2].double() - want.sum(0)).abs() <= bound.sum(0) + (n / 16 + 32) * E * (want.abs().sum(0) + bound.sum(0))).all())
