@@ -104,7 +104,7 @@ def check(x, ids, t, mode, scale=1.0, want_status=0):
     return loss, lse, log_rest
 
 
-def check_grad(x, ids, t, mode, scale=1.0, in_place=False, out_pad=0, want_status=0):
+def check_grad(x, ids, t, mode, scale=1.0, in_place=False, out_pad=0, want_status=0, least=1e-37):
     n, V = x.shape
     _, lse, log_rest, _ = run(x, ids, t, mode, scale)
     g = torch.Generator(device="cuda").manual_seed(n * 7 + V)
@@ -132,7 +132,7 @@ def check_grad(x, ids, t, mode, scale=1.0, in_place=False, out_pad=0, want_statu
     want = torch.where(some[:, None], gs * (Q * p - qs - share), torch.zeros_like(p))
     far = z.abs().masked_fill(z == -INF, 0) + torch.nan_to_num(torch.logsumexp(z, 1), neginf=0).abs()[:, None] + torch.nan_to_num(r_rest, neginf=0).abs()[:, None] + 8
     bound = gs.abs() * (4 * E * far * (Q * p + share) + 2 * E * qs)
-    close(out, want, bound + 1e-37, "dlogits")
+    close(out, want, bound + least, "dlogits")
     return out
 
 
@@ -225,6 +225,52 @@ def test_a_small_rest_keeps_its_digits(dtype):
     loss, _, log_rest, _ = run(x, ids, half, "rest", 1.0)
     assert bool((loss == INF).all()) and bool((log_rest == -INF).all())
     check_grad(x, ids, half, "rest")
+
+
+def below(n, V, top, gap, scale, dtype, seed):
+    """Rows whose alternatives lie at least `gap` scaled units above every other token."""
+    x, ids, t = make(n, V, top, seed, dtype, none=0.0)
+    at = ids.long()
+    high = x.float().clone()
+    high.scatter_(1, at, high.gather(1, at) + gap / scale)
+    return high.to(dtype), ids, t
+
+
+def rest_apart(x, ids, t, scale):
+    """Loss, lse and log_rest against 64 bits.  An exponent scale * x is taken with the scale times log2 e in 32 bits: 2^-24
+    of it, which both sides of a difference of logits share, so 2^-24 of the difference; what else errs is as in check()."""
+    loss, lse, log_rest, st = run(x, ids, t, "rest", scale)
+    assert st == 0
+    z, logp, on, at, q, tt, r_rest, rest, taken = parts(x, ids, t, "rest", scale)
+    e_all, e_rest = sum_error(z, torch.ones_like(taken)), sum_error(z, ~taken)
+    lp = logp.gather(1, at)
+    want = (q * (tt - lp)).sum(1) + rest * (torch.log(rest) - r_rest)
+    assert bool((rest > 0).all())
+    close(lse, torch.logsumexp(z, 1), e_all + 2 * E * torch.logsumexp(z, 1).abs(), "lse")
+    close(log_rest, r_rest, e_rest + e_all + E * r_rest.abs(), "log_rest")
+    close(loss, want, q.sum(1) * e_all + rest * (e_rest + e_all) + E * ((q * lp.abs()).sum(1) + rest * r_rest.abs()) + 1e-12 * (q * tt.abs()).sum(1), "loss")
+    return loss, lse, log_rest
+
+
+@pytest.mark.parametrize("scale", [1.0, 10.0])
+@pytest.mark.parametrize("gap", [70.0, 85.0, 100.0, 1000.0, 30000.0])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,V", [(4, 3000), (3, 20011), (2, 140000), (1000, 1500)])
+def test_a_rest_far_below_the_alternatives(n, V, dtype, gap, scale):
+    """p_r far below the smallest fp32 number: its logarithm, the loss and the gradient are finite all the same.  A CTA per
+    row, and clusters."""
+    x, ids, t = below(n, V, 4, gap, scale, dtype, n + V)
+    loss, _, log_rest = rest_apart(x, ids, t, scale)
+    assert bool((log_rest < -gap / 2).all()) and bool(torch.isfinite(log_rest).all()) and bool(torch.isfinite(loss).all())
+    # (exponentials below 2^-126 are 0: times scale |g| (Q + q_r) at most, with |g| < 6 here and Q + q_r < 2)
+    least = 2.0 ** -126 * scale * 12
+    for in_place in (False, True):
+        d = check_grad(x, ids, t, "rest", scale=scale, in_place=in_place, least=least)
+        assert bool(torch.isfinite(d.float()).all())
+    # ... and the alternatives as far below the others
+    x, ids, t = below(n, V, 4, -gap, scale, dtype, n + V + 1)
+    rest_apart(x, ids, t, scale)
+    check_grad(x, ids, t, "rest", scale=scale, least=least)
 
 
 def test_infinite_terms():
