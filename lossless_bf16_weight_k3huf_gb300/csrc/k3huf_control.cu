@@ -15,6 +15,7 @@
 // (Counters of the vocabulary's size, cleared per row, cost 409 us instead of 123.)
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "k3huf_rows.h"
 #include "k3huf_tc.h"
@@ -74,6 +75,22 @@ __device__ __forceinline__ void store_unit(__nv_bfloat16 *p, const float (&f)[kU
 #pragma unroll
     for (int k = 0; k < 4; ++k) h[k] = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
     __stcs(reinterpret_cast<uint4 *>(p), o);
+}
+
+// ... a unit of bf16 as it is, -infinity where the mask's bit is 0 (by way of fp32 every NaN would become the same one)
+__device__ __forceinline__ void store_allowed(__nv_bfloat16 *p, const Raw<__nv_bfloat16> &r, uint32_t ok) {
+    uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t keep = (ok >> (2 * k) & 1 ? 0xFFFFu : 0u) | (ok >> (2 * k + 1) & 1 ? 0xFFFF0000u : 0u);
+        w[k] = (w[k] & keep) | (0xFF80FF80u & ~keep);
+    }
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(w[0], w[1], w[2], w[3]));
+}
+// ... and one value
+template <typename T, typename U> __device__ __forceinline__ void copy_to(U *to, const T *from) {
+    if constexpr (std::is_same_v<T, U>) *to = *from;
+    else st_f32(to, ld_f32(from));
 }
 
 // A row's span [from, to) of a list, or nothing (and the status bit) where it is none.
@@ -146,11 +163,15 @@ __global__ void __launch_bounds__(kMaxThreads) control_kernel(const __grid_const
             for (int i = 0; i < kUnits<T>; ++i) {
                 const uint32_t j = u0 + (i * P.streaming + tid) * kUnit;
                 if (j >= last || (in_place && ok[i] == 0xFFu)) continue;
-                float f[kUnit];
-                unpack_unit(raw[i], f);
+                if constexpr (std::is_same_v<T, U> && sizeof(T) == 2) {
+                    store_allowed(y + j, raw[i], ok[i]);
+                } else {
+                    float f[kUnit];
+                    unpack_unit(raw[i], f);
 #pragma unroll
-                for (uint32_t k = 0; k < kUnit; ++k) f[k] = ok[i] >> k & 1 ? f[k] : -INFINITY;
-                store_unit(y + j, f);
+                    for (uint32_t k = 0; k < kUnit; ++k) f[k] = ok[i] >> k & 1 ? f[k] : -INFINITY;
+                    store_unit(y + j, f);
+                }
             }
 #pragma unroll
             for (int i = 0; i < kUnits<T>; ++i) raw[i] = next[i], ok[i] = ahead[i];
@@ -161,7 +182,7 @@ __global__ void __launch_bounds__(kMaxThreads) control_kernel(const __grid_const
         for (uint32_t i = tid; i < rest; i += P.streaming) {
             const uint32_t j = j0 + i < first ? j0 + i : j0 + i + (last - first);
             if (banned(j)) st_f32(y + j, -INFINITY);
-            else if (!in_place) st_f32(y + j, ld_f32(x + j));
+            else if (!in_place) copy_to(y + j, x + j);
         }
         if (P.streaming < blockDim.x) __syncthreads();
         return;

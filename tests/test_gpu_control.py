@@ -224,6 +224,39 @@ def test_untouched_logits_keep_their_value():
     assert torch.equal(out.view(torch.int16)[~touched], x.view(torch.int16)[~touched])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,V", [(3, 20011), (40, 1000), (700, 3001)])
+def test_untouched_nan_keep_their_bits(n, V, dtype):
+    """NaN of either sign and any payload: copied, copied to rows that sit otherwise, in place beside banned tokens."""
+    bits = (torch.int16, (0x7FC0, -0x40, 0x7F81, -1, 0x7FFF, -0x7F)) if dtype == BF else (torch.int32, (0x7FC00000, -0x400000, 0x7F800001, -1, 0x7FABCDEF, -0x7FFFFF))
+    for k, (allowed, in_place, pad) in enumerate([(None, False, 0), (0.6, False, 0), (0.6, False, 3), (None, False, 1), (0.9, True, 0), (0.5, True, 5)]):
+        x, c, allow = case(n, V, seed=n + k, x_type=dtype, history=20, bias=3, allowed=allowed, pad=pad if in_place else 0)
+        r = np.random.default_rng(k)
+        where = torch.from_numpy(r.random((n, V)) < 0.2).cuda()
+        some = torch.tensor(bits[1], dtype=bits[0], device="cuda")[torch.from_numpy(r.integers(0, 6, (n, V))).cuda()]
+        x = x.contiguous()
+        x.view(bits[0])[where] = some[where]
+        keep = torch.ones(n, V, dtype=torch.bool, device="cuda")
+        for t in range(n):
+            a, _, e = c["spans"][t].tolist()
+            h = c["history"][a:e].long()
+            keep[t, h[h >= 0]] = False
+            a, e = c["bias_spans"][t].tolist()
+            keep[t, c["bias_ids"][a:e].long()] = False
+        banned = torch.zeros_like(keep)
+        if allow is not None:
+            state = c["mask_rows"].long()
+            banned = ~torch.from_numpy(allow).cuda()[state.clamp(min=0)] & (state >= 0)[:, None]
+        whole = torch.zeros(n, V + pad, dtype=dtype, device="cuda")
+        out, st = whole[:, :V], status()
+        if in_place:
+            out.copy_(x)
+        assert not in_place or torch.equal(out.contiguous().view(bits[0]), x.view(bits[0]))
+        k3.logits_control(out if in_place else x, out, st, **c)
+        got = out.contiguous()
+        assert torch.equal(got.view(bits[0])[keep & ~banned], x.view(bits[0])[keep & ~banned]) and bool((got[banned] == -INF).all()) and int(st) == 0
+
+
 def test_infinities_nan_and_masks_of_nothing():
     x, c, bits = case(6, 700, seed=6, allowed=0.5)
     x[0, :50] = -INF
