@@ -581,7 +581,9 @@ int k3huf_token_logprobs_grad(const void *d_logits, uint32_t type, uint64_t stri
  * From a decoded weight to its logits and what is done with them: the product of
  * many tokens with a bf16 weight (k3huf_decode_tensor's output), the control of
  * logits before a token is chosen, distillation from a teacher's alternatives.
- * The conventions of the operators above hold here too. */
+ * The conventions of the operators above hold here too.  An output overlaps no
+ * other argument but where it says so; the products refuse (K3HUF_E_ARG) one that
+ * starts where such an argument does. */
 
 /* act(z): z; max(z, 0); z / (1 + exp(-z)); the tanh form of GELU,
  * z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))). */
@@ -605,7 +607,8 @@ int k3huf_linear_scratch_bytes(uint64_t n_tokens, uint64_t rows, uint64_t cols, 
  *  d_residual: rows of y's type, or NULL; may be d_y itself (then
  *    residual_stride = y_stride);
  *  d_y: n_tokens rows of `rows` elements of y_type;
- *  d_z: where a backward pass wants z, rows of z_type; or NULL.
+ *  d_z: where a backward pass wants z, rows of z_type; or NULL.  May be d_residual,
+ *    where that is of the same type and stride.
  * Sums are fp32: for fp32 y they leave the tensor core every 512 values of the
  * contraction, whose additions round to one side.  Up to 2^31 - 1 tokens, rows
  * and columns. */

@@ -1019,6 +1019,10 @@ extern "C" int k3huf_linear(const void *d_x, uint64_t x_stride, uint64_t n_token
         return K3HUF_E_ARG;
     if (n_tokens == 0) return K3HUF_OK;
     if (!d_x || !d_w || !d_y) return K3HUF_E_ARG;
+    // (other CTAs read x and w, and the bias, while a result is written)
+    for (const void *out : {d_y, d_z})
+        if (out && (out == d_x || out == d_w || out == d_bias)) return K3HUF_E_ARG;
+    if (d_z && d_z == d_residual && (z_type != y_type || z_stride != residual_stride)) return K3HUF_E_ARG;
     Operand w{d_w, w_stride, rows, uint32_t(cols)}, x{d_x, x_stride, n_tokens, uint32_t(cols)};
     const uint64_t need = need_of(w) + need_of(x);
     if (need && (!d_scratch || scratch_bytes < need)) return K3HUF_E_ARG;
@@ -1044,6 +1048,7 @@ extern "C" int k3huf_linear_dz(const void *d_z, uint32_t z_type, uint64_t z_stri
     if ((d_dz && d_dz == d_dy && (dy_type != K3HUF_BF16 || dy_stride != dz_stride)) || (d_dz && d_dz == d_z && (z_type != K3HUF_BF16 || z_stride != dz_stride))) return K3HUF_E_ARG;
     const bool add = (flags & K3HUF_ACCUMULATE) != 0;
     if (n_tokens == 0 && (!d_dbias || add)) return K3HUF_OK;
+    if (n_tokens && d_dbias && (d_dbias == d_z || d_dbias == d_dy || d_dbias == d_dz)) return K3HUF_E_ARG;
     uint64_t sms = 0;
     const int rc = sm_count(&sms);
     if (rc) return rc;
@@ -1087,6 +1092,9 @@ extern "C" int k3huf_linear_grad(const void *d_x, uint64_t x_stride, uint64_t n_
     const bool add = (flags & K3HUF_ACCUMULATE) != 0;
     if (n_tokens == 0) return d_dw && !add ? cuda_rc(cudaMemsetAsync(d_dw, 0, rows * cols * 4, st)) : K3HUF_OK;
     if ((!d_dx && !d_dw) || !d_dz || (d_dx && !d_w) || (d_dw && !d_x)) return K3HUF_E_ARG;
+    // (dx is written before dW's sums read x and dz; and other CTAs read what a result is made from while it is written)
+    if (d_dx && (d_dx == d_dz || d_dx == d_w || d_dx == d_dw || (d_dw && d_dx == d_x))) return K3HUF_E_ARG;
+    if (d_dw && (d_dw == d_dz || d_dw == d_x || (d_dx && d_dw == d_w))) return K3HUF_E_ARG;
     Operand dz{d_dz, dz_stride, n_tokens, uint32_t(rows)}, w{d_w, w_stride, rows, uint32_t(cols)}, x{d_x, x_stride, n_tokens, uint32_t(cols)};
     const uint64_t need = need_of(dz) + (d_dx ? need_of(w) : 0) + (d_dw ? need_of(x) : 0);
     if (need && (!d_scratch || scratch_bytes < need)) return K3HUF_E_ARG;

@@ -384,3 +384,15 @@ def test_warps_that_part_meet_again_at_the_clusters_barriers(n, rows, cols):
     bound = 16 * E * (1 + z.double().abs()) * dy.double().abs()
     check(first[1], want, bound, "dz")
     assert bool(((first[2].double() - want.sum(0)).abs() <= bound.sum(0) + (n / 16 + 32) * E * (want.abs().sum(0) + bound.sum(0))).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,rows,cols,pad", [(3, 300, 1000, 0), (40, 520, 320, 0), (1003, 4104, 192, 0), (1003, 4104, 192, 1)])
+def test_z_over_the_residual(n, rows, cols, pad, dtype):
+    """z may be written where the residual is read, of the same type and stride: bit for bit what separate buffers give."""
+    x, w, r = normal(n, cols, seed=1), normal(rows, cols, seed=2, std=0.05), normal(n, rows, seed=3, dtype=dtype, pad=pad)
+    z, st = torch.empty(n, rows + pad, dtype=dtype, device="cuda")[:, :rows], status()
+    y, over = torch.empty(n, rows, dtype=dtype, device="cuda"), torch.empty(n, rows, dtype=dtype, device="cuda")
+    k3.linear(x, w, y, st, residual=r, act="silu", z=z)
+    k3.linear(x, w, over, st, residual=r, act="silu", z=r)
+    assert torch.equal(y, over) and torch.equal(z, r) and int(st) == 0

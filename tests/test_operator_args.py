@@ -196,3 +196,52 @@ def test_distill_grad(lib):
                dict(top=65), dict(mode=3), dict(mode=0), dict(rest=None), dict(rest=P + 2), dict(lse=None), dict(lse=P + 1), dict(g=None), dict(g=P + 2),
                dict(d=None), dict(d=P + 2), dict(ds=49), dict(ds=60), dict(st=None)):
         assert call(**kw) == k3.E_ARG, kw
+
+
+def test_products_refuse_outputs_over_their_inputs(lib):
+    """Every argument at an address of its own, but for the one pair that is named."""
+    x, w, bias, res, y, z, dz, dx, dw, dy, db = (P + (k << 16) for k in range(11))
+
+    def linear(x=x, w=w, bias=bias, res=res, y=y, z=z, zs=32, zt=0):
+        return lib.k3huf_linear(x, 32, 4, w, 32, 32, 32, bias, 0, 1, res, 32, y, 32, 0, z, zs, zt, None, 0, P, None)
+
+    for kw in (dict(y=x), dict(y=w), dict(y=bias), dict(y=z), dict(z=x), dict(z=w), dict(z=bias), dict(z=res, zt=1), dict(z=res, zs=40)):
+        assert linear(**kw) == k3.E_ARG, kw
+
+    def grad(x=x, w=w, dz=dz, dx=dx, dw=dw):
+        return lib.k3huf_linear_grad(x, 32, 4, w, 32, 32, 32, dz, 32, dx, 32, 0, dw, None, 0, P, 0, None)
+
+    for kw in (dict(dx=x), dict(dx=dz), dict(dx=dz, dw=None), dict(dx=w), dict(dx=w, dw=None), dict(dx=dw), dict(dw=x), dict(dw=x, dx=None), dict(dw=dz),
+               dict(dw=dz, dx=None), dict(dw=w)):
+        assert grad(**kw) == k3.E_ARG, kw
+
+    def slope(db):
+        return lib.k3huf_linear_dz(z, 0, 32, dy, 0, 32, 4, 32, 2, dz, 32, db, 0, None)
+
+    for at in (z, dy, dz):
+        assert slope(at) == k3.E_ARG
+
+
+def test_products_refuse_one_argument_at_a_time(lib):
+    """The refusals of each argument, with all others as they should be."""
+    x, w, bias, res, y, z, dz, dx, dw = (P + (k << 16) for k in range(9))
+
+    def linear(x=x, xs=64, n=4, w=w, ws=64, rows=32, cols=64, bias=bias, bt=0, act=1, res=res, rs=32, y=y, ys=32, yt=1, z=z, zs=32, zt=0, scratch=None, size=0, st=P):
+        return lib.k3huf_linear(x, xs, n, w, ws, rows, cols, bias, bt, act, res, rs, y, ys, yt, z, zs, zt, scratch, size, st, None)
+
+    need = k3.linear_scratch_bytes(4, 32, 64, any=True)
+    for kw in (dict(x=None), dict(x=x + 1), dict(xs=63), dict(n=1 << 31), dict(w=None), dict(w=w + 1), dict(ws=63), dict(rows=0), dict(rows=1 << 31, ys=1 << 31, rs=1 << 31, zs=1 << 31),
+               dict(cols=0), dict(cols=1 << 31, xs=1 << 31, ws=1 << 31), dict(bias=bias + 1), dict(bt=1, bias=bias + 2), dict(bt=2), dict(act=4), dict(res=res + 2),
+               dict(rs=31), dict(res=y, rs=40), dict(y=None), dict(y=y + 2), dict(ys=31), dict(yt=2), dict(z=z + 1), dict(zs=31), dict(zt=2), dict(zt=1, z=z + 2),
+               dict(st=None), dict(st=P + 2), dict(scratch=P + 16, size=1 << 20), dict(xs=65, ws=65), dict(xs=65, ws=65, scratch=P, size=need - 1), dict(xs=65),
+               dict(ws=65), dict(x=x + 2), dict(w=w + 8)):
+        assert linear(**kw) == k3.E_ARG, kw
+
+    def grad(x=x, xs=64, n=4, w=w, ws=64, rows=32, cols=64, dz=dz, dzs=32, dx=dx, dxs=64, dxt=0, dw=dw, scratch=None, size=0, st=P, flags=0):
+        return lib.k3huf_linear_grad(x, xs, n, w, ws, rows, cols, dz, dzs, dx, dxs, dxt, dw, scratch, size, st, flags, None)
+
+    need = k3.linear_scratch_bytes(4, 32, 64, grad=True, any=True)
+    for kw in (dict(x=None), dict(x=x + 1), dict(xs=63), dict(n=1 << 31), dict(w=None), dict(w=w + 1), dict(ws=63), dict(rows=0), dict(cols=0), dict(dz=None),
+               dict(dz=dz + 1), dict(dzs=31), dict(dx=dx + 1), dict(dxt=1, dx=dx + 2), dict(dxt=2), dict(dxs=63), dict(dw=dw + 2), dict(dx=None, dw=None), dict(st=None),
+               dict(flags=8), dict(scratch=P + 16, size=1 << 20), dict(xs=65), dict(ws=65), dict(dzs=33), dict(xs=65, ws=65, dzs=33, scratch=P, size=need - 1)):
+        assert grad(**kw) == k3.E_ARG, kw
