@@ -871,27 +871,28 @@ struct Cut {
 // Clusters of so many CTAs, each with an SM of its own, that the GPU holds at once: fewer than its SMs would make room for, as
 // a cluster lies within one of its parts (50 clusters of three do not fit: 186 x 3176 x 9960 57 us with them, 45 in twos).
 uint64_t clusters_of(uint32_t splits, uint64_t sms) {
-    static std::atomic<int> known[kMaxSplits + 1];
-    int n = known[splits];
-    if (n == 0) {
-        constexpr auto kernel = product_kernel<128, false, false>;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(splits);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = Shape<128>::smem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = splits;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Shape<128>::smem)) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
-            (void)cudaGetLastError();         // (only the choice depends on it)
-            n = int(sms / splits);
-        }
-        known[splits] = n;
+    static std::atomic<int> known[64][kMaxSplits + 1];        // (by device: a cut decides the order of a result's sums)
+    int dev = 0, n = 0;
+    const bool kept = cudaGetDevice(&dev) == cudaSuccess && dev < 64;
+    if (kept) n = known[dev][splits].load(std::memory_order_relaxed);
+    if (n > 0) return uint64_t(n);
+    constexpr auto kernel = product_kernel<128, false, false>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(splits);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Shape<128>::smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Shape<128>::smem)) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+        (void)cudaGetLastError();             // (only the choice depends on it, and the next call asks again)
+        return sms / splits;
     }
+    if (kept) known[dev][splits].store(n, std::memory_order_relaxed);
     return uint64_t(n);
 }
 
