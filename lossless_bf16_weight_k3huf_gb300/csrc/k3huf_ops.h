@@ -79,9 +79,11 @@ inline int sm_count(uint64_t *sms) {
     static std::atomic<int> known[64];
     int dev = 0, n = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) == 0) {
+    const bool kept = e == cudaSuccess && dev < 64;
+    if (kept) n = known[dev].load(std::memory_order_relaxed);
+    if (e == cudaSuccess && n == 0) {
         e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (e == cudaSuccess) known[dev].store(n, std::memory_order_relaxed);
+        if (e == cudaSuccess && kept) known[dev].store(n, std::memory_order_relaxed);
     }
     *sms = uint64_t(n > 0 ? n : 1);
     return cuda_rc(e);

@@ -1,5 +1,5 @@
 """How a product is cut on devices that differ, against a CUDA runtime that answers for them (no GPU: launches are noted, not
-made).  The cut decides the order of a result's sums, so it may depend on the device of the call and on nothing that was
+made, and no device is visible).  The cut decides the order of a result's sums, so it may depend on the device of the call and on nothing that was
 asked before."""
 import os
 import subprocess
@@ -45,6 +45,7 @@ CALLS = """
 import ctypes, sys
 import lossless_bf16_weight_k3huf_gb300 as k3
 fake, lib, P = ctypes.CDLL(sys.argv[1]), k3._lib(), 1 << 20
+assert ctypes.cast(ctypes.CDLL(None).cudaLaunchKernelExC, ctypes.c_void_p).value == ctypes.cast(fake.cudaLaunchKernelExC, ctypes.c_void_p).value
 noted = (ctypes.c_int * 2).in_dll(fake, "noted")
 for step in sys.argv[2:]:
     dev, _, failing = step.partition("!")
@@ -65,7 +66,7 @@ def run(tmp_path_factory):
 
     def run(*steps):
         """Cuts by step: device, or device!1 where the query for its clusters fails."""
-        out = subprocess.run([sys.executable, "-c", CALLS, so, *steps], cwd=ROOT, check=True, capture_output=True, text=True, env={**os.environ, "LD_PRELOAD": so}).stdout
+        out = subprocess.run([sys.executable, "-c", CALLS, so, *steps], cwd=ROOT, check=True, capture_output=True, text=True, env={**os.environ, "LD_PRELOAD": so, "CUDA_VISIBLE_DEVICES": ""}).stdout
         cuts = [[] for _ in steps]
         for k, line in enumerate(out.splitlines()):
             cuts[k // 4].append(line.split()[1:])
@@ -83,3 +84,8 @@ def test_a_cut_depends_on_its_device_alone(run):
 
 def test_a_query_that_fails_is_asked_again(run):
     assert run("2!1", "2", "2!1")[1:] == [run("2")[0]] * 2
+
+
+def test_devices_beyond_those_that_are_kept(run):
+    """Their SMs were taken for one, and the cut divided by the pairs that one SM makes."""
+    assert run("70") == run("2") and run("1", "70", "0", "70")[1::2] == run("2") * 2
