@@ -203,6 +203,67 @@ def test_alternatives_alike_and_far_apart(mode, dtype):
     check_grad(x, ids, t, mode, scale=1.3)
 
 
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("n,V,dtype,pad", [(1000, 3000, BF, 0), (1000, 3000, F32, 5), (300, 50021, F32, 0), (700, 50021, BF, 3), (2000, 700, BF, 1)])
+def test_gradient_of_more_pieces_than_ctas(n, V, dtype, pad, mode):
+    """Each CTA works on several pieces: the next one's factors and logits are fetched, and this one's alternatives written,
+    while it is at work; rows without alternatives lie between."""
+    x, ids, t = make(n, V, 20, n + V, dtype, pad=pad)
+    ids[::7] = -1
+    ids[3::11, 4] = ids[3::11, 17]
+    a = check_grad(x, ids, t, mode, scale=0.9)
+    b = check_grad(x, ids, t, mode, scale=0.9, in_place=True)
+    c = check_grad(x, ids, t, mode, scale=0.9, out_pad=1)           # (rows that do not sit alike: one value at a time)
+    assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("shift", [0, 3])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,V", [(5, 60013), (310, 262149), (5, 262149), (500, 60013)])
+def test_vectors_that_hold_alternatives_carry_the_rest(n, V, dtype, shift):
+    """The stream passes over the 16-byte vectors that may hold an alternative, and another warp adds what else they hold.
+    Here that is all there is: the other tokens lie e^-60 below.  One vector lost, or added twice, is 1/700 of the sum or
+    more.  Its terms, fewer than 400, and zeros are added: 2^-24 of it each, with a few units of every exponential."""
+    E_, r = (4 if dtype == F32 else 8), np.random.default_rng(V)
+    cycle = (128 if V <= 65536 else 256) * 64                       # vectors after which a thread's bits come round
+    width = (V + 15) // 8 * 8
+    buf = torch.full((n, width), -60.0, dtype=dtype, device="cuda")
+    x5, ids5 = np.full((5, V), -60.0), np.zeros((5, 64), dtype=np.int64)
+    for row in range(5):
+        j = r.integers(0, min(V // 4, cycle * E_) - 16, 8)
+        step = cycle * E_ if 3 * cycle * E_ < V else V // 4
+        ids5[row] = np.concatenate([j, j + step, j + 2 * step, j + 2 * step + 1, j + 3 * step, j + 7, r.permutation(j), r.permutation(j + 2 * step)])
+        if row % 2:
+            ids5[row] = r.integers(0, V, 64)
+        ids5[row] = ids5[row][r.permutation(64)]
+        ids5[row, :2] = 0, V - 1                                    # (the row's ends, whose vectors are not whole)
+        taken = set(ids5[row].tolist())
+        homes = {(i + shift) // E_ % cycle for i in taken}
+        k = 0
+        for home in homes:
+            for at in range(home, (V + shift + E_ - 1) // E_, cycle):
+                inside = [e for e in range(at * E_ - shift, at * E_ - shift + E_) if 0 <= e < V and e not in taken]
+                if inside:
+                    x5[row, r.choice(inside)] = (k % 8) / 16 - 0.25
+                    k += 1
+        assert 8 < k < 400
+        x5[row, list(taken)] = r.integers(-16, 16, len(taken)) / 16
+    x = buf[:, shift:shift + V]
+    x.copy_(torch.from_numpy(x5).cuda().to(dtype).repeat(n // 5, 1))
+    assert x.data_ptr() % 16 == shift * x.element_size()
+    ids = torch.from_numpy(ids5).cuda().to(torch.int32).repeat(n // 5, 1).contiguous()
+    t = (-5.0 - torch.rand(5, 64, generator=torch.Generator(device="cuda").manual_seed(V), device="cuda")).repeat(n // 5, 1).contiguous()
+    loss, lse, log_rest, st = run(x, ids, t, "rest", 1.0)
+    assert st == 0
+    z, logp, on, at, q, tt, r_rest, rest, _ = parts(x[:5], ids[:5], t[:5], "rest", 1.0)
+    assert bool((rest > 0.1).all())
+    want = (q * (tt - logp.gather(1, at))).sum(1) + rest * (torch.log(rest) - r_rest)
+    bound = (400 + 16 + 4 + 2 * 2) * E                              # (exponents of 2 at most)
+    for got, ref, b, what in ((lse, torch.logsumexp(z, 1), bound, "lse"), (log_rest, r_rest, 2 * bound, "log_rest"), (loss, want, 3 * bound, "loss")):
+        close(got, ref.repeat(n // 5), torch.full((n,), b, dtype=torch.float64, device="cuda") + 1e-9, what)
+        assert torch.equal(got, got[:5].repeat(n // 5))
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_a_small_rest_keeps_its_digits(dtype):
     """The alternatives hold nearly all of p: the rest's sum is not a difference."""
