@@ -357,6 +357,57 @@ def test_graph_streams_and_no_rows():
     k3.logits_control(none, none, st)
 
 
+def two_launches():
+    return 2 * torch.cuda.get_device_properties(0).multi_processor_count + 9
+
+
+@pytest.mark.parametrize("x_type,out_type,in_place,history,bias,allowed", [
+    (BF, BF, True, 60, 5, 0.7), (F32, F32, True, 60, 5, 0.03), (F32, BF, False, 60, 5, 0.9), (BF, F32, False, 60, 5, None), (BF, BF, False, None, 0, 0.5),
+    (F32, F32, True, None, 0, 0.5), (F32, F32, True, 200, 8, None), (BF, BF, False, None, 6, 0.5), (F32, F32, False, None, 0, None)])
+@pytest.mark.parametrize("V", [517, 9001, 40016])
+def test_many_rows_in_two_launches(V, x_type, out_type, in_place, history, bias, allowed):
+    """More rows than the GPU holds at once: the stream and the lists are launches of their own, the second beginning while
+    the first one ends.  With and without either, in place and not, of either type."""
+    n = two_launches() if V > 9001 else 700
+    x, c, bits = case(n, V, seed=V + n, x_type=x_type, history=history, bias=bias, allowed=allowed, pad=V % 3)
+    assert check(x, c, bits, out_type=out_type, in_place=in_place, pad=V % 2) == 0
+
+
+def test_many_rows_of_long_lists():
+    """... whose rows touch more tokens than the lists' launch looks after at once, beside rows that touch none."""
+    n, V, r = two_launches(), 30011, np.random.default_rng(3)
+    x, c, bits = case(n, V, seed=5, x_type=BF, history=3, bias=3, allowed=0.8)
+    length = r.integers(0, 200, n)
+    length[[0, 7, n - 1]] = 20000, 9000, 15000
+    ends = np.cumsum(length)
+    c["history"] = torch.from_numpy(r.integers(0, V, ends[-1])).cuda()
+    c["spans"] = torch.from_numpy(np.stack([ends - length, ends - length // 3, ends], 1)).cuda()
+    for in_place in (False, True):
+        assert check(x, c, bits, out_type=BF, in_place=in_place) == 0
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_two_launches_in_a_graph(in_place):
+    """Captured, replayed one after the other over other logits: each replay gives what the call gives."""
+    n, V = two_launches(), 9001
+    x, c, _ = case(n, V, seed=9, x_type=BF, history=300, allowed=0.7)
+    held, out, st = x.clone(), torch.empty_like(x), status()
+    if in_place:
+        out = held
+    graph = torch.cuda.CUDAGraph()
+    k3.logits_control(x.clone(), torch.empty_like(x), st, **c)
+    with torch.cuda.graph(graph):
+        k3.logits_control(held, out, st, **c)
+    for k in range(5):
+        now = x.roll(k, 1) * (1 + k)
+        held.copy_(now)
+        want = torch.empty_like(x)
+        k3.logits_control(now, want, st, **c)
+        graph.replay()
+        assert torch.equal(out, want), k
+    assert int(st) == 0
+
+
 def test_refusals_of_the_binding():
     x, c, _ = case(3, 100, seed=1, allowed=0.5)
     out, st = torch.empty_like(x), status()

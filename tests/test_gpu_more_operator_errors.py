@@ -36,6 +36,9 @@ def calls():
     made["linear_dz"] = lambda s: k3.linear_dz(z, z, dz, act="silu", dbias=bias, stream=s)
     made["control few"] = lambda s: k3.logits_control(x, o, st, history=history, spans=spans, stream=s)
     made["control many"] = lambda s: k3.logits_control(many, many_out, st, history=history, spans=more, stream=s)
+    most = 2 * torch.cuda.get_device_properties(0).multi_processor_count + 9
+    rows, rows_out, of_rows = empty(most, 300, dtype=BF), empty(most, 300), torch.tensor([[0, 3, 9]] * most, device="cuda")
+    made["control in two launches"] = lambda s: k3.logits_control(rows, rows_out, st, history=history, spans=of_rows, stream=s)
     made["distill"] = lambda s: k3.distill(x, ids, t, lp, st, stream=s)
     made["distill_grad"] = lambda s: k3.distill_grad(x, ids, t, lp, lp, o, st, stream=s)
     return made
@@ -63,3 +66,7 @@ def test_a_refused_launch_leaves_no_error_behind(runtime, name):  # noqa: F811
     assert e.value.code == k3.E_CUDA and left == 0
     call(0)
     torch.cuda.synchronize()
+
+
+def test_a_refused_launch_of_two_leaves_no_error_behind(runtime):  # noqa: F811
+    test_a_refused_launch_leaves_no_error_behind(runtime, "control in two launches")
