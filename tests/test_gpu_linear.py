@@ -396,3 +396,53 @@ def test_z_over_the_residual(n, rows, cols, pad, dtype):
     k3.linear(x, w, y, st, residual=r, act="silu", z=z)
     k3.linear(x, w, over, st, residual=r, act="silu", z=r)
     assert torch.equal(y, over) and torch.equal(z, r) and int(st) == 0
+
+
+def signs(n, K, seed):
+    """n x K values, zero but for one of each 16 along K, which is 1 or -1; and their sums over each 64."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    at = torch.arange(0, K, 16, device="cuda")
+    at = at + (torch.rand(len(at), generator=g, device="cuda") * (K - at).clamp(max=16)).long()
+    v = torch.randint(0, 2, (n, len(at)), generator=g, device="cuda").float() * 2 - 1
+    x = torch.zeros(n, K, dtype=BF, device="cuda")
+    x[:, at] = v.to(BF)
+    return x, torch.zeros(n, (K + 63) // 64, device="cuda").index_add_(1, at // 64, v)
+
+
+def steps_of(m, K):
+    """m x K: row r is 1 where k / 64 is r modulo m."""
+    k = torch.arange(K, device="cuda")
+    w = torch.zeros(m, K, dtype=BF, device="cuda")
+    w[k // 64 % m, k] = 1
+    return w
+
+
+def by_step(sums, m):
+    """What such a product gives: whole numbers, exact in bf16 up to 256."""
+    want = torch.zeros(sums.shape[0], m, device="cuda").index_add_(1, torch.arange(sums.shape[1], device="cuda") % m, sums)
+    assert float(want.abs().max()) <= 256
+    return want
+
+
+@pytest.mark.parametrize("n,rows,cols", [(2048, 2048, 66000), (600, 3000, 66000), (20, 130, 530000), (1000, 1000, 132000), (300, 2000, 70000), (7, 1000, 140000)])
+def test_every_step_of_several_runs_counts_once(n, rows, cols):
+    """Results from single steps of the contraction, bit for bit: runs of 65536 values and of 512, in pairs of CTAs (the
+    first two shapes) and where a cluster shares them."""
+    x, sums = signs(n, cols, seed=n)
+    w, want, st = steps_of(rows, cols), by_step(sums, rows), status()
+    for y_type in (BF, F32):
+        y = torch.empty(n, rows, dtype=y_type, device="cuda")
+        k3.linear(x, w, y, st)
+        assert torch.equal(y.float(), want), y_type
+    # the same sums as dz W
+    w = w.T.contiguous()
+    for dx_type in (BF, F32):
+        dx = torch.empty(n, rows, dtype=dx_type, device="cuda")
+        k3.linear_grad(None, w, x, st, dx=dx, scratch=scratch(n, cols, rows, grad=True))
+        assert torch.equal(dx.float(), want), dx_type
+    # ... and, over the tokens, as dz^T x
+    if n * rows <= 1 << 20:
+        dw = torch.empty(n, rows, device="cuda")
+        k3.linear_grad(w, None, x.T.contiguous(), st, dw=dw, scratch=scratch(cols, n, rows, grad=True))
+        assert torch.equal(dw, want)
+    assert int(st) == 0

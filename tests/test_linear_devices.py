@@ -1,6 +1,6 @@
-"""How a product is cut on devices that differ, against a CUDA runtime that answers for them (no GPU: launches are noted, not
-made, and no device is visible).  The cut decides the order of a result's sums, so it may depend on the device of the call and on nothing that was
-asked before."""
+"""How a product is cut on devices that differ, against a CUDA runtime that answers for them (no GPU: launches are noted,
+not made, and no device is visible).  The cut decides the order of a result's sums, so it may depend on the device of
+the call and on nothing that was asked before."""
 import os
 import subprocess
 import sys
