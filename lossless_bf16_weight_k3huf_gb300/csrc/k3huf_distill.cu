@@ -444,40 +444,35 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == 256 ? 4 : kRest ? 6
     }
     __syncthreads();
     if (C == 1 && warp > 0) return;
-    // one warp: the warps' sums, then the CTAs', and, at last, the alternatives' with them.  The rest keeps a maximum and a sum
-    // of its own: p_r may lie as far below the alternatives as the logits do, and its logarithm is wanted, not what it adds
-    float m, big;                             // the largest of what was streamed (without the alternatives, where there is a rest); of all
-    double rest, total;                       // the sums beside them
-    auto add = [&](const Part *parts, uint32_t count, bool tops) {
-        Part p{-3.402823466e38f, {0.f, 0.f}};
-        if (uint32_t(lane) < count) p = parts[lane];
+    // one warp: the warps' sums, then the CTAs'
+    float m;                                  // the largest of what was streamed (without the alternatives, where there is a rest)
+    double rest;                              // its sum, beside that
+    auto add = [&](const Part *parts, uint32_t count) {
+        const Part p = uint32_t(lane) < count ? parts[lane] : Part{-3.402823466e38f, {0.f, 0.f}};
         m = p.m;
 #pragma unroll
         for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        auto beside = [&](float of) { return p.sum.hi == 0.f ? 0. : wide(two_mul(p.sum, {weight32(below(p.m, of, P.scale2)), 0.f})); };
-        const double of_rest = beside(m);
-        big = m;
-        if (tops) {
-            big = fmaxf(m, s_terms.top);
-            if (uint32_t(lane) == count) p = {s_terms.top, s_terms.top_sum};
-            const double of_all = beside(big);
-            rest = warp_sum(of_rest), total = warp_sum(of_all);
-        } else {
-            rest = total = warp_sum(of_rest);
-        }
+        rest = warp_sum(p.sum.hi == 0.f ? 0. : wide(two_mul(p.sum, {weight32(below(p.m, m, P.scale2)), 0.f})));
     };
-    if (C == 1) {
-        add(s_part, kParts, kRest);
-    } else {
-        add(s_part, kParts, false);
+    add(s_part, kParts);
+    if (C > 1) {
         cluster_wait();
         if (tid == 0) cluster.map_shared_rank(s_all, 0)[rank] = Part{m, narrow(rest)};
         cluster_arrive();
         cluster_wait();
         if (rank > 0 || warp > 0) return;
-        add(s_all, C, kRest);
+        add(s_all, C);
     }
     const Terms R = s_terms;
+    // With the alternatives' sum (a lane for each of the two), beside the larger maximum.  The rest keeps its own: p_r may lie
+    // as far below the alternatives as the logits do, and its logarithm is wanted, not what it adds to them.
+    float big = m;
+    double total = rest;
+    if constexpr (kRest) {
+        big = fmaxf(m, R.top);
+        const double one = lane == 0 ? rest : wide(R.top_sum), v = one == 0. ? 0. : one * wide(weight(below(lane == 0 ? m : R.top, big, P.scale2)));
+        total = __shfl_sync(0xffffffffu, v, 0) + __shfl_sync(0xffffffffu, v, 1);
+    }
     // (a lane each; of what is 0, or not there, no logarithm is used)
     const double of = lane == 0 ? total : lane == 1 && kRest ? rest : lane == 2 ? R.rest : lane == 3 ? R.whole : 1., logs = log_of(of == 0. ? 1. : of);
     const double log_total = __shfl_sync(0xffffffffu, logs, 0), log_q = __shfl_sync(0xffffffffu, logs, 2), log_whole = __shfl_sync(0xffffffffu, logs, 3);
