@@ -586,7 +586,10 @@ int k3huf_token_logprobs_grad(const void *d_logits, uint32_t type, uint64_t stri
  * starts where such an argument does. */
 
 /* act(z): z; max(z, 0); z / (1 + exp(-z)); the tanh form of GELU,
- * z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))). */
+ * z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))).  In fp32, with the hardware's
+ * exponential and quotient: off by 8 x 2^-24 of |z| at most, and by (8 + 6 |u|)
+ * 2^-24 of itself, u being what the exponential is taken of (z for SiLU, 2 sqrt(2 /
+ * pi) (z + 0.044715 z^3) for GELU); a result below 2^-119 may be 0. */
 #define K3HUF_ACT_NONE 0u
 #define K3HUF_ACT_RELU 1u
 #define K3HUF_ACT_SILU 2u
@@ -609,9 +612,12 @@ int k3huf_linear_scratch_bytes(uint64_t n_tokens, uint64_t rows, uint64_t cols, 
  *  d_y: n_tokens rows of `rows` elements of y_type;
  *  d_z: where a backward pass wants z, rows of z_type; or NULL.  May be d_residual,
  *    where that is of the same type and stride.
- * Sums are fp32: for fp32 y they leave the tensor core every 512 values of the
- * contraction, whose additions round to one side.  Up to 2^31 - 1 tokens, rows
- * and columns. */
+ * Sums are fp32, in the tensor core, whose additions (of 16 products each) round to
+ * one side, by 1.3e-8 of the sum on average.  Where y or z is fp32 they leave it
+ * every 512 values of the contraction, some 4e-7 of the sum off; for bf16 results
+ * every 65536, some 5e-5 off (of sums of 8192 random products 99.5% come out as the
+ * exact sum rounded, and 99.97% where z is fp32).  So do the gradients' sums below.
+ * Up to 2^31 - 1 tokens, rows and columns. */
 int k3huf_linear(const void *d_x, uint64_t x_stride, uint64_t n_tokens, const void *d_w, uint64_t w_stride,
                  uint64_t rows, uint64_t cols, const void *d_bias, uint32_t bias_type, uint32_t act,
                  const void *d_residual, uint64_t residual_stride, void *d_y, uint64_t y_stride, uint32_t y_type,
@@ -629,7 +635,8 @@ int k3huf_linear_dz(const void *d_z, uint32_t z_type, uint64_t z_stride, const v
 
 /* The gradients of the product for dz (n_tokens rows of `rows` bf16):
  *  dx[t] = dz[t] W: rows of cols elements of dx_type (d_dx NULL: not wanted, and
- *    d_w is not read), the dx_base of k3huf_adapter_grad;
+ *    d_w is not read), the dx_base of k3huf_adapter_grad.  It may be d_x where dW is
+ *    not wanted;
  *  dW = sum over the tokens of dz[t]^T x[t]: rows x cols floats, contiguous (d_dw
  *    NULL: not wanted, and d_x is not read); with K3HUF_ACCUMULATE added to. */
 int k3huf_linear_grad(const void *d_x, uint64_t x_stride, uint64_t n_tokens, const void *d_w, uint64_t w_stride,
@@ -686,8 +693,11 @@ int k3huf_logits_control(const k3huf_control_t *control, const void *d_logits, u
  *    exponentials of the scaled logits), d_log_rest (log p_r; K3HUF_DISTILL_REST
  *    only): n floats, or NULL.
  * A term of q 0 is 0; a q above 0 against p 0 gives an infinite loss.  Logits of
- * -infinity have p 0; a NaN or +infinity makes the row's results NaN.  Up to
- * 2^27 - 1 rows. */
+ * -infinity have p 0; a NaN or +infinity makes the row's results NaN.  p_r may be far
+ * below the smallest fp32 number: log p_r is what is computed.  The sum over the
+ * vocabulary is fp32 in each thread, with the hardware's exponential, and 45 bits
+ * and more from there: a loss errs by about 2^-24 of the mass of q, however small it
+ * is itself.  Up to 2^27 - 1 rows. */
 #define K3HUF_DISTILL_GIVEN      0u
 #define K3HUF_DISTILL_NORMALISED 1u
 #define K3HUF_DISTILL_REST       2u
@@ -698,7 +708,10 @@ int k3huf_distill(const void *d_logits, uint32_t type, uint64_t stride, uint64_t
 /* Its gradient with respect to the logits for the gradient g of the loss (not read
  * for a row without alternatives, whose gradient is 0): with Q = sum q (+ q_r),
  *   dlogits[j] = scale g (Q p_j - q_j) for an alternative,
- *                scale g (Q - q_r / p_r) p_j for another token.
+ *                scale g (Q - q_r / p_r) p_j for another token,
+ * with p_j and p_j / p_r as exponentials of what is left of scale * logits, lse and
+ * log p_r, which are fp32: relative to itself a gradient is off by a few times 2^-24
+ * of the largest of these.
  *  d_lse, d_log_rest (K3HUF_DISTILL_REST, else NULL): as k3huf_distill gave them;
  *  d_dlogits: of the logits' type, out_stride apart; may be d_logits itself (then
  *    out_stride = stride). */

@@ -9,7 +9,8 @@
 //
 // A loss is what is left of terms far larger than itself, so what there are few of (the alternatives' terms, the
 // rest's mass, the logarithms) is computed in 64 bits or pairs of floats; the sum over the vocabulary in 32.  p_r is summed over the
-// other tokens alone, never taken as a difference: a small rest keeps its digits.
+// other tokens alone, never taken as a difference, beside their own maximum: a small rest keeps its digits, and its logarithm
+// reaches as far down as the logits do.
 //
 // Forward, one read of the logits: a CTA streams a row, or the CTAs of a cluster when there are fewer rows than the
 // GPU holds CTAs.  To leave the alternatives out of the rest's sum, every thread has a bit for each of its

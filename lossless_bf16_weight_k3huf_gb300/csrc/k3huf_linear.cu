@@ -7,11 +7,13 @@
 // with A = W, B = x for y; A = W^T, B = dz for dx; A = x^T, B = dz^T for dW.  An operand that lies
 // contraction-last is read K-major, one that lies contraction-first (W for dx; x and dz for dW) MN-major from
 // the same 128-byte swizzled tiles, so nothing is transposed in memory.  i is the tile's 128 lanes of TMEM: a
-// warp's store of one j is 32 neighbouring elements of the result, and the epilogue needs no shared memory.
+// warp's store of one j is 32 neighbouring elements of the result, and the results need no shared memory (a residual
+// comes through it, see Ahead).
 //
-// Bound by the tensor cores where there are many tokens (4096 x 8192 x 8192 bf16 285 to 290 us, 1.9 PFLOP/s; 8192 x 24576
-// x 8192 1.70 to 1.73 ms), by the read of the weight where there are few (3 x 8192 x 8192 26 us, 5.2 TB/s with the
-// launch), by the epilogue where the contraction is short (8192 x 8192 x 576 62 us).
+// Bound by the tensor cores where there are many tokens (4096 x 8192 x 8192 bf16 285 to 296 us, 1.9 PFLOP/s, the tensor
+// pipe busy in 97% of the cycles; 8192 x 24576 x 8192 1.70 to 1.97 ms, as the power limit allows), by the read of the
+// weight where there are few (3 x 8192 x 8192 26 to 29 us, 4.6 to 5.2 TB/s with the launch), by the epilogue where the
+// contraction is short (8192 x 8192 x 576 62 to 70 us).
 #include <algorithm>
 #include <cmath>
 
@@ -123,7 +125,9 @@ __device__ __forceinline__ void residual_at(const Epilogue &e, uint32_t i, uint3
     }
 }
 
-// Sums to values of the result.
+// Sums to values of the result.  (With the hardware's exponential and quotient, for fp32 results too: they err by some units
+// of the last place more than expf and a division, with which the slopes of 4095 x 24576 took 299 us instead of 100.  A
+// quotient by more than 2^126 is 0.)
 template <int kCount>
 __device__ __forceinline__ void apply(const Epilogue &e, uint32_t i, uint32_t j, uint32_t size_j, float (&v)[kCount], float bias, const float (&res)[kCount]) {
     if (e.bias) {
@@ -724,7 +728,8 @@ struct SlopeParams {
 
 // dz and the columns' sums in one read of z and dy.  A CTA takes kSlopeLanes x kPer columns (kPer neighbouring ones per
 // thread) and its share of the tokens; the CTAs of a cluster, which share the columns, add up in the order of their tokens.
-// Bound by HBM: 4095 x 24576 bf16 102 us, 5.9 TB/s.
+// Bound by HBM: 4095 x 24576 bf16 102 to 104 us, 5.9 TB/s.  Narrow rows leave SMs idle (8192 tokens x 64 35 us, x 576 38,
+// x 1024 41), and rows of no multiple of 8 go one value at a time (4095 x 24571 186 us).
 constexpr int kSlopeThreads = 256, kSlopeLanes = 16, kSlopePerSm = 4;        // threads along the columns
 template <typename T, int kPer> struct Few {              // neighbouring values as loaded
     T v[kPer];

@@ -1,7 +1,7 @@
 // Shared by the translation units of the operators that stand next to the
-// coded weights (embedding rows, adapters, token log probabilities): element
-// loads and stores, warp sums, launches and argument checks.  Included from
-// .cu files only.
+// coded weights (embedding rows, adapters, token log probabilities, products,
+// control of logits, distillation): element loads and stores, warp sums,
+// launches and argument checks.  Included from .cu files only.
 #pragma once
 
 #include <cuda_bf16.h>

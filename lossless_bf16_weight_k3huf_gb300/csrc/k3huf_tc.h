@@ -1,4 +1,4 @@
-// Fifth-generation tensor core primitives for the adapter kernels: shared
+// Fifth-generation tensor core primitives for the adapters and the products: shared
 // memory tiles of 128-byte rows, their descriptors, tcgen05 instructions and
 // bounded barrier waits.  Included from .cu files only.
 //

@@ -101,6 +101,24 @@ def test_epilogues(act, n):
                 forward(n, 200, 320, act=act, y_type=y_type, bias=bias, res=res, seed=n)
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activations_hold_what_the_header_says(act):
+    """An fp32 exponential of u errs by (2 + 1.2 |u|) units of 2^-23 (its rounded exponent), a quotient by two; GELU's u by
+    three roundings more.  So (8 + 2.4 |u|) 2^-24 of the value for SiLU, (8 + 6 |u|) for GELU, and, as the exponential is no
+    part of the value where it is small, 8 x 2^-24 of |z|; a quotient by more than 2^126 is 0."""
+    z = torch.cat([torch.linspace(-100, 100, 2000001, device="cuda"), -torch.logspace(-6, 2, 1000001, device="cuda"), torch.logspace(-6, 30, 1000001, device="cuda")])
+    z = z[: z.numel() // 8 * 8].contiguous()
+    n = z.numel()
+    one, w, y, st = torch.ones(1, 8, dtype=BF, device="cuda"), torch.zeros(n, 8, dtype=BF, device="cuda"), torch.empty(1, n, device="cuda"), status()
+    k3.linear(one, w, y, st, bias=z, act=act)                       # (products of 0: z is the bias)
+    z = z.double()
+    u = z if act == "silu" else 2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+    want = z / (1 + torch.exp(-u))
+    off = (y[0].double() - want).abs()
+    assert bool((off <= (8 + (2.4 if act == "silu" else 6) * u.abs().clamp(max=200)) * E * want.abs() + 2.0 ** -119).all())
+    assert bool((off <= 8 * E * z.abs() + 2.0 ** -119).all()) and int(st) == 0
+
+
 @pytest.mark.parametrize("pad", [(1, 0, 0, 0), (0, 3, 0, 0), (5, 7, 1, 1)])
 def test_rows_of_any_alignment(pad):
     for n in (1, 4, 70, 300):
