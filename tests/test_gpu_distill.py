@@ -334,6 +334,23 @@ def test_a_rest_far_below_the_alternatives(n, V, dtype, gap, scale):
     check_grad(x, ids, t, "rest", scale=scale, least=least)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_what_the_sum_errs_by_cancels_between_near_distributions(dtype):
+    """With d what the other tokens' sum errs by, relative to itself, the loss errs by (p_r - q_r) d: both of its logarithms
+    take the same sum.  Its exponentials err by 1 x 2^-24 in the root mean square, nearly all to one side, and their rounded
+    arguments to both, so d is 2 x 2^-24 at most in that mean over the rows; half a unit of the loss is its own rounding.
+    (Sums that are rounded apart err by a third of a unit, 1.6 times this bound.)"""
+    x, ids, t = make(512, 131072, 20, 41, dtype, none=0.0)
+    loss, _, log_rest, _ = run(x, ids, t, "rest", 1.0)
+    _, logp, _, at, q, tt, r_rest, rest, _ = parts(x, ids, t, "rest", 1.0)
+    want = (q * (tt - logp.gather(1, at))).sum(1) + rest * (torch.log(rest) - r_rest)
+
+    def rms(v):
+        return float(v.pow(2).mean().sqrt())
+
+    assert rms(loss.double() - want) <= 2 * E * rms(r_rest.exp() - rest) + E * rms(want)
+
+
 def test_infinite_terms():
     x, ids, t = make(6, 4000, 8, 4, none=0.0)
     at = ids.long()
